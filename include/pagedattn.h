@@ -89,7 +89,10 @@ enum {
   PA_DEVERR_CONTEXT_LEN = 4,  /* context_lens[b] < 0 or > block_table_stride * block_size */
   PA_DEVERR_COPY_PAIR = 8,    /* a copy pair with src or dst outside [0, num_blocks) */
   PA_DEVERR_QUERY_LOC = 16,   /* query_start_loc not non-decreasing, or a chunk longer than its context */
-  PA_DEVERR_TIMEOUT = 32      /* a bounded wait in a pipelined kernel gave up (the kernel returned early) */
+  PA_DEVERR_TIMEOUT = 32,     /* a bounded wait in a pipelined kernel gave up (the kernel returned early) */
+  PA_DEVERR_TREE = 64,        /* a drafted tree wider than its mask, a parent not below its node, or an
+                                 accepted node below its place */
+  PA_DEVERR_NO_BLOCKS = 128   /* the free list held too few blocks for a batch */
 };
 
 /* Options for pa_set_option / pa_get_option.  The only process-wide option is the checked mode. */
@@ -246,6 +249,121 @@ PA_API int paged_attention_prefill_ex(void* out, const void* q, const int32_t* q
                                       int64_t num_blocks, int block_size, float scale, int n_q_heads,
                                       int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts,
                                       void* stream);
+
+/*
+ * build_block_tables — the index arrays of a serving step, built on the device from the requests'
+ * lengths in one launch: block tables grown from a free list, the slot and position of every new
+ * token, query_start_loc, context_lens and, for drafted trees, the mask paged_attention_tree reads.
+ * The calls that follow in the step (paged_kv_write, the attention calls) take them as they are, so
+ * a step needs no host round trip and can be captured in a CUDA graph.
+ *   history_lens      int32 [batch]: tokens of the sequence already in the cache
+ *   new_lens          int32 [batch]: tokens the step adds (0 allowed)
+ *   block_table       int32 [batch][block_table_stride], max_blocks entries of a row used: row b
+ *                     holds block_counts[b] blocks and grows, in place, to the
+ *                     ceil((history + new) / block_size) that the step needs.  A row that holds more
+ *                     (blocks kept from rejected drafts) keeps them.
+ *   block_counts      int32 [batch], updated in place
+ *   free_blocks       int32 [free_capacity], a stack: entries [0, free_state[0]) are free.  Blocks are
+ *                     taken from its top in batch order.
+ *   free_state        int32 [2]: the number of free blocks, updated in place, and a word of the
+ *                     library's own that is 0 before and after every call.  Calls that share
+ *                     free_state or block_counts must not overlap.
+ *   num_blocks        blocks of the pool: an id outside [0, num_blocks) taken from free_blocks is
+ *                     entered as -1 and recorded as PA_DEVERR_BLOCK_ID
+ *   parents           optional int32 [token_capacity]: new token t is the node of a drafted tree
+ *                     whose parent is node parents[t] of the same sequence (numbered from 0 within
+ *                     the sequence, below the node's own number), or -1: it follows the history.
+ *                     A parent outside [-1, own number) counts as -1 and is recorded as
+ *                     PA_DEVERR_TREE.  NULL: every token follows the one before it.
+ *   query_start_loc   int32 [batch + 1] (written): running sums of new_lens
+ *   context_lens      int32 [batch] (written): history + new
+ *   slot_mapping      int64 [token_capacity] (written): slot of position history + j for new token j
+ *                     of a sequence; -1 (paged_kv_write skips it) behind the last sequence's tokens
+ *   positions         int32 [token_capacity] (written): history + j, or with parents history + the
+ *                     number of the node's proper ancestors; 0 behind the last sequence's tokens
+ *   tree_mask         int64 [token_capacity][mask_words], with parents only: bit s % 64 of word s / 64
+ *                     of row t is set when node s is token t's node or one of its ancestors; 0
+ *                     behind the last sequence's tokens
+ * A sequence that does not fit gets nothing: its table row and count stay, its slots are -1, its
+ * positions and mask rows 0 and its context_lens entry is 0.  That is a negative length or one past
+ * max_blocks * block_size (PA_DEVERR_CONTEXT_LEN), tokens past token_capacity
+ * (PA_DEVERR_QUERY_LOC), a count outside [ceil(history / block_size), max_blocks]
+ * (PA_DEVERR_BLOCK_ID), a tree of more than 64 * mask_words nodes (PA_DEVERR_TREE), or a need that
+ * the free blocks left by the sequences before it do not cover (PA_DEVERR_NO_BLOCKS; once one
+ * sequence finds too few, no later one takes any).  Checked mode returns PA_ERANGE for each of these.
+ * batch == 0 is a no-op.  Index arrays need the alignment of their type only.
+ */
+PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_lens, int batch, int32_t* block_table,
+                              int64_t block_table_stride, int64_t max_blocks, int32_t* block_counts,
+                              const int32_t* free_blocks, int64_t free_capacity, int32_t* free_state,
+                              int64_t num_blocks, int block_size, const int32_t* parents, int32_t* query_start_loc,
+                              int32_t* context_lens, int64_t* slot_mapping, int32_t* positions,
+                              int64_t token_capacity, int64_t* tree_mask, int mask_words, void* stream);
+
+/*
+ * paged_attention_tree — a tree of drafted tokens per sequence attends over the paged context: every
+ * node sees the whole history and, of the tree, its ancestors and itself.
+ *   q, out          [total_q][n_q_heads][head_dim]
+ *   query_start_loc int32 [batch + 1]: sequence b owns the m_b = qsl[b+1] - qsl[b] <= max_nodes nodes
+ *                   qsl[b] .. qsl[b+1]-1; m_b = 0 is allowed, and so are rows from qsl[batch] to
+ *                   total_q (a padded batch): those rows of out are left as they were.
+ *   tree_mask       int64 [total_q][mask_words]: node r of a tree sees node s of it when bit s % 64 of
+ *                   word s / 64 of its row is set (any pattern, not trees alone).  Every m_b must be
+ *                   at most 64 * mask_words.  NULL: the drafted tokens form a chain, each seeing the
+ *                   ones before it and itself (mask_words is ignored).
+ *   max_nodes       bound on m_b, >= 1 (it sizes the launch)
+ *   context_lens    int32 [batch]: history + m_b.  The keys and values of the nodes are the last m_b
+ *                   positions of the context, in node order, already written.
+ *   scale           finite and > 0
+ *   out[r][i] = sum_j softmax_j(scale * q[r][i] . K_j) V_j over the keys node r sees.  A row that sees
+ *   nothing gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and
+ *   NaN included); a non-finite key or value that it sees gives non-finite outputs.
+ *   workspace       optional scratch for splitting long contexts, at least
+ *                   paged_attention_tree_workspace_size(...) bytes for the same sizes and opts,
+ *                   16-byte aligned, no initialisation needed.  NULL: no splitting (slower for few
+ *                   sequences with long contexts).  Calls that may overlap need one each.
+ *   opts            may be NULL.  kv_block_stride_bytes, partition_tokens as for the decode call;
+ *                   prefill_kernel: 0 auto (tcgen05 tensor cores for bf16/fp16 pools with
+ *                   block_size % 16 == 0, else CUDA cores), 1 CUDA cores, 2 tcgen05
+ *                   (PA_EUNSUPPORTED if the shape does not allow it).
+ * A sequence whose rows are out of order, more than max_nodes or 64 * mask_words, or more than its
+ * context, gives zeros in the rows it has among total_q and is recorded as PA_DEVERR_QUERY_LOC (or
+ * PA_DEVERR_TREE); checked mode returns PA_ERANGE.
+ */
+PA_API int paged_attention_tree(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q,
+                                const int64_t* tree_mask, int mask_words, int max_nodes, const void* k_pool,
+                                const void* v_pool, const int32_t* block_table, int64_t block_table_stride,
+                                const int32_t* context_lens, int batch, int64_t num_blocks, int block_size,
+                                float scale, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype,
+                                void* workspace, size_t workspace_bytes, const pa_opts* opts, void* stream);
+
+/* Workspace bytes paged_attention_tree needs to split contexts as long as the table allows, on the
+ * current device (0 if it does not split).  Invalid sizes give 0. */
+PA_API size_t paged_attention_tree_workspace_size(int batch, int64_t total_q, int max_nodes,
+                                                  int64_t block_table_stride, int block_size, int n_q_heads,
+                                                  int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts);
+
+/*
+ * paged_kv_accept — keep the accepted drafted tokens: move their K/V rows to the end of the history,
+ * in every layer, so that the context of sequence b becomes history_lens[b] + accepted_lens[b].
+ *   k_pool, v_pool  the first layer's pools; layer l's lie l * layer_stride_bytes further on (a
+ *                   multiple of 16; ignored for one layer).  Written in place, bit for bit.
+ *   accepted        int32 [batch][accepted_stride]: the nodes kept, at least accepted_lens[b] of
+ *                   them (<= max_accepted), in path order: node accepted[b][i], whose row is position
+ *                   history_lens[b] + accepted[b][i], moves to position history_lens[b] + i.  In an
+ *                   ascending list (parents before their children) entry i is at least i; a smaller
+ *                   one is not moved and recorded as PA_DEVERR_TREE.
+ *   accepted_lens   int32 [batch], 0 .. max_accepted (more: the first max_accepted are moved and
+ *                   PA_DEVERR_QUERY_LOC recorded)
+ * Positions past the table row, and table entries outside the pool, are not moved and recorded
+ * (PA_DEVERR_CONTEXT_LEN, PA_DEVERR_BLOCK_ID); checked mode returns PA_ERANGE.  Two sequences must not
+ * share the blocks that hold their drafted tokens.  opts: only kv_block_stride_bytes applies.
+ */
+PA_API int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride_bytes,
+                           const int32_t* accepted, int64_t accepted_stride, int max_accepted,
+                           const int32_t* accepted_lens, const int32_t* history_lens, const int32_t* block_table,
+                           int64_t block_table_stride, int batch, int64_t num_blocks, int block_size, int n_kv_heads,
+                           int head_dim, pa_dtype dtype, const pa_opts* opts, void* stream);
 
 /*
  * copy_blocks — make physical block dst a bit copy of block src, in both pools, for each pair.

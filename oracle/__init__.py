@@ -20,3 +20,4 @@ from .paged_oracle import (  # noqa: F401
     to_int,
     transfer_blocks,
 )
+from . import tree_oracle as tree  # noqa: F401

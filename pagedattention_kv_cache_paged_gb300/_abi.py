@@ -11,6 +11,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,6 +25,7 @@ PA_OK, PA_EINVAL, PA_EDTYPE, PA_ERANGE, PA_EWORKSPACE, PA_ECUDA, PA_EUNSUPPORTED
 PA_OPT_CHECKED = 1
 PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_CONTEXT_LEN = 1, 2, 4
 PA_DEVERR_COPY_PAIR, PA_DEVERR_QUERY_LOC, PA_DEVERR_TIMEOUT = 8, 16, 32
+PA_DEVERR_TREE, PA_DEVERR_NO_BLOCKS = 64, 128
 
 _vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 
@@ -45,6 +47,11 @@ _WS = [_i32, _i64, _i32, _i32, _i32, _i32]
 _PREFILL = [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i32, _f32, _i32, _i32, _i32, _i32]
 _COPY = [_vp, _vp, _vp, _i64, _i64, _i64]
 _SWAP = [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64]
+_TABLES = [_vp, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32]
+_TREE = [_vp, _vp, _vp, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i32, _f32, _i32, _i32, _i32, _i32,
+         _vp, _sz, _opts_p]
+_TREE_WS = [_i32, _i64, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _opts_p]
+_ACCEPT = [_vp, _vp, _i32, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _i32, _i32, _opts_p]
 SIGNATURES = {
     "paged_kv_write": (_i32, _KV_WRITE + [_vp]),
     "paged_kv_write_ex": (_i32, _KV_WRITE + [_opts_p, _vp]),
@@ -58,6 +65,10 @@ SIGNATURES = {
     "paged_attention_decode_fused_ex": (_i32, _FUSED + [_opts_p, _vp]),
     "paged_attention_prefill": (_i32, _PREFILL + [_vp]),
     "paged_attention_prefill_ex": (_i32, _PREFILL + [_opts_p, _vp]),
+    "build_block_tables": (_i32, _TABLES + [_vp]),
+    "paged_attention_tree": (_i32, _TREE + [_vp]),
+    "paged_attention_tree_workspace_size": (_sz, _TREE_WS),
+    "paged_kv_accept": (_i32, _ACCEPT + [_vp]),
     "copy_blocks": (_i32, _COPY + [_vp]),
     "copy_blocks_ex": (_i32, _COPY + [_opts_p, _vp]),
     "swap_blocks": (_i32, _SWAP + [_vp]),
@@ -385,6 +396,229 @@ def paged_attention_prefill(q, query_start_loc, k_pool, v_pool, block_table, con
                                         _stream(stream))
     _check("paged_attention_prefill", st)
     return out
+
+
+class _OnDevice:
+    """The current device set to the tensors' own while a call is made (the library launches on the
+    current device); nothing to do when it is that already."""
+
+    def __init__(self, device):
+        other = device.type == "cuda" and device.index != torch.cuda.current_device()
+        self._guard = torch.cuda.device(device) if other else None
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+
+
+def _vector(t, name: str, n: int, dtype=torch.int32) -> int:
+    ptr = _dev(t, name, dtype)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+    return ptr
+
+
+class StepTables(NamedTuple):
+    """What :func:`build_block_tables` writes: the index arrays of one serving step."""
+    query_start_loc: torch.Tensor           # int32 [batch + 1]
+    context_lens: torch.Tensor              # int32 [batch]
+    slot_mapping: torch.Tensor              # int64 [tokens]
+    positions: torch.Tensor                 # int32 [tokens]
+    tree_mask: Optional[torch.Tensor]       # int64 [tokens, words], with parents only
+
+
+def build_block_tables(history_lens, new_lens, block_table, block_counts, free_blocks, free_state, block_size: int,
+                       num_blocks: int, num_tokens: int | None = None, parents=None, mask_words: int | None = None,
+                       out: StepTables | None = None, stream=None) -> StepTables:
+    """The index arrays of a step from the requests' lengths, on the device, in one launch.
+
+    ``history_lens, new_lens`` int32 [B]: tokens in the cache and tokens added.  ``block_table`` int32
+    [B, max_blocks] and ``block_counts`` int32 [B] grow in place from ``free_blocks`` (int32, a stack
+    whose first ``free_state[0]`` entries are free; ``free_state`` int32 [2] = (count, 0), updated in
+    place).  ``parents`` int32 [tokens]: the new tokens are drafted trees (see the header); the result
+    then holds the mask for :func:`paged_attention_tree`, ``mask_words`` (default 1) words of 64 nodes
+    a row.  The token arrays have ``num_tokens`` rows (default: those of ``parents`` or of ``out``);
+    rows behind the last sequence's tokens get slot -1.  ``out``: the arrays of an earlier call, to be
+    written again (a captured step).  Sequences that do not fit get nothing and are recorded in the
+    device error word."""
+    lib = load_library()
+    dev = history_lens.device
+    B = int(history_lens.numel())
+    if block_table.dim() != 2 or block_table.shape[0] != B or (B and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [batch, max_blocks] with contiguous rows")
+    if out is None:
+        T = num_tokens if num_tokens is not None else (int(parents.numel()) if parents is not None else None)
+        if T is None:
+            raise ValueError("num_tokens is needed without parents or out")
+        words = 1 if mask_words is None else mask_words
+        with _OnDevice(dev):
+            out = StepTables(torch.empty(B + 1, dtype=torch.int32, device=dev),
+                             torch.empty(B, dtype=torch.int32, device=dev),
+                             torch.empty(T, dtype=torch.int64, device=dev),
+                             torch.empty(T, dtype=torch.int32, device=dev),
+                             torch.empty((T, words), dtype=torch.int64, device=dev) if parents is not None else None)
+        if B == 0:
+            out.query_start_loc.zero_()
+            out.slot_mapping.fill_(-1)
+            out.positions.zero_()
+            if out.tree_mask is not None:
+                out.tree_mask.zero_()
+    qsl, ctx, slots, pos, mask = out
+    T = int(slots.numel())
+    if num_tokens is not None and num_tokens != T:
+        raise ValueError(f"out holds {T} tokens, num_tokens is {num_tokens}")
+    words = 0
+    if parents is not None:
+        if mask is None or mask.dim() != 2 or mask.shape[0] != T or (mask_words is not None
+                                                                    and mask.shape[1] != mask_words):
+            raise ValueError("with parents, out.tree_mask must be [tokens, mask_words]")
+        words = int(mask.shape[1])
+    _same_device(dev, new_lens=new_lens, block_table=block_table, block_counts=block_counts, free_blocks=free_blocks,
+                 free_state=free_state, parents=parents, query_start_loc=qsl, context_lens=ctx, slot_mapping=slots,
+                 positions=pos, tree_mask=mask)
+    with _OnDevice(dev):
+        st = lib.build_block_tables(
+            _vector(history_lens, "history_lens", B), _vector(new_lens, "new_lens", B), B,
+            _dev(block_table, "block_table", torch.int32, contiguous=False), int(block_table.stride(0)),
+            int(block_table.shape[1]), _vector(block_counts, "block_counts", B),
+            _dev(free_blocks, "free_blocks", torch.int32), int(free_blocks.numel()),
+            _vector(free_state, "free_state", 2), num_blocks, block_size,
+            _vector(parents, "parents", T) if parents is not None else None,
+            _vector(qsl, "query_start_loc", B + 1), _vector(ctx, "context_lens", B),
+            _vector(slots, "slot_mapping", T, torch.int64), _vector(pos, "positions", T), T,
+            _dev(mask, "tree_mask", torch.int64) if parents is not None else None, words, _stream(stream))
+    _check("build_block_tables", st)
+    return out
+
+
+def tree_workspace_size(batch: int, total_q: int, max_nodes: int, block_table_stride: int, block_size: int,
+                        n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                        partition_tokens: int = 0, kernel: int = 0) -> int:
+    """Workspace bytes of :func:`paged_attention_tree` for these sizes on the current device."""
+    lib = load_library()
+    opts = make_opts(partition_tokens=partition_tokens, prefill_kernel=kernel)
+    return int(lib.paged_attention_tree_workspace_size(batch, total_q, max_nodes, block_table_stride, block_size,
+                                                       n_q_heads, n_kv_heads, head_dim, _code(dtype),
+                                                       ctypes.byref(opts)))
+
+
+def _scratch(nbytes: int, device, stream):
+    """Scratch memory of one call, from the allocator's pool of the stream that the call runs on, so
+    that it is not handed to another stream while the call may still use it (and stays with a graph
+    that is being captured)."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_table, context_lens, scale=None,
+                         out=None, max_nodes: int | None = None, workspace="auto", stream=None, kernel: int = 0,
+                         partition_tokens: int = 0):
+    """Attention of drafted trees: ``q [total_q, Hq, D]`` (sequence b's nodes are rows
+    ``query_start_loc[b] .. query_start_loc[b + 1]``) over each sequence's paged context, whose last
+    positions hold the nodes -> ``out [total_q, Hq, D]``.
+
+    A node sees the history and the nodes set in its row of ``tree_mask`` (int64 [total_q, words], see
+    :func:`build_block_tables`); ``tree_mask`` None: a chain, each node seeing the ones before it and
+    itself.  ``max_nodes`` bounds the nodes of one sequence (default: what the mask, or total_q,
+    allows); a tight bound saves idle blocks.  ``workspace``: "auto" (allocated for the call on its
+    stream), None (contexts are not split) or a caller-owned uint8 CUDA tensor.  ``kernel``: 0 auto, 1
+    CUDA cores, 2 tcgen05.  Rows from ``query_start_loc[batch]`` on are left as they were."""
+    lib = load_library()
+    NB, S, Hkv, D = _pool_dims(k_pool, v_pool)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [total_q, n_q_heads, head_dim]")
+    total_q, Hq, dev = int(q.shape[0]), int(q.shape[1]), q.device
+    B = int(context_lens.numel())
+    if block_table.dim() != 2 or block_table.shape[0] != B or (B and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [batch, max_blocks] with contiguous rows")
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q or tree_mask.shape[1] < 1:
+            raise ValueError("tree_mask must be [total_q, words]")
+        words = int(tree_mask.shape[1])
+    if max_nodes is None:
+        max_nodes = max(1, min(total_q, 64 * words) if words else total_q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    dt = k_pool.dtype
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    _same_device(dev, query_start_loc=query_start_loc, tree_mask=tree_mask, k_pool=k_pool, v_pool=v_pool,
+                 block_table=block_table, context_lens=context_lens, out=out)
+    opts = make_opts(_block_stride_bytes(k_pool, v_pool), prefill_kernel=kernel, partition_tokens=partition_tokens)
+    bt_stride = int(block_table.stride(0))
+    with _OnDevice(dev):
+        ws = workspace
+        if isinstance(workspace, str) and workspace == "auto":
+            n = lib.paged_attention_tree_workspace_size(B, total_q, max_nodes, bt_stride, S, Hq, Hkv, D, _code(dt),
+                                                        ctypes.byref(opts))
+            ws = _scratch(n, dev, stream) if n else None
+        elif ws is not None:
+            _same_device(dev, workspace=ws)
+        st = lib.paged_attention_tree(
+            _dev(out, "out", dt), _dev(q, "q", dt), _vector(query_start_loc, "query_start_loc", B + 1), total_q,
+            _dev(tree_mask, "tree_mask", torch.int64) if words else None, words, max_nodes,
+            _pool(k_pool, "k_pool", dt), _pool(v_pool, "v_pool", dt),
+            _dev(block_table, "block_table", torch.int32, contiguous=False), bt_stride,
+            _vector(context_lens, "context_lens", B), B, NB, S, float(scale), Hq, Hkv, D, _code(dt),
+            _dev(ws, "workspace", torch.uint8) if ws is not None else None, int(ws.numel()) if ws is not None else 0,
+            ctypes.byref(opts), _stream(stream))
+    _check("paged_attention_tree", st)
+    return out
+
+
+def paged_kv_accept(k_pool, v_pool, accepted, accepted_lens, history_lens, block_table, stream=None):
+    """Keep accepted drafted tokens: for every sequence b and ``i < accepted_lens[b]``, the K/V rows of
+    node ``accepted[b, i]`` (position ``history_lens[b] + accepted[b, i]``) move to position
+    ``history_lens[b] + i``.  ``accepted`` int32 [B, A], each list ascending.  The pools are one
+    layer's ``[num_blocks, block_size, Hkv, D]`` or all layers' ``[layers, num_blocks, ...]``."""
+    lib = load_library()
+    if k_pool.dim() != v_pool.dim() or k_pool.dim() not in (4, 5) or k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, n_kv_heads, head_dim], with the "
+                         "layers in front or without")
+    layers, layer_stride = 1, 0
+    k0, v0 = k_pool, v_pool
+    if k_pool.dim() == 5:
+        layers = int(k_pool.shape[0])
+        if layers == 0:
+            return
+        if layers > 1 and k_pool.stride(0) != v_pool.stride(0):
+            raise ValueError("the layers of k_pool and v_pool must be equally far apart")
+        layer_stride = int(k_pool.stride(0)) * k_pool.element_size()
+        k0, v0 = k_pool[0], v_pool[0]
+    NB, S, Hkv, D = _pool_dims(k0, v0)
+    dt, dev = k0.dtype, k0.device
+    B = int(accepted_lens.numel())
+    if accepted.dim() != 2 or accepted.shape[0] != B or (accepted.shape[1] and accepted.stride(1) != 1):
+        raise ValueError("accepted must be [batch, entries] with contiguous rows")
+    if block_table.dim() != 2 or block_table.shape[0] != B or (B and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [batch, max_blocks] with contiguous rows")
+    _same_device(dev, v_pool=v0, accepted=accepted, accepted_lens=accepted_lens, history_lens=history_lens,
+                 block_table=block_table)
+    opts = make_opts(_block_stride_bytes(k0, v0))
+    with _OnDevice(dev):
+        st = lib.paged_kv_accept(
+            _pool(k0, "k_pool"), _pool(v0, "v_pool", dt), layers, layer_stride,
+            _dev(accepted, "accepted", torch.int32, contiguous=False), int(accepted.stride(0)),
+            int(accepted.shape[1]), _vector(accepted_lens, "accepted_lens", B),
+            _vector(history_lens, "history_lens", B), _dev(block_table, "block_table", torch.int32, contiguous=False),
+            int(block_table.stride(0)), B, NB, S, Hkv, D, _code(dt), ctypes.byref(opts), _stream(stream))
+    _check("paged_kv_accept", st)
 
 
 def copy_blocks(k_pool, v_pool, block_pairs, stream=None):

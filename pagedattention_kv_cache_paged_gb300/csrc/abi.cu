@@ -470,6 +470,292 @@ int prefill_impl(void* out, const void* q, const int32_t* query_start_loc, int64
   return finish(e, launches);
 }
 
+// --------------------------------------------------------------------------------------------
+// drafted trees
+// --------------------------------------------------------------------------------------------
+
+// Checked mode of build_block_tables: the same fitting rules as on the device, on the host.
+int validate_tables_step(const TablesArgs& a, cudaStream_t s) {
+  std::vector<int32_t> hist, fresh, counts, state, parents;
+  int rc;
+  if ((rc = copy_to_host(hist, a.history_lens, a.batch, s))) return rc;
+  if ((rc = copy_to_host(fresh, a.new_lens, a.batch, s))) return rc;
+  if ((rc = copy_to_host(counts, a.block_counts, a.batch, s))) return rc;
+  if ((rc = copy_to_host(state, a.free_state, (int64_t)2, s))) return rc;
+  if (state[0] < 0 || state[0] > a.free_capacity) return PA_ERANGE;
+  if (a.parents && (rc = copy_to_host(parents, a.parents, a.token_capacity, s))) return rc;
+  int64_t tok = 0, taken = 0;
+  for (int b = 0; b < a.batch; ++b) {
+    const int64_t h = hist[(size_t)b], m = fresh[(size_t)b], c = counts[(size_t)b];
+    if (h < 0 || m < 0 || h + m > ((int64_t)a.max_blocks << a.block_shift)) return PA_ERANGE;
+    if (c < (h + a.block_size - 1) / a.block_size || c > a.max_blocks) return PA_ERANGE;
+    if (tok + m > a.token_capacity) return PA_ERANGE;
+    const int64_t blocks = (h + m + a.block_size - 1) / a.block_size;
+    if (blocks > c) taken += blocks - c;
+    if (taken > state[0]) return PA_ERANGE;
+    if (a.parents) {
+      if (m > (int64_t)64 * a.mask_words) return PA_ERANGE;
+      for (int64_t j = 0; j < m; ++j) {
+        const int32_t p = parents[(size_t)(tok + j)];
+        if (p < -1 || p >= j) return PA_ERANGE;
+      }
+    }
+    tok += m;
+  }
+  std::vector<int32_t> ids;
+  if ((rc = copy_to_host(ids, a.free_blocks + (state[0] - taken), taken, s))) return rc;
+  for (int32_t id : ids)
+    if (id < 0 || id >= a.num_blocks) return PA_ERANGE;
+  return PA_OK;
+}
+
+int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int batch, int32_t* block_table,
+                      int64_t block_table_stride, int64_t max_blocks, int32_t* block_counts,
+                      const int32_t* free_blocks, int64_t free_capacity, int32_t* free_state, int64_t num_blocks,
+                      int block_size, const int32_t* parents, int32_t* query_start_loc, int32_t* context_lens,
+                      int64_t* slot_mapping, int32_t* positions, int64_t token_capacity, int64_t* tree_mask,
+                      int mask_words, void* stream) {
+  if (batch < 0 || num_blocks <= 0 || max_blocks <= 0 || block_table_stride < max_blocks || free_capacity < 0 ||
+      free_capacity > INT32_MAX || token_capacity < 0 || token_capacity > INT32_MAX || block_size <= 0)
+    return PA_EINVAL;
+  if (!is_pow2(block_size) || block_size > 256) return PA_EUNSUPPORTED;
+  if (batch == 0) return PA_OK;
+  if (!history_lens || !new_lens || !block_table || !block_counts || !free_state || !query_start_loc || !context_lens)
+    return PA_EINVAL;
+  if (free_capacity > 0 && !free_blocks) return PA_EINVAL;
+  if (token_capacity > 0 && (!slot_mapping || !positions)) return PA_EINVAL;
+  if (parents && (mask_words < 1 || mask_words > (INT32_MAX >> 6) || (token_capacity > 0 && !tree_mask)))
+    return PA_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned* err = nullptr;
+  int rc = device_info(&err, nullptr);
+  if (rc) return rc;
+  TablesArgs a{};
+  a.history_lens = history_lens;
+  a.new_lens = new_lens;
+  a.batch = batch;
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.block_size = block_size;
+  a.block_shift = log2i(block_size);
+  // positions are int32: entries past what they reach are never used
+  a.max_blocks = (int32_t)(max_blocks < (INT32_MAX >> a.block_shift) ? max_blocks : (INT32_MAX >> a.block_shift));
+  a.block_counts = block_counts;
+  a.free_blocks = free_blocks;
+  a.free_capacity = free_capacity;
+  a.free_state = free_state;
+  a.num_blocks = num_blocks;
+  a.parents = parents;
+  a.query_start_loc = query_start_loc;
+  a.context_lens = context_lens;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.token_capacity = token_capacity;
+  a.tree_mask = tree_mask;
+  a.mask_words = parents ? mask_words : 0;
+  a.err = err;
+  if (checked() && (rc = validate_tables_step(a, s))) return rc;
+  int launches = 0;
+  cudaError_t e = launch_block_tables(a, s, &launches);
+  return finish(e, launches);
+}
+
+// Split plan of the tree attention: partitions of 256 to 1024 tokens, as many as give every SM two
+// CTAs when all rows are as long as their table allows.
+void plan_tree(int batch, int max_nodes, int n_kv_heads, int group, int sms, int64_t bt_stride, int block_size,
+               int64_t partition_tokens, int* part_tokens, int* max_parts) {
+  const int64_t max_len = table_capacity(bt_stride, block_size);
+  int64_t p = partition_tokens;
+  if (p <= 0) {
+    const int64_t rows = (int64_t)batch * n_kv_heads * (((int64_t)max_nodes * group + 127) / 128);
+    const int64_t wave = (int64_t)(sms > 0 ? sms : 1) * 2;
+    const int64_t parts = wave / rows > 1 ? wave / rows : 1;
+    p = (max_len + parts - 1) / parts;
+    p = p < 256 ? 256 : (p > 1024 ? 1024 : p);
+  }
+  p = (p + block_size - 1) / block_size * block_size;
+  if (p >= max_len) {
+    *part_tokens = (int)(max_len > 0 ? max_len : block_size);
+    *max_parts = 1;
+    return;
+  }
+  *part_tokens = (int)p;
+  *max_parts = (int)((max_len + p - 1) / p);
+}
+
+size_t tree_workspace_impl(int batch, int64_t total_q, int max_nodes, int64_t block_table_stride, int block_size,
+                           int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts) {
+  if (batch <= 0 || total_q <= 0 || max_nodes <= 0 || block_table_stride <= 0 || block_size <= 0 || n_q_heads <= 0 ||
+      n_kv_heads <= 0 || head_dim <= 0 || n_q_heads % n_kv_heads != 0 || check_dtype(dtype))
+    return 0;
+  pa_opts o;
+  if (read_opts(opts, &o)) return 0;
+  int sms = 0;
+  if (device_info(nullptr, &sms)) return 0;
+  int part = 0, max_parts = 1;
+  plan_tree(batch, max_nodes, n_kv_heads, n_q_heads / n_kv_heads, sms, block_table_stride, block_size,
+            o.partition_tokens, &part, &max_parts);
+  return workspace_layout(total_q * n_q_heads, max_parts, head_dim).bytes;
+}
+
+int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q, const int64_t* tree_mask,
+              int mask_words, int max_nodes, const void* k_pool, const void* v_pool, const int32_t* block_table,
+              int64_t block_table_stride, const int32_t* context_lens, int batch, int64_t num_blocks, int block_size,
+              float scale, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, void* workspace,
+              size_t workspace_bytes, const pa_opts* opts, void* stream) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  pa_opts o;
+  if ((rc = read_opts(opts, &o))) return rc;
+  if ((rc = check_heads(n_q_heads, n_kv_heads, head_dim))) return rc;
+  if (batch < 0 || total_q < 0 || num_blocks <= 0 || block_table_stride <= 0 || block_size <= 0 || max_nodes < 1)
+    return PA_EINVAL;
+  if (!is_pow2(block_size) || block_size > 256) return PA_EUNSUPPORTED;
+  if (!(scale > 0.f) || scale > 3.0e38f) return PA_EINVAL;
+  if (tree_mask && (mask_words < 1 || mask_words > (INT32_MAX >> 6))) return PA_EINVAL;
+  if (batch == 0 || total_q == 0) return PA_OK;
+  if (total_q > INT32_MAX) return PA_EINVAL;
+  if (!out || !q || !query_start_loc || !k_pool || !v_pool || !block_table || !context_lens) return PA_EINVAL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return PA_EINVAL;
+  if (max_nodes > total_q) max_nodes = (int)total_q;
+  const int64_t block_elems = (int64_t)block_size * n_kv_heads * head_dim;
+  int64_t stride_bytes = 0;
+  if ((rc = pool_block_stride(o, block_elems * dtype_bytes(dtype), &stride_bytes))) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned* err = nullptr;
+  int sms = 0;
+  if ((rc = device_info(&err, &sms))) return rc;
+  const int group = n_q_heads / n_kv_heads;
+  if (o.prefill_kernel == 2) return PA_EUNSUPPORTED;
+  int part_tokens = 0, max_parts = 1;
+  plan_tree(batch, max_nodes, n_kv_heads, group, sms, block_table_stride, block_size, o.partition_tokens,
+            &part_tokens, &max_parts);
+  const WsLayout ws = workspace_layout(total_q * n_q_heads, max_parts, head_dim);
+  if (max_parts > 1) {
+    if (workspace == nullptr) {
+      max_parts = 1;
+      part_tokens = (int)table_capacity(block_table_stride, block_size);
+    } else if (workspace_bytes < ws.bytes || !aligned16(workspace)) {
+      return PA_EWORKSPACE;
+    }
+  }
+  if (checked()) {
+    std::vector<int32_t> lens, qsl;
+    rc = validate_tables(block_table, block_table_stride, context_lens, batch, num_blocks, block_size, s, &lens);
+    if (rc) return rc;
+    if ((rc = copy_to_host(qsl, query_start_loc, (int64_t)batch + 1, s))) return rc;
+    if (qsl[0] < 0 || qsl[(size_t)batch] > total_q) return PA_ERANGE;
+    for (int b = 0; b < batch; ++b) {
+      const int64_t m = (int64_t)qsl[(size_t)b + 1] - qsl[(size_t)b];
+      if (m < 0 || m > max_nodes || m > lens[(size_t)b]) return PA_ERANGE;
+      if (tree_mask && m > (int64_t)64 * mask_words) return PA_ERANGE;
+    }
+  }
+  TreeArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.tree_mask = tree_mask;
+  a.mask_words = mask_words;
+  a.max_nodes = max_nodes;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.block_shift = log2i(block_size);
+  a.kv_block_stride = stride_bytes / dtype_bytes(dtype);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.n_q_heads = n_q_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.group = group;
+  a.group_shift = log2i(group);
+  a.head_dim = head_dim;
+  a.part_tokens = part_tokens;
+  a.max_parts = max_parts;
+  if (max_parts > 1) {
+    char* base = static_cast<char*>(workspace);
+    a.ws_acc = reinterpret_cast<float*>(base);
+    a.ws_m = reinterpret_cast<float*>(base + ws.off_m);
+    a.ws_l = reinterpret_cast<float*>(base + ws.off_l);
+  }
+  a.err = err;
+  a.epoch = next_epoch();
+  int launches = 0;
+  cudaError_t e = launch_tree_simt(a, dtype, s, &launches);
+  if (e == cudaSuccess && max_parts > 1) e = launch_tree_merge(a, dtype, s, &launches);
+  return finish(e, launches);
+}
+
+int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride_bytes, const int32_t* accepted,
+                int64_t accepted_stride, int max_accepted, const int32_t* accepted_lens, const int32_t* history_lens,
+                const int32_t* block_table, int64_t block_table_stride, int batch, int64_t num_blocks, int block_size,
+                int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts, void* stream) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  pa_opts o;
+  if ((rc = read_opts(opts, &o))) return rc;
+  if (batch < 0 || num_layers < 0 || max_accepted < 0 || accepted_stride < max_accepted || num_blocks <= 0 ||
+      block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0 || block_table_stride <= 0)
+    return PA_EINVAL;
+  if (num_layers > 1 && (layer_stride_bytes <= 0 || layer_stride_bytes % 16 != 0)) return PA_EINVAL;
+  if (batch == 0 || num_layers == 0 || max_accepted == 0) return PA_OK;
+  if (!k_pool || !v_pool || !accepted || !accepted_lens || !history_lens || !block_table) return PA_EINVAL;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_EINVAL;
+  const int64_t row_bytes = (int64_t)n_kv_heads * head_dim * dtype_bytes(dtype);
+  if (row_bytes % 16 != 0) return PA_EUNSUPPORTED;
+  if (row_bytes / 16 > (INT32_MAX >> 1)) return PA_EUNSUPPORTED;
+  int64_t stride_bytes = 0;
+  if ((rc = pool_block_stride(o, row_bytes * block_size, &stride_bytes))) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned* err = nullptr;
+  if ((rc = device_info(&err, nullptr))) return rc;
+  if (checked()) {
+    std::vector<int32_t> acc, acc_lens, hist, table;
+    if ((rc = copy_to_host(acc_lens, accepted_lens, batch, s))) return rc;
+    if ((rc = copy_to_host(hist, history_lens, batch, s))) return rc;
+    if ((rc = copy_to_host(acc, accepted, (int64_t)(batch - 1) * accepted_stride + max_accepted, s))) return rc;
+    if ((rc = copy_to_host(table, block_table, (int64_t)batch * block_table_stride, s))) return rc;
+    for (int b = 0; b < batch; ++b) {
+      if (acc_lens[(size_t)b] < 0 || acc_lens[(size_t)b] > max_accepted || hist[(size_t)b] < 0) return PA_ERANGE;
+      for (int i = 0; i < acc_lens[(size_t)b]; ++i) {
+        const int64_t idx = acc[(size_t)(b * accepted_stride + i)];
+        const int64_t src = hist[(size_t)b] + idx, dst = hist[(size_t)b] + i;
+        if (idx < i || src >= block_table_stride * block_size) return PA_ERANGE;
+        for (const int64_t p : {src, dst}) {
+          const int32_t id = table[(size_t)(b * block_table_stride + p / block_size)];
+          if (id < 0 || id >= num_blocks) return PA_ERANGE;
+        }
+      }
+    }
+  }
+  AcceptArgs a{};
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.num_layers = num_layers;
+  a.layer_stride_vecs = num_layers > 1 ? layer_stride_bytes / 16 : 0;
+  a.accepted = accepted;
+  a.accepted_stride = accepted_stride;
+  a.max_accepted = max_accepted;
+  a.accepted_lens = accepted_lens;
+  a.history_lens = history_lens;
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.batch = batch;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.row_vecs = (int)(row_bytes / 16);
+  a.block_stride_vecs = stride_bytes / 16;
+  a.err = err;
+  int launches = 0;
+  cudaError_t e = launch_kv_accept(a, s, &launches);
+  return finish(e, launches);
+}
+
 int copy_blocks_impl(void* k_pool, void* v_pool, const int64_t* block_pairs, int64_t n_pairs, int64_t num_blocks,
                      int64_t block_bytes, const pa_opts* opts, void* stream) {
   pa_opts o;
@@ -733,6 +1019,45 @@ int paged_attention_prefill_ex(void* out, const void* q, const int32_t* query_st
   return prefill_impl(out, q, query_start_loc, total_q, k_pool, v_pool, block_table, block_table_stride,
                       context_lens, batch, num_blocks, block_size, scale, n_q_heads, n_kv_heads, head_dim, dtype,
                       opts, stream);
+}
+
+int build_block_tables(const int32_t* history_lens, const int32_t* new_lens, int batch, int32_t* block_table,
+                       int64_t block_table_stride, int64_t max_blocks, int32_t* block_counts,
+                       const int32_t* free_blocks, int64_t free_capacity, int32_t* free_state, int64_t num_blocks,
+                       int block_size, const int32_t* parents, int32_t* query_start_loc, int32_t* context_lens,
+                       int64_t* slot_mapping, int32_t* positions, int64_t token_capacity, int64_t* tree_mask,
+                       int mask_words, void* stream) {
+  return block_tables_impl(history_lens, new_lens, batch, block_table, block_table_stride, max_blocks, block_counts,
+                           free_blocks, free_capacity, free_state, num_blocks, block_size, parents, query_start_loc,
+                           context_lens, slot_mapping, positions, token_capacity, tree_mask, mask_words, stream);
+}
+
+int paged_attention_tree(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q,
+                         const int64_t* tree_mask, int mask_words, int max_nodes, const void* k_pool,
+                         const void* v_pool, const int32_t* block_table, int64_t block_table_stride,
+                         const int32_t* context_lens, int batch, int64_t num_blocks, int block_size, float scale,
+                         int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, void* workspace,
+                         size_t workspace_bytes, const pa_opts* opts, void* stream) {
+  return tree_impl(out, q, query_start_loc, total_q, tree_mask, mask_words, max_nodes, k_pool, v_pool, block_table,
+                   block_table_stride, context_lens, batch, num_blocks, block_size, scale, n_q_heads, n_kv_heads,
+                   head_dim, dtype, workspace, workspace_bytes, opts, stream);
+}
+
+size_t paged_attention_tree_workspace_size(int batch, int64_t total_q, int max_nodes, int64_t block_table_stride,
+                                           int block_size, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype,
+                                           const pa_opts* opts) {
+  return tree_workspace_impl(batch, total_q, max_nodes, block_table_stride, block_size, n_q_heads, n_kv_heads,
+                             head_dim, dtype, opts);
+}
+
+int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride_bytes, const int32_t* accepted,
+                    int64_t accepted_stride, int max_accepted, const int32_t* accepted_lens,
+                    const int32_t* history_lens, const int32_t* block_table, int64_t block_table_stride, int batch,
+                    int64_t num_blocks, int block_size, int n_kv_heads, int head_dim, pa_dtype dtype,
+                    const pa_opts* opts, void* stream) {
+  return accept_impl(k_pool, v_pool, num_layers, layer_stride_bytes, accepted, accepted_stride, max_accepted,
+                     accepted_lens, history_lens, block_table, block_table_stride, batch, num_blocks, block_size,
+                     n_kv_heads, head_dim, dtype, opts, stream);
 }
 
 int copy_blocks(void* k_pool, void* v_pool, const int64_t* block_pairs, int64_t n_pairs,

@@ -116,12 +116,98 @@ struct MergeArgs {
   int64_t max_len;                 // clamp for context_lens (bt_stride * block_size)
 };
 
+// build_block_tables (see include/pagedattn.h for the arrays).
+struct TablesArgs {
+  const int32_t* history_lens;
+  const int32_t* new_lens;
+  int batch;
+  int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;              // entries of a table row (clamped so that positions fit int32)
+  int32_t* block_counts;
+  const int32_t* free_blocks;
+  int64_t free_capacity;
+  int32_t* free_state;
+  int64_t num_blocks;
+  int block_size;
+  int block_shift;
+  const int32_t* parents;          // nullptr: chains
+  int32_t* query_start_loc;
+  int32_t* context_lens;
+  int64_t* slot_mapping;
+  int32_t* positions;
+  int64_t token_capacity;
+  int64_t* tree_mask;
+  int mask_words;
+  unsigned* err;
+};
+
+// paged_attention_tree: one launch over (sequence, tile of its nodes, KV head, partition).
+struct TreeArgs {
+  void* out;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  const int64_t* tree_mask;        // nullptr: chains
+  int mask_words;
+  int max_nodes;
+  int batch;
+  int64_t total_q;
+  int64_t num_blocks;
+  int block_size;
+  int block_shift;
+  int64_t kv_block_stride;         // elements from one block of a pool to the next
+  float scale_log2;                // scale * log2(e)
+  int n_q_heads;
+  int n_kv_heads;
+  int group;
+  int group_shift;                 // log2(group)
+  int head_dim;
+  int part_tokens;                 // tokens per partition
+  int max_parts;                   // partitions per row in the grid (1 = no split)
+  float* ws_m;                     // [total_q * n_q_heads][max_parts]
+  float* ws_l;
+  float* ws_acc;                   // [total_q * n_q_heads][max_parts][head_dim]
+  unsigned* err;
+  unsigned epoch;
+};
+
+struct AcceptArgs {
+  void* k_pool;
+  void* v_pool;
+  int num_layers;
+  int64_t layer_stride_vecs;       // 16-byte vectors from one layer's pool to the next
+  const int32_t* accepted;
+  int64_t accepted_stride;
+  int max_accepted;
+  const int32_t* accepted_lens;
+  const int32_t* history_lens;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int batch;
+  int64_t num_blocks;
+  int block_size;
+  int row_vecs;                    // 16-byte vectors per token row
+  int64_t block_stride_vecs;
+  unsigned* err;
+};
+
 // Launchers: return cudaSuccess or the launch error.  `launches` is incremented per kernel.
 cudaError_t launch_kv_write(const KvWriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_swap_blocks(const SwapArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_attn_simt(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_lse_merge(const MergeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+
+cudaError_t launch_block_tables(const TablesArgs& a, cudaStream_t s, int* launches);
+cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s, int* launches);
+// Tree attention on CUDA cores (every dtype and shape), then the merge of split contexts.
+cudaError_t launch_tree_simt(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+cudaError_t launch_tree_merge(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 
 // TMA view of a pool: 3-D tensor (column = n_kv_heads * head_dim, token in block, block) with the
 // pool's block stride, boxes of 64 columns x 16 tokens x 1 block, 128-byte swizzle.
