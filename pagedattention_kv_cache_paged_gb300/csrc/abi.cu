@@ -626,7 +626,9 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   int sms = 0;
   if ((rc = device_info(&err, &sms))) return rc;
   const int group = n_q_heads / n_kv_heads;
-  if (o.prefill_kernel == 2) return PA_EUNSUPPORTED;
+  const bool tc_ok = decode_tc_supported(dtype, block_size, head_dim, group, num_blocks);
+  if (o.prefill_kernel == 2 && !tc_ok) return PA_EUNSUPPORTED;
+  const bool use_tc = o.prefill_kernel == 2 || (o.prefill_kernel == 0 && tc_ok);
   int part_tokens = 0, max_parts = 1;
   plan_tree(batch, max_nodes, n_kv_heads, group, sms, block_table_stride, block_size, o.partition_tokens,
             &part_tokens, &max_parts);
@@ -686,7 +688,7 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.err = err;
   a.epoch = next_epoch();
   int launches = 0;
-  cudaError_t e = launch_tree_simt(a, dtype, s, &launches);
+  cudaError_t e = use_tc ? launch_tree_umma(a, dtype, s, &launches) : launch_tree_simt(a, dtype, s, &launches);
   if (e == cudaSuccess && max_parts > 1) e = launch_tree_merge(a, dtype, s, &launches);
   return finish(e, launches);
 }

@@ -207,6 +207,8 @@ cudaError_t launch_block_tables(const TablesArgs& a, cudaStream_t s, int* launch
 cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s, int* launches);
 // Tree attention on CUDA cores (every dtype and shape), then the merge of split contexts.
 cudaError_t launch_tree_simt(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+// The same on tcgen05 tensor cores (the support set of the tensor-core decode).
+cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_tree_merge(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 
 // TMA view of a pool: 3-D tensor (column = n_kv_heads * head_dim, token in block, block) with the
