@@ -137,8 +137,11 @@ __global__ void __launch_bounds__(kTuThreads, 2)
   uint64_t* q_ready = bars + 16;
   uint64_t* s_full = bars + 17;   // [2] S(j) in buffer j % 2
   uint64_t* p_full = bars + 19;   // [2] P(j) written (and O rescaled)
-  uint64_t* pv_done = bars + 21;  // one phase per tile: O += P(j) V(j) done
-  uint64_t* fin = bars + 22;      // a launch that gave up: its products are over
+  uint64_t* pv_done = bars + 21;  // [2] O += P(j) V(j) done, in barrier j % 2
+  // (a wait tells a phase from the next one only: at the end the last two products may be outstanding or
+  // both over, so the last one has a barrier of its own)
+  uint64_t* o_full = bars + 23;   // O complete
+  uint64_t* fin = bars + 24;      // a launch that gave up: its products are over
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
   int* bad_v = reinterpret_cast<int*>(base + 516);  // V of the drafted region holds non-finite elements
   volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 544);  // [8] sub-tiles loaded, per tile
@@ -197,9 +200,10 @@ __global__ void __launch_bounds__(kTuThreads, 2)
     for (int k = 0; k < 2; ++k) {
       mbar_init(&s_full[k], 1);
       mbar_init(&p_full[k], 32 * live_warps);
+      mbar_init(&pv_done[k], 1);
     }
     mbar_init(q_ready, 1);
-    mbar_init(pv_done, 1);
+    mbar_init(o_full, 1);
     mbar_init(fin, 1);
     *bad_v = 0;
     fence_barrier_init();
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(kTuThreads, 2)
           umma_ts(tO, tS(j & 1) + 8u * (uint32_t)kk, umma_desc_sw128(va + kk * 2048, Cfg::kKvHalf, 1024), id_pv,
                   (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&vempty[j % kStages]);
-        umma_commit(pv_done);
+        umma_commit(j == n_tiles - 1 ? o_full : &pv_done[j & 1]);
       }
       if (!ok) {
         raise_timeout(a.err, a.epoch);
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kTuThreads, 2)
       l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
       if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
         // O is stable once the product of tile j - 1 is done; that of tile j waits for this warp
-        if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (unsigned)((j - 1) & 1), a.err, a.epoch))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(j - 1) & 1], (unsigned)(((j - 1) >> 1) & 1), a.err, a.epoch))) {
           alive = false;
           return;
         }
@@ -492,10 +496,7 @@ __global__ void __launch_bounds__(kTuThreads, 2)
         tc_fence_before();
         mbar_arrive(&p_full[j & 1]);
       }
-      // the last two products may still be running (S of the last tile was issued before the first of
-      // them), and a wait tells one phase from the next only: one after the other
-      for (int j = max(n_tiles - 2, 0); j < n_tiles && alive; ++j)
-        alive = __all_sync(0xffffffffu, mbar_wait(pv_done, (unsigned)(j & 1), a.err, a.epoch));
+      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(o_full, 0, a.err, a.epoch));
       tc_fence_after();
       if (!alive && lane == 0) raise_timeout(a.err, a.epoch);
     }
