@@ -560,42 +560,83 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
   return finish(e, launches);
 }
 
-// Split plan of the tree attention: partitions of 256 to 1024 tokens, as many as give every SM two
-// CTAs when all rows are as long as their table allows.
-void plan_tree(int batch, int max_nodes, int n_kv_heads, int group, int sms, int64_t bt_stride, int block_size,
-               int64_t partition_tokens, int* part_tokens, int* max_parts) {
+// How a tree-attention call divides its work and what its partial states take (one plan for the launch
+// and for the size the caller asks for).
+struct TreePlan {
+  int part_tokens = 0, max_parts = 1;  // CUDA cores
+  int ctas = 0, share = 0;             // tcgen05
+  size_t bytes = 0, off_m = 0, off_l = 0, off_rec = 0;
+};
+
+TreePlan plan_tree(bool tensor_cores, int batch, int64_t total_q, int max_nodes, int n_q_heads, int n_kv_heads,
+                   int head_dim, int sms, int64_t bt_stride, int block_size, int64_t partition_tokens) {
+  TreePlan p;
+  const int group = n_q_heads / n_kv_heads;
   const int64_t max_len = table_capacity(bt_stride, block_size);
-  int64_t p = partition_tokens;
-  if (p <= 0) {
-    const int64_t rows = (int64_t)batch * n_kv_heads * (((int64_t)max_nodes * group + 127) / 128);
-    const int64_t wave = (int64_t)(sms > 0 ? sms : 1) * 2;
-    const int64_t parts = wave / rows > 1 ? wave / rows : 1;
-    p = (max_len + parts - 1) / parts;
-    p = p < 256 ? 256 : (p > 1024 ? 1024 : p);
+  auto up16 = [](size_t x) { return (x + 15) & ~size_t(15); };
+  if (sms < 1) sms = 1;
+  if (tensor_cores) {
+    // one CTA per SM, each with an equal share; an explicit partition length sets the share instead
+    const int unit_rows = tree_unit_rows(max_nodes, group);
+    const int64_t units = (int64_t)batch * n_kv_heads * (((int64_t)max_nodes * group + unit_rows - 1) / unit_rows);
+    const int64_t tiles = (max_len + 63) / 64;
+    bool split = tiles > 8;  // (shorter contexts are never cut, see tu_schedule)
+    int64_t ctas = units < sms ? units * (tiles < sms ? tiles : sms) : sms;
+    ctas = ctas < sms ? ctas : sms;
+    if (partition_tokens > 0) {
+      p.share = (int)((partition_tokens + 63) / 64);
+      ctas = (units * tiles + p.share - 1) / p.share;
+      split = tiles > 1;
+    }
+    p.ctas = (int)(ctas < 65535 ? ctas : 65535);  // (grid.y of the join)
+    if (partition_tokens > 0 && ctas > 65535) p.share = (int)((units * tiles + 65534) / 65535);
+    if (split) {
+      const size_t rows = (size_t)p.ctas * 2 * (size_t)unit_rows;
+      p.off_m = rows * (size_t)head_dim * sizeof(float);
+      p.off_l = p.off_m + up16(rows * sizeof(float));
+      p.off_rec = p.off_l + up16(rows * sizeof(float));
+      p.bytes = p.off_rec + up16((size_t)p.ctas * sizeof(TreeRec));
+    }
+    return p;
   }
-  p = (p + block_size - 1) / block_size * block_size;
-  if (p >= max_len) {
-    *part_tokens = (int)(max_len > 0 ? max_len : block_size);
-    *max_parts = 1;
-    return;
+  // partitions of 256 to 1024 tokens, as many as give every SM two CTAs when all rows are as long as
+  // their table allows
+  int64_t part = partition_tokens;
+  if (part <= 0) {
+    const int64_t rows = (int64_t)batch * n_kv_heads * max_nodes;
+    const int64_t parts = 2 * sms / rows > 1 ? 2 * sms / rows : 1;
+    part = (max_len + parts - 1) / parts;
+    part = part < 256 ? 256 : (part > 1024 ? 1024 : part);
   }
-  *part_tokens = (int)p;
-  *max_parts = (int)((max_len + p - 1) / p);
+  part = (part + block_size - 1) / block_size * block_size;
+  if (part >= max_len) {
+    p.part_tokens = (int)(max_len > 0 ? max_len : block_size);
+    return p;
+  }
+  p.part_tokens = (int)part;
+  p.max_parts = (int)((max_len + part - 1) / part);
+  const WsLayout w = workspace_layout(total_q * n_q_heads, p.max_parts, head_dim);
+  p.bytes = w.bytes;
+  p.off_m = w.off_m;
+  p.off_l = w.off_l;
+  return p;
 }
 
 size_t tree_workspace_impl(int batch, int64_t total_q, int max_nodes, int64_t block_table_stride, int block_size,
                            int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts) {
   if (batch <= 0 || total_q <= 0 || max_nodes <= 0 || block_table_stride <= 0 || block_size <= 0 || n_q_heads <= 0 ||
-      n_kv_heads <= 0 || head_dim <= 0 || n_q_heads % n_kv_heads != 0 || check_dtype(dtype))
+      n_kv_heads <= 0 || head_dim <= 0 || check_dtype(dtype) || check_heads(n_q_heads, n_kv_heads, head_dim))
     return 0;
   pa_opts o;
   if (read_opts(opts, &o)) return 0;
   int sms = 0;
   if (device_info(nullptr, &sms)) return 0;
-  int part = 0, max_parts = 1;
-  plan_tree(batch, max_nodes, n_kv_heads, n_q_heads / n_kv_heads, sms, block_table_stride, block_size,
-            o.partition_tokens, &part, &max_parts);
-  return workspace_layout(total_q * n_q_heads, max_parts, head_dim).bytes;
+  if (max_nodes > total_q) max_nodes = (int)total_q;
+  const bool use_tc =
+      o.prefill_kernel != 1 && decode_tc_supported(dtype, block_size, head_dim, n_q_heads / n_kv_heads, 1);
+  return plan_tree(use_tc, batch, total_q, max_nodes, n_q_heads, n_kv_heads, head_dim, sms, block_table_stride,
+                   block_size, o.partition_tokens)
+      .bytes;
 }
 
 int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q, const int64_t* tree_mask,
@@ -629,17 +670,13 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   const bool tc_ok = decode_tc_supported(dtype, block_size, head_dim, group, num_blocks);
   if (o.prefill_kernel == 2 && !tc_ok) return PA_EUNSUPPORTED;
   const bool use_tc = o.prefill_kernel == 2 || (o.prefill_kernel == 0 && tc_ok);
-  int part_tokens = 0, max_parts = 1;
-  plan_tree(batch, max_nodes, n_kv_heads, group, sms, block_table_stride, block_size, o.partition_tokens,
-            &part_tokens, &max_parts);
-  const WsLayout ws = workspace_layout(total_q * n_q_heads, max_parts, head_dim);
-  if (max_parts > 1) {
-    if (workspace == nullptr) {
-      max_parts = 1;
-      part_tokens = (int)table_capacity(block_table_stride, block_size);
-    } else if (workspace_bytes < ws.bytes || !aligned16(workspace)) {
-      return PA_EWORKSPACE;
-    }
+  TreePlan plan = plan_tree(use_tc, batch, total_q, max_nodes, n_q_heads, n_kv_heads, head_dim, sms,
+                            block_table_stride, block_size, o.partition_tokens);
+  const bool split = plan.bytes > 0 && workspace != nullptr;
+  if (split && (workspace_bytes < plan.bytes || !aligned16(workspace))) return PA_EWORKSPACE;
+  if (!split) {
+    plan.max_parts = 1;
+    plan.part_tokens = (int)table_capacity(block_table_stride, block_size);
   }
   if (checked()) {
     std::vector<int32_t> lens, qsl;
@@ -677,19 +714,24 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.group = group;
   a.group_shift = log2i(group);
   a.head_dim = head_dim;
-  a.part_tokens = part_tokens;
-  a.max_parts = max_parts;
-  if (max_parts > 1) {
+  a.part_tokens = plan.part_tokens;
+  a.max_parts = plan.max_parts;
+  a.ctas = plan.ctas;
+  a.share = plan.share;
+  a.split = split;
+  if (split) {
     char* base = static_cast<char*>(workspace);
     a.ws_acc = reinterpret_cast<float*>(base);
-    a.ws_m = reinterpret_cast<float*>(base + ws.off_m);
-    a.ws_l = reinterpret_cast<float*>(base + ws.off_l);
+    a.ws_m = reinterpret_cast<float*>(base + plan.off_m);
+    a.ws_l = reinterpret_cast<float*>(base + plan.off_l);
+    a.ws_rec = reinterpret_cast<TreeRec*>(base + plan.off_rec);
   }
   a.err = err;
   a.epoch = next_epoch();
   int launches = 0;
   cudaError_t e = use_tc ? launch_tree_umma(a, dtype, s, &launches) : launch_tree_simt(a, dtype, s, &launches);
-  if (e == cudaSuccess && max_parts > 1) e = launch_tree_merge(a, dtype, s, &launches);
+  if (e == cudaSuccess && split)
+    e = use_tc ? launch_tree_join(a, dtype, s, &launches) : launch_tree_merge(a, dtype, s, &launches);
   return finish(e, launches);
 }
 

@@ -167,14 +167,34 @@ struct TreeArgs {
   int group;
   int group_shift;                 // log2(group)
   int head_dim;
-  int part_tokens;                 // tokens per partition
-  int max_parts;                   // partitions per row in the grid (1 = no split)
-  float* ws_m;                     // [total_q * n_q_heads][max_parts]
+  // CUDA-core kernel: partitions of part_tokens keys, max_parts per row in the grid (1 = no split);
+  // partial states ws_m, ws_l [total_q * n_q_heads][max_parts], ws_acc [..][max_parts][head_dim]
+  int part_tokens;
+  int max_parts;
+  // tcgen05 kernel: `ctas` CTAs that take `share` key tiles each (0: an equal share of the work), units
+  // cut where needed if `split`; two partial states per CTA, ws_m, ws_l [ctas][2][rows],
+  // ws_acc [ctas][2][rows][head_dim], and a record of the unit cut at its end, ws_rec [ctas]
+  int ctas;
+  int share;
+  int split;
+  struct TreeRec* ws_rec;
+  float* ws_m;
   float* ws_l;
-  float* ws_acc;                   // [total_q * n_q_heads][max_parts][head_dim]
+  float* ws_acc;
   unsigned* err;
   unsigned epoch;
 };
+
+// A unit whose first piece CTA c computed (in its second slot) and whose last one CTA `last` did: rows
+// of the output from row0 on (rows = 0: none).
+struct TreeRec {
+  int64_t row0;
+  int32_t rows;
+  int32_t last;
+};
+
+// Rows of a unit of the tcgen05 tree attention: one or two tiles of 128 (node, head) rows.
+inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes * group <= 128 ? 128 : 256; }
 
 struct AcceptArgs {
   void* k_pool;
@@ -209,6 +229,7 @@ cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s, int* launches)
 cudaError_t launch_tree_simt(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 // The same on tcgen05 tensor cores (the support set of the tensor-core decode).
 cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+cudaError_t launch_tree_join(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_tree_merge(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 
 // TMA view of a pool: 3-D tensor (column = n_kv_heads * head_dim, token in block, block) with the

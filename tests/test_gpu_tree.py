@@ -285,7 +285,8 @@ def test_other_streams_and_a_captured_step_share_nothing(cuda_lib, kernel):
 def test_workspaces(cuda_lib, kernel):
     pa = cuda_lib
     case = TreeCase(30, [900, 300], [16, 9], q_heads=8, kv_heads=2, head_dim=64, block_size=16, dtype=BF16)
-    n = pa.tree_workspace_size(2, 25, 16, case.table.shape[1], 16, 8, 2, 64, BF16, partition_tokens=64)
+    n = pa.tree_workspace_size(2, 25, 16, case.table.shape[1], 16, 8, 2, 64, BF16, partition_tokens=64,
+                               kernel=kernel)
     assert n > 0
     auto = run(pa, case, kernel=kernel, partition_tokens=64, max_nodes=16)
     own = run(pa, case, kernel=kernel, partition_tokens=64, max_nodes=16,
