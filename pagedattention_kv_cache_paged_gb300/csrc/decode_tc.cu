@@ -479,6 +479,22 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, pa_dtype dt, int64_t nu
   return r == CUDA_SUCCESS;
 }
 
+bool encode_group_map(CUtensorMap* map, const void* pool, pa_dtype dt, int64_t num_blocks, int block_size,
+                      int n_kv_heads, int head_dim, int64_t block_stride) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = (cuuint64_t)n_kv_heads * head_dim * 2;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)n_kv_heads * head_dim / 64, (cuuint64_t)block_size / 8,
+                              (cuuint64_t)num_blocks};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)block_stride * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)head_dim / 64, (cuuint32_t)(block_size < 64 ? block_size : 64) / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapDataType ty = dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUresult r = fn(map, ty, 5, const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Queries [total_q][n_q_heads][head_dim] viewed as a 3-D tensor (column, head, token); boxes of 64
 // columns x heads_box heads x tokens_box tokens with the 128-byte swizzle, so that one box lands as
 // heads_box * tokens_box rows of 128 bytes ordered (token, head).  Rows past total_q read as zeros.

@@ -237,6 +237,12 @@ cudaError_t launch_tree_merge(const TreeArgs& a, pa_dtype dt, cudaStream_t s, in
 bool encode_pool_map(CUtensorMap* map, const void* pool, pa_dtype dt, int64_t num_blocks, int block_size,
                      int n_kv_heads, int head_dim, int64_t block_stride);
 
+// TMA view of a pool for whole rows of a KV head: 5-D tensor (column in a 64-column half, token in an 8-token
+// group, half, group in block, block), boxes of min(block_size, 64) tokens x head_dim, 128-byte swizzle: a
+// box lands as [group][half][8 rows of 128 bytes].
+bool encode_group_map(CUtensorMap* map, const void* pool, pa_dtype dt, int64_t num_blocks, int block_size,
+                      int n_kv_heads, int head_dim, int64_t block_stride);
+
 // TMA view of the queries [total_q][n_q_heads][head_dim]: 3-D tensor (column, head, token), boxes of
 // 64 columns x heads_box heads x tokens_box tokens, 128-byte swizzle, rows past total_q read as zeros.
 bool encode_q_map(CUtensorMap* map, const void* q, pa_dtype dt, int64_t total_q, int n_q_heads, int head_dim,

@@ -4,9 +4,13 @@
 // S = Q K^T into a TMEM buffer, the softmax threads (one TMEM lane each) turn it into P in place, O +=
 // P V in TMEM; one pass with a running stabiliser that moves only when the maximum grows by more than
 // 2^8 (numerator and denominator use the same one, so the result is the softmax's in real arithmetic).
-// K and V pass through one ring of 16 KB (8 KB at head_dim 64) stages in the order in which the
-// products need them; the ring runs on into the next unit while the last one is finished, so that
+// K and V pass through a ring each that runs on into the next unit while the last one is finished, so that
 // the loads never pause at a border.
+//
+// One thread is too slow to keep an SM's share of HBM3e moving (a wait, an issue and a commit cost it a
+// few hundred cycles, a 64-key tile passes every 1,400), so the control work is spread over five warps: K
+// and V producers, S products, P V products, Q; and each tile has one commit per product, whose barrier
+// tells the softmax, the producer and the other issuer alike.
 //
 // Two groups of four softmax warps, each with two S buffers and an O of its own (512 TMEM columns):
 //   narrow (a sequence's rows fit one 128-row tile): the groups take the key tiles of the unit in
@@ -20,9 +24,9 @@
 // value cannot be deselected (0 * NaN), so in those tiles non-finite elements of V are zeroed in
 // shared memory before the product, and added at the end, by themselves, to the rows that see them.
 //
-// Warps: 0-3 and 4-7 softmax, 8 K/V producer (TMA: one box of 16 keys x 64 columns per lane), 9 MMA,
-// 10 Q producer.  Every wait is bounded (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the
-// next one only, so each barrier below is waited for before its next phase but one can complete.
+// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 S, 11 P V, 12 Q.  Every wait is bounded
+// (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each barrier below is
+// waited for before its next phase but one can complete.
 #include <cudaTypedefs.h>
 #include <float.h>
 
@@ -31,7 +35,7 @@
 
 namespace pa {
 
-constexpr int kTuThreads = 352;
+constexpr int kTuThreads = 416;
 constexpr int kTuSubs = kTreeKeys / 16;
 constexpr float kTuRescale = 8.f;
 
@@ -41,13 +45,14 @@ struct TuCfg {
   static constexpr int kQHalf = 128 * 128;          // one 64-column half of a 128-row Q tile
   static constexpr int kQTile = kQHalf * kHalves;
   static constexpr int kQBytes = (kWide ? 2 : 1) * kQTile;
-  static constexpr int kKvHalf = kTreeKeys * 128;
-  static constexpr int kKvBytes = kKvHalf * kHalves;  // a stage: one K or V tile
+  static constexpr int kKvBytes = kTreeKeys * D * 2;  // a stage: one K or V tile
+  static constexpr int kGroup = 1024 * kHalves;     // 8 keys of it
   static constexpr int kHead = 4096;                // barriers, masks, row statistics
   static constexpr int kFit = (227 * 1024 - 1024 - kHead - kQBytes) / kKvBytes;
-  static constexpr int kStages = kFit < 24 ? kFit : 24;
-  static constexpr int kSmemBytes = 1024 + kHead + kQBytes + kStages * kKvBytes;
-  static constexpr int kAhead = kWide ? 1 : 2;      // key tiles whose S is issued before a tile's P V
+  static constexpr int kKStages = kFit / 2 < 12 ? kFit / 2 : 12;
+  static constexpr int kVStages = kFit - kFit / 2 < 12 ? kFit - kFit / 2 : 12;
+  static constexpr int kSmemBytes = 1024 + kHead + kQBytes + (kKStages + kVStages) * kKvBytes;
+  static constexpr int kBufs = kWide ? 2 : 4;       // S buffers: tiles whose scores or weights are in TMEM
 };
 
 // Whether one of the two 16-bit floats in w is infinite or NaN.
@@ -193,32 +198,35 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   using Cfg = TuCfg<D, kWide>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kHalves = Cfg::kHalves;
-  constexpr int kStages = Cfg::kStages;
-  constexpr int kAhead = Cfg::kAhead;
+  constexpr int kKStages = Cfg::kKStages, kVStages = Cfg::kVStages, kBufs = Cfg::kBufs;
   constexpr int kUnitRows = kWide ? 256 : 128;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Tile i of the CTA (counted over its units): K stage i % kKStages, V stage i % kVStages, S buffer i % kBufs.
   uint64_t* bars = reinterpret_cast<uint64_t*>(base);
-  uint64_t* full = bars;           // [kStages] the stage's tile landed
-  uint64_t* empty = bars + 24;     // [kStages] the products that read it are done
-  uint64_t* q_full = bars + 48;    // one phase per unit
-  uint64_t* q_empty = bars + 49;   // one phase per unit: its S products are done
-  uint64_t* o_full = bars + 50;    // one phase per unit: both Os complete
-  uint64_t* o_free = bars + 51;    // one phase per unit: both Os read
-  uint64_t* s_full = bars + 52;    // [4] S buffer holds a tile's scores
-  uint64_t* p_full = bars + 56;    // [4] its weights are written (and O rescaled)
-  uint64_t* pv_done = bars + 60;   // [4] O += P V of the buffer done
-  uint64_t* ml_full = bars + 64;   // one phase per unit (narrow): both groups' statistics written
-  uint64_t* fin = bars + 65;       // a launch that gave up: its products are over
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 532);
-  volatile int* bad_v = reinterpret_cast<int*>(base + 536);  // V of a drafted region held non-finite elements
-  volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 544);  // [32] sub-tiles loaded, per tile
-  TuSched* sched = reinterpret_cast<TuSched*>(base + 672);
+  uint64_t* kfull = bars;          // [kKStages] the tile's keys landed
+  uint64_t* vfull = bars + 12;     // [kVStages] its values
+  uint64_t* sdone = bars + 24;     // [kKStages] its scores are in its S buffer (and the K stage is free)
+  uint64_t* vdone = bars + 36;     // [kVStages] O += P V done (and the V stage and the S buffer are free)
+  uint64_t* p_full = bars + 48;    // [kBufs] its weights are written (and O rescaled)
+  uint64_t* q_full = bars + 52;    // one phase per unit
+  uint64_t* o_free = bars + 53;    // one phase per unit: both Os read
+  uint64_t* ml_full = bars + 54;   // one phase per unit (narrow): both groups' statistics written
+  uint64_t* q_empty = bars + 55;   // one phase per unit: its S products are done (sdone would not do: the Q
+                                   // producer may be more than one phase ahead of it)
+  uint64_t* fin = bars + 56;       // [2] all products of an issuer are over
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 480);
+  volatile int* bad_v = reinterpret_cast<int*>(base + 484);  // V of a drafted region held non-finite elements
+  volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 512);  // [32] 16-key sub-tiles loaded, per tile
+  TuSched* sched = reinterpret_cast<TuSched*>(base + 640);
   float2* ml = reinterpret_cast<float2*>(base + 2048);  // [2][128] the groups' (maximum, sum) per row
-  static_assert(sizeof(TuSched) <= 2048 - 672 && kStages <= 24, "head of the shared memory");
+  static_assert(sizeof(TuSched) <= 2048 - 640 && kKStages <= 12 && kVStages <= 12, "head of the shared memory");
+  // (S of tile i + kBufs waits for P V of tile i, and phases stay one apart only if the rings are not shorter)
+  static_assert(kKStages >= kBufs && kVStages >= kBufs, "ring depths");
   uint8_t* qs = base + Cfg::kHead;
-  uint8_t* ring = qs + Cfg::kQBytes;
+  uint8_t* ks = qs + Cfg::kQBytes;
+  uint8_t* vs = ks + kKStages * Cfg::kKvBytes;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -227,25 +235,25 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
     prefetch_tensormap(&qmap);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int k = 0; k < kKStages; ++k) {
+      mbar_init(&kfull[k], 1);
+      mbar_init(&sdone[k], 1);
     }
+    for (int k = 0; k < kVStages; ++k) {
+      mbar_init(&vfull[k], 1);
+      mbar_init(&vdone[k], 1);
+    }
+    for (int k = 0; k < kBufs; ++k) mbar_init(&p_full[k], kWide ? 8 : 4);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(o_full, 1);
     mbar_init(o_free, 8);
     mbar_init(ml_full, 8);
-    mbar_init(fin, 1);
-    for (int k = 0; k < 4; ++k) {
-      mbar_init(&s_full[k], 1);
-      mbar_init(&p_full[k], 4);
-      mbar_init(&pv_done[k], 1);
-    }
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     *bad_v = 0;
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == 10) tmem_alloc(tmem_slot, 512);
   // nothing of global memory is read or written before the preceding grid is over
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -256,84 +264,82 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const TreeSpan span = sched->span;
-  // S buffer i (0..3) and O of group g.  Narrow: tile t of the CTA (counted over its units) is group t % 2's
-  // and in buffer t % 4.  Wide: group g's tile t is in buffer 2 (t % 2) + g.
-  auto tS = [&](int i) { return tmem + 64u * (uint32_t)i; };
+  // S of group g in buffer i, and its O.  Narrow: tile i is group i % 2's and its four buffers are the four
+  // 64-column ranges; wide: a buffer holds both groups' scores.
+  auto tS = [&](int i, int g) { return tmem + 64u * (uint32_t)(kWide ? 2 * i + g : i); };
   auto tO = [&](int g) { return tmem + 256u + 128u * (uint32_t)g; };
 
-  if (warp == 8) {
-    // -------------------------------------- K/V producer -----------------------------------------
-    constexpr int kBoxes = kTuSubs * kHalves;  // boxes of a tile: one per lane
-    const int sub = lane / kHalves, half = lane % kHalves;
-    const bool mine = lane < kBoxes;
+  if (warp == 8 || warp == 9) {
+    // ------------------------------- producers: warp 8 K, warp 9 V --------------------------------
+    // One box is 8 x (up to 8) keys x head_dim of one block: a tile takes 64 / min(block_size, 64) of them,
+    // one per lane, and lies in shared memory as [8-key group][64-column half][8][128 bytes, swizzled].
+    const bool is_v = warp == 9;
+    uint64_t* full = is_v ? vfull : kfull;
+    uint64_t* freed = is_v ? vdone : sdone;
+    uint8_t* ring = is_v ? vs : ks;
+    const CUtensorMap* map = is_v ? &vmap : &kmap;
+    const int depth = is_v ? kVStages : kKStages;
+    const int box_keys = min(a.block_size, kTreeKeys), boxes = kTreeKeys / box_keys;
     const uint64_t once = l2_policy_evict_first();
-    int op = 0, t = 0;
+    int t = 0, s = 0, round = 0;
     bool alive = true;
     TreeWalk walk(a, span, nodes_unit);
     TreeUnit w;
     while (alive && walk.next(w)) {
       const int32_t* table = a.block_table + (int64_t)w.b * a.bt_stride;
-      const int n = w.x1 - w.x0;
-      // table entry of this lane's sub-tile of tile i of the piece (-1: behind the context)
-      auto entry = [&](int i) -> int {
-        const int pos = (w.x0 + i) * kTreeKeys + sub * 16;
-        return mine && i < n && pos < w.sq.n ? ld_nc_s32(table + (pos >> a.block_shift)) : -1;
+      // table entry of this lane's box of tile x of the unit (-1: behind the context)
+      auto entry = [&](int x) -> int {
+        const int pos = x * kTreeKeys + lane * box_keys;
+        return lane < boxes && x < w.x1 && pos < w.sq.n ? ld_nc_s32(table + (pos >> a.block_shift)) : -1;
       };
-      auto load = [&](bool v, int i, int blk) {  // whole warp
-        const int s = op % kStages;
-        if (op >= kStages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (unsigned)((op / kStages - 1) & 1), a.err,
-                                                                a.epoch))) {
+      int blk = entry(w.x0);
+      for (int x = w.x0; x < w.x1; ++x, ++t) {
+        const int blk_next = entry(x + 1);
+        if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&freed[s], (unsigned)((round - 1) & 1), a.err, a.epoch))) {
           alive = false;
-          return;
+          break;
         }
-        const int pos = (w.x0 + i) * kTreeKeys + sub * 16;
-        const bool in = mine && pos < w.sq.n;
+        const int pos = x * kTreeKeys + lane * box_keys;
+        const bool in = lane < boxes && pos < w.sq.n;
         const bool ok = in && blk >= 0 && blk < a.num_blocks;
-        if (in && !ok && !v && half == 0) raise_error(a.err, PA_DEVERR_BLOCK_ID);
+        if (in && !ok && !is_v) raise_error(a.err, PA_DEVERR_BLOCK_ID);
         const unsigned lanes = __ballot_sync(0xffffffffu, ok);
         if (lane == 0) {
-          if (!v) {
+          if (!is_v) {
+            // 16-key sub-tiles that hold data.  Read after S of the tile, which waits for the arrival
+            // below; tile t - 32, the slot's last, is more than a ring ago.
             uint32_t m = 0;
-#pragma unroll
-            for (int u = 0; u < kTuSubs; ++u) m |= ((lanes >> (u * kHalves)) & 1u) << u;
-            // read after S of the tile, which waits for the arrival below; the slot is free: K of tile
-            // t - 32 is more than a ring ago, and so is V of it, whose product followed its weights
-            kmask[(t + i) & 31] = m;
+            const int per = box_keys / 16;
+            for (int k = 0; k < boxes; ++k)
+              if ((lanes >> k) & 1u) m |= ((1u << per) - 1u) << (k * per);
+            kmask[t & 31] = m;
           }
-          if (lanes != 0) mbar_arrive_expect_tx(&full[s], (unsigned)__popc(lanes) * 2048u);
+          if (lanes != 0) mbar_arrive_expect_tx(&full[s], (unsigned)(__popc(lanes) * box_keys * D * 2));
           else mbar_arrive(&full[s]);
         }
         __syncwarp();
         if (ok) {
-          uint8_t* dst = ring + s * Cfg::kKvBytes + half * Cfg::kKvHalf + sub * 2048;
-          const CUtensorMap* map = v ? &vmap : &kmap;
-          const int x = w.kvh * D + half * 64, y = pos & (a.block_size - 1);
           // the last reader of the keys marks them first to be evicted
-          if (w.last_tile) tma_load_3d_hint(dst, map, x, y, blk, &full[s], once);
-          else tma_load_3d(dst, map, x, y, blk, &full[s]);
+          uint8_t* dst = ring + s * Cfg::kKvBytes + lane * box_keys * D * 2;
+          const int group = (pos & (a.block_size - 1)) >> 3;
+          if (w.last_tile) tma_load_5d_hint(dst, map, 0, 0, w.kvh * kHalves, group, blk, &full[s], once);
+          else tma_load_5d(dst, map, 0, 0, w.kvh * kHalves, group, blk, &full[s]);
         }
-        ++op;
-      };
-      int e[kAhead + 2];  // entries of tiles i + 1, i, .., i - kAhead
-#pragma unroll
-      for (int k = 0; k < kAhead + 2; ++k) e[k] = -1;
-      e[0] = entry(0);
-      for (int i = 0; i < n + kAhead && alive; ++i) {
-#pragma unroll
-        for (int k = kAhead + 1; k > 0; --k) e[k] = e[k - 1];
-        e[0] = entry(i + 1);
-        if (i < n) load(false, i, e[1]);
-        if (alive && i >= kAhead) load(true, i - kAhead, e[1 + kAhead]);
+        blk = blk_next;
+        if (++s == depth) {
+          s = 0;
+          ++round;
+        }
       }
-      t += n;
     }
-    if (!alive && lane == 0) {
-      raise_timeout(a.err, a.epoch);
-      // leave no copy in flight: the last load of each stage, bounded (none is loaded again after it)
-      for (int k = op > kStages ? op - kStages : 0; k < op; ++k)
-        mbar_wait_for(&full[k % kStages], (unsigned)((k / kStages) & 1), nullptr, 0, 100000000ull);
+    if (lane == 0) {
+      if (!alive) raise_timeout(a.err, a.epoch);
+      // leave no copy in flight, whatever the other warps have made of this launch: the last load of each
+      // stage (the stage is not loaded again after it)
+      for (int k = t > depth ? t - depth : 0; k < t; ++k) mbar_wait(&full[k % depth], (unsigned)((k / depth) & 1));
     }
-  } else if (warp == 10) {
+    __syncwarp();
+  } else if (warp == 12) {
     // --------------------------------------- Q producer ------------------------------------------
     if (lane == 0) {
       int un = 0;
@@ -353,100 +359,100 @@ __global__ void __launch_bounds__(kTuThreads, 1)
             tma_load_3d(qs + k * Cfg::kQTile + h * Cfg::kQHalf, &qmap, h * 64, w.kvh << a.group_shift,
                         (int)(w.sq.q0 + w.node0) + k * (128 >> a.group_shift), q_full);
       }
-      if (!alive) {
-        raise_timeout(a.err, a.epoch);
-        mbar_wait_for(q_full, (unsigned)((un - 1) & 1), nullptr, 0, 100000000ull);
-      }
+      if (!alive) raise_timeout(a.err, a.epoch);
+      if (un > 0) mbar_wait(q_full, (unsigned)((un - 1) & 1));  // no copy in flight
     }
     __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------ MMA ----------------------------------------------
+  } else if (warp == 10) {
+    // -------------------------------------- S = Q K^T --------------------------------------------
     if (lane == 0) {
-      const uint32_t id_s = umma_idesc_f16(kBf16, 128, kTreeKeys, false, false);
-      const uint32_t id_pv = umma_idesc_f16(kBf16, 128, D, false, true);
-      int op = 0, t = 0, t1 = 0, un = 0;  // ring position, tiles of the CTA, of group 1 (wide), unit
+      const uint32_t id = umma_idesc_f16(kBf16, 128, kTreeKeys, false, false);
+      const uint64_t qd = umma_desc_sw128(smem_u32(qs), 16, 1024), kd = umma_desc_sw128(smem_u32(ks), 16, Cfg::kGroup);
+      int t = 0, s = 0, round = 0, un = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
         ok = ok && mbar_wait(bar, (unsigned)(phase & 1), a.err, a.epoch);
         return ok;
       };
-      auto issue_s = [&](int buf, int q_tile, const uint8_t* stage) {
-        const uint32_t qa = smem_u32(qs + q_tile * Cfg::kQTile), ka = smem_u32(stage);
+      TreeWalk walk(a, span, nodes_unit);
+      TreeUnit w;
+      while (ok && walk.next(w)) {
+        const bool two = kWide && w.rows > 128;
+        if (!wait(q_full, un)) break;
+        for (int x = w.x0; x < w.x1; ++x, ++t) {
+          // the buffer still holds the weights of tile t - kBufs until their product is done
+          if (t >= kBufs && !wait(&vdone[(t - kBufs) % kVStages], (t - kBufs) / kVStages)) break;
+          if (!wait(&kfull[s], round)) break;
+          tc_fence_after();
+          const uint64_t kt = kd + (uint64_t)(s * (Cfg::kKvBytes >> 4));
+          const int buf = t % kBufs;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tS(buf), umma_desc_sw128(qa + (kk >> 2) * Cfg::kQHalf + (kk & 3) * 32, 16, 1024),
-                  umma_desc_sw128(ka + (kk >> 2) * Cfg::kKvHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-        umma_commit(&s_full[buf]);
-      };
-      auto issue_pv = [&](int buf, int g, const uint8_t* stage, bool first) {
-        const uint32_t va = smem_u32(stage);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tS(buf, 0), qd + (kk >> 2) * (Cfg::kQHalf >> 4) + (kk & 3) * 2, kt + (kk >> 2) * 64 + (kk & 3) * 2, id,
+                    kk > 0 ? 1u : 0u);
+          if (two) {
 #pragma unroll
-        for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-          umma_ts(tO(g), tS(buf) + 8u * (uint32_t)kk, umma_desc_sw128(va + kk * 2048, Cfg::kKvHalf, 1024), id_pv,
-                  (!first || kk > 0) ? 1u : 0u);
-        umma_commit(&pv_done[buf]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(tS(buf, 1), qd + (Cfg::kQTile >> 4) + (kk >> 2) * (Cfg::kQHalf >> 4) + (kk & 3) * 2,
+                      kt + (kk >> 2) * 64 + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&sdone[s]);
+          if (x == w.x1 - 1) umma_commit(q_empty);
+          if (++s == kKStages) {
+            s = 0;
+            ++round;
+          }
+        }
+        ++un;
+      }
+      if (!ok) raise_timeout(a.err, a.epoch);
+      umma_commit(&fin[0]);  // no product in flight when the tensor memory is given back
+      mbar_wait(&fin[0], 0);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // -------------------------------------- O += P V ---------------------------------------------
+    if (lane == 0) {
+      const uint32_t id = umma_idesc_f16(kBf16, 128, D, false, true);
+      const uint64_t vd = umma_desc_sw128(smem_u32(vs), 1024, Cfg::kGroup);
+      int t = 0, s = 0, round = 0, un = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = ok && mbar_wait(bar, (unsigned)(phase & 1), a.err, a.epoch);
+        return ok;
       };
       TreeWalk walk(a, span, nodes_unit);
       TreeUnit w;
       while (ok && walk.next(w)) {
-        const int n = w.x1 - w.x0;
         const bool two = kWide && w.rows > 128;
-        if (!wait(q_full, un)) break;
-        // An S overwrites the weights of the tile four (wide: two) before it, whose P V was issued first and
-        // reads them first: products of one thread run in issue order.
-        for (int i = 0; i < n + kAhead; ++i) {
-          if (i < n) {
-            const int s = op % kStages;
-            if (!wait(&full[s], op / kStages)) break;
-            tc_fence_after();
-            const uint8_t* stage = ring + s * Cfg::kKvBytes;
-            if (kWide) {
-              issue_s(2 * ((t + i) & 1), 0, stage);
-              if (two) issue_s(2 * ((t1 + i) & 1) + 1, 1, stage);
-            } else {
-              issue_s((t + i) & 3, 0, stage);
-            }
-            umma_commit(&empty[s]);
-            if (i == n - 1) umma_commit(q_empty);
-            ++op;
+        // the unit's first products overwrite the Os that the unit before it left
+        if (un > 0 && !wait(o_free, un - 1)) break;
+        for (int x = w.x0; x < w.x1; ++x, ++t) {
+          const int buf = t % kBufs;
+          if (!wait(&vfull[s], round) || !wait(&p_full[buf], t / kBufs)) break;
+          tc_fence_after();
+          const uint64_t vt = vd + (uint64_t)(s * (Cfg::kKvBytes >> 4));
+          const int g = kWide ? 0 : t & 1;
+          const uint32_t more = x >= w.x0 + (kWide ? 1 : 2) ? 1u : 0u;
+#pragma unroll
+          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+            umma_ts(tO(g), tS(buf, g) + 8u * (uint32_t)kk, vt + kk * (2 * Cfg::kGroup >> 4), id, kk > 0 ? 1u : more);
+          if (two) {
+#pragma unroll
+            for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+              umma_ts(tO(1), tS(buf, 1) + 8u * (uint32_t)kk, vt + kk * (2 * Cfg::kGroup >> 4), id, kk > 0 ? 1u : more);
           }
-          if (i >= kAhead) {
-            const int k = i - kAhead, s = op % kStages;
-            if (!wait(&full[s], op / kStages)) break;
-            const uint8_t* stage = ring + s * Cfg::kKvBytes;
-            // the unit's first P V overwrites the O that the unit before it left
-            if (k == 0 && un > 0 && !wait(o_free, un - 1)) break;
-            if (kWide) {
-              const int buf = 2 * ((t + k) & 1);
-              if (!wait(&p_full[buf], (t + k) >> 1)) break;
-              tc_fence_after();
-              issue_pv(buf, 0, stage, k == 0);
-              if (two) {
-                const int buf1 = 2 * ((t1 + k) & 1) + 1;
-                if (!wait(&p_full[buf1], (t1 + k) >> 1)) break;
-                tc_fence_after();
-                issue_pv(buf1, 1, stage, k == 0);
-              }
-            } else {
-              const int buf = (t + k) & 3;
-              if (!wait(&p_full[buf], (t + k) >> 2)) break;
-              tc_fence_after();
-              issue_pv(buf, (t + k) & 1, stage, k < 2);
-            }
-            umma_commit(&empty[s]);
-            if (k == n - 1) umma_commit(o_full);
-            ++op;
+          umma_commit(&vdone[s]);
+          if (++s == kVStages) {
+            s = 0;
+            ++round;
           }
         }
-        t += n;
-        if (two) t1 += n;
         ++un;
       }
-      if (!ok) {
-        raise_timeout(a.err, a.epoch);
-        umma_commit(fin);
-        mbar_wait(fin, 0);
-      }
+      if (!ok) raise_timeout(a.err, a.epoch);
+      umma_commit(&fin[1]);  // no product in flight when the tensor memory is given back
+      mbar_wait(&fin[1], 0);
     }
     __syncwarp();
   } else {
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     const int grp = warp >> 2;
     const int r = threadIdx.x & 127;  // row of the group's tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    int t = 0, tg = 0, op = 0, un = 0;  // tiles of the CTA and of this group, ring position, unit
+    int t = 0, un = 0;  // tiles of the CTA's earlier units, and those
     bool alive = true, cut = false;
     TreeWalk walk(a, span, nodes_unit);
     TreeUnit w;
@@ -492,11 +498,11 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         return keep;
       };
 
-      // Scores of S buffer buf into weights; `before` >= 0: the buffer of the group's previous tile of the
-      // unit, and its phase.  kMasked: the tile may hold keys that the row does not see.
-      auto tile = [&](auto masked, int buf, uint64_t keep, int before, int before_phase) {
+      // Scores of S buffer buf into weights; `before` >= 0: the group's previous tile of the unit.
+      // kMasked: the tile may hold keys that the row does not see.
+      auto tile = [&](auto masked, int buf, uint64_t keep, int before) {
         constexpr bool kMasked = decltype(masked)::value;
-        const uint32_t srow = tS(buf) + lane_base;
+        const uint32_t srow = tS(buf, grp) + lane_base;
         uint32_t sv[64];
         tmem_ld32(srow, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
         tmem_ld32(srow + 32u, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
@@ -542,7 +548,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
         if (before >= 0 && __any_sync(0xffffffffu, corr != 1.f)) {
           // O is stable once the product of the group's previous tile is done; this tile's waits for us
-          if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[before], (unsigned)(before_phase & 1), a.err, a.epoch))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&vdone[before % kVStages], (unsigned)((before / kVStages) & 1),
+                                                           a.err, a.epoch))) {
             alive = false;
             return;
           }
@@ -559,36 +566,32 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       };
 
       const int step = kWide ? 1 : 2;
-      for (int i = kWide ? 0 : ((grp - t) & 1); i < n && rows > 0; i += step) {
-        const int buf = kWide ? 2 * ((tg + i) & 1) + grp : (t + i) & 3;
-        const int phase = kWide ? (tg + i) >> 1 : (t + i) >> 2;
-        const int before = i < step ? -1 : (kWide ? 2 * ((tg + i - 1) & 1) + grp : (t + i - 2) & 3);
-        const int before_phase = kWide ? (tg + i - 1) >> 1 : (t + i - 2) >> 2;
+      for (int i = kWide ? 0 : ((grp - t) & 1); i < n; i += step) {
+        const int ti = t + i, buf = ti % kBufs, before = i < step ? -1 : ti - step;
         const int kb = (w.x0 + i) * kTreeKeys;
         const bool edge = kb + kTreeKeys > hist;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (unsigned)(phase & 1), a.err, a.epoch))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sdone[ti % kKStages], (unsigned)((ti / kKStages) & 1), a.err, a.epoch))) {
           alive = false;
           break;
         }
         tc_fence_after();
-        const uint32_t loaded = kmask[(t + i) & 31];
+        const uint32_t loaded = kmask[ti & 31];
         if (!edge && loaded == (1u << kTuSubs) - 1u) {
-          if (live) tile(std::false_type{}, buf, ~0ull, before, before_phase);
+          if (live) tile(std::false_type{}, buf, ~0ull, before);
         } else {
-          if (live) tile(std::true_type{}, buf, visible(kb, loaded), before, before_phase);
+          if (live) tile(std::true_type{}, buf, visible(kb, loaded), before);
           if (!kWide || grp == 0) {
             // V of the tile: rows without a token zeroed, non-finite elements of drafted tokens taken out
-            // (wide: the other group's product is issued after this one's)
-            const int vop = op + min(n, i + kAhead + 1) + i;
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[vop % kStages], (unsigned)((vop / kStages) & 1), a.err,
+            if (!__all_sync(0xffffffffu, mbar_wait(&vfull[ti % kVStages], (unsigned)((ti / kVStages) & 1), a.err,
                                                    a.epoch))) {
               alive = false;
               break;
             }
-            uint8_t* vst = ring + (vop % kStages) * Cfg::kKvBytes;
+            uint8_t* vst = vs + (ti % kVStages) * Cfg::kKvBytes;
             for (int e = r; e < kTreeKeys * 8 * kHalves; e += 128) {
               const int key = e / (8 * kHalves), c = e % (8 * kHalves);
-              uint4* p = reinterpret_cast<uint4*>(vst + (c >> 3) * Cfg::kKvHalf + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+              uint4* p = reinterpret_cast<uint4*>(vst + (key >> 3) * Cfg::kGroup + (c >> 3) * 1024 + (key & 7) * 128 +
+                                                   (((c & 7) ^ (key & 7)) << 4));
               if (kb + key >= w.sq.n || !((loaded >> (key >> 4)) & 1u)) {
                 *p = make_uint4(0, 0, 0, 0);
               } else if (kb + key >= hist) {
@@ -613,7 +616,10 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(o_full, (unsigned)(un & 1), a.err, a.epoch));
+      // both Os: products complete in the order in which their one thread issued them
+      const int end = t + n - 1;
+      if (alive)
+        alive = __all_sync(0xffffffffu, mbar_wait(&vdone[end % kVStages], (unsigned)((end / kVStages) & 1), a.err, a.epoch));
       if (!alive) break;
       tc_fence_after();
 
@@ -731,8 +737,6 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         }
       }
       t += n;
-      if (rows > 0) tg += n;
-      op += 2 * n;
       ++un;
     }
     if (!alive && lane == 0) raise_timeout(a.err, a.epoch);
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -834,8 +838,8 @@ static cudaError_t launch_tu_rows(const TreeArgs& a, const CUtensorMap& km, cons
 
 cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
   CUtensorMap km, vm;
-  if (!encode_pool_map(&km, a.k_pool, dt, a.num_blocks, a.block_size, a.n_kv_heads, a.head_dim, a.kv_block_stride) ||
-      !encode_pool_map(&vm, a.v_pool, dt, a.num_blocks, a.block_size, a.n_kv_heads, a.head_dim, a.kv_block_stride))
+  if (!encode_group_map(&km, a.k_pool, dt, a.num_blocks, a.block_size, a.n_kv_heads, a.head_dim, a.kv_block_stride) ||
+      !encode_group_map(&vm, a.v_pool, dt, a.num_blocks, a.block_size, a.n_kv_heads, a.head_dim, a.kv_block_stride))
     return cudaErrorInvalidValue;
   cudaError_t e;
   if (dt == PA_BF16)

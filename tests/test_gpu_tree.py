@@ -254,6 +254,7 @@ def test_other_streams_and_a_captured_step_share_nothing(cuda_lib, kernel):
              for i in range(2)]
     want = [run(pa, c, kernel=kernel, partition_tokens=64).cpu() for c in cases]
     ds = [c.device() for c in cases]
+    torch.cuda.synchronize()  # the inputs, before other streams read them
     graphs, outs = [], []
     for c, d in zip(cases, ds):
         s = torch.cuda.Stream()
