@@ -7,7 +7,9 @@ library is missing or fails to load, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -27,6 +29,7 @@ PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_CONTEXT_LEN = 1, 2, 4
 PA_DEVERR_COPY_PAIR, PA_DEVERR_QUERY_LOC, PA_DEVERR_TIMEOUT = 8, 16, 32
 PA_DEVERR_TREE, PA_DEVERR_NO_BLOCKS = 64, 128
 
+_I32, _I64 = torch.int32, torch.int64
 _vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 
 
@@ -398,34 +401,88 @@ def paged_attention_prefill(q, query_start_loc, k_pool, v_pool, block_table, con
     return out
 
 
-class _OnDevice:
-    """The current device set to the tensors' own while a call is made (the library launches on the
-    current device); nothing to do when it is that already."""
+# The calls below are short enough on the device for the host's side to count, so their checks are few
+# attribute reads on the way that succeeds; _refuse says what is wrong on the other.
 
-    def __init__(self, device):
-        other = device.type == "cuda" and device.index != torch.cuda.current_device()
-        self._guard = torch.cuda.device(device) if other else None
+class _OnDevice:
+    """The current device set to index ``dev`` while a call is made (the library launches on the current
+    device)."""
+
+    def __init__(self, dev: int):
+        self._guard = torch.cuda.device(dev)
 
     def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
+        self._guard.__enter__()
 
     def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+        self._guard.__exit__(*exc)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+_HERE = contextlib.nullcontext()
 
 
-def _vector(t, name: str, n: int, dtype=torch.int32) -> int:
-    ptr = _dev(t, name, dtype)
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
-    return ptr
+def _on(dev: int):
+    return _HERE if dev < 0 or dev == torch.cuda.current_device() else _OnDevice(dev)
+
+
+def _refuse(t, name: str, dtype, dev: int, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, name: str, dtype, dev: int, shape=None) -> int:
+    """Pointer of a contiguous CUDA tensor of a type, device and (optionally) shape."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev or dev < 0
+            or not t.is_contiguous() or (shape is not None and t.shape != shape)):
+        _refuse(t, name, dtype, dev, shape)
+    return t.data_ptr()
+
+
+def _table(t, name: str, rows: int, dev: int) -> tuple:
+    """(pointer, row stride, columns) of an int32 [rows, columns] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or (rows and t.shape[1] and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [batch, entries] with contiguous rows")
+    if t.dtype != torch.int32 or t.get_device() != dev or dev < 0:
+        _refuse(t, name, torch.int32, dev, None)
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def _pools(k, v, dev: int, lead: int = 0) -> tuple:
+    """(pointers, shape, block stride in elements) of two pools of one layout (see :func:`_pool`) behind
+    ``lead`` dimensions of layers."""
+    shape, stride, vstride = k.shape[lead:], k.stride()[lead:], v.stride()[lead:]
+    if len(shape) != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, n_kv_heads, head_dim] of one dtype")
+    NB, S, H, D = shape
+    if stride != (S * H * D, H * D, D, 1) or vstride != stride or k.get_device() != dev or v.get_device() != dev:
+        _pool(k[0] if lead else k, "k_pool"), _pool(v[0] if lead else v, "v_pool", k.dtype)
+        for name, t in (("k_pool", k), ("v_pool", v)):
+            if t.get_device() != dev:
+                _refuse(t, name, k.dtype, dev, None)
+        if NB > 1 and vstride[0] != stride[0]:
+            raise ValueError(f"k_pool and v_pool must share one block stride (got {stride[0]} and {vstride[0]} elements)")
+    return k.data_ptr(), v.data_ptr(), NB, S, H, D, (stride[0] if NB > 1 else S * H * D)
+
+
+@functools.lru_cache(maxsize=256)
+def _opts_of(kv_block_stride_bytes: int, prefill_kernel: int, partition_tokens: int):
+    return ctypes.byref(make_opts(kv_block_stride_bytes, prefill_kernel=prefill_kernel,
+                                  partition_tokens=partition_tokens))
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 class StepTables(NamedTuple):
@@ -451,22 +508,20 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
     rows behind the last sequence's tokens get slot -1.  ``out``: the arrays of an earlier call, to be
     written again (a captured step).  Sequences that do not fit get nothing and are recorded in the
     device error word."""
-    lib = load_library()
-    dev = history_lens.device
-    B = int(history_lens.numel())
-    if block_table.dim() != 2 or block_table.shape[0] != B or (B and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [batch, max_blocks] with contiguous rows")
+    lib = _lib or load_library()
+    B, dev = history_lens.numel(), history_lens.get_device()
     if out is None:
-        T = num_tokens if num_tokens is not None else (int(parents.numel()) if parents is not None else None)
+        T = num_tokens if num_tokens is not None else (parents.numel() if parents is not None else None)
         if T is None:
             raise ValueError("num_tokens is needed without parents or out")
         words = 1 if mask_words is None else mask_words
-        with _OnDevice(dev):
-            out = StepTables(torch.empty(B + 1, dtype=torch.int32, device=dev),
-                             torch.empty(B, dtype=torch.int32, device=dev),
-                             torch.empty(T, dtype=torch.int64, device=dev),
-                             torch.empty(T, dtype=torch.int32, device=dev),
-                             torch.empty((T, words), dtype=torch.int64, device=dev) if parents is not None else None)
+        with _on(dev):
+            d = history_lens.device
+            out = StepTables(torch.empty(B + 1, dtype=torch.int32, device=d),
+                             torch.empty(B, dtype=torch.int32, device=d),
+                             torch.empty(T, dtype=torch.int64, device=d),
+                             torch.empty(T, dtype=torch.int32, device=d),
+                             torch.empty((T, words), dtype=torch.int64, device=d) if parents is not None else None)
         if B == 0:
             out.query_start_loc.zero_()
             out.slot_mapping.fill_(-1)
@@ -474,42 +529,46 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
             if out.tree_mask is not None:
                 out.tree_mask.zero_()
     qsl, ctx, slots, pos, mask = out
-    T = int(slots.numel())
+    T, words, par, msk = slots.numel(), 0, None, None
     if num_tokens is not None and num_tokens != T:
         raise ValueError(f"out holds {T} tokens, num_tokens is {num_tokens}")
-    words = 0
     if parents is not None:
-        if mask is None or mask.dim() != 2 or mask.shape[0] != T or (mask_words is not None
-                                                                    and mask.shape[1] != mask_words):
+        if mask is None or mask.dim() != 2 or (mask_words is not None and mask.shape[1] != mask_words):
             raise ValueError("with parents, out.tree_mask must be [tokens, mask_words]")
-        words = int(mask.shape[1])
-    _same_device(dev, new_lens=new_lens, block_table=block_table, block_counts=block_counts, free_blocks=free_blocks,
-                 free_state=free_state, parents=parents, query_start_loc=qsl, context_lens=ctx, slot_mapping=slots,
-                 positions=pos, tree_mask=mask)
-    with _OnDevice(dev):
-        st = lib.build_block_tables(
-            _vector(history_lens, "history_lens", B), _vector(new_lens, "new_lens", B), B,
-            _dev(block_table, "block_table", torch.int32, contiguous=False), int(block_table.stride(0)),
-            int(block_table.shape[1]), _vector(block_counts, "block_counts", B),
-            _dev(free_blocks, "free_blocks", torch.int32), int(free_blocks.numel()),
-            _vector(free_state, "free_state", 2), num_blocks, block_size,
-            _vector(parents, "parents", T) if parents is not None else None,
-            _vector(qsl, "query_start_loc", B + 1), _vector(ctx, "context_lens", B),
-            _vector(slots, "slot_mapping", T, torch.int64), _vector(pos, "positions", T), T,
-            _dev(mask, "tree_mask", torch.int64) if parents is not None else None, words, _stream(stream))
-    _check("build_block_tables", st)
+        words = mask.shape[1]
+        par = _arg(parents, "parents", _I32, dev, (T,))
+        msk = _arg(mask, "tree_mask", _I64, dev, (T, words))
+    table, stride, entries = _table(block_table, "block_table", B, dev)
+    args = (_arg(history_lens, "history_lens", _I32, dev, (B,)), _arg(new_lens, "new_lens", _I32, dev, (B,)), B, table,
+            stride, entries, _arg(block_counts, "block_counts", _I32, dev, (B,)),
+            _arg(free_blocks, "free_blocks", _I32, dev), free_blocks.numel(),
+            _arg(free_state, "free_state", _I32, dev, (2,)), num_blocks, block_size, par,
+            _arg(qsl, "query_start_loc", _I32, dev, (B + 1,)), _arg(ctx, "context_lens", _I32, dev, (B,)),
+            _arg(slots, "slot_mapping", _I64, dev, (T,)), _arg(pos, "positions", _I32, dev, (T,)), T, msk, words,
+            _raw_stream(stream, dev))
+    if dev == torch.cuda.current_device():
+        st = lib.build_block_tables(*args)
+    else:
+        with _OnDevice(dev):
+            st = lib.build_block_tables(*args)
+    if st:
+        _check("build_block_tables", st)
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_workspace(dev: int, batch, total_q, max_nodes, stride, S, Hq, Hkv, D, code, kernel, partition_tokens) -> int:
+    with _on(dev):
+        return int(load_library().paged_attention_tree_workspace_size(
+            batch, total_q, max_nodes, stride, S, Hq, Hkv, D, code, _opts_of(0, kernel, partition_tokens)))
 
 
 def tree_workspace_size(batch: int, total_q: int, max_nodes: int, block_table_stride: int, block_size: int,
                         n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
                         partition_tokens: int = 0, kernel: int = 0) -> int:
     """Workspace bytes of :func:`paged_attention_tree` for these sizes on the current device."""
-    lib = load_library()
-    opts = make_opts(partition_tokens=partition_tokens, prefill_kernel=kernel)
-    return int(lib.paged_attention_tree_workspace_size(batch, total_q, max_nodes, block_table_stride, block_size,
-                                                       n_q_heads, n_kv_heads, head_dim, _code(dtype),
-                                                       ctypes.byref(opts)))
+    return _tree_workspace(torch.cuda.current_device(), batch, total_q, max_nodes, block_table_stride, block_size,
+                           n_q_heads, n_kv_heads, head_dim, _code(dtype), kernel, partition_tokens)
 
 
 def _scratch(nbytes: int, device, stream):
@@ -536,49 +595,44 @@ def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_ta
     allows); a tight bound saves idle blocks.  ``workspace``: "auto" (allocated for the call on its
     stream), None (contexts are not split) or a caller-owned uint8 CUDA tensor.  ``kernel``: 0 auto, 1
     CUDA cores, 2 tcgen05.  Rows from ``query_start_loc[batch]`` on are left as they were."""
-    lib = load_library()
-    NB, S, Hkv, D = _pool_dims(k_pool, v_pool)
-    if q.dim() != 3 or q.shape[2] != D:
+    lib = _lib or load_library()
+    dev, shape = q.get_device(), q.shape
+    kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev)
+    if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [total_q, n_q_heads, head_dim]")
-    total_q, Hq, dev = int(q.shape[0]), int(q.shape[1]), q.device
-    B = int(context_lens.numel())
-    if block_table.dim() != 2 or block_table.shape[0] != B or (B and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [batch, max_blocks] with contiguous rows")
-    words = 0
+    total_q, Hq, _ = shape
+    dt, B = k_pool.dtype, context_lens.numel()
+    code = _code(dt)
+    words, mask = 0, None
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q or tree_mask.shape[1] < 1:
             raise ValueError("tree_mask must be [total_q, words]")
-        words = int(tree_mask.shape[1])
+        words = tree_mask.shape[1]
+        mask = _arg(tree_mask, "tree_mask", _I64, dev)
     if max_nodes is None:
         max_nodes = max(1, min(total_q, 64 * words) if words else total_q)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dt = k_pool.dtype
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    _same_device(dev, query_start_loc=query_start_loc, tree_mask=tree_mask, k_pool=k_pool, v_pool=v_pool,
-                 block_table=block_table, context_lens=context_lens, out=out)
-    opts = make_opts(_block_stride_bytes(k_pool, v_pool), prefill_kernel=kernel, partition_tokens=partition_tokens)
-    bt_stride = int(block_table.stride(0))
-    with _OnDevice(dev):
-        ws = workspace
-        if isinstance(workspace, str) and workspace == "auto":
-            n = lib.paged_attention_tree_workspace_size(B, total_q, max_nodes, bt_stride, S, Hq, Hkv, D, _code(dt),
-                                                        ctypes.byref(opts))
-            ws = _scratch(n, dev, stream) if n else None
-        elif ws is not None:
-            _same_device(dev, workspace=ws)
-        st = lib.paged_attention_tree(
-            _dev(out, "out", dt), _dev(q, "q", dt), _vector(query_start_loc, "query_start_loc", B + 1), total_q,
-            _dev(tree_mask, "tree_mask", torch.int64) if words else None, words, max_nodes,
-            _pool(k_pool, "k_pool", dt), _pool(v_pool, "v_pool", dt),
-            _dev(block_table, "block_table", torch.int32, contiguous=False), bt_stride,
-            _vector(context_lens, "context_lens", B), B, NB, S, float(scale), Hq, Hkv, D, _code(dt),
-            _dev(ws, "workspace", torch.uint8) if ws is not None else None, int(ws.numel()) if ws is not None else 0,
-            ctypes.byref(opts), _stream(stream))
-    _check("paged_attention_tree", st)
+    table, bt_stride, _ = _table(block_table, "block_table", B, dev)
+    args = (_arg(out, "out", dt, dev, shape), _arg(q, "q", dt, dev),
+            _arg(query_start_loc, "query_start_loc", _I32, dev, (B + 1,)), total_q, mask, words, max_nodes, kp, vp,
+            table, bt_stride, _arg(context_lens, "context_lens", _I32, dev, (B,)), B, NB, S, scale, Hq, Hkv, D, code)
+    ws = workspace
+    if workspace is not None and isinstance(workspace, str) and workspace == "auto":
+        n = _tree_workspace(dev, B, total_q, max_nodes, bt_stride, S, Hq, Hkv, D, code, kernel, partition_tokens)
+        ws = _scratch(n, q.device, stream) if n else None
+    args += ((_arg(ws, "workspace", torch.uint8, dev), ws.numel()) if ws is not None else (None, 0))
+    args += (_opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), kernel, partition_tokens),
+             _raw_stream(stream, dev))
+    if dev == torch.cuda.current_device():
+        st = lib.paged_attention_tree(*args)
+    else:
+        with _OnDevice(dev):
+            st = lib.paged_attention_tree(*args)
+    if st:
+        _check("paged_attention_tree", st)
     return out
 
 
@@ -587,38 +641,32 @@ def paged_kv_accept(k_pool, v_pool, accepted, accepted_lens, history_lens, block
     node ``accepted[b, i]`` (position ``history_lens[b] + accepted[b, i]``) move to position
     ``history_lens[b] + i``.  ``accepted`` int32 [B, A], each list ascending.  The pools are one
     layer's ``[num_blocks, block_size, Hkv, D]`` or all layers' ``[layers, num_blocks, ...]``."""
-    lib = load_library()
-    if k_pool.dim() != v_pool.dim() or k_pool.dim() not in (4, 5) or k_pool.shape != v_pool.shape:
-        raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, n_kv_heads, head_dim], with the "
-                         "layers in front or without")
-    layers, layer_stride = 1, 0
-    k0, v0 = k_pool, v_pool
-    if k_pool.dim() == 5:
-        layers = int(k_pool.shape[0])
+    lib = _lib or load_library()
+    dev, layers, layer_stride, shape = k_pool.get_device(), 1, 0, k_pool.shape
+    lead = 1 if len(shape) == 5 else 0
+    if lead and v_pool.shape == shape:
+        layers = shape[0]
         if layers == 0:
             return
-        if layers > 1 and k_pool.stride(0) != v_pool.stride(0):
+        layer_stride = k_pool.stride(0)
+        if layers > 1 and v_pool.stride(0) != layer_stride:
             raise ValueError("the layers of k_pool and v_pool must be equally far apart")
-        layer_stride = int(k_pool.stride(0)) * k_pool.element_size()
-        k0, v0 = k_pool[0], v_pool[0]
-    NB, S, Hkv, D = _pool_dims(k0, v0)
-    dt, dev = k0.dtype, k0.device
-    B = int(accepted_lens.numel())
-    if accepted.dim() != 2 or accepted.shape[0] != B or (accepted.shape[1] and accepted.stride(1) != 1):
-        raise ValueError("accepted must be [batch, entries] with contiguous rows")
-    if block_table.dim() != 2 or block_table.shape[0] != B or (B and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [batch, max_blocks] with contiguous rows")
-    _same_device(dev, v_pool=v0, accepted=accepted, accepted_lens=accepted_lens, history_lens=history_lens,
-                 block_table=block_table)
-    opts = make_opts(_block_stride_bytes(k0, v0))
-    with _OnDevice(dev):
-        st = lib.paged_kv_accept(
-            _pool(k0, "k_pool"), _pool(v0, "v_pool", dt), layers, layer_stride,
-            _dev(accepted, "accepted", torch.int32, contiguous=False), int(accepted.stride(0)),
-            int(accepted.shape[1]), _vector(accepted_lens, "accepted_lens", B),
-            _vector(history_lens, "history_lens", B), _dev(block_table, "block_table", torch.int32, contiguous=False),
-            int(block_table.stride(0)), B, NB, S, Hkv, D, _code(dt), ctypes.byref(opts), _stream(stream))
-    _check("paged_kv_accept", st)
+        layer_stride *= k_pool.element_size()
+    kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev, lead)
+    B = accepted_lens.numel()
+    acc, acc_stride, entries = _table(accepted, "accepted", B, dev)
+    table, bt_stride, _ = _table(block_table, "block_table", B, dev)
+    args = (kp, vp, layers, layer_stride, acc, acc_stride, entries,
+            _arg(accepted_lens, "accepted_lens", _I32, dev, (B,)), _arg(history_lens, "history_lens", _I32, dev, (B,)),
+            table, bt_stride, B, NB, S, Hkv, D, _code(k_pool.dtype),
+            _opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), 0, 0), _raw_stream(stream, dev))
+    if dev == torch.cuda.current_device():
+        st = lib.paged_kv_accept(*args)
+    else:
+        with _OnDevice(dev):
+            st = lib.paged_kv_accept(*args)
+    if st:
+        _check("paged_kv_accept", st)
 
 
 def copy_blocks(k_pool, v_pool, block_pairs, stream=None):
