@@ -579,12 +579,13 @@ TreePlan plan_tree(bool tensor_cores, int batch, int64_t total_q, int max_nodes,
     // one CTA per SM, each with an equal share; an explicit partition length sets the share instead
     const int unit_rows = tree_unit_rows(max_nodes, group);
     const int64_t units = (int64_t)batch * n_kv_heads * (((int64_t)max_nodes * group + unit_rows - 1) / unit_rows);
-    const int64_t tiles = (max_len + 63) / 64;
-    bool split = tiles > 8;  // (shorter contexts are never cut, see tu_schedule)
+    const int keys = tree_tile_keys(head_dim, unit_rows);
+    const int64_t tiles = (max_len + keys - 1) / keys;
+    bool split = tiles > tree_min_share(unit_rows) - tree_gap(unit_rows);
     int64_t ctas = units < sms ? units * (tiles < sms ? tiles : sms) : sms;
     ctas = ctas < sms ? ctas : sms;
     if (partition_tokens > 0) {
-      p.share = (int)((partition_tokens + 63) / 64);
+      p.share = (int)((partition_tokens + keys - 1) / keys);
       ctas = (units * tiles + p.share - 1) / p.share;
       split = tiles > 1;
     }

@@ -195,6 +195,11 @@ struct TreeRec {
 
 // Rows of a unit of the tcgen05 tree attention: one or two tiles of 128 (node, head) rows.
 inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes * group <= 128 ? 128 : 256; }
+// Keys of one of its key tiles (see tree_umma.cu), and the fewest tiles a CTA takes; shorter contexts are
+// never cut.
+constexpr int tree_tile_keys(int head_dim, int unit_rows) { return head_dim == 64 || unit_rows == 256 ? 128 : 64; }
+constexpr int tree_gap(int unit_rows) { return unit_rows == 256 ? 3 : 4; }
+constexpr int tree_min_share(int unit_rows) { return unit_rows == 256 ? 8 : 12; }
 
 struct AcceptArgs {
   void* k_pool;

@@ -36,22 +36,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
 // Division of the tensor-core kernel's work among its CTAs.
 //
 // A unit is (sequence, KV head, tile of its nodes); its key tiles are read in order.  All units in a
-// row (sequences, then KV heads, then node tiles) make one line of tiles, each unit followed by
-// `kTreeGap` tiles' worth of what it costs besides its keys, and CTA c takes positions
-// [c * share, (c + 1) * share) of the line: every CTA streams the same bytes whatever the lengths, and
-// only the units that a cut falls into have to be joined afterwards.  A cut closer than `snap` tiles to
-// a unit's border moves to it.
-constexpr int kTreeKeys = 64;  // keys per tile
-constexpr int kTreeGap = 4;
-constexpr int kTreeSnap = 3;
-constexpr int kTreeMinShare = 12;
-
+// row (sequences, then KV heads, then node tiles) make one line of key tiles, each unit followed by a gap
+// for what it costs besides its keys, and CTA c takes positions [c * share, (c + 1) * share) of the line:
+// every CTA streams the same bytes whatever the lengths, and only the units that a cut falls into have to
+// be joined afterwards.  A cut closer than `snap` tiles to a unit's border moves to it.
 struct TreeSpan {
   int b0, u0, x0;  // first sequence, unit of it, tile of that
   int b1, u1, x1;  // end (exclusive); b1 = batch: the end of the line
 };
-
-__device__ __forceinline__ int tree_tiles(int n) { return (n + kTreeKeys - 1) / kTreeKeys; }
 
 // Tile of a unit of T tiles at which a cut at position x of the unit (its gap included) is made.
 __device__ __forceinline__ int tree_cut(int64_t x, int T, int snap) {
@@ -66,10 +58,11 @@ __device__ __forceinline__ int tree_cut(int64_t x, int T, int snap) {
 struct TreeUnit {
   TreeSeq sq;
   int b, kvh, node0, rows;  // rows: (node, head) rows that exist
-  int T, x0, x1;            // tiles of the unit, and those of this CTA
+  int T, x0, x1;            // key tiles of the unit, and those of this CTA
   bool last_tile;           // no later node tile reads the same keys
 };
 
+template <int kKeys>
 struct TreeWalk {
   const TreeArgs& a;
   const TreeSpan span;
@@ -97,7 +90,7 @@ struct TreeWalk {
       w.kvh = u / q_tiles;
       w.node0 = qt * nodes_unit;
       w.rows = min(nodes_unit, sq.m - w.node0) << a.group_shift;
-      w.T = tree_tiles(sq.n);
+      w.T = (sq.n + kKeys - 1) / kKeys;
       w.x0 = x;
       w.x1 = b == span.b1 && u == span.u1 ? span.x1 : w.T;
       w.last_tile = qt == q_tiles - 1;

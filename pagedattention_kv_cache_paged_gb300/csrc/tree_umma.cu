@@ -1,32 +1,34 @@
 // tcgen05 tree attention (bf16/fp16 pools, block_size % 16 == 0).
 //
-// Persistent: one CTA per SM walks its equal share of the units (tree_common.cuh).  Per 64-key tile:
-// S = Q K^T into a TMEM buffer, the softmax threads (one TMEM lane each) turn it into P in place, O +=
-// P V in TMEM; one pass with a running stabiliser that moves only when the maximum grows by more than
-// 2^8 (numerator and denominator use the same one, so the result is the softmax's in real arithmetic).
-// K and V pass through a ring each that runs on into the next unit while the last one is finished, so that
-// the loads never pause at a border.
+// Persistent: one CTA per SM walks its equal share of the units (tree_common.cuh).  Per key tile: S = Q K^T
+// into a TMEM buffer, the softmax threads (one TMEM lane each) turn it into P in place, O += P V in TMEM;
+// one pass with a running stabiliser that moves only when the maximum grows by more than 2^8 (numerator
+// and denominator use the same one, so the result is the softmax's in real arithmetic).  K and V pass
+// through a ring each that runs on into the next unit while the last one is finished, so that the loads
+// never pause at a border.
 //
-// One thread is too slow to keep an SM's share of HBM3e moving (a wait, an issue and a commit cost it a
-// few hundred cycles, a 64-key tile passes every 1,400), so the control work is spread over five warps: K
-// and V producers, S products, P V products, Q; and each tile has one commit per product, whose barrier
-// tells the softmax, the producer and the other issuer alike.
+// Two groups of four softmax warps, each with an O of its own.
+//   Narrow kernel (no sequence has more than 128 (node, head) rows): bound by HBM.  The groups take the key
+//     tiles of a unit in turn and their states are joined at its end (both Os lie in the same TMEM lanes, so
+//     only (maximum, sum) goes through shared memory, and each group writes half of the columns).  A tile
+//     passes every 1,400 cycles at HBM's rate, the round S, softmax, P V through the barriers takes about
+//     3,500, so four tiles (three at head_dim 64, which takes 128-key tiles to have the same bytes per
+//     round) are in flight; and one thread would need 2,100 cycles for the waits, issues and commits of a
+//     tile, so four warps share them (K, V, S, P V), each product's one commit telling the softmax, the
+//     producer and the other issuer alike.
+//   Wide kernel: bound by the softmax and the tensor core.  A unit of more than 128 rows has two Q tiles,
+//     one per group, that share every 128-key K and V tile; one thread issues S_0(j), P_1(j-1) V, S_1(j),
+//     P_0(j) V, .., so that products in issue order need no barrier between a P V and the S that overwrites
+//     its P.  A unit of at most 128 rows goes through the same sequence with the groups on tiles in turn.
 //
-// Two groups of four softmax warps, each with two S buffers and an O of its own (512 TMEM columns):
-//   narrow (a sequence's rows fit one 128-row tile): the groups take the key tiles of the unit in
-//     turn, which halves the serial work per tile; their states are joined at the unit's end (both
-//     Os lie in the same TMEM lanes, so only (maximum, sum) goes through shared memory, and each
-//     group writes half of the columns);
-//   wide: the unit has two 128-row tiles, one per group, that share every K and V tile.
+// Masks.  Only tiles that reach into the drafted region look at masks: a row's visibility bits are cut
+// out of its mask words.  A masked score becomes -inf by selection, whatever it was.  A masked value cannot
+// be deselected (0 * NaN), so in those tiles non-finite elements of V are zeroed in shared memory before
+// the product, and added at the end, by themselves, to the rows that see them.
 //
-// Masks.  Only tiles that reach into the drafted region look at masks: a row's 64 visibility bits are
-// cut out of its mask words.  A masked score becomes -inf by selection, whatever it was.  A masked
-// value cannot be deselected (0 * NaN), so in those tiles non-finite elements of V are zeroed in
-// shared memory before the product, and added at the end, by themselves, to the rows that see them.
-//
-// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 S, 11 P V, 12 Q.  Every wait is bounded
-// (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each barrier below is
-// waited for before its next phase but one can complete.
+// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 Q and S (wide: both products), 11 P V (wide: Q).
+// Every wait is bounded (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each
+// barrier below is waited for before its next phase but one can complete.
 #include <cudaTypedefs.h>
 #include <float.h>
 
@@ -35,24 +37,30 @@
 
 namespace pa {
 
-constexpr int kTuThreads = 416;
-constexpr int kTuSubs = kTreeKeys / 16;
+// 12 warps: a thirteenth would leave 128 registers a thread
+constexpr int kTuThreads = 384;
 constexpr float kTuRescale = 8.f;
 
 template <int D, bool kWide>
 struct TuCfg {
+  static constexpr int kUnitRows = kWide ? 256 : 128;
+  static constexpr int kKeys = tree_tile_keys(D, kUnitRows);
+  static constexpr int kSubs = kKeys / 16;
   static constexpr int kHalves = D / 64;
   static constexpr int kQHalf = 128 * 128;          // one 64-column half of a 128-row Q tile
   static constexpr int kQTile = kQHalf * kHalves;
   static constexpr int kQBytes = (kWide ? 2 : 1) * kQTile;
-  static constexpr int kKvBytes = kTreeKeys * D * 2;  // a stage: one K or V tile
+  static constexpr int kKvBytes = kKeys * D * 2;    // a stage: one K or V tile
   static constexpr int kGroup = 1024 * kHalves;     // 8 keys of it
-  static constexpr int kHead = 4096;                // barriers, masks, row statistics
+  static constexpr int kHead = kWide ? 2048 : 4096;  // barriers, masks, row statistics
   static constexpr int kFit = (227 * 1024 - 1024 - kHead - kQBytes) / kKvBytes;
   static constexpr int kKStages = kFit / 2 < 12 ? kFit / 2 : 12;
   static constexpr int kVStages = kFit - kFit / 2 < 12 ? kFit - kFit / 2 : 12;
   static constexpr int kSmemBytes = 1024 + kHead + kQBytes + (kKStages + kVStages) * kKvBytes;
-  static constexpr int kBufs = kWide ? 2 : 4;       // S buffers: tiles whose scores or weights are in TMEM
+  // TMEM: S buffers (narrow: tiles in flight; wide: one per group), then the two Os
+  static constexpr int kBufs = kWide ? 2 : (512 - 2 * D) / kKeys;
+  static constexpr int kOColumn = kBufs * kKeys;
+  static_assert(kOColumn + 2 * D <= 512, "tensor memory");
 };
 
 // Whether one of the two 16-bit floats in w is infinite or NaN.
@@ -78,6 +86,53 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 
+// 64 consecutive scores of this thread's row; those it does not see become -inf (kMasked).
+template <bool kMasked>
+__device__ __forceinline__ void tu_scores(uint32_t taddr, uint64_t keep, uint32_t (&sv)[64]) {
+  tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+  tmem_ld32(taddr + 32u, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+  tmem_wait_ld();
+  tmem_pin32(*reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+  tmem_pin32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+  if (kMasked) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+      if (!((keep >> c) & 1ull)) sv[c] = 0xff800000u;
+  }
+}
+
+__device__ __forceinline__ float tu_max(const uint32_t (&sv)[64]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 64; c += 8)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      m[u] = fmax3(m[u], __uint_as_float(sv[c + 2 * u]), __uint_as_float(sv[c + 2 * u + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Weights 2^(s * sc - m) of 64 scores as 16-bit pairs into the 32 columns at taddr; their sum.  Weights are
+// rounded to the pool's type for the product with V (half a step each); the sum keeps 32 bits.
+template <bool kBf16>
+__device__ __forceinline__ float tu_weights(uint32_t taddr, const uint32_t (&sv)[64], float sc, float m) {
+  const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(-m, -m);
+  uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+  uint32_t p[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sc2, nm2), x0, x1);
+    const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+    sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(e0, e1));
+    p[c] = pack2<kBf16>(e0, e1);
+  }
+  tmem_st32(taddr, p);
+  float a0, a1, b0, b1;
+  f2_unpack(sum2[0], a0, a1);
+  f2_unpack(sum2[1], b0, b1);
+  return (a0 + a1) + (b0 + b1);
+}
+
 // The span of this CTA (all threads; sm: one word per warp twice, carry and result).
 struct TuSched {
   int64_t sums[kTuThreads / 32];
@@ -90,10 +145,12 @@ struct TuSched {
   int refused;  // a sequence of the batch is refused, and its rows are this CTA's to zero
 };
 
+template <int kKeys, int kUnitRows>
 __device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, TuSched& sm) {
+  constexpr int kGap = tree_gap(kUnitRows), kMinShare = tree_min_share(kUnitRows), kSnap = kGap - 1;
   constexpr int kWarps = kTuThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gap = a.share > 0 ? 0 : kTreeGap;
+  const int gap = a.share > 0 ? 0 : kGap;
   if (threadIdx.x == 0) {
     sm.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
     sm.carry = 0;
@@ -109,7 +166,7 @@ __device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, T
       if (s.m > 0 && b % gridDim.x == blockIdx.x) sm.refused = 1;
     }
     if (s.n == 0 || s.m == 0) return 0;
-    tiles = tree_tiles(s.n);
+    tiles = (s.n + kKeys - 1) / kKeys;
     units = (s.m + nodes_unit - 1) / nodes_unit * a.n_kv_heads;
     return (int64_t)units * (tiles + gap);
   };
@@ -142,10 +199,10 @@ __device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, T
   if (share <= 0) {
     // fewer CTAs than that would wait longer for their first keys than they save
     share = (total + gridDim.x - 1) / gridDim.x;
-    share = max(share, min(longest, (int64_t)kTreeMinShare));
+    share = max(share, min(longest, (int64_t)kMinShare));
   }
   // contexts that are never cut: every border moves to the nearest unit's
-  const int snap = !a.split || longest <= (a.share > 0 ? 0 : kTreeMinShare) ? INT32_MAX : (a.share > 0 ? 1 : kTreeSnap);
+  const int snap = !a.split || longest <= (a.share > 0 ? 0 : kMinShare) ? INT32_MAX : (a.share > 0 ? 1 : kSnap);
   const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share;
   if (threadIdx.x == 0) {
     sm.share = share;
@@ -196,34 +253,40 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     tree_umma_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
   using Cfg = TuCfg<D, kWide>;
+  using Walk = TreeWalk<Cfg::kKeys>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int kHalves = Cfg::kHalves;
+  constexpr int kHalves = Cfg::kHalves, kKeys = Cfg::kKeys, kSubs = Cfg::kSubs;
   constexpr int kKStages = Cfg::kKStages, kVStages = Cfg::kVStages, kBufs = Cfg::kBufs;
-  constexpr int kUnitRows = kWide ? 256 : 128;
+  constexpr int kUnitRows = Cfg::kUnitRows;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // Tile i of the CTA (counted over its units): K stage i % kKStages, V stage i % kVStages, S buffer i % kBufs.
+  // Tile t of the CTA (counted over its units): K stage t % kKStages, V stage t % kVStages, narrow: S buffer
+  // t % kBufs and group t % 2.  "Item": a tile's scores of one group.
   uint64_t* bars = reinterpret_cast<uint64_t*>(base);
   uint64_t* kfull = bars;          // [kKStages] the tile's keys landed
   uint64_t* vfull = bars + 12;     // [kVStages] its values
-  uint64_t* sdone = bars + 24;     // [kKStages] its scores are in its S buffer (and the K stage is free)
-  uint64_t* vdone = bars + 36;     // [kVStages] O += P V done (and the V stage and the S buffer are free)
-  uint64_t* p_full = bars + 48;    // [kBufs] its weights are written (and O rescaled)
+  uint64_t* sdone = bars + 24;     // [kKStages] the S products of the tile are done (the K stage is free)
+  uint64_t* vdone = bars + 36;     // [kVStages] the P V products of the tile are done (the V stage is free)
+  uint64_t* p_full = bars + 48;    // [kBufs] the buffer's weights are written (and O rescaled)
   uint64_t* q_full = bars + 52;    // one phase per unit
   uint64_t* o_free = bars + 53;    // one phase per unit: both Os read
-  uint64_t* ml_full = bars + 54;   // one phase per unit (narrow): both groups' statistics written
-  uint64_t* q_empty = bars + 55;   // one phase per unit: its S products are done (sdone would not do: the Q
-                                   // producer may be more than one phase ahead of it)
+  uint64_t* ml_full = bars + 54;   // one phase per unit whose groups are joined: statistics written
+  uint64_t* q_empty = bars + 55;   // wide: one phase per unit: its S products are done (sdone would not do: the
+                                   // Q producer may be more than one phase ahead of it)
   uint64_t* fin = bars + 56;       // [2] all products of an issuer are over
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 480);
-  volatile int* bad_v = reinterpret_cast<int*>(base + 484);  // V of a drafted region held non-finite elements
+  uint64_t* s_full = bars + 58;    // [2] wide: the group's scores are written, one phase per item
+  uint64_t* o_full = bars + 60;    // wide: one phase per unit: both Os complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 496);
+  volatile int* bad_v = reinterpret_cast<int*>(base + 500);  // V of a drafted region held non-finite elements
   volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 512);  // [32] 16-key sub-tiles loaded, per tile
   TuSched* sched = reinterpret_cast<TuSched*>(base + 640);
-  float2* ml = reinterpret_cast<float2*>(base + 2048);  // [2][128] the groups' (maximum, sum) per row
-  static_assert(sizeof(TuSched) <= 2048 - 640 && kKStages <= 12 && kVStages <= 12, "head of the shared memory");
-  // (S of tile i + kBufs waits for P V of tile i, and phases stay one apart only if the rings are not shorter)
-  static_assert(kKStages >= kBufs && kVStages >= kBufs, "ring depths");
+  // (maximum, sum) per row: narrow [2][128], of both groups; wide [128], of group 1
+  float2* ml = reinterpret_cast<float2*>(base + (kWide ? 1024 : 2048));
+  static_assert(640 + sizeof(TuSched) <= (kWide ? 1024 : 2048) && kKStages <= 12 && kVStages <= 12, "head");
+  // (S of tile t + kBufs waits for P V of tile t, and phases stay one apart only if the rings are not shorter)
+  static_assert(kWide || (kKStages >= kBufs && kVStages >= kBufs && kBufs <= 4), "ring depths");
+  static_assert(kKStages >= 2 && kVStages >= 2, "ring depths");
   uint8_t* qs = base + Cfg::kHead;
   uint8_t* ks = qs + Cfg::kQBytes;
   uint8_t* vs = ks + kKStages * Cfg::kKvBytes;
@@ -243,13 +306,16 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       mbar_init(&vfull[k], 1);
       mbar_init(&vdone[k], 1);
     }
-    for (int k = 0; k < kBufs; ++k) mbar_init(&p_full[k], kWide ? 8 : 4);
+    for (int k = 0; k < kBufs; ++k) mbar_init(&p_full[k], 4);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 8);
     mbar_init(ml_full, 8);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(o_full, 1);
     *bad_v = 0;
     fence_barrier_init();
   }
@@ -258,20 +324,29 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
   const int nodes_unit = kUnitRows >> a.group_shift;
-  tu_schedule(a, nodes_unit, *sched);
+  tu_schedule<kKeys, kUnitRows>(a, nodes_unit, *sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const TreeSpan span = sched->span;
-  // S of group g in buffer i, and its O.  Narrow: tile i is group i % 2's and its four buffers are the four
-  // 64-column ranges; wide: a buffer holds both groups' scores.
-  auto tS = [&](int i, int g) { return tmem + 64u * (uint32_t)(kWide ? 2 * i + g : i); };
-  auto tO = [&](int g) { return tmem + 256u + 128u * (uint32_t)g; };
+  auto tS = [&](int buf) { return tmem + (uint32_t)(kKeys * buf); };  // wide: buffer = group
+  auto tO = [&](int g) { return tmem + (uint32_t)(Cfg::kOColumn + D * g); };
+
+  // the Q tiles of a unit (one thread)
+  auto load_q = [&](const TreeUnit& w) {
+    const int tiles = kWide && w.rows > 128 ? 2 : 1;
+    mbar_arrive_expect_tx(q_full, tiles * Cfg::kQTile);
+    for (int k = 0; k < tiles; ++k)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        tma_load_3d(qs + k * Cfg::kQTile + h * Cfg::kQHalf, &qmap, h * 64, w.kvh << a.group_shift,
+                    (int)(w.sq.q0 + w.node0) + k * (128 >> a.group_shift), q_full);
+  };
 
   if (warp == 8 || warp == 9) {
     // ------------------------------- producers: warp 8 K, warp 9 V --------------------------------
-    // One box is 8 x (up to 8) keys x head_dim of one block: a tile takes 64 / min(block_size, 64) of them,
+    // One box is 8 x (up to 8) keys x head_dim of one block: a tile takes kKeys / min(block_size, 64) of them,
     // one per lane, and lies in shared memory as [8-key group][64-column half][8][128 bytes, swizzled].
     const bool is_v = warp == 9;
     uint64_t* full = is_v ? vfull : kfull;
@@ -279,17 +354,17 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     uint8_t* ring = is_v ? vs : ks;
     const CUtensorMap* map = is_v ? &vmap : &kmap;
     const int depth = is_v ? kVStages : kKStages;
-    const int box_keys = min(a.block_size, kTreeKeys), boxes = kTreeKeys / box_keys;
+    const int box_keys = min(a.block_size, 64), boxes = kKeys / box_keys;
     const uint64_t once = l2_policy_evict_first();
     int t = 0, s = 0, round = 0;
     bool alive = true;
-    TreeWalk walk(a, span, nodes_unit);
+    Walk walk(a, span, nodes_unit);
     TreeUnit w;
     while (alive && walk.next(w)) {
       const int32_t* table = a.block_table + (int64_t)w.b * a.bt_stride;
       // table entry of this lane's box of tile x of the unit (-1: behind the context)
       auto entry = [&](int x) -> int {
-        const int pos = x * kTreeKeys + lane * box_keys;
+        const int pos = x * kKeys + lane * box_keys;
         return lane < boxes && x < w.x1 && pos < w.sq.n ? ld_nc_s32(table + (pos >> a.block_shift)) : -1;
       };
       int blk = entry(w.x0);
@@ -299,7 +374,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
           alive = false;
           break;
         }
-        const int pos = x * kTreeKeys + lane * box_keys;
+        const int pos = x * kKeys + lane * box_keys;
         const bool in = lane < boxes && pos < w.sq.n;
         const bool ok = in && blk >= 0 && blk < a.num_blocks;
         if (in && !ok && !is_v) raise_error(a.err, PA_DEVERR_BLOCK_ID);
@@ -339,120 +414,142 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       for (int k = t > depth ? t - depth : 0; k < t; ++k) mbar_wait(&full[k % depth], (unsigned)((k / depth) & 1));
     }
     __syncwarp();
-  } else if (warp == 12) {
+  } else if (kWide && warp == 11) {
     // --------------------------------------- Q producer ------------------------------------------
     if (lane == 0) {
       int un = 0;
       bool alive = true;
-      TreeWalk walk(a, span, nodes_unit);
+      Walk walk(a, span, nodes_unit);
       TreeUnit w;
       for (; walk.next(w); ++un) {
         if (un > 0 && !mbar_wait(q_empty, (unsigned)((un - 1) & 1), a.err, a.epoch)) {
           alive = false;
           break;
         }
-        const int tiles = kWide && w.rows > 128 ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, tiles * Cfg::kQTile);
-        for (int k = 0; k < tiles; ++k)
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            tma_load_3d(qs + k * Cfg::kQTile + h * Cfg::kQHalf, &qmap, h * 64, w.kvh << a.group_shift,
-                        (int)(w.sq.q0 + w.node0) + k * (128 >> a.group_shift), q_full);
+        load_q(w);
       }
       if (!alive) raise_timeout(a.err, a.epoch);
       if (un > 0) mbar_wait(q_full, (unsigned)((un - 1) & 1));  // no copy in flight
     }
     __syncwarp();
-  } else if (warp == 10) {
-    // -------------------------------------- S = Q K^T --------------------------------------------
-    if (lane == 0) {
-      const uint32_t id = umma_idesc_f16(kBf16, 128, kTreeKeys, false, false);
+  } else if (warp == 10 || warp == 11) {
+    // ------------------- products: narrow: warp 10 Q and S, warp 11 P V; wide: warp 10 ---------------
+    if (lane == 0 && (!kWide || warp == 10)) {
+      const uint32_t id_s = umma_idesc_f16(kBf16, 128, kKeys, false, false);
+      const uint32_t id_pv = umma_idesc_f16(kBf16, 128, D, false, true);
       const uint64_t qd = umma_desc_sw128(smem_u32(qs), 16, 1024), kd = umma_desc_sw128(smem_u32(ks), 16, Cfg::kGroup);
-      int t = 0, s = 0, round = 0, un = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && mbar_wait(bar, (unsigned)(phase & 1), a.err, a.epoch);
-        return ok;
-      };
-      TreeWalk walk(a, span, nodes_unit);
-      TreeUnit w;
-      while (ok && walk.next(w)) {
-        const bool two = kWide && w.rows > 128;
-        if (!wait(q_full, un)) break;
-        for (int x = w.x0; x < w.x1; ++x, ++t) {
-          // the buffer still holds the weights of tile t - kBufs until their product is done
-          if (t >= kBufs && !wait(&vdone[(t - kBufs) % kVStages], (t - kBufs) / kVStages)) break;
-          if (!wait(&kfull[s], round)) break;
-          tc_fence_after();
-          const uint64_t kt = kd + (uint64_t)(s * (Cfg::kKvBytes >> 4));
-          const int buf = t % kBufs;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tS(buf, 0), qd + (kk >> 2) * (Cfg::kQHalf >> 4) + (kk & 3) * 2, kt + (kk >> 2) * 64 + (kk & 3) * 2, id,
-                    kk > 0 ? 1u : 0u);
-          if (two) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(tS(buf, 1), qd + (Cfg::kQTile >> 4) + (kk >> 2) * (Cfg::kQHalf >> 4) + (kk & 3) * 2,
-                      kt + (kk >> 2) * 64 + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&sdone[s]);
-          if (x == w.x1 - 1) umma_commit(q_empty);
-          if (++s == kKStages) {
-            s = 0;
-            ++round;
-          }
-        }
-        ++un;
-      }
-      if (!ok) raise_timeout(a.err, a.epoch);
-      umma_commit(&fin[0]);  // no product in flight when the tensor memory is given back
-      mbar_wait(&fin[0], 0);
-    }
-    __syncwarp();
-  } else if (warp == 11) {
-    // -------------------------------------- O += P V ---------------------------------------------
-    if (lane == 0) {
-      const uint32_t id = umma_idesc_f16(kBf16, 128, D, false, true);
       const uint64_t vd = umma_desc_sw128(smem_u32(vs), 1024, Cfg::kGroup);
-      int t = 0, s = 0, round = 0, un = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
         ok = ok && mbar_wait(bar, (unsigned)(phase & 1), a.err, a.epoch);
         return ok;
       };
-      TreeWalk walk(a, span, nodes_unit);
+      auto s_product = [&](int buf, int q_tile, int stage) {
+        const uint64_t q = qd + (uint64_t)(q_tile * (Cfg::kQTile >> 4)), k = kd + (uint64_t)(stage * (Cfg::kKvBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(tS(buf), q + (kk >> 2) * (Cfg::kQHalf >> 4) + (kk & 3) * 2, k + (kk >> 2) * 64 + (kk & 3) * 2, id_s,
+                  kk > 0 ? 1u : 0u);
+      };
+      auto pv_product = [&](int g, int buf, int stage, bool first) {
+        const uint64_t v = vd + (uint64_t)(stage * (Cfg::kKvBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          umma_ts(tO(g), tS(buf) + 8u * (uint32_t)kk, v + kk * (2 * Cfg::kGroup >> 4), id_pv, kk > 0 || !first ? 1u : 0u);
+      };
+      Walk walk(a, span, nodes_unit);
       TreeUnit w;
-      while (ok && walk.next(w)) {
-        const bool two = kWide && w.rows > 128;
-        // the unit's first products overwrite the Os that the unit before it left
-        if (un > 0 && !wait(o_free, un - 1)) break;
-        for (int x = w.x0; x < w.x1; ++x, ++t) {
-          const int buf = t % kBufs;
-          if (!wait(&vfull[s], round) || !wait(&p_full[buf], t / kBufs)) break;
-          tc_fence_after();
-          const uint64_t vt = vd + (uint64_t)(s * (Cfg::kKvBytes >> 4));
-          const int g = kWide ? 0 : t & 1;
-          const uint32_t more = x >= w.x0 + (kWide ? 1 : 2) ? 1u : 0u;
-#pragma unroll
-          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-            umma_ts(tO(g), tS(buf, g) + 8u * (uint32_t)kk, vt + kk * (2 * Cfg::kGroup >> 4), id, kk > 0 ? 1u : more);
-          if (two) {
-#pragma unroll
-            for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-              umma_ts(tO(1), tS(buf, 1) + 8u * (uint32_t)kk, vt + kk * (2 * Cfg::kGroup >> 4), id, kk > 0 ? 1u : more);
+      int un = 0;
+      if constexpr (kWide) {
+        int ks_ = 0, kr = 0, vs_ = 0, vr = 0;  // ring stages and rounds
+        int done[2] = {0, 0};                  // items of each group so far
+        while (ok && walk.next(w)) {
+          const bool pair = w.rows > 128;
+          const int items = (w.x1 - w.x0) << (pair ? 1 : 0);
+          if (!wait(q_full, un)) break;
+          // item k: group k % 2; S of item k overwrites P of item k - 2, whose P V was issued before it
+          for (int k = 0; k <= items; ++k) {
+            if (k < items) {
+              const int g = k & 1;
+              if ((!pair || g == 0) && !wait(&kfull[ks_], kr)) break;
+              tc_fence_after();
+              s_product(g, pair ? g : 0, ks_);
+              umma_commit(&s_full[g]);
+              if (!pair || g == 1) {
+                umma_commit(&sdone[ks_]);
+                if (++ks_ == kKStages) {
+                  ks_ = 0;
+                  ++kr;
+                }
+              }
+              if (k == items - 1) umma_commit(q_empty);
+            }
+            if (k > 0) {
+              const int j = k - 1, g = j & 1;
+              if ((!pair || g == 0) && !wait(&vfull[vs_], vr)) break;
+              // the unit's first product overwrites the Os that the unit before it left
+              if (j == 0 && un > 0 && !wait(o_free, un - 1)) break;
+              if (!wait(&p_full[g], done[g])) break;
+              ++done[g];
+              tc_fence_after();
+              pv_product(g, g, vs_, j < 2);
+              if (!pair || g == 1) {
+                umma_commit(&vdone[vs_]);
+                if (++vs_ == kVStages) {
+                  vs_ = 0;
+                  ++vr;
+                }
+              }
+              if (j == items - 1) umma_commit(o_full);
+            }
           }
-          umma_commit(&vdone[s]);
-          if (++s == kVStages) {
-            s = 0;
-            ++round;
-          }
+          ++un;
         }
-        ++un;
+      } else if (warp == 10) {
+        int t = 0, s = 0, round = 0;
+        while (ok && walk.next(w)) {
+          // Q is free once the S products of the unit before are done
+          if (t > 0 && !wait(&sdone[(t - 1) % kKStages], (t - 1) / kKStages)) break;
+          load_q(w);
+          if (!wait(q_full, un)) {
+            mbar_wait(q_full, (unsigned)(un & 1));  // no copy in flight
+            break;
+          }
+          for (int x = w.x0; x < w.x1; ++x, ++t) {
+            // the buffer still holds the weights of tile t - kBufs until their product is done
+            if (t >= kBufs && !wait(&vdone[(t - kBufs) % kVStages], (t - kBufs) / kVStages)) break;
+            if (!wait(&kfull[s], round)) break;
+            tc_fence_after();
+            s_product(t % kBufs, 0, s);
+            umma_commit(&sdone[s]);
+            if (++s == kKStages) {
+              s = 0;
+              ++round;
+            }
+          }
+          ++un;
+        }
+      } else {
+        int t = 0, s = 0, round = 0;
+        while (ok && walk.next(w)) {
+          // the unit's first products overwrite the Os that the unit before it left
+          if (un > 0 && !wait(o_free, un - 1)) break;
+          for (int x = w.x0; x < w.x1; ++x, ++t) {
+            if (!wait(&vfull[s], round) || !wait(&p_full[t % kBufs], t / kBufs)) break;
+            tc_fence_after();
+            pv_product(t & 1, t % kBufs, s, x < w.x0 + 2);
+            umma_commit(&vdone[s]);
+            if (++s == kVStages) {
+              s = 0;
+              ++round;
+            }
+          }
+          ++un;
+        }
       }
       if (!ok) raise_timeout(a.err, a.epoch);
-      umma_commit(&fin[1]);  // no product in flight when the tensor memory is given back
-      mbar_wait(&fin[1], 0);
+      umma_commit(&fin[warp - 10]);  // no product in flight when the tensor memory is given back
+      mbar_wait(&fin[warp - 10], 0);
     }
     __syncwarp();
   } else {
@@ -460,29 +557,32 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     const int grp = warp >> 2;
     const int r = threadIdx.x & 127;  // row of the group's tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    int t = 0, un = 0;  // tiles of the CTA's earlier units, and those
+    int t = 0, un = 0, item = 0, solo = 0;  // tiles of earlier units, those, this group's items, joined units
     bool alive = true, cut = false;
-    TreeWalk walk(a, span, nodes_unit);
+    Walk walk(a, span, nodes_unit);
     TreeUnit w;
     while (alive && walk.next(w)) {
       const int n = w.x1 - w.x0;
       const int hist = w.sq.n - w.sq.m;
-      const int rows = kWide ? min(128, w.rows - 128 * grp) : w.rows;  // of this group's tile
-      const bool live = (r & ~31) < rows;                               // whole warps
-      const int node = w.node0 + (kWide ? grp * (128 >> a.group_shift) : 0) + (max(min(r, rows - 1), 0) >> a.group_shift);
+      const bool pair = kWide && w.rows > 128;                        // two Q tiles, one per group
+      const int rows = pair ? min(128, w.rows - 128 * grp) : w.rows;  // of this group's tile
+      const bool live = (r & ~31) < rows;                             // whole warps
+      const int node = w.node0 + (pair ? grp * (128 >> a.group_shift) : 0) + (min(r, rows - 1) >> a.group_shift);
       const int64_t* words = a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
       float m_use = -INFINITY, l_run = 0.f;
 
-      // Bits of the tile at key kb that this row sees (bit c: key kb + c), sub-tiles that are not
-      // loaded and keys behind the context left out.
+      // Bits of the 64 keys from kb on that this row sees (bit c: key kb + c); `loaded`: their sub-tiles
+      // that hold data.
       auto visible = [&](int kb, uint32_t loaded) -> uint64_t {
-        const int s0 = kb - hist;  // node of the tile's first key
+        const int nv = w.sq.n - kb;
+        if (nv <= 0) return 0ull;
+        const int s0 = kb - hist;  // node of the first key
         uint64_t keep;
-        if (s0 + kTreeKeys <= 0) {
+        if (s0 + 64 <= 0) {
           keep = ~0ull;
         } else if (words == nullptr) {
-          const int nv = node + 1 - s0;  // chain: nodes up to its own
-          keep = nv <= 0 ? 0ull : (nv >= 64 ? ~0ull : (1ull << nv) - 1ull);
+          const int c = node + 1 - s0;  // chain: nodes up to its own
+          keep = c <= 0 ? 0ull : (c >= 64 ? ~0ull : (1ull << c) - 1ull);
         } else if (s0 < 0) {
           keep = ((uint64_t)__ldg(words) << -s0) | ((1ull << -s0) - 1ull);
         } else {
@@ -490,66 +590,47 @@ __global__ void __launch_bounds__(kTuThreads, 1)
           keep = (i < a.mask_words ? (uint64_t)__ldg(words + i) : 0ull) >> sh;
           if (sh != 0 && i + 1 < a.mask_words) keep |= (uint64_t)__ldg(words + i + 1) << (64 - sh);
         }
-        const int nv = w.sq.n - kb;
         if (nv < 64) keep &= (1ull << nv) - 1ull;
 #pragma unroll
-        for (int u = 0; u < kTuSubs; ++u)
+        for (int u = 0; u < 4; ++u)
           if (!((loaded >> u) & 1u)) keep &= ~(0xffffull << (16 * u));
         return keep;
       };
 
       // Scores of S buffer buf into weights; `before` >= 0: the group's previous tile of the unit.
       // kMasked: the tile may hold keys that the row does not see.
-      auto tile = [&](auto masked, int buf, uint64_t keep, int before) {
+      auto tile = [&](auto masked, int buf, uint64_t keep0, uint64_t keep1, int before) {
         constexpr bool kMasked = decltype(masked)::value;
-        const uint32_t srow = tS(buf, grp) + lane_base;
+        const uint32_t srow = tS(buf) + lane_base;
+        // 128 keys in two blocks of 64, read twice (maximum, weights): a whole row does not stay in
+        // registers, and a loop keeps the code in the instruction cache.  Block h's weights go to columns
+        // 32 h .. 32 h + 31, whose scores have been read by then.
         uint32_t sv[64];
-        tmem_ld32(srow, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-        tmem_ld32(srow + 32u, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-        tmem_wait_ld();
-        tmem_pin32(*reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-        tmem_pin32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-        if (kMasked) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((keep >> c) & 1ull)) sv[c] = 0xff800000u;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int h = kKeys / 64 - 1; h >= 0; --h) {
+          tu_scores<kMasked>(srow + 64u * h, h ? keep1 : keep0, sv);
+          top = fmaxf(top, tu_max(sv));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 64; c += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mx[u] = fmax3(mx[u], __uint_as_float(sv[c + 2 * u]), __uint_as_float(sv[c + 2 * u + 1]));
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-        if (!kMasked || keep != 0) top = fmaxf(top, -FLT_MAX);  // keys were seen, whatever their scores
+        top *= a.scale_log2;
+        if (!kMasked || (keep0 | keep1) != 0) top = fmaxf(top, -FLT_MAX);  // keys were seen, whatever their scores
         float corr = 1.f;
         if (top > m_use + kTuRescale || (m_use == -INFINITY && top != -INFINITY)) {
           corr = fast_exp2(m_use - top);  // m_use = -inf: 0
           m_use = top;
         }
         const float m_sub = m_use == -INFINITY ? 0.f : m_use;
-        const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-m_sub, -m_sub);
-        uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        uint32_t p[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sc2, nm2), x0, x1);
-          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-          sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(e0, e1));
-          // weights are rounded to the pool's type for the product with V (half a step each); their sum
-          // keeps 32 bits
-          p[c] = pack2<kBf16>(e0, e1);
+#pragma unroll 1
+        for (int h = 0; h < kKeys / 64; ++h) {
+          if (kKeys == 128) tu_scores<kMasked>(srow + 64u * h, h ? keep1 : keep0, sv);
+          sum += tu_weights<kBf16>(srow + 32u * h, sv, a.scale_log2, m_sub);
         }
-        tmem_st32(srow, p);
-        float a0, a1, b0, b1;
-        f2_unpack(sum2[0], a0, a1);
-        f2_unpack(sum2[1], b0, b1);
-        l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
+        l_run = l_run * corr + sum;
         if (before >= 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          // O is stable once the product of the group's previous tile is done; this tile's waits for us
-          if (!__all_sync(0xffffffffu, mbar_wait(&vdone[before % kVStages], (unsigned)((before / kVStages) & 1),
-                                                           a.err, a.epoch))) {
+          // O is stable once the product of the group's previous tile is done (wide: it was issued before this
+          // tile's S and is); this tile's waits for us
+          if (!kWide && !__all_sync(0xffffffffu, mbar_wait(&vdone[before % kVStages],
+                                                           (unsigned)((before / kVStages) & 1), a.err, a.epoch))) {
             alive = false;
             return;
           }
@@ -565,36 +646,40 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         }
       };
 
-      const int step = kWide ? 1 : 2;
-      for (int i = kWide ? 0 : ((grp - t) & 1); i < n; i += step) {
-        const int ti = t + i, buf = ti % kBufs, before = i < step ? -1 : ti - step;
-        const int kb = (w.x0 + i) * kTreeKeys;
-        const bool edge = kb + kTreeKeys > hist;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sdone[ti % kKStages], (unsigned)((ti / kKStages) & 1), a.err, a.epoch))) {
+      const int step = pair ? 1 : 2;
+      for (int i = pair ? 0 : (kWide ? grp : ((grp - t) & 1)); i < n; i += step, ++item) {
+        const int ti = t + i, buf = kWide ? grp : ti % kBufs, before = i < step ? -1 : ti - step;
+        const int kb = (w.x0 + i) * kKeys;
+        uint64_t* scores = kWide ? &s_full[grp] : &sdone[ti % kKStages];
+        if (!__all_sync(0xffffffffu, mbar_wait(scores, (unsigned)((kWide ? item : ti / kKStages) & 1), a.err, a.epoch))) {
           alive = false;
           break;
         }
         tc_fence_after();
         const uint32_t loaded = kmask[ti & 31];
-        if (!edge && loaded == (1u << kTuSubs) - 1u) {
-          if (live) tile(std::false_type{}, buf, ~0ull, before);
+        if (kb + kKeys <= hist && loaded == (1u << kSubs) - 1u) {
+          if (live) tile(std::false_type{}, buf, ~0ull, ~0ull, before);
         } else {
-          if (live) tile(std::true_type{}, buf, visible(kb, loaded), before);
-          if (!kWide || grp == 0) {
+          if (live)
+            tile(std::true_type{}, buf, visible(kb, loaded & 15u), kKeys == 128 ? visible(kb + 64, loaded >> 4) : 0ull,
+                 before);
+          if (!pair || grp == 0) {
             // V of the tile: rows without a token zeroed, non-finite elements of drafted tokens taken out
+            // (pair: the other group's product is issued after this one's)
             if (!__all_sync(0xffffffffu, mbar_wait(&vfull[ti % kVStages], (unsigned)((ti / kVStages) & 1), a.err,
                                                    a.epoch))) {
               alive = false;
               break;
             }
             uint8_t* vst = vs + (ti % kVStages) * Cfg::kKvBytes;
-            for (int e = r; e < kTreeKeys * 8 * kHalves; e += 128) {
+            for (int e = r; e < kKeys * 8 * kHalves; e += 128) {
               const int key = e / (8 * kHalves), c = e % (8 * kHalves);
+              if (kb + key < hist && ((loaded >> (key >> 4)) & 1u)) continue;
               uint4* p = reinterpret_cast<uint4*>(vst + (key >> 3) * Cfg::kGroup + (c >> 3) * 1024 + (key & 7) * 128 +
-                                                   (((c & 7) ^ (key & 7)) << 4));
+                                                  (((c & 7) ^ (key & 7)) << 4));
               if (kb + key >= w.sq.n || !((loaded >> (key >> 4)) & 1u)) {
                 *p = make_uint4(0, 0, 0, 0);
-              } else if (kb + key >= hist) {
+              } else {
                 uint4 x = *p;
                 if (any_nonfinite<kBf16>(x.x) || any_nonfinite<kBf16>(x.y) || any_nonfinite<kBf16>(x.z) ||
                     any_nonfinite<kBf16>(x.w)) {
@@ -616,71 +701,76 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      // both Os: products complete in the order in which their one thread issued them
+      // both Os (narrow: products complete in the order in which their one thread issued them)
       const int end = t + n - 1;
+      uint64_t* complete = kWide ? o_full : &vdone[end % kVStages];
       if (alive)
-        alive = __all_sync(0xffffffffu, mbar_wait(&vdone[end % kVStages], (unsigned)((end / kVStages) & 1), a.err, a.epoch));
+        alive = __all_sync(0xffffffffu, mbar_wait(complete, (unsigned)((kWide ? un : end / kVStages) & 1), a.err, a.epoch));
       if (!alive) break;
       tc_fence_after();
 
       // ---- the unit's rows: the output, or this CTA's piece of it ----------------------------------
       const bool whole = w.x0 == 0 && w.x1 == w.T;
       const int64_t row0 = (w.sq.q0 + w.node0) * a.n_q_heads + ((int64_t)w.kvh << a.group_shift);
-      const int ur = kWide ? 128 * grp + r : r;  // row of the unit
+      const int ur = pair ? 128 * grp + r : r;  // row of the unit
       const int64_t qh = row0 + (int64_t)(ur >> a.group_shift) * a.n_q_heads + (ur & (a.group - 1));
       const int64_t piece = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * kUnitRows + ur;
-      float M = m_use, L = l_run, f0 = 1.f, f1 = 0.f;
-      bool has0 = true, has1 = false;
-      if (!kWide) {
-        ml[128 * grp + r] = make_float2(m_use, l_run);
+      // what this thread writes: columns [c_begin, c_end) of f0 O_0 + f1 O_1 (factors of absent Os unused)
+      bool use0 = grp == 0, use1 = grp == 1;
+      float M = m_use, L = l_run, f0 = 1.f, f1 = 1.f;
+      int c_begin = 0, c_end = D;
+      if (!pair) {
+        if (!kWide || grp == 1) ml[kWide ? r : 128 * grp + r] = make_float2(m_use, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full);
-        if (!__all_sync(0xffffffffu, mbar_wait(ml_full, (unsigned)(un & 1), a.err, a.epoch))) {
-          alive = false;
-          break;
+        if (kWide && grp == 1) {
+          c_end = 0;  // group 0 writes the unit
+        } else {
+          if (!__all_sync(0xffffffffu, mbar_wait(ml_full, (unsigned)(solo & 1), a.err, a.epoch))) {
+            alive = false;
+            break;
+          }
+          const int first = kWide ? 0 : t & 1;  // the group of the unit's first tile
+          use0 = n > 1 || first == 0;
+          use1 = n > 1 || first == 1;
+          const float2 s0 = kWide ? make_float2(m_use, l_run) : ml[r], s1 = ml[kWide ? r : 128 + r];
+          M = fmaxf(s0.x, s1.x);
+          const float M0 = M == -INFINITY ? 0.f : M;
+          f0 = fast_exp2(s0.x - M0);
+          f1 = fast_exp2(s1.x - M0);
+          L = fmaf(s0.y, f0, s1.y * f1);
+          if (!kWide) {
+            c_begin = grp * (D / 2);
+            c_end = c_begin + D / 2;
+          }
         }
-        has0 = n > 1 || (t & 1) == 0;
-        has1 = n > 1 || (t & 1) == 1;
-        const float2 s0 = ml[r], s1 = ml[128 + r];
-        M = fmaxf(s0.x, s1.x);
-        const float M0 = M == -INFINITY ? 0.f : M;
-        f0 = fast_exp2(s0.x - M0);
-        f1 = fast_exp2(s1.x - M0);
-        L = fmaf(s0.y, f0, s1.y * f1);
+        ++solo;
       }
       const bool none = M == -INFINITY;  // the row sees none of these keys
       const float norm = whole ? (none ? 0.f : 1.f / L) : 1.f;
-      constexpr int kCols = kWide ? D : D / 2;
-      const int col0 = kWide ? 0 : grp * kCols;
       if (live) {
 #pragma unroll 1
-        for (int c0 = col0; c0 < col0 + kCols; c0 += 32) {
+        for (int c0 = c_begin; c0 < c_end; c0 += 32) {
           float acc[32];
           uint32_t v[32];
-          if (kWide) {
-            tmem_ld32_sync(tO(grp) + lane_base + c0, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]);
-          } else {
+          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+          if (use0) {
+            tmem_ld32_sync(tO(0) + lane_base + c0, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-            if (has0) {
-              tmem_ld32_sync(tO(0) + lane_base + c0, v);
+            for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]) * f0;
+          }
+          if (use1) {
+            tmem_ld32_sync(tO(1) + lane_base + c0, v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]) * f0;
-            }
-            if (has1) {
-              tmem_ld32_sync(tO(1) + lane_base + c0, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(v[i]), f1, acc[i]);
-            }
+            for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(v[i]), f1, acc[i]);
           }
           if (r < rows) {
             if (*bad_v != 0) {
               // the non-finite elements that were taken out of V, for the rows that see them
               const int32_t* table = a.block_table + (int64_t)w.b * a.bt_stride;
-              const int end = min(w.x1 * kTreeKeys, w.sq.n);
-              for (int pos = max(w.x0 * kTreeKeys, hist); pos < end; ++pos) {
+              const int last = min(w.x1 * kKeys, w.sq.n);
+              for (int pos = max(w.x0 * kKeys, hist); pos < last; ++pos) {
                 const int s = pos - hist;
                 const bool see = words != nullptr ? ((__ldg(words + (s >> 6)) >> (s & 63)) & 1) != 0 : s <= node;
                 const int blk = __ldg(table + (pos >> a.block_shift));
@@ -717,7 +807,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
             }
           }
         }
-        if (!whole && r < rows && (kWide || grp == 0)) {
+        if (!whole && r < rows && (pair || grp == 0)) {
           a.ws_m[piece] = M;
           a.ws_l[piece] = none ? 0.f : L;
         }
