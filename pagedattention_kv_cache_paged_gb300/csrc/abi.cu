@@ -560,6 +560,16 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
   return finish(e, launches);
 }
 
+// Whether the tensor-core tree attention's line of key tiles (tree_common.cuh) has 32-bit positions for
+// contexts as long as the table allows.
+bool tree_line_fits(int batch, int max_nodes, int n_kv_heads, int group, int head_dim, int64_t bt_stride,
+                    int block_size) {
+  const int unit_rows = tree_unit_rows(max_nodes, group);
+  const int64_t units = ((int64_t)max_nodes * group + unit_rows - 1) / unit_rows * n_kv_heads;
+  const int64_t tiles = table_capacity(bt_stride, block_size) / tree_tile_keys(head_dim, unit_rows) + 1 + tree_gap(unit_rows);
+  return units < (int64_t(1) << 30) / tiles / (batch > 0 ? batch : 1);
+}
+
 // How a tree-attention call divides its work and what its partial states take (one plan for the launch
 // and for the size the caller asks for).
 struct TreePlan {
@@ -633,8 +643,9 @@ size_t tree_workspace_impl(int batch, int64_t total_q, int max_nodes, int64_t bl
   int sms = 0;
   if (device_info(nullptr, &sms)) return 0;
   if (max_nodes > total_q) max_nodes = (int)total_q;
-  const bool use_tc =
-      o.prefill_kernel != 1 && decode_tc_supported(dtype, block_size, head_dim, n_q_heads / n_kv_heads, 1);
+  const int group = n_q_heads / n_kv_heads;
+  const bool use_tc = o.prefill_kernel != 1 && decode_tc_supported(dtype, block_size, head_dim, group, 1) &&
+                      tree_line_fits(batch, max_nodes, n_kv_heads, group, head_dim, block_table_stride, block_size);
   return plan_tree(use_tc, batch, total_q, max_nodes, n_q_heads, n_kv_heads, head_dim, sms, block_table_stride,
                    block_size, o.partition_tokens)
       .bytes;
@@ -668,7 +679,8 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   int sms = 0;
   if ((rc = device_info(&err, &sms))) return rc;
   const int group = n_q_heads / n_kv_heads;
-  const bool tc_ok = decode_tc_supported(dtype, block_size, head_dim, group, num_blocks);
+  const bool tc_ok = decode_tc_supported(dtype, block_size, head_dim, group, num_blocks) &&
+                     tree_line_fits(batch, max_nodes, n_kv_heads, group, head_dim, block_table_stride, block_size);
   if (o.prefill_kernel == 2 && !tc_ok) return PA_EUNSUPPORTED;
   const bool use_tc = o.prefill_kernel == 2 || (o.prefill_kernel == 0 && tc_ok);
   TreePlan plan = plan_tree(use_tc, batch, total_q, max_nodes, n_q_heads, n_kv_heads, head_dim, sms,

@@ -31,6 +31,24 @@ __device__ __forceinline__ int ld_nc_s32(const int32_t* p) {
   return v;
 }
 
+__device__ __forceinline__ int64_t ld_nc_s64(const int64_t* p) {
+  int64_t v;
+  asm volatile("ld.global.nc.s64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
+}
+
+// 32 bytes to global memory: one store when the address is a multiple of 32, else two of 16 bytes.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&x)[8], bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // 2^x with the hardware approximation (ex2.approx; -inf -> +0).
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;

@@ -133,32 +133,33 @@ __device__ __forceinline__ float tu_weights(uint32_t taddr, const uint32_t (&sv)
   return (a0 + a1) + (b0 + b1);
 }
 
-// The span of this CTA (all threads; sm: one word per warp twice, carry and result).
+// Where a CTA's span of the line begins and ends.
 struct TuSched {
-  int64_t sums[kTuThreads / 32];
-  int64_t tops[kTuThreads / 32];
-  int64_t carry;
+  alignas(16) int32_t sums[kTuThreads / 32];
+  alignas(16) int32_t tops[kTuThreads / 32];
+  int32_t share;
+  int32_t cut_start;  // where the unit that the span ends in begins on the line
+  int32_t snap;
   TreeSpan span;
-  int64_t share;
-  int64_t cut_start;  // where the unit that the span ends in begins on the line
-  int snap;
-  int refused;  // a sequence of the batch is refused, and its rows are this CTA's to zero
+  int32_t refused;    // a sequence of the batch is refused, and its rows are this CTA's to zero
 };
 
+__device__ __forceinline__ void tu_schedule_init(const TreeArgs& a, TuSched& sm) {
+  sm.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
+  sm.refused = 0;
+}
+
+// All threads; sm initialised, and a barrier since.  The caller's next barrier publishes the result.  One
+// thread looks after one sequence at a time; positions on the line fit 32 bits (the host sees to it).
 template <int kKeys, int kUnitRows>
 __device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, TuSched& sm) {
-  constexpr int kGap = tree_gap(kUnitRows), kMinShare = tree_min_share(kUnitRows), kSnap = kGap - 1;
   constexpr int kWarps = kTuThreads / 32;
+  constexpr int kGap = tree_gap(kUnitRows), kMinShare = tree_min_share(kUnitRows), kSnap = kGap - 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gap = a.share > 0 ? 0 : kGap;
-  if (threadIdx.x == 0) {
-    sm.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
-    sm.carry = 0;
-    sm.refused = 0;
-  }
-  int tiles = 0, units = 0;
-  auto look = [&](int b) -> int64_t {  // this thread's sequence: its length on the line
-    tiles = units = 0;
+  int tiles = 0;
+  auto look = [&](int b) -> int {  // this thread's sequence: its length on the line
+    tiles = 0;
     if (b >= a.batch) return 0;
     const TreeSeq s = tree_seq(a, b);
     if (s.bad) {
@@ -167,39 +168,46 @@ __device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, T
     }
     if (s.n == 0 || s.m == 0) return 0;
     tiles = (s.n + kKeys - 1) / kKeys;
-    units = (s.m + nodes_unit - 1) / nodes_unit * a.n_kv_heads;
-    return (int64_t)units * (tiles + gap);
+    return (s.m + nodes_unit - 1) / nodes_unit * a.n_kv_heads * (tiles + gap);
   };
-  __syncthreads();
-  // the whole line and its longest unit
-  int64_t mine = 0, total = 0, longest = 0;
-  for (int b = threadIdx.x; b < a.batch; b += kTuThreads) {
-    const int64_t c = look(b);
-    total += c;
-    longest = max(longest, (int64_t)(c > 0 ? tiles + gap : 0));
-    mine = c;
+  const bool one_chunk = a.batch <= kTuThreads;
+  int c = look(threadIdx.x);
+  int total = c, longest = c > 0 ? tiles + gap : 0;
+  for (int b = threadIdx.x + kTuThreads; b < a.batch; b += kTuThreads) {
+    const int more = look(b);
+    total += more;
+    longest = max(longest, more > 0 ? tiles + gap : 0);
   }
+  auto scan = [&](int x) {  // inclusive, over the warp
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, off);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
-  }
-  if (lane == 0) {
-    sm.sums[warp] = total;
-    sm.tops[warp] = longest;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += u;
+    }
+    return x;
+  };
+  int v = one_chunk ? scan(c) : 0;
+  const int warp_total = one_chunk ? v : __reduce_add_sync(0xffffffffu, total);  // (in lane 31)
+  const int warp_top = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    sm.sums[warp] = warp_total;
+    sm.tops[warp] = warp_top;
   }
   __syncthreads();
+  int pre = 0;
   total = longest = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    total += sm.sums[w];
+    const int x = sm.sums[w];
+    if (w < warp) pre += x;
+    total += x;
     longest = max(longest, sm.tops[w]);
   }
-  int64_t share = a.share;
+  int share = a.share;
   if (share <= 0) {
-    // fewer CTAs than that would wait longer for their first keys than they save
-    share = (total + gridDim.x - 1) / gridDim.x;
-    share = max(share, min(longest, (int64_t)kMinShare));
+    // fewer tiles than kMinShare would wait longer for their first keys than they save
+    share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+    share = max(share, min(longest, kMinShare));
   }
   // contexts that are never cut: every border moves to the nearest unit's
   const int snap = !a.split || longest <= (a.share > 0 ? 0 : kMinShare) ? INT32_MAX : (a.share > 0 ? 1 : kSnap);
@@ -208,43 +216,44 @@ __device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, T
     sm.share = share;
     sm.snap = snap;
   }
-  const bool one_chunk = a.batch <= kTuThreads;
-  __syncthreads();
-  for (int b0 = 0; b0 < a.batch; b0 += kTuThreads) {
-    const int b = b0 + threadIdx.x;
-    const int64_t c = one_chunk ? mine : look(b);
-    int64_t v = c;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, v, off);
-      if (lane >= off) v += t;
+  // this thread's sequence b lies at [first, first + c) of the line
+  auto place = [&](int b, int64_t first) {
+    const unsigned len = (unsigned)(tiles + gap);
+    if (c > 0 && lo >= first && lo < first + c) {
+      const unsigned off = (unsigned)(lo - first), u = off / len;
+      sm.span.b0 = b;
+      sm.span.u0 = (int)u;
+      sm.span.x0 = tree_cut(off - u * len, tiles, snap);
+      // the producers' first table entries
+      const int pos = min(sm.span.x0, tiles - 1) * kKeys;
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.block_table + (int64_t)b * a.bt_stride + (pos >> a.block_shift)));
     }
+    if (c > 0 && hi >= first && hi < first + c) {
+      const unsigned off = (unsigned)(hi - first), u = off / len;
+      sm.span.b1 = b;
+      sm.span.u1 = (int)u;
+      sm.span.x1 = tree_cut(off - u * len, tiles, snap);
+      sm.cut_start = (int)(hi - (off - u * len));
+    }
+  };
+  if (one_chunk) {
+    place(threadIdx.x, (int64_t)pre + v - c);
+    return;
+  }
+  int carry = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kTuThreads) {
+    c = look(b0 + threadIdx.x);
+    v = scan(c);
+    __syncthreads();  // the sums before have been read
     if (lane == 31) sm.sums[warp] = v;
     __syncthreads();
-    int64_t pre = sm.carry, chunk = 0;
+    pre = carry;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) pre += sm.sums[w];
-      chunk += sm.sums[w];
+      carry += sm.sums[w];
     }
-    pre += v - c;
-    const int64_t len = tiles + gap;
-    if (c > 0 && lo >= pre && lo < pre + c) {
-      const int64_t off = lo - pre;
-      sm.span.b0 = b;
-      sm.span.u0 = (int)(off / len);
-      sm.span.x0 = tree_cut(off % len, tiles, snap);
-    }
-    if (c > 0 && hi >= pre && hi < pre + c) {
-      const int64_t off = hi - pre;
-      sm.span.b1 = b;
-      sm.span.u1 = (int)(off / len);
-      sm.span.x1 = tree_cut(off % len, tiles, snap);
-      sm.cut_start = hi - off % len;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) sm.carry += chunk;
-    __syncthreads();
+    place(b0 + threadIdx.x, (int64_t)pre + v - c);
   }
 }
 
@@ -317,9 +326,11 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     mbar_init(&s_full[1], 1);
     mbar_init(o_full, 1);
     *bad_v = 0;
+    tu_schedule_init(a, *sched);
     fence_barrier_init();
   }
   if (warp == 10) tmem_alloc(tmem_slot, 512);
+  __syncthreads();
   // nothing of global memory is read or written before the preceding grid is over
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -557,6 +568,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     const int grp = warp >> 2;
     const int r = threadIdx.x & 127;  // row of the group's tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    // rows are 16-byte aligned at least; whole 32-byte sectors per thread halve the store traffic
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.ws_acc)) & 31u) == 0;
     int t = 0, un = 0, item = 0, solo = 0;  // tiles of earlier units, those, this group's items, joined units
     bool alive = true, cut = false;
     Walk walk(a, span, nodes_unit);
@@ -569,6 +582,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       const bool live = (r & ~31) < rows;                             // whole warps
       const int node = w.node0 + (pair ? grp * (128 >> a.group_shift) : 0) + (min(r, rows - 1) >> a.group_shift);
       const int64_t* words = a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
+      // (read before it is needed: most trees have one mask word, and no tile reaches it before the first)
+      const uint64_t word0 = words != nullptr && live ? (uint64_t)ld_nc_s64(words) : 0ull;
       float m_use = -INFINITY, l_run = 0.f;
 
       // Bits of the 64 keys from kb on that this row sees (bit c: key kb + c); `loaded`: their sub-tiles
@@ -584,10 +599,10 @@ __global__ void __launch_bounds__(kTuThreads, 1)
           const int c = node + 1 - s0;  // chain: nodes up to its own
           keep = c <= 0 ? 0ull : (c >= 64 ? ~0ull : (1ull << c) - 1ull);
         } else if (s0 < 0) {
-          keep = ((uint64_t)__ldg(words) << -s0) | ((1ull << -s0) - 1ull);
+          keep = (word0 << -s0) | ((1ull << -s0) - 1ull);
         } else {
           const int i = s0 >> 6, sh = s0 & 63;
-          keep = (i < a.mask_words ? (uint64_t)__ldg(words + i) : 0ull) >> sh;
+          keep = (i == 0 ? word0 : (i < a.mask_words ? (uint64_t)__ldg(words + i) : 0ull)) >> sh;
           if (sh != 0 && i + 1 < a.mask_words) keep |= (uint64_t)__ldg(words + i + 1) << (64 - sh);
         }
         if (nv < 64) keep &= (1ull << nv) - 1ull;
@@ -609,7 +624,10 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int h = kKeys / 64 - 1; h >= 0; --h) {
-          tu_scores<kMasked>(srow + 64u * h, h ? keep1 : keep0, sv);
+          const uint64_t keep = h ? keep1 : keep0;
+          // a block that no row of the warp sees is neither read nor exponentiated
+          if (kMasked && kKeys == 128 && __all_sync(0xffffffffu, keep == 0ull)) continue;
+          tu_scores<kMasked>(srow + 64u * h, keep, sv);
           top = fmaxf(top, tu_max(sv));
         }
         top *= a.scale_log2;
@@ -622,7 +640,15 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         const float m_sub = m_use == -INFINITY ? 0.f : m_use;
 #pragma unroll 1
         for (int h = 0; h < kKeys / 64; ++h) {
-          if (kKeys == 128) tu_scores<kMasked>(srow + 64u * h, h ? keep1 : keep0, sv);
+          const uint64_t keep = h ? keep1 : keep0;
+          if (kMasked && kKeys == 128 && __all_sync(0xffffffffu, keep == 0ull)) {
+            uint32_t z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0u;
+            tmem_st32(srow + 32u * h, z);
+            continue;
+          }
+          if (kKeys == 128) tu_scores<kMasked>(srow + 64u * h, keep, sv);
           sum += tu_weights<kBf16>(srow + 32u * h, sv, a.scale_log2, m_sub);
         }
         l_run = l_run * corr + sum;
@@ -671,15 +697,18 @@ __global__ void __launch_bounds__(kTuThreads, 1)
               alive = false;
               break;
             }
-            uint8_t* vst = vs + (ti % kVStages) * Cfg::kKvBytes;
-            for (int e = r; e < kKeys * 8 * kHalves; e += 128) {
-              const int key = e / (8 * kHalves), c = e % (8 * kHalves);
-              if (kb + key < hist && ((loaded >> (key >> 4)) & 1u)) continue;
-              uint4* p = reinterpret_cast<uint4*>(vst + (key >> 3) * Cfg::kGroup + (c >> 3) * 1024 + (key & 7) * 128 +
-                                                  (((c & 7) ^ (key & 7)) << 4));
+            // one thread: one 16-byte column of every 8th (16th) key
+            uint8_t* col = vs + (ti % kVStages) * Cfg::kKvBytes;
+            const int c = r % (8 * kHalves), key0 = r / (8 * kHalves);
+            constexpr int kStep = 128 / (8 * kHalves);  // 8 or 16: the swizzle stays the same
+            col += (c >> 3) * 1024 + (key0 & 7) * 128 + (((c & 7) ^ (key0 & 7)) << 4);
+            const bool all = loaded == (1u << kSubs) - 1u;
+            // (keys of the history that are loaded stay as they are)
+            for (int key = key0 + (all ? max(0, hist - kb) / kStep * kStep : 0); key < kKeys; key += kStep) {
+              uint4* p = reinterpret_cast<uint4*>(col + (key >> 3) * Cfg::kGroup);
               if (kb + key >= w.sq.n || !((loaded >> (key >> 4)) & 1u)) {
                 *p = make_uint4(0, 0, 0, 0);
-              } else {
+              } else if (kb + key >= hist) {
                 uint4 x = *p;
                 if (any_nonfinite<kBf16>(x.x) || any_nonfinite<kBf16>(x.y) || any_nonfinite<kBf16>(x.z) ||
                     any_nonfinite<kBf16>(x.w)) {
@@ -787,23 +816,22 @@ __global__ void __launch_bounds__(kTuThreads, 1)
             if (whole) {
               T* o = static_cast<T*>(a.out) + qh * D + c0;
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                float f[8];
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = none ? 0.f : acc[i + e] * norm;
-                uint4 x;
-                x.x = pack2<kBf16>(f[0], f[1]);
-                x.y = pack2<kBf16>(f[2], f[3]);
-                x.z = pack2<kBf16>(f[4], f[5]);
-                x.w = pack2<kBf16>(f[6], f[7]);
-                *reinterpret_cast<uint4*>(o + i) = x;
+                for (int e = 0; e < 8; ++e)
+                  x[e] = none ? 0u : pack2<kBf16>(acc[i + 2 * e] * norm, acc[i + 2 * e + 1] * norm);
+                st_global32(o + i, x, aligned);
               }
             } else {
               float* o = a.ws_acc + piece * D + c0;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(o + i) = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                         : make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = none ? 0u : __float_as_uint(acc[i + e]);
+                st_global32(o + i, x, aligned);
+              }
             }
           }
         }
@@ -820,10 +848,10 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         cut = true;  // at most one unit of a CTA: the one that its span ends in
         if (threadIdx.x == 0) {
           // the CTA that the unit's last tile went to
-          const int64_t at = sched->cut_start, share = sched->share;
-          int64_t last = (at + w.T - 1) / share;
-          if (tree_cut(last * share - at, w.T, sched->snap) == w.T) --last;
-          a.ws_rec[blockIdx.x] = TreeRec{row0, w.rows, (int32_t)last};
+          const int at = sched->cut_start, share = sched->share;
+          int last = (at + w.T - 1) / share;
+          if (tree_cut((int64_t)last * share - at, w.T, sched->snap) == w.T) --last;
+          a.ws_rec[blockIdx.x] = TreeRec{row0, w.rows, last};
         }
       }
       t += n;
