@@ -17,17 +17,17 @@
 //     tile, so four warps share them (K, V, S, P V), each product's one commit telling the softmax, the
 //     producer and the other issuer alike.
 //   Wide kernel: bound by the softmax and the tensor core.  A unit of more than 128 rows has two Q tiles,
-//     one per group, that share every 128-key K and V tile; one thread issues S_0(j), P_1(j-1) V, S_1(j),
-//     P_0(j) V, .., so that products in issue order need no barrier between a P V and the S that overwrites
-//     its P.  A unit of at most 128 rows goes through the same sequence with the groups on tiles in turn.
+//     one per group, that share every 128-key K and V tile; each group has one S buffer, and while one
+//     computes its softmax the tensor core has the other's products.  (A barrier that is complete already
+//     costs its waiter 110-230 cycles, a commit 100: one thread issuing both products took 4,600 cycles a
+//     tile without ever having to wait.)  In a unit of at most 128 rows the groups take tiles in turn.
 //
 // Masks.  Only tiles that reach into the drafted region look at masks: a row's visibility bits are cut
 // out of its mask words.  A masked score becomes -inf by selection, whatever it was.  A masked value cannot
 // be deselected (0 * NaN), so in those tiles non-finite elements of V are zeroed in shared memory before
 // the product, and added at the end, by themselves, to the rows that see them.
 //
-// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 Q and S (wide: both products), 11 P V (wide: Q).
-// Every wait is bounded (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each
+// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 Q and S, 11 P V.  Every wait is bounded (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each
 // barrier below is waited for before its next phase but one can complete.
 #include <cudaTypedefs.h>
 #include <float.h>
@@ -281,13 +281,12 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   uint64_t* q_full = bars + 52;    // one phase per unit
   uint64_t* o_free = bars + 53;    // one phase per unit: both Os read
   uint64_t* ml_full = bars + 54;   // one phase per unit whose groups are joined: statistics written
-  uint64_t* q_empty = bars + 55;   // wide: one phase per unit: its S products are done (sdone would not do: the
-                                   // Q producer may be more than one phase ahead of it)
-  uint64_t* fin = bars + 56;       // [2] all products of an issuer are over
-  uint64_t* s_full = bars + 58;    // [2] wide: the group's scores are written, one phase per item
+  uint64_t* fin = bars + 55;       // [2] all products of an issuer are over
+  uint64_t* s_full = bars + 61;    // [2] wide: the group's scores are written, one phase per item
+  uint64_t* pv_done = bars + 57;   // [2] wide: O += P V of the group's item done, one phase per item
   uint64_t* o_full = bars + 60;    // wide: one phase per unit: both Os complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 496);
-  volatile int* bad_v = reinterpret_cast<int*>(base + 500);  // V of a drafted region held non-finite elements
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 504);
+  volatile int* bad_v = reinterpret_cast<int*>(base + 508);  // V of a drafted region held non-finite elements
   volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 512);  // [32] 16-key sub-tiles loaded, per tile
   TuSched* sched = reinterpret_cast<TuSched*>(base + 640);
   // (maximum, sum) per row: narrow [2][128], of both groups; wide [128], of group 1
@@ -317,13 +316,14 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     }
     for (int k = 0; k < kBufs; ++k) mbar_init(&p_full[k], 4);
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     mbar_init(o_free, 8);
     mbar_init(ml_full, 8);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
+    mbar_init(&pv_done[0], 1);
+    mbar_init(&pv_done[1], 1);
     mbar_init(o_full, 1);
     *bad_v = 0;
     tu_schedule_init(a, *sched);
@@ -425,27 +425,9 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       for (int k = t > depth ? t - depth : 0; k < t; ++k) mbar_wait(&full[k % depth], (unsigned)((k / depth) & 1));
     }
     __syncwarp();
-  } else if (kWide && warp == 11) {
-    // --------------------------------------- Q producer ------------------------------------------
-    if (lane == 0) {
-      int un = 0;
-      bool alive = true;
-      Walk walk(a, span, nodes_unit);
-      TreeUnit w;
-      for (; walk.next(w); ++un) {
-        if (un > 0 && !mbar_wait(q_empty, (unsigned)((un - 1) & 1), a.err, a.epoch)) {
-          alive = false;
-          break;
-        }
-        load_q(w);
-      }
-      if (!alive) raise_timeout(a.err, a.epoch);
-      if (un > 0) mbar_wait(q_full, (unsigned)((un - 1) & 1));  // no copy in flight
-    }
-    __syncwarp();
   } else if (warp == 10 || warp == 11) {
-    // ------------------- products: narrow: warp 10 Q and S, warp 11 P V; wide: warp 10 ---------------
-    if (lane == 0 && (!kWide || warp == 10)) {
+    // ------------------------- products: warp 10 Q and S, warp 11 P V ------------------------------
+    if (lane == 0) {
       const uint32_t id_s = umma_idesc_f16(kBf16, 128, kKeys, false, false);
       const uint32_t id_pv = umma_idesc_f16(kBf16, 128, D, false, true);
       const uint64_t qd = umma_desc_sw128(smem_u32(qs), 16, 1024), kd = umma_desc_sw128(smem_u32(ks), 16, Cfg::kGroup);
@@ -471,53 +453,9 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       Walk walk(a, span, nodes_unit);
       TreeUnit w;
       int un = 0;
-      if constexpr (kWide) {
-        int ks_ = 0, kr = 0, vs_ = 0, vr = 0;  // ring stages and rounds
-        int done[2] = {0, 0};                  // items of each group so far
-        while (ok && walk.next(w)) {
-          const bool pair = w.rows > 128;
-          const int items = (w.x1 - w.x0) << (pair ? 1 : 0);
-          if (!wait(q_full, un)) break;
-          // item k: group k % 2; S of item k overwrites P of item k - 2, whose P V was issued before it
-          for (int k = 0; k <= items; ++k) {
-            if (k < items) {
-              const int g = k & 1;
-              if ((!pair || g == 0) && !wait(&kfull[ks_], kr)) break;
-              tc_fence_after();
-              s_product(g, pair ? g : 0, ks_);
-              umma_commit(&s_full[g]);
-              if (!pair || g == 1) {
-                umma_commit(&sdone[ks_]);
-                if (++ks_ == kKStages) {
-                  ks_ = 0;
-                  ++kr;
-                }
-              }
-              if (k == items - 1) umma_commit(q_empty);
-            }
-            if (k > 0) {
-              const int j = k - 1, g = j & 1;
-              if ((!pair || g == 0) && !wait(&vfull[vs_], vr)) break;
-              // the unit's first product overwrites the Os that the unit before it left
-              if (j == 0 && un > 0 && !wait(o_free, un - 1)) break;
-              if (!wait(&p_full[g], done[g])) break;
-              ++done[g];
-              tc_fence_after();
-              pv_product(g, g, vs_, j < 2);
-              if (!pair || g == 1) {
-                umma_commit(&vdone[vs_]);
-                if (++vs_ == kVStages) {
-                  vs_ = 0;
-                  ++vr;
-                }
-              }
-              if (j == items - 1) umma_commit(o_full);
-            }
-          }
-          ++un;
-        }
-      } else if (warp == 10) {
-        int t = 0, s = 0, round = 0;
+      int t = 0, s = 0, round = 0;  // tiles so far, ring stage and round
+      int done0 = 0, done1 = 0;     // wide: items of each group so far
+      if (warp == 10) {
         while (ok && walk.next(w)) {
           // Q is free once the S products of the unit before are done
           if (t > 0 && !wait(&sdone[(t - 1) % kKStages], (t - 1) / kKStages)) break;
@@ -526,12 +464,21 @@ __global__ void __launch_bounds__(kTuThreads, 1)
             mbar_wait(q_full, (unsigned)(un & 1));  // no copy in flight
             break;
           }
-          for (int x = w.x0; x < w.x1; ++x, ++t) {
-            // the buffer still holds the weights of tile t - kBufs until their product is done
-            if (t >= kBufs && !wait(&vdone[(t - kBufs) % kVStages], (t - kBufs) / kVStages)) break;
+          const bool pair = kWide && w.rows > 128;
+          for (int x = w.x0; x < w.x1 && ok; ++x, ++t) {
+            // an S overwrites weights: of the tile kBufs before (narrow), of the group's item before (wide)
+            if (!kWide && t >= kBufs && !wait(&vdone[(t - kBufs) % kVStages], (t - kBufs) / kVStages)) break;
             if (!wait(&kfull[s], round)) break;
-            tc_fence_after();
-            s_product(t % kBufs, 0, s);
+            for (int g = kWide && !pair ? (x - w.x0) & 1 : 0, last = pair ? 1 : g; g <= last; ++g) {
+              if (kWide) {
+                const int done = g ? done1++ : done0++;
+                if (done > 0 && !wait(&pv_done[g], done - 1)) break;
+              }
+              tc_fence_after();
+              s_product(kWide ? g : t % kBufs, pair ? g : 0, s);
+              if (kWide) umma_commit(&s_full[g]);
+            }
+            if (!ok) break;
             umma_commit(&sdone[s]);
             if (++s == kKStages) {
               s = 0;
@@ -541,20 +488,28 @@ __global__ void __launch_bounds__(kTuThreads, 1)
           ++un;
         }
       } else {
-        int t = 0, s = 0, round = 0;
         while (ok && walk.next(w)) {
+          const bool pair = kWide && w.rows > 128;
           // the unit's first products overwrite the Os that the unit before it left
           if (un > 0 && !wait(o_free, un - 1)) break;
-          for (int x = w.x0; x < w.x1; ++x, ++t) {
-            if (!wait(&vfull[s], round) || !wait(&p_full[t % kBufs], t / kBufs)) break;
-            tc_fence_after();
-            pv_product(t & 1, t % kBufs, s, x < w.x0 + 2);
+          for (int x = w.x0; x < w.x1 && ok; ++x, ++t) {
+            const int i = x - w.x0;
+            if (!wait(&vfull[s], round)) break;
+            for (int g = kWide ? (pair ? 0 : i & 1) : t & 1, last = pair ? 1 : g; g <= last; ++g) {
+              const int phase = kWide ? (g ? done1++ : done0++) : t / kBufs;
+              if (!wait(&p_full[kWide ? g : t % kBufs], phase)) break;
+              tc_fence_after();
+              pv_product(g, kWide ? g : t % kBufs, s, pair ? i == 0 : i < 2);
+              if (kWide) umma_commit(&pv_done[g]);
+            }
+            if (!ok) break;
             umma_commit(&vdone[s]);
             if (++s == kVStages) {
               s = 0;
               ++round;
             }
           }
+          if (kWide && ok) umma_commit(o_full);
           ++un;
         }
       }
@@ -653,8 +608,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         }
         l_run = l_run * corr + sum;
         if (before >= 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          // O is stable once the product of the group's previous tile is done (wide: it was issued before this
-          // tile's S and is); this tile's waits for us
+          // O is stable once the product of the group's previous tile is done (wide: this tile's S waited for
+          // it); this tile's waits for us
           if (!kWide && !__all_sync(0xffffffffu, mbar_wait(&vdone[before % kVStages],
                                                            (unsigned)((before / kVStages) & 1), a.err, a.epoch))) {
             alive = false;
