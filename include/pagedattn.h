@@ -291,7 +291,8 @@ PA_API int paged_attention_prefill_ex(void* out, const void* q, const int32_t* q
  * (PA_DEVERR_BLOCK_ID), a tree of more than 64 * mask_words nodes (PA_DEVERR_TREE), or a need that
  * the free blocks left by the sequences before it do not cover (PA_DEVERR_NO_BLOCKS; once one
  * sequence finds too few, no later one takes any).  Checked mode returns PA_ERANGE for each of these.
- * batch == 0 is a no-op.  Index arrays need the alignment of their type only.
+ * batch == 0 is a no-op.  Index arrays need the alignment of their type only.  What is written must not
+ * overlap what is read (context_lens == history_lens returns PA_EINVAL), but for the arrays updated in place.
  */
 PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_lens, int batch, int32_t* block_table,
                               int64_t block_table_stride, int64_t max_blocks, int32_t* block_counts,

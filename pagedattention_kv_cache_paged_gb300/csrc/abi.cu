@@ -524,6 +524,7 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
     return PA_EINVAL;
   if (free_capacity > 0 && !free_blocks) return PA_EINVAL;
   if (token_capacity > 0 && (!slot_mapping || !positions)) return PA_EINVAL;
+  if (context_lens == history_lens || context_lens == new_lens) return PA_EINVAL;  // read while it is written
   if (parents && (mask_words < 1 || mask_words > (INT32_MAX >> 6) || (token_capacity > 0 && !tree_mask)))
     return PA_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

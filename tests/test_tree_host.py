@@ -59,7 +59,7 @@ def test_tree_workspace_of_bad_sizes_is_zero(lib):
     assert lib.paged_attention_tree_workspace_size(*good[:8], 9, None) == 0
 
 
-TABLES = dict(hist=P, new=P, batch=2, table=P, stride=8, cap=8, counts=P, free=P, free_n=16, state=P, blocks=16, bs=16,
+TABLES = dict(hist=P + 64, new=P + 128, batch=2, table=P, stride=8, cap=8, counts=P, free=P, free_n=16, state=P, blocks=16, bs=16,
               parents=None, qsl=P, ctx=P, slots=P, pos=P, tokens=8, mask=None, words=0, stream=None)
 
 
@@ -70,7 +70,7 @@ TABLES = dict(hist=P, new=P, batch=2, table=P, stride=8, cap=8, counts=P, free=P
     (dict(table=None), "EINVAL"), (dict(counts=None), "EINVAL"), (dict(free=None), "EINVAL"), (dict(state=None), "EINVAL"),
     (dict(qsl=None), "EINVAL"), (dict(ctx=None), "EINVAL"), (dict(slots=None), "EINVAL"), (dict(pos=None), "EINVAL"),
     (dict(parents=P), "EINVAL"), (dict(parents=P, words=1), "EINVAL"), (dict(parents=P, mask=P), "EINVAL"),
-    (dict(batch=0), "OK"),
+    (dict(ctx=P + 64), "EINVAL"), (dict(ctx=P + 128), "EINVAL"), (dict(batch=0), "OK"),
 ])
 def test_tables_refusals(lib, change, status):
     assert call(lib, "build_block_tables", list(TABLES), TABLES, **change) == getattr(pa, "PA_" + status)
