@@ -561,77 +561,64 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
   return finish(e, launches);
 }
 
-// Whether the tensor-core tree attention's line of key tiles (tree_common.cuh) has 32-bit positions for
-// contexts as long as the table allows.
-bool tree_line_fits(int batch, int max_nodes, int n_kv_heads, int group, int head_dim, int64_t bt_stride,
-                    int block_size) {
-  const int unit_rows = tree_unit_rows(max_nodes, group);
-  const int64_t units = ((int64_t)max_nodes * group + unit_rows - 1) / unit_rows * n_kv_heads;
-  const int64_t tiles = table_capacity(bt_stride, block_size) / tree_tile_keys(head_dim, unit_rows) + 1 + tree_gap(unit_rows);
-  return units < (int64_t(1) << 30) / tiles / (batch > 0 ? batch : 1);
-}
-
 // How a tree-attention call divides its work and what its partial states take (one plan for the launch
 // and for the size the caller asks for).
 struct TreePlan {
-  int part_tokens = 0, max_parts = 1;  // CUDA cores
-  int ctas = 0, share = 0;             // tcgen05
+  bool tensor_cores = false;
+  bool fits = false;  // positions on the line of key tiles (tree_common.cuh) fit 32 bits
+  int unit_rows = 0, ctas = 0, share = 0;
   size_t bytes = 0, off_m = 0, off_l = 0, off_rec = 0;
 };
 
-TreePlan plan_tree(bool tensor_cores, int batch, int64_t total_q, int max_nodes, int n_q_heads, int n_kv_heads,
-                   int head_dim, int sms, int64_t bt_stride, int block_size, int64_t partition_tokens) {
+TreePlan plan_tree(bool tensor_cores, int batch, int max_nodes, int n_q_heads, int n_kv_heads, int head_dim, int sms,
+                   int64_t bt_stride, int block_size, int64_t partition_tokens) {
   TreePlan p;
+  p.tensor_cores = tensor_cores;
   const int group = n_q_heads / n_kv_heads;
+  p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_simt_rows(max_nodes, group);
+  const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : tree_simt_keys(head_dim);
+  const int gap = tensor_cores ? tree_gap(p.unit_rows) : kTreeSimtGap;
+  const int min_share = tensor_cores ? tree_min_share(p.unit_rows) : kTreeSimtMinShare;
+  const int nodes_unit = p.unit_rows / group;
   const int64_t max_len = table_capacity(bt_stride, block_size);
-  auto up16 = [](size_t x) { return (x + 15) & ~size_t(15); };
-  if (sms < 1) sms = 1;
-  if (tensor_cores) {
-    // one CTA per SM, each with an equal share; an explicit partition length sets the share instead
-    const int unit_rows = tree_unit_rows(max_nodes, group);
-    const int64_t units = (int64_t)batch * n_kv_heads * (((int64_t)max_nodes * group + unit_rows - 1) / unit_rows);
-    const int keys = tree_tile_keys(head_dim, unit_rows);
-    const int64_t tiles = (max_len + keys - 1) / keys;
-    bool split = tiles > tree_min_share(unit_rows) - tree_gap(unit_rows);
-    int64_t ctas = units < sms ? units * (tiles < sms ? tiles : sms) : sms;
-    ctas = ctas < sms ? ctas : sms;
-    if (partition_tokens > 0) {
-      p.share = (int)((partition_tokens + keys - 1) / keys);
-      ctas = (units * tiles + p.share - 1) / p.share;
-      split = tiles > 1;
-    }
-    p.ctas = (int)(ctas < 65535 ? ctas : 65535);  // (grid.y of the join)
-    if (partition_tokens > 0 && ctas > 65535) p.share = (int)((units * tiles + 65534) / 65535);
-    if (split) {
-      const size_t rows = (size_t)p.ctas * 2 * (size_t)unit_rows;
-      p.off_m = rows * (size_t)head_dim * sizeof(float);
-      p.off_l = p.off_m + up16(rows * sizeof(float));
-      p.off_rec = p.off_l + up16(rows * sizeof(float));
-      p.bytes = p.off_rec + up16((size_t)p.ctas * sizeof(TreeRec));
-    }
-    return p;
+  const int64_t tiles = (max_len + keys - 1) / keys;
+  int64_t units = ((int64_t)max_nodes + nodes_unit - 1) / nodes_unit * n_kv_heads;
+  p.fits = units < (int64_t(1) << 30) / (tiles + gap) / (batch > 0 ? batch : 1);
+  if (!p.fits) return p;
+  units *= batch;
+  // tcgen05: one CTA per SM, else two, with an equal share each; an explicit partition length sets the share
+  const int64_t most = (int64_t)(sms > 0 ? sms : 1) * (tensor_cores ? 1 : 2);
+  int64_t ctas = units * tiles < most ? units * tiles : most;
+  bool split = tiles > min_share - gap;  // (shorter contexts are never cut, see tree_schedule)
+  if (partition_tokens > 0) {
+    int64_t share = (partition_tokens + keys - 1) / keys;
+    if ((units * tiles + share - 1) / share > 65535) share = (units * tiles + 65534) / 65535;  // (grid of the join)
+    p.share = (int)share;
+    ctas = (units * tiles + share - 1) / share;
+    split = tiles > 1;
   }
-  // partitions of 256 to 1024 tokens, as many as give every SM two CTAs when all rows are as long as
-  // their table allows
-  int64_t part = partition_tokens;
-  if (part <= 0) {
-    const int64_t rows = (int64_t)batch * n_kv_heads * max_nodes;
-    const int64_t parts = 2 * sms / rows > 1 ? 2 * sms / rows : 1;
-    part = (max_len + parts - 1) / parts;
-    part = part < 256 ? 256 : (part > 1024 ? 1024 : part);
+  p.ctas = (int)ctas;
+  if (split) {
+    auto up16 = [](size_t x) { return (x + 15) & ~size_t(15); };
+    const size_t rows = (size_t)p.ctas * 2 * (size_t)p.unit_rows;
+    p.off_m = rows * (size_t)head_dim * sizeof(float);
+    p.off_l = p.off_m + up16(rows * sizeof(float));
+    p.off_rec = p.off_l + up16(rows * sizeof(float));
+    p.bytes = p.off_rec + up16((size_t)p.ctas * sizeof(TreeRec));
   }
-  part = (part + block_size - 1) / block_size * block_size;
-  if (part >= max_len) {
-    p.part_tokens = (int)(max_len > 0 ? max_len : block_size);
-    return p;
-  }
-  p.part_tokens = (int)part;
-  p.max_parts = (int)((max_len + part - 1) / part);
-  const WsLayout w = workspace_layout(total_q * n_q_heads, p.max_parts, head_dim);
-  p.bytes = w.bytes;
-  p.off_m = w.off_m;
-  p.off_l = w.off_l;
   return p;
+}
+
+// The plan of a call: tensor cores where the shape and the options allow them.
+TreePlan plan_tree_call(const pa_opts& o, int batch, int max_nodes, int n_q_heads, int n_kv_heads, int head_dim,
+                        pa_dtype dtype, int sms, int64_t num_blocks, int64_t bt_stride, int block_size) {
+  if (o.prefill_kernel != 1 && decode_tc_supported(dtype, block_size, head_dim, n_q_heads / n_kv_heads, num_blocks)) {
+    const TreePlan p = plan_tree(true, batch, max_nodes, n_q_heads, n_kv_heads, head_dim, sms, bt_stride, block_size,
+                                 o.partition_tokens);
+    if (p.fits) return p;
+  }
+  return plan_tree(false, batch, max_nodes, n_q_heads, n_kv_heads, head_dim, sms, bt_stride, block_size,
+                   o.partition_tokens);
 }
 
 size_t tree_workspace_impl(int batch, int64_t total_q, int max_nodes, int64_t block_table_stride, int block_size,
@@ -644,11 +631,8 @@ size_t tree_workspace_impl(int batch, int64_t total_q, int max_nodes, int64_t bl
   int sms = 0;
   if (device_info(nullptr, &sms)) return 0;
   if (max_nodes > total_q) max_nodes = (int)total_q;
-  const int group = n_q_heads / n_kv_heads;
-  const bool use_tc = o.prefill_kernel != 1 && decode_tc_supported(dtype, block_size, head_dim, group, 1) &&
-                      tree_line_fits(batch, max_nodes, n_kv_heads, group, head_dim, block_table_stride, block_size);
-  return plan_tree(use_tc, batch, total_q, max_nodes, n_q_heads, n_kv_heads, head_dim, sms, block_table_stride,
-                   block_size, o.partition_tokens)
+  return plan_tree_call(o, batch, max_nodes, n_q_heads, n_kv_heads, head_dim, dtype, sms, 1, block_table_stride,
+                        block_size)
       .bytes;
 }
 
@@ -680,18 +664,11 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   int sms = 0;
   if ((rc = device_info(&err, &sms))) return rc;
   const int group = n_q_heads / n_kv_heads;
-  const bool tc_ok = decode_tc_supported(dtype, block_size, head_dim, group, num_blocks) &&
-                     tree_line_fits(batch, max_nodes, n_kv_heads, group, head_dim, block_table_stride, block_size);
-  if (o.prefill_kernel == 2 && !tc_ok) return PA_EUNSUPPORTED;
-  const bool use_tc = o.prefill_kernel == 2 || (o.prefill_kernel == 0 && tc_ok);
-  TreePlan plan = plan_tree(use_tc, batch, total_q, max_nodes, n_q_heads, n_kv_heads, head_dim, sms,
-                            block_table_stride, block_size, o.partition_tokens);
+  const TreePlan plan = plan_tree_call(o, batch, max_nodes, n_q_heads, n_kv_heads, head_dim, dtype, sms, num_blocks,
+                                       block_table_stride, block_size);
+  if (!plan.fits || (o.prefill_kernel == 2 && !plan.tensor_cores)) return PA_EUNSUPPORTED;
   const bool split = plan.bytes > 0 && workspace != nullptr;
   if (split && (workspace_bytes < plan.bytes || !aligned16(workspace))) return PA_EWORKSPACE;
-  if (!split) {
-    plan.max_parts = 1;
-    plan.part_tokens = (int)table_capacity(block_table_stride, block_size);
-  }
   if (checked()) {
     std::vector<int32_t> lens, qsl;
     rc = validate_tables(block_table, block_table_stride, context_lens, batch, num_blocks, block_size, s, &lens);
@@ -728,8 +705,6 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.group = group;
   a.group_shift = log2i(group);
   a.head_dim = head_dim;
-  a.part_tokens = plan.part_tokens;
-  a.max_parts = plan.max_parts;
   a.ctas = plan.ctas;
   a.share = plan.share;
   a.split = split;
@@ -743,9 +718,8 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.err = err;
   a.epoch = next_epoch();
   int launches = 0;
-  cudaError_t e = use_tc ? launch_tree_umma(a, dtype, s, &launches) : launch_tree_simt(a, dtype, s, &launches);
-  if (e == cudaSuccess && split)
-    e = use_tc ? launch_tree_join(a, dtype, s, &launches) : launch_tree_merge(a, dtype, s, &launches);
+  cudaError_t e = plan.tensor_cores ? launch_tree_umma(a, dtype, s, &launches) : launch_tree_simt(a, dtype, s, &launches);
+  if (e == cudaSuccess && split) e = launch_tree_join(a, dtype, plan.unit_rows, s, &launches);
   return finish(e, launches);
 }
 

@@ -167,13 +167,9 @@ struct TreeArgs {
   int group;
   int group_shift;                 // log2(group)
   int head_dim;
-  // CUDA-core kernel: partitions of part_tokens keys, max_parts per row in the grid (1 = no split);
-  // partial states ws_m, ws_l [total_q * n_q_heads][max_parts], ws_acc [..][max_parts][head_dim]
-  int part_tokens;
-  int max_parts;
-  // tcgen05 kernel: `ctas` CTAs that take `share` key tiles each (0: an equal share of the work), units
-  // cut where needed if `split`; two partial states per CTA, ws_m, ws_l [ctas][2][rows],
-  // ws_acc [ctas][2][rows][head_dim], and a record of the unit cut at its end, ws_rec [ctas]
+  // `ctas` CTAs that take `share` key tiles each (0: an equal share of the work), units cut where needed if
+  // `split`; two partial states per CTA, ws_m, ws_l [ctas][2][unit rows], ws_acc [..][head_dim], and a record
+  // of the unit cut at its end, ws_rec [ctas]
   int ctas;
   int share;
   int split;
@@ -193,13 +189,20 @@ struct TreeRec {
   int32_t last;
 };
 
-// Rows of a unit of the tcgen05 tree attention: one or two tiles of 128 (node, head) rows.
+// Shapes of the tree attention's work (tree_common.cuh): (node, head) rows of a unit, keys of its key tiles,
+// what a unit costs besides its keys in tiles, and the fewest tiles a CTA takes; shorter contexts are never cut.
+// tcgen05: one or two tiles of 128 rows.
 inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes * group <= 128 ? 128 : 256; }
-// Keys of one of its key tiles (see tree_umma.cu), and the fewest tiles a CTA takes; shorter contexts are
-// never cut.
 constexpr int tree_tile_keys(int head_dim, int unit_rows) { return head_dim == 64 || unit_rows == 256 ? 128 : 64; }
 constexpr int tree_gap(int unit_rows) { return unit_rows == 256 ? 3 : 4; }
 constexpr int tree_min_share(int unit_rows) { return unit_rows == 256 ? 8 : 12; }
+// CUDA cores: 8 threads' worth of 1, 2, 4 or 8 rows (a whole query group at least).
+inline int tree_simt_rows(int max_nodes, int group) {
+  const int64_t rows = (int64_t)max_nodes * group;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+constexpr int tree_simt_keys(int head_dim) { return head_dim == 64 ? 64 : 32; }
+constexpr int kTreeSimtGap = 1, kTreeSimtMinShare = 2;
 
 struct AcceptArgs {
   void* k_pool;
@@ -230,12 +233,12 @@ cudaError_t launch_lse_merge(const MergeArgs& a, pa_dtype dt, cudaStream_t s, in
 
 cudaError_t launch_block_tables(const TablesArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s, int* launches);
-// Tree attention on CUDA cores (every dtype and shape), then the merge of split contexts.
+// Tree attention on CUDA cores (every dtype and shape).
 cudaError_t launch_tree_simt(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 // The same on tcgen05 tensor cores (the support set of the tensor-core decode).
 cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
-cudaError_t launch_tree_join(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
-cudaError_t launch_tree_merge(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+// Units cut between CTAs, after either.
+cudaError_t launch_tree_join(const TreeArgs& a, pa_dtype dt, int unit_rows, cudaStream_t s, int* launches);
 
 // TMA view of a pool: 3-D tensor (column = n_kv_heads * head_dim, token in block, block) with the
 // pool's block stride, boxes of 64 columns x 16 tokens x 1 block, 128-byte swizzle.

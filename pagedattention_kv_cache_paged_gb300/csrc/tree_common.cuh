@@ -101,4 +101,154 @@ struct TreeWalk {
   }
 };
 
+// Where a CTA's span of the line begins and ends.
+struct TreeSched {
+  int32_t sums[16];  // per warp
+  int32_t tops[16];
+  int32_t share;
+  int32_t cut_start;  // where the unit that the span ends in begins on the line
+  int32_t snap;
+  TreeSpan span;
+  int32_t refused;    // a sequence of the batch is refused, and its rows are this CTA's to zero
+};
+
+__device__ __forceinline__ void tree_schedule_init(const TreeArgs& a, TreeSched& sm) {
+  sm.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
+  sm.refused = 0;
+}
+
+// All threads; sm initialised, and a barrier since.  The caller's next barrier publishes the result.  One
+// thread looks after one sequence at a time; positions on the line fit 32 bits (the host sees to it).
+template <int kThreads, int kKeys, int kGap, int kMinShare>
+__device__ __forceinline__ void tree_schedule(const TreeArgs& a, int nodes_unit, TreeSched& sm) {
+  constexpr int kWarps = kThreads / 32, kSnap = kGap - 1;
+  static_assert(kWarps <= 16, "sums per warp");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gap = a.share > 0 ? 0 : kGap;
+  int tiles = 0;
+  auto look = [&](int b) -> int {  // this thread's sequence: its length on the line
+    tiles = 0;
+    if (b >= a.batch) return 0;
+    const TreeSeq s = tree_seq(a, b);
+    if (s.bad) {
+      if (blockIdx.x == 0) raise_error(a.err, s.bad);
+      if (s.m > 0 && b % gridDim.x == blockIdx.x) sm.refused = 1;
+    }
+    if (s.n == 0 || s.m == 0) return 0;
+    tiles = (s.n + kKeys - 1) / kKeys;
+    return (s.m + nodes_unit - 1) / nodes_unit * a.n_kv_heads * (tiles + gap);
+  };
+  const bool one_chunk = a.batch <= kThreads;
+  int c = look(threadIdx.x);
+  int total = c, longest = c > 0 ? tiles + gap : 0;
+  for (int b = threadIdx.x + kThreads; b < a.batch; b += kThreads) {
+    const int more = look(b);
+    total += more;
+    longest = max(longest, more > 0 ? tiles + gap : 0);
+  }
+  auto scan = [&](int x) {  // inclusive, over the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += u;
+    }
+    return x;
+  };
+  int v = one_chunk ? scan(c) : 0;
+  const int warp_total = one_chunk ? v : __reduce_add_sync(0xffffffffu, total);  // (in lane 31)
+  const int warp_top = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    sm.sums[warp] = warp_total;
+    sm.tops[warp] = warp_top;
+  }
+  __syncthreads();
+  int pre = 0;
+  total = longest = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int x = sm.sums[w];
+    if (w < warp) pre += x;
+    total += x;
+    longest = max(longest, sm.tops[w]);
+  }
+  int share = a.share;
+  if (share <= 0) {
+    // fewer tiles than kMinShare would wait longer for their first keys than they save
+    share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+    share = max(share, min(longest, kMinShare));
+  }
+  // contexts that are never cut: every border moves to the nearest unit's
+  const int snap = !a.split || longest <= (a.share > 0 ? 0 : kMinShare) ? INT32_MAX : (a.share > 0 ? 1 : kSnap);
+  const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share;
+  if (threadIdx.x == 0) {
+    sm.share = share;
+    sm.snap = snap;
+  }
+  // this thread's sequence b lies at [first, first + c) of the line
+  auto place = [&](int b, int64_t first) {
+    const unsigned len = (unsigned)(tiles + gap);
+    if (c > 0 && lo >= first && lo < first + c) {
+      const unsigned off = (unsigned)(lo - first), u = off / len;
+      sm.span.b0 = b;
+      sm.span.u0 = (int)u;
+      sm.span.x0 = tree_cut(off - u * len, tiles, snap);
+      // the producers' first table entries
+      const int pos = min(sm.span.x0, tiles - 1) * kKeys;
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.block_table + (int64_t)b * a.bt_stride + (pos >> a.block_shift)));
+    }
+    if (c > 0 && hi >= first && hi < first + c) {
+      const unsigned off = (unsigned)(hi - first), u = off / len;
+      sm.span.b1 = b;
+      sm.span.u1 = (int)u;
+      sm.span.x1 = tree_cut(off - u * len, tiles, snap);
+      sm.cut_start = (int)(hi - (off - u * len));
+    }
+  };
+  if (one_chunk) {
+    place(threadIdx.x, (int64_t)pre + v - c);
+    return;
+  }
+  int carry = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    c = look(b0 + threadIdx.x);
+    v = scan(c);
+    __syncthreads();  // the sums before have been read
+    if (lane == 31) sm.sums[warp] = v;
+    __syncthreads();
+    pre = carry;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) pre += sm.sums[w];
+      carry += sm.sums[w];
+    }
+    place(b0 + threadIdx.x, (int64_t)pre + v - c);
+  }
+}
+
+// Zeros for the sequences whose lengths do not fit together (the rows that are this CTA's).
+template <typename T>
+__device__ __forceinline__ void tree_zero_refused(const TreeArgs& a) {
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    const TreeSeq s = tree_seq(a, b);
+    if (s.n != 0 || s.bad == 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + s.q0 * a.n_q_heads * a.head_dim);
+    const int64_t n = (int64_t)s.m * a.n_q_heads * a.head_dim * sizeof(T) / 16;
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// The record of a unit that starts in this CTA and ends in a later one (one thread).
+__device__ __forceinline__ void tree_record(const TreeArgs& a, const TreeSched& sm, const TreeUnit& w, int64_t row0,
+                                            TreeRec* rec) {
+  // the CTA that the unit's last tile went to
+  int last = (sm.cut_start + w.T - 1) / sm.share;
+  if (tree_cut((int64_t)last * sm.share - sm.cut_start, w.T, sm.snap) == w.T) --last;
+  *rec = TreeRec{row0, w.rows, last};
+}
+
+// Whether a row (the mask words of its node, or nullptr and the node of a chain) sees node s.
+__device__ __forceinline__ bool tree_sees(const int64_t* words, int node, int s) {
+  return words != nullptr ? ((__ldg(words + (s >> 6)) >> (s & 63)) & 1) != 0 : s <= node;
+}
+
 }  // namespace pa

@@ -32,6 +32,8 @@
 #include <cudaTypedefs.h>
 #include <float.h>
 
+#include <algorithm>
+
 #include "pa_ptx.cuh"
 #include "tree_common.cuh"
 
@@ -133,130 +135,6 @@ __device__ __forceinline__ float tu_weights(uint32_t taddr, const uint32_t (&sv)
   return (a0 + a1) + (b0 + b1);
 }
 
-// Where a CTA's span of the line begins and ends.
-struct TuSched {
-  alignas(16) int32_t sums[kTuThreads / 32];
-  alignas(16) int32_t tops[kTuThreads / 32];
-  int32_t share;
-  int32_t cut_start;  // where the unit that the span ends in begins on the line
-  int32_t snap;
-  TreeSpan span;
-  int32_t refused;    // a sequence of the batch is refused, and its rows are this CTA's to zero
-};
-
-__device__ __forceinline__ void tu_schedule_init(const TreeArgs& a, TuSched& sm) {
-  sm.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
-  sm.refused = 0;
-}
-
-// All threads; sm initialised, and a barrier since.  The caller's next barrier publishes the result.  One
-// thread looks after one sequence at a time; positions on the line fit 32 bits (the host sees to it).
-template <int kKeys, int kUnitRows>
-__device__ __forceinline__ void tu_schedule(const TreeArgs& a, int nodes_unit, TuSched& sm) {
-  constexpr int kWarps = kTuThreads / 32;
-  constexpr int kGap = tree_gap(kUnitRows), kMinShare = tree_min_share(kUnitRows), kSnap = kGap - 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gap = a.share > 0 ? 0 : kGap;
-  int tiles = 0;
-  auto look = [&](int b) -> int {  // this thread's sequence: its length on the line
-    tiles = 0;
-    if (b >= a.batch) return 0;
-    const TreeSeq s = tree_seq(a, b);
-    if (s.bad) {
-      if (blockIdx.x == 0) raise_error(a.err, s.bad);
-      if (s.m > 0 && b % gridDim.x == blockIdx.x) sm.refused = 1;
-    }
-    if (s.n == 0 || s.m == 0) return 0;
-    tiles = (s.n + kKeys - 1) / kKeys;
-    return (s.m + nodes_unit - 1) / nodes_unit * a.n_kv_heads * (tiles + gap);
-  };
-  const bool one_chunk = a.batch <= kTuThreads;
-  int c = look(threadIdx.x);
-  int total = c, longest = c > 0 ? tiles + gap : 0;
-  for (int b = threadIdx.x + kTuThreads; b < a.batch; b += kTuThreads) {
-    const int more = look(b);
-    total += more;
-    longest = max(longest, more > 0 ? tiles + gap : 0);
-  }
-  auto scan = [&](int x) {  // inclusive, over the warp
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += u;
-    }
-    return x;
-  };
-  int v = one_chunk ? scan(c) : 0;
-  const int warp_total = one_chunk ? v : __reduce_add_sync(0xffffffffu, total);  // (in lane 31)
-  const int warp_top = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    sm.sums[warp] = warp_total;
-    sm.tops[warp] = warp_top;
-  }
-  __syncthreads();
-  int pre = 0;
-  total = longest = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int x = sm.sums[w];
-    if (w < warp) pre += x;
-    total += x;
-    longest = max(longest, sm.tops[w]);
-  }
-  int share = a.share;
-  if (share <= 0) {
-    // fewer tiles than kMinShare would wait longer for their first keys than they save
-    share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
-    share = max(share, min(longest, kMinShare));
-  }
-  // contexts that are never cut: every border moves to the nearest unit's
-  const int snap = !a.split || longest <= (a.share > 0 ? 0 : kMinShare) ? INT32_MAX : (a.share > 0 ? 1 : kSnap);
-  const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share;
-  if (threadIdx.x == 0) {
-    sm.share = share;
-    sm.snap = snap;
-  }
-  // this thread's sequence b lies at [first, first + c) of the line
-  auto place = [&](int b, int64_t first) {
-    const unsigned len = (unsigned)(tiles + gap);
-    if (c > 0 && lo >= first && lo < first + c) {
-      const unsigned off = (unsigned)(lo - first), u = off / len;
-      sm.span.b0 = b;
-      sm.span.u0 = (int)u;
-      sm.span.x0 = tree_cut(off - u * len, tiles, snap);
-      // the producers' first table entries
-      const int pos = min(sm.span.x0, tiles - 1) * kKeys;
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.block_table + (int64_t)b * a.bt_stride + (pos >> a.block_shift)));
-    }
-    if (c > 0 && hi >= first && hi < first + c) {
-      const unsigned off = (unsigned)(hi - first), u = off / len;
-      sm.span.b1 = b;
-      sm.span.u1 = (int)u;
-      sm.span.x1 = tree_cut(off - u * len, tiles, snap);
-      sm.cut_start = (int)(hi - (off - u * len));
-    }
-  };
-  if (one_chunk) {
-    place(threadIdx.x, (int64_t)pre + v - c);
-    return;
-  }
-  int carry = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kTuThreads) {
-    c = look(b0 + threadIdx.x);
-    v = scan(c);
-    __syncthreads();  // the sums before have been read
-    if (lane == 31) sm.sums[warp] = v;
-    __syncthreads();
-    pre = carry;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) pre += sm.sums[w];
-      carry += sm.sums[w];
-    }
-    place(b0 + threadIdx.x, (int64_t)pre + v - c);
-  }
-}
-
 template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(kTuThreads, 1)
     tree_umma_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -288,10 +166,10 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 504);
   volatile int* bad_v = reinterpret_cast<int*>(base + 508);  // V of a drafted region held non-finite elements
   volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 512);  // [32] 16-key sub-tiles loaded, per tile
-  TuSched* sched = reinterpret_cast<TuSched*>(base + 640);
+  TreeSched* sched = reinterpret_cast<TreeSched*>(base + 640);
   // (maximum, sum) per row: narrow [2][128], of both groups; wide [128], of group 1
   float2* ml = reinterpret_cast<float2*>(base + (kWide ? 1024 : 2048));
-  static_assert(640 + sizeof(TuSched) <= (kWide ? 1024 : 2048) && kKStages <= 12 && kVStages <= 12, "head");
+  static_assert(640 + sizeof(TreeSched) <= (kWide ? 1024 : 2048) && kKStages <= 12 && kVStages <= 12, "head");
   // (S of tile t + kBufs waits for P V of tile t, and phases stay one apart only if the rings are not shorter)
   static_assert(kWide || (kKStages >= kBufs && kVStages >= kBufs && kBufs <= 4), "ring depths");
   static_assert(kKStages >= 2 && kVStages >= 2, "ring depths");
@@ -326,7 +204,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     mbar_init(&pv_done[1], 1);
     mbar_init(o_full, 1);
     *bad_v = 0;
-    tu_schedule_init(a, *sched);
+    tree_schedule_init(a, *sched);
     fence_barrier_init();
   }
   if (warp == 10) tmem_alloc(tmem_slot, 512);
@@ -335,7 +213,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
   const int nodes_unit = kUnitRows >> a.group_shift;
-  tu_schedule<kKeys, kUnitRows>(a, nodes_unit, *sched);
+  tree_schedule<kTuThreads, kKeys, tree_gap(kUnitRows), tree_min_share(kUnitRows)>(a, nodes_unit, *sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -756,9 +634,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
               const int last = min(w.x1 * kKeys, w.sq.n);
               for (int pos = max(w.x0 * kKeys, hist); pos < last; ++pos) {
                 const int s = pos - hist;
-                const bool see = words != nullptr ? ((__ldg(words + (s >> 6)) >> (s & 63)) & 1) != 0 : s <= node;
                 const int blk = __ldg(table + (pos >> a.block_shift));
-                if (!see || blk < 0 || blk >= a.num_blocks) continue;
+                if (!tree_sees(words, node, s) || blk < 0 || blk >= a.num_blocks) continue;
                 const T* vr = static_cast<const T*>(a.v_pool) + (int64_t)blk * a.kv_block_stride +
                               ((int64_t)(pos & (a.block_size - 1)) * a.n_kv_heads + w.kvh) * D + c0;
 #pragma unroll
@@ -801,13 +678,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       if (lane == 0) mbar_arrive(o_free);
       if (!whole && w.x0 == 0) {
         cut = true;  // at most one unit of a CTA: the one that its span ends in
-        if (threadIdx.x == 0) {
-          // the CTA that the unit's last tile went to
-          const int at = sched->cut_start, share = sched->share;
-          int last = (at + w.T - 1) / share;
-          if (tree_cut((int64_t)last * share - at, w.T, sched->snap) == w.T) --last;
-          a.ws_rec[blockIdx.x] = TreeRec{row0, w.rows, last};
-        }
+        if (threadIdx.x == 0) tree_record(a, *sched, w, row0, a.ws_rec + blockIdx.x);
       }
       t += n;
       ++un;
@@ -821,15 +692,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (sched->refused) {
-    // sequences whose lengths do not fit together: zeros
-    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-      const TreeSeq s = tree_seq(a, b);
-      if (s.n != 0 || s.bad == 0) continue;
-      uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + s.q0 * a.n_q_heads * D);
-      for (int64_t i = threadIdx.x; i < (int64_t)s.m * a.n_q_heads * (D / 8); i += kTuThreads) o[i] = make_uint4(0, 0, 0, 0);
-    }
-  }
+  if (sched->refused) tree_zero_refused<T>(a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -925,9 +788,8 @@ cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int
 }
 
 template <typename T, int D>
-static cudaError_t launch_join(const TreeArgs& a, cudaStream_t s) {
-  const int unit_rows = tree_unit_rows(a.max_nodes, a.group);
-  const int64_t rows = min((int64_t)a.max_nodes * a.group, (int64_t)unit_rows);
+static cudaError_t launch_join(const TreeArgs& a, int unit_rows, cudaStream_t s) {
+  const int64_t rows = std::min((int64_t)a.max_nodes * a.group, (int64_t)unit_rows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows + kTjWarps - 1) / kTjWarps), (unsigned)a.ctas);
   cfg.blockDim = dim3(kTjWarps * 32);
@@ -940,10 +802,19 @@ static cudaError_t launch_join(const TreeArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, a, unit_rows);
 }
 
-cudaError_t launch_tree_join(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
+template <typename T>
+static cudaError_t launch_join_t(const TreeArgs& a, int unit_rows, cudaStream_t s) {
+  return a.head_dim == 64 ? launch_join<T, 64>(a, unit_rows, s) : launch_join<T, 128>(a, unit_rows, s);
+}
+
+cudaError_t launch_tree_join(const TreeArgs& a, pa_dtype dt, int unit_rows, cudaStream_t s, int* launches) {
   ++*launches;
-  if (dt == PA_BF16) return a.head_dim == 64 ? launch_join<__nv_bfloat16, 64>(a, s) : launch_join<__nv_bfloat16, 128>(a, s);
-  return a.head_dim == 64 ? launch_join<__half, 64>(a, s) : launch_join<__half, 128>(a, s);
+  switch (dt) {
+    case PA_BF16: return launch_join_t<__nv_bfloat16>(a, unit_rows, s);
+    case PA_FP16: return launch_join_t<__half>(a, unit_rows, s);
+    case PA_FP32: return launch_join_t<float>(a, unit_rows, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace pa
