@@ -575,7 +575,7 @@ TreePlan plan_tree(bool tensor_cores, int batch, int max_nodes, int n_q_heads, i
   TreePlan p;
   p.tensor_cores = tensor_cores;
   const int group = n_q_heads / n_kv_heads;
-  p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_simt_rows(max_nodes, group);
+  p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_simt_rows(max_nodes, group, head_dim);
   const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : tree_simt_keys(head_dim);
   const int gap = tensor_cores ? tree_gap(p.unit_rows) : kTreeSimtGap;
   const int min_share = tensor_cores ? tree_min_share(p.unit_rows) : kTreeSimtMinShare;

@@ -196,12 +196,13 @@ inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes 
 constexpr int tree_tile_keys(int head_dim, int unit_rows) { return head_dim == 64 || unit_rows == 256 ? 128 : 64; }
 constexpr int tree_gap(int unit_rows) { return unit_rows == 256 ? 3 : 4; }
 constexpr int tree_min_share(int unit_rows) { return unit_rows == 256 ? 8 : 12; }
-// CUDA cores: 8 threads' worth of 1, 2, 4 or 8 rows (a whole query group at least).
-inline int tree_simt_rows(int max_nodes, int group) {
+// CUDA cores: up to 32 rows (16 at head_dim 128), a whole query group at least; four warps take 32 (16) keys of a
+// tile each.
+inline int tree_simt_rows(int max_nodes, int group, int head_dim) {
   const int64_t rows = (int64_t)max_nodes * group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32;
 }
-constexpr int tree_simt_keys(int head_dim) { return head_dim == 64 ? 64 : 32; }
+constexpr int tree_simt_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
 constexpr int kTreeSimtGap = 1, kTreeSimtMinShare = 2;
 
 struct AcceptArgs {

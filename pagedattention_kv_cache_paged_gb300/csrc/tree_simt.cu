@@ -1,13 +1,14 @@
 // Tree attention on CUDA cores (every dtype and shape; the kernel of fp32 pools).
 //
-// Two CTAs of 128 threads per SM walk their equal share of the units (tree_common.cuh).  A unit's rows
-// (up to 64 (node, head) rows) stay in shared memory; its key tiles (64 keys, 32 at head_dim 128) are
-// staged there in fp32 with cp.async, two deep.  Per tile: S = Q K^T, one online-softmax step (running
-// maximum and sum, accumulator rescaled), O += P V, all in fp32 registers: thread (ty, tx) of 8 x 16 holds
-// kRT rows x every 16th key of S, and the same rows x head_dim / 16 columns of O; P goes through shared memory
-// within the warp.  Per four dimensions it reads kRT + 4 vectors for 16 kRT fma's, so with 4 rows or more the
-// fma units bound it (37 T fma/s), with fewer the reads do, and below 16 rows HBM.  Rows are padded by 16
-// bytes, which spreads the 16 keys that a half-warp reads over the banks.
+// Two CTAs of four warps per SM walk their equal share of the units (tree_common.cuh).  A unit's rows (up to
+// 32 (node, head) rows, 16 at head_dim 128) stay in shared memory.  Each warp takes its own 32 (16) keys of
+// every key tile, staged in fp32 with cp.async through a ring of three buffers of its own (K, V, the next
+// K), and keeps its own softmax state (running maximum, sum and rescaled accumulator) for all rows, so that
+// nothing is read from shared memory twice and the warps meet at the end of the unit only, where their
+// states are joined.  Lane (rg, cg) of 4 x 8 holds kRT rows x every 8th key of S, and the same rows x head_dim
+// / 8 columns of O; P takes K's buffer on its way from one layout to the other.  Per four dimensions (keys) a
+// warp reads kRT + 4 (kRT + 8) conflict-free 128-byte wavefronts for 16 (32) kRT fma's per lane: with 8 rows
+// or more a lane's work is bound by the fma units (37 T fma/s), with few rows in all by HBM.
 //
 // Masks are looked at in tiles that reach into the drafted region only: a masked score becomes -inf by
 // selection.  A masked value cannot be deselected in a product (0 * NaN), so there non-finite elements of V
@@ -22,17 +23,19 @@
 
 namespace pa {
 
-constexpr int kTsThreads = 128;
+constexpr int kTsWarps = 4;
+constexpr int kTsThreads = 32 * kTsWarps;
 
 template <int D, int kRT>
 struct TsCfg {
-  static constexpr int kRows = 8 * kRT;
-  static constexpr int kKeys = tree_simt_keys(D);
-  static constexpr int kRow = D + 4;        // floats per staged row of Q, K and V
-  static constexpr int kPRow = kKeys + 4;   // of P
-  static constexpr int kKV = kKeys * kRow;
-  static constexpr int kFloats = kRows * kRow + 4 * kKV + kRows * kPRow;
-  static constexpr int kSmemBytes = kFloats * 4;
+  static constexpr int kRows = 4 * kRT;
+  static constexpr int kKeys = tree_simt_keys(D);    // of a tile
+  static constexpr int kWarpKeys = kKeys / kTsWarps;
+  static constexpr int kRow = D + 4;                 // floats per staged row of Q, K and V: spreads rows over banks
+  static constexpr int kPRow = kWarpKeys + 4;
+  static constexpr int kSlot = kWarpKeys * kRow;     // one K or V buffer
+  static constexpr int kSmemBytes = (kRows * kRow + kTsWarps * 3 * kSlot) * 4;
+  static_assert(kRows * kPRow <= kSlot && kRows * D <= 3 * kSlot, "P in a K buffer, O in a ring");
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
@@ -54,24 +57,24 @@ __device__ __forceinline__ void fma4(float& acc, const float4& a, const float4& 
 template <typename T, int D, int kRT>
 __global__ void __launch_bounds__(kTsThreads, 2) tree_simt_kernel(const TreeArgs a) {
   using Cfg = TsCfg<D, kRT>;
-  constexpr int kKeys = Cfg::kKeys, kRow = Cfg::kRow, kPRow = Cfg::kPRow, kRows = Cfg::kRows;
-  constexpr int kCK = kKeys / 16;        // keys per thread
-  constexpr int kOC = D / 64;            // 4-column groups per thread
+  constexpr int kKeys = Cfg::kKeys, kWK = Cfg::kWarpKeys, kRow = Cfg::kRow, kPRow = Cfg::kPRow, kRows = Cfg::kRows;
+  constexpr int kSlot = Cfg::kSlot;
+  constexpr int kKJ = kWK / 8;           // keys per lane
+  constexpr int kOC = D / 32;            // 4-column groups per lane
   constexpr int kVec = Elt<T>::kVec;     // elements per 16 bytes of a pool row
-  constexpr int kRowVecs = D / kVec;
-  constexpr int kRowsPass = kTsThreads / kRowVecs;
+  constexpr int kRowVecs = D / kVec;     // lanes per pool row
+  constexpr int kPass = 32 / kRowVecs;   // pool rows per pass of the warp
 
   extern __shared__ __align__(16) float smem[];
-  float* const qs = smem;                     // [kRows][kRow]
-  float* const ks = qs + kRows * kRow;        // [2][kKeys][kRow]
-  float* const vs = ks + 2 * Cfg::kKV;        // [2][kKeys][kRow]
-  float* const ps = vs + 2 * Cfg::kKV;        // [kRows][kPRow]
+  float* const qs = smem;                               // [kRows][kRow]
+  float* const rings = qs + kRows * kRow;               // [warps][3][kWK][kRow]
   __shared__ TreeSched sched;
-  __shared__ int64_t s_off[2][kKeys];         // element offset of each key's pool row of KV head 0; -1: none
-  __shared__ int s_gap[2];                    // x + 1: a key inside the context has no data in tile x
+  __shared__ float s_m[kTsWarps][kRows], s_l[kTsWarps][kRows];
   __shared__ int s_bad_v;
 
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rg = lane >> 3, cg = lane & 7;
+  float* const ring = rings + warp * 3 * kSlot;
   if (tid == 0) {
     tree_schedule_init(a, sched);
     s_bad_v = 0;
@@ -95,56 +98,46 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_simt_kernel(const TreeArgs
     auto out_row = [&](int r) -> int64_t {
       return row0 + (int64_t)(r >> a.group_shift) * a.n_q_heads + (r & (a.group - 1));
     };
-    // where the keys of tile x lie, into s_off[buf] (one thread per key)
-    auto locate = [&](int x, int buf) {
-      if (tid < kKeys) {
-        const int pos = x * kKeys + tid;
-        int64_t off = -1;
-        if (x < w.x1 && pos < w.sq.n) {
-          const int blk = __ldg(table + (pos >> a.block_shift));
-          if (blk < 0 || blk >= a.num_blocks) {
-            raise_error(a.err, PA_DEVERR_BLOCK_ID);
-            s_gap[buf] = x + 1;
-          } else {
-            off = (int64_t)blk * a.kv_block_stride + (pos & bmask) * row_elems;
-          }
-        }
-        s_off[buf][tid] = off;
-      }
+    auto words_of = [&](int node) -> const int64_t* {
+      return a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
     };
-    // tile in s_off[buf] into K and V buffer buf, zeros where there is no key
-    auto load = [&](int buf) {
-      const T* kp = static_cast<const T*>(a.k_pool) + (int64_t)w.kvh * D + (tid % kRowVecs) * kVec;
-      const T* vp = static_cast<const T*>(a.v_pool) + (int64_t)w.kvh * D + (tid % kRowVecs) * kVec;
+    // element offset of the pool row (KV head 0) of this lane's key of the warp's part of tile x; -1: no key
+    auto locate = [&](int x) -> int64_t {
+      const int pos = x * kKeys + warp * kWK + lane;
+      if (lane >= kWK || x >= w.x1 || pos >= w.sq.n) return -1;
+      const int blk = __ldg(table + (pos >> a.block_shift));
+      if (blk < 0 || blk >= a.num_blocks) {
+        raise_error(a.err, PA_DEVERR_BLOCK_ID);
+        return -1;
+      }
+      return (int64_t)blk * a.kv_block_stride + (pos & bmask) * row_elems;
+    };
+    // the warp's keys (or values) at the lanes' offsets `off` into a buffer, zeros where there is no key
+    auto load = [&](float* dst, const void* pool, int64_t off) {
+      const T* src = static_cast<const T*>(pool) + (int64_t)w.kvh * D + (lane % kRowVecs) * kVec;
 #pragma unroll
-      for (int r = 0; r < kKeys; r += kRowsPass) {
-        const int key = r + tid / kRowVecs;
-        const int64_t off = s_off[buf][key];
-        const int at = (buf * kKeys + key) * kRow + (tid % kRowVecs) * kVec;
+      for (int k = 0; k < kWK; k += kPass) {
+        const int key = k + lane / kRowVecs;
+        const int64_t o = __shfl_sync(0xffffffffu, off, key);
+        float* at = dst + key * kRow + (lane % kRowVecs) * kVec;
         if constexpr (kVec == 4) {
-          cp_async16(ks + at, kp + (off < 0 ? 0 : off), off >= 0);
-          cp_async16(vs + at, vp + (off < 0 ? 0 : off), off >= 0);
+          cp_async16(at, src + (o < 0 ? 0 : o), o >= 0);
         } else {
-          uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-          if (off >= 0) {
-            kv = __ldg(reinterpret_cast<const uint4*>(kp + off));
-            vv = __ldg(reinterpret_cast<const uint4*>(vp + off));
-          }
           float f[8];
-          Elt<T>::unpack(kv, f);
-          *reinterpret_cast<float4*>(ks + at) = make_float4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<float4*>(ks + at + 4) = make_float4(f[4], f[5], f[6], f[7]);
-          Elt<T>::unpack(vv, f);
-          *reinterpret_cast<float4*>(vs + at) = make_float4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<float4*>(vs + at + 4) = make_float4(f[4], f[5], f[6], f[7]);
+          Elt<T>::unpack(o >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + o)) : make_uint4(0, 0, 0, 0), f);
+          *reinterpret_cast<float4*>(at) = make_float4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<float4*>(at + 4) = make_float4(f[4], f[5], f[6], f[7]);
         }
       }
       cp_async_commit();
     };
 
-    if (tid < 2) s_gap[tid] = 0;
     __syncthreads();  // the unit before is done with the shared memory
-    locate(w.x0, 0);
+    // loads in the order K, V, K, V, ..: load number i goes to buffer i % 3, each a group of its own
+    int64_t off = locate(w.x0), off_next = locate(w.x0 + 1);
+    load(ring, a.k_pool, off);
+    load(ring + kSlot, a.v_pool, off);
+    load(ring + 2 * kSlot, a.k_pool, off_next);
     // the rows, scaled into the log2 domain; rows behind the last are zeros
     for (int i = tid; i < kRows * (D / 4); i += kTsThreads) {
       const int r = i / (D / 4), c = i % (D / 4) * 4;
@@ -157,34 +150,96 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_simt_kernel(const TreeArgs
       *reinterpret_cast<float4*>(qs + r * kRow + c) = make_float4(f[0], f[1], f[2], f[3]);
     }
     __syncthreads();
-    load(0);
-    locate(w.x0 + 1, 1);
 
+    // row i of this lane: 4 i + rg
     float m[kRT], l[kRT], o[kRT][kOC * 4];
-    bool seen[kRT];
+    unsigned seen = 0;
 #pragma unroll
     for (int i = 0; i < kRT; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
-      seen[i] = false;
 #pragma unroll
       for (int e = 0; e < kOC * 4; ++e) o[i][e] = 0.f;
     }
+    int slot = 0;  // of K of the tile
     for (int x = w.x0; x < w.x1; ++x) {
-      const int buf = (x - w.x0) & 1;
-      cp_async_wait<0>();
-      __syncthreads();  // tile x is here, s_off of tile x + 1 is, and everyone is done with tile x - 1
-      const int kb = x * kKeys;
-      const bool edge = kb + kKeys > hist || s_gap[buf] == x + 1;
-      bool ok[kCK];
+      float* const kt = ring + slot * kSlot;
+      float* const vt = ring + (slot == 2 ? 0 : slot + 1) * kSlot;
+      const int kb = x * kKeys + warp * kWK;
+      const unsigned have = __ballot_sync(0xffffffffu, off >= 0);  // keys of the tile with data
+      const unsigned full = kWK == 32 ? 0xffffffffu : (1u << (kWK & 31)) - 1u;
+      const bool edge = kb + kWK > hist || have != full;
+      const int64_t off_after = locate(x + 2);
+      cp_async_wait<2>();
+      __syncwarp();
+
+      // ---- S = Q K^T: keys cg + 8 j ----
+      float s[kRT][kKJ];
+#pragma unroll
+      for (int i = 0; i < kRT; ++i)
+#pragma unroll
+        for (int j = 0; j < kKJ; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 q[kRT], k[kKJ];
+#pragma unroll
+        for (int i = 0; i < kRT; ++i) q[i] = *reinterpret_cast<const float4*>(qs + (4 * i + rg) * kRow + d);
+#pragma unroll
+        for (int j = 0; j < kKJ; ++j) k[j] = *reinterpret_cast<const float4*>(kt + (cg + 8 * j) * kRow + d);
+#pragma unroll
+        for (int i = 0; i < kRT; ++i)
+#pragma unroll
+          for (int j = 0; j < kKJ; ++j) fma4(s[i][j], q[i], k[j]);
+      }
       if (edge) {
 #pragma unroll
-        for (int j = 0; j < kCK; ++j) ok[j] = s_off[buf][tx + 16 * j] >= 0;
+        for (int i = 0; i < kRT; ++i) {
+          const int node = w.node0 + (min(4 * i + rg, w.rows - 1) >> a.group_shift);
+          const int64_t* words = words_of(node);
+          bool any = false;
+#pragma unroll
+          for (int j = 0; j < kKJ; ++j) {
+            const int pos = kb + cg + 8 * j;
+            const bool see = ((have >> (cg + 8 * j)) & 1u) != 0 && (pos < hist || tree_sees(words, node, pos - hist));
+            if (!see) s[i][j] = -INFINITY;
+            any |= see;
+          }
+          if ((__ballot_sync(0xffffffffu, any) >> (8 * rg)) & 0xffu) seen |= 1u << i;
+        }
+      } else {
+        seen = 0xffffffffu;
+      }
+      // ---- softmax step; the eight lanes of a row group hold its rows ----
+      __syncwarp();  // K has been read: its buffer takes P
+#pragma unroll
+      for (int i = 0; i < kRT; ++i) {
+        float mx = s[i][0];
+#pragma unroll
+        for (int j = 1; j < kKJ; ++j) mx = fmaxf(mx, s[i][j]);
+#pragma unroll
+        for (int b = 1; b < 8; b <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
+        const float m_new = fmaxf(m[i], mx);
+        const float m_sub = m_new == -INFINITY ? 0.f : m_new;
+        const float corr = fast_exp2(m[i] - m_sub);  // m = -inf: 0
+        m[i] = m_new;
+        l[i] *= corr;
+#pragma unroll
+        for (int e = 0; e < kOC * 4; ++e) o[i][e] *= corr;
+#pragma unroll
+        for (int j = 0; j < kKJ; ++j) {
+          const float p = fast_exp2(s[i][j] - m_sub);
+          l[i] += p;
+          kt[(4 * i + rg) * kPRow + cg + 8 * j] = p;
+        }
+      }
+      cp_async_wait<1>();
+      __syncwarp();
+      if (edge) {
         // non-finite values of drafted tokens (keys without data are zeros)
-        for (int i = tid; i < kKeys * (D / 4); i += kTsThreads) {
+        for (int i = lane; i < kWK * (D / 4); i += 32) {
           const int key = i / (D / 4);
           if (kb + key < hist) continue;
-          float4* p = reinterpret_cast<float4*>(vs + (buf * kKeys + key) * kRow + i % (D / 4) * 4);
+          float4* p = reinterpret_cast<float4*>(vt + key * kRow + i % (D / 4) * 4);
           float4 v = *p;
           if (!(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX)) {
             v.x = fabsf(v.x) <= FLT_MAX ? v.x : 0.f;
@@ -195,86 +250,19 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_simt_kernel(const TreeArgs
             s_bad_v = 1;
           }
         }
-        __syncthreads();
+        __syncwarp();
       }
-      if (x + 1 < w.x1) load(buf ^ 1);
-
-      // ---- S = Q K^T: rows ty * kRT + i, keys tx + 16 j ----
-      float s[kRT][kCK];
-#pragma unroll
-      for (int i = 0; i < kRT; ++i)
-#pragma unroll
-        for (int j = 0; j < kCK; ++j) s[i][j] = 0.f;
-      const float* kt = ks + buf * Cfg::kKV + tx * kRow;
-      const float* qt = qs + ty * kRT * kRow;
-#pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 q[kRT], k[kCK];
-#pragma unroll
-        for (int i = 0; i < kRT; ++i) q[i] = *reinterpret_cast<const float4*>(qt + i * kRow + d);
-#pragma unroll
-        for (int j = 0; j < kCK; ++j) k[j] = *reinterpret_cast<const float4*>(kt + 16 * j * kRow + d);
-#pragma unroll
-        for (int i = 0; i < kRT; ++i)
-#pragma unroll
-          for (int j = 0; j < kCK; ++j) fma4(s[i][j], q[i], k[j]);
-      }
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-          const int r = min(ty * kRT + i, w.rows - 1), node = w.node0 + (r >> a.group_shift);
-          const int64_t* words = a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
-          bool any = false;
-#pragma unroll
-          for (int j = 0; j < kCK; ++j) {
-            const int pos = kb + tx + 16 * j;
-            const bool see = ok[j] && (pos < hist || tree_sees(words, node, pos - hist));
-            if (!see) s[i][j] = -INFINITY;
-            any |= see;
-          }
-          // (a half-warp holds the row)
-          seen[i] |= ((__ballot_sync(0xffffffffu, any) >> (tid & 16)) & 0xffffu) != 0;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kRT; ++i) seen[i] = true;
-      }
-      // ---- softmax step ----
-#pragma unroll
-      for (int i = 0; i < kRT; ++i) {
-        float mx = s[i][0];
-#pragma unroll
-        for (int j = 1; j < kCK; ++j) mx = fmaxf(mx, s[i][j]);
-#pragma unroll
-        for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float m_new = fmaxf(m[i], mx);
-        const float m_sub = m_new == -INFINITY ? 0.f : m_new;
-        const float corr = fast_exp2(m[i] - m_sub);  // m = -inf: 0
-        m[i] = m_new;
-        l[i] *= corr;
-#pragma unroll
-        for (int e = 0; e < kOC * 4; ++e) o[i][e] *= corr;
-#pragma unroll
-        for (int j = 0; j < kCK; ++j) {
-          const float p = fast_exp2(s[i][j] - m_sub);
-          l[i] += p;
-          ps[(ty * kRT + i) * kPRow + tx + 16 * j] = p;
-        }
-      }
-      __syncwarp();  // the rows of P that a warp reads are its own
-      // ---- O += P V: columns 4 tx + 64 e ----
-      const float* vt = vs + buf * Cfg::kKV + tx * 4;
-      const float* pt = ps + ty * kRT * kPRow;
+      // ---- O += P V: columns 4 cg + 32 e ----
 #pragma unroll 2
-      for (int k = 0; k < kKeys; k += 4) {
+      for (int k = 0; k < kWK; k += 4) {
         float4 p[kRT];
 #pragma unroll
-        for (int i = 0; i < kRT; ++i) p[i] = *reinterpret_cast<const float4*>(pt + i * kPRow + k);
+        for (int i = 0; i < kRT; ++i) p[i] = *reinterpret_cast<const float4*>(kt + (4 * i + rg) * kPRow + k);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
           for (int e = 0; e < kOC; ++e) {
-            const float4 v = *reinterpret_cast<const float4*>(vt + (k + u) * kRow + 64 * e);
+            const float4 v = *reinterpret_cast<const float4*>(vt + (k + u) * kRow + 4 * cg + 32 * e);
 #pragma unroll
             for (int i = 0; i < kRT; ++i) {
               const float pu = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
@@ -286,50 +274,77 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_simt_kernel(const TreeArgs
           }
         }
       }
-      __syncthreads();  // s_off[buf] has been read
-      locate(x + 2, buf);
+      __syncwarp();  // P and V have been read: V of the next tile and K of the one after it
+      load(kt, a.v_pool, off_next);
+      load(vt, a.k_pool, off_after);
+      slot = slot == 0 ? 2 : slot - 1;
+      off = off_next;
+      off_next = off_after;
     }
 
-    // ---- the unit's rows: the output, or this CTA's piece of it ----
-    const bool whole = w.x0 == 0 && w.x1 == w.T;
+    // ---- join the warps' states and write the unit's rows, or this CTA's piece of them ----
+    cp_async_wait<0>();
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < kRT; ++i) {
-      const int r = ty * kRT + i;
 #pragma unroll
-      for (int off = 1; off < 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-      if (r >= w.rows) continue;
-      const int node = w.node0 + (r >> a.group_shift);
+      for (int b = 1; b < 8; b <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], b);
+      const int r = 4 * i + rg;
+      if (cg == 0) {
+        s_m[warp][r] = (seen >> i) & 1u ? fmaxf(m[i], -FLT_MAX) : -INFINITY;
+        s_l[warp][r] = l[i];
+      }
+#pragma unroll
+      for (int e = 0; e < kOC; ++e)
+        *reinterpret_cast<float4*>(ring + r * D + 4 * cg + 32 * e) =
+            make_float4(o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]);
+    }
+    __syncthreads();
+    const bool whole = w.x0 == 0 && w.x1 == w.T;
+    for (int i = tid; i < w.rows * (D / 4); i += kTsThreads) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kTsWarps; ++k) M = fmaxf(M, s_m[k][r]);
+      float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (M != -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < kTsWarps; ++k) {
+          const float f = fast_exp2(s_m[k][r] - M);  // a warp without keys: 0, and its sums are 0
+          const float4 v = *reinterpret_cast<const float4*>(rings + k * 3 * kSlot + r * D + c);
+          L = fmaf(s_l[k][r], f, L);
+          acc[0] = fmaf(v.x, f, acc[0]);
+          acc[1] = fmaf(v.y, f, acc[1]);
+          acc[2] = fmaf(v.z, f, acc[2]);
+          acc[3] = fmaf(v.w, f, acc[3]);
+        }
+      }
       if (s_bad_v != 0) {
         // the non-finite elements that were taken out of V, for the rows that see them
-        const int64_t* words = a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
+        const int node = w.node0 + (r >> a.group_shift);
         const int last = min(w.x1 * kKeys, w.sq.n);
         for (int pos = max(w.x0 * kKeys, hist); pos < last; ++pos) {
           const int blk = __ldg(table + (pos >> a.block_shift));
-          if (!tree_sees(words, node, pos - hist) || blk < 0 || blk >= a.num_blocks) continue;
+          if (!tree_sees(words_of(node), node, pos - hist) || blk < 0 || blk >= a.num_blocks) continue;
           const T* v = static_cast<const T*>(a.v_pool) + (int64_t)blk * a.kv_block_stride + (pos & bmask) * row_elems +
-                       (int64_t)w.kvh * D + tx * 4;
+                       (int64_t)w.kvh * D + c;
 #pragma unroll
-          for (int e = 0; e < kOC * 4; ++e) {
-            const float f = static_cast<float>(v[(e >> 2) * 64 + (e & 3)]);
-            if (!(fabsf(f) <= FLT_MAX)) o[i][e] += f;
+          for (int e = 0; e < 4; ++e) {
+            const float f = static_cast<float>(v[e]);
+            if (!(fabsf(f) <= FLT_MAX)) acc[e] += f;
           }
         }
       }
-      const float M = seen[i] ? fmaxf(m[i], -FLT_MAX) : -INFINITY;
       if (whole) {
-        T* out = static_cast<T*>(a.out) + out_row(r) * D + tx * 4;
+        T* out = static_cast<T*>(a.out) + out_row(r) * D + c;
 #pragma unroll
-        for (int e = 0; e < kOC * 4; ++e)
-          out[(e >> 2) * 64 + (e & 3)] = Elt<T>::from_float(seen[i] ? o[i][e] / l[i] : 0.f);
+        for (int e = 0; e < 4; ++e) out[e] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[e] / L);
       } else {
         const int64_t piece = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * kRows + r;
-#pragma unroll
-        for (int e = 0; e < kOC; ++e)
-          *reinterpret_cast<float4*>(a.ws_acc + piece * D + tx * 4 + 64 * e) =
-              make_float4(o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]);
-        if (tx == 0) {
+        *reinterpret_cast<float4*>(a.ws_acc + piece * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (c == 0) {
           a.ws_m[piece] = M;
-          a.ws_l[piece] = l[i];
+          a.ws_l[piece] = L;
         }
       }
     }
@@ -369,11 +384,12 @@ static cudaError_t launch_ts(const TreeArgs& a, cudaStream_t s) {
 
 template <typename T, int D>
 static cudaError_t launch_ts_rows(const TreeArgs& a, cudaStream_t s) {
-  switch (tree_simt_rows(a.max_nodes, a.group)) {
-    case 8: return launch_ts<T, D, 1>(a, s);
-    case 16: return launch_ts<T, D, 2>(a, s);
-    case 32: return launch_ts<T, D, 4>(a, s);
-    default: return launch_ts<T, D, 8>(a, s);
+  switch (tree_simt_rows(a.max_nodes, a.group, D)) {
+    case 8: return launch_ts<T, D, 2>(a, s);
+    case 16: return launch_ts<T, D, 4>(a, s);
+    default:
+      if constexpr (D == 64) return launch_ts<T, D, 8>(a, s);
+      return cudaErrorInvalidValue;
   }
 }
 
