@@ -575,10 +575,10 @@ TreePlan plan_tree(bool tensor_cores, int batch, int max_nodes, int n_q_heads, i
   TreePlan p;
   p.tensor_cores = tensor_cores;
   const int group = n_q_heads / n_kv_heads;
-  p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_simt_rows(max_nodes, group, head_dim);
-  const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : tree_simt_keys(head_dim);
-  const int gap = tensor_cores ? tree_gap(p.unit_rows) : kTreeSimtGap;
-  const int min_share = tensor_cores ? tree_min_share(p.unit_rows) : kTreeSimtMinShare;
+  p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_split_rows(max_nodes, group, head_dim);
+  const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : tree_split_keys(head_dim);
+  const int gap = tensor_cores ? tree_gap(p.unit_rows) : kTreeSplitGap;
+  const int min_share = tensor_cores ? tree_min_share(p.unit_rows) : kTreeSplitMinShare;
   const int nodes_unit = p.unit_rows / group;
   const int64_t max_len = table_capacity(bt_stride, block_size);
   const int64_t tiles = (max_len + keys - 1) / keys;
@@ -718,7 +718,7 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.err = err;
   a.epoch = next_epoch();
   int launches = 0;
-  cudaError_t e = plan.tensor_cores ? launch_tree_umma(a, dtype, s, &launches) : launch_tree_simt(a, dtype, s, &launches);
+  cudaError_t e = plan.tensor_cores ? launch_tree_umma(a, dtype, s, &launches) : launch_tree_split(a, dtype, s, &launches);
   if (e == cudaSuccess && split) e = launch_tree_join(a, dtype, plan.unit_rows, s, &launches);
   return finish(e, launches);
 }

@@ -196,14 +196,12 @@ inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes 
 constexpr int tree_tile_keys(int head_dim, int unit_rows) { return head_dim == 64 || unit_rows == 256 ? 128 : 64; }
 constexpr int tree_gap(int unit_rows) { return unit_rows == 256 ? 3 : 4; }
 constexpr int tree_min_share(int unit_rows) { return unit_rows == 256 ? 8 : 12; }
-// CUDA cores: up to 32 rows (16 at head_dim 128), a whole query group at least; four warps take 32 (16) keys of a
-// tile each.
-inline int tree_simt_rows(int max_nodes, int group, int head_dim) {
-  const int64_t rows = (int64_t)max_nodes * group;
-  return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32;
+// mma.sync: one or two m16 tiles of rows; four warps take 32 (16 at head_dim 128) keys of a tile each.
+inline int tree_split_rows(int max_nodes, int group, int head_dim) {
+  return (int64_t)max_nodes * group <= 16 || head_dim == 128 ? 16 : 32;
 }
-constexpr int tree_simt_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
-constexpr int kTreeSimtGap = 1, kTreeSimtMinShare = 2;
+constexpr int tree_split_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
+constexpr int kTreeSplitGap = 1, kTreeSplitMinShare = 2;
 
 struct AcceptArgs {
   void* k_pool;
@@ -234,8 +232,8 @@ cudaError_t launch_lse_merge(const MergeArgs& a, pa_dtype dt, cudaStream_t s, in
 
 cudaError_t launch_block_tables(const TablesArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s, int* launches);
-// Tree attention on CUDA cores (every dtype and shape).
-cudaError_t launch_tree_simt(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+// Tree attention with mma.sync on values split into 16-bit parts (every dtype and block size).
+cudaError_t launch_tree_split(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 // The same on tcgen05 tensor cores (the support set of the tensor-core decode).
 cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 // Units cut between CTAs, after either.
