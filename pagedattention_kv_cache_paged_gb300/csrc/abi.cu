@@ -576,7 +576,7 @@ TreePlan plan_tree(bool tensor_cores, int batch, int max_nodes, int n_q_heads, i
   p.tensor_cores = tensor_cores;
   const int group = n_q_heads / n_kv_heads;
   p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_split_rows(max_nodes, group, head_dim);
-  const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : tree_split_keys(head_dim);
+  const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : kTreeSplitKeys;
   const int gap = tensor_cores ? tree_gap(p.unit_rows) : kTreeSplitGap;
   const int min_share = tensor_cores ? tree_min_share(p.unit_rows) : kTreeSplitMinShare;
   const int nodes_unit = p.unit_rows / group;
@@ -586,8 +586,8 @@ TreePlan plan_tree(bool tensor_cores, int batch, int max_nodes, int n_q_heads, i
   p.fits = units < (int64_t(1) << 30) / (tiles + gap) / (batch > 0 ? batch : 1);
   if (!p.fits) return p;
   units *= batch;
-  // tcgen05: one CTA per SM, else two, with an equal share each; an explicit partition length sets the share
-  const int64_t most = (int64_t)(sms > 0 ? sms : 1) * (tensor_cores ? 1 : 2);
+  // one resident set of CTAs with an equal share each; an explicit partition length sets the share
+  const int64_t most = (int64_t)(sms > 0 ? sms : 1) * (tensor_cores ? 1 : tree_split_ctas(head_dim));
   int64_t ctas = units * tiles < most ? units * tiles : most;
   bool split = tiles > min_share - gap;  // (shorter contexts are never cut, see tree_schedule)
   if (partition_tokens > 0) {

@@ -7,8 +7,8 @@
 // pool's type.  On CUDA cores the same work is bound by shared memory, which hands every lane its operands
 // (64 us where this takes HBM_US at 12 rows of head_dim 64): in fragments each value is read once per warp.
 //
-// Two CTAs of four warps per SM walk their equal share of the units (tree_common.cuh); a unit has up to 32
-// (node, head) rows (16 at head_dim 128).  Each warp takes its own 32 (16) keys of every key tile, staged in
+// Three (at head_dim 128 two) CTAs of four warps per SM walk their equal share of the units (tree_common.cuh); a
+// unit has up to 32 (node, head) rows (16 at head_dim 128).  Each warp takes its own 16 keys of every key tile, staged in
 // fp32 with cp.async through a ring of three buffers of its own, and keeps its own softmax state (running
 // maximum, sum and rescaled accumulator) for all rows; the warps meet at the end of the unit, where their states
 // are joined.  The order of the contracted index is free, so a lane's four dimensions (S) and four keys (P V)
@@ -41,12 +41,12 @@ template <> struct Parts<float> { static constexpr int kN = 3; };
 template <typename T, int D, int kMT>
 struct TsCfg {
   static constexpr int kRows = 16 * kMT;
-  static constexpr int kKeys = tree_split_keys(D);    // of a tile
+  static constexpr int kKeys = kTreeSplitKeys;    // of a tile
   static constexpr int kWarpKeys = kKeys / kTsWarps;
   static constexpr int kSlot = kWarpKeys * D;         // floats of one K or V buffer
   static constexpr int kQFrags = kMT * (D / 16) * Parts<T>::kN * 32;  // 16 bytes each
   static constexpr int kSmemBytes = kQFrags * 16 + kTsWarps * 3 * kSlot * 4;
-  static_assert(kRows * D <= 3 * kSlot, "O in a ring");
+  static_assert(kRows * D <= 3 * kSlot && kWarpKeys % 16 == 0 && kWarpKeys <= 32, "O in a ring, steps of 16 keys");
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
@@ -72,7 +72,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&part)[kN]) {
 }
 
 template <typename T, int D, int kMT>
-__global__ void __launch_bounds__(kTsThreads, 2) tree_split_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_kernel(const TreeArgs a) {
   using Cfg = TsCfg<T, D, kMT>;
   constexpr int kKeys = Cfg::kKeys, kWK = Cfg::kWarpKeys, kRows = Cfg::kRows, kSlot = Cfg::kSlot;
   constexpr int kN = Parts<T>::kN;       // parts of q, k and v
