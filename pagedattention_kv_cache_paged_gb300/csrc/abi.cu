@@ -745,7 +745,8 @@ int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride
   if ((rc = pool_block_stride(o, row_bytes * block_size, &stride_bytes))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned* err = nullptr;
-  if ((rc = device_info(&err, nullptr))) return rc;
+  int sms = 0;
+  if ((rc = device_info(&err, &sms))) return rc;
   if (checked()) {
     std::vector<int32_t> acc, acc_lens, hist, table;
     if ((rc = copy_to_host(acc_lens, accepted_lens, batch, s))) return rc;
@@ -784,7 +785,7 @@ int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride
   a.block_stride_vecs = stride_bytes / 16;
   a.err = err;
   int launches = 0;
-  cudaError_t e = launch_kv_accept(a, s, &launches);
+  cudaError_t e = launch_kv_accept(a, sms, s, &launches);
   return finish(e, launches);
 }
 
