@@ -524,7 +524,12 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
     return PA_EINVAL;
   if (free_capacity > 0 && !free_blocks) return PA_EINVAL;
   if (token_capacity > 0 && (!slot_mapping || !positions)) return PA_EINVAL;
-  if (context_lens == history_lens || context_lens == new_lens) return PA_EINVAL;  // read while it is written
+  // the lengths are read while the arrays of the step are written
+  auto overlap = [&](const int32_t* p, int64_t n, const int32_t* q) { return p < q + batch && q < p + n; };
+  for (const int32_t* lens : {history_lens, new_lens})
+    if (overlap(context_lens, batch, lens) || overlap(query_start_loc, (int64_t)batch + 1, lens) ||
+        overlap(block_counts, batch, lens))
+      return PA_EINVAL;
   if (parents && (mask_words < 1 || mask_words > (INT32_MAX >> 6) || (token_capacity > 0 && !tree_mask)))
     return PA_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -577,8 +582,8 @@ TreePlan plan_tree(bool tensor_cores, int batch, int max_nodes, int n_q_heads, i
   const int group = n_q_heads / n_kv_heads;
   p.unit_rows = tensor_cores ? tree_unit_rows(max_nodes, group) : tree_split_rows(max_nodes, group, head_dim);
   const int keys = tensor_cores ? tree_tile_keys(head_dim, p.unit_rows) : kTreeSplitKeys;
-  const int gap = tensor_cores ? tree_gap(p.unit_rows) : kTreeSplitGap;
-  const int min_share = tensor_cores ? tree_min_share(p.unit_rows) : kTreeSplitMinShare;
+  const int gap = tensor_cores ? kTreeGap : kTreeSplitGap;
+  const int min_share = tensor_cores ? kTreeMinShare : kTreeSplitMinShare;
   const int nodes_unit = p.unit_rows / group;
   const int64_t max_len = table_capacity(bt_stride, block_size);
   const int64_t tiles = (max_len + keys - 1) / keys;

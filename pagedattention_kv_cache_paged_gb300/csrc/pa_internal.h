@@ -194,8 +194,7 @@ struct TreeRec {
 // tcgen05: one or two tiles of 128 rows.
 inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes * group <= 128 ? 128 : 256; }
 constexpr int tree_tile_keys(int head_dim, int unit_rows) { return head_dim == 64 || unit_rows == 256 ? 128 : 64; }
-constexpr int tree_gap(int unit_rows) { return 3; }
-constexpr int tree_min_share(int unit_rows) { return 8; }
+constexpr int kTreeGap = 3, kTreeMinShare = 8;
 // mma.sync: one or two m16 tiles of rows; four warps take 16 keys of a tile each; CTAs per SM.
 inline int tree_split_rows(int max_nodes, int group, int head_dim) {
   return (int64_t)max_nodes * group <= 16 || head_dim == 128 ? 16 : 32;

@@ -27,8 +27,9 @@
 // be deselected (0 * NaN), so in those tiles non-finite elements of V are zeroed in shared memory before
 // the product, and added at the end, by themselves, to the rows that see them.
 //
-// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 Q and S, 11 P V.  Every wait is bounded (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each
-// barrier below is waited for before its next phase but one can complete.
+// Warps: 0-3 and 4-7 softmax, 8 K and 9 V producer (TMA), 10 Q and S, 11 P V.  Every wait is bounded
+// (PA_DEVERR_TIMEOUT).  A wait tells a barrier's phase from the next one only, so each barrier below is
+// waited for before its next phase but one can complete.
 #include <cudaTypedefs.h>
 #include <float.h>
 
@@ -86,7 +87,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-
 
 // 64 consecutive scores of this thread's row; those it does not see become -inf (kMasked).
 template <bool kMasked>
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
   const int nodes_unit = kUnitRows >> a.group_shift;
-  tree_schedule<kTuThreads, kKeys, tree_gap(kUnitRows), tree_min_share(kUnitRows)>(a, nodes_unit, *sched);
+  tree_schedule<kTuThreads, kKeys, kTreeGap, kTreeMinShare>(a, nodes_unit, *sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

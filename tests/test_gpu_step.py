@@ -299,6 +299,22 @@ def test_accept_long_lists(cuda_lib, lens):
     assert cuda_lib.device_error_flags() == 0
 
 
+@pytest.mark.parametrize("batch,layers", [(40, 40), (30, 41), (1, 700), (1300, 3)])
+@pytest.mark.parametrize("H,D", [(1, 64), (2, 128)])
+def test_accept_with_several_layers_to_a_block_of_threads(cuda_lib, batch, layers, H, D):
+    rng = np.random.default_rng(batch)
+    case = accept_case(batch, rng.integers(0, 20, batch).tolist(), 12, rng.integers(0, 12, batch).tolist(), 16, H, D,
+                       torch.float16, layers)
+    k, v, acc, lens, hist, table = case
+    dk, dv = k.cuda(), v.cuda()
+    cuda_lib.paged_kv_accept(dk, dv, acc.cuda(), lens.cuda(), hist.cuda(), table.cuda())
+    # every layer as the oracle moves one: all of them side by side as the heads of one
+    side = lambda x: x.permute(1, 2, 0, 3, 4).flatten(2, 3)
+    rk, rv = oracle.tree.paged_kv_accept(side(k), side(v), acc, lens, hist, table)
+    assert torch.equal(side(dk.cpu()), rk) and torch.equal(side(dv.cpu()), rv)
+    assert cuda_lib.device_error_flags() == 0
+
+
 def test_accept_lists_that_chain_through_each_other(cuda_lib):
     """Each row moves one place: every source is the destination of the entry after it."""
     case = list(accept_case(3, [5], 90, [80], 16, 2, 64, torch.float32))

@@ -316,3 +316,59 @@ def test_an_empty_batch(cuda_lib):
              block_table=d["block_table"][:0], context_lens=d["context_lens"][:0])
     cuda_lib.paged_attention_tree(**d)
     assert cuda_lib.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", [FP16, FP32])
+@pytest.mark.parametrize("batch", [129, 384, 385, 900])
+def test_more_sequences_than_threads(cuda_lib, kernel, dtype, batch):
+    """Lengths are looked at in chunks of a CTA's threads; one sequence of a late chunk is refused."""
+    rng = np.random.default_rng(batch)
+    hist, new = rng.integers(0, 70, batch), rng.integers(0, 5, batch)
+    hist[::17] = rng.integers(500, 900, len(hist[::17]))
+    hist[:3] = new[:3] = 0
+    new[batch - 2] = 3
+    case = TreeCase(batch, hist.tolist(), new.tolist(), q_heads=4, kv_heads=2, head_dim=64, block_size=16, dtype=dtype)
+    check(cuda_lib, case, run(cuda_lib, case, kernel=kernel, max_nodes=4), kernel)
+    d = case.device()
+    d["context_lens"][batch - 2] = 2
+    got = cuda_lib.paged_attention_tree(**d, scale=case.scale, kernel=kernel, max_nodes=4)
+    q0 = int(case.qsl[batch - 2])
+    assert (got[q0:q0 + 3] == 0).all() and cuda_lib.device_error_flags() == cuda_lib.PA_DEVERR_QUERY_LOC
+    got[q0:q0 + 3] = run(cuda_lib, case, kernel=kernel, max_nodes=4)[q0:q0 + 3]
+    check(cuda_lib, case, got, kernel)
+
+
+@pytest.mark.parametrize("dtype,G,m", [(BF16, 4, 16), (FP16, 8, 40), (FP32, 1, 12), (BF16, 1, 300)])
+def test_many_long_calls_behind_one_another(cuda_lib, dtype, G, m):
+    """Calls that overlap at their ends: the same bits every time, and no wait runs out."""
+    rng = np.random.default_rng(m)
+    case = TreeCase(m, rng.integers(0, 1500, 12).tolist(), rng.integers(1, m + 1, 12).tolist(), q_heads=8 * G, kv_heads=8,
+                    head_dim=128, block_size=16, dtype=dtype, words=5)
+    d = case.device()
+    first = cuda_lib.paged_attention_tree(**d, scale=case.scale, max_nodes=m)
+    outs = [torch.empty_like(first) for _ in range(4)]
+    for i in range(200):
+        cuda_lib.paged_attention_tree(**d, scale=case.scale, max_nodes=m, out=outs[i % 4])
+    check(cuda_lib, case, first)
+    assert all(torch.equal(o, first) for o in outs)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_the_largest_values(cuda_lib, dtype, kernel):
+    """The largest finite numbers: where a row does not see them they do nothing, where it does they keep their
+    size."""
+    case = TreeCase(40, [70, 5], [24, 9], q_heads=4, kv_heads=2, head_dim=64, block_size=16, dtype=dtype)
+    top = torch.finfo(dtype).max
+    for b in range(2):
+        for j, x in ((2, top), (3, -top)):
+            blk, tok = case.row_of(b, case.hist[b] + j)
+            case.v[blk, tok] = x
+            case.k[blk, tok, :, :9] = x
+    for row in range(33):
+        case.mask[row] &= ~12
+    check(cuda_lib, case, run(cuda_lib, case, kernel=kernel), kernel)
+    blk, tok = case.row_of(0, 33)
+    case.v[blk, tok, :, 7] = top
+    check(cuda_lib, case, run(cuda_lib, case, kernel=kernel), kernel)

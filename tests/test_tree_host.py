@@ -71,6 +71,7 @@ TABLES = dict(hist=P + 64, new=P + 128, batch=2, table=P, stride=8, cap=8, count
     (dict(qsl=None), "EINVAL"), (dict(ctx=None), "EINVAL"), (dict(slots=None), "EINVAL"), (dict(pos=None), "EINVAL"),
     (dict(parents=P), "EINVAL"), (dict(parents=P, words=1), "EINVAL"), (dict(parents=P, mask=P), "EINVAL"),
     (dict(ctx=P + 64), "EINVAL"), (dict(ctx=P + 128), "EINVAL"), (dict(batch=0), "OK"),
+    (dict(ctx=P + 68), "EINVAL"), (dict(ctx=P + 60), "EINVAL"), (dict(qsl=P + 56), "EINVAL"), (dict(counts=P + 132), "EINVAL"),
 ])
 def test_tables_refusals(lib, change, status):
     assert call(lib, "build_block_tables", list(TABLES), TABLES, **change) == getattr(pa, "PA_" + status)
