@@ -20,7 +20,11 @@
 //     one per group, that share every 128-key K and V tile; each group has one S buffer, and while one
 //     computes its softmax the tensor core has the other's products.  (A barrier that is complete already
 //     costs its waiter 110-230 cycles, a commit 100: one thread issuing both products took 4,600 cycles a
-//     tile without ever having to wait.)  In a unit of at most 128 rows the groups take tiles in turn.
+//     tile without ever having to wait.)  Each group starts on the next unit by itself, and the scores of
+//     the first 64 keys of a tile stay in registers between maximum and weights (171 -> 163 us).  A tile takes a
+//     group 3,700 cycles: 1,700 of softmax, the rest the round P V, S through the barriers; all 128 scores of
+//     a row in registers, an S buffer for both groups and weights of their own instead took 5,500 (TMEM
+//     reads and instructions of two warps per scheduler).  In a unit of at most 128 rows the groups take tiles in turn.
 //
 // Masks.  Only tiles that reach into the drafted region look at masks: a row's visibility bits are cut
 // out of its mask words.  A masked score becomes -inf by selection, whatever it was.  A masked value cannot
@@ -88,47 +92,39 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
-// 64 consecutive scores of this thread's row; those it does not see become -inf (kMasked).
-template <bool kMasked>
-__device__ __forceinline__ void tu_scores(uint32_t taddr, uint64_t keep, uint32_t (&sv)[64]) {
-  tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-  tmem_ld32(taddr + 32u, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-  tmem_wait_ld();
-  tmem_pin32(*reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-  tmem_pin32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-  if (kMasked) {
+// Scores this thread's row does not see (of 32 consecutive ones, by the bits of keep) become -inf.
+__device__ __forceinline__ void tu_select(uint32_t (&sv)[32], uint32_t keep) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c)
-      if (!((keep >> c) & 1ull)) sv[c] = 0xff800000u;
-  }
+  for (int c = 0; c < 32; ++c)
+    if (!((keep >> c) & 1u)) sv[c] = 0xff800000u;
 }
 
-__device__ __forceinline__ float tu_max(const uint32_t (&sv)[64]) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+__device__ __forceinline__ float tu_max(const uint32_t (&sv)[32], float top) {
+  float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int c = 0; c < 64; c += 8)
+  for (int c = 0; c < 32; c += 8)
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       m[u] = fmax3(m[u], __uint_as_float(sv[c + 2 * u]), __uint_as_float(sv[c + 2 * u + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Weights 2^(s * sc - m) of 64 scores as 16-bit pairs into the 32 columns at taddr; their sum.  Weights are
+// Weights 2^(s * sc - m) of 32 scores as 16-bit pairs into the 16 columns at taddr; their sum.  Weights are
 // rounded to the pool's type for the product with V (half a step each); the sum keeps 32 bits.
 template <bool kBf16>
-__device__ __forceinline__ float tu_weights(uint32_t taddr, const uint32_t (&sv)[64], float sc, float m) {
+__device__ __forceinline__ float tu_weights(uint32_t taddr, const uint32_t (&sv)[32], float sc, float m) {
   const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(-m, -m);
   uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-  uint32_t p[32];
+  uint32_t p[16];
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
+  for (int c = 0; c < 16; ++c) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sc2, nm2), x0, x1);
     const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
     sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(e0, e1));
     p[c] = pack2<kBf16>(e0, e1);
   }
-  tmem_st32(taddr, p);
+  tmem_st16(taddr, p);
   float a0, a1, b0, b1;
   f2_unpack(sum2[0], a0, a1);
   f2_unpack(sum2[1], b0, b1);
@@ -157,12 +153,12 @@ __global__ void __launch_bounds__(kTuThreads, 1)
   uint64_t* vdone = bars + 36;     // [kVStages] the P V products of the tile are done (the V stage is free)
   uint64_t* p_full = bars + 48;    // [kBufs] the buffer's weights are written (and O rescaled)
   uint64_t* q_full = bars + 52;    // one phase per unit
-  uint64_t* o_free = bars + 53;    // one phase per unit: both Os read
+  uint64_t* o_full = bars + 53;    // wide: one phase per unit of one Q tile: both Os complete
   uint64_t* ml_full = bars + 54;   // one phase per unit whose groups are joined: statistics written
   uint64_t* fin = bars + 55;       // [2] all products of an issuer are over
   uint64_t* s_full = bars + 61;    // [2] wide: the group's scores are written, one phase per item
   uint64_t* pv_done = bars + 57;   // [2] wide: O += P V of the group's item done, one phase per item
-  uint64_t* o_full = bars + 60;    // wide: one phase per unit: both Os complete
+  uint64_t* o_free = bars + 59;    // [2] one phase per unit: the Os read (narrow: both, [0]; wide: each)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 504);
   volatile int* bad_v = reinterpret_cast<int*>(base + 508);  // V of a drafted region held non-finite elements
   volatile uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 512);  // [32] 16-key sub-tiles loaded, per tile
@@ -194,7 +190,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
     }
     for (int k = 0; k < kBufs; ++k) mbar_init(&p_full[k], 4);
     mbar_init(q_full, 1);
-    mbar_init(o_free, 8);
+    mbar_init(&o_free[0], kWide ? 4 : 8);
+    mbar_init(&o_free[1], 4);
     mbar_init(ml_full, 8);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
@@ -369,11 +366,12 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         while (ok && walk.next(w)) {
           const bool pair = kWide && w.rows > 128;
           // the unit's first products overwrite the Os that the unit before it left
-          if (un > 0 && !wait(o_free, un - 1)) break;
+          if (!kWide && un > 0 && !wait(o_free, un - 1)) break;
           for (int x = w.x0; x < w.x1 && ok; ++x, ++t) {
             const int i = x - w.x0;
             if (!wait(&vfull[s], round)) break;
             for (int g = kWide ? (pair ? 0 : i & 1) : t & 1, last = pair ? 1 : g; g <= last; ++g) {
+              if (kWide && un > 0 && i < (pair ? 1 : 2) && !wait(&o_free[g], un - 1)) break;
               const int phase = kWide ? (g ? done1++ : done0++) : t / kBufs;
               if (!wait(&p_full[kWide ? g : t % kBufs], phase)) break;
               tc_fence_after();
@@ -387,7 +385,10 @@ __global__ void __launch_bounds__(kTuThreads, 1)
               ++round;
             }
           }
-          if (kWide && ok) umma_commit(o_full);
+          if (kWide && !pair) {
+            if (w.x1 - w.x0 == 1 && un > 0 && !wait(&o_free[1], un - 1)) break;  // (no phase is left out)
+            if (ok) umma_commit(o_full);
+          }
           ++un;
         }
       }
@@ -450,18 +451,30 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       auto tile = [&](auto masked, int buf, uint64_t keep0, uint64_t keep1, int before) {
         constexpr bool kMasked = decltype(masked)::value;
         const uint32_t srow = tS(buf) + lane_base;
-        // 128 keys in two blocks of 64, read twice (maximum, weights): a whole row does not stay in
-        // registers, and a loop keeps the code in the instruction cache.  Block h's weights go to columns
-        // 32 h .. 32 h + 31, whose scores have been read by then.
-        uint32_t sv[64];
+        // Blocks of 64 keys.  128 are read twice but for the first block (maximum, weights), as a whole row does not
+        // stay in registers, and the loops keep the code in the instruction cache.  Weights go to columns whose
+        // scores have been read by then.
+        int last = kKeys / 64 - 1;  // the last block that a row of the warp sees
+        if (kMasked && kKeys == 128 && __all_sync(0xffffffffu, keep1 == 0ull)) last = 0;
+        uint32_t lo[32], hi[32];
+        auto load = [&](int h) {
+          const uint64_t keep = h ? keep1 : keep0;
+          tmem_ld32(srow + 64u * h, lo);
+          tmem_ld32(srow + 64u * h + 32u, hi);
+          tmem_wait_ld();
+          tmem_pin32(lo);
+          tmem_pin32(hi);
+          if (kMasked) {
+            tu_select(lo, (uint32_t)keep);
+            tu_select(hi, (uint32_t)(keep >> 32));
+          }
+        };
         float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-        for (int h = kKeys / 64 - 1; h >= 0; --h) {
-          const uint64_t keep = h ? keep1 : keep0;
-          // a block that no row of the warp sees is neither read nor exponentiated
-          if (kMasked && kKeys == 128 && __all_sync(0xffffffffu, keep == 0ull)) continue;
-          tu_scores<kMasked>(srow + 64u * h, keep, sv);
-          top = fmaxf(top, tu_max(sv));
+        for (int h = last; h >= 0; --h) {
+          load(h);
+          top = tu_max(lo, top);
+          top = tu_max(hi, top);
         }
         top *= a.scale_log2;
         if (!kMasked || (keep0 | keep1) != 0) top = fmaxf(top, -FLT_MAX);  // keys were seen, whatever their scores
@@ -472,17 +485,16 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         }
         const float m_sub = m_use == -INFINITY ? 0.f : m_use;
 #pragma unroll 1
-        for (int h = 0; h < kKeys / 64; ++h) {
-          const uint64_t keep = h ? keep1 : keep0;
-          if (kMasked && kKeys == 128 && __all_sync(0xffffffffu, keep == 0ull)) {
-            uint32_t z[32];
+        for (int h = 0; h <= last; ++h) {
+          if (kKeys == 128 && h > 0) load(h);
+          sum += tu_weights<kBf16>(srow + 32u * h, lo, a.scale_log2, m_sub);
+          sum += tu_weights<kBf16>(srow + 32u * h + 16u, hi, a.scale_log2, m_sub);
+        }
+        if (kMasked && kKeys == 128 && last == 0) {
+          uint32_t z[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0u;
-            tmem_st32(srow + 32u * h, z);
-            continue;
-          }
-          if (kKeys == 128) tu_scores<kMasked>(srow + 64u * h, keep, sv);
-          sum += tu_weights<kBf16>(srow + 32u * h, sv, a.scale_log2, m_sub);
+          for (int i = 0; i < 32; ++i) z[i] = 0u;
+          tmem_st32(srow + 32u, z);
         }
         l_run = l_run * corr + sum;
         if (before >= 0 && __any_sync(0xffffffffu, corr != 1.f)) {
@@ -563,11 +575,12 @@ __global__ void __launch_bounds__(kTuThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      // both Os (narrow: products complete in the order in which their one thread issued them)
+      // the Os that this group reads: its own (pair), or both (products complete in the order in which their one
+      // thread issued them)
       const int end = t + n - 1;
-      uint64_t* complete = kWide ? o_full : &vdone[end % kVStages];
-      if (alive)
-        alive = __all_sync(0xffffffffu, mbar_wait(complete, (unsigned)((kWide ? un : end / kVStages) & 1), a.err, a.epoch));
+      uint64_t* complete = !kWide ? &vdone[end % kVStages] : pair ? &pv_done[grp] : o_full;
+      const int phase = !kWide ? end / kVStages : pair ? item - 1 : solo;
+      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(complete, (unsigned)(phase & 1), a.err, a.epoch));
       if (!alive) break;
       tc_fence_after();
 
@@ -675,7 +688,16 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       // O has been read: the next unit's first products may overwrite it
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) {
+        if (!kWide) {
+          mbar_arrive(o_free);
+        } else if (pair) {
+          mbar_arrive(&o_free[grp]);
+        } else if (grp == 0) {  // (it has read both)
+          mbar_arrive(&o_free[0]);
+          mbar_arrive(&o_free[1]);
+        }
+      }
       if (!whole && w.x0 == 0) {
         cut = true;  // at most one unit of a CTA: the one that its span ends in
         if (threadIdx.x == 0) tree_record(a, *sched, w, row0, a.ws_rec + blockIdx.x);
