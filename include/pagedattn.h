@@ -110,7 +110,8 @@ enum {
  *                          CUDA cores), 1 CUDA cores, 2 tensor cores (PA_EUNSUPPORTED if the shape
  *                          does not allow them)
  *   prefill_kernel         0 auto (tcgen05 tensor cores where the shape allows, else CUDA cores),
- *                          1 CUDA cores, 2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it)
+ *                          1 CUDA cores, 2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it);
+ *                          for paged_attention_tree see there
  *   partition_tokens       split-K partition length in tokens, rounded up to block_size, at most
  *                          2^30; 0 = automatic (see paged_attention_decode_workspace_size)
  *   reserved               must be 0
@@ -292,7 +293,8 @@ PA_API int paged_attention_prefill_ex(void* out, const void* q, const int32_t* q
  * the free blocks left by the sequences before it do not cover (PA_DEVERR_NO_BLOCKS; once one
  * sequence finds too few, no later one takes any).  Checked mode returns PA_ERANGE for each of these.
  * batch == 0 is a no-op.  Index arrays need the alignment of their type only.  What is written must not
- * overlap what is read (context_lens == history_lens returns PA_EINVAL), but for the arrays updated in place.
+ * overlap what is read, but for the arrays updated in place (context_lens, query_start_loc or block_counts
+ * over history_lens or new_lens returns PA_EINVAL).
  */
 PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_lens, int batch, int32_t* block_table,
                               int64_t block_table_stride, int64_t max_blocks, int32_t* block_counts,
@@ -318,18 +320,23 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *   scale           finite and > 0
  *   out[r][i] = sum_j softmax_j(scale * q[r][i] . K_j) V_j over the keys node r sees.  A row that sees
  *   nothing gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and
- *   NaN included); a non-finite key or value that it sees gives non-finite outputs.
+ *   NaN included); a non-finite value that it sees gives non-finite outputs, a non-finite key those of its
+ *   score (NaN in fp32 pools).
  *   workspace       optional scratch for splitting long contexts, at least
  *                   paged_attention_tree_workspace_size(...) bytes for the same sizes and opts,
  *                   16-byte aligned, no initialisation needed.  NULL: no splitting (slower for few
  *                   sequences with long contexts).  Calls that may overlap need one each.
- *   opts            may be NULL.  kv_block_stride_bytes, partition_tokens as for the decode call;
- *                   prefill_kernel: 0 auto (tcgen05 tensor cores for bf16/fp16 pools with
- *                   block_size % 16 == 0, else CUDA cores), 1 CUDA cores, 2 tcgen05
- *                   (PA_EUNSUPPORTED if the shape does not allow it).
+ *   opts            may be NULL.  kv_block_stride_bytes as for the decode call.  partition_tokens: keys
+ *                   that a block of threads takes, rounded up to whole tiles of 64 or 128 (0 = an equal
+ *                   share of the work); contexts are cut wherever such a share ends.  prefill_kernel:
+ *                   0 auto (tcgen05 tensor cores for bf16/fp16 pools with block_size % 16 == 0, else 1),
+ *                   1 the kernel of every type and block size (mma.sync; weights are not rounded to the
+ *                   pool's type, and fp32 values are split into bf16 parts that hold their 24 bits),
+ *                   2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it).
  * A sequence whose rows are out of order, more than max_nodes or 64 * mask_words, or more than its
  * context, gives zeros in the rows it has among total_q and is recorded as PA_DEVERR_QUERY_LOC (or
- * PA_DEVERR_TREE); checked mode returns PA_ERANGE.
+ * PA_DEVERR_TREE); checked mode returns PA_ERANGE.  A batch whose tables allow 2^30 key tiles or more in all
+ * returns PA_EUNSUPPORTED.
  */
 PA_API int paged_attention_tree(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q,
                                 const int64_t* tree_mask, int mask_words, int max_nodes, const void* k_pool,

@@ -594,7 +594,8 @@ def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_ta
     itself.  ``max_nodes`` bounds the nodes of one sequence (default: what the mask, or total_q,
     allows); a tight bound saves idle blocks.  ``workspace``: "auto" (allocated for the call on its
     stream), None (contexts are not split) or a caller-owned uint8 CUDA tensor.  ``kernel``: 0 auto, 1
-    CUDA cores, 2 tcgen05.  Rows from ``query_start_loc[batch]`` on are left as they were."""
+    mma.sync (every type and block size), 2 tcgen05.  ``partition_tokens``: keys a block of threads takes
+    (0: an equal share).  Rows from ``query_start_loc[batch]`` on are left as they were."""
     lib = _lib or load_library()
     dev, shape = q.get_device(), q.shape
     kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev)

@@ -372,3 +372,11 @@ def test_the_largest_values(cuda_lib, dtype, kernel):
     blk, tok = case.row_of(0, 33)
     case.v[blk, tok, :, 7] = top
     check(cuda_lib, case, run(cuda_lib, case, kernel=kernel), kernel)
+
+
+def test_more_work_than_positions_of_the_plan(cuda_lib):
+    """Refused on the host, before the arrays matter."""
+    pa = cuda_lib
+    p = torch.zeros(64, dtype=torch.int64, device="cuda").data_ptr()
+    assert pa.load_library().paged_attention_tree(p, p, p, 8, None, 0, 4, p, p, p, 2 ** 24, p, 2 ** 10, 8, 16, 0.125, 8, 2,
+                                                  64, pa.PA_BF16, None, 0, None, None) == pa.PA_EUNSUPPORTED
