@@ -2,20 +2,23 @@
 //
 // fp32 on bf16 tensor cores: x = x0 + x1 + x2, each part the bf16 rounding of what the ones before leave, holds
 // the 24 bits of x, and of the nine products of two split values the six with i + j <= 2 are formed (the others
-// come to at most 2^-23 of the product, of either sign); sums are the tensor core's, in fp32.  fp16 values split into two
-// parts and bf16 ones are their own first part, both exactly; weights are split like fp32 values whatever the
-// pool's type.  On CUDA cores the same work is bound by shared memory, which hands every lane its operands
-// (64 us where this takes 49: 27 sequences of up to 1,941 tokens, 12 drafts, 12 heads, head_dim 64; 59 -> 56 at
-// head_dim 128): in fragments each value is read once per warp.
+// come to at most 2^-23 of the product, of either sign); sums are the tensor core's, in fp32.  fp16 values split
+// into two parts and bf16 ones are their own first part, both exactly; weights are split like fp32 values whatever
+// the pool's type.  On CUDA cores the same work is bound by shared memory, which hands every lane its operands
+// (27 sequences of up to 1,941 tokens, 12 drafts, 12 heads, head_dim 64: 64 us where this takes 49, 3.4 TB/s): in
+// fragments each value is read once per warp.  Bound by the products (six for one, in tiles of 16 rows) where a
+// unit has many rows, by HBM where it has few (21 sequences of up to 8,984 tokens, head_dim 128, 4 rows: 4.5 TB/s),
+// and by the latency of a unit's start and end where contexts are short.
 //
 // Three (at head_dim 128 two) CTAs of four warps per SM walk their equal share of the units (tree_common.cuh); a
-// unit has up to 32 (node, head) rows (16 at head_dim 128).  Each warp takes its own 16 keys of every key tile, staged in
-// fp32 with cp.async through a ring of three buffers of its own, and keeps its own softmax state (running
+// unit has up to 32 (node, head) rows (16 at head_dim 128).  Each warp takes its own 16 keys of every key tile,
+// staged in fp32 with cp.async through a ring of three buffers of its own, and keeps its own softmax state (running
 // maximum, sum and rescaled accumulator) for all rows; the warps meet at the end of the unit, where their states
 // are joined.  The order of the contracted index is free, so a lane's four dimensions (S) and four keys (P V)
 // are consecutive: K and V fragments are 16-byte reads, and column c of the two score tiles of 16 keys is key
 // 4 (c / 2) + c % 2 and that + 2, so that P is an operand as it stands.  16-byte chunks of a staged row are
-// permuted (by the row's bit 0 in K, bits 2 and 3 in V) so that eight lanes meet all banks.
+// permuted (by the row's bit 0 in K, bits 2 and 3 in V) so that eight lanes meet all banks.  32 keys a warp with
+// two CTAs per SM took 59 us for the batch above.
 //
 // Masks are looked at in tiles that reach into the drafted region only: a masked score becomes -inf by
 // selection.  A masked value cannot be deselected in a product (0 * NaN), so there non-finite elements of V
@@ -64,6 +67,27 @@ __device__ __forceinline__ uint32_t pack2_finite(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Four consecutive elements (of a row that starts on 16 bytes).
+__device__ __forceinline__ void read4(const float* p, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void write4(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+template <typename T>
+__device__ __forceinline__ void read4(const T* p, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = static_cast<float>(e[i]);
+}
+template <typename T>
+__device__ __forceinline__ void write4(T* p, const float (&f)[4]) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]));
 }
 
 // The first kN bf16 parts of two values, packed in pairs (a in the low halves).
@@ -128,14 +152,15 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
     auto words_of = [&](int node) -> const int64_t* {
       return a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
     };
-    // element offset of the pool row (KV head 0) of this lane's key of the warp's part of tile x; -1: no key
+    // element offset of the pool row (KV head 0) of this lane's key of the warp's part of tile x; -1: no key,
+    // -2: a key whose block is out of range
     auto locate = [&](int x) -> int64_t {
       const int pos = x * kKeys + warp * kWK + lane;
       if (lane >= kWK || x >= w.x1 || pos >= w.sq.n) return -1;
       const int blk = __ldg(table + (pos >> a.block_shift));
       if (blk < 0 || blk >= a.num_blocks) {
         raise_error(a.err, PA_DEVERR_BLOCK_ID);
-        return -1;
+        return -2;
       }
       return (int64_t)blk * a.kv_block_stride + (pos & bmask) * row_elems;
     };
@@ -145,6 +170,10 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
     // the warp's keys (or values) at the lanes' offsets `off` into a buffer, zeros where there is no key
     auto load = [&](auto is_v, float* dst, int64_t off) {
       constexpr bool kV = decltype(is_v)::value;
+      if (!__any_sync(0xffffffffu, off != -1)) {  // (behind the last tile)
+        cp_async_commit();
+        return;
+      }
       const T* src = static_cast<const T*>(kV ? a.v_pool : a.k_pool) + (int64_t)w.kvh * D + (lane % kRowVecs) * kVec;
 #pragma unroll
       for (int k = 0; k < kWK; k += kPass) {
@@ -178,11 +207,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = 16 * mt + 8 * h + (l >> 2);
-        if (r < w.rows) {
-          const T* q = static_cast<const T*>(a.q) + out_row(r) * D + 16 * step + 4 * (l & 3);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[h][e] = static_cast<float>(q[e]);
-        }
+        if (r < w.rows) read4(static_cast<const T*>(a.q) + out_row(r) * D + 16 * step + 4 * (l & 3), f[h]);
       }
       uint32_t p0[kN], p1[kN], p2[kN], p3[kN];
       split2<kN>(f[0][0], f[0][1], p0);
@@ -205,7 +230,8 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
       for (int i = 0; i < kOT; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
     }
     int slot = 0;  // of K of the tile
-    for (int x = w.x0; x < w.x1; ++x) {
+    const int x_end = min(w.x1, (w.sq.n - warp * kWK + kKeys - 1) / kKeys);  // (in the last tile a warp may have no keys)
+    for (int x = w.x0; x < x_end; ++x) {
       float* const kt = ring + slot * kSlot;
       float* const vt = ring + (slot == 2 ? 0 : slot + 1) * kSlot;
       const int kb = x * kKeys + warp * kWK;
@@ -370,6 +396,9 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
     // ---- join the warps' states and write the unit's rows, or this CTA's piece of them ----
     cp_async_wait<0>();
     __syncwarp();
+    // (positions ascend over the warps and the tiles: these had keys in the first tile, the others nowhere)
+    const int busy = min(kTsWarps, (min(w.x1 * kKeys, w.sq.n) - w.x0 * kKeys + kWK - 1) / kWK);
+    if (warp < busy)
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
@@ -398,11 +427,12 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
       const int r = i / (D / 4), c = i % (D / 4) * 4;
       float M = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kTsWarps; ++k) M = fmaxf(M, s_m[k][r]);
+      for (int k = 0; k < kTsWarps; ++k) M = k < busy ? fmaxf(M, s_m[k][r]) : M;
       float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
       if (M != -INFINITY) {
 #pragma unroll
         for (int k = 0; k < kTsWarps; ++k) {
+          if (k >= busy) break;
           const float f = fast_exp2(s_m[k][r] - M);  // a warp without keys: 0, and its sums are 0
           const float4 v = *reinterpret_cast<const float4*>(rings + k * 3 * kSlot + r * D + c);
           L = fmaf(s_l[k][r], f, L);
@@ -429,9 +459,9 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
         }
       }
       if (whole) {
-        T* out = static_cast<T*>(a.out) + out_row(r) * D + c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[e] / L);
+        for (int e = 0; e < 4; ++e) acc[e] = M == -INFINITY ? 0.f : acc[e] / L;
+        write4(static_cast<T*>(a.out) + out_row(r) * D + c, acc);
       } else {
         const int64_t piece = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * kRows + r;
         *reinterpret_cast<float4*>(a.ws_acc + piece * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);

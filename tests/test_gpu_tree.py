@@ -380,3 +380,22 @@ def test_more_work_than_positions_of_the_plan(cuda_lib):
     p = torch.zeros(64, dtype=torch.int64, device="cuda").data_ptr()
     assert pa.load_library().paged_attention_tree(p, p, p, 8, None, 0, 4, p, p, p, 2 ** 24, p, 2 ** 10, 8, 16, 0.125, 8, 2,
                                                   64, pa.PA_BF16, None, 0, None, None) == pa.PA_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("entry", [0, 1, 2, 3, 5])
+def test_what_an_earlier_sequence_left_does_not_stand_in_for_a_bad_block(cuda_lib, kernel, dtype, entry):
+    """One CTA takes both sequences; every drafted key of the first is NaN."""
+    pa = cuda_lib
+    case = TreeCase(41, [100, 80], [60, 9], q_heads=4, kv_heads=1, head_dim=64, block_size=16, dtype=dtype)
+    for j in range(60):
+        blk, tok = case.row_of(0, 100 + j)
+        case.k[blk, tok] = float("nan")
+    case.table[1, entry] = -1
+    got = run(pa, case, kernel=kernel, partition_tokens=8192)
+    assert torch.isfinite(got[60:].float()).all()
+    assert pa.device_error_flags() == pa.PA_DEVERR_BLOCK_ID
+    case.k = torch.nan_to_num(case.k)
+    case.v = torch.nan_to_num(case.v)
+    assert torch.equal(got[60:], run(pa, case, kernel=kernel, partition_tokens=8192)[60:])
