@@ -724,7 +724,8 @@ constexpr int kTjWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kTjWarps * 32) tree_join_kernel(const TreeArgs a, int unit_rows) {
-  constexpr int kPer = D / 32;
+  constexpr int kPer = D / 32;  // columns of a lane
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.y;
   pdl_launch_dependents();
@@ -734,28 +735,41 @@ __global__ void __launch_bounds__(kTjWarps * 32) tree_join_kernel(const TreeArgs
   if (r >= rec.rows) return;
   const int pieces = rec.last - c + 1;
   auto piece = [&](int i) -> int64_t { return ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * unit_rows + r; };
-  float M = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) M = fmaxf(M, a.ws_m[piece(i)]);
+  auto columns = [&](int64_t p) { return *reinterpret_cast<const Vec*>(a.ws_acc + p * D + lane * kPer); };
+  // a unit has two pieces, or the rare long one more: the first two are read at once, before their maxima
+  const int64_t p0 = piece(0), p1 = piece(1);
+  const float m0 = a.ws_m[p0], m1 = a.ws_m[p1], l0 = a.ws_l[p0], l1 = a.ws_l[p1];
+  const Vec v0 = columns(p0), v1 = columns(p1);
+  float M = fmaxf(m0, m1);
+  for (int i = 2 + lane; i < pieces; i += 32) M = fmaxf(M, a.ws_m[piece(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
   float L = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  if (M != -INFINITY) {
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const int64_t p = piece(i);
-      const float f = fast_exp2(a.ws_m[p] - M);
-      L = fmaf(a.ws_l[p], f, L);
-      const float* src = a.ws_acc + p * D + lane * kPer;
+  auto add = [&](float m, float l, const Vec& v) {
+    const float f = fast_exp2(m - base);
+    L = fmaf(l, f, L);
+    const float* x = reinterpret_cast<const float*>(&v);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(src[k], f, acc[k]);
-    }
+    for (int k = 0; k < kPer; ++k) acc[k] = fmaf(x[k], f, acc[k]);
+  };
+  add(m0, l0, v0);
+  add(m1, l1, v1);
+#pragma unroll 4
+  for (int i = 2; i < pieces; ++i) {
+    const int64_t p = piece(i);
+    add(a.ws_m[p], a.ws_l[p], columns(p));
   }
   const int64_t qh = rec.row0 + (int64_t)(r >> a.group_shift) * a.n_q_heads + (r & (a.group - 1));
   T* o = static_cast<T*>(a.out) + qh * D + lane * kPer;
+  alignas(16) T x[kPer];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) o[k] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[k] / L);
+  for (int k = 0; k < kPer; ++k) x[k] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[k] / L);
+  if constexpr (sizeof(x) == 16) *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(x);
+  else if constexpr (sizeof(x) == 8) *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(x);
+  else *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(x);
 }
 
 // ------------------------------------------------------------------------------------------------
