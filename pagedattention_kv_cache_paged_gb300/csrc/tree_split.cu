@@ -2,13 +2,18 @@
 //
 // fp32 on bf16 tensor cores: x = x0 + x1 + x2, each part the bf16 rounding of what the ones before leave, holds
 // the 24 bits of x, and of the nine products of two split values the six with i + j <= 2 are formed (the others
-// come to at most 2^-23 of the product, of either sign); sums are the tensor core's, in fp32.  fp16 values split
-// into two parts and bf16 ones are their own first part, both exactly; weights are split like fp32 values whatever
-// the pool's type.  On CUDA cores the same work is bound by shared memory, which hands every lane its operands
-// (27 sequences of up to 1,941 tokens, 12 drafts, 12 heads, head_dim 64: 64 us where this takes 49, 3.4 TB/s): in
-// fragments each value is read once per warp.  Bound by the products (six for one, in tiles of 16 rows) where a
-// unit has many rows, by HBM where it has few (21 sequences of up to 8,984 tokens, head_dim 128, 4 rows: 4.5 TB/s),
-// and by the latency of a unit's start and end where contexts are short.
+// come to at most 2^-23 of the product, of either sign).  fp16 values split into two parts and bf16 ones are their
+// own first part, both exactly; weights are split like fp32 values whatever the pool's type.  The tensor core adds
+// in fp32 but cuts off where it should round, so that one accumulator for a whole context loses its last bits one
+// after the other (28,000 keys: 5e-6 of the result).  For fp32 pools the products of 16 dimensions (S) or 16 keys
+// (P V) are therefore summed by themselves, small ones first, and added up by rounded additions (2e-7, for 4-6 %
+// of the time).
+//
+// On CUDA cores the same work is bound by shared memory, which hands every lane its operands (27 sequences of up to
+// 1,941 tokens, 12 drafts, 12 heads, head_dim 64, fp32: 64 us where this takes 53, 3.1 TB/s): in fragments each
+// value is read once per warp.  Bound by the products (six for one, in tiles of 16 rows) where a unit has many rows,
+// by HBM where it has few (21 sequences of up to 8,984 tokens, head_dim 128, 4 rows: 4.2 TB/s), and by the latency
+// of a unit's start and end where contexts are short.
 //
 // Three (at head_dim 128 two) CTAs of four warps per SM walk their equal share of the units (tree_common.cuh); a
 // unit has up to 32 (node, head) rows (16 at head_dim 128).  Each warp takes its own 16 keys of every key tile,
@@ -18,7 +23,7 @@
 // are consecutive: K and V fragments are 16-byte reads, and column c of the two score tiles of 16 keys is key
 // 4 (c / 2) + c % 2 and that + 2, so that P is an operand as it stands.  16-byte chunks of a staged row are
 // permuted (by the row's bit 0 in K, bits 2 and 3 in V) so that eight lanes meet all banks.  32 keys a warp with
-// two CTAs per SM took 59 us for the batch above.
+// two CTAs per SM took 20 % longer.
 //
 // Masks are looked at in tiles that reach into the drafted region only: a masked score becomes -inf by
 // selection.  A masked value cannot be deselected in a product (0 * NaN), so there non-finite elements of V
@@ -50,7 +55,7 @@ struct TsCfg {
   static constexpr int kSlot = kWarpKeys * D;         // floats of one K or V buffer
   static constexpr int kQFrags = kMT * (D / 16) * Parts<T>::kN * 32;  // 16 bytes each
   static constexpr int kSmemBytes = kQFrags * 16 + kTsWarps * 3 * kSlot * 4;
-  static_assert(kRows * D <= 3 * kSlot && kWarpKeys % 16 == 0 && kWarpKeys <= 32, "O in a ring, steps of 16 keys");
+  static_assert(kRows * D <= 3 * kSlot && kWarpKeys == 16, "O in a ring, one step of 16 keys");
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
@@ -109,6 +114,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
   using Cfg = TsCfg<T, D, kMT>;
   constexpr int kKeys = Cfg::kKeys, kWK = Cfg::kWarpKeys, kRows = Cfg::kRows, kSlot = Cfg::kSlot;
   constexpr int kN = Parts<T>::kN;       // parts of q, k and v
+  constexpr bool kFresh = kN == 3;       // sums of a step's products on their own first
   constexpr int kNT = kWK / 8;           // score tiles of 8 keys
   constexpr int kKD = D / 16;            // steps of 16 dimensions
   constexpr int kOT = D / 8;             // output tiles of 8 columns
@@ -265,13 +271,18 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
           split2<kN>(k.x, k.y, b0);
           split2<kN>(k.z, k.w, b1);
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+          for (int mt = 0; mt < kMT; ++mt) {
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            float(&f)[4] = kFresh ? part : s[mt][n];
 #pragma unroll
-            for (int i = kN - 1; i >= 0; --i)
+            for (int d = 2; d >= 0; --d)  // small products first
 #pragma unroll
-              for (int j = kN - 1; j >= 0; --j)
-                if (i + j <= 2)
-                  mma_16816<true>(s[mt][n], q[mt][i].x, q[mt][i].y, q[mt][i].z, q[mt][i].w, b0[j], b1[j]);
+              for (int i = 0; i < kN; ++i)
+                if (i <= d && d - i < kN)
+                  mma_16816<true>(f, q[mt][i].x, q[mt][i].y, q[mt][i].z, q[mt][i].w, b0[d - i], b1[d - i]);
+#pragma unroll
+            for (int e = 0; kFresh && e < 4; ++e) s[mt][n][e] += part[e];
+          }
         }
       }
       __syncwarp();  // K has been read: V of the next tile
@@ -301,6 +312,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
         seen = 0xffffffffu;
       }
       // ---- softmax step; the four lanes of a row group hold its rows ----
+      float corr[kMT][2];
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.scale_log2;
           const float m_new = fmaxf(m[mt][h], mx);
           const float m_sub = m_new == -INFINITY ? 0.f : m_new;
-          const float corr = fast_exp2(m[mt][h] - m_sub);  // m = -inf: 0
+          corr[mt][h] = fast_exp2(m[mt][h] - m_sub);  // m = -inf: 0
           m[mt][h] = m_new;
           float sum = 0.f;
 #pragma unroll
@@ -324,12 +336,12 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
               sum += p;
             }
           }
-          l[mt][h] = l[mt][h] * corr + sum;
-          if (__any_sync(0xffffffffu, corr != 1.f)) {
+          l[mt][h] = l[mt][h] * corr[mt][h] + sum;
+          if (!kFresh && __any_sync(0xffffffffu, corr[mt][h] != 1.f)) {
 #pragma unroll
             for (int i = 0; i < kOT; ++i) {
-              o[mt][i][2 * h] *= corr;
-              o[mt][i][2 * h + 1] *= corr;
+              o[mt][i][2 * h] *= corr[mt][h];
+              o[mt][i][2 * h + 1] *= corr[mt][h];
             }
           }
         }
@@ -353,22 +365,22 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
         }
         __syncwarp();
       }
-      // ---- O += P V: 16 keys at a time; columns 32 b + 4 c + q make up output tile 4 b + q ----
-#pragma unroll
-      for (int n = 0; n < kNT; n += 2) {
+      // ---- O += P V; columns 32 b + 4 c + q make up output tile 4 b + q ----
+      {
+        static_assert(kNT == 2, "one step of 16 keys");
         uint32_t p[kMT][4][3];
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
-          split2<3>(s[mt][n][0], s[mt][n][1], p[mt][0]);
-          split2<3>(s[mt][n][2], s[mt][n][3], p[mt][1]);
-          split2<3>(s[mt][n + 1][0], s[mt][n + 1][1], p[mt][2]);
-          split2<3>(s[mt][n + 1][2], s[mt][n + 1][3], p[mt][3]);
+          split2<3>(s[mt][0][0], s[mt][0][1], p[mt][0]);
+          split2<3>(s[mt][0][2], s[mt][0][3], p[mt][1]);
+          split2<3>(s[mt][1][0], s[mt][1][1], p[mt][2]);
+          split2<3>(s[mt][1][2], s[mt][1][3], p[mt][3]);
         }
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
           float4 v[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) v[u] = vc[v_chunk(8 * n + 4 * t + u, 8 * b + g)];
+          for (int u = 0; u < 4; ++u) v[u] = vc[v_chunk(4 * t + u, 8 * b + g)];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             auto pick = [&](const float4& f) { return c == 0 ? f.x : c == 1 ? f.y : c == 2 ? f.z : f.w; };
@@ -376,13 +388,19 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
             split2<kN>(pick(v[0]), pick(v[1]), b0);
             split2<kN>(pick(v[2]), pick(v[3]), b1);
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int mt = 0; mt < kMT; ++mt) {
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              float(&at)[4] = o[mt][4 * b + c];
+              float(&f)[4] = kFresh ? part : at;
 #pragma unroll
-              for (int i = 2; i >= 0; --i)
+              for (int d = 2; d >= 0; --d)
 #pragma unroll
-                for (int j = kN - 1; j >= 0; --j)
-                  if (i + j <= 2)
-                    mma_16816<true>(o[mt][4 * b + c], p[mt][0][i], p[mt][1][i], p[mt][2][i], p[mt][3][i], b0[j], b1[j]);
+                for (int i = 0; i < 3; ++i)
+                  if (i <= d && d - i < kN)
+                    mma_16816<true>(f, p[mt][0][i], p[mt][1][i], p[mt][2][i], p[mt][3][i], b0[d - i], b1[d - i]);
+#pragma unroll
+              for (int e = 0; kFresh && e < 4; ++e) at[e] = fmaf(at[e], corr[mt][e >> 1], part[e]);
+            }
           }
         }
       }

@@ -399,3 +399,17 @@ def test_what_an_earlier_sequence_left_does_not_stand_in_for_a_bad_block(cuda_li
     case.k = torch.nan_to_num(case.k)
     case.v = torch.nan_to_num(case.v)
     assert torch.equal(got[60:], run(pa, case, kernel=kernel, partition_tokens=8192)[60:])
+
+
+def test_long_fp32_contexts_keep_their_last_bits(cuda_lib):
+    """One CTA sums up 12,000 keys.  Relative to the result, as root mean squares: 2^-24 for its rounding; partial
+    sums of 16 keys that are cut off, at most 2^-22; 188 rounded additions to the running sums of each of four
+    warps, at most 2^-24 each and of either sign, so about sqrt(188) / 2 of one, 2^-21.2; scores of size 1, off by
+    four such steps, at most 2^-21, independent from key to key.  Below 2^-20 together; a sum whose every step is
+    cut off comes to 188 * 6 * 2^-24 or 2^-14 at most, and to several times 2^-20 in fact."""
+    case = TreeCase(42, [12000, 11000], [6, 3], q_heads=1, kv_heads=1, head_dim=64, block_size=32, dtype=FP32)
+    got = run(cuda_lib, case, partition_tokens=16384)
+    rows, ref, _, _ = oracle.tree.paged_tree_attention(case.q, case.qsl, case.mask, case.k, case.v, case.table, case.ctx,
+                                                       case.scale)
+    off = got.cpu().double().numpy()[rows] - ref
+    assert np.sqrt((off ** 2).mean() / (ref ** 2).mean()) < 2.0 ** -20
