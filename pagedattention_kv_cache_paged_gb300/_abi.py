@@ -422,7 +422,7 @@ _HERE = contextlib.nullcontext()
 
 
 def _on(dev: int):
-    return _HERE if dev < 0 or dev == torch.cuda.current_device() else _OnDevice(dev)
+    return _HERE if dev < 0 or dev == torch._C._cuda_getDevice() else _OnDevice(dev)
 
 
 def _refuse(t, name: str, dtype, dev: int, shape):
@@ -441,33 +441,44 @@ def _refuse(t, name: str, dtype, dev: int, shape):
 
 def _arg(t, name: str, dtype, dev: int, shape=None) -> int:
     """Pointer of a contiguous CUDA tensor of a type, device and (optionally) shape."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev or dev < 0
-            or not t.is_contiguous() or (shape is not None and t.shape != shape)):
-        _refuse(t, name, dtype, dev, shape)
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, shape)
+
+
+def _vec(t, name: str, dtype, dev: int, n: int) -> int:
+    """Pointer of a contiguous CUDA tensor of ``n`` elements of a type and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.is_contiguous()
+            and t.numel() == n):
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, (n,))
 
 
 def _table(t, name: str, rows: int, dev: int) -> tuple:
     """(pointer, row stride, columns) of an int32 [rows, columns] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or (rows and t.shape[1] and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or (stride[1] != 1 and rows and shape[1]):
         raise ValueError(f"{name} must be [batch, entries] with contiguous rows")
-    if t.dtype != torch.int32 or t.get_device() != dev or dev < 0:
-        _refuse(t, name, torch.int32, dev, None)
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    if t.dtype is not _I32 or t.get_device() != dev or dev < 0:
+        _refuse(t, name, _I32, dev, None)
+    return t.data_ptr(), stride[0], shape[1]
 
 
 def _pools(k, v, dev: int, lead: int = 0) -> tuple:
     """(pointers, shape, block stride in elements) of two pools of one layout (see :func:`_pool`) behind
     ``lead`` dimensions of layers."""
-    shape, stride, vstride = k.shape[lead:], k.stride()[lead:], v.stride()[lead:]
-    if len(shape) != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    shape, stride, vstride, dtype = k.shape, k.stride(), v.stride(), k.dtype
+    if len(shape) != 4 + lead or shape != v.shape or dtype is not v.dtype:
         raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, n_kv_heads, head_dim] of one dtype")
+    if lead:
+        shape, stride, vstride = shape[lead:], stride[lead:], vstride[lead:]
     NB, S, H, D = shape
     if stride != (S * H * D, H * D, D, 1) or vstride != stride or k.get_device() != dev or v.get_device() != dev:
-        _pool(k[0] if lead else k, "k_pool"), _pool(v[0] if lead else v, "v_pool", k.dtype)
+        _pool(k[0] if lead else k, "k_pool"), _pool(v[0] if lead else v, "v_pool", dtype)
         for name, t in (("k_pool", k), ("v_pool", v)):
             if t.get_device() != dev:
-                _refuse(t, name, k.dtype, dev, None)
+                _refuse(t, name, dtype, dev, None)
         if NB > 1 and vstride[0] != stride[0]:
             raise ValueError(f"k_pool and v_pool must share one block stride (got {stride[0]} and {vstride[0]} elements)")
     return k.data_ptr(), v.data_ptr(), NB, S, H, D, (stride[0] if NB > 1 else S * H * D)
@@ -536,17 +547,17 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
         if mask is None or mask.dim() != 2 or (mask_words is not None and mask.shape[1] != mask_words):
             raise ValueError("with parents, out.tree_mask must be [tokens, mask_words]")
         words = mask.shape[1]
-        par = _arg(parents, "parents", _I32, dev, (T,))
+        par = _vec(parents, "parents", _I32, dev, T)
         msk = _arg(mask, "tree_mask", _I64, dev, (T, words))
     table, stride, entries = _table(block_table, "block_table", B, dev)
-    args = (_arg(history_lens, "history_lens", _I32, dev, (B,)), _arg(new_lens, "new_lens", _I32, dev, (B,)), B, table,
-            stride, entries, _arg(block_counts, "block_counts", _I32, dev, (B,)),
+    args = (_vec(history_lens, "history_lens", _I32, dev, B), _vec(new_lens, "new_lens", _I32, dev, B), B, table,
+            stride, entries, _vec(block_counts, "block_counts", _I32, dev, B),
             _arg(free_blocks, "free_blocks", _I32, dev), free_blocks.numel(),
-            _arg(free_state, "free_state", _I32, dev, (2,)), num_blocks, block_size, par,
-            _arg(qsl, "query_start_loc", _I32, dev, (B + 1,)), _arg(ctx, "context_lens", _I32, dev, (B,)),
-            _arg(slots, "slot_mapping", _I64, dev, (T,)), _arg(pos, "positions", _I32, dev, (T,)), T, msk, words,
+            _vec(free_state, "free_state", _I32, dev, 2), num_blocks, block_size, par,
+            _vec(qsl, "query_start_loc", _I32, dev, B + 1), _vec(ctx, "context_lens", _I32, dev, B),
+            _vec(slots, "slot_mapping", _I64, dev, T), _vec(pos, "positions", _I32, dev, T), T, msk, words,
             _raw_stream(stream, dev))
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = lib.build_block_tables(*args)
     else:
         with _OnDevice(dev):
@@ -571,15 +582,17 @@ def tree_workspace_size(batch: int, total_q: int, max_nodes: int, block_table_st
                            n_q_heads, n_kv_heads, head_dim, _code(dtype), kernel, partition_tokens)
 
 
-def _scratch(nbytes: int, device, stream):
-    """Scratch memory of one call, from the allocator's pool of the stream that the call runs on, so
-    that it is not handed to another stream while the call may still use it (and stays with a graph
-    that is being captured)."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _run_tree(lib, args: tuple, ws: tuple, tail: tuple) -> int:
+    """The call itself, on the current device.  ``ws`` = (None, n): scratch of its own, which comes from the
+    allocator's pool of the stream that the call runs on and goes back there at once, so no other stream is
+    handed it while the call may use it, and a graph that is being captured keeps it."""
+    if ws[0] is not None or ws[1] == 0:
+        return lib.paged_attention_tree(*args, *ws, *tail)
+    scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws[1], tail[1])
+    try:
+        return lib.paged_attention_tree(*args, scratch, ws[1], *tail)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
 
 
 def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_table, context_lens, scale=None,
@@ -606,9 +619,10 @@ def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_ta
     code = _code(dt)
     words, mask = 0, None
     if tree_mask is not None:
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q or tree_mask.shape[1] < 1:
+        of_mask = tree_mask.shape
+        if len(of_mask) != 2 or of_mask[0] != total_q or of_mask[1] < 1:
             raise ValueError("tree_mask must be [total_q, words]")
-        words = tree_mask.shape[1]
+        words = of_mask[1]
         mask = _arg(tree_mask, "tree_mask", _I64, dev)
     if max_nodes is None:
         max_nodes = max(1, min(total_q, 64 * words) if words else total_q)
@@ -618,20 +632,21 @@ def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_ta
         out = torch.empty_like(q)
     table, bt_stride, _ = _table(block_table, "block_table", B, dev)
     args = (_arg(out, "out", dt, dev, shape), _arg(q, "q", dt, dev),
-            _arg(query_start_loc, "query_start_loc", _I32, dev, (B + 1,)), total_q, mask, words, max_nodes, kp, vp,
-            table, bt_stride, _arg(context_lens, "context_lens", _I32, dev, (B,)), B, NB, S, scale, Hq, Hkv, D, code)
-    ws = workspace
-    if workspace is not None and isinstance(workspace, str) and workspace == "auto":
-        n = _tree_workspace(dev, B, total_q, max_nodes, bt_stride, S, Hq, Hkv, D, code, kernel, partition_tokens)
-        ws = _scratch(n, q.device, stream) if n else None
-    args += ((_arg(ws, "workspace", torch.uint8, dev), ws.numel()) if ws is not None else (None, 0))
-    args += (_opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), kernel, partition_tokens),
-             _raw_stream(stream, dev))
-    if dev == torch.cuda.current_device():
-        st = lib.paged_attention_tree(*args)
+            _vec(query_start_loc, "query_start_loc", _I32, dev, B + 1), total_q, mask, words, max_nodes, kp, vp,
+            table, bt_stride, _vec(context_lens, "context_lens", _I32, dev, B), B, NB, S, scale, Hq, Hkv, D, code)
+    if workspace is None:
+        ws = None, 0
+    elif isinstance(workspace, str) and workspace == "auto":
+        ws = None, _tree_workspace(dev, B, total_q, max_nodes, bt_stride, S, Hq, Hkv, D, code, kernel, partition_tokens)
+    else:
+        ws = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
+    tail = (_opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), kernel, partition_tokens),
+            _raw_stream(stream, dev))
+    if dev == torch._C._cuda_getDevice():
+        st = _run_tree(lib, args, ws, tail)
     else:
         with _OnDevice(dev):
-            st = lib.paged_attention_tree(*args)
+            st = _run_tree(lib, args, ws, tail)
     if st:
         _check("paged_attention_tree", st)
     return out
@@ -658,10 +673,10 @@ def paged_kv_accept(k_pool, v_pool, accepted, accepted_lens, history_lens, block
     acc, acc_stride, entries = _table(accepted, "accepted", B, dev)
     table, bt_stride, _ = _table(block_table, "block_table", B, dev)
     args = (kp, vp, layers, layer_stride, acc, acc_stride, entries,
-            _arg(accepted_lens, "accepted_lens", _I32, dev, (B,)), _arg(history_lens, "history_lens", _I32, dev, (B,)),
+            _vec(accepted_lens, "accepted_lens", _I32, dev, B), _vec(history_lens, "history_lens", _I32, dev, B),
             table, bt_stride, B, NB, S, Hkv, D, _code(k_pool.dtype),
             _opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), 0, 0), _raw_stream(stream, dev))
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = lib.paged_kv_accept(*args)
     else:
         with _OnDevice(dev):
