@@ -8,23 +8,25 @@
 // never pause at a border.
 //
 // Two groups of four softmax warps, each with an O of its own.
-//   Narrow kernel (no sequence has more than 128 (node, head) rows): bound by HBM.  The groups take the key
-//     tiles of a unit in turn and their states are joined at its end (both Os lie in the same TMEM lanes, so
-//     only (maximum, sum) goes through shared memory, and each group writes half of the columns).  A tile
-//     passes every 1,400 cycles at HBM's rate, the round S, softmax, P V through the barriers takes about
-//     3,500, so four tiles (three at head_dim 64, which takes 128-key tiles to have the same bytes per
-//     round) are in flight; and one thread would need 2,100 cycles for the waits, issues and commits of a
-//     tile, so four warps share them (K, V, S, P V), each product's one commit telling the softmax, the
-//     producer and the other issuer alike.
-//   Wide kernel: bound by the softmax and the tensor core.  A unit of more than 128 rows has two Q tiles,
-//     one per group, that share every 128-key K and V tile; each group has one S buffer, and while one
-//     computes its softmax the tensor core has the other's products.  (A barrier that is complete already
-//     costs its waiter 110-230 cycles, a commit 100: one thread issuing both products took 4,600 cycles a
-//     tile without ever having to wait.)  Each group starts on the next unit by itself, and the scores of
-//     the first 64 keys of a tile stay in registers between maximum and weights (171 -> 163 us).  A tile takes a
-//     group 3,700 cycles: 1,700 of softmax, the rest the round P V, S through the barriers; all 128 scores of
-//     a row in registers, an S buffer for both groups and weights of their own instead took 5,500 (TMEM
-//     reads and instructions of two warps per scheduler).  In a unit of at most 128 rows the groups take tiles in turn.
+//   Narrow kernel (no sequence has more than 128 (node, head) rows): bound by HBM (618 MB of a serving batch
+//     with up to 16 drafts in 102 us, 1.34 GB of four long documents in 211 us: 6.1 and 6.4 TB/s).  The groups
+//     take the key tiles of a unit in turn and their states are joined at its end (both Os lie in the same TMEM
+//     lanes, so only (maximum, sum) goes through shared memory, and each group writes half of the columns).  A
+//     tile passes every 1,400 cycles at HBM's rate, the round S, softmax, P V through the barriers takes about
+//     3,500, so four tiles (three at head_dim 64, which takes 128-key tiles to have the same bytes per round)
+//     are in flight; and one thread would need 2,100 cycles for the waits, issues and commits of a tile, so four
+//     warps share them (K, V, S, P V), each product's one commit telling the softmax, the producer and the other
+//     issuer alike.
+//   Wide kernel: bound by the softmax and the tensor core (the serving batch with 48 to 64 drafts, 134 GFLOP:
+//     161 us, 0.83 PFLOP/s).  A unit of more than 128 rows has two Q tiles, one per group, that share every
+//     128-key K and V tile; each group has one S buffer, and while one computes its softmax the tensor core has
+//     the other's products.  (A barrier that is complete already costs its waiter 110-230 cycles, a commit 100:
+//     one thread issuing both products took 4,600 cycles a tile without ever having to wait.)  Each group starts
+//     on the next unit by itself, and the scores of the first 64 keys of a tile stay in registers between maximum
+//     and weights (171 -> 163 us).  A tile takes a group 3,600 cycles: 1,650 of softmax, the rest the round P V, S
+//     through the barriers.  All 128 scores of a row in registers, an S buffer for both groups and weights of
+//     their own instead took 5,500 (2,700 of softmax).  In a unit of at most 128 rows the groups take tiles in
+//     turn.
 //
 // Masks.  Only tiles that reach into the drafted region look at masks: a row's visibility bits are cut
 // out of its mask words.  A masked score becomes -inf by selection, whatever it was.  A masked value cannot
