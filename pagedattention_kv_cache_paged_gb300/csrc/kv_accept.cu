@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kAccThreads, kAccCtas) kv_accept_kernel(const 
 }
 
 cudaError_t launch_kv_accept(const AcceptArgs& a, int sms, cudaStream_t s, int* launches) {
-  // Layers of a sequence divided among its CTAs for two rounds of CTAs: a CTA looks its rows up once, and the
-  // second round evens out lists of different lengths.  64 sequences x 32 layers: 12.8 us; one round 13.2,
+  // Layers of a sequence divided among its CTAs for two waves of CTAs: a CTA looks its rows up once, and the
+  // second wave evens out lists of different lengths.  64 sequences x 32 layers: 12.8 us; one wave 13.2,
   // a CTA per layer 13.7.
   const int per_seq = std::max(1, std::min(a.num_layers, 2 * sms * kAccCtas / a.batch));
   const int layers_cta = (a.num_layers + per_seq - 1) / per_seq;
