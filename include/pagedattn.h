@@ -333,9 +333,11 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *                   1 the kernel of every type and block size (mma.sync; weights are not rounded to the
  *                   pool's type, and fp32 values are split into bf16 parts that hold their 24 bits),
  *                   2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it).
- * A sequence whose rows are out of order, more than max_nodes or 64 * mask_words, or more than its
- * context, gives zeros in the rows it has among total_q and is recorded as PA_DEVERR_QUERY_LOC (or
- * PA_DEVERR_TREE); checked mode returns PA_ERANGE.  A batch whose tables allow 2^30 key tiles or more in all
+ * A sequence whose rows are out of order, reach past total_q, are more than max_nodes or 64 * mask_words,
+ * or more than its context, or whose context is negative or longer than its table row, gives zeros in all
+ * the rows it has among total_q (rows that an unordered query_start_loc gives to two sequences hold either's)
+ * and is recorded as PA_DEVERR_QUERY_LOC (or PA_DEVERR_TREE, PA_DEVERR_CONTEXT_LEN); checked mode returns
+ * PA_ERANGE.  A batch whose tables allow 2^30 key tiles or more in all
  * returns PA_EUNSUPPORTED.
  */
 PA_API int paged_attention_tree(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q,

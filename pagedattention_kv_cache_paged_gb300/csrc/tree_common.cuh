@@ -8,9 +8,9 @@ namespace pa {
 
 // The rows and lengths of sequence b, or n = 0 and an error bit when they do not fit together.
 struct TreeSeq {
-  int64_t q0;
-  int m;      // nodes (0: no rows of this sequence are written)
-  int n;      // context length; 0 when the sequence is refused
+  int64_t q0;  // first row (refused: the first among the call's)
+  int m;       // nodes; of a refused sequence the rows that it has among the call's, all of which become zeros
+  int n;       // context length; 0 when the sequence is refused
   unsigned bad;
 };
 
@@ -21,14 +21,16 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   s.q0 = q0;
   if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
     s.bad = PA_DEVERR_QUERY_LOC;
-    s.n = 0;
-    return s;
+  } else {
+    if (q1 - q0 > a.max_nodes || s.n < q1 - q0) s.bad |= PA_DEVERR_QUERY_LOC;
+    if (a.tree_mask != nullptr && q1 - q0 > (int64_t)64 * a.mask_words) s.bad |= PA_DEVERR_TREE;
+    if (s.n < 0 || s.n > (a.bt_stride << a.block_shift)) s.bad |= PA_DEVERR_CONTEXT_LEN;
   }
-  s.m = (int)min(q1 - q0, (int64_t)a.max_nodes);
-  if (q1 - q0 > a.max_nodes || s.n < q1 - q0) s.bad |= PA_DEVERR_QUERY_LOC;
-  if (a.tree_mask != nullptr && q1 - q0 > (int64_t)64 * a.mask_words) s.bad |= PA_DEVERR_TREE;
-  if (s.n < 0 || s.n > (a.bt_stride << a.block_shift)) s.bad |= PA_DEVERR_CONTEXT_LEN;
-  if (s.bad) s.n = 0;
+  if (s.bad) {
+    s.n = 0;
+    s.q0 = max(q0, (int64_t)0);
+  }
+  s.m = (int)max(min(q1, a.total_q) - s.q0, (int64_t)0);
   return s;
 }
 
@@ -225,7 +227,7 @@ __device__ __forceinline__ void tree_schedule(const TreeArgs& a, int nodes_unit,
   }
 }
 
-// Zeros for the sequences whose lengths do not fit together (the rows that are this CTA's).
+// Zeros for the sequences whose lengths do not fit together (those that fall to this CTA).
 template <typename T>
 __device__ __forceinline__ void tree_zero_refused(const TreeArgs& a) {
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {

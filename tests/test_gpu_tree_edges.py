@@ -1,0 +1,85 @@
+"""GPU tests of paged_attention_tree at the edges of what its calls allow: refused sequences, tables and pools of
+unusual layout, weights and scores at the ends of a type's range."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tree_cases import TreeCase
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _clean(cuda_lib):
+    cuda_lib.device_error_flags(clear=True)
+    yield
+    cuda_lib.set_checked_mode(False)
+    cuda_lib.device_error_flags(clear=True)
+
+
+def refused(pa, case, rows, flag, kernel, **change):
+    """The call over a buffer of sevens: zeros in `rows`, the fitting sequences' results elsewhere, sevens in none
+    of both."""
+    d = case.device()
+    good = pa.paged_attention_tree(**d, scale=case.scale, kernel=kernel, workspace=None)
+    qsl = change.pop("qsl", case.qsl.tolist())
+    kept = change.pop("kept")
+    d["query_start_loc"] = torch.tensor(qsl, dtype=torch.int32, device="cuda")
+    out = torch.full_like(d["q"], 7.0)
+    pa.paged_attention_tree(**d, scale=case.scale, kernel=kernel, out=out, workspace=None, **change)
+    assert pa.device_error_flags() == flag
+    for r in range(out.shape[0]):
+        want = torch.zeros_like(out[r]) if r in rows else good[r] if r in kept else torch.full_like(out[r], 7.0)
+        assert torch.equal(out[r], want), r
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_every_row_of_a_refused_sequence_is_zero(cuda_lib, kernel, dtype):
+    pa = cuda_lib
+    case = TreeCase(15, [64, 100, 3], [5, 7, 4], q_heads=4, kv_heads=2, head_dim=64, block_size=16, dtype=dtype, tail=4)
+    first, last = set(range(5)), set(range(12, 16))
+    # two nodes more than max_nodes
+    refused(pa, case, set(range(5, 12)), pa.PA_DEVERR_QUERY_LOC, kernel, kept=first | last, max_nodes=5)
+    # the last sequence reaches past the rows: those that it has
+    refused(pa, case, set(range(12, 20)), pa.PA_DEVERR_QUERY_LOC, kernel, kept=first | set(range(5, 12)),
+            qsl=[0, 5, 12, 23])
+    refused(pa, case, set(range(12, 20)), pa.PA_DEVERR_QUERY_LOC, kernel, kept=first | set(range(5, 12)),
+            qsl=[0, 5, 12, 2 ** 31 - 1])
+    # the first begins before them, and one that has none of them
+    refused(pa, case, first, pa.PA_DEVERR_QUERY_LOC, kernel, kept=set(range(5, 12)) | last, qsl=[-2, 5, 12, 16])
+    refused(pa, case, set(), pa.PA_DEVERR_QUERY_LOC, kernel, kept=first | set(range(5, 12)), qsl=[0, 5, 12, -9])
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_a_tree_wider_than_its_mask_gives_zeros(cuda_lib, kernel):
+    pa = cuda_lib
+    case = TreeCase(16, [40, 9], [70, 3], q_heads=4, kv_heads=2, head_dim=64, block_size=16, dtype=BF16, words=2)
+    d = case.device()
+    good = pa.paged_attention_tree(**d, scale=case.scale, kernel=kernel, workspace=None)
+    d["tree_mask"] = d["tree_mask"][:, :1].contiguous()
+    out = torch.full_like(good, 7.0)
+    pa.paged_attention_tree(**d, scale=case.scale, kernel=kernel, out=out, max_nodes=73, workspace=None)
+    assert pa.device_error_flags() == pa.PA_DEVERR_TREE
+    assert (out[:70] == 0).all() and torch.equal(out[70:], good[70:])
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_a_sequence_that_straddles_the_token_arrays(cuda_lib, kernel):
+    """What build_block_tables leaves of a sequence past its arrays, attention turns into zeros."""
+    pa = cuda_lib
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.full((3, 8), -1, dtype=torch.int32, device="cuda")
+    table[0, :1], table[1, :3], table[2, :1] = i32([0]), i32([1, 2, 3]), i32([4])
+    t = pa.build_block_tables(i32([16, 40, 3]), i32([3, 30, 5]), table, i32([1, 3, 1]), i32(list(range(5, 24))),
+                              i32([19, 0]), 16, 24, num_tokens=20)
+    assert pa.device_error_flags() == pa.PA_DEVERR_QUERY_LOC
+    k, v = (torch.randn((24, 16, 2, 64), device="cuda").to(BF16) for _ in range(2))
+    q = torch.randn((20, 4, 64), device="cuda").to(BF16)
+    out = torch.full_like(q, 7.0)
+    pa.paged_attention_tree(q, t.query_start_loc, None, k, v, table, t.context_lens, out=out, kernel=kernel)
+    assert pa.device_error_flags() == pa.PA_DEVERR_QUERY_LOC
+    assert (out[3:] == 0).all() and torch.isfinite(out).all() and not (out[:3] == 7.0).any() and (out[:3] != 0).any()
