@@ -329,7 +329,9 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *   opts            may be NULL.  kv_block_stride_bytes as for the decode call.  partition_tokens: keys
  *                   that a block of threads takes, rounded up to whole tiles of 64 or 128 (0 = an equal
  *                   share of the work); contexts are cut wherever such a share ends.  prefill_kernel:
- *                   0 auto (tcgen05 tensor cores for bf16/fp16 pools with block_size % 16 == 0, else 1),
+ *                   0 auto (tcgen05 tensor cores for bf16/fp16 pools with block_size % 16 == 0, else 1;
+ *                   tcgen05 rounds each softmax weight to the pool's type for the product with V, in fp16
+ *                   by at least 2^-32 of the row's largest, while its sum keeps 32 bits),
  *                   1 the kernel of every type and block size (mma.sync; weights are not rounded to the
  *                   pool's type, and fp32 values are split into bf16 parts that hold their 24 bits),
  *                   2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it).

@@ -49,6 +49,10 @@ namespace pa {
 // 12 warps: a thirteenth would leave 128 registers a thread
 constexpr int kTuThreads = 384;
 constexpr float kTuRescale = 8.f;
+// fp16 weights are formed 2^7 higher: the largest, 2^(8 + 7), still fits, and what the type's smallest step rounds
+// away of a weight is at most 2^-32 of the row's largest (unscaled 2^-25: 131,000 keys of that weight next to one
+// strong key lost 0.4 % of the result).  Sums and accumulators carry the factor alike and lose it in the quotient.
+constexpr float kTuLift = 7.f;
 
 template <int D, bool kWide>
 struct TuCfg {
@@ -112,7 +116,9 @@ __device__ __forceinline__ float tu_max(const uint32_t (&sv)[32], float top) {
 }
 
 // Weights 2^(s * sc - m) of 32 scores as 16-bit pairs into the 16 columns at taddr; their sum.  Weights are
-// rounded to the pool's type for the product with V (half a step each); the sum keeps 32 bits.
+// rounded to the pool's type for the product with V, as its tensor-core operand has to be (half a step each, so for
+// random values the output's error grows from one rounding's to two's: bf16 1.7e-3 -> 2.3e-3 of the result as root
+// mean squares); the sum keeps 32 bits.
 template <bool kBf16>
 __device__ __forceinline__ float tu_weights(uint32_t taddr, const uint32_t (&sv)[32], float sc, float m) {
   const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(-m, -m);
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
           corr = fast_exp2(m_use - top);  // m_use = -inf: 0
           m_use = top;
         }
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;
+        const float m_sub = m_use == -INFINITY ? 0.f : kBf16 ? m_use : m_use - kTuLift;
 #pragma unroll 1
         for (int h = 0; h <= last; ++h) {
           if (kKeys == 128 && h > 0) load(h);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from tree_cases import TreeCase
+from tree_cases import TreeCase, bound
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,69 @@ def test_a_sequence_that_straddles_the_token_arrays(cuda_lib, kernel):
     pa.paged_attention_tree(q, t.query_start_loc, None, k, v, table, t.context_lens, out=out, kernel=kernel)
     assert pa.device_error_flags() == pa.PA_DEVERR_QUERY_LOC
     assert (out[3:] == 0).all() and torch.isfinite(out).all() and not (out[:3] == 7.0).any() and (out[:3] != 0).any()
+
+
+def tight_bound(case, ref, spread, size, tensor_cores: bool):
+    """tree_cases.bound with two of its terms put right for fp16: a result is off by half a step of its type, and that
+    is never less than 2^-25; a weight that tensor cores round is off by half a step of itself, but at least by 2^-32
+    of the row's largest (they are formed 2^7 higher, and 2^-25 is the half step of the smallest numbers)."""
+    keys, values = int(case.ctx.max()), float(case.v[torch.isfinite(case.v)].abs().max())
+    half = torch.finfo(case.dtype).eps / 2
+    tol = bound(case.dtype, ref, spread, size, keys, case.q.shape[2], values, False)
+    if case.dtype == FP16:
+        tol = tol + 2.0 ** -25
+    if tensor_cores:
+        tol = tol + spread * half * (1 + half) ** 2
+        if case.dtype == FP16:
+            tol = tol + keys * 2.0 ** -32 * values * (1 + half)
+    return tol
+
+
+def check_tight(pa, case, kernel, **kw):
+    got = pa.paged_attention_tree(**case.device(), scale=case.scale, kernel=kernel, **kw)
+    rows, ref, spread, size = oracle.tree.paged_tree_attention(case.q, case.qsl, case.mask, case.k, case.v, case.table,
+                                                               case.ctx, case.scale)
+    tol = tight_bound(case, ref, spread, size, kernel != 1 and case.dtype != FP32)
+    off = np.abs(got.cpu().double().numpy()[rows] - ref) - tol
+    assert (off <= 0).all(), f"worst excess {off.max()} at {np.unravel_index(off.argmax(), off.shape)}"
+    assert pa.device_error_flags() == 0
+    return ref
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("strong", [0, 700, 4990])
+@pytest.mark.parametrize("part", [0, 8192])
+def test_many_weak_keys_next_to_a_strong_one(cuda_lib, kernel, m, strong, part):
+    """5,000 weights of 2^-25.5 of the largest, which fp16 numbers below 2^-24 cannot hold, make up the whole result."""
+    case = TreeCase(50, [4996], [m], q_heads=8, kv_heads=2, head_dim=64, block_size=16, dtype=FP16, words=0)
+    case.q = torch.ones_like(case.q)
+    token = ~torch.isnan(case.k)
+    case.k[token], case.v[token] = 0.0, 1.0
+    blk, tok = case.row_of(0, strong)
+    case.k[blk, tok] = 25.5 / (8 * 1.4426950408889634)  # 64 of them times the scale of 1/8
+    case.v[blk, tok] = 0.0
+    ref = check_tight(cuda_lib, case, kernel, partition_tokens=part)
+    assert (ref[0] > 5e-5).all() and (ref < 3e-4).all()
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("gain,size", [(1.0, 2.0 ** -9), (6.0, 1.0), (30.0, 2.0 ** -12)])
+def test_small_results_and_uneven_weights(cuda_lib, kernel, dtype, gain, size):
+    case = TreeCase(51, [700, 20, 0], [9, 60, 5], q_heads=8, kv_heads=2, head_dim=128, block_size=16, dtype=dtype, gain=gain)
+    case.v = (case.v.float() * size).to(dtype)
+    check_tight(cuda_lib, case, kernel)
+    check_tight(cuda_lib, case, kernel, partition_tokens=128)
+
+
+@pytest.mark.parametrize("m", [9, 60])
+def test_fp16_weights_at_their_largest(cuda_lib, m):
+    """The maximum grows by almost 2^8 within what moves no stabiliser, 64 keys at a time, under large values."""
+    case = TreeCase(52, [640], [m], q_heads=4, kv_heads=1, head_dim=64, block_size=16, dtype=FP16)
+    case.q = torch.ones_like(case.q)
+    for j in range(640 + m):
+        blk, tok = case.row_of(0, j)
+        case.k[blk, tok] = 7.9 / (8 * 1.4426950408889634) * (j // 64) / 2
+        case.v[blk, tok] = 60000.0
+    check_tight(cuda_lib, case, 0)
