@@ -2,8 +2,10 @@
 //
 // fp32 on bf16 tensor cores: x = x0 + x1 + x2, each part the bf16 rounding of what the ones before leave, holds
 // the 24 bits of x, and of the nine products of two split values the six with i + j <= 2 are formed (the others
-// come to at most 2^-23 of the product, of either sign).  fp16 values split into two parts and bf16 ones are their
-// own first part, both exactly; weights are split like fp32 values whatever the pool's type.  The tensor core adds
+// come to at most 2^-23 of the product, of either sign).  16-bit queries and keys are operands as they are (so that
+// the score of an infinite key is what it should be: a second part of infinity, or a product with it, would be NaN);
+// fp16 values of V split into two parts and bf16 ones are their own first part, both exactly, and weights are split
+// like fp32 values whatever the pool's type.  The tensor core adds
 // in fp32 but cuts off where it should round, so that one accumulator for a whole context loses its last bits one
 // after the other (28,000 keys: 5e-6 of the result).  For fp32 pools the products of 16 dimensions (S) or 16 keys
 // (P V) are therefore summed by themselves, small ones first, and added up by rounded additions (2e-7, for 4-6 %
@@ -42,10 +44,10 @@ constexpr int kTsWarps = 4;
 constexpr int kTsThreads = 32 * kTsWarps;
 
 template <typename T>
-struct Parts;  // bf16 parts that hold a value of T
-template <> struct Parts<__nv_bfloat16> { static constexpr int kN = 1; };
-template <> struct Parts<__half> { static constexpr int kN = 2; };
-template <> struct Parts<float> { static constexpr int kN = 3; };
+struct Parts;  // 16-bit parts of a query's or key's element, and the bf16 parts that hold one of V
+template <> struct Parts<__nv_bfloat16> { static constexpr int kScore = 1, kN = 1; };
+template <> struct Parts<__half> { static constexpr int kScore = 1, kN = 2; };
+template <> struct Parts<float> { static constexpr int kScore = 3, kN = 3; };
 
 template <typename T, int D, int kMT>
 struct TsCfg {
@@ -53,7 +55,7 @@ struct TsCfg {
   static constexpr int kKeys = kTreeSplitKeys;    // of a tile
   static constexpr int kWarpKeys = kKeys / kTsWarps;
   static constexpr int kSlot = kWarpKeys * D;         // floats of one K or V buffer
-  static constexpr int kQFrags = kMT * (D / 16) * Parts<T>::kN * 32;  // 16 bytes each
+  static constexpr int kQFrags = kMT * (D / 16) * Parts<T>::kScore * 32;  // 16 bytes each
   static constexpr int kSmemBytes = kQFrags * 16 + kTsWarps * 3 * kSlot * 4;
   static_assert(kRows * D <= 3 * kSlot && kWarpKeys == 16, "O in a ring, one step of 16 keys");
 };
@@ -109,11 +111,20 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&part)[kN]) {
   }
 }
 
+// Two elements of a query or key as operands of their own type (fp16) or in bf16 parts.
+template <typename T, int kN>
+__device__ __forceinline__ void split_score(float a, float b, uint32_t (&part)[kN]) {
+  if constexpr (std::is_same<T, __half>::value) part[0] = pack2<false>(a, b);
+  else split2<kN>(a, b, part);
+}
+
 template <typename T, int D, int kMT>
 __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_kernel(const TreeArgs a) {
   using Cfg = TsCfg<T, D, kMT>;
   constexpr int kKeys = Cfg::kKeys, kWK = Cfg::kWarpKeys, kRows = Cfg::kRows, kSlot = Cfg::kSlot;
-  constexpr int kN = Parts<T>::kN;       // parts of q, k and v
+  constexpr int kS = Parts<T>::kScore;   // parts of q and k
+  constexpr int kN = Parts<T>::kN;       // parts of v
+  constexpr bool kScoreBf16 = !std::is_same<T, __half>::value;
   constexpr bool kFresh = kN == 3;       // sums of a step's products on their own first
   constexpr int kNT = kWK / 8;           // score tiles of 8 keys
   constexpr int kKD = D / 16;            // steps of 16 dimensions
@@ -215,13 +226,13 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
         const int r = 16 * mt + 8 * h + (l >> 2);
         if (r < w.rows) read4(static_cast<const T*>(a.q) + out_row(r) * D + 16 * step + 4 * (l & 3), f[h]);
       }
-      uint32_t p0[kN], p1[kN], p2[kN], p3[kN];
-      split2<kN>(f[0][0], f[0][1], p0);
-      split2<kN>(f[1][0], f[1][1], p1);
-      split2<kN>(f[0][2], f[0][3], p2);
-      split2<kN>(f[1][2], f[1][3], p3);
+      uint32_t p0[kS], p1[kS], p2[kS], p3[kS];
+      split_score<T>(f[0][0], f[0][1], p0);
+      split_score<T>(f[1][0], f[1][1], p1);
+      split_score<T>(f[0][2], f[0][3], p2);
+      split_score<T>(f[1][2], f[1][3], p3);
 #pragma unroll
-      for (int p = 0; p < kN; ++p) qf[((mt * kKD + step) * kN + p) * 32 + l] = make_uint4(p0[p], p1[p], p2[p], p3[p]);
+      for (int p = 0; p < kS; ++p) qf[((mt * kKD + step) * kS + p) * 32 + l] = make_uint4(p0[p], p1[p], p2[p], p3[p]);
     }
     __syncthreads();
 
@@ -257,19 +268,19 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
       const float4* const kc = reinterpret_cast<const float4*>(kt);
 #pragma unroll
       for (int step = 0; step < kKD; ++step) {
-        uint4 q[kMT][kN];
+        uint4 q[kMT][kS];
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-          for (int p = 0; p < kN; ++p) q[mt][p] = qf[((mt * kKD + step) * kN + p) * 32 + lane];
+          for (int p = 0; p < kS; ++p) q[mt][p] = qf[((mt * kKD + step) * kS + p) * 32 + lane];
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
           // column g of score tile n is key 16 (n / 2) + 4 (g / 2) + g % 2 + 2 (n % 2)
           const int key = 16 * (n >> 1) + 4 * (g >> 1) + (g & 1) + 2 * (n & 1);
           const float4 k = kc[k_chunk(key, 4 * step + t)];
-          uint32_t b0[kN], b1[kN];
-          split2<kN>(k.x, k.y, b0);
-          split2<kN>(k.z, k.w, b1);
+          uint32_t b0[kS], b1[kS];
+          split_score<T>(k.x, k.y, b0);
+          split_score<T>(k.z, k.w, b1);
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt) {
             float part[4] = {0.f, 0.f, 0.f, 0.f};
@@ -277,9 +288,9 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
 #pragma unroll
             for (int d = 2; d >= 0; --d)  // small products first
 #pragma unroll
-              for (int i = 0; i < kN; ++i)
-                if (i <= d && d - i < kN)
-                  mma_16816<true>(f, q[mt][i].x, q[mt][i].y, q[mt][i].z, q[mt][i].w, b0[d - i], b1[d - i]);
+              for (int i = 0; i < kS; ++i)
+                if (i <= d && d - i < kS)
+                  mma_16816<kScoreBf16>(f, q[mt][i].x, q[mt][i].y, q[mt][i].z, q[mt][i].w, b0[d - i], b1[d - i]);
 #pragma unroll
             for (int e = 0; kFresh && e < 4; ++e) s[mt][n][e] += part[e];
           }

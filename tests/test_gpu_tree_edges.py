@@ -149,3 +149,25 @@ def test_fp16_weights_at_their_largest(cuda_lib, m):
         case.k[blk, tok] = 7.9 / (8 * 1.4426950408889634) * (j // 64) / 2
         case.v[blk, tok] = 60000.0
     check_tight(cuda_lib, case, 0)
+
+
+@pytest.mark.parametrize("kernel,S", [(0, 16), (1, 16), (0, 4)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("part", [0, 64])
+def test_a_seen_key_whose_score_is_minus_infinity_has_no_weight(cuda_lib, kernel, S, dtype, part):
+    """Results as if no row saw the key, whatever the block size."""
+    case = TreeCase(53, [90, 3, 128], [20, 50, 64], q_heads=8, kv_heads=2, head_dim=64, block_size=S, dtype=dtype)
+    case.q = case.q.abs() + 0.5
+    for b in range(3):
+        blk, tok = case.row_of(b, case.hist[b] + 7)
+        case.k[blk, tok] = -float("inf")
+    sevens = (case.mask[:, 0] >> 7) & 1
+    assert sevens.any() and not sevens.all()
+    got = cuda_lib.paged_attention_tree(**case.device(), scale=case.scale, kernel=kernel, partition_tokens=part)
+    case.mask[:, 0] &= ~(1 << 7)
+    case.k = torch.nan_to_num(case.k, neginf=0.0)
+    rows, ref, spread, size = oracle.tree.paged_tree_attention(case.q, case.qsl, case.mask, case.k, case.v, case.table,
+                                                               case.ctx, case.scale)
+    tol = tight_bound(case, ref, spread, size, kernel == 0 and S == 16)
+    assert (np.abs(got.cpu().double().numpy()[rows] - ref) <= tol).all()
+    assert cuda_lib.device_error_flags() == 0
