@@ -456,13 +456,14 @@ def _vec(t, name: str, dtype, dev: int, n: int) -> int:
 
 
 def _table(t, name: str, rows: int, dev: int) -> tuple:
-    """(pointer, row stride, columns) of an int32 [rows, columns] tensor whose rows are contiguous."""
+    """(pointer, row stride, columns) of an int32 [rows, columns] tensor whose rows are contiguous.  (The stride of a
+    dimension of size 1 means nothing: an [n, 1] tensor transposed has 1 there.)"""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != rows or (stride[1] != 1 and rows and shape[1]):
         raise ValueError(f"{name} must be [batch, entries] with contiguous rows")
     if t.dtype is not _I32 or t.get_device() != dev or dev < 0:
         _refuse(t, name, _I32, dev, None)
-    return t.data_ptr(), stride[0], shape[1]
+    return t.data_ptr(), stride[0] if rows != 1 else shape[1], shape[1]
 
 
 def _pools(k, v, dev: int, lead: int = 0) -> tuple:

@@ -171,3 +171,36 @@ def test_a_seen_key_whose_score_is_minus_infinity_has_no_weight(cuda_lib, kernel
     tol = tight_bound(case, ref, spread, size, kernel == 0 and S == 16)
     assert (np.abs(got.cpu().double().numpy()[rows] - ref) <= tol).all()
     assert cuda_lib.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_one_sequence_with_a_transposed_table(cuda_lib, kernel):
+    """A [1, n] table is contiguous whatever its first stride says."""
+    pa = cuda_lib
+    case = TreeCase(54, [300], [9], q_heads=4, kv_heads=2, head_dim=64, block_size=16, dtype=BF16)
+    d = case.device()
+    d["block_table"] = d["block_table"][0].clone()[:, None].t()
+    assert d["block_table"].stride() == (1, 1) and d["block_table"].shape[1] > 1
+    out = pa.paged_attention_tree(**d, scale=case.scale, kernel=kernel)
+    assert pa.device_error_flags() == 0
+    rows, ref, spread, size = oracle.tree.paged_tree_attention(case.q, case.qsl, case.mask, case.k, case.v, case.table,
+                                                               case.ctx, case.scale)
+    tol = tight_bound(case, ref, spread, size, kernel == 0)
+    assert (np.abs(out.cpu().double().numpy()[rows] - ref) <= tol).all()
+
+
+def test_one_sequence_with_transposed_tables_in_the_rest_of_the_step(cuda_lib):
+    pa = cuda_lib
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = i32([[5], [3], [0], [-1], [-1]]).t()
+    assert table.stride() == (1, 1)
+    t = pa.build_block_tables(i32([40]), i32([20]), table, i32([3]), i32([1, 2, 4]), i32([3, 0]), 16, 6, num_tokens=20)
+    assert table.cpu().tolist() == [[5, 3, 0, 4, -1]]
+    p = np.arange(40, 60)
+    assert np.array_equal(t.slot_mapping.cpu().numpy(), np.array([5, 3, 0, 4])[p // 16] * 16 + p % 16)
+    k, v = (torch.randn((6, 16, 2, 64), device="cuda") for _ in range(2))
+    accepted = i32([[2], [9], [18]]).t()
+    want = oracle.tree.paged_kv_accept(k.cpu(), v.cpu(), accepted.cpu(), i32([3]).cpu(), i32([40]).cpu(), table.cpu())
+    pa.paged_kv_accept(k, v, accepted, i32([3]), i32([40]), table)
+    assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
+    assert pa.device_error_flags() == 0
