@@ -534,12 +534,6 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
                              torch.empty(T, dtype=torch.int64, device=d),
                              torch.empty(T, dtype=torch.int32, device=d),
                              torch.empty((T, words), dtype=torch.int64, device=d) if parents is not None else None)
-        if B == 0:
-            out.query_start_loc.zero_()
-            out.slot_mapping.fill_(-1)
-            out.positions.zero_()
-            if out.tree_mask is not None:
-                out.tree_mask.zero_()
     qsl, ctx, slots, pos, mask = out
     T, words, par, msk = slots.numel(), 0, None, None
     if num_tokens is not None and num_tokens != T:
@@ -565,7 +559,25 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
             st = lib.build_block_tables(*args)
     if st:
         _check("build_block_tables", st)
+    if B == 0:
+        _fill_empty_step(out, stream, dev)
     return out
+
+
+def _fill_empty_step(out: StepTables, stream, dev: int):
+    """The arrays of a step without sequences, for which the library does nothing: every token row lies behind the
+    last sequence."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif not isinstance(stream, torch.cuda.Stream):
+        ptr = int(stream)  # (0 is no external stream but the default one)
+        stream = torch.cuda.ExternalStream(ptr, device=dev) if ptr else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        out.query_start_loc.zero_()
+        out.slot_mapping.fill_(-1)
+        out.positions.zero_()
+        if out.tree_mask is not None:
+            out.tree_mask.zero_()
 
 
 @functools.lru_cache(maxsize=1024)

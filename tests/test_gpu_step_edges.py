@@ -1,0 +1,61 @@
+"""GPU tests of the step calls at the edges of what they allow: empty batches, chains of launches without another kernel
+between them, views whose rows end with their memory."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _clean(cuda_lib):
+    cuda_lib.device_error_flags(clear=True)
+    yield
+    cuda_lib.set_checked_mode(False)
+    cuda_lib.device_error_flags(clear=True)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("trees", [False, True])
+@pytest.mark.parametrize("where", ["current", "stream", "raw", "default"])
+def test_an_empty_batch_leaves_no_step_behind(cuda_lib, trees, where):
+    """Arrays of an earlier step, written again for no sequences: no slot of that step is left, and what the call writes
+    it writes in the order of its stream."""
+    pa = cuda_lib
+    table = torch.full((2, 8), -1, dtype=torch.int32, device="cuda")
+    free, state = i32(list(range(16))), i32([16, 0])
+    parents = i32([-1, 0, 1, -1, 0, 0, 0, 0, 0]) if trees else None
+    t = pa.build_block_tables(i32([0, 0]), i32([3, 4]), table, i32([0, 0]), free, state, 16, 16, num_tokens=9, parents=parents)
+    assert (t.slot_mapping[:7] >= 0).all()
+    none = i32([])
+    out = t._replace(query_start_loc=t.query_start_loc[:1], context_lens=t.context_lens[:0])
+    torch.cuda.synchronize()
+    side = torch.cuda.default_stream() if where == "default" else torch.cuda.Stream()
+    if where != "current":
+        with torch.cuda.stream(side):  # some 10 ms of waiting, then another writer of the same arrays
+            torch.cuda._sleep(20_000_000)
+            t.slot_mapping.fill_(77)
+            t.query_start_loc.fill_(9)
+    stream = {"current": None, "stream": side, "raw": side.cuda_stream, "default": 0}[where]
+    with torch.cuda.stream(torch.cuda.Stream() if where == "default" else torch.cuda.current_stream()):
+        got = pa.build_block_tables(none, none, table[:0], none, free, state, 16, 16, parents=parents, out=out, stream=stream)
+        fresh = pa.build_block_tables(none, none, table[:0], none, free, state, 16, 16, num_tokens=9, parents=parents,
+                                      stream=stream)
+    torch.cuda.synchronize()
+    assert got is out
+    for o in (got, fresh):
+        assert o.query_start_loc.cpu().tolist() == [0] and o.context_lens.numel() == 0
+        assert (o.slot_mapping == -1).all() and (o.positions == 0).all() and o.slot_mapping.numel() == 9
+        assert (o.tree_mask is not None) == trees and (not trees or (o.tree_mask == 0).all())
+    assert state.cpu().tolist() == [15 - 1, 0] and pa.device_error_flags() == 0
+    pool = torch.zeros((2, 16, 16, 1, 64), device="cuda")
+    new = torch.ones((9, 1, 64), device="cuda")
+    pa.paged_kv_write(new, new, got.slot_mapping, pool[0], pool[1])
+    assert (pool == 0).all()
