@@ -317,7 +317,7 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *   max_nodes       bound on m_b, >= 1 (it sizes the launch)
  *   context_lens    int32 [batch]: history + m_b.  The keys and values of the nodes are the last m_b
  *                   positions of the context, in node order, already written.
- *   scale           finite and > 0
+ *   scale           > 0, and finite times log2(e) as well (at most 2.35e38)
  *   out[r][i] = sum_j softmax_j(scale * q[r][i] . K_j) V_j over the keys node r sees.  A row that sees
  *   nothing gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and
  *   NaN included); a non-finite value that it sees gives non-finite outputs, a non-finite key those of its

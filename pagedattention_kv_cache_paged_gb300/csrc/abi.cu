@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <mutex>
 #include <unordered_set>
@@ -654,7 +655,8 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   if (batch < 0 || total_q < 0 || num_blocks <= 0 || block_table_stride <= 0 || block_size <= 0 || max_nodes < 1)
     return PA_EINVAL;
   if (!is_pow2(block_size) || block_size > 256) return PA_EUNSUPPORTED;
-  if (!(scale > 0.f) || scale > 3.0e38f) return PA_EINVAL;
+  const float scale_log2 = scale * 1.4426950408889634f;  // (what the kernels hold of it; infinity would make 0 NaN)
+  if (!(scale > 0.f) || !std::isfinite(scale_log2)) return PA_EINVAL;
   if (tree_mask && (mask_words < 1 || mask_words > (INT32_MAX >> 6))) return PA_EINVAL;
   if (batch == 0 || total_q == 0) return PA_OK;
   if (total_q > INT32_MAX) return PA_EINVAL;
@@ -704,7 +706,7 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.block_size = block_size;
   a.block_shift = log2i(block_size);
   a.kv_block_stride = stride_bytes / dtype_bytes(dtype);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.n_q_heads = n_q_heads;
   a.n_kv_heads = n_kv_heads;
   a.group = group;
