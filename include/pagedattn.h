@@ -315,7 +315,7 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *                   at most 64 * mask_words.  NULL: the drafted tokens form a chain, each seeing the
  *                   ones before it and itself (mask_words is ignored).
  *   max_nodes       bound on m_b, >= 1 (it sizes the launch)
- *   context_lens    int32 [batch]: history + m_b.  The keys and values of the nodes are the last m_b
+ *   context_lens    int32 [batch]: history + m_b, at most 2^31 - 4096.  The keys and values of the nodes are the last m_b
  *                   positions of the context, in node order, already written.
  *   scale           > 0, and finite times log2(e) as well (at most 2.35e38)
  *   out[r][i] = sum_j softmax_j(scale * q[r][i] . K_j) V_j over the keys node r sees.  A row that sees
@@ -336,7 +336,7 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *                   pool's type, and fp32 values are split into bf16 parts that hold their 24 bits),
  *                   2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it).
  * A sequence whose rows are out of order, reach past total_q, are more than max_nodes or 64 * mask_words,
- * or more than its context, or whose context is negative or longer than its table row, gives zeros in all
+ * or more than its context, or whose context is negative, longer than its table row or too long, gives zeros in all
  * the rows it has among total_q (rows that an unordered query_start_loc gives to two sequences hold either's)
  * and is recorded as PA_DEVERR_QUERY_LOC (or PA_DEVERR_TREE, PA_DEVERR_CONTEXT_LEN); checked mode returns
  * PA_ERANGE.  A batch whose tables allow 2^30 key tiles or more in all

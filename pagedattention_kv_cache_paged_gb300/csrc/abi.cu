@@ -684,7 +684,7 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
     if (qsl[0] < 0 || qsl[(size_t)batch] > total_q) return PA_ERANGE;
     for (int b = 0; b < batch; ++b) {
       const int64_t m = (int64_t)qsl[(size_t)b + 1] - qsl[(size_t)b];
-      if (m < 0 || m > max_nodes || m > lens[(size_t)b]) return PA_ERANGE;
+      if (m < 0 || m > max_nodes || m > lens[(size_t)b] || lens[(size_t)b] > kTreeMaxContext) return PA_ERANGE;
       if (tree_mask && m > (int64_t)64 * mask_words) return PA_ERANGE;
     }
   }

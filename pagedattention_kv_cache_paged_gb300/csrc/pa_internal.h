@@ -195,6 +195,8 @@ struct TreeRec {
 inline int tree_unit_rows(int max_nodes, int group) { return (int64_t)max_nodes * group <= 128 ? 128 : 256; }
 constexpr int tree_tile_keys(int head_dim, int unit_rows) { return head_dim == 64 || unit_rows == 256 ? 128 : 64; }
 constexpr int kTreeGap = 3, kTreeMinShare = 8;
+// Longest context: positions are int32, and a lane looks up to two tiles and 31 boxes of 64 keys past its tile's start.
+constexpr int32_t kTreeMaxContext = INT32_MAX - 4095;
 // mma.sync: one or two m16 tiles of rows; four warps take 16 keys of a tile each; CTAs per SM.
 inline int tree_split_rows(int max_nodes, int group, int head_dim) {
   return (int64_t)max_nodes * group <= 16 || head_dim == 128 ? 16 : 32;

@@ -24,7 +24,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   } else {
     if (q1 - q0 > a.max_nodes || s.n < q1 - q0) s.bad |= PA_DEVERR_QUERY_LOC;
     if (a.tree_mask != nullptr && q1 - q0 > (int64_t)64 * a.mask_words) s.bad |= PA_DEVERR_TREE;
-    if (s.n < 0 || s.n > (a.bt_stride << a.block_shift)) s.bad |= PA_DEVERR_CONTEXT_LEN;
+    if (s.n < 0 || s.n > (a.bt_stride << a.block_shift) || s.n > kTreeMaxContext) s.bad |= PA_DEVERR_CONTEXT_LEN;
   }
   if (s.bad) {
     s.n = 0;

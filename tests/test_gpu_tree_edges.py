@@ -204,3 +204,21 @@ def test_one_sequence_with_transposed_tables_in_the_rest_of_the_step(cuda_lib):
     pa.paged_kv_accept(k, v, accepted, i32([3]), i32([40]), table)
     assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
     assert pa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("m", [2, 70])
+def test_the_longest_contexts(cuda_lib, kernel, m):
+    """Tables of 2^31 tokens that name the same block over and over, keys all alike, values all 1, so that every sum is a
+    whole number and the result 1: 2^31 - 4096 tokens are attended, one more is refused."""
+    pa = cuda_lib
+    k = torch.ones((1, 256, 1, 64), dtype=BF16, device="cuda")
+    q = torch.ones((m, 2, 64), dtype=BF16, device="cuda")
+    table = torch.zeros((1, 2 ** 23), dtype=torch.int32, device="cuda")
+    qsl = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    for n, flag in ((2 ** 31 - 1, pa.PA_DEVERR_CONTEXT_LEN), (2 ** 31 - 4095, pa.PA_DEVERR_CONTEXT_LEN), (2 ** 31 - 4096, 0)):
+        out = torch.full_like(q, 7.0)
+        ctx = torch.tensor([n], dtype=torch.int32, device="cuda")
+        pa.paged_attention_tree(q, qsl, None, k, k, table, ctx, out=out, kernel=kernel)
+        assert pa.device_error_flags() == flag
+        assert (out == (0.0 if flag else 1.0)).all()
