@@ -156,12 +156,17 @@ int validate_tables(const int32_t* block_table, int64_t bt_stride, const int32_t
   std::vector<int32_t> lens, table;
   int rc = copy_to_host(lens, context_lens, batch, s);
   if (rc) return rc;
-  rc = copy_to_host(table, block_table, (int64_t)batch * bt_stride, s);
-  if (rc) return rc;
+  // (the last row of a view may end before its stride does: nothing is read that no context reaches)
+  int64_t reach = 0;
   for (int b = 0; b < batch; ++b) {
     const int64_t n = lens[b];
     if (n < 0 || n > bt_stride * block_size) return PA_ERANGE;
-    const int64_t nb = (n + block_size - 1) / block_size;
+    if (n > 0) reach = b * bt_stride + (n + block_size - 1) / block_size;
+  }
+  rc = copy_to_host(table, block_table, reach, s);
+  if (rc) return rc;
+  for (int b = 0; b < batch; ++b) {
+    const int64_t nb = ((int64_t)lens[b] + block_size - 1) / block_size;
     for (int64_t j = 0; j < nb; ++j) {
       const int64_t id = table[(size_t)(b * bt_stride + j)];
       if (id < 0 || id >= num_blocks) return PA_ERANGE;
@@ -759,7 +764,9 @@ int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride
     if ((rc = copy_to_host(acc_lens, accepted_lens, batch, s))) return rc;
     if ((rc = copy_to_host(hist, history_lens, batch, s))) return rc;
     if ((rc = copy_to_host(acc, accepted, (int64_t)(batch - 1) * accepted_stride + max_accepted, s))) return rc;
-    if ((rc = copy_to_host(table, block_table, (int64_t)batch * block_table_stride, s))) return rc;
+    // table entries of the rows that move, and how far into the tables they reach (see validate_tables)
+    std::vector<int64_t> entries;
+    int64_t reach = 0;
     for (int b = 0; b < batch; ++b) {
       if (acc_lens[(size_t)b] < 0 || acc_lens[(size_t)b] > max_accepted || hist[(size_t)b] < 0) return PA_ERANGE;
       for (int i = 0; i < acc_lens[(size_t)b]; ++i) {
@@ -767,11 +774,14 @@ int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride
         const int64_t src = hist[(size_t)b] + idx, dst = hist[(size_t)b] + i;
         if (idx < i || src >= block_table_stride * block_size) return PA_ERANGE;
         for (const int64_t p : {src, dst}) {
-          const int32_t id = table[(size_t)(b * block_table_stride + p / block_size)];
-          if (id < 0 || id >= num_blocks) return PA_ERANGE;
+          entries.push_back(b * block_table_stride + p / block_size);
+          reach = reach > entries.back() ? reach : entries.back() + 1;
         }
       }
     }
+    if ((rc = copy_to_host(table, block_table, reach, s))) return rc;
+    for (const int64_t e : entries)
+      if (table[(size_t)e] < 0 || table[(size_t)e] >= num_blocks) return PA_ERANGE;
   }
   AcceptArgs a{};
   a.k_pool = k_pool;

@@ -59,3 +59,39 @@ def test_an_empty_batch_leaves_no_step_behind(cuda_lib, trees, where):
     new = torch.ones((9, 1, 64), device="cuda")
     pa.paged_kv_write(new, new, got.slot_mapping, pool[0], pool[1])
     assert (pool == 0).all()
+
+
+def test_checked_mode_reads_no_further_than_the_rows_of_a_view(cuda_lib):
+    """Tables whose last row ends with its memory, though the stride of a row does not."""
+    pa = cuda_lib
+    torch.cuda.empty_cache()
+    wide = torch.full((2, 10 * 2 ** 18), -9, dtype=torch.int32, device="cuda")  # 20 MiB, a segment of its own
+    table = wide[:, 8:]
+    table[:, :3] = i32([[0, 1, 2], [3, 4, 5]])
+    lists = torch.full((2, 10 * 2 ** 18), -9, dtype=torch.int32, device="cuda")[:, -4:]
+    lists[:, :2] = i32([[0, 3], [1, 2]])
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn((6, 16, 2, 64), generator=g) for _ in range(2))
+    q = torch.randn((8, 4, 64), generator=g)
+    hist, ctx, qsl = i32([30, 40]), i32([34, 44]), i32([0, 4, 8])
+    dk, dv = k.cuda(), v.cuda()
+    pa.set_checked_mode(True)
+    out = pa.paged_attention_tree(q.cuda(), qsl, None, dk, dv, table, ctx)
+    pa.paged_kv_accept(dk, dv, lists, i32([2, 2]), hist, table)
+    torch.cuda.synchronize()
+    pa.set_checked_mode(False)
+    small = table[:, :3].cpu()
+    ref = oracle.tree.paged_tree_attention(q, qsl.cpu(), None, k, v, small, ctx.cpu(), 0.125)[1]
+    # (a score of 64 products of order 1, weights and sums of 44 keys, in 32 bits: below 2^-24 * 4 * (64 + 44) times
+    # values of 4)
+    assert np.abs(out.cpu().double().numpy() - ref).max() < 2.0 ** -24 * 4 * 108 * 4
+    want = oracle.tree.paged_kv_accept(k, v, lists.cpu(), i32([2, 2]).cpu(), hist.cpu(), small)
+    assert torch.equal(dk.cpu(), want[0]) and torch.equal(dv.cpu(), want[1])
+    # and what is wrong is found: an entry inside a context, an entry of a moved row
+    table[1, 2] = 6
+    pa.set_checked_mode(True)
+    for call in (lambda: pa.paged_attention_tree(q.cuda(), qsl, None, dk, dv, table, ctx),
+                 lambda: pa.paged_kv_accept(dk, dv, lists, i32([2, 2]), hist, table)):
+        with pytest.raises(pa.PagedAttnError) as e:
+            call()
+        assert e.value.status == pa.PA_ERANGE
