@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <exception>
 #include <mutex>
 #include <unordered_set>
 #include <vector>
@@ -143,7 +144,11 @@ int check_heads(int n_q_heads, int n_kv_heads, int head_dim) {
 
 template <typename T>
 int copy_to_host(std::vector<T>& dst, const T* src, int64_t n, cudaStream_t s) {
-  dst.resize((size_t)n);
+  try {
+    dst.resize((size_t)n);
+  } catch (const std::exception&) {  // (no exception may leave a C entry)
+    return fail_cuda(cudaErrorMemoryAllocation);
+  }
   if (n == 0) return PA_OK;
   cudaError_t e = cudaMemcpyAsync(dst.data(), src, sizeof(T) * (size_t)n, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
@@ -764,24 +769,27 @@ int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride
     if ((rc = copy_to_host(acc_lens, accepted_lens, batch, s))) return rc;
     if ((rc = copy_to_host(hist, history_lens, batch, s))) return rc;
     if ((rc = copy_to_host(acc, accepted, (int64_t)(batch - 1) * accepted_stride + max_accepted, s))) return rc;
-    // table entries of the rows that move, and how far into the tables they reach (see validate_tables)
-    std::vector<int64_t> entries;
-    int64_t reach = 0;
+    int64_t reach = 0;  // how far into the tables the rows that move reach (see validate_tables)
     for (int b = 0; b < batch; ++b) {
       if (acc_lens[(size_t)b] < 0 || acc_lens[(size_t)b] > max_accepted || hist[(size_t)b] < 0) return PA_ERANGE;
       for (int i = 0; i < acc_lens[(size_t)b]; ++i) {
         const int64_t idx = acc[(size_t)(b * accepted_stride + i)];
-        const int64_t src = hist[(size_t)b] + idx, dst = hist[(size_t)b] + i;
+        const int64_t src = hist[(size_t)b] + idx;
         if (idx < i || src >= block_table_stride * block_size) return PA_ERANGE;
-        for (const int64_t p : {src, dst}) {
-          entries.push_back(b * block_table_stride + p / block_size);
-          reach = reach > entries.back() ? reach : entries.back() + 1;
-        }
+        const int64_t end = b * block_table_stride + src / block_size + 1;  // (dst does not lie behind src)
+        reach = reach > end ? reach : end;
       }
     }
     if ((rc = copy_to_host(table, block_table, reach, s))) return rc;
-    for (const int64_t e : entries)
-      if (table[(size_t)e] < 0 || table[(size_t)e] >= num_blocks) return PA_ERANGE;
+    for (int b = 0; b < batch; ++b) {
+      for (int i = 0; i < acc_lens[(size_t)b]; ++i) {
+        const int64_t src = (int64_t)hist[(size_t)b] + acc[(size_t)(b * accepted_stride + i)];
+        for (const int64_t p : {src, (int64_t)hist[(size_t)b] + i}) {
+          const int32_t id = table[(size_t)(b * block_table_stride + p / block_size)];
+          if (id < 0 || id >= num_blocks) return PA_ERANGE;
+        }
+      }
+    }
   }
   AcceptArgs a{};
   a.k_pool = k_pool;

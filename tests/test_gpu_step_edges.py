@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import oracle
+from pagedattention_kv_cache_paged_gb300 import _abi
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,14 @@ def test_checked_mode_reads_no_further_than_the_rows_of_a_view(cuda_lib):
         with pytest.raises(pa.PagedAttnError) as e:
             call()
         assert e.value.status == pa.PA_ERANGE
+
+
+def test_checked_mode_without_memory_for_its_copy_returns(cuda_lib):
+    """A list stride that no memory holds: an error code, and no exception out of the library."""
+    pa = cuda_lib
+    p = torch.zeros(2 ** 16, dtype=torch.int32, device="cuda").data_ptr()
+    pa.set_checked_mode(True)
+    before = pa.launch_count()
+    assert pa.load_library().paged_kv_accept(p, p, 1, 0, p, 2 ** 61, 4, p, p, p, 8, 2, 4, 16, 1, 64, pa.PA_FP32, None,
+                                             None) == _abi.PA_ECUDA
+    assert pa.launch_count() == before
