@@ -350,7 +350,7 @@ PA_API int paged_attention_tree(void* out, const void* q, const int32_t* query_s
                                 void* workspace, size_t workspace_bytes, const pa_opts* opts, void* stream);
 
 /* Workspace bytes paged_attention_tree needs to split contexts as long as the table allows, on the
- * current device (0 if it does not split).  Invalid sizes give 0. */
+ * current device (0 if it does not split).  What the call refuses gives 0. */
 PA_API size_t paged_attention_tree_workspace_size(int batch, int64_t total_q, int max_nodes,
                                                   int64_t block_table_stride, int block_size, int n_q_heads,
                                                   int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts);

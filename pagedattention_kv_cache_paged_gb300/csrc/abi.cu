@@ -639,17 +639,18 @@ TreePlan plan_tree_call(const pa_opts& o, int batch, int max_nodes, int n_q_head
 
 size_t tree_workspace_impl(int batch, int64_t total_q, int max_nodes, int64_t block_table_stride, int block_size,
                            int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts) {
-  if (batch <= 0 || total_q <= 0 || max_nodes <= 0 || block_table_stride <= 0 || block_size <= 0 || n_q_heads <= 0 ||
-      n_kv_heads <= 0 || head_dim <= 0 || check_dtype(dtype) || check_heads(n_q_heads, n_kv_heads, head_dim))
+  if (batch <= 0 || total_q <= 0 || max_nodes <= 0 || block_table_stride <= 0 || !is_pow2(block_size) ||
+      block_size > 256 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || check_dtype(dtype) ||
+      check_heads(n_q_heads, n_kv_heads, head_dim))
     return 0;
   pa_opts o;
   if (read_opts(opts, &o)) return 0;
   int sms = 0;
   if (device_info(nullptr, &sms)) return 0;
   if (max_nodes > total_q) max_nodes = (int)total_q;
-  return plan_tree_call(o, batch, max_nodes, n_q_heads, n_kv_heads, head_dim, dtype, sms, 1, block_table_stride,
-                        block_size)
-      .bytes;
+  const TreePlan plan = plan_tree_call(o, batch, max_nodes, n_q_heads, n_kv_heads, head_dim, dtype, sms, 1,
+                                       block_table_stride, block_size);
+  return o.prefill_kernel == 2 && !plan.tensor_cores ? 0 : plan.bytes;
 }
 
 int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q, const int64_t* tree_mask,

@@ -127,3 +127,13 @@ def test_workspace_sizes(cuda_lib):
         bad = list(good)
         bad[i] = wrong
         assert lib.paged_attention_tree_workspace_size(*bad, None) == 0, (i, wrong)
+
+
+def test_workspace_sizes_of_refused_blocks_and_kernels(cuda_lib):
+    pa = cuda_lib
+    size = lambda S, dtype, kernel: pa.tree_workspace_size(2, 8, 4, 512, S, 8, 2, 64, dtype, kernel=kernel)
+    for S in (3, 12, 24, 512):
+        assert size(S, torch.bfloat16, 0) == 0, S
+    assert size(8, torch.bfloat16, 0) > 0 and size(8, torch.bfloat16, 2) == 0
+    assert size(16, torch.float32, 0) > 0 and size(16, torch.float32, 2) == 0
+    assert size(16, torch.bfloat16, 2) > 0
