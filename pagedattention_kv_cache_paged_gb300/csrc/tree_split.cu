@@ -253,8 +253,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
       float* const vt = ring + (slot == 2 ? 0 : slot + 1) * kSlot;
       const int kb = x * kKeys + warp * kWK;
       const unsigned have = __ballot_sync(0xffffffffu, off >= 0);  // keys of the tile with data
-      const unsigned full = kWK == 32 ? 0xffffffffu : (1u << (kWK & 31)) - 1u;
-      const bool edge = kb + kWK > hist || have != full;
+      const bool edge = kb + kWK > hist || have != (1u << kWK) - 1u;
       const int64_t off_after = locate(x + 2);
       cp_async_wait<2>();
       __syncwarp();
