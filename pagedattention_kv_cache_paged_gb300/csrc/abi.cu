@@ -545,7 +545,8 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
     return PA_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned* err = nullptr;
-  int rc = device_info(&err, nullptr);
+  int sms = 0;
+  int rc = device_info(&err, &sms);
   if (rc) return rc;
   TablesArgs a{};
   a.history_lens = history_lens;
@@ -573,7 +574,7 @@ int block_tables_impl(const int32_t* history_lens, const int32_t* new_lens, int 
   a.err = err;
   if (checked() && (rc = validate_tables_step(a, s))) return rc;
   int launches = 0;
-  cudaError_t e = launch_block_tables(a, s, &launches);
+  cudaError_t e = launch_block_tables(a, sms, s, &launches);
   return finish(e, launches);
 }
 

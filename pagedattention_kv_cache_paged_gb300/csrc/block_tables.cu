@@ -292,13 +292,13 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const TablesAr
   }
 }
 
-cudaError_t launch_block_tables(const TablesArgs& a, cudaStream_t s, int* launches) {
+cudaError_t launch_block_tables(const TablesArgs& a, int sms, cudaStream_t s, int* launches) {
   // One CTA while its threads have a group of four tokens each (with trees one); then as many CTAs as keep
   // that up, two per SM at most, in whole groups.
   const bool tree = a.parents != nullptr;
   const int64_t share = tree ? kBtThreads : 4 * kBtThreads;
   int64_t ctas = (a.token_capacity + share - 1) / share;
-  ctas = ctas < 1 ? 1 : (ctas > 296 ? 296 : ctas);
+  ctas = ctas < 1 ? 1 : (ctas > 2 * sms ? 2 * sms : ctas);
   const int64_t per_cta = ((a.token_capacity + ctas - 1) / ctas + 3) / 4 * 4;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.slot_mapping) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
   cudaLaunchConfig_t cfg = {};

@@ -231,7 +231,7 @@ cudaError_t launch_swap_blocks(const SwapArgs& a, cudaStream_t s, int* launches)
 cudaError_t launch_attn_simt(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_lse_merge(const MergeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 
-cudaError_t launch_block_tables(const TablesArgs& a, cudaStream_t s, int* launches);
+cudaError_t launch_block_tables(const TablesArgs& a, int sms, cudaStream_t s, int* launches);
 cudaError_t launch_kv_accept(const AcceptArgs& a, int sms, cudaStream_t s, int* launches);
 // Tree attention with mma.sync on values split into 16-bit parts (every dtype and block size).
 cudaError_t launch_tree_split(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
