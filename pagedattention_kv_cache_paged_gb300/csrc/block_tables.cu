@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const TablesAr
   pdl_launch_dependents();
   const int64_t count = a.free_state[0];
   if (kTree)
-    for (int i = tid; i < kBtStage && lo + i < hi; i += kBtThreads) stage[i] = __ldg(a.parents + lo + i);
+    for (int i = tid; i < kBtStage && lo + i < hi; i += kBtThreads) stage[i] = ld_s32(a.parents + lo + i);
   if (tid == 0) {
     sm.carry_tok = sm.carry_take = 0;
     sm.served = 0;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const TablesAr
   // parent of the node at token t
   auto parent = [&](int64_t t) -> int32_t {
     const int64_t i = t - lo;
-    return i >= 0 && i < kBtStage ? stage[i] : __ldg(a.parents + t);
+    return i >= 0 && i < kBtStage ? stage[i] : ld_s32(a.parents + t);
   };
   for (int b0 = 0; b0 < a.batch; b0 += kBtSeqs) {
     bt_chunk(a, sm, b0, avail, blockIdx.x == 0, alone);

@@ -262,11 +262,11 @@ __global__ void __launch_bounds__(kTcWarps * 32, G > 8 ? 2 : PA_TC_MIN_CTAS)
   const int64_t t_begin = (int64_t)part * a.part_tokens;
   // tile j of this warp covers tokens [tile_t0(j), tile_t0(j) + 16)
   auto tile_t0 = [&](int j) -> int64_t { return t_begin + (int64_t)(warp + kTcWarps * j) * kTile; };
-  auto tile_block = [&](int j) -> int { return __ldg(table + (tile_t0(j) >> a.block_shift)); };
+  auto tile_block = [&](int j) -> int { return ld_s32(table + (tile_t0(j) >> a.block_shift)); };
   // The loads that do not depend on one another go out together, so that their latencies overlap:
   // the context length, the table entries of this warp's first tiles (read ahead of the length:
   // every position below the table's capacity has an entry) and the Q fragments.
-  int64_t len = __ldg(a.context_lens + b);
+  int64_t len = ld_s32(a.context_lens + b);
   int blk_first[kStages];
 #pragma unroll
   for (int j = 0; j < kStages; ++j)
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kTcWarps * 32, G > 8 ? 2 : PA_TC_MIN_CTAS)
   int64_t new_row = -1;  // element offset of the new token's pool row
   if (a.k_new != nullptr && len > 0 && part == n_parts_row - 1) {
     const int64_t last = len - 1;
-    const int64_t s_new = __ldg(a.slot_mapping + b);
-    const int blk_last = __ldg(table + (last >> a.block_shift));
+    const int64_t s_new = ld_s64(a.slot_mapping + b);
+    const int blk_last = ld_s32(table + (last >> a.block_shift));
     const int64_t expect = (blk_last >= 0 && blk_last < a.num_blocks)
                                ? ((int64_t)blk_last << a.block_shift) + (last & bmask) : -2;
     if (s_new >= 0) {

@@ -31,9 +31,17 @@ __device__ __forceinline__ int ld_nc_s32(const int32_t* p) {
   return v;
 }
 
-__device__ __forceinline__ int64_t ld_nc_s64(const int64_t* p) {
+// The same for what the preceding grid may write (lengths, tables, masks) in a grid launched with programmatic
+// serialization: it starts while they are being written, so they are not read-only for it, and the load must stay
+// behind griddepcontrol.wait.
+__device__ __forceinline__ int ld_s32(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int64_t ld_s64(const int64_t* p) {
   int64_t v;
-  asm volatile("ld.global.nc.s64 %0, [%1];" : "=l"(v) : "l"(p));
+  asm volatile("ld.global.s64 %0, [%1];" : "=l"(v) : "l"(p));
   return v;
 }
 

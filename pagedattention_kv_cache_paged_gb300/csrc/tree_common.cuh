@@ -16,8 +16,8 @@ struct TreeSeq {
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   TreeSeq s{};
-  const int64_t q0 = __ldg(a.query_start_loc + b), q1 = __ldg(a.query_start_loc + b + 1);
-  s.n = __ldg(a.context_lens + b);
+  const int64_t q0 = ld_s32(a.query_start_loc + b), q1 = ld_s32(a.query_start_loc + b + 1);
+  s.n = ld_s32(a.context_lens + b);
   s.q0 = q0;
   if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
     s.bad = PA_DEVERR_QUERY_LOC;
@@ -250,7 +250,7 @@ __device__ __forceinline__ void tree_record(const TreeArgs& a, const TreeSched& 
 
 // Whether a row (the mask words of its node, or nullptr and the node of a chain) sees node s.
 __device__ __forceinline__ bool tree_sees(const int64_t* words, int node, int s) {
-  return words != nullptr ? ((__ldg(words + (s >> 6)) >> (s & 63)) & 1) != 0 : s <= node;
+  return words != nullptr ? ((ld_s64(words + (s >> 6)) >> (s & 63)) & 1) != 0 : s <= node;
 }
 
 }  // namespace pa

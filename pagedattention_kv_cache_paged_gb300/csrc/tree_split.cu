@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
     auto locate = [&](int x) -> int64_t {
       const int pos = x * kKeys + warp * kWK + lane;
       if (lane >= kWK || x >= w.x1 || pos >= w.sq.n) return -1;
-      const int blk = __ldg(table + (pos >> a.block_shift));
+      const int blk = ld_s32(table + (pos >> a.block_shift));
       if (blk < 0 || blk >= a.num_blocks) {
         raise_error(a.err, PA_DEVERR_BLOCK_ID);
         return -2;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
           cp_async16(at + (kV ? v_chunk(key, c) : k_chunk(key, c)), src + (o < 0 ? 0 : o), o >= 0);
         } else {
           float f[8];
-          Elt<T>::unpack(o >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + o)) : make_uint4(0, 0, 0, 0), f);
+          Elt<T>::unpack(o >= 0 ? *reinterpret_cast<const uint4*>(src + o) : make_uint4(0, 0, 0, 0), f);
           at[kV ? v_chunk(key, c) : k_chunk(key, c)] = make_float4(f[0], f[1], f[2], f[3]);
           at[kV ? v_chunk(key, c + 1) : k_chunk(key, c + 1)] = make_float4(f[4], f[5], f[6], f[7]);
         }
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
         const int node = w.node0 + (r >> a.group_shift);
         const int last = min(w.x1 * kKeys, w.sq.n);
         for (int pos = max(w.x0 * kKeys, hist); pos < last; ++pos) {
-          const int blk = __ldg(table + (pos >> a.block_shift));
+          const int blk = ld_s32(table + (pos >> a.block_shift));
           if (!tree_sees(words_of(node), node, pos - hist) || blk < 0 || blk >= a.num_blocks) continue;
           const T* v = static_cast<const T*>(a.v_pool) + (int64_t)blk * a.kv_block_stride + (pos & bmask) * row_elems +
                        (int64_t)w.kvh * D + c;

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       // table entry of this lane's box of tile x of the unit (-1: behind the context)
       auto entry = [&](int x) -> int {
         const int pos = x * kKeys + lane * box_keys;
-        return lane < boxes && x < w.x1 && pos < w.sq.n ? ld_nc_s32(table + (pos >> a.block_shift)) : -1;
+        return lane < boxes && x < w.x1 && pos < w.sq.n ? ld_s32(table + (pos >> a.block_shift)) : -1;
       };
       int blk = entry(w.x0);
       for (int x = w.x0; x < w.x1; ++x, ++t) {
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
       const int node = w.node0 + (pair ? grp * (128 >> a.group_shift) : 0) + (min(r, rows - 1) >> a.group_shift);
       const int64_t* words = a.tree_mask != nullptr ? a.tree_mask + (w.sq.q0 + node) * a.mask_words : nullptr;
       // (read before it is needed: most trees have one mask word, and no tile reaches it before the first)
-      const uint64_t word0 = words != nullptr && live ? (uint64_t)ld_nc_s64(words) : 0ull;
+      const uint64_t word0 = words != nullptr && live ? (uint64_t)ld_s64(words) : 0ull;
       float m_use = -INFINITY, l_run = 0.f;
 
       // Bits of the 64 keys from kb on that this row sees (bit c: key kb + c); `loaded`: their sub-tiles
@@ -444,8 +444,8 @@ __global__ void __launch_bounds__(kTuThreads, 1)
           keep = (word0 << -s0) | ((1ull << -s0) - 1ull);
         } else {
           const int i = s0 >> 6, sh = s0 & 63;
-          keep = (i == 0 ? word0 : (i < a.mask_words ? (uint64_t)__ldg(words + i) : 0ull)) >> sh;
-          if (sh != 0 && i + 1 < a.mask_words) keep |= (uint64_t)__ldg(words + i + 1) << (64 - sh);
+          keep = (i == 0 ? word0 : (i < a.mask_words ? (uint64_t)ld_s64(words + i) : 0ull)) >> sh;
+          if (sh != 0 && i + 1 < a.mask_words) keep |= (uint64_t)ld_s64(words + i + 1) << (64 - sh);
         }
         if (nv < 64) keep &= (1ull << nv) - 1ull;
 #pragma unroll
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kTuThreads, 1)
               const int last = min(w.x1 * kKeys, w.sq.n);
               for (int pos = max(w.x0 * kKeys, hist); pos < last; ++pos) {
                 const int s = pos - hist;
-                const int blk = __ldg(table + (pos >> a.block_shift));
+                const int blk = ld_s32(table + (pos >> a.block_shift));
                 if (!tree_sees(words, node, s) || blk < 0 || blk >= a.num_blocks) continue;
                 const T* vr = static_cast<const T*>(a.v_pool) + (int64_t)blk * a.kv_block_stride +
                               ((int64_t)(pos & (a.block_size - 1)) * a.n_kv_heads + w.kvh) * D + c0;

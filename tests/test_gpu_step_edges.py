@@ -107,3 +107,96 @@ def test_checked_mode_without_memory_for_its_copy_returns(cuda_lib):
     assert pa.load_library().paged_kv_accept(p, p, 1, 0, p, 2 ** 61, 4, p, p, p, 8, 2, 4, 16, 1, 64, pa.PA_FP32, None,
                                              None) == _abi.PA_ECUDA
     assert pa.launch_count() == before
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("call", ["decode", "decode_cuda_cores", "decode_fp32", "decode_fused", "prefill", "tree", "tree_mma_sync",
+                                  "tree_fp32", "chain"])
+def test_tables_right_before_attention(cuda_lib, call, graph):
+    """No launch between the tables of a step and the call that reads them: lengths, blocks and masks are those of this
+    step every time, though the steps take turns between two batches that share all arrays."""
+    pa = cuda_lib
+    B, S, H, G, D = 48, 16, 4, 4, 128
+    m = 1 if call.startswith("decode") else 6
+    dtype = FP32 if call.endswith("fp32") else BF16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rng = np.random.default_rng(5)
+    blocks = 2 * B * 72  # (a half for each batch: the fused call writes rows)
+    k, v = (torch.randn((blocks, S, H, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn((B * m, H * G, D), generator=g, device="cuda").to(dtype)
+    new_k, new_v = (torch.randn((B, H, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+    trees = call.startswith("tree")
+    batches = []
+    for i in range(2):
+        held = rng.integers(0, 70, B) if i else np.sort(rng.integers(0, 30, B))
+        ids = rng.permutation(B * 72) + i * B * 72
+        table = np.full((B, 72), -1)
+        table[np.arange(72)[None] < held[:, None]] = ids[:held.sum()]
+        free = np.zeros(B * 72, np.int64)
+        free[:B * 72 - held.sum()] = ids[held.sum():]
+        parents = np.concatenate([[-1] + [rng.integers(-1, j) for j in range(1, m)] for _ in range(B)])
+        batches.append(dict(hist=i32(held * S), table=i32(table), counts=i32(held), free=i32(free),
+                            state=i32([B * 72 - held.sum(), 0]), parents=i32(parents) if trees else None))
+    d = {n: x.clone() for n, x in batches[0].items() if n != "hist" and x is not None}
+    new = i32([m] * B)
+    t = pa.build_block_tables(batches[0]["hist"], new, d["table"], d["counts"], d["free"], d["state"], S, blocks,
+                              num_tokens=B * m, parents=d.get("parents"))
+    out = torch.empty_like(q)
+
+    def step(i):
+        for n in d:
+            d[n].copy_(batches[i][n])
+        pa.build_block_tables(batches[i]["hist"], new, d["table"], d["counts"], d["free"], d["state"], S, blocks,
+                              parents=d.get("parents"), out=t)
+        if call == "decode_fused":
+            pa.paged_attention_decode_fused(q, new_k, new_v, t.slot_mapping, k, v, d["table"], t.context_lens, out=out)
+        elif call.startswith("decode"):
+            pa.paged_attention_decode(q, k, v, d["table"], t.context_lens, out=out, decode_kernel=int(call.endswith("cores")))
+        elif call == "prefill":
+            pa.paged_attention_prefill(q, t.query_start_loc, k, v, d["table"], t.context_lens, out=out)
+        else:
+            pa.paged_attention_tree(q, t.query_start_loc, t.tree_mask, k, v, d["table"], t.context_lens, out=out, max_nodes=m,
+                                    kernel=int(call == "tree_mma_sync"))
+
+    want = []
+    for i in range(2):
+        for n in d:
+            d[n].copy_(batches[i][n])
+        pa.build_block_tables(batches[i]["hist"], new, d["table"], d["counts"], d["free"], d["state"], S, blocks,
+                              parents=d.get("parents"), out=t)
+        torch.cuda.synchronize()
+        assert int(t.slot_mapping.min()) >= 0
+        step(i)  # (the fused call writes the same rows again)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    # the reference batch on its own tables, without this call's history
+    i = 1
+    for n in d:
+        d[n].copy_(batches[i][n])
+    pa.build_block_tables(batches[i]["hist"], new, d["table"], d["counts"], d["free"], d["state"], S, blocks,
+                          parents=d.get("parents"), out=t)
+    torch.cuda.synchronize()
+    rows, ref, _, _ = oracle.tree.paged_tree_attention(q.cpu(), t.query_start_loc.cpu(), None if t.tree_mask is None else
+                                                       t.tree_mask.cpu(), k.cpu(), v.cpu(), d["table"].cpu(),
+                                                       t.context_lens.cpu(), D ** -0.5)
+    assert np.abs(want[1].double().cpu().numpy()[rows] - ref).max() < (1e-5 if dtype == FP32 else 2e-2)
+    assert not torch.equal(want[0], want[1])
+    kept = [torch.empty_like(out) for _ in range(40)]
+    if graph:
+        s = torch.cuda.Stream()
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr, stream=s):
+            for j, o in enumerate(kept):
+                step(j % 2)
+                o.copy_(out)
+        for _ in range(5):
+            gr.replay()
+    else:
+        for j, o in enumerate(kept * 5):
+            step(j % 2)
+            o.copy_(out)
+    torch.cuda.synchronize()
+    for j, o in enumerate(kept):
+        assert torch.equal(o, want[j % 2]), j
+    assert pa.device_error_flags() == 0
