@@ -2,6 +2,7 @@
 // planning and dispatch to the kernels.  Holds no arithmetic of the method itself.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -712,6 +713,7 @@ int tree_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t 
   a.tree_mask = tree_mask;
   a.mask_words = mask_words;
   a.max_nodes = max_nodes;
+  a.max_context = (int32_t)std::min(table_capacity(block_table_stride, block_size), (int64_t)kTreeMaxContext);
   a.batch = batch;
   a.total_q = total_q;
   a.num_blocks = num_blocks;

@@ -155,6 +155,7 @@ struct TreeArgs {
   const int64_t* tree_mask;        // nullptr: chains
   int mask_words;
   int max_nodes;
+  int32_t max_context;             // longest context that a table row and kTreeMaxContext allow
   int batch;
   int64_t total_q;
   int64_t num_blocks;

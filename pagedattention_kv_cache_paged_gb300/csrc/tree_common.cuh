@@ -16,21 +16,22 @@ struct TreeSeq {
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b) {
   TreeSeq s{};
-  const int64_t q0 = ld_s32(a.query_start_loc + b), q1 = ld_s32(a.query_start_loc + b + 1);
+  const int q0 = ld_s32(a.query_start_loc + b), q1 = ld_s32(a.query_start_loc + b + 1);
   s.n = ld_s32(a.context_lens + b);
   s.q0 = q0;
   if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
     s.bad = PA_DEVERR_QUERY_LOC;
   } else {
-    if (q1 - q0 > a.max_nodes || s.n < q1 - q0) s.bad |= PA_DEVERR_QUERY_LOC;
-    if (a.tree_mask != nullptr && q1 - q0 > (int64_t)64 * a.mask_words) s.bad |= PA_DEVERR_TREE;
-    if (s.n < 0 || s.n > (a.bt_stride << a.block_shift) || s.n > kTreeMaxContext) s.bad |= PA_DEVERR_CONTEXT_LEN;
+    s.m = q1 - q0;
+    if (s.m > a.max_nodes || s.n < s.m) s.bad |= PA_DEVERR_QUERY_LOC;
+    if (a.tree_mask != nullptr && s.m > 64 * a.mask_words) s.bad |= PA_DEVERR_TREE;
+    if ((unsigned)s.n > (unsigned)a.max_context) s.bad |= PA_DEVERR_CONTEXT_LEN;
   }
   if (s.bad) {
     s.n = 0;
-    s.q0 = max(q0, (int64_t)0);
+    s.q0 = max(q0, 0);
+    s.m = (int)max(min((int64_t)q1, a.total_q) - s.q0, (int64_t)0);
   }
-  s.m = (int)max(min(q1, a.total_q) - s.q0, (int64_t)0);
   return s;
 }
 
