@@ -200,3 +200,121 @@ def test_tables_right_before_attention(cuda_lib, call, graph):
     for j, o in enumerate(kept):
         assert torch.equal(o, want[j % 2]), j
     assert pa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("unified", [False, True])
+def test_accept_with_the_layers_of_a_block_side_by_side(cuda_lib, dtype, unified):
+    """Pools [num_blocks, layers, ..]: a layer is nearer than the next block."""
+    L, NB, S, H, D = 3, 9, 16, 2, 64
+    g = torch.Generator().manual_seed(2)
+    pool = torch.randn((NB, L, 2, S, H, D), generator=g).to(dtype)
+    dp = pool.cuda()
+    if not unified:
+        dp = [dp[:, :, i].contiguous() for i in range(2)]
+    k, v = ((dp[:, :, i] if unified else dp[i]).transpose(0, 1) for i in range(2))
+    acc, n_acc, hist = i32([[1, 2, 9], [0, 5, -3]]), i32([3, 2]), i32([13, 30])
+    table = i32([[7, 2, -1, -1], [0, 5, 3, 1]])
+    cuda_lib.paged_kv_accept(k, v, acc, n_acc, hist, table)
+    assert cuda_lib.device_error_flags() == 0
+    for layer in range(L):
+        want = oracle.tree.paged_kv_accept(pool[:, layer, 0], pool[:, layer, 1], acc.cpu(), n_acc.cpu(), hist.cpu(),
+                                           table.cpu())
+        assert torch.equal(k[layer].cpu(), want[0]) and torch.equal(v[layer].cpu(), want[1])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_step_on_a_stream_given_to_the_calls(cuda_lib, raw):
+    """Every call in the order of the stream it is given, behind what that stream has to do first."""
+    pa = cuda_lib
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((40, 16, 2, 64), generator=g, device="cuda") for _ in range(2))
+    q = torch.randn((9, 4, 64), generator=g, device="cuda")
+    kn, vn = (torch.randn((9, 2, 64), generator=g, device="cuda") for _ in range(2))
+    parents, acc, n_acc = i32([-1, 0, 0, 1, 1, -1, -1, 1, 2]), i32([[0, 2], [1, 3]]), i32([2, 2])
+
+    def step(hist, stream, slow):
+        pools = [k.clone(), v.clone()]
+        table, counts, state = torch.full((2, 12), -1, dtype=torch.int32, device="cuda"), i32([7, 2]), i32([31, 0])
+        table[0, :7], table[1, :2] = torch.arange(7, device="cuda"), torch.arange(7, 9, device="cuda")
+        free = torch.arange(9, 40, dtype=torch.int32, device="cuda")
+        h, m = i32([1, 1]), i32([5, 4])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            if slow:
+                torch.cuda._sleep(10_000_000)
+            h.copy_(hist)
+        s = stream.cuda_stream if raw else stream
+        t = pa.build_block_tables(h, m, table, counts, free, state, 16, 40, parents=parents, stream=s)
+        pa.paged_kv_write(kn, vn, t.slot_mapping, *pools, stream=s)
+        out = pa.paged_attention_tree(q, t.query_start_loc, t.tree_mask, *pools, table, t.context_lens, max_nodes=5, stream=s)
+        pa.paged_kv_accept(*pools, acc, n_acc, h, table, stream=s)
+        return [out, *pools, table, counts, state, *t]
+
+    hist = i32([100, 30])
+    want = step(hist, torch.cuda.current_stream(), False)
+    torch.cuda.synchronize()
+    got = step(hist, torch.cuda.Stream(), True)
+    torch.cuda.synchronize()
+    assert pa.device_error_flags() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_trees_of_many_mask_words(cuda_lib, kernel):
+    """Trees of up to 700 nodes, some almost chains: masks as built, attention over them as the oracle has it."""
+    pa = cuda_lib
+    rng = np.random.default_rng(8)
+    new, hist, words = [700, 3, 450, 0, 129], [20, 5, 0, 40, 100], 11
+    parents = np.concatenate([[-1] + [j - 1 if rng.random() < 0.97 else rng.integers(-1, j) for j in range(1, m)]
+                              for m in new if m])
+    total = int(sum(new))
+    held = [-(-h // 16) for h in hist]
+    blocks = sum(-(-(h + m) // 16) for h, m in zip(hist, new)) + 2
+    ids = rng.permutation(blocks)
+    table = np.full((5, 50), -1)
+    at = 0
+    for b, c in enumerate(held):
+        table[b, :c] = ids[at:at + c]
+        at += c
+    free = np.zeros(blocks, np.int64)
+    free[:blocks - at] = ids[at:]
+    args = [i32(table), i32(held), i32(free), i32([blocks - at, 0])]
+    t = pa.build_block_tables(i32(hist), i32(new), *args, 16, blocks, parents=i32(parents), mask_words=words)
+    ref = oracle.tree.step_tables(hist, new, i32(table).cpu(), i32(held).cpu(), i32(free).cpu(), blocks - at, 16, total,
+                                  parents, words)
+    for name in ("query_start_loc", "context_lens", "slot_mapping", "positions", "tree_mask"):
+        assert np.array_equal(getattr(t, name).cpu().numpy(), ref[name]), name
+    g = torch.Generator().manual_seed(8)
+    k, v = (torch.randn((blocks, 16, 2, 64), generator=g) for _ in range(2))
+    q = torch.randn((total, 4, 64), generator=g)
+    for dtype, tol in ((BF16, 2e-2), (FP32, 1e-5)):
+        out = pa.paged_attention_tree(q.to(dtype).cuda(), t.query_start_loc, t.tree_mask, k.to(dtype).cuda(),
+                                      v.to(dtype).cuda(), args[0], t.context_lens, kernel=kernel)
+        rows, want, _, _ = oracle.tree.paged_tree_attention(q.to(dtype), t.query_start_loc.cpu(), t.tree_mask.cpu(),
+                                                            k.to(dtype), v.to(dtype), args[0].cpu(), t.context_lens.cpu(),
+                                                            0.125)
+        assert np.abs(out.cpu().double().numpy()[rows] - want).max() <= tol
+    assert pa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_batch_of_30000_chains_of_one_node_is_a_decode_batch(cuda_lib, kernel, dtype):
+    pa = cuda_lib
+    B = 30000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v = (torch.randn((64, 16, 2, 64), generator=g, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn((B + 5, 8, 64), generator=g, device="cuda").to(dtype)
+    q[B:] = float("nan")  # rows behind the last sequence
+    table = torch.randint(0, 64, (B, 3), generator=g, device="cuda", dtype=torch.int32)
+    ctx = torch.randint(1, 49, (B,), generator=g, device="cuda", dtype=torch.int32)
+    out = torch.full_like(q, 7.0)
+    pa.paged_attention_tree(q, torch.arange(B + 1, dtype=torch.int32, device="cuda"), None, k, v, table, ctx, out=out,
+                            max_nodes=1, kernel=kernel)
+    want = pa.paged_attention_decode(q[:B].contiguous(), k, v, table, ctx, decode_kernel=1)
+    assert pa.device_error_flags() == 0
+    # (both within the framework's 2e-2 and 1e-5 of the definition)
+    assert (out[:B].double() - want.double()).abs().max() <= (2e-5 if dtype == FP32 else 4e-2)
+    assert (out[B:] == 7.0).all()

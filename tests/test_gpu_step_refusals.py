@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from pagedattention_kv_cache_paged_gb300 import _abi
 from tree_cases import TreeCase
 
 pytestmark = pytest.mark.gpu
@@ -137,3 +138,22 @@ def test_workspace_sizes_of_refused_blocks_and_kernels(cuda_lib):
     assert size(8, torch.bfloat16, 0) > 0 and size(8, torch.bfloat16, 2) == 0
     assert size(16, torch.float32, 0) > 0 and size(16, torch.float32, 2) == 0
     assert size(16, torch.bfloat16, 2) > 0
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(kernel=2), "EUNSUPPORTED"), (dict(kernel=3), "EINVAL"), (dict(kernel=-1), "EINVAL"),
+    (dict(partition_tokens=-1), "EINVAL"), (dict(partition_tokens=2 ** 30 + 1), "EINVAL"), (dict(scale=0), "EINVAL"),
+    (dict(scale=-1.0), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(max_nodes=0), "EINVAL"),
+])
+def test_options_that_the_library_refuses(cuda_lib, change, status):
+    with pytest.raises(cuda_lib.PagedAttnError) as e:
+        cuda_lib.paged_attention_tree(**{**tree_args(), **change})
+    assert e.value.status == getattr(_abi, "PA_" + status)
+
+
+def test_options_as_other_numbers(cuda_lib):
+    """What numpy and torch hold numbers in."""
+    pa, args = cuda_lib, tree_args()
+    want = pa.paged_attention_tree(**args, scale=0.25, max_nodes=4)
+    for scale in (np.float32(0.25), torch.tensor(0.25)):
+        assert torch.equal(pa.paged_attention_tree(**args, scale=scale, max_nodes=np.int64(4)), want)
