@@ -267,8 +267,9 @@ PA_API int paged_attention_prefill_ex(void* out, const void* q, const int32_t* q
  *   free_blocks       int32 [free_capacity], a stack: entries [0, free_state[0]) are free.  Blocks are
  *                     taken from its top in batch order.
  *   free_state        int32 [2]: the number of free blocks, updated in place, and a word of the
- *                     library's own that is 0 before and after every call.  Calls that share
- *                     free_state or block_counts must not overlap.
+ *                     library's own that is 0 before and after every call (with another value
+ *                     there the counts may stay as they were; checked mode returns PA_ERANGE).
+ *                     Calls that share free_state or block_counts must not overlap.
  *   num_blocks        blocks of the pool: an id outside [0, num_blocks) taken from free_blocks is
  *                     entered as -1 and recorded as PA_DEVERR_BLOCK_ID
  *   parents           optional int32 [token_capacity]: new token t is the node of a drafted tree

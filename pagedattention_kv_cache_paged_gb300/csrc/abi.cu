@@ -494,7 +494,7 @@ int validate_tables_step(const TablesArgs& a, cudaStream_t s) {
   if ((rc = copy_to_host(fresh, a.new_lens, a.batch, s))) return rc;
   if ((rc = copy_to_host(counts, a.block_counts, a.batch, s))) return rc;
   if ((rc = copy_to_host(state, a.free_state, (int64_t)2, s))) return rc;
-  if (state[0] < 0 || state[0] > a.free_capacity) return PA_ERANGE;
+  if (state[0] < 0 || state[0] > a.free_capacity || state[1] != 0) return PA_ERANGE;
   if (a.parents && (rc = copy_to_host(parents, a.parents, a.token_capacity, s))) return rc;
   int64_t tok = 0, taken = 0;
   for (int b = 0; b < a.batch; ++b) {

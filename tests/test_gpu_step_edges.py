@@ -318,3 +318,15 @@ def test_a_batch_of_30000_chains_of_one_node_is_a_decode_batch(cuda_lib, kernel,
     # (both within the framework's 2e-2 and 1e-5 of the definition)
     assert (out[:B].double() - want.double()).abs().max() <= (2e-5 if dtype == FP32 else 4e-2)
     assert (out[B:] == 7.0).all()
+
+
+def test_checked_mode_looks_at_the_librarys_word_of_the_free_list(cuda_lib):
+    pa = cuda_lib
+    args = lambda word: (i32([0]), i32([5]), i32([[-1, -1]]), i32([0]), i32([3, 1]), i32([2, word]), 16, 8)
+    pa.set_checked_mode(True)
+    t = pa.build_block_tables(*args(0), num_tokens=5)
+    assert t.slot_mapping.cpu().tolist() == list(range(16, 21))
+    for word in (1, -1):
+        with pytest.raises(pa.PagedAttnError) as e:
+            pa.build_block_tables(*args(word), num_tokens=5)
+        assert e.value.status == pa.PA_ERANGE
