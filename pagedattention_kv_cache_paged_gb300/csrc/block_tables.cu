@@ -18,8 +18,8 @@
 // context_lens entry (0 if it did not fit) needs beyond its count.  A grid of one CTA does without.
 //
 // Bound by latency: two dependent rounds to memory (lengths, then ids), the scan between them, and the ticket.
-// 64 trees of up to 16 tokens: 7.4 us.  256 trees of 60 to 128: 10.3 us, half of it the walks up the ancestors.
-// 2,048 prompts, 1.1 M tokens, 13.8 MB written: 12.2 us, 1.1 TB/s; of 16,000 cycles the lengths and their sums
+// 64 trees of up to 16 tokens: 6.4 us.  256 trees of 60 to 128: 10.4 us, half of it the walks up the ancestors.
+// 2,048 prompts, 1.1 M tokens, 13.8 MB written: 12.0 us, 1.1 TB/s; of 16,000 cycles the lengths and their sums
 // take 4,700, the two rounds of search, id and stores of each thread 8,900, the ticket 2,700.
 #include "pa_common.cuh"
 #include "pa_internal.h"

@@ -5,10 +5,11 @@
 // the drafted region, and a row may be the source of one entry and the destination of a later one
 // (idx[0] = 1, idx[1] = 2), never of an earlier one: a destination i is read by a later entry j > i
 // only if idx[j] = i < j.  So one thread that owns a 16-byte column of a layer's rows may load a batch
-// of entries, then store it, and go on to the next batch: no other thread touches its column.  Memory
-// bound: every row is read once and written once.  288 rows of 2 KB, K and V, in 32 layers (75 MB):
-// 12.8 us, 5.9 TB/s; one row moved in one layer takes 2.3 us, four loads behind one another (list,
-// table, row, store).  Eight rows in flight at four CTAs per SM: four at eight CTAs 15.2 us.
+// of entries, then store it, and go on to the next batch: no other thread touches its column.  Every
+// row that moves is read once and written once.  288 rows of 2 KB, K and V, in 32 layers, of which 261
+// move (68 MB): 14.3 us in calls that take turns over eight batches' pools, so that the rows come from DRAM and go
+// back there (4.8 TB/s, 0.71 of the copy rate), 9.7 us over one batch's, which stay in L2.  Bound by the chain of a CTA
+// (list, table, row, store), one wave behind the other, and by DRAM on top of it; three rows in one layer take 2.4 us.  Eight rows in flight at four CTAs per SM: four at eight CTAs 15.8 us.
 #include <algorithm>
 
 #include "pa_common.cuh"
@@ -97,8 +98,8 @@ __global__ void __launch_bounds__(kAccThreads, kAccCtas) kv_accept_kernel(const 
 
 cudaError_t launch_kv_accept(const AcceptArgs& a, int sms, cudaStream_t s, int* launches) {
   // Layers of a sequence divided among its CTAs for two waves of CTAs: a CTA looks its rows up once, and the
-  // second wave evens out lists of different lengths.  64 sequences x 32 layers: 12.8 us; one wave 13.2,
-  // a CTA per layer 13.7.
+  // second wave evens out lists of different lengths.  64 sequences x 32 layers: 14.3 us; one wave 14.8,
+  // a CTA per layer 14.8.
   const int per_seq = std::max(1, std::min(a.num_layers, 2 * sms * kAccCtas / a.batch));
   const int layers_cta = (a.num_layers + per_seq - 1) / per_seq;
   const int64_t grid = (int64_t)a.batch * ((a.num_layers + layers_cta - 1) / layers_cta);

@@ -12,10 +12,12 @@
 // of the time).
 //
 // On CUDA cores the same work is bound by shared memory, which hands every lane its operands (27 sequences of up to
-// 1,941 tokens, 12 drafts, 12 heads, head_dim 64, fp32: 64 us where this takes 53, 3.1 TB/s): in fragments each
+// 1,941 tokens, 12 drafts, 12 heads, head_dim 64, fp32: 64 us where this takes 54, 3.1 TB/s): in fragments each
 // value is read once per warp.  Bound by the products (six for one, in tiles of 16 rows) where a unit has many rows,
 // by HBM where it has few (21 sequences of up to 8,984 tokens, head_dim 128, 4 rows: 4.2 TB/s), and by the latency
-// of a unit's start and end where contexts are short.
+// of a unit's start and end where contexts are short.  16-bit pools with blocks of 8 (16 requests of up to 1,941
+// tokens, 12 drafts, 32 / 8 heads, head_dim 128, 67.5 MB): bf16 84.6 us, fp16 89.4, 0.8 TB/s, bound like fp32 ones by
+// tiles of 16 rows that each read their keys again (three of them a KV head) and by the split of weights and values.
 //
 // Three (at head_dim 128 two) CTAs of four warps per SM walk their equal share of the units (tree_common.cuh); a
 // unit has up to 32 (node, head) rows (16 at head_dim 128).  Each warp takes its own 16 keys of every key tile,

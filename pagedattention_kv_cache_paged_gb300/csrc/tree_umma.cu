@@ -9,7 +9,7 @@
 //
 // Two groups of four softmax warps, each with an O of its own.
 //   Narrow kernel (no sequence has more than 128 (node, head) rows): bound by HBM (618 MB of a serving batch
-//     with up to 16 drafts in 102 us, 1.34 GB of four long documents in 211 us: 6.1 and 6.4 TB/s).  The groups
+//     with up to 16 drafts in 102 us, 1.34 GB of four long documents in 210 us: 6.0 and 6.4 TB/s).  The groups
 //     take the key tiles of a unit in turn and their states are joined at its end (both Os lie in the same TMEM
 //     lanes, so only (maximum, sum) goes through shared memory, and each group writes half of the columns).  A
 //     tile passes every 1,400 cycles at HBM's rate, the round S, softmax, P V through the barriers takes about
@@ -18,7 +18,7 @@
 //     warps share them (K, V, S, P V), each product's one commit telling the softmax, the producer and the other
 //     issuer alike.
 //   Wide kernel: bound by the softmax and the tensor core (the serving batch with 48 to 64 drafts, 134 GFLOP:
-//     161 us, 0.83 PFLOP/s).  A unit of more than 128 rows has two Q tiles, one per group, that share every
+//     160 us, 0.84 PFLOP/s).  A unit of more than 128 rows has two Q tiles, one per group, that share every
 //     128-key K and V tile; each group has one S buffer, and while one computes its softmax the tensor core has
 //     the other's products.  (A barrier that is complete already costs its waiter 110-230 cycles, a commit 100:
 //     one thread issuing both products took 4,600 cycles a tile without ever having to wait.)  Each group starts
