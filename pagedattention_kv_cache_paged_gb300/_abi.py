@@ -425,14 +425,15 @@ def _on(dev: int):
     return _HERE if dev < 0 or dev == torch._C._cuda_getDevice() else _OnDevice(dev)
 
 
-def _tensor(t, name: str):
-    """Refuses what is no tensor, before any of its attributes is read."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+def _tensors(**named):
+    """Refuses what is no tensor: for where reading an argument's attributes has failed."""
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def _refuse(t, name: str, dtype, dev: int, shape):
-    _tensor(t, name)
+    _tensors(**{name: t})
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -463,8 +464,11 @@ def _vec(t, name: str, dtype, dev: int, n: int) -> int:
 def _table(t, name: str, rows: int, dev: int) -> tuple:
     """(pointer, row stride, columns) of an int32 [rows, columns] tensor whose rows are contiguous.  (The stride of a
     dimension of size 1 means nothing: an [n, 1] tensor transposed has 1 there.)"""
-    _tensor(t, name)
-    shape, stride = t.shape, t.stride()
+    try:
+        shape, stride = t.shape, t.stride()
+    except AttributeError:
+        _tensors(**{name: t})
+        raise
     if len(shape) != 2 or shape[0] != rows or (stride[1] != 1 and rows and shape[1]):
         raise ValueError(f"{name} must be [batch, entries] with contiguous rows")
     if t.dtype is not _I32 or t.get_device() != dev or dev < 0:
@@ -475,8 +479,11 @@ def _table(t, name: str, rows: int, dev: int) -> tuple:
 def _pools(k, v, dev: int, lead: int = 0) -> tuple:
     """(pointers, shape, block stride in elements) of two pools of one layout (see :func:`_pool`) behind
     ``lead`` dimensions of layers."""
-    _tensor(k, "k_pool"), _tensor(v, "v_pool")
-    shape, stride, vstride, dtype = k.shape, k.stride(), v.stride(), k.dtype
+    try:
+        shape, stride, vstride, dtype = k.shape, k.stride(), v.stride(), k.dtype
+    except AttributeError:
+        _tensors(k_pool=k, v_pool=v)
+        raise
     if len(shape) != 4 + lead or shape != v.shape or dtype is not v.dtype:
         raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, n_kv_heads, head_dim] of one dtype")
     if lead:
@@ -528,12 +535,15 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
     written again (a captured step).  Sequences that do not fit get nothing and are recorded in the
     device error word."""
     lib = _lib or load_library()
-    _tensor(history_lens, "history_lens")
-    if parents is not None:
-        _tensor(parents, "parents")
-    B, dev = history_lens.numel(), history_lens.get_device()
+    try:
+        B, dev = history_lens.numel(), history_lens.get_device()
+        T = num_tokens
+        if out is None and T is None and parents is not None:
+            T = parents.numel()
+    except AttributeError:
+        _tensors(history_lens=history_lens, **({} if parents is None else {"parents": parents}))
+        raise
     if out is None:
-        T = num_tokens if num_tokens is not None else (parents.numel() if parents is not None else None)
         if T is None:
             raise ValueError("num_tokens is needed without parents or out")
         words = 1 if mask_words is None else mask_words
@@ -545,15 +555,17 @@ def build_block_tables(history_lens, new_lens, block_table, block_counts, free_b
                              torch.empty(T, dtype=torch.int32, device=d),
                              torch.empty((T, words), dtype=torch.int64, device=d) if parents is not None else None)
     qsl, ctx, slots, pos, mask = out
-    _tensor(slots, "slot_mapping")
-    T, words, par, msk = slots.numel(), 0, None, None
+    try:
+        T, words, par, msk = slots.numel(), 0, None, None
+        if parents is not None and (mask is None or mask.dim() != 2 or
+                                    (mask_words is not None and mask.shape[1] != mask_words)):
+            raise ValueError("with parents, out.tree_mask must be [tokens, mask_words]")
+    except AttributeError:
+        _tensors(slot_mapping=slots, **({} if mask is None else {"tree_mask": mask}))
+        raise
     if num_tokens is not None and num_tokens != T:
         raise ValueError(f"out holds {T} tokens, num_tokens is {num_tokens}")
     if parents is not None:
-        if mask is not None:
-            _tensor(mask, "tree_mask")
-        if mask is None or mask.dim() != 2 or (mask_words is not None and mask.shape[1] != mask_words):
-            raise ValueError("with parents, out.tree_mask must be [tokens, mask_words]")
         words = mask.shape[1]
         par = _vec(parents, "parents", _I32, dev, T)
         msk = _arg(mask, "tree_mask", _I64, dev, (T, words))
@@ -636,18 +648,20 @@ def paged_attention_tree(q, query_start_loc, tree_mask, k_pool, v_pool, block_ta
     mma.sync (every type and block size), 2 tcgen05.  ``partition_tokens``: keys a block of threads takes
     (0: an equal share).  Rows from ``query_start_loc[batch]`` on are left as they were."""
     lib = _lib or load_library()
-    _tensor(q, "q"), _tensor(context_lens, "context_lens")
-    dev, shape = q.get_device(), q.shape
+    try:
+        dev, shape, B = q.get_device(), q.shape, context_lens.numel()
+        of_mask = None if tree_mask is None else tree_mask.shape
+    except AttributeError:
+        _tensors(q=q, context_lens=context_lens, **({} if tree_mask is None else {"tree_mask": tree_mask}))
+        raise
     kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev)
     if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [total_q, n_q_heads, head_dim]")
     total_q, Hq, _ = shape
-    dt, B = k_pool.dtype, context_lens.numel()
+    dt = k_pool.dtype
     code = _code(dt)
     words, mask = 0, None
     if tree_mask is not None:
-        _tensor(tree_mask, "tree_mask")
-        of_mask = tree_mask.shape
         if len(of_mask) != 2 or of_mask[0] != total_q or of_mask[1] < 1:
             raise ValueError("tree_mask must be [total_q, words]")
         words = of_mask[1]
@@ -686,19 +700,22 @@ def paged_kv_accept(k_pool, v_pool, accepted, accepted_lens, history_lens, block
     ``history_lens[b] + i``.  ``accepted`` int32 [B, A], each list ascending.  The pools are one
     layer's ``[num_blocks, block_size, Hkv, D]`` or all layers' ``[layers, num_blocks, ...]``."""
     lib = _lib or load_library()
-    _tensor(k_pool, "k_pool"), _tensor(v_pool, "v_pool"), _tensor(accepted_lens, "accepted_lens")
-    dev, layers, layer_stride, shape = k_pool.get_device(), 1, 0, k_pool.shape
+    try:
+        dev, layers, layer_stride, shape, B = k_pool.get_device(), 1, 0, k_pool.shape, accepted_lens.numel()
+        vshape, vstride = v_pool.shape, v_pool.stride()
+    except AttributeError:
+        _tensors(k_pool=k_pool, v_pool=v_pool, accepted_lens=accepted_lens)
+        raise
     lead = 1 if len(shape) == 5 else 0
-    if lead and v_pool.shape == shape:
+    if lead and vshape == shape:
         layers = shape[0]
         if layers == 0:
             return
         layer_stride = k_pool.stride(0)
-        if layers > 1 and v_pool.stride(0) != layer_stride:
+        if layers > 1 and vstride[0] != layer_stride:
             raise ValueError("the layers of k_pool and v_pool must be equally far apart")
         layer_stride *= k_pool.element_size()
     kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev, lead)
-    B = accepted_lens.numel()
     acc, acc_stride, entries = _table(accepted, "accepted", B, dev)
     table, bt_stride, _ = _table(block_table, "block_table", B, dev)
     args = (kp, vp, layers, layer_stride, acc, acc_stride, entries,
