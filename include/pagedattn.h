@@ -316,8 +316,8 @@ PA_API int build_block_tables(const int32_t* history_lens, const int32_t* new_le
  *                   at most 64 * mask_words.  NULL: the drafted tokens form a chain, each seeing the
  *                   ones before it and itself (mask_words is ignored).
  *   max_nodes       bound on m_b, >= 1 (it sizes the launch)
- *   context_lens    int32 [batch]: history + m_b, at most 2^31 - 4096.  The keys and values of the nodes are the last m_b
- *                   positions of the context, in node order, already written.
+ *   context_lens    int32 [batch]: history + m_b, at most 2^31 - 4096.  The keys and values of the nodes are
+ *                   the last m_b positions of the context, in node order, already written.
  *   scale           > 0, and finite times log2(e) as well (at most 2.35e38)
  *   out[r][i] = sum_j softmax_j(scale * q[r][i] . K_j) V_j over the keys node r sees.  A row that sees
  *   nothing gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and

@@ -9,7 +9,8 @@
 // row that moves is read once and written once.  288 rows of 2 KB, K and V, in 32 layers, of which 261
 // move (68 MB): 14.3 us in calls that take turns over eight batches' pools, so that the rows come from DRAM and go
 // back there (4.8 TB/s, 0.71 of the copy rate), 9.7 us over one batch's, which stay in L2.  Bound by the chain of a CTA
-// (list, table, row, store), one wave behind the other, and by DRAM on top of it; three rows in one layer take 2.4 us.  Eight rows in flight at four CTAs per SM: four at eight CTAs 15.8 us.
+// (list, table, row, store), one wave behind the other, and by DRAM on top of it; three rows in one layer take
+// 2.4 us.  Eight rows in flight at four CTAs per SM: four at eight CTAs 15.8 us.
 #include <algorithm>
 
 #include "pa_common.cuh"

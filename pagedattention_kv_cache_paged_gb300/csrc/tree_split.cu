@@ -16,7 +16,7 @@
 // value is read once per warp.  Bound by the products (six for one, in tiles of 16 rows) where a unit has many rows,
 // by HBM where it has few (21 sequences of up to 8,984 tokens, head_dim 128, 4 rows: 4.2 TB/s), and by the latency
 // of a unit's start and end where contexts are short.  16-bit pools with blocks of 8 (16 requests of up to 1,941
-// tokens, 12 drafts, 32 / 8 heads, head_dim 128, 67.5 MB): bf16 84.6 us, fp16 89.4, 0.8 TB/s, bound like fp32 ones by
+// tokens, 12 drafts, 32 / 8 heads, head_dim 128, 67.5 MB): bf16 89.6 us, fp16 85.1, 0.8 TB/s, bound like fp32 ones by
 // tiles of 16 rows that each read their keys again (three of them a KV head) and by the split of weights and values.
 //
 // Three (at head_dim 128 two) CTAs of four warps per SM walk their equal share of the units (tree_common.cuh); a
@@ -333,17 +333,19 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
 #pragma unroll
           for (int n = 0; n < kNT; ++n) mx = fmaxf(mx, fmaxf(s[mt][n][2 * h], s[mt][n][2 * h + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.scale_log2;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float m_new = fmaxf(m[mt][h], mx);
           const float m_sub = m_new == -INFINITY ? 0.f : m_new;
-          corr[mt][h] = fast_exp2(m[mt][h] - m_sub);  // m = -inf: 0
+          corr[mt][h] = fast_exp2((m[mt][h] - m_sub) * a.scale_log2);  // m = -inf: 0
           m[mt][h] = m_new;
           float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p = fast_exp2(fmaf(s[mt][n][2 * h + e], a.scale_log2, -m_sub));
+              // (the difference first: of s * scale - m in one rounding the rounding of m is left, which passes 2^7
+              // for scores of 2^31)
+              const float p = fast_exp2((s[mt][n][2 * h + e] - m_sub) * a.scale_log2);
               s[mt][n][2 * h + e] = p;
               sum += p;
             }
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kTsThreads, tree_split_ctas(D)) tree_split_ker
 #pragma unroll
         for (int k = 0; k < kTsWarps; ++k) {
           if (k >= busy) break;
-          const float f = fast_exp2(s_m[k][r] - M);  // a warp without keys: 0, and its sums are 0
+          const float f = fast_exp2((s_m[k][r] - M) * a.scale_log2);  // a warp without keys: 0, and its sums are 0
           const float4 v = *reinterpret_cast<const float4*>(rings + k * 3 * kSlot + r * D + c);
           L = fmaf(s_l[k][r], f, L);
           acc[0] = fmaf(v.x, f, acc[0]);

@@ -222,3 +222,31 @@ def test_the_longest_contexts(cuda_lib, kernel, m):
         pa.paged_attention_tree(q, qsl, None, k, k, table, ctx, out=out, kernel=kernel)
         assert pa.device_error_flags() == flag
         assert (out == (0.0 if flag else 1.0)).all()
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("m", [5, 40])
+@pytest.mark.parametrize("part", [0, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_far_beyond_the_exponents_range(cuda_lib, kernel, dtype, m, part, sign):
+    """Queries and keys that are powers of two times small whole numbers, so that every score is exact in 32 bits and
+    two different ones are far more than 2^128 apart: the largest take it all, equal ones in equal parts."""
+    case = TreeCase(55, [300, 20], [m, 9], q_heads=8, kv_heads=2, head_dim=64, block_size=16, dtype=dtype)
+    q, k = (2.0 ** 11, 2.0 ** 9) if dtype == FP16 else (2.0 ** 35, 2.0 ** 30)
+    rng = np.random.default_rng(int(sign) + m)
+    case.q = torch.full_like(case.q, sign * q)
+    for b in range(2):
+        for j in range(int(case.ctx[b])):
+            blk, tok = case.row_of(b, j)
+            case.k[blk, tok] = k * float(rng.integers(64, 100))
+            if j in (17, 18, 130, 299):  # the largest scores and the smallest ones are met four and two times
+                case.k[blk, tok] = k * (120.0 if sign > 0 else 60.0)
+    got = cuda_lib.paged_attention_tree(**case.device(), scale=case.scale, kernel=kernel, partition_tokens=part)
+    assert cuda_lib.device_error_flags() == 0
+    rows, ref, spread, _ = oracle.tree.paged_tree_attention(case.q, case.qsl, case.mask, case.k, case.v, case.table, case.ctx,
+                                                            case.scale)
+    # weights are 0 or exactly alike, so nothing is rounded but a sum of a few values and the output
+    half = torch.finfo(dtype).eps / 2
+    tol = half * np.abs(ref) + spread * 8 * 2.0 ** -24 + (2.0 ** -25 if dtype == FP16 else 0.0)
+    assert (np.abs(got.cpu().double().numpy()[rows] - ref) <= tol * (1 + half)).all()
