@@ -111,7 +111,7 @@ enum {
  *                          does not allow them)
  *   prefill_kernel         0 auto (tcgen05 tensor cores where the shape allows, else CUDA cores),
  *                          1 CUDA cores, 2 tcgen05 (PA_EUNSUPPORTED if the shape does not allow it);
- *                          for paged_attention_tree see there
+ *                          for paged_attention_tree and paged_attention_window see there
  *   partition_tokens       split-K partition length in tokens, rounded up to block_size, at most
  *                          2^30; 0 = automatic (see paged_attention_decode_workspace_size)
  *   reserved               must be 0
@@ -377,6 +377,106 @@ PA_API int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t l
                            const int32_t* accepted_lens, const int32_t* history_lens, const int32_t* block_table,
                            int64_t block_table_stride, int batch, int64_t num_blocks, int block_size, int n_kv_heads,
                            int head_dim, pa_dtype dtype, const pa_opts* opts, void* stream);
+
+/*
+ * paged_attention_window — attention over a sliding window and the first tokens of the context: the query at
+ * position p attends to the positions j <= p with j > p - window (itself and the window - 1 before it) or j < sinks.
+ * Single tokens and causal chunks; what no query of a sequence sees is not read, neither keys, values nor table
+ * entries, so blocks that lie before the window (and hold no sink) may have been given back to the pool.
+ *   q, out          [total_q][n_q_heads][head_dim]
+ *   query_start_loc NULL: one query per sequence, the last position of its context (total_q = batch).  Else
+ *                   int32 [batch + 1], as for paged_attention_prefill: sequence b owns the rows qsl[b] ..
+ *                   qsl[b+1]-1, the last m_b positions of its context.  Rows before qsl[0] and from qsl[batch] on
+ *                   (a padded batch) are left as they were.
+ *   window          >= 1; INT32_MAX hides nothing
+ *   sinks           >= 0
+ *   context_lens    int32 [batch], at most 2^31 - 4096 without query_start_loc
+ *   scale           > 0, and finite times log2(e) as well (at most 2.35e38)
+ * An empty context gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and NaN
+ * included); a non-finite value that it sees gives non-finite outputs, a non-finite key those of its score.
+ *   workspace       without query_start_loc: optional scratch for splitting contexts, at least
+ *                   paged_attention_window_workspace_size(...) bytes for the same sizes and opts, 16-byte aligned, no
+ *                   initialisation needed.  NULL: no splitting (slower for few sequences).  Calls that may overlap
+ *                   need one each.  With query_start_loc it is not used.
+ *   opts            may be NULL.  kv_block_stride_bytes as for the decode call.  Without query_start_loc:
+ *                   partition_tokens is the number of visible tokens that a block of threads takes, rounded up to
+ *                   whole steps of 64 (0 = an equal share of the work).  With it, prefill_kernel: 0 or 1, CUDA
+ *                   cores (2: PA_EUNSUPPORTED).
+ * A sequence whose context is negative or longer than its table row, or whose chunk is longer than its context, gives
+ * zeros in its rows and is recorded as PA_DEVERR_CONTEXT_LEN (with query_start_loc PA_DEVERR_QUERY_LOC); table
+ * entries outside the pool are masked and recorded as PA_DEVERR_BLOCK_ID.  Checked mode returns PA_ERANGE for each.
+ */
+PA_API int paged_attention_window(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q, int window,
+                                  int sinks, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                                  int64_t block_table_stride, const int32_t* context_lens, int batch,
+                                  int64_t num_blocks, int block_size, float scale, int n_q_heads, int n_kv_heads,
+                                  int head_dim, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                  const pa_opts* opts, void* stream);
+
+/* Workspace bytes paged_attention_window needs (without query_start_loc) to split contexts as long as the table and the
+ * window allow, on the current device (0 if it does not split).  What the call refuses gives 0. */
+PA_API size_t paged_attention_window_workspace_size(int batch, int64_t block_table_stride, int block_size, int window,
+                                                    int sinks, int n_q_heads, int n_kv_heads, int head_dim,
+                                                    pa_dtype dtype, const pa_opts* opts);
+
+/*
+ * The 4-bit cache.  Keys and values of [num_blocks][block_size][n_kv_heads] rows as
+ *   k_codes, v_codes    uint8 [..][head_dim / 2]: two codes of 0 .. 15 in a byte, the even dimension in its low half
+ *   k_params, v_params  bf16 [..][head_dim / 32]: (scale, zero) of each group of 64 dimensions, zero a whole number
+ * value = scale * (code - zero).  Four contiguous arrays, 16-byte aligned; 72 bytes instead of 256 a row of 128 bf16
+ * values.  Slots and tables are those of the pools.  copy_blocks and swap_blocks move blocks of it (codes and params
+ * are two pairs of pools of their own block bytes).
+ * What a group of values x is packed to: lo = min(0, min x), hi = max(0, max x),
+ *   scale = bf16(fp32(hi / 15) - fp32(lo / 15)), the difference rounded to fp32 first, or 0 (and all codes 0) if that
+ *           is below 2^-126
+ *   zero  = round(-lo / scale), code = round(x / scale) + zero, both clamped to 0 .. 15; the quotients, as real numbers,
+ *           are rounded to the nearest whole number, halves to the even one
+ * so a value that lies between lo and hi comes back within half a scale or so (one next to the ends within 9/16).
+ * A group that holds an infinity or NaN gets scale NaN: all its values are NaN.
+ */
+
+/*
+ * paged_kv_write_q4 — paged_kv_write into the 4-bit cache: this step's K/V rows packed and scattered through
+ * slot_mapping (a negative slot writes nothing; slots past the cache are skipped and recorded as PA_DEVERR_SLOT; slots
+ * must be distinct, checked mode returns PA_ERANGE for both).
+ *   k_new, v_new   [n_tokens][n_kv_heads][head_dim], dtype
+ */
+PA_API int paged_kv_write_q4(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens,
+                             void* k_codes, void* v_codes, void* k_params, void* v_params, int64_t num_blocks,
+                             int block_size, int n_kv_heads, int head_dim, pa_dtype dtype, void* stream);
+
+/*
+ * paged_kv_unpack_q4 — blocks of the 4-bit cache as values, into blocks of a K pool and a V pool: what a later chunk of
+ * a prompt attends to (paged_attention_prefill and the other calls over pools read the copy).
+ *   block_pairs  int64 [n_pairs][2] = (block of the cache, block of the pools).  A destination must not appear twice
+ *                (checked mode returns PA_ERANGE); ids out of range are skipped and recorded as PA_DEVERR_COPY_PAIR.
+ *   opts         may be NULL; only kv_block_stride_bytes (of the pools) applies.
+ * Values are rounded to dtype; what passes its largest number, as the rounded scale of a group may, becomes that.
+ */
+PA_API int paged_kv_unpack_q4(const void* k_codes, const void* v_codes, const void* k_params, const void* v_params,
+                              int64_t cache_blocks, void* k_pool, void* v_pool, int64_t num_blocks,
+                              const int64_t* block_pairs, int64_t n_pairs, int block_size, int n_kv_heads, int head_dim,
+                              pa_dtype dtype, const pa_opts* opts, void* stream);
+
+/*
+ * paged_attention_decode_q4 — paged_attention_decode over the 4-bit cache, behind a window if wanted: one query per
+ * sequence attends to all of its context (window INT32_MAX), or to the last `window` positions and the first `sinks`.
+ *   q, out       [batch][n_q_heads][head_dim], dtype (the cache's rows may have been packed from another one)
+ * window, sinks, context_lens, scale, empty contexts, refused sequences and blocks, and the workspace (of
+ * paged_attention_decode_q4_workspace_size bytes) as for paged_attention_window without query_start_loc; opts: only
+ * partition_tokens applies (rounded up to steps of 16 to 128 tokens).
+ * Products with the codes are exact.  Weights are rounded to bf16 for bf16 queries; for fp16 and fp32 they are split
+ * into bf16 parts that hold 16 and 24 bits.
+ */
+PA_API int paged_attention_decode_q4(void* out, const void* q, const void* k_codes, const void* v_codes,
+                                     const void* k_params, const void* v_params, const int32_t* block_table,
+                                     int64_t block_table_stride, const int32_t* context_lens, int batch,
+                                     int64_t num_blocks, int block_size, int window, int sinks, float scale,
+                                     int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, const pa_opts* opts, void* stream);
+PA_API size_t paged_attention_decode_q4_workspace_size(int batch, int64_t block_table_stride, int block_size, int window,
+                                                       int sinks, int n_q_heads, int n_kv_heads, int head_dim,
+                                                       pa_dtype dtype, const pa_opts* opts);
 
 /*
  * copy_blocks — make physical block dst a bit copy of block src, in both pools, for each pair.

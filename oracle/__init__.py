@@ -21,3 +21,4 @@ from .paged_oracle import (  # noqa: F401
     transfer_blocks,
 )
 from . import tree_oracle as tree  # noqa: F401
+from . import window_oracle as window  # noqa: F401

@@ -55,6 +55,13 @@ _TREE = [_vp, _vp, _vp, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i32, _
          _vp, _sz, _opts_p]
 _TREE_WS = [_i32, _i64, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _opts_p]
 _ACCEPT = [_vp, _vp, _i32, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _i32, _i32, _opts_p]
+_WINDOW = [_vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i32, _f32, _i32, _i32, _i32, _i32, _vp,
+           _sz, _opts_p]
+_LINE_WS = [_i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _opts_p]
+_WRITE_Q4 = [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32]
+_UNPACK_Q4 = [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _opts_p]
+_DECODE_Q4 = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _i32,
+              _vp, _sz, _opts_p]
 SIGNATURES = {
     "paged_kv_write": (_i32, _KV_WRITE + [_vp]),
     "paged_kv_write_ex": (_i32, _KV_WRITE + [_opts_p, _vp]),
@@ -72,6 +79,12 @@ SIGNATURES = {
     "paged_attention_tree": (_i32, _TREE + [_vp]),
     "paged_attention_tree_workspace_size": (_sz, _TREE_WS),
     "paged_kv_accept": (_i32, _ACCEPT + [_vp]),
+    "paged_attention_window": (_i32, _WINDOW + [_vp]),
+    "paged_attention_window_workspace_size": (_sz, _LINE_WS),
+    "paged_kv_write_q4": (_i32, _WRITE_Q4 + [_vp]),
+    "paged_kv_unpack_q4": (_i32, _UNPACK_Q4 + [_vp]),
+    "paged_attention_decode_q4": (_i32, _DECODE_Q4 + [_vp]),
+    "paged_attention_decode_q4_workspace_size": (_sz, _LINE_WS),
     "copy_blocks": (_i32, _COPY + [_vp]),
     "copy_blocks_ex": (_i32, _COPY + [_opts_p, _vp]),
     "swap_blocks": (_i32, _SWAP + [_vp]),
@@ -729,6 +742,221 @@ def paged_kv_accept(k_pool, v_pool, accepted, accepted_lens, history_lens, block
             st = lib.paged_kv_accept(*args)
     if st:
         _check("paged_kv_accept", st)
+
+
+# A window that hides nothing.
+WINDOW_ALL = 2 ** 31 - 1
+
+
+@functools.lru_cache(maxsize=1024)
+def _line_workspace(dev: int, packed: bool, batch, stride, S, window, sinks, Hq, Hkv, D, code, partition_tokens) -> int:
+    lib = load_library()
+    size = lib.paged_attention_decode_q4_workspace_size if packed else lib.paged_attention_window_workspace_size
+    with _on(dev):
+        return int(size(batch, stride, S, window, sinks, Hq, Hkv, D, code, _opts_of(0, 0, partition_tokens)))
+
+
+def window_workspace_size(batch: int, block_table_stride: int, block_size: int, window: int, sinks: int,
+                          n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                          partition_tokens: int = 0) -> int:
+    """Workspace bytes of :func:`paged_attention_window` (single tokens) for these sizes on the current device."""
+    return _line_workspace(torch.cuda.current_device(), False, batch, block_table_stride, block_size, window, sinks,
+                           n_q_heads, n_kv_heads, head_dim, _code(dtype), partition_tokens)
+
+
+def decode_q4_workspace_size(batch: int, block_table_stride: int, block_size: int, window: int, sinks: int,
+                             n_q_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                             partition_tokens: int = 0) -> int:
+    """Workspace bytes of :func:`paged_attention_decode_q4` for these sizes on the current device."""
+    return _line_workspace(torch.cuda.current_device(), True, batch, block_table_stride, block_size, window, sinks,
+                           n_q_heads, n_kv_heads, head_dim, _code(dtype), partition_tokens)
+
+
+def _int32(**named):
+    """Refuses what a C int does not hold (ctypes would cut it off)."""
+    for name, x in named.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits, got {x}")
+
+
+def _call_with_workspace(fn, args: tuple, ws: tuple, tail: tuple, dev: int) -> int:
+    """The call itself, on device ``dev``.  ``ws`` = (None, n): scratch of its own (see :func:`_run_tree`)."""
+    if dev != torch._C._cuda_getDevice():
+        with _OnDevice(dev):
+            return _call_with_workspace(fn, args, ws, tail, dev)
+    if ws[0] is not None or ws[1] == 0:
+        return fn(*args, *ws, *tail)
+    scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws[1], tail[1])
+    try:
+        return fn(*args, scratch, ws[1], *tail)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
+
+
+def paged_attention_window(q, query_start_loc, k_pool, v_pool, block_table, context_lens, window: int, sinks: int = 0,
+                           scale=None, out=None, workspace="auto", stream=None, kernel: int = 0,
+                           partition_tokens: int = 0):
+    """Attention over a sliding window and the first tokens: the query at position p attends to the positions
+    ``j <= p`` with ``j > p - window`` or ``j < sinks``.
+
+    ``query_start_loc`` None: ``q [B, Hq, D]`` holds one query per sequence, its last position.  Else ``q [total_q,
+    Hq, D]`` holds causal chunks delimited by it, as for :func:`paged_attention_prefill`; rows before its first and from
+    its last entry on are left as they were.  Table entries of blocks that no query sees are not read: such blocks may
+    have been freed.  ``workspace`` (single tokens only): "auto" (allocated for the call on its stream), None (contexts
+    are not split) or a caller-owned uint8 CUDA tensor.  ``kernel`` (chunks): 0 auto, 1 CUDA cores, 2 tcgen05.
+    ``partition_tokens`` (single tokens): visible tokens that a block of threads takes (0: an equal share)."""
+    lib = _lib or load_library()
+    try:
+        dev, shape, B = q.get_device(), q.shape, context_lens.numel()
+    except AttributeError:
+        _tensors(q=q, context_lens=context_lens)
+        raise
+    kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev)
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError("q must be [total_q, n_q_heads, head_dim]")
+    _int32(window=window, sinks=sinks)
+    total_q, Hq, _ = shape
+    dt = k_pool.dtype
+    code = _code(dt)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    table, bt_stride, _ = _table(block_table, "block_table", B, dev)
+    if query_start_loc is None:
+        qsl = None
+        if total_q != B:
+            raise ValueError(f"without query_start_loc q must hold one query per sequence ({B}), got {total_q}")
+    else:
+        qsl = _vec(query_start_loc, "query_start_loc", _I32, dev, B + 1)
+    args = (_arg(out, "out", dt, dev, shape), _arg(q, "q", dt, dev), qsl, total_q, window, sinks, kp, vp, table,
+            bt_stride, _vec(context_lens, "context_lens", _I32, dev, B), B, NB, S, scale, Hq, Hkv, D, code)
+    if workspace is None or qsl is not None:
+        ws = None, 0
+    elif isinstance(workspace, str) and workspace == "auto":
+        ws = None, _line_workspace(dev, False, B, bt_stride, S, window, sinks, Hq, Hkv, D, code, partition_tokens)
+    else:
+        ws = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
+    tail = (_opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), kernel, partition_tokens),
+            _raw_stream(stream, dev))
+    st = _call_with_workspace(lib.paged_attention_window, args, ws, tail, dev)
+    if st:
+        _check("paged_attention_window", st)
+    return out
+
+
+class Q4Cache(NamedTuple):
+    """The 4-bit cache of one layer (see include/pagedattn.h): codes ``[num_blocks, block_size, Hkv, D / 2]`` uint8 and
+    (scale, zero) pairs ``[num_blocks, block_size, Hkv, D / 32]`` bf16.  ``copy_blocks(c.k_codes, c.v_codes, pairs)``
+    and ``copy_blocks(c.k_params, c.v_params, pairs)`` copy blocks of it, and :func:`swap_blocks` in the same way."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_params: torch.Tensor
+    v_params: torch.Tensor
+
+
+def q4_cache(num_blocks: int, block_size: int, n_kv_heads: int, head_dim: int, device="cuda") -> Q4Cache:
+    """An empty 4-bit cache (zeros)."""
+    shape = (num_blocks, block_size, n_kv_heads)
+    codes = [torch.zeros(shape + (head_dim // 2,), dtype=torch.uint8, device=device) for _ in range(2)]
+    params = [torch.zeros(shape + (head_dim // 32,), dtype=torch.bfloat16, device=device) for _ in range(2)]
+    return Q4Cache(*codes, *params)
+
+
+def _cache(cache, dev: int) -> tuple:
+    """(pointers, block count, block size, KV heads, head_dim) of a 4-bit cache on device ``dev``."""
+    try:
+        kc, vc, kp, vp = cache
+        NB, S, Hkv, half = kc.shape
+    except (TypeError, ValueError, AttributeError):
+        raise TypeError("cache must be a Q4Cache: k_codes, v_codes [num_blocks, block_size, n_kv_heads, head_dim / 2], "
+                        "k_params, v_params [.., head_dim / 32]") from None
+    D = 2 * half
+    if D % 32:
+        raise ValueError(f"head_dim {D} is not a multiple of 32")
+    rows, pairs = (NB, S, Hkv, half), (NB, S, Hkv, D // 32)
+    return (_arg(kc, "k_codes", torch.uint8, dev, rows), _arg(vc, "v_codes", torch.uint8, dev, rows),
+            _arg(kp, "k_params", torch.bfloat16, dev, pairs), _arg(vp, "v_params", torch.bfloat16, dev, pairs), NB, S, Hkv, D)
+
+
+def paged_kv_write_q4(k_new, v_new, slot_mapping, cache: Q4Cache, stream=None):
+    """Pack ``k_new, v_new [T, Hkv, D]`` into the 4-bit cache at ``slot_mapping`` (int64 [T]; negative: nothing)."""
+    lib = _lib or load_library()
+    try:
+        dev, dt, T = k_new.get_device(), k_new.dtype, slot_mapping.numel()
+    except AttributeError:
+        _tensors(k_new=k_new, slot_mapping=slot_mapping)
+        raise
+    *ptrs, NB, S, Hkv, D = _cache(cache, dev)
+    args = (_arg(k_new, "k_new", dt, dev, (T, Hkv, D)), _arg(v_new, "v_new", dt, dev, (T, Hkv, D)),
+            _vec(slot_mapping, "slot_mapping", _I64, dev, T), T, *ptrs, NB, S, Hkv, D, _code(dt),
+            _raw_stream(stream, dev))
+    with _on(dev):
+        st = lib.paged_kv_write_q4(*args)
+    if st:
+        _check("paged_kv_write_q4", st)
+
+
+def paged_kv_unpack_q4(cache: Q4Cache, k_pool, v_pool, block_pairs, stream=None):
+    """Unpack blocks of the 4-bit cache into a K and a V pool ``[num_blocks, block_size, Hkv, D]``: for each row (block
+    of the cache, block of the pools) of int64 ``block_pairs [n, 2]``."""
+    lib = _lib or load_library()
+    try:
+        dev, shape = k_pool.get_device(), block_pairs.shape
+    except AttributeError:
+        _tensors(k_pool=k_pool, block_pairs=block_pairs)
+        raise
+    kp, vp, NB, S, Hkv, D, stride = _pools(k_pool, v_pool, dev)
+    *ptrs, cache_blocks, cs, ch, cd = _cache(cache, dev)
+    if (S, Hkv, D) != (cs, ch, cd):
+        raise ValueError(f"blocks of the pools are {[S, Hkv, D]}, of the cache {[cs, ch, cd]}")
+    if len(shape) != 2 or shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    args = (*ptrs, cache_blocks, kp, vp, NB, _arg(block_pairs, "block_pairs", _I64, dev), shape[0], S, Hkv, D,
+            _code(k_pool.dtype), _opts_of(0 if stride == S * Hkv * D else stride * k_pool.element_size(), 0, 0),
+            _raw_stream(stream, dev))
+    with _on(dev):
+        st = lib.paged_kv_unpack_q4(*args)
+    if st:
+        _check("paged_kv_unpack_q4", st)
+
+
+def paged_attention_decode_q4(q, cache: Q4Cache, block_table, context_lens, window: int | None = None, sinks: int = 0,
+                              scale=None, out=None, workspace="auto", stream=None, partition_tokens: int = 0):
+    """Decode attention over the 4-bit cache: ``q [B, Hq, D]`` over the paged context of each sequence -> ``out [B, Hq,
+    D]``; ``window`` (None: all of the context) and ``sinks`` as for :func:`paged_attention_window`, and the other
+    arguments too."""
+    lib = _lib or load_library()
+    try:
+        dev, shape, dt, B = q.get_device(), q.shape, q.dtype, context_lens.numel()
+    except AttributeError:
+        _tensors(q=q, context_lens=context_lens)
+        raise
+    *ptrs, NB, S, Hkv, D = _cache(cache, dev)
+    if len(shape) != 3 or shape[0] != B or shape[2] != D:
+        raise ValueError("q must be [batch, n_q_heads, head_dim]")
+    Hq, code = shape[1], _code(dt)
+    if window is None:
+        window = WINDOW_ALL
+    _int32(window=window, sinks=sinks)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    table, bt_stride, _ = _table(block_table, "block_table", B, dev)
+    args = (_arg(out, "out", dt, dev, shape), _arg(q, "q", dt, dev), *ptrs, table, bt_stride,
+            _vec(context_lens, "context_lens", _I32, dev, B), B, NB, S, window, sinks, scale, Hq, Hkv, D, code)
+    if workspace is None:
+        ws = None, 0
+    elif isinstance(workspace, str) and workspace == "auto":
+        ws = None, _line_workspace(dev, True, B, bt_stride, S, window, sinks, Hq, Hkv, D, code, partition_tokens)
+    else:
+        ws = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
+    st = _call_with_workspace(lib.paged_attention_decode_q4, args, ws,
+                              (_opts_of(0, 0, partition_tokens), _raw_stream(stream, dev)), dev)
+    if st:
+        _check("paged_attention_decode_q4", st)
+    return out
 
 
 def copy_blocks(k_pool, v_pool, block_pairs, stream=None):

@@ -182,6 +182,19 @@ int validate_tables(const int32_t* block_table, int64_t bt_stride, const int32_t
   return PA_OK;
 }
 
+// Checked mode: slots of distinct rows inside the pool (negative ones write nothing).
+int validate_slots(const int64_t* slot_mapping, int64_t n_tokens, int64_t total_slots, cudaStream_t s) {
+  std::vector<int64_t> slots;
+  int rc = copy_to_host(slots, slot_mapping, n_tokens, s);
+  if (rc) return rc;
+  std::unordered_set<int64_t> seen;
+  for (int64_t v : slots) {
+    if (v < 0) continue;
+    if (v >= total_slots || !seen.insert(v).second) return PA_ERANGE;
+  }
+  return PA_OK;
+}
+
 // Split-K plan: partition length in tokens and partitions per row.  The automatic length gives the
 // grid at most one wave of the tensor-core decode (3 resident CTAs per SM, 2 for groups of 16 query
 // heads, times the device's SM count) when every row is as long as the table allows: each row gets
@@ -266,15 +279,7 @@ int kv_write_impl(const void* k_new, const void* v_new, const int64_t* slot_mapp
   unsigned* err = nullptr;
   if ((rc = device_info(&err, nullptr))) return rc;
   const int64_t total_slots = num_blocks * block_size;
-  if (checked()) {
-    std::vector<int64_t> slots;
-    if ((rc = copy_to_host(slots, slot_mapping, n_tokens, s))) return rc;
-    std::unordered_set<int64_t> seen;
-    for (int64_t v : slots) {
-      if (v < 0) continue;
-      if (v >= total_slots || !seen.insert(v).second) return PA_ERANGE;
-    }
-  }
+  if (checked() && (rc = validate_slots(slot_mapping, n_tokens, total_slots, s))) return rc;
   KvWriteArgs a{k_new,        v_new,     slot_mapping,      n_tokens, k_pool, v_pool, total_slots,
                 (int)(row_bytes / 16), block_size, stride_bytes / 16, err};
   int launches = 0;
@@ -818,6 +823,334 @@ int accept_impl(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride
   return finish(e, launches);
 }
 
+// --------------------------------------------------------------------------------------------
+// windowed attention and the 4-bit cache
+// --------------------------------------------------------------------------------------------
+
+// Checked mode: lengths, and the table entries of the positions that some query sees; qsl nullptr: one query each.
+int validate_window(const int32_t* block_table, int64_t bt_stride, const int32_t* context_lens, int batch,
+                    int64_t num_blocks, int block_size, int window, int sinks, const int32_t* query_start_loc,
+                    int64_t total_q, cudaStream_t s) {
+  std::vector<int32_t> lens, qsl, table;
+  int rc = copy_to_host(lens, context_lens, batch, s);
+  if (rc) return rc;
+  if (query_start_loc) {
+    if ((rc = copy_to_host(qsl, query_start_loc, (int64_t)batch + 1, s))) return rc;
+    if (qsl[0] < 0 || qsl[(size_t)batch] > total_q) return PA_ERANGE;
+  }
+  int64_t reach = 0;  // (see validate_tables)
+  for (int b = 0; b < batch; ++b) {
+    const int64_t n = lens[(size_t)b];
+    if (n < 0 || n > bt_stride * block_size || (!query_start_loc && n > kTreeMaxContext)) return PA_ERANGE;
+    if (query_start_loc) {
+      const int64_t m = (int64_t)qsl[(size_t)b + 1] - qsl[(size_t)b];
+      if (m < 0 || m > n) return PA_ERANGE;
+    }
+    if (n > 0) reach = b * bt_stride + (n + block_size - 1) / block_size;
+  }
+  if ((rc = copy_to_host(table, block_table, reach, s))) return rc;
+  for (int b = 0; b < batch; ++b) {
+    const int64_t n = lens[(size_t)b], m = query_start_loc ? (int64_t)qsl[(size_t)b + 1] - qsl[(size_t)b] : 1;
+    if (n == 0 || m == 0) continue;
+    const int64_t low = std::max<int64_t>(n - m + 1 - window, 0), first = std::min<int64_t>(sinks, low);
+    const int64_t blocks = (n + block_size - 1) / block_size;
+    for (int64_t j = 0; j < blocks; ++j) {
+      if (j * block_size >= first && (j + 1) * block_size <= low) continue;
+      const int64_t id = table[(size_t)(b * bt_stride + j)];
+      if (id < 0 || id >= num_blocks) return PA_ERANGE;
+    }
+  }
+  return PA_OK;
+}
+
+// How a decode call over visible tokens divides its work (see TreePlan).
+struct LinePlan {
+  bool fits = false;
+  int heads = 0, units = 0, ctas = 0, share = 0;
+  bool split = false;
+  size_t bytes = 0, off_m = 0, off_l = 0, off_rec = 0;
+};
+
+LinePlan plan_line(bool packed, int batch, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, int sms,
+                   int64_t bt_stride, int block_size, int window, int sinks, int64_t partition_tokens) {
+  LinePlan p;
+  const int group = n_q_heads / n_kv_heads;
+  p.heads = line_heads(packed, n_kv_heads);
+  p.units = n_kv_heads / p.heads;
+  const int step = 16 * (line_warps(packed) / p.heads);
+  const int64_t max_seen = std::min(table_capacity(bt_stride, block_size), (int64_t)window + sinks);
+  const int64_t tiles = (max_seen + step - 1) / step;
+  p.fits = (int64_t)p.units * batch < (int64_t(1) << 30) / (tiles + kLineGap);
+  if (!p.fits) return p;
+  const int64_t work = (int64_t)p.units * batch * tiles;
+  int64_t ctas = std::min(work, (int64_t)(sms > 0 ? sms : 1) * line_ctas(packed, dtype, head_dim, group));
+  p.split = tiles + kLineGap > line_min_share(packed);  // (shorter contexts are never cut, see line_schedule)
+  if (partition_tokens > 0) {
+    int64_t share = (partition_tokens + step - 1) / step;
+    if ((work + share - 1) / share > 65535) share = (work + 65534) / 65535;  // (grid of the join)
+    p.share = (int)share;
+    ctas = (work + share - 1) / share;
+    p.split = tiles > 1;
+  }
+  p.ctas = (int)ctas;
+  if (p.split) {
+    auto up16 = [](size_t x) { return (x + 15) & ~size_t(15); };
+    const size_t rows = (size_t)p.ctas * 2 * (size_t)(p.heads * group);
+    p.off_m = rows * (size_t)head_dim * sizeof(float);
+    p.off_l = p.off_m + up16(rows * sizeof(float));
+    p.off_rec = p.off_l + up16(rows * sizeof(float));
+    p.bytes = p.off_rec + up16((size_t)p.ctas * sizeof(TreeRec));
+  }
+  return p;
+}
+
+size_t line_workspace_impl(bool packed, int batch, int64_t block_table_stride, int block_size, int window, int sinks,
+                           int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts) {
+  if (batch <= 0 || block_table_stride <= 0 || !is_pow2(block_size) || block_size > 256 || window < 1 || sinks < 0 ||
+      check_dtype(dtype) || check_heads(n_q_heads, n_kv_heads, head_dim))
+    return 0;
+  pa_opts o;
+  if (read_opts(opts, &o)) return 0;
+  int sms = 0;
+  if (device_info(nullptr, &sms)) return 0;
+  return plan_line(packed, batch, n_q_heads, n_kv_heads, head_dim, dtype, sms, block_table_stride, block_size, window,
+                   sinks, o.partition_tokens)
+      .bytes;
+}
+
+// The checks that attention over a window shares, whatever it reads; scale_log2: what the kernels hold of the scale.
+int check_window(int batch, int64_t num_blocks, int block_size, int64_t block_table_stride, int window, int sinks,
+                 float scale, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, float* scale_log2) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if ((rc = check_heads(n_q_heads, n_kv_heads, head_dim))) return rc;
+  if (batch < 0 || num_blocks <= 0 || block_table_stride <= 0 || block_size <= 0 || window < 1 || sinks < 0)
+    return PA_EINVAL;
+  if (!is_pow2(block_size) || block_size > 256) return PA_EUNSUPPORTED;
+  *scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !std::isfinite(*scale_log2)) return PA_EINVAL;
+  return PA_OK;
+}
+
+// Decode over visible tokens: what is left once the caller's own checks are made (a holds the tensors and the cache).
+int run_line(LineArgs& a, bool packed, int64_t bt_stride, int batch, int64_t num_blocks, int block_size, int window,
+             int sinks, float scale_log2, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, void* workspace,
+             size_t workspace_bytes, const pa_opts& o, cudaStream_t s) {
+  unsigned* err = nullptr;
+  int sms = 0;
+  int rc = device_info(&err, &sms);
+  if (rc) return rc;
+  const LinePlan plan = plan_line(packed, batch, n_q_heads, n_kv_heads, head_dim, dtype, sms, bt_stride, block_size,
+                                  window, sinks, o.partition_tokens);
+  if (!plan.fits) return PA_EUNSUPPORTED;
+  const bool split = plan.split && workspace != nullptr;
+  if (split && (workspace_bytes < plan.bytes || !aligned16(workspace))) return PA_EWORKSPACE;
+  if (checked()) {
+    rc = validate_window(a.block_table, bt_stride, a.context_lens, batch, num_blocks, block_size, window, sinks,
+                         nullptr, 0, s);
+    if (rc) return rc;
+  }
+  a.bt_stride = bt_stride;
+  a.batch = batch;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.block_shift = log2i(block_size);
+  a.window = window;
+  a.sinks = sinks;
+  a.max_context = (int32_t)std::min(table_capacity(bt_stride, block_size), (int64_t)kTreeMaxContext);
+  a.scale_log2 = scale_log2;
+  a.n_q_heads = n_q_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.group = n_q_heads / n_kv_heads;
+  a.head_dim = head_dim;
+  a.heads = plan.heads;
+  a.units = plan.units;
+  a.ctas = plan.ctas;
+  a.share = plan.share;
+  a.min_share = line_min_share(packed);
+  a.split = split;
+  if (split) {
+    char* base = static_cast<char*>(workspace);
+    a.ws_acc = reinterpret_cast<float*>(base);
+    a.ws_m = reinterpret_cast<float*>(base + plan.off_m);
+    a.ws_l = reinterpret_cast<float*>(base + plan.off_l);
+    a.ws_rec = reinterpret_cast<TreeRec*>(base + plan.off_rec);
+  }
+  a.err = err;
+  int launches = 0;
+  cudaError_t e = launch_line_decode(a, dtype, packed, s, &launches);
+  return finish(e, launches);
+}
+
+int window_impl(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q, int window, int sinks,
+                const void* k_pool, const void* v_pool, const int32_t* block_table, int64_t block_table_stride,
+                const int32_t* context_lens, int batch, int64_t num_blocks, int block_size, float scale, int n_q_heads,
+                int n_kv_heads, int head_dim, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                const pa_opts* opts, void* stream) {
+  float scale_log2 = 0.f;
+  int rc = check_window(batch, num_blocks, block_size, block_table_stride, window, sinks, scale, n_q_heads, n_kv_heads,
+                        head_dim, dtype, &scale_log2);
+  if (rc) return rc;
+  pa_opts o;
+  if ((rc = read_opts(opts, &o))) return rc;
+  if (total_q < 0 || (!query_start_loc && total_q != batch)) return PA_EINVAL;
+  if (batch == 0 || total_q == 0) return PA_OK;
+  if (total_q > INT32_MAX) return PA_EINVAL;
+  if (!out || !q || !k_pool || !v_pool || !block_table || !context_lens) return PA_EINVAL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return PA_EINVAL;
+  int64_t stride_bytes = 0;
+  if ((rc = pool_block_stride(o, (int64_t)block_size * n_kv_heads * head_dim * dtype_bytes(dtype), &stride_bytes)))
+    return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!query_start_loc) {
+    LineArgs a{};
+    a.out = out;
+    a.q = q;
+    a.k = k_pool;
+    a.v = v_pool;
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.block_stride = stride_bytes / dtype_bytes(dtype);
+    return run_line(a, false, block_table_stride, batch, num_blocks, block_size, window, sinks, scale_log2, n_q_heads,
+                    n_kv_heads, head_dim, dtype, workspace, workspace_bytes, o, s);
+  }
+  unsigned* err = nullptr;
+  if ((rc = device_info(&err, nullptr))) return rc;
+  const int group = n_q_heads / n_kv_heads;
+  if (o.prefill_kernel == 2) return PA_EUNSUPPORTED;
+  if (checked()) {
+    rc = validate_window(block_table, block_table_stride, context_lens, batch, num_blocks, block_size, window, sinks,
+                         query_start_loc, total_q, s);
+    if (rc) return rc;
+  }
+  AttnArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.batch = batch;
+  a.rows = total_q;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.block_shift = log2i(block_size);
+  a.kv_block_stride = stride_bytes / dtype_bytes(dtype);
+  a.scale_log2 = scale_log2;
+  a.n_q_heads = n_q_heads;
+  a.n_kv_heads = n_kv_heads;
+  a.group = group;
+  a.head_dim = head_dim;
+  a.part_tokens = (int)table_capacity(block_table_stride, block_size);
+  a.max_parts = 1;
+  a.err = err;
+  a.epoch = next_epoch();
+  a.window = window;
+  a.sinks = sinks;
+  int launches = 0;
+  cudaError_t e = launch_attn_simt_window(a, dtype, s, &launches);
+  return finish(e, launches);
+}
+
+// The sizes of a 4-bit cache, and its pointers.
+int check_q4(const void* k_codes, const void* v_codes, const void* k_params, const void* v_params, int64_t num_blocks,
+             int block_size, int n_kv_heads, int head_dim) {
+  if (num_blocks <= 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0) return PA_EINVAL;
+  if (head_dim != 64 && head_dim != 128) return PA_EUNSUPPORTED;
+  if (!is_pow2(block_size) || block_size > 256) return PA_EUNSUPPORTED;
+  if (!k_codes || !v_codes || !k_params || !v_params) return PA_EINVAL;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_params) || !aligned16(v_params)) return PA_EINVAL;
+  if ((int64_t)n_kv_heads * head_dim * block_size > INT32_MAX) return PA_EUNSUPPORTED;
+  return PA_OK;
+}
+
+int write_q4_impl(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens, void* k_codes,
+                  void* v_codes, void* k_params, void* v_params, int64_t num_blocks, int block_size, int n_kv_heads,
+                  int head_dim, pa_dtype dtype, void* stream) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (n_tokens < 0) return PA_EINVAL;
+  if ((rc = check_q4(k_codes, v_codes, k_params, v_params, num_blocks, block_size, n_kv_heads, head_dim))) return rc;
+  if (n_tokens == 0) return PA_OK;
+  if (!k_new || !v_new || !slot_mapping || !aligned16(k_new) || !aligned16(v_new)) return PA_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned* err = nullptr;
+  if ((rc = device_info(&err, nullptr))) return rc;
+  const int64_t total_slots = num_blocks * block_size;
+  if (checked() && (rc = validate_slots(slot_mapping, n_tokens, total_slots, s))) return rc;
+  const Q4WriteArgs a{k_new,    v_new,    slot_mapping, n_tokens,    k_codes,
+                      v_codes,  k_params, v_params,     total_slots, n_kv_heads * head_dim / 8,
+                      err};
+  int launches = 0;
+  cudaError_t e = launch_kv_write_q4(a, dtype, s, &launches);
+  return finish(e, launches);
+}
+
+int unpack_q4_impl(const void* k_codes, const void* v_codes, const void* k_params, const void* v_params,
+                   int64_t cache_blocks, void* k_pool, void* v_pool, int64_t num_blocks, const int64_t* block_pairs,
+                   int64_t n_pairs, int block_size, int n_kv_heads, int head_dim, pa_dtype dtype, const pa_opts* opts,
+                   void* stream) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  pa_opts o;
+  if ((rc = read_opts(opts, &o))) return rc;
+  if (n_pairs < 0 || num_blocks <= 0) return PA_EINVAL;
+  if ((rc = check_q4(k_codes, v_codes, k_params, v_params, cache_blocks, block_size, n_kv_heads, head_dim))) return rc;
+  const int64_t block_elems = (int64_t)block_size * n_kv_heads * head_dim;
+  int64_t stride_bytes = 0;
+  if ((rc = pool_block_stride(o, block_elems * dtype_bytes(dtype), &stride_bytes))) return rc;
+  if (n_pairs == 0) return PA_OK;
+  if (!k_pool || !v_pool || !block_pairs || !aligned16(k_pool) || !aligned16(v_pool)) return PA_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned* err = nullptr;
+  if ((rc = device_info(&err, nullptr))) return rc;
+  if (checked()) {
+    std::vector<int64_t> pairs;
+    if ((rc = copy_to_host(pairs, block_pairs, 2 * n_pairs, s))) return rc;
+    std::unordered_set<int64_t> dsts;
+    for (int64_t i = 0; i < n_pairs; ++i) {
+      const int64_t src = pairs[(size_t)(2 * i)], dst = pairs[(size_t)(2 * i + 1)];
+      if (src < 0 || src >= cache_blocks || dst < 0 || dst >= num_blocks) return PA_ERANGE;
+      if (!dsts.insert(dst).second) return PA_ERANGE;
+    }
+  }
+  const Q4UnpackArgs a{k_codes, v_codes,     k_params, v_params, cache_blocks, k_pool, v_pool, num_blocks,
+                       block_pairs, n_pairs, (int)(block_elems / 8), stride_bytes / dtype_bytes(dtype), err};
+  int launches = 0;
+  cudaError_t e = launch_kv_unpack_q4(a, dtype, s, &launches);
+  return finish(e, launches);
+}
+
+int decode_q4_impl(void* out, const void* q, const void* k_codes, const void* v_codes, const void* k_params,
+                   const void* v_params, const int32_t* block_table, int64_t block_table_stride,
+                   const int32_t* context_lens, int batch, int64_t num_blocks, int block_size, int window, int sinks,
+                   float scale, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype, void* workspace,
+                   size_t workspace_bytes, const pa_opts* opts, void* stream) {
+  float scale_log2 = 0.f;
+  int rc = check_window(batch, num_blocks, block_size, block_table_stride, window, sinks, scale, n_q_heads, n_kv_heads,
+                        head_dim, dtype, &scale_log2);
+  if (rc) return rc;
+  pa_opts o;
+  if ((rc = read_opts(opts, &o))) return rc;
+  if (o.kv_block_stride_bytes != 0) return PA_EINVAL;
+  if (batch == 0) return PA_OK;
+  if ((rc = check_q4(k_codes, v_codes, k_params, v_params, num_blocks, block_size, n_kv_heads, head_dim))) return rc;
+  if (!out || !q || !block_table || !context_lens || !aligned16(out) || !aligned16(q)) return PA_EINVAL;
+  LineArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k = k_codes;
+  a.v = v_codes;
+  a.k_params = k_params;
+  a.v_params = v_params;
+  a.block_table = block_table;
+  a.context_lens = context_lens;
+  return run_line(a, true, block_table_stride, batch, num_blocks, block_size, window, sinks, scale_log2, n_q_heads,
+                  n_kv_heads, head_dim, dtype, workspace, workspace_bytes, o, static_cast<cudaStream_t>(stream));
+}
+
 int copy_blocks_impl(void* k_pool, void* v_pool, const int64_t* block_pairs, int64_t n_pairs, int64_t num_blocks,
                      int64_t block_bytes, const pa_opts* opts, void* stream) {
   pa_opts o;
@@ -1120,6 +1453,56 @@ int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t layer_st
   return accept_impl(k_pool, v_pool, num_layers, layer_stride_bytes, accepted, accepted_stride, max_accepted,
                      accepted_lens, history_lens, block_table, block_table_stride, batch, num_blocks, block_size,
                      n_kv_heads, head_dim, dtype, opts, stream);
+}
+
+int paged_attention_window(void* out, const void* q, const int32_t* query_start_loc, int64_t total_q, int window,
+                           int sinks, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                           int64_t block_table_stride, const int32_t* context_lens, int batch, int64_t num_blocks,
+                           int block_size, float scale, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype,
+                           void* workspace, size_t workspace_bytes, const pa_opts* opts, void* stream) {
+  return window_impl(out, q, query_start_loc, total_q, window, sinks, k_pool, v_pool, block_table, block_table_stride,
+                     context_lens, batch, num_blocks, block_size, scale, n_q_heads, n_kv_heads, head_dim, dtype,
+                     workspace, workspace_bytes, opts, stream);
+}
+
+size_t paged_attention_window_workspace_size(int batch, int64_t block_table_stride, int block_size, int window,
+                                             int sinks, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype,
+                                             const pa_opts* opts) {
+  return line_workspace_impl(false, batch, block_table_stride, block_size, window, sinks, n_q_heads, n_kv_heads,
+                             head_dim, dtype, opts);
+}
+
+int paged_kv_write_q4(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens,
+                      void* k_codes, void* v_codes, void* k_params, void* v_params, int64_t num_blocks, int block_size,
+                      int n_kv_heads, int head_dim, pa_dtype dtype, void* stream) {
+  return write_q4_impl(k_new, v_new, slot_mapping, n_tokens, k_codes, v_codes, k_params, v_params, num_blocks,
+                       block_size, n_kv_heads, head_dim, dtype, stream);
+}
+
+int paged_kv_unpack_q4(const void* k_codes, const void* v_codes, const void* k_params, const void* v_params,
+                       int64_t cache_blocks, void* k_pool, void* v_pool, int64_t num_blocks,
+                       const int64_t* block_pairs, int64_t n_pairs, int block_size, int n_kv_heads, int head_dim,
+                       pa_dtype dtype, const pa_opts* opts, void* stream) {
+  return unpack_q4_impl(k_codes, v_codes, k_params, v_params, cache_blocks, k_pool, v_pool, num_blocks, block_pairs,
+                        n_pairs, block_size, n_kv_heads, head_dim, dtype, opts, stream);
+}
+
+int paged_attention_decode_q4(void* out, const void* q, const void* k_codes, const void* v_codes,
+                              const void* k_params, const void* v_params, const int32_t* block_table,
+                              int64_t block_table_stride, const int32_t* context_lens, int batch, int64_t num_blocks,
+                              int block_size, int window, int sinks, float scale, int n_q_heads, int n_kv_heads,
+                              int head_dim, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                              const pa_opts* opts, void* stream) {
+  return decode_q4_impl(out, q, k_codes, v_codes, k_params, v_params, block_table, block_table_stride, context_lens,
+                        batch, num_blocks, block_size, window, sinks, scale, n_q_heads, n_kv_heads, head_dim, dtype,
+                        workspace, workspace_bytes, opts, stream);
+}
+
+size_t paged_attention_decode_q4_workspace_size(int batch, int64_t block_table_stride, int block_size, int window,
+                                                int sinks, int n_q_heads, int n_kv_heads, int head_dim, pa_dtype dtype,
+                                                const pa_opts* opts) {
+  return line_workspace_impl(true, batch, block_table_stride, block_size, window, sinks, n_q_heads, n_kv_heads,
+                             head_dim, dtype, opts);
 }
 
 int copy_blocks(void* k_pool, void* v_pool, const int64_t* block_pairs, int64_t n_pairs,

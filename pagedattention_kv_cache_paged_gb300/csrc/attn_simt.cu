@@ -1,5 +1,5 @@
 // CUDA-core paged attention: decode rows (one query token per sequence) and prefill rows (one
-// query token of a causal chunk), for every dtype and supported shape.
+// query token of a causal chunk), for every dtype and supported shape; chunks also behind a sliding window.
 //
 // What it computes — JuliaPagedAttn README, "Online Softmax": one pass over the context with a
 // running maximum, a running sum and an accumulator rescaled when the maximum grows; output =
@@ -13,6 +13,9 @@
 // A row's tokens [0, len) are cut into partitions of part_tokens; a row with one partition writes
 // its output directly, otherwise the CTA stores its partial state (max, sum, accumulator; log2
 // domain) in the workspace for the log-sum-exp merge kernel.
+//
+// The windowed form (paged_attention_window, chunks) reads the sinks and the window of a row as one line of tokens,
+// and nothing else of the context.
 //
 // Inside a CTA each warp streams its own chunks of kRowsPerLoad * kUnroll tokens: a 16-byte vector
 // per lane per token row (kLanesPerRow lanes cover one row of head_dim), kUnroll K and V loads in
@@ -28,13 +31,14 @@ namespace pa {
 constexpr int kSimtWarps = 4;
 constexpr int kSimtUnroll = 4;
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool kWindow>
 __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnArgs a) {
   constexpr int kVec = Elt<T>::kVec;          // elements per 16-byte vector
   constexpr int kLanesPerRow = D / kVec;      // lanes covering one K/V row
   constexpr int kRowsPerLoad = 32 / kLanesPerRow;
   constexpr int kChunk = kRowsPerLoad * kSimtUnroll;
   static_assert(kLanesPerRow <= 32 && 32 % kLanesPerRow == 0, "head_dim / vector width");
+  static_assert(kSimtUnroll == 4, "tokens in flight per lane");
 
   __shared__ float sm_m[kSimtWarps][G];
   __shared__ float sm_l[kSimtWarps][G];
@@ -64,6 +68,10 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
     const int64_t q1 = __ldg(a.query_start_loc + b + 1);
     const int64_t n = __ldg(a.context_lens + b);
     len = n - (q1 - q0) + (row - q0) + 1;  // causal bound of query r = row - q0
+    if constexpr (kWindow) {  // rows before the first sequence and behind the last one are left as they were
+      if (row < q0 || (b == a.batch - 1 && row >= q1)) return;
+      if (n < q1 - q0 || n > max_len) len = 0;
+    }
     if (row < q0 || row >= q1 || len < 1) {
       if (threadIdx.x == 0) raise_error(a.err, PA_DEVERR_QUERY_LOC);
       len = 0;
@@ -72,6 +80,15 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
   if (len < 0 || len > max_len) {
     if (threadIdx.x == 0) raise_error(a.err, PA_DEVERR_CONTEXT_LEN);
     len = len < 0 ? 0 : max_len;
+  }
+  // windowed: tokens are numbered as the row sees them, the sinks and then the window; token t from `first` on lies at
+  // position t + skip
+  int64_t first = 0, skip = 0;
+  if constexpr (kWindow) {
+    const int64_t low = len > a.window ? len - a.window : 0;
+    first = min((int64_t)a.sinks, low);
+    skip = low - first;
+    len -= skip;
   }
   const int n_parts_row = len == 0 ? 1 : (int)((len + a.part_tokens - 1) / a.part_tokens);
   if (part >= n_parts_row) return;
@@ -103,7 +120,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
   // fused write (decode rows only): the partition holding the last context position writes this
   // step's K/V row there and takes it straight from k_new / v_new
   int64_t new_row = -1, patch_pos = -1;  // new_row: element offset of the new token's pool row
-  if (a.k_new != nullptr && a.query_start_loc == nullptr && len > 0 && part == n_parts_row - 1) {
+  if (!kWindow && a.k_new != nullptr && a.query_start_loc == nullptr && len > 0 && part == n_parts_row - 1) {
     const int64_t last = len - 1;
     const int64_t s_new = __ldg(a.slot_mapping + b);
     const int blk_last = __ldg(table + (last >> a.block_shift));
@@ -132,7 +149,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
       kr[u] = make_uint4(0, 0, 0, 0);
       vr[u] = make_uint4(0, 0, 0, 0);
       if (valid[u]) {
-        const int blk = __ldg(table + (t >> a.block_shift));
+        const int64_t pos = kWindow && t >= first ? t + skip : t;
+        const int blk = __ldg(table + (pos >> a.block_shift));
         if (blk < 0 || blk >= a.num_blocks) {
           raise_error(a.err, PA_DEVERR_BLOCK_ID);
           valid[u] = false;
@@ -144,7 +162,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
           *reinterpret_cast<uint4*>(static_cast<T*>(a.k_pool_w) + poff) = kr[u];
           *reinterpret_cast<uint4*>(static_cast<T*>(a.v_pool_w) + poff) = vr[u];
         } else {
-          const int64_t off = (int64_t)blk * a.kv_block_stride + (t & bmask) * row_elems;
+          const int64_t off = (int64_t)blk * a.kv_block_stride + (pos & bmask) * row_elems;
           kr[u] = ld_stream16(kbase + off);
           vr[u] = ld_stream16(vbase + off);
         }
@@ -172,6 +190,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
       float mx = s[0][h];
 #pragma unroll
       for (int u = 1; u < kSimtUnroll; ++u) mx = fmaxf(mx, s[u][h]);
+      // (a row that saw keys has a finite maximum, also where every score is -inf)
+      if (kWindow && (valid[0] || valid[1] || valid[2] || valid[3])) mx = fmaxf(mx, -FLT_MAX);
 #pragma unroll
       for (int off = kLanesPerRow; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float m_new = fmaxf(m[h], mx);
@@ -229,12 +249,12 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kSimtWarps; ++w)
-      if (sm_l[w][h] != 0.f) M = fmaxf(M, sm_m[w][h]);
+      if (kWindow || sm_l[w][h] != 0.f) M = fmaxf(M, sm_m[w][h]);
     float L = 0.f, A = 0.f;
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kSimtWarps; ++w) {
-        if (sm_l[w][h] != 0.f) {
+        if (kWindow || sm_l[w][h] != 0.f) {
           const float f = fast_exp2(sm_m[w][h] - M);
           L = fmaf(sm_l[w][h], f, L);
           A = fmaf(sm_acc[w][h][d], f, A);
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
     const int64_t qh = row * a.n_q_heads + (int64_t)kvh * G + h;  // global (row, query head)
     if (direct) {
       T* o = static_cast<T*>(a.out) + qh * D + d;
-      *o = Elt<T>::from_float(L != 0.f ? A / L : 0.f);
+      *o = Elt<T>::from_float((kWindow ? M != -INFINITY : L != 0.f) ? A / L : 0.f);
     } else {
       const int64_t pi = qh * a.max_parts + part;
       a.ws_acc[pi * D + d] = A;
@@ -256,43 +276,52 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWindow>
 static cudaError_t launch_simt_g(const AttnArgs& a, cudaStream_t s) {
   const int64_t grid = a.rows * (int64_t)a.max_parts * a.n_kv_heads;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 blk(kSimtWarps * 32);
   switch (a.group) {
-    case 1: attn_simt_kernel<T, D, 1><<<(unsigned)grid, blk, 0, s>>>(a); break;
-    case 2: attn_simt_kernel<T, D, 2><<<(unsigned)grid, blk, 0, s>>>(a); break;
-    case 4: attn_simt_kernel<T, D, 4><<<(unsigned)grid, blk, 0, s>>>(a); break;
-    case 8: attn_simt_kernel<T, D, 8><<<(unsigned)grid, blk, 0, s>>>(a); break;
-    case 16: attn_simt_kernel<T, D, 16><<<(unsigned)grid, blk, 0, s>>>(a); break;
+    case 1: attn_simt_kernel<T, D, 1, kWindow><<<(unsigned)grid, blk, 0, s>>>(a); break;
+    case 2: attn_simt_kernel<T, D, 2, kWindow><<<(unsigned)grid, blk, 0, s>>>(a); break;
+    case 4: attn_simt_kernel<T, D, 4, kWindow><<<(unsigned)grid, blk, 0, s>>>(a); break;
+    case 8: attn_simt_kernel<T, D, 8, kWindow><<<(unsigned)grid, blk, 0, s>>>(a); break;
+    case 16: attn_simt_kernel<T, D, 16, kWindow><<<(unsigned)grid, blk, 0, s>>>(a); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool kWindow>
 static cudaError_t launch_simt_t(const AttnArgs& a, cudaStream_t s) {
   switch (a.head_dim) {
-    case 64: return launch_simt_g<T, 64>(a, s);
-    case 128: return launch_simt_g<T, 128>(a, s);
+    case 64: return launch_simt_g<T, 64, kWindow>(a, s);
+    case 128: return launch_simt_g<T, 128, kWindow>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
-cudaError_t launch_attn_simt(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
+template <bool kWindow>
+static cudaError_t launch_simt(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
   if (a.rows == 0) return cudaSuccess;
   cudaError_t e;
   switch (dt) {
-    case PA_BF16: e = launch_simt_t<__nv_bfloat16>(a, s); break;
-    case PA_FP16: e = launch_simt_t<__half>(a, s); break;
-    case PA_FP32: e = launch_simt_t<float>(a, s); break;
+    case PA_BF16: e = launch_simt_t<__nv_bfloat16, kWindow>(a, s); break;
+    case PA_FP16: e = launch_simt_t<__half, kWindow>(a, s); break;
+    case PA_FP32: e = launch_simt_t<float, kWindow>(a, s); break;
     default: return cudaErrorInvalidValue;
   }
   ++*launches;
   return e;
+}
+
+cudaError_t launch_attn_simt(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
+  return launch_simt<false>(a, dt, s, launches);
+}
+
+cudaError_t launch_attn_simt_window(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
+  return launch_simt<true>(a, dt, s, launches);
 }
 
 }  // namespace pa

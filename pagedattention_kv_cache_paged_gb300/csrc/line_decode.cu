@@ -1,0 +1,1123 @@
+// Decode attention over the visible part of a context: a sliding window and the first tokens ("sinks"), or all of
+// it.  Pools of 16-bit values (paged_attention_window) and the 4-bit cache (paged_attention_decode_q4), every block
+// size.
+//
+// out = softmax(scale * q K^T) V over the positions j < sinks and j >= n - window.  The visible positions, packed to
+// the left, make a unit's line of tokens: nothing else is read, neither rows nor table entries.
+//
+// Division of the work.  A unit is (sequence, `heads` KV heads next to one another).  All units in a row make one line
+// of steps, a step being 16 tokens for every warp of the CTA; each CTA takes an equal share of it, whatever the
+// lengths, and units that a cut falls into are joined by a second launch (as in tree attention, tree_common.cuh).
+//
+// A warp works by itself.  It takes 16 tokens of one KV head a step, copied into a ring of its own in shared memory by
+// cp.async a few steps ahead (also across units, so that the loads never pause; table entries are read one step
+// earlier still), and forms both products with mma.sync m16n8k16 in the transposed form: S^T = K Q^T with the tokens
+// as rows and the query heads as columns, O^T = V^T P^T with the dimensions as rows.  So a query group of up to 8
+// heads costs 8 columns instead of 16 rows, K and V are the wide operand, and a head's stabiliser and accumulator
+// lie in the same lanes.  One pass with a running stabiliser (a score, unscaled) that moves only when a weight
+// would grow by more than 2^8: a vote per step, no shuffles.  The warps of a head are joined in shared memory at the
+// end of a unit.
+//
+// 16-bit pools: K and V^T fragments by ldmatrix, weights rounded to the pool's type for the product with V (as the
+// framework's other tensor-core kernels do; in fp16 formed 2^7 higher, see tree_umma.cu).
+//
+// 4-bit cache: codes become 16-bit operands with one or two logical instructions for two values and without any
+// conversion, since the order of a contraction is free: the dimensions (tokens) of an operand register are those
+// whose codes lie 16 bits apart.
+//   K: bf16 has (word & 0x000f000f) | 0x4300.. = 128 + code, and scale * (sum q (128 + code) - (128 + zero) sum q) is
+//      the score's part of a group; fp16 has code * 2^-24 (bits 0-3) and code * 2^-20 (bits 4-7) as they stand.
+//   V: 128 + code minus 128 + zero in bf16, both exact; weight * scale is rounded to bf16 (bf16 queries), or to two
+//      (fp16) or three (fp32) bf16 parts that hold its 16 or 24 bits.
+//   fp32 queries are three bf16 parts of 8 bits each and K is (code - zero), so products are exact, and each step's sums
+//   are formed by themselves and added up by rounded additions.
+#include <float.h>
+
+#include <algorithm>
+
+#include "pa_ptx.cuh"
+#include "q4_common.cuh"
+#include "tree_common.cuh"
+
+namespace pa {
+
+// ------------------------------------------------------------------------------------------------
+// Sequences and the line
+// ------------------------------------------------------------------------------------------------
+
+// What is visible of a sequence: its first tokens and its last ones, `seen` in all; position of visible token v is v, or
+// v + skip from `first` on.
+struct LineSeq {
+  int first, skip, seen;
+  bool bad;
+};
+
+__device__ __forceinline__ LineSeq line_seq(const LineArgs& a, int b) {
+  LineSeq s{};
+  const int n = ld_s32(a.context_lens + b);
+  if (n < 0 || n > a.max_context) {
+    s.bad = true;
+    return s;
+  }
+  const int low = n > a.window ? n - a.window : 0;
+  s.first = min(a.sinks, low);
+  s.skip = low - s.first;
+  s.seen = n - s.skip;
+  return s;
+}
+
+struct LineUnit {
+  LineSeq sq;
+  int b, hg;       // sequence, group of KV heads
+  int T, x0, x1;   // steps of the unit, and those of this CTA
+};
+
+// The units of a CTA's span one after the other (loads and products walk on their own).
+struct LineWalk {
+  const LineArgs& a;
+  const TreeSpan span;
+  const int step_tokens;
+  int b, u, x;
+  LineSeq sq;
+
+  __device__ __forceinline__ LineWalk(const LineArgs& args, const TreeSpan& s, int tokens)
+      : a(args), span(s), step_tokens(tokens), b(s.b0), u(s.u0), x(s.x0) {
+    sq = LineSeq{};
+    if (b < a.batch) sq = line_seq(a, b);
+  }
+  __device__ __forceinline__ bool next(LineUnit& w) {
+    for (;;) {
+      if (b >= a.batch || b > span.b1 || (b == span.b1 && u > span.u1)) return false;
+      if (sq.seen == 0 || u >= a.units) {
+        ++b;
+        u = x = 0;
+        if (b < a.batch) sq = line_seq(a, b);
+        continue;
+      }
+      w.sq = sq;
+      w.b = b;
+      w.hg = u;
+      w.T = (sq.seen + step_tokens - 1) / step_tokens;
+      w.x0 = x;
+      w.x1 = b == span.b1 && u == span.u1 ? span.x1 : w.T;
+      ++u;
+      x = 0;
+      if (w.x0 < w.x1) return true;
+    }
+  }
+};
+
+// All threads; sm initialised (span empty, refused 0), and a barrier since.  The caller's next barrier publishes it.
+template <int kThreads>
+__device__ __forceinline__ void line_schedule(const LineArgs& a, int step_tokens, TreeSched& sm) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gap = a.share > 0 ? 0 : kLineGap;
+  int tiles = 0;
+  auto look = [&](int b) -> int {  // length of sequence b on the line
+    tiles = 0;
+    if (b >= a.batch) return 0;
+    const LineSeq s = line_seq(a, b);
+    if (s.bad && blockIdx.x == 0) raise_error(a.err, PA_DEVERR_CONTEXT_LEN);
+    if (s.seen == 0) {
+      if (b % gridDim.x == blockIdx.x) sm.refused = 1;
+      return 0;
+    }
+    tiles = (s.seen + step_tokens - 1) / step_tokens;
+    return a.units * (tiles + gap);
+  };
+  int total = 0, longest = 0;
+  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+    const int c = look(b);
+    total += c;
+    longest = max(longest, c > 0 ? tiles + gap : 0);
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    sm.sums[warp] = total;
+    sm.tops[warp] = longest;
+  }
+  __syncthreads();
+  total = longest = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    total += sm.sums[w];
+    longest = max(longest, sm.tops[w]);
+  }
+  int share = a.share;
+  if (share <= 0) {
+    share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+    share = max(share, min(longest, a.min_share));
+  }
+  const int snap = !a.split || longest <= (a.share > 0 ? 0 : a.min_share) ? INT32_MAX : (a.share > 0 ? 1 : kLineGap - 1);
+  const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share;
+  if (threadIdx.x == 0) {
+    sm.share = share;
+    sm.snap = snap;
+  }
+  int carry = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const int c = look(b);
+    int v = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    __syncthreads();  // the sums before have been read
+    if (lane == 31) sm.sums[warp] = v;
+    __syncthreads();
+    int pre = carry;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) pre += sm.sums[w];
+      carry += sm.sums[w];
+    }
+    if (c > 0) {
+      const int64_t at = (int64_t)pre + v - c;  // this thread's sequence lies at [at, at + c)
+      const unsigned len = (unsigned)(tiles + gap);
+      if (lo >= at && lo < at + c) {
+        const unsigned off = (unsigned)(lo - at), u = off / len;
+        sm.span.b0 = b;
+        sm.span.u0 = (int)u;
+        sm.span.x0 = tree_cut(off - u * len, tiles, snap);
+      }
+      if (hi >= at && hi < at + c) {
+        const unsigned off = (unsigned)(hi - at), u = off / len;
+        sm.span.b1 = b;
+        sm.span.u1 = (int)u;
+        sm.span.x1 = tree_cut(off - u * len, tiles, snap);
+        sm.cut_start = (int)(hi - (off - u * len));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Copies and fragments
+// ------------------------------------------------------------------------------------------------
+
+// kBytes (4, 8 or 16) to shared memory, zeros when !ok; asynchronous.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? kBytes : 0;
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// An 8 x 8 tile of 16-bit values, two a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 lds128(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t p, const float4& v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t p, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(p), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float c) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+}
+
+// (x & a) | b
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(a), "r"(b));
+  return r;
+}
+
+// a - b of two bf16 pairs.
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Nibble k (0 .. 3) of both halves of w as bf16: 128 + code.
+__device__ __forceinline__ uint32_t code_bf16(uint32_t w, int k) {
+  return and_or(k == 0 ? w : w >> (4 * k), 0x000f000fu, 0x43004300u);
+}
+constexpr float kCodeBias = 128.f;  // of code_bf16
+
+// Weights are formed 2^8 lower (sums and accumulators alike; the quotient is the same), so that the largest is 1 and its
+// product with the largest values stays finite.
+constexpr float kLineLift = -8.f;
+
+// A softmax row's state: a lane has heads 2 tig and 2 tig + 1 of every 8 (columns of the transposed products).
+template <int NT>
+struct LineState {
+  float m[NT][2];  // stabiliser (an unscaled score), the same in the lanes of a column
+  float l[NT][2];  // this lane's share of the sum
+};
+
+// Weights of a step: s[nt][0..1] token g, [2..3] token g + 8 (rows), heads 2 tig, 2 tig + 1 (columns); ok0, ok1: whether
+// the two tokens exist.  Scores become weights; where a stabiliser moved, `rescale` is called with its factors.
+template <int NT, typename Rescale>
+__device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool ok1, float sc, float lift,
+                                             LineState<NT>& st, Rescale rescale) {
+  constexpr float kGrow = 8.f;
+  bool move = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      move |= (i < 2 ? ok0 : ok1) && !((s[nt][i] - st.m[nt][i & 1]) * sc <= kGrow);  // (also at the start, and for NaN)
+  if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // (at least the lowest number where there is a token: what saw only scores of -inf is told from what saw none)
+        float mx = fmaxf(ok0 ? fmaxf(s[nt][e], -FLT_MAX) : -INFINITY, ok1 ? fmaxf(s[nt][2 + e], -FLT_MAX) : -INFINITY);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float old = st.m[nt][e], m = fmaxf(old, mx);
+        f[e] = old == m ? 1.f : fast_exp2((old - m) * sc);
+        st.m[nt][e] = m;
+        st.l[nt][e] *= f[e];
+      }
+      rescale(nt, f[0], f[1]);
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = (i < 2 ? ok0 : ok1) ? fast_exp2(fmaf(s[nt][i] - st.m[nt][i & 1], sc, lift)) : 0.f;
+      s[nt][i] = p;
+      st.l[nt][i & 1] += p;
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// 16-bit pools
+// ------------------------------------------------------------------------------------------------
+template <typename T, int D, int NT>
+struct FullRows {
+  using Out = T;
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kWarps = 4, kCtas = 3;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRow = 2 * D;             // bytes of a token
+  static constexpr int kStage = 2 * 16 * kRow;   // K, then V
+  static constexpr int kExtra = 0;               // shared memory of a warp besides its ring
+  static constexpr float kLift = kBf16 ? kLineLift : 7.f;
+  static constexpr int kAcc = D / 16;
+
+  const T* k;
+  const T* v;
+  uint32_t q[NT][D / 16][2];
+
+  __device__ __forceinline__ FullRows(const LineArgs& a, uint32_t)
+      : k(static_cast<const T*>(a.k)), v(static_cast<const T*>(a.v)) {}
+
+  // 8-element chunk c of token t of an operand, in its place (ldmatrix reads eight rows of a chunk without conflicts)
+  static __device__ __forceinline__ uint32_t at(int t, int c) { return (uint32_t)(t * kRow + ((c ^ (t & 7)) << 4)); }
+
+  // tokens r and r + 8 of the step (r = lane / 4), rows `row` of the pools (element offsets)
+  __device__ __forceinline__ void load(const LineArgs& a, uint32_t st, int lane, const int64_t (&row)[2],
+                                       const bool (&ok)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = (lane >> 2) + 8 * h;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int c = (lane & 3) + 4 * i;
+        copy_async<16>(st + at(t, c), k + row[h] + 8 * c, ok[h]);
+        copy_async<16>(st + 16 * kRow + at(t, c), v + row[h] + 8 * c, ok[h]);
+      }
+    }
+  }
+  // (block, token in it) of KV head h as an offset
+  static __device__ __forceinline__ int64_t row_of(const LineArgs& a, int block, int token, int h) {
+    return block * a.block_stride + (int64_t)(token * a.n_kv_heads + h) * D;
+  }
+
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane) {
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool have = nt * 8 + g < a.group;
+      const T* p = static_cast<const T*>(a.q) + (head0 + nt * 8 + g) * D + 2 * tig;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          q[nt][ks][h] = have ? (uint32_t)ld_s32(reinterpret_cast<const int32_t*>(p + ks * 16 + 8 * h)) : 0u;
+    }
+  }
+
+  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, float sc, LineState<NT>& ls,
+                                       float (&o)[NT][kAcc][4]) const {
+    float s[NT][4], s2[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
+    const int mi = lane >> 3, r = lane & 7;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t x[4];
+      ldsm_x4(st + at(r + 8 * (mi & 1), 2 * ks + (mi >> 1)), x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma_16816<kBf16>(ks & 1 ? s2[nt] : s[nt], x[0], x[1], x[2], x[3], q[nt][ks][0], q[nt][ks][1]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
+    line_softmax<NT>(s, ok0, ok1, sc, kLift, ls, [&](int nt, float f0, float f1) {
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i) {
+        o[nt][i][0] *= f0, o[nt][i][2] *= f0;
+        o[nt][i][1] *= f1, o[nt][i][3] *= f1;
+      }
+    });
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) p[nt][h] = transpose8(pack2<kBf16>(s[nt][2 * h], s[nt][2 * h + 1]));
+#pragma unroll
+    for (int mt = 0; mt < kAcc; ++mt) {
+      uint32_t x[4];
+      ldsm_x4_t(st + 16 * kRow + at(r + 8 * (mi >> 1), 2 * mt + (mi & 1)), x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_16816<kBf16>(o[nt][mt], x[0], x[1], x[2], x[3], p[nt][0], p[nt][1]);
+    }
+  }
+  // dimension of accumulator i, element pair h (rows g and g + 8)
+  static __device__ __forceinline__ int dim_of(int i, int h, int g) { return 16 * i + g + 8 * h; }
+};
+
+// ------------------------------------------------------------------------------------------------
+// fp32 pools: products on CUDA cores, in 32 bits throughout.  A lane has the scores of its two tokens and two heads
+// (16 products for four 16-byte reads), and of its two heads D / 8 dimensions of the output; weights pass through
+// shared memory.
+// ------------------------------------------------------------------------------------------------
+template <int D, int NT>
+struct FloatRows {
+  using Out = float;
+  static constexpr int kWarps = 4, kCtas = 1;
+  static constexpr int kStages = D == 128 ? (NT == 2 ? 2 : 3) : 4;
+  static constexpr int kRow = 4 * D;
+  static constexpr int kStage = 2 * 16 * kRow;
+  static constexpr int kQuery = NT * 8 * kRow;               // a warp's queries
+  static constexpr int kExtra = kQuery + NT * 16 * 8 * 4;    // and the weights of a step, [nt][token][head]
+  static constexpr float kLift = kLineLift;
+  static constexpr int kAcc = D / 16;
+
+  const float* k;
+  const float* v;
+  uint32_t own;
+
+  __device__ __forceinline__ FloatRows(const LineArgs& a, uint32_t extra)
+      : k(static_cast<const float*>(a.k)), v(static_cast<const float*>(a.v)), own(extra) {}
+
+  // 4-element chunk c of token (or head) t: rows of a chunk read together lie in different banks
+  static __device__ __forceinline__ uint32_t at(int t, int c) { return (uint32_t)(t * kRow + ((c ^ (t & 7)) << 4)); }
+
+  __device__ __forceinline__ void load(const LineArgs&, uint32_t st, int lane, const int64_t (&row)[2],
+                                       const bool (&ok)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = (lane >> 2) + 8 * h;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const int c = (lane & 3) + 4 * i;
+        copy_async<16>(st + at(t, c), k + row[h] + 4 * c, ok[h]);
+        copy_async<16>(st + 16 * kRow + at(t, c), v + row[h] + 4 * c, ok[h]);
+      }
+    }
+  }
+  static __device__ __forceinline__ int64_t row_of(const LineArgs& a, int block, int token, int h) {
+    return block * a.block_stride + (int64_t)(token * a.n_kv_heads + h) * D;
+  }
+
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane) {
+    __syncwarp();
+    for (int i = lane; i < NT * 8 * (D / 4); i += 32) {
+      const int h = i / (D / 4), c = i % (D / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (h < a.group) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (head0 + h) * D + 4 * c);
+      sts128(own + at(h, c), x);
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, float sc, LineState<NT>& ls,
+                                       float (&o)[NT][kAcc][4]) const {
+    const int g = lane >> 2, tig = lane & 3;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 4; ++c) {
+      const float4 k0 = lds128(st + at(g, c)), k1 = lds128(st + at(g + 8, c));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 x = lds128(own + at(nt * 8 + 2 * tig + e, c));
+          s[nt][e] = dot4(x, k0, s[nt][e]);
+          s[nt][2 + e] = dot4(x, k1, s[nt][2 + e]);
+        }
+    }
+    line_softmax<NT>(s, ok0, ok1, sc, kLift, ls, [&](int nt, float f0, float f1) {
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i) {
+        o[nt][i][0] *= f0, o[nt][i][2] *= f0;
+        o[nt][i][1] *= f1, o[nt][i][3] *= f1;
+      }
+    });
+    const uint32_t ps = own + kQuery;
+    __syncwarp();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sts64(ps + (nt * 16 + g + 8 * h) * 32 + 8 * tig, s[nt][2 * h], s[nt][2 * h + 1]);
+    __syncwarp();
+#pragma unroll 4
+    for (int t = 0; t < 16; ++t) {
+      float4 x[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) x[i] = lds128(st + 16 * kRow + at(t, g + 8 * i));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint2 w = lds64(ps + (nt * 16 + t) * 32 + 8 * tig);
+        const float p0 = __uint_as_float(w.x), p1 = __uint_as_float(w.y);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {  // dimensions 32 i + 4 g .. + 3: accumulators 2 i and 2 i + 1
+          float(&u)[4] = o[nt][2 * i];
+          float(&y)[4] = o[nt][2 * i + 1];
+          u[0] = fmaf(p0, x[i].x, u[0]), u[1] = fmaf(p1, x[i].x, u[1]);
+          u[2] = fmaf(p0, x[i].y, u[2]), u[3] = fmaf(p1, x[i].y, u[3]);
+          y[0] = fmaf(p0, x[i].z, y[0]), y[1] = fmaf(p1, x[i].z, y[1]);
+          y[2] = fmaf(p0, x[i].w, y[2]), y[3] = fmaf(p1, x[i].w, y[3]);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ int dim_of(int i, int h, int g) { return 32 * (i >> 1) + 4 * g + 2 * (i & 1) + h; }
+};
+
+// ------------------------------------------------------------------------------------------------
+// The 4-bit cache
+// ------------------------------------------------------------------------------------------------
+template <typename T, int D, int NT>
+struct PackedRows {
+  using Out = T;
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value, kHalf = std::is_same<T, __half>::value;
+  static constexpr bool kWide = sizeof(T) == 4;                   // fp32 queries
+  static constexpr int kQParts = kWide ? 3 : 1;                   // bf16 parts of a query
+  static constexpr int kPParts = kWide ? 3 : (kHalf ? 2 : 1);     // bf16 parts of a weight
+  static constexpr int kWarps = 8, kCtas = kWide || NT == 2 ? 1 : 2;
+  static constexpr int kStages = 4;
+  static constexpr int kGroups = D / kQ4Group;
+  static constexpr int kRow = D / 2;                // bytes of a token's codes
+  static constexpr int kPair = 4 * kGroups;         // and of its scales and zeros
+  static constexpr int kParams = 2 * 16 * kRow;     // K codes, V codes, K params, V params
+  static constexpr int kStage = kParams + 2 * 16 * kPair;
+  static constexpr int kExtra = 0;
+  static constexpr float kLift = kLineLift;
+  static constexpr int kAcc = D / 16;
+
+  const uint8_t *kc, *vc, *kp, *vp;
+  uint32_t q[NT][kQParts][kGroups][4][2];
+  float sum_q[NT][kGroups][2];  // sums of a group's query values, heads 2 tig, 2 tig + 1
+
+  __device__ __forceinline__ PackedRows(const LineArgs& a, uint32_t)
+      : kc(static_cast<const uint8_t*>(a.k)), vc(static_cast<const uint8_t*>(a.v)),
+        kp(static_cast<const uint8_t*>(a.k_params)), vp(static_cast<const uint8_t*>(a.v_params)) {}
+
+  // Byte x of the codes of the token in place t: halves of 32 bytes trade places in every second pair of rows, so that
+  // four rows' halves lie in different banks.
+  static __device__ __forceinline__ uint32_t at(int t, int x) {
+    return (uint32_t)(t * kRow + (kGroups == 2 ? x ^ ((t & 2) << 4) : x));
+  }
+  // Place of token t's V codes: even tokens first, because a lane's tokens of a product are two apart.
+  static __device__ __forceinline__ int v_place(int t) { return (t & 8) | ((t & 1) << 2) | ((t >> 1) & 3); }
+
+  __device__ __forceinline__ void load(const LineArgs&, uint32_t st, int lane, const int64_t (&row)[2],
+                                       const bool (&ok)[2]) const {
+    constexpr int kPiece = kRow / 4;
+    const int c = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = (lane >> 2) + 8 * h;
+      copy_async<kPiece>(st + at(t, c * kPiece), kc + row[h] * kRow + c * kPiece, ok[h]);
+      copy_async<kPiece>(st + 16 * kRow + at(v_place(t), c * kPiece), vc + row[h] * kRow + c * kPiece, ok[h]);
+    }
+    // K's and V's pairs of the two tokens, one of the four a lane
+    const int64_t r = c & 1 ? row[1] : row[0];
+    const bool have = c & 1 ? ok[1] : ok[0];
+    copy_async<kPair>(st + kParams + (c & 2 ? 16 * kPair : 0) + ((lane >> 2) + 8 * (c & 1)) * kPair,
+                      (c & 2 ? vp : kp) + r * kPair, have);
+  }
+  static __device__ __forceinline__ int64_t row_of(const LineArgs& a, int block, int token, int h) {
+    return (int64_t)(((int64_t)block << a.block_shift) + token) * a.n_kv_heads + h;
+  }
+
+  // Lane (g, tig) has the values of dimensions 16 tig .. + 15 of each group of head g; product j of a group takes those
+  // at j and j + 4 (the low and the high half of a word of codes), and at j + 8 and j + 12.
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane) {
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool have = nt * 8 + g < a.group;
+      const T* p = static_cast<const T*>(a.q) + (head0 + nt * 8 + g) * D + 16 * tig;
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr) {
+        float x[16];
+        if constexpr (kWide) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = have ? *reinterpret_cast<const float4*>(p + gr * kQ4Group + 4 * i) : make_float4(0, 0, 0, 0);
+            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = have ? *reinterpret_cast<const uint4*>(p + gr * kQ4Group + 8 * i) : make_uint4(0, 0, 0, 0);
+            Elt<T>::unpack(v, *reinterpret_cast<float(*)[8]>(&x[8 * i]));
+          }
+        }
+        float part = 0.f;  // of head g; the sums are needed by the lanes that have it as a column
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part += x[i];
+        part += __shfl_xor_sync(0xffffffffu, part, 1);
+        part += __shfl_xor_sync(0xffffffffu, part, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sum_q[nt][gr][e] = __shfl_sync(0xffffffffu, part, (2 * tig + e) * 4);
+#pragma unroll
+        for (int w = 0; w < kQParts; ++w)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float &u = x[8 * h + j], &v = x[8 * h + j + 4];
+              const uint32_t both = pack2<!kHalf>(u, v);
+              q[nt][w][gr][j][h] = both;
+              if constexpr (kWide) {  // what is left, exactly
+                u -= __uint_as_float(both << 16);
+                v -= __uint_as_float(both & 0xffff0000u);
+              }
+            }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, float sc, LineState<NT>& ls,
+                                       float (&o)[NT][kAcc][4]) const {
+    const int g = lane >> 2, tig = lane & 3;
+    // ---- scores ----
+    uint32_t pair[2][kGroups];  // K's (scale, zero) of tokens g and g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t p = st + kParams + (g + 8 * h) * kPair;
+      if constexpr (kGroups == 2) {
+        const uint2 v = lds64(p);
+        pair[h][0] = v.x, pair[h][1] = v.y;
+      } else {
+        pair[h][0] = lds32(p);
+      }
+    }
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      uint2 w[2];  // 16 codes of tokens g and g + 8
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[h] = lds64(st + at(g + 8 * h, 32 * gr + 8 * tig));
+      float c0[NT][4], c1[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c0[nt][i] = c1[nt][i] = 0.f;
+      uint32_t bias[2];  // 128 + zero, twice
+      if constexpr (kWide) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float b = q4_zero(pair[h][gr]) + kCodeBias;
+          bias[h] = (__float_as_uint(b) >> 16) | __float_as_uint(b);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t x[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (kHalf) {  // code * 2^-24 (even j) and code * 2^-20
+            const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
+            x[h] = (j < 2 ? w[h].x : w[h].x >> 8) & mask;
+            x[2 + h] = (j < 2 ? w[h].y : w[h].y >> 8) & mask;
+          } else {
+            x[h] = code_bf16(w[h].x, j);
+            x[2 + h] = code_bf16(w[h].y, j);
+            if constexpr (kWide) {
+              x[h] = sub_bf16x2(x[h], bias[h]);
+              x[2 + h] = sub_bf16x2(x[2 + h], bias[h]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int p = 0; p < kQParts; ++p)
+            mma_16816<!kHalf>(j & 1 ? c1[nt] : c0[nt], x[0], x[1], x[2], x[3], q[nt][p][gr][j][0], q[nt][p][gr][j][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pr = pair[i >> 1][gr];
+          float dot;  // sum of q * (code - zero)
+          if constexpr (kWide) dot = c0[nt][i] + c1[nt][i];
+          else if constexpr (kHalf)
+            dot = fmaf(-q4_zero(pr), sum_q[nt][gr][i & 1], fmaf(c1[nt][i], 1048576.f, c0[nt][i] * 16777216.f));
+          else dot = fmaf(-(q4_zero(pr) + kCodeBias), sum_q[nt][gr][i & 1], c0[nt][i] + c1[nt][i]);
+          s[nt][i] = fmaf(q4_scale(pr), dot, s[nt][i]);
+        }
+    }
+    line_softmax<NT>(s, ok0, ok1, sc, kLift, ls, [&](int nt, float f0, float f1) {
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i) {
+        o[nt][i][0] *= f0, o[nt][i][2] *= f0;
+        o[nt][i][1] *= f1, o[nt][i][3] *= f1;
+      }
+    });
+    // ---- values ----
+    const uint32_t vst = st + 16 * kRow, vps = st + kParams + 16 * kPair;
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      // weights times scales, transposed: rows heads, columns tokens
+      const float sv[2] = {q4_scale(lds32(vps + g * kPair + 4 * gr)), q4_scale(lds32(vps + (g + 8) * kPair + 4 * gr))};
+      uint32_t p[NT][kPParts][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float u = s[nt][2 * h] * sv[h], v = s[nt][2 * h + 1] * sv[h];
+          // (a weight of 0 with a scale that is not finite belongs to no token or is 0 * NaN as the formula has it)
+#pragma unroll
+          for (int w = 0; w < kPParts; ++w) {
+            const uint32_t both = pack2<true>(u, v);
+            p[nt][w][h] = transpose8(both);
+            u -= __uint_as_float(both << 16);
+            v -= __uint_as_float(both & 0xffff0000u);
+          }
+        }
+      // tokens 2 tig and 2 tig + 1, then those 8 further on: 128 + zero of both, and the codes with the tokens of a pair
+      // in the halves of a word
+      uint32_t bias[2], m[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = 2 * tig + 8 * h;
+        const uint32_t za = lds32(vps + t * kPair + 4 * gr), zb = lds32(vps + (t + 1) * kPair + 4 * gr);
+        uint32_t z = __byte_perm(za, zb, 0x7632);
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(bias[h]) : "r"(z), "r"(0x43004300u));
+        const uint32_t ca = lds32(vst + at(v_place(t), 32 * gr + 4 * g));
+        const uint32_t cb = lds32(vst + at(v_place(t + 1), 32 * gr + 4 * g));
+        m[h][0] = __byte_perm(ca, cb, 0x5410);
+        m[h][1] = __byte_perm(ca, cb, 0x7632);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t x[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[2 * h] = sub_bf16x2(code_bf16(m[h][0], j), bias[h]);
+          x[2 * h + 1] = sub_bf16x2(code_bf16(m[h][1], j), bias[h]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float(&acc)[4] = o[nt][4 * gr + j];
+          if constexpr (kWide) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = kPParts - 1; w >= 0; --w) mma_16816<true>(d, x[0], x[1], x[2], x[3], p[nt][w][0], p[nt][w][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] += d[i];
+          } else {
+#pragma unroll
+            for (int w = 0; w < kPParts; ++w) mma_16816<true>(acc, x[0], x[1], x[2], x[3], p[nt][w][0], p[nt][w][1]);
+          }
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ int dim_of(int i, int h, int g) {
+    return kQ4Group * (i / 4) + 8 * g + (i & 3) + 4 * h;
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// The kernel
+// ------------------------------------------------------------------------------------------------
+template <typename Rows>
+struct LineCfg {
+  static constexpr int kThreads = Rows::kWarps * 32;
+  static constexpr int kRing = Rows::kWarps * (Rows::kStages * Rows::kStage + Rows::kExtra);
+};
+
+// Shared memory: the warps' rings (and what else a warp needs), then their states at the end of a unit, [warp][row][head_dim], [warp][row] twice.
+template <typename Rows, int D>
+constexpr int line_smem(int group) {
+  return LineCfg<Rows>::kRing + Rows::kWarps * group * (D + 2) * 4;
+}
+constexpr int kLineStatic = 256;  // TreeSched
+static_assert(sizeof(TreeSched) <= kLineStatic, "the schedule's shared memory");
+
+template <typename Rows, int D, int NT>
+__global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_decode_kernel(const LineArgs a) {
+  using T = typename Rows::Out;
+  constexpr int kWarps = Rows::kWarps, kStages = Rows::kStages, kThreads = LineCfg<Rows>::kThreads;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ TreeSched sched;
+  float* const out_o = reinterpret_cast<float*>(smem + LineCfg<Rows>::kRing);
+  float* const out_m = out_o + kWarps * a.group * D;
+  float* const out_l = out_m + kWarps * a.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lanes_head = kWarps / a.heads;  // warps of a KV head
+  const int head = warp / lanes_head, part = warp - head * lanes_head;
+  const int step_tokens = 16 * lanes_head;
+  if (threadIdx.x == 0) {
+    sched.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
+    sched.refused = 0;
+  }
+  __syncthreads();
+  pdl_wait_primary();
+  line_schedule<kThreads>(a, step_tokens, sched);
+  __syncthreads();
+  pdl_launch_dependents();
+  const TreeSpan span = sched.span;
+  if (a.split && threadIdx.x == 0) a.ws_rec[blockIdx.x] = TreeRec{0, 0, 0};
+
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * Rows::kStage + Rows::kExtra));
+  Rows rows(a, ring + kStages * Rows::kStage);
+
+  // ---- the loads, kStages - 1 steps ahead ----
+  LineWalk ahead(a, span, step_tokens);
+  LineUnit lu;
+  bool more = ahead.next(lu);
+  int lx = more ? lu.x0 : 0;
+  int block[2];
+  bool have[2];
+  unsigned oks = 0;  // two bits a step in flight: whether this lane's two tokens exist
+  auto position = [&](int v) { return v < lu.sq.first ? v : v + lu.sq.skip; };
+  auto token = [&](int h) { return (lx * lanes_head + part) * 16 + (lane >> 2) + 8 * h; };
+  auto look = [&]() {  // table entries of the next step
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int v = token(h);
+      have[h] = more && v < lu.sq.seen;
+      block[h] = have[h] ? ld_s32(a.block_table + lu.b * a.bt_stride + (position(v) >> a.block_shift)) : 0;
+    }
+  };
+  auto load = [&](int stage) {
+    if (more) {
+      int64_t row[2];
+      bool ok[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ok[h] = have[h];
+        if (have[h] && (block[h] < 0 || block[h] >= a.num_blocks)) {
+          raise_error(a.err, PA_DEVERR_BLOCK_ID);
+          ok[h] = false;
+        }
+        row[h] = ok[h] ? Rows::row_of(a, block[h], position(token(h)) & (a.block_size - 1), lu.hg * a.heads + head) : 0;
+      }
+      rows.load(a, ring + stage * Rows::kStage, lane, row, ok);
+      oks = oks << 2 | (ok[1] ? 2u : 0u) | (ok[0] ? 1u : 0u);
+      if (++lx == lu.x1) {
+        more = ahead.next(lu);
+        lx = more ? lu.x0 : 0;
+      }
+      look();
+    } else {
+      oks <<= 2;
+    }
+    copy_commit();
+  };
+  look();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load(s);
+
+  // ---- the products ----
+  LineWalk walk(a, span, step_tokens);
+  LineUnit w;
+  int stage = 0;
+  while (walk.next(w)) {
+    const int64_t head0 = (int64_t)w.b * a.n_q_heads + (int64_t)(w.hg * a.heads + head) * a.group;
+    rows.query(a, head0, lane);
+    LineState<NT> ls;
+    float o[NT][Rows::kAcc][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ls.m[nt][e] = -INFINITY;
+        ls.l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < Rows::kAcc; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+    }
+    for (int x = w.x0; x < w.x1; ++x) {
+      copy_wait<kStages - 2>();
+      __syncwarp();  // every lane's copies of this step are there, and the stage before has been read by all
+      const unsigned ok = oks >> (2 * (kStages - 2));
+      load(stage == 0 ? kStages - 1 : stage - 1);
+      rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, a.scale_log2, ls, o);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    // ---- the unit's end: the warps of a head joined ----
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = ls.l[nt][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        const int r = nt * 8 + 2 * tig + e;
+        if (r < a.group) {
+          float* p = out_o + (warp * a.group + r) * D;
+#pragma unroll
+          for (int i = 0; i < Rows::kAcc; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) p[Rows::dim_of(i, h, g)] = o[nt][i][2 * h + e];
+          if (g == 0) {
+            out_m[warp * a.group + r] = ls.m[nt][e];
+            out_l[warp * a.group + r] = l;
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = w.x0 == 0 && w.x1 == w.T;
+    const int unit_rows = a.heads * a.group;
+    const int64_t row0 = (int64_t)w.b * a.n_q_heads + (int64_t)w.hg * unit_rows;
+    const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * unit_rows;
+    for (int i = threadIdx.x; i < unit_rows * D; i += kThreads) {
+      const int r = i / D, d = i - r * D;
+      const int w0 = r / a.group * lanes_head, rr = r - r / a.group * a.group;
+      float M = -INFINITY, L = 0.f, A = 0.f;
+      for (int k = 0; k < lanes_head; ++k) M = fmaxf(M, out_m[(w0 + k) * a.group + rr]);
+      if (M != -INFINITY) {
+        for (int k = 0; k < lanes_head; ++k) {
+          const int at = (w0 + k) * a.group + rr;
+          const float f = fast_exp2((out_m[at] - M) * a.scale_log2);
+          L = fmaf(out_l[at], f, L);
+          A = fmaf(out_o[at * D + d], f, A);
+        }
+      }
+      if (whole) {
+        static_cast<T*>(a.out)[(row0 + r) * D + d] = Elt<T>::from_float(M == -INFINITY ? 0.f : A / L);
+      } else {
+        a.ws_acc[(slot0 + r) * D + d] = A;
+        if (d == 0) {
+          a.ws_m[slot0 + r] = M;
+          a.ws_l[slot0 + r] = L;
+        }
+      }
+    }
+    if (!whole && w.x0 == 0 && threadIdx.x == 0) {
+      // the CTA that the unit's last step went to
+      int last = (sched.cut_start + w.T - 1) / sched.share;
+      if (tree_cut((int64_t)last * sched.share - sched.cut_start, w.T, sched.snap) == w.T) --last;
+      a.ws_rec[blockIdx.x] = TreeRec{row0, unit_rows, last};
+    }
+    __syncthreads();
+  }
+  copy_wait<0>();
+  // sequences that see nothing
+  if (sched.refused) {
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+      if (line_seq(a, b).seen != 0) continue;
+      uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)b * a.n_q_heads * D);
+      const int64_t n = (int64_t)a.n_q_heads * D * (int)sizeof(T) / 16;
+      for (int64_t i = threadIdx.x; i < n; i += kThreads) p[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Units cut between CTAs: one warp per row, all its pieces (the first in the second slot of the CTA that the unit
+// begins in, the others in the first slots of the CTAs after it).
+constexpr int kLjWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kLjWarps * 32) line_join_kernel(const LineArgs a) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.y;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const TreeRec rec = a.ws_rec[c];
+  const int r = blockIdx.x * kLjWarps + (threadIdx.x >> 5);
+  if (r >= rec.rows) return;
+  const int unit_rows = a.heads * a.group;
+  const int pieces = rec.last - c + 1;
+  auto piece = [&](int i) -> int64_t { return ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * unit_rows + r; };
+  float M = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) M = fmaxf(M, a.ws_m[piece(i)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const int64_t p = piece(i);
+    const float f = fast_exp2((a.ws_m[p] - base) * a.scale_log2);
+    L = fmaf(a.ws_l[p], f, L);
+    const float* x = a.ws_acc + p * D + lane * kPer;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = fmaf(x[k], f, acc[k]);
+  }
+  T* o = static_cast<T*>(a.out) + (rec.row0 + r) * D + lane * kPer;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) o[k] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[k] / L);
+}
+
+// ------------------------------------------------------------------------------------------------
+namespace {
+
+cudaLaunchConfig_t overlapped(dim3 grid, int threads, int smem, cudaStream_t s, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <typename Rows, int D, int NT>
+cudaError_t launch_rows(const LineArgs& a, cudaStream_t s) {
+  constexpr int most = line_smem<Rows, D>(8 * NT);
+  static_assert(most + kLineStatic <= 227 * 1024, "shared memory of a CTA");
+  static bool attr_set[64] = {};  // per instantiation and device; idempotent, so a race is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(line_decode_kernel<Rows, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      overlapped(dim3((unsigned)a.ctas), LineCfg<Rows>::kThreads, line_smem<Rows, D>(a.group), s, attr);
+  return cudaLaunchKernelEx(&cfg, line_decode_kernel<Rows, D, NT>, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_packed(const LineArgs& a, cudaStream_t s) {
+  return a.group > 8 ? launch_rows<PackedRows<T, D, 2>, D, 2>(a, s) : launch_rows<PackedRows<T, D, 1>, D, 1>(a, s);
+}
+template <typename T, int D>
+cudaError_t launch_full(const LineArgs& a, cudaStream_t s) {
+  return a.group > 8 ? launch_rows<FullRows<T, D, 2>, D, 2>(a, s) : launch_rows<FullRows<T, D, 1>, D, 1>(a, s);
+}
+
+template <int D>
+cudaError_t launch_float(const LineArgs& a, cudaStream_t s) {
+  return a.group > 8 ? launch_rows<FloatRows<D, 2>, D, 2>(a, s) : launch_rows<FloatRows<D, 1>, D, 1>(a, s);
+}
+
+template <typename Rows, int D>
+int resident(int group) {
+  const int fit = 228 * 1024 / (line_smem<Rows, D>(group) + kLineStatic + 1024);
+  return std::max(1, std::min(fit, Rows::kCtas));
+}
+template <int D, int NT>
+int resident_of(bool packed, pa_dtype dt, int group) {
+  if (packed)
+    return dt == PA_BF16   ? resident<PackedRows<__nv_bfloat16, D, NT>, D>(group)
+           : dt == PA_FP16 ? resident<PackedRows<__half, D, NT>, D>(group)
+                           : resident<PackedRows<float, D, NT>, D>(group);
+  return dt == PA_FP32 ? resident<FloatRows<D, NT>, D>(group) : resident<FullRows<__half, D, NT>, D>(group);
+}
+
+template <typename T>
+cudaError_t launch_join(const LineArgs& a, cudaStream_t s) {
+  const int rows = a.heads * a.group;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      overlapped(dim3((unsigned)((rows + kLjWarps - 1) / kLjWarps), (unsigned)a.ctas), kLjWarps * 32, 0, s, attr);
+  return a.head_dim == 64 ? cudaLaunchKernelEx(&cfg, line_join_kernel<T, 64>, a)
+                          : cudaLaunchKernelEx(&cfg, line_join_kernel<T, 128>, a);
+}
+
+}  // namespace
+
+int line_ctas(bool packed, pa_dtype dt, int head_dim, int group) {
+  if (head_dim == 64) return group > 8 ? resident_of<64, 2>(packed, dt, group) : resident_of<64, 1>(packed, dt, group);
+  return group > 8 ? resident_of<128, 2>(packed, dt, group) : resident_of<128, 1>(packed, dt, group);
+}
+
+cudaError_t launch_line_decode(const LineArgs& a, pa_dtype dt, bool packed, cudaStream_t s, int* launches) {
+  cudaError_t e = cudaErrorInvalidValue;
+  const bool d64 = a.head_dim == 64;
+  if (packed) {
+    if (dt == PA_BF16) e = d64 ? launch_packed<__nv_bfloat16, 64>(a, s) : launch_packed<__nv_bfloat16, 128>(a, s);
+    if (dt == PA_FP16) e = d64 ? launch_packed<__half, 64>(a, s) : launch_packed<__half, 128>(a, s);
+    if (dt == PA_FP32) e = d64 ? launch_packed<float, 64>(a, s) : launch_packed<float, 128>(a, s);
+  } else {
+    if (dt == PA_BF16) e = d64 ? launch_full<__nv_bfloat16, 64>(a, s) : launch_full<__nv_bfloat16, 128>(a, s);
+    if (dt == PA_FP16) e = d64 ? launch_full<__half, 64>(a, s) : launch_full<__half, 128>(a, s);
+    if (dt == PA_FP32) e = d64 ? launch_float<64>(a, s) : launch_float<128>(a, s);
+  }
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (!a.split) return e;
+  ++*launches;
+  switch (dt) {
+    case PA_BF16: return launch_join<__nv_bfloat16>(a, s);
+    case PA_FP16: return launch_join<__half>(a, s);
+    case PA_FP32: return launch_join<float>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pa

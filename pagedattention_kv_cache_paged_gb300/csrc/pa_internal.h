@@ -97,6 +97,10 @@ struct AttnArgs {
   const int64_t* slot_mapping;
   void* k_pool_w;                  // the pools again, writable
   void* v_pool_w;
+  // sliding window (the kernels' windowed forms only): a query at position p sees j > p - window and j < sinks; with
+  // query_start_loc, rows that belong to no sequence are left as they were
+  int window;
+  int sinks;
 };
 
 struct MergeArgs {
@@ -225,6 +229,89 @@ struct AcceptArgs {
   unsigned* err;
 };
 
+// Rows packed into the 4-bit cache (q4_common.cuh).
+struct Q4WriteArgs {
+  const void* k_new;
+  const void* v_new;
+  const int64_t* slot_mapping;
+  int64_t n_tokens;
+  void* k_codes;
+  void* v_codes;
+  void* k_params;
+  void* v_params;
+  int64_t total_slots;             // num_blocks * block_size
+  int row_lanes;                   // n_kv_heads * head_dim / 8 (values of a thread)
+  unsigned* err;
+};
+
+// Blocks of the 4-bit cache unpacked into pools.
+struct Q4UnpackArgs {
+  const void* k_codes;
+  const void* v_codes;
+  const void* k_params;
+  const void* v_params;
+  int64_t cache_blocks;
+  void* k_pool;
+  void* v_pool;
+  int64_t num_blocks;
+  const int64_t* pairs;            // (block of the cache, block of the pools)
+  int64_t n_pairs;
+  int block_words;                 // 32-bit words of codes in a block
+  int64_t block_stride;            // elements from one block of a pool to the next
+  unsigned* err;
+};
+
+// Decode over the visible part of a context (line_decode.cu): pools or the 4-bit cache.
+struct LineArgs {
+  void* out;
+  const void* q;
+  const void* k;                   // pool, or codes
+  const void* v;
+  const void* k_params;            // 4-bit cache
+  const void* v_params;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  int batch;
+  int64_t num_blocks;
+  int block_size;
+  int block_shift;                 // log2(block_size)
+  int64_t block_stride;            // elements from one block of a pool to the next
+  int window;
+  int sinks;
+  int32_t max_context;             // longest context that a table row and kTreeMaxContext allow
+  float scale_log2;                // scale * log2(e)
+  int n_q_heads;
+  int n_kv_heads;
+  int group;                       // n_q_heads / n_kv_heads
+  int head_dim;
+  int heads;                       // KV heads of a CTA
+  int units;                       // n_kv_heads / heads
+  // `ctas` CTAs that take `share` steps each (0: an equal share, at least min_share), units cut where needed if `split`;
+  // partial states and records as in TreeArgs, with heads * group rows a unit
+  int ctas;
+  int share;
+  int min_share;
+  int split;
+  struct TreeRec* ws_rec;
+  float* ws_m;
+  float* ws_l;
+  float* ws_acc;
+  unsigned* err;
+};
+
+// Warps of a CTA of the line decode (each takes 16 tokens of a KV head a step) and KV heads that it has side by side:
+// in the 4-bit cache up to eight, whose rows of 32 or 64 bytes lie next to one another.
+constexpr int line_warps(bool packed) { return packed ? 8 : 4; }
+inline int line_heads(bool packed, int n_kv_heads) {
+  int h = packed ? line_warps(true) : 1;
+  while (n_kv_heads % h != 0) h >>= 1;
+  return h;
+}
+// What a unit costs besides its steps, and the fewest steps that a CTA takes; shorter units are never cut.
+constexpr int kLineGap = 2;
+constexpr int line_min_share(bool packed) { return packed ? 4 : 4; }
+
 // Launchers: return cudaSuccess or the launch error.  `launches` is incremented per kernel.
 cudaError_t launch_kv_write(const KvWriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t s, int* launches);
@@ -240,6 +327,14 @@ cudaError_t launch_tree_split(const TreeArgs& a, pa_dtype dt, cudaStream_t s, in
 cudaError_t launch_tree_umma(const TreeArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 // Units cut between CTAs, after either.
 cudaError_t launch_tree_join(const TreeArgs& a, pa_dtype dt, int unit_rows, cudaStream_t s, int* launches);
+
+cudaError_t launch_kv_write_q4(const Q4WriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+cudaError_t launch_kv_unpack_q4(const Q4UnpackArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+cudaError_t launch_line_decode(const LineArgs& a, pa_dtype dt, bool packed, cudaStream_t s, int* launches);
+// CTAs of it that an SM holds.
+int line_ctas(bool packed, pa_dtype dt, int head_dim, int group);
+// The windowed form of the CUDA-core attention (every dtype and block size), decode and chunks.
+cudaError_t launch_attn_simt_window(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 
 // TMA view of a pool: 3-D tensor (column = n_kv_heads * head_dim, token in block, block) with the
 // pool's block stride, boxes of 64 columns x 16 tokens x 1 block, 128-byte swizzle.
