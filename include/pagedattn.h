@@ -390,7 +390,7 @@ PA_API int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t l
  *                   (a padded batch) are left as they were.
  *   window          >= 1; INT32_MAX hides nothing
  *   sinks           >= 0
- *   context_lens    int32 [batch], at most 2^31 - 4096 without query_start_loc
+ *   context_lens    int32 [batch], at most 2^31 - 4096
  *   scale           > 0, and finite times log2(e) as well (at most 2.35e38)
  * An empty context gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and NaN
  * included); a non-finite value that it sees gives non-finite outputs, a non-finite key those of its score.
@@ -400,8 +400,9 @@ PA_API int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t l
  *                   need one each.  With query_start_loc it is not used.
  *   opts            may be NULL.  kv_block_stride_bytes as for the decode call.  Without query_start_loc:
  *                   partition_tokens is the number of visible tokens that a block of threads takes, rounded up to
- *                   whole steps of 64 (0 = an equal share of the work).  With it, prefill_kernel: 0 or 1, CUDA
- *                   cores (2: PA_EUNSUPPORTED).
+ *                   whole steps of 64 (0 = an equal share of the work).  With it, prefill_kernel: 0 auto (tcgen05 for
+ *                   bf16/fp16 pools with block_size % 16 == 0, else CUDA cores), 1 CUDA cores, 2 tcgen05
+ *                   (PA_EUNSUPPORTED if the shape does not allow it).
  * A sequence whose context is negative or longer than its table row, or whose chunk is longer than its context, gives
  * zeros in its rows and is recorded as PA_DEVERR_CONTEXT_LEN (with query_start_loc PA_DEVERR_QUERY_LOC); table
  * entries outside the pool are masked and recorded as PA_DEVERR_BLOCK_ID.  Checked mode returns PA_ERANGE for each.

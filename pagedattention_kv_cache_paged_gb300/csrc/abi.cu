@@ -841,7 +841,7 @@ int validate_window(const int32_t* block_table, int64_t bt_stride, const int32_t
   int64_t reach = 0;  // (see validate_tables)
   for (int b = 0; b < batch; ++b) {
     const int64_t n = lens[(size_t)b];
-    if (n < 0 || n > bt_stride * block_size || (!query_start_loc && n > kTreeMaxContext)) return PA_ERANGE;
+    if (n < 0 || n > bt_stride * block_size || n > kTreeMaxContext) return PA_ERANGE;
     if (query_start_loc) {
       const int64_t m = (int64_t)qsl[(size_t)b + 1] - qsl[(size_t)b];
       if (m < 0 || m > n) return PA_ERANGE;
@@ -1017,7 +1017,8 @@ int window_impl(void* out, const void* q, const int32_t* query_start_loc, int64_
   unsigned* err = nullptr;
   if ((rc = device_info(&err, nullptr))) return rc;
   const int group = n_q_heads / n_kv_heads;
-  if (o.prefill_kernel == 2) return PA_EUNSUPPORTED;
+  const bool tc_ok = decode_tc_supported(dtype, block_size, head_dim, group, num_blocks);
+  if (o.prefill_kernel == 2 && !tc_ok) return PA_EUNSUPPORTED;
   if (checked()) {
     rc = validate_window(block_table, block_table_stride, context_lens, batch, num_blocks, block_size, window, sinks,
                          query_start_loc, total_q, s);
@@ -1050,7 +1051,8 @@ int window_impl(void* out, const void* q, const int32_t* query_start_loc, int64_
   a.window = window;
   a.sinks = sinks;
   int launches = 0;
-  cudaError_t e = launch_attn_simt_window(a, dtype, s, &launches);
+  cudaError_t e = tc_ok && o.prefill_kernel != 1 ? launch_prefill_umma_window(a, dtype, s, &launches)
+                                                 : launch_attn_simt_window(a, dtype, s, &launches);
   return finish(e, launches);
 }
 

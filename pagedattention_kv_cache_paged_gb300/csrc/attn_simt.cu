@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(const AttnAr
     len = n - (q1 - q0) + (row - q0) + 1;  // causal bound of query r = row - q0
     if constexpr (kWindow) {  // rows before the first sequence and behind the last one are left as they were
       if (row < q0 || (b == a.batch - 1 && row >= q1)) return;
-      if (n < q1 - q0 || n > max_len) len = 0;
+      if (n < q1 - q0 || n > max_len || n > kTreeMaxContext) len = 0;
     }
     if (row < q0 || row >= q1 || len < 1) {
       if (threadIdx.x == 0) raise_error(a.err, PA_DEVERR_QUERY_LOC);
