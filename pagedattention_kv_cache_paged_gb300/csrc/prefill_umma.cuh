@@ -38,12 +38,14 @@
 //              the new S_k also covers that P V, so O_k is stable whenever a group sees a new S_k
 //              and rescaling needs no extra wait.
 // Windowed form (kWindow; paged_attention_window): a query at position p attends to j > p - window and j < sinks.
-// An item's tiles are those that hold sinks and those from its first row's window on; the tiles between them, and
-// 16-key sub-tiles that no row of the segment sees, are neither loaded nor looked up.  Tiles that the window's lower end
-// or the sinks' end falls into take the general mask.  A masked value cannot be deselected in a product (0 * NaN), so in
-// every tile that some row of the item sees only in part non-finite elements of V are zeroed in shared memory and, at
-// the item's end, added, by themselves, to the rows that see them.  The stabiliser is an unscaled score (see
-// tree_umma.cu for why, and for the lift of fp16 weights).  Rows that belong to no sequence are not written.
+// An item's keys are the 16-key sub-tiles that hold sinks and those from its first row's window on, packed into tiles
+// without a gap (a sub-tile is a box of its own anyway); nothing else is loaded or looked up.  Tiles that the window's
+// lower end or the sinks' end falls into take the general mask.  The stabiliser is an unscaled score (see tree_umma.cu
+// for why, and for the lift of fp16 weights).  Rows that belong to no sequence are not written.
+// A masked value cannot be deselected in a product (0 * NaN): a row's outputs may be non-finite because of a value that
+// another row of the item sees.  Looking through V for that in every tile that some row sees in part cost a quarter of
+// the time, so it is looked for in the results: a CTA that has written a non-finite output goes through its rows again
+// at its end, and recomputes those whose own keys do not explain it (um_mend).
 // Every mbarrier wait is bounded (PA_DEVERR_TIMEOUT, with a cooperative abort); TMEM is always
 // released.  The stabilising maximum is exact bookkeeping: numerator and denominator use the
 // same one, so the result equals the running-max form of "Online Softmax" in real arithmetic.
@@ -306,15 +308,6 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& v) {
   return (r & 0x7fff7fffu) != 0u;
 }
 
-// A pair of them with its non-finite halves replaced by zero.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
-  constexpr uint32_t e = kBf16 ? 0x7f80u : 0x7c00u;
-  if ((w & e) == e) w &= 0xffff0000u;
-  if (((w >> 16) & e) == e) w &= 0x0000ffffu;
-  return w;
-}
-
 // Sequence of query row t: the largest b < batch with qsl[b] <= t, searched by one thread with
 // rounds of 8 independent loads (three rounds for batch <= 512).
 __device__ __forceinline__ int find_sequence_8(const int32_t* qsl, int batch, int t) {
@@ -333,6 +326,83 @@ __device__ __forceinline__ int find_sequence_8(const int32_t* qsl, int batch, in
     lo = nlo;
   }
   return lo;
+}
+
+// Windowed form, after the CTA's last item: its outputs that are not finite are kept where a value that the row sees, or
+// a score of it, is not finite either; the others come from a product of weight 0 with another row's value, and the
+// row is computed again, on CUDA cores.  A warp takes a row, a lane D / 32 of its columns; keys from the row's own
+// down, so that a row of a model that has diverged is explained by the first.
+template <typename T, int D, int G>
+__device__ __noinline__ void um_mend(const AttnArgs& a, int max_len) {
+  constexpr int kQB = kUmRows / G, kPer = D / 32;
+  const int rows = (int)a.rows;
+  const int n_items = (rows + kQB - 1) / kQB * a.n_kv_heads;
+  const int lane = threadIdx.x & 31;
+  for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+    const int kvh = w % a.n_kv_heads, T0 = w / a.n_kv_heads * kQB;
+    for (int r = threadIdx.x >> 5; r < kUmRows; r += kUmThreads / 32) {
+      const int tok = T0 + r / G;
+      if (tok >= rows) break;
+      const int b = find_sequence(a.query_start_loc, a.batch, tok);
+      const int q0 = ld_nc_s32(a.query_start_loc + b), q1 = ld_nc_s32(a.query_start_loc + b + 1);
+      const int n = ld_nc_s32(a.context_lens + b);
+      if (tok < q0 || tok >= q1 || n < q1 - q0 || n > max_len) continue;
+      const int64_t at = ((int64_t)tok * a.n_q_heads + kvh * G + r % G) * D + lane * kPer;
+      T* out = static_cast<T*>(a.out) + at;
+      bool open[kPer];  // columns to explain
+      bool any = false;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        open[c] = !(fabsf(static_cast<float>(out[c])) <= FLT_MAX);
+        any |= open[c];
+      }
+      if (!__any_sync(0xffffffffu, any)) continue;
+      const int pos = n - (q1 - q0) + (tok - q0);
+      const int low = max(pos + 1 - a.window, 0), first = min(a.sinks, low);
+      const int32_t* table = a.block_table + (int64_t)b * a.bt_stride;
+      float q[kPer], acc[kPer];
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        q[c] = static_cast<float>(static_cast<const T*>(a.q)[at + c]);
+        acc[c] = 0.f;
+      }
+      float m = -INFINITY, l = 0.f;
+      bool keep = false;  // a score is not finite, or every column is explained
+      for (int j = pos; j >= 0 && !keep; --j) {
+        if (j < low && j >= first) j = first - 1;
+        if (j < 0) break;
+        const int blk = ld_nc_s32(table + (j >> a.block_shift));
+        if (blk < 0 || blk >= a.num_blocks) continue;
+        const int64_t src = (int64_t)blk * a.kv_block_stride +
+                            ((int64_t)(j & (a.block_size - 1)) * a.n_kv_heads + kvh) * D + lane * kPer;
+        const T* k = static_cast<const T*>(a.k_pool) + src;
+        const T* v = static_cast<const T*>(a.v_pool) + src;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) s = fmaf(q[c], static_cast<float>(k[c]), s);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        const float m_new = fmaxf(m, fmaxf(s, -FLT_MAX));
+        const float f = fast_exp2((m - m_new) * a.scale_log2), p = fast_exp2((s - m_new) * a.scale_log2);
+        m = m_new;
+        l = fmaf(l, f, p);
+        any = false;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+          const float x = static_cast<float>(v[c]);
+          acc[c] = fmaf(p, x, acc[c] * f);
+          if (!(fabsf(x) <= FLT_MAX)) open[c] = false;
+          any |= open[c];
+        }
+        // (the scores are the same in every lane; +inf has the weight NaN)
+        keep = s != s || s == INFINITY || !__any_sync(0xffffffffu, any);
+      }
+      if (keep) continue;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c)
+        if (open[c]) out[c] = Elt<T>::from_float(m == -INFINITY ? 0.f : acc[c] / l);
+    }
+  }
 }
 
 template <typename T, int D, int G, bool kWindow>
@@ -373,8 +443,7 @@ __global__ void __launch_bounds__(kUmThreads)
   uint8_t* vs = ks + kUmKStages * Cfg::kKvBytes;   // [kUmVStages][V tile]
   static_assert(kUmKStages <= 4 && kUmVStages <= 4, "barrier slots");
   static_assert(576 + kUmSegSlots * 32 <= 1024 && 60 * 8 <= 512, "records and barriers fit their 1 KB slot");
-  // windowed: the last item (counted by the CTA) of each parity in whose tiles V held non-finite elements
-  volatile int* bad_item = reinterpret_cast<int*>(base + 832);
+  volatile int* bad_out = reinterpret_cast<int*>(base + 832);  // windowed: an output was not finite
 
   // Work items are (block of kQB query tokens, KV head) pairs; this CTA takes items blockIdx.x,
   // blockIdx.x + gridDim.x, ...  Query rows, positions and lengths all fit in int32
@@ -417,7 +486,7 @@ __global__ void __launch_bounds__(kUmThreads)
     }
     mbar_init(fin, 1);
     for (int s = 0; s < 8; ++s) mbar_init(&mready[s], 1);
-    if (kWindow) bad_item[0] = bad_item[1] = -1;
+    if (kWindow) *bad_out = 0;
     fence_barrier_init();
   }
   if (warp == 10) tmem_alloc(tmem_slot, kUmTmemCols);
@@ -458,32 +527,22 @@ __global__ void __launch_bounds__(kUmThreads)
     }
     return sg;
   };
-  // The segment's tiles in order: number of them, and the first key of tile i.  Windowed: tiles that hold sinks (if those
-  // end before the window begins), then tiles from the window's on.
-  auto sink_tiles = [&](const Seg& sg) -> int { return (min(a.sinks, sg.low) + kUmKeys - 1) / kUmKeys; };
-  auto tiles_of = [&](const Seg& sg) -> int {
-    const int end = (sg.kv_end + kUmKeys - 1) / kUmKeys;
+  // The segment's keys as a line of 16-key sub-tiles.  Windowed: those that hold sinks (if these end before the window
+  // begins), then those from the window's first key on.
+  struct Subs {
+    int sinks, skip, n;  // how many hold sinks, how many are left out behind them, how many in all
+  };
+  auto subs_of = [&](const Seg& sg) -> Subs {
+    const int end = (sg.kv_end + 15) >> 4;
     if constexpr (kWindow) {
-      const int ns = sink_tiles(sg);
-      return end - max(sg.low / kUmKeys, ns) + ns;
+      const int ns = (min(a.sinks, sg.low) + 15) >> 4, skip = max((sg.low >> 4) - ns, 0);
+      return Subs{ns, skip, end - skip};
     }
-    return end;
+    return Subs{0, 0, end};
   };
-  auto first_key = [&](const Seg& sg, int tile) -> int {
-    if constexpr (kWindow) {
-      const int ns = sink_tiles(sg);
-      if (tile >= ns) tile += max(sg.low / kUmKeys, ns) - ns;
-    }
-    return tile * kUmKeys;
-  };
-  // Windowed: whether some row of a segment whose first row lies at position `first` does not see all of the tile at kb.
-  auto cut_tile = [&](const Seg& sg, int first, int kb) -> bool {
-    return kb + kUmKeys > first + 1 || !(kb >= sg.kv_end - a.window || kb + kUmKeys <= a.sinks);
-  };
-  // whether some row of the segment may see one of the 16 keys from k0 on
-  auto wanted = [&](const Seg& sg, int k0) -> bool {
-    return k0 < sg.kv_end && (!kWindow || k0 < a.sinks || k0 + 16 > sg.low);
-  };
+  auto tiles_of = [&](const Seg& sg) -> int { return (subs_of(sg).n + kUmSub - 1) / kUmSub; };
+  // first key of sub-tile u
+  auto sub_key = [](const Subs& sb, int u) -> int { return 16 * (kWindow && u >= sb.sinks ? u + sb.skip : u); };
   // Segment record idx of the K producer's stream, read by the whole warp, which then releases the
   // slot (every reader releases a record as soon as it has read it, so the ring never holds up a
   // reader the K producer waits for).  ok = false: the wait gave up (nothing is read).
@@ -678,15 +737,16 @@ __global__ void __launch_bounds__(kUmThreads)
           }
           ++rec;
           const int32_t* table = a.block_table + (int64_t)sg.b * a.bt_stride;
-          const int nt = tiles_of(sg);
+          const Subs sb = subs_of(sg);
+          const int nt = (sb.n + kUmSub - 1) / kUmSub;
           // the table entries of a tile's 16-key sub-tiles (-1: past the segment's keys), read one
           // tile ahead so that their latency passes during the wait for the ring slot
           int ys[kUmSub];
           auto table_of = [&](int tile, int (&dst)[kUmSub]) {
 #pragma unroll
             for (int sub = 0; sub < kUmSub; ++sub) {
-              const int k0 = first_key(sg, tile) + sub * 16;
-              dst[sub] = wanted(sg, k0) ? ld_nc_s32(table + (k0 >> a.block_shift)) : -1;
+              const int u = tile * kUmSub + sub;
+              dst[sub] = u < sb.n ? ld_nc_s32(table + (sub_key(sb, u) >> a.block_shift)) : -1;
             }
           };
           if (nt > 0) table_of(0, ys);
@@ -702,8 +762,7 @@ __global__ void __launch_bounds__(kUmThreads)
             unsigned m = 0;
 #pragma unroll
             for (int sub = 0; sub < kUmSub; ++sub) {
-              const int k0 = first_key(sg, tile) + sub * 16;
-              if (wanted(sg, k0)) {
+              if (tile * kUmSub + sub < sb.n) {
                 if (ys[sub] < 0 || ys[sub] >= a.num_blocks) {
                   if (!is_v) raise_error(a.err, PA_DEVERR_BLOCK_ID);
                 } else {
@@ -727,7 +786,7 @@ __global__ void __launch_bounds__(kUmThreads)
 #pragma unroll
               for (int sub = 0; sub < kUmSub; ++sub) {
                 if (!((m >> sub) & 1u)) continue;
-                const int yo = (first_key(sg, tile) + sub * 16) & bmask;
+                const int yo = sub_key(sb, tile * kUmSub + sub) & bmask;
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
                   tma_load_3d(st + h * Cfg::kKvHalf + sub * 2048, map, kvh * D + h * 64, yo, ys[sub], &full[s]);
@@ -849,14 +908,12 @@ __global__ void __launch_bounds__(kUmThreads)
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     int i = 0;    // tiles of this CTA so far
     int rec = 0;  // segment records read
-    int item = 0;
     bool alive = true;
-    for (int w = blockIdx.x; w < n_items && alive; w += gridDim.x, ++item) {
+    for (int w = blockIdx.x; w < n_items && alive; w += gridDim.x) {
       const int kvh = w % a.n_kv_heads;
       const int T0 = w / a.n_kv_heads * kQB;
       const int T1 = min(T0 + kQB, rows);
-      Seg own{};         // windowed: the segment of this thread's row
-      int own_pos = -1;  // and the row's position
+      bool mine = true;  // windowed: this thread's row belongs to a sequence
       const int tok = T0 + row / G;
       const int head = kvh * G + row % G;
       const int i0 = i;
@@ -873,14 +930,15 @@ __global__ void __launch_bounds__(kUmThreads)
         const int bound = (sg.ok && tok >= t && tok < sg.seg1) ? sg.pos0 + (tok - sg.q0) : -1;
         const int low = kWindow ? bound + 1 - a.window : 0;  // first key of the row's window
         if constexpr (kWindow) {
-          if (tok >= t && tok < sg.seg1) {
-            own = sg;
-            own_pos = bound;
-          }
+          if (tok >= t && tok < sg.seg1) mine = sg.mine;
         }
-        const int nt = tiles_of(sg);
+        const Subs sb = subs_of(sg);
+        const int nt = (sb.n + kUmSub - 1) / kUmSub;
         for (int tile = 0; tile < nt; ++tile, ++i) {
-          const int kb = first_key(sg, tile);
+          // key of the tile's first column; windowed, a tile may begin with sub-tiles of sinks: columns below `split`
+          // are keys from tile * kUmKeys on, the others continue to kb + column
+          const int split = kWindow ? 16 * max(sb.sinks - tile * kUmSub, 0) : 0;
+          const int kb = kWindow && split < kUmKeys ? tile * kUmKeys + 16 * sb.skip : tile * kUmKeys;
           if (!__all_sync(0xffffffffu, mbar_wait(&mready[i & 7], (unsigned)((i >> 3) & 1), a.err, a.epoch))) {
             alive = false;
             break;
@@ -897,23 +955,32 @@ __global__ void __launch_bounds__(kUmThreads)
           const float sc = a.scale_log2;
           const unsigned all_sub = (1u << kUmSub) - 1u;
           // (windowed: whether the window's lower end and the sinks' end leave the tile alone in every row of the warp)
-          const bool uncut = !kWindow || __all_sync(0xffffffffu, kb >= low || kb + kUmKeys <= a.sinks);
+          const bool mixed = kWindow && split > 0 && split < kUmKeys;
+          const bool uncut = !kWindow || (!mixed && __all_sync(0xffffffffu, kb >= low || kb + kUmKeys <= a.sinks));
           const bool unmasked = __all_sync(0xffffffffu, loaded == all_sub && kb + kUmKeys - 1 <= bound) && uncut;
           uint32_t mask[kUmKeys / 32];
           {
-            const int lim = bound - kb;  // keys c <= lim are causal
-            const int nv = lim < 0 ? 0 : (lim >= kUmKeys ? kUmKeys : lim + 1);
+            // keys from k0 on that the row sees, 32 columns
+            auto seen = [&](int k0) -> uint32_t {
+              const int nv = bound - k0 + 1;  // causal
+              uint32_t m = nv >= 32 ? 0xFFFFFFFFu : (nv <= 0 ? 0u : ((1u << nv) - 1u));
+              if constexpr (kWindow) {  // from the window's first key on, and below the sinks' end
+                const int from = max(low - k0, 0), to = max(a.sinks - k0, 0);
+                m &= (from < 32 ? 0xFFFFFFFFu << from : 0u) | (to < 32 ? (1u << to) - 1u : 0xFFFFFFFFu);
+              }
+              return m;
+            };
 #pragma unroll
             for (int q = 0; q < kUmKeys / 32; ++q) {
-              const int lo = 32 * q;
-              const uint32_t cm = nv >= lo + 32 ? 0xFFFFFFFFu : (nv <= lo ? 0u : ((1u << (nv - lo)) - 1u));
               const uint32_t lm = (((loaded >> (2 * q)) & 1u) ? 0x0000FFFFu : 0u) |
                                   (((loaded >> (2 * q + 1)) & 1u) ? 0xFFFF0000u : 0u);
-              mask[q] = cm & lm;
-              if constexpr (kWindow) {  // from the window's first key on, and below the sinks' end
-                const int from = max(low - kb - lo, 0), to = max(a.sinks - kb - lo, 0);
-                mask[q] &= (from < 32 ? 0xFFFFFFFFu << from : 0u) | (to < 32 ? (1u << to) - 1u : 0xFFFFFFFFu);
+              mask[q] = seen(kb + 32 * q);
+              if (mixed) {
+                const int h = split - 32 * q;
+                const uint32_t head = h >= 32 ? 0xFFFFFFFFu : (h <= 0 ? 0u : (1u << h) - 1u);
+                mask[q] = (mask[q] & ~head) | (seen(tile * kUmKeys + 32 * q) & head);
               }
+              mask[q] &= lm;
             }
           }
           const uint32_t srow = tS(grp) + lane_base;
@@ -951,12 +1018,8 @@ __global__ void __launch_bounds__(kUmThreads)
             }
           }
           // group 0 zeroes V rows that hold no data or lie past the context (group 1's P V is issued
-          // after group 0's, so it sees the zeros too); windowed, also non-finite elements, in tiles that some row of the
-          // item sees only in part
-          bool edge = kb + kUmKeys > sg.n || loaded != all_sub;
-          if constexpr (kWindow)
-            edge |= sg.seg1 - t < T1 - T0 || cut_tile(sg, sg.pos0 + (t - sg.q0), kb);
-          if (grp == 0 && edge) {
+          // after group 0's, so it sees the zeros too)
+          if (grp == 0 && (kb + kUmKeys > sg.n || loaded != all_sub)) {
             if (!__all_sync(0xffffffffu, mbar_wait(&vfull[i % kUmVStages], (unsigned)((i / kUmVStages) & 1), a.err, a.epoch))) {
               alive = false;
               break;
@@ -965,17 +1028,8 @@ __global__ void __launch_bounds__(kUmThreads)
             for (int e = r; e < kUmKeys * 8 * kHalves; e += 128) {
               const int key = e / (8 * kHalves);
               const int c = e % (8 * kHalves);
-              uint4* at = reinterpret_cast<uint4*>(vst + sw_off(key, c, Cfg::kKvHalf));
-              if (kb + key >= sg.n || !((loaded >> (key >> 4)) & 1u)) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else if constexpr (kWindow) {
-                const uint4 x = *at;
-                if (any_nonfinite<kBf16>(x)) {
-                  *at = make_uint4(drop_nonfinite<kBf16>(x.x), drop_nonfinite<kBf16>(x.y), drop_nonfinite<kBf16>(x.z),
-                                   drop_nonfinite<kBf16>(x.w));
-                  bad_item[item & 1] = item;
-                }
-              }
+              if (kb + key >= sg.n || !((loaded >> (key >> 4)) & 1u))
+                *reinterpret_cast<uint4*>(vst + sw_off(key, c, Cfg::kKvHalf)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
@@ -997,29 +1051,7 @@ __global__ void __launch_bounds__(kUmThreads)
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t v[32];
         tmem_ld32_sync(tO(grp) + lane_base + c0, v);
-        if constexpr (kWindow) {
-          // the non-finite elements that were taken out of V, for the rows that see them
-          if (have && own.ok && bad_item[item & 1] == item) {
-            const int32_t* table = a.block_table + (int64_t)own.b * a.bt_stride;
-            const int nt = tiles_of(own);
-            for (int tile = 0; tile < nt; ++tile) {
-              const int kb = first_key(own, tile);
-              for (int pos = kb; pos < min(kb + kUmKeys, own_pos + 1); ++pos) {
-                if (pos <= own_pos - a.window && pos >= a.sinks) continue;
-                const int blk = ld_nc_s32(table + (pos >> a.block_shift));
-                if (blk < 0 || blk >= a.num_blocks) continue;
-                const T* vr = static_cast<const T*>(a.v_pool) + (int64_t)blk * a.kv_block_stride +
-                              ((int64_t)(pos & bmask) * a.n_kv_heads + kvh) * D + c0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  const float x = static_cast<float>(vr[j]);
-                  if (!(fabsf(x) <= FLT_MAX)) v[j] = __float_as_uint(__uint_as_float(v[j]) + x);
-                }
-              }
-            }
-          }
-        }
-        if (tok < T1 && (!kWindow || own.mine)) {
+        if (tok < T1 && (!kWindow || mine)) {
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
             float f[8];
@@ -1030,6 +1062,7 @@ __global__ void __launch_bounds__(kUmThreads)
             wv.y = pack2<kBf16>(f[2], f[3]);
             wv.z = pack2<kBf16>(f[4], f[5]);
             wv.w = pack2<kBf16>(f[6], f[7]);
+            if (kWindow && any_nonfinite<kBf16>(wv)) *bad_out = 1;
             *reinterpret_cast<uint4*>(orow + c0 + j) = wv;
           }
         }
@@ -1045,6 +1078,9 @@ __global__ void __launch_bounds__(kUmThreads)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kUmTmemCols);
+  }
+  if constexpr (kWindow) {
+    if (*bad_out != 0) um_mend<T, D, G>(a, max_len);
   }
 }
 
