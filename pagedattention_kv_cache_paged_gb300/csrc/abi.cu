@@ -1065,6 +1065,7 @@ int check_q4(const void* k_codes, const void* v_codes, const void* k_params, con
   if (!k_codes || !v_codes || !k_params || !v_params) return PA_EINVAL;
   if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_params) || !aligned16(v_params)) return PA_EINVAL;
   if ((int64_t)n_kv_heads * head_dim * block_size > INT32_MAX) return PA_EUNSUPPORTED;
+  if (num_blocks > ((int64_t(1) << 32) - 1) / ((int64_t)n_kv_heads * block_size)) return PA_EUNSUPPORTED;  // 32-bit rows
   return PA_OK;
 }
 

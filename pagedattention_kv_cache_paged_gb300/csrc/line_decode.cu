@@ -21,15 +21,9 @@
 // 16-bit pools: K and V^T fragments by ldmatrix, weights rounded to the pool's type for the product with V (as the
 // framework's other tensor-core kernels do; in fp16 formed 2^7 higher, see tree_umma.cu).
 //
-// 4-bit cache: codes become 16-bit operands with one or two logical instructions for two values and without any
-// conversion, since the order of a contraction is free: the dimensions (tokens) of an operand register are those
-// whose codes lie 16 bits apart.
-//   K: bf16 has (word & 0x000f000f) | 0x4300.. = 128 + code, and scale * (sum q (128 + code) - (128 + zero) sum q) is
-//      the score's part of a group; fp16 has code * 2^-24 (bits 0-3) and code * 2^-20 (bits 4-7) as they stand.
-//   V: 128 + code minus 128 + zero in bf16, both exact; weight * scale is rounded to bf16 (bf16 queries), or to two
-//      (fp16) or three (fp32) bf16 parts that hold its 16 or 24 bits.
-//   fp32 queries are three bf16 parts of 8 bits each and K is (code - zero), so products are exact, and each step's sums
-//   are formed by themselves and added up by rounded additions.
+// 4-bit cache: codes become 16-bit operands with a logical instruction or two for two values and without any conversion,
+// since the order of a contraction is free: the dimensions (tokens) of an operand register are those whose codes lie 16
+// bits apart.  See PackedRows (bf16 and fp16 queries) and PackedWideRows (fp32).
 #include <float.h>
 
 #include <algorithm>
@@ -236,6 +230,11 @@ __device__ __forceinline__ float4 lds128(uint32_t p) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 lds128u(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts128(uint32_t p, const float4& v) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
@@ -260,6 +259,12 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Nibble k (0 .. 3) of both halves of w as bf16: 128 + code.
 __device__ __forceinline__ uint32_t code_bf16(uint32_t w, int k) {
   return and_or(k == 0 ? w : w >> (4 * k), 0x000f000fu, 0x43004300u);
@@ -273,22 +278,27 @@ constexpr float kLineLift = -8.f;
 // A softmax row's state: a lane has heads 2 tig and 2 tig + 1 of every 8 (columns of the transposed products).
 template <int NT>
 struct LineState {
-  float m[NT][2];  // stabiliser (an unscaled score), the same in the lanes of a column
-  float l[NT][2];  // this lane's share of the sum
+  float sc[NT][2];  // exponent (base 2) of a weight per unit of score
+  float m[NT][2];   // stabiliser (a score), the same in the lanes of a column
+  float l[NT][2];   // this lane's share of the sum
 };
 
 // Weights of a step: s[nt][0..1] token g, [2..3] token g + 8 (rows), heads 2 tig, 2 tig + 1 (columns); ok0, ok1: whether
-// the two tokens exist.  Scores become weights; where a stabiliser moved, `rescale` is called with its factors.
+// the two tokens exist.  Scores become weights; where a stabiliser moved, or `more` of a lane asked for it,
+// `rescale(nt, f0, f1)` is called with the factors of the columns' accumulators.
 template <int NT, typename Rescale>
-__device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool ok1, float sc, float lift,
-                                             LineState<NT>& st, Rescale rescale) {
+__device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool ok1, float lift, LineState<NT>& st,
+                                             bool more, Rescale rescale) {
   constexpr float kGrow = 8.f;
-  bool move = false;
+  float x[NT][4];
+  bool move = more;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      move |= (i < 2 ? ok0 : ok1) && !((s[nt][i] - st.m[nt][i & 1]) * sc <= kGrow);  // (also at the start, and for NaN)
+    for (int i = 0; i < 4; ++i) {
+      x[nt][i] = (s[nt][i] - st.m[nt][i & 1]) * st.sc[nt][i & 1];
+      move |= (i < 2 ? ok0 : ok1) && !(x[nt][i] <= kGrow);  // (also at the start, and for NaN)
+    }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -300,9 +310,11 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         const float old = st.m[nt][e], m = fmaxf(old, mx);
-        f[e] = old == m ? 1.f : fast_exp2((old - m) * sc);
+        f[e] = old == m ? 1.f : fast_exp2((old - m) * st.sc[nt][e]);
         st.m[nt][e] = m;
         st.l[nt][e] *= f[e];
+        x[nt][e] = (s[nt][e] - m) * st.sc[nt][e];
+        x[nt][2 + e] = (s[nt][2 + e] - m) * st.sc[nt][e];
       }
       rescale(nt, f[0], f[1]);
     }
@@ -311,7 +323,7 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float p = (i < 2 ? ok0 : ok1) ? fast_exp2(fmaf(s[nt][i] - st.m[nt][i & 1], sc, lift)) : 0.f;
+      const float p = (i < 2 ? ok0 : ok1) ? fast_exp2(lift == 0.f ? x[nt][i] : x[nt][i] + lift) : 0.f;
       s[nt][i] = p;
       st.l[nt][i & 1] += p;
     }
@@ -323,6 +335,7 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
 template <typename T, int D, int NT>
 struct FullRows {
   using Out = T;
+  using Row = int64_t;  // offset of a row
   static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   static constexpr int kWarps = 4, kCtas = 3;
   static constexpr int kStages = D == 128 ? 2 : 4;
@@ -336,7 +349,7 @@ struct FullRows {
   const T* v;
   uint32_t q[NT][D / 16][2];
 
-  __device__ __forceinline__ FullRows(const LineArgs& a, uint32_t)
+  __device__ __forceinline__ FullRows(const LineArgs& a, uint32_t, int)
       : k(static_cast<const T*>(a.k)), v(static_cast<const T*>(a.v)) {}
 
   // 8-element chunk c of token t of an operand, in its place (ldmatrix reads eight rows of a chunk without conflicts)
@@ -361,7 +374,7 @@ struct FullRows {
     return block * a.block_stride + (int64_t)(token * a.n_kv_heads + h) * D;
   }
 
-  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane) {
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane, LineState<NT>& ls) {
     const int g = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -375,8 +388,8 @@ struct FullRows {
     }
   }
 
-  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, float sc, LineState<NT>& ls,
-                                       float (&o)[NT][kAcc][4]) const {
+  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, LineState<NT>& ls,
+                                       float (&o)[NT][kAcc][4]) {
     float s[NT][4], s2[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -395,7 +408,7 @@ struct FullRows {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
-    line_softmax<NT>(s, ok0, ok1, sc, kLift, ls, [&](int nt, float f0, float f1) {
+    line_softmax<NT>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
         o[nt][i][0] *= f0, o[nt][i][2] *= f0;
@@ -415,6 +428,7 @@ struct FullRows {
       for (int nt = 0; nt < NT; ++nt) mma_16816<kBf16>(o[nt][mt], x[0], x[1], x[2], x[3], p[nt][0], p[nt][1]);
     }
   }
+  __device__ __forceinline__ void finish(LineState<NT>&, float (&)[NT][kAcc][4]) const {}
   // dimension of accumulator i, element pair h (rows g and g + 8)
   static __device__ __forceinline__ int dim_of(int i, int h, int g) { return 16 * i + g + 8 * h; }
 };
@@ -427,6 +441,7 @@ struct FullRows {
 template <int D, int NT>
 struct FloatRows {
   using Out = float;
+  using Row = int64_t;
   static constexpr int kWarps = 4, kCtas = 1;
   static constexpr int kStages = D == 128 ? (NT == 2 ? 2 : 3) : 4;
   static constexpr int kRow = 4 * D;
@@ -440,7 +455,7 @@ struct FloatRows {
   const float* v;
   uint32_t own;
 
-  __device__ __forceinline__ FloatRows(const LineArgs& a, uint32_t extra)
+  __device__ __forceinline__ FloatRows(const LineArgs& a, uint32_t extra, int)
       : k(static_cast<const float*>(a.k)), v(static_cast<const float*>(a.v)), own(extra) {}
 
   // 4-element chunk c of token (or head) t: rows of a chunk read together lie in different banks
@@ -463,7 +478,7 @@ struct FloatRows {
     return block * a.block_stride + (int64_t)(token * a.n_kv_heads + h) * D;
   }
 
-  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane) {
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane, LineState<NT>& ls) {
     __syncwarp();
     for (int i = lane; i < NT * 8 * (D / 4); i += 32) {
       const int h = i / (D / 4), c = i % (D / 4);
@@ -474,8 +489,8 @@ struct FloatRows {
     __syncwarp();
   }
 
-  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, float sc, LineState<NT>& ls,
-                                       float (&o)[NT][kAcc][4]) const {
+  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, LineState<NT>& ls,
+                                       float (&o)[NT][kAcc][4]) {
     const int g = lane >> 2, tig = lane & 3;
     float s[NT][4];
 #pragma unroll
@@ -494,7 +509,7 @@ struct FloatRows {
           s[nt][2 + e] = dot4(x, k1, s[nt][2 + e]);
         }
     }
-    line_softmax<NT>(s, ok0, ok1, sc, kLift, ls, [&](int nt, float f0, float f1) {
+    line_softmax<NT>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
         o[nt][i][0] *= f0, o[nt][i][2] *= f0;
@@ -529,37 +544,28 @@ struct FloatRows {
       }
     }
   }
+  __device__ __forceinline__ void finish(LineState<NT>&, float (&)[NT][kAcc][4]) const {}
   static __device__ __forceinline__ int dim_of(int i, int h, int g) { return 32 * (i >> 1) + 4 * g + 2 * (i & 1) + h; }
 };
 
 // ------------------------------------------------------------------------------------------------
 // The 4-bit cache
 // ------------------------------------------------------------------------------------------------
-template <typename T, int D, int NT>
-struct PackedRows {
-  using Out = T;
-  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value, kHalf = std::is_same<T, __half>::value;
-  static constexpr bool kWide = sizeof(T) == 4;                   // fp32 queries
-  static constexpr int kQParts = kWide ? 3 : 1;                   // bf16 parts of a query
-  static constexpr int kPParts = kWide ? 3 : (kHalf ? 2 : 1);     // bf16 parts of a weight
-  static constexpr int kWarps = 8, kCtas = kWide || NT == 2 ? 1 : 2;
-  static constexpr int kStages = 4;
+
+// What both forms share: a step's codes, scales and zeros in shared memory.
+template <int D>
+struct PackedStage {
   static constexpr int kGroups = D / kQ4Group;
   static constexpr int kRow = D / 2;                // bytes of a token's codes
   static constexpr int kPair = 4 * kGroups;         // and of its scales and zeros
-  static constexpr int kParams = 2 * 16 * kRow;     // K codes, V codes, K params, V params
+  static constexpr int kParams = 2 * 16 * kRow;     // K codes, V codes, K pairs, V pairs
+  static constexpr int kVParams = kParams + 16 * kPair;
   static constexpr int kStage = kParams + 2 * 16 * kPair;
-  static constexpr int kExtra = 0;
-  static constexpr float kLift = kLineLift;
-  static constexpr int kAcc = D / 16;
+  static constexpr int kPiece = kRow / 4;           // a lane copies a quarter of a token's codes
+  using Row = uint32_t;  // number of a row; more than 2^32 rows do not fit the memory, and the host refuses them
 
-  const uint8_t *kc, *vc, *kp, *vp;
-  uint32_t q[NT][kQParts][kGroups][4][2];
-  float sum_q[NT][kGroups][2];  // sums of a group's query values, heads 2 tig, 2 tig + 1
-
-  __device__ __forceinline__ PackedRows(const LineArgs& a, uint32_t)
-      : kc(static_cast<const uint8_t*>(a.k)), vc(static_cast<const uint8_t*>(a.v)),
-        kp(static_cast<const uint8_t*>(a.k_params)), vp(static_cast<const uint8_t*>(a.v_params)) {}
+  const uint8_t *kc, *vc, *pairs;  // this lane's piece of row 0
+  uint32_t dk, dv, dp;             // and where pieces of its first token go
 
   // Byte x of the codes of the token in place t: halves of 32 bytes trade places in every second pair of rows, so that
   // four rows' halves lie in different banks.
@@ -569,90 +575,345 @@ struct PackedRows {
   // Place of token t's V codes: even tokens first, because a lane's tokens of a product are two apart.
   static __device__ __forceinline__ int v_place(int t) { return (t & 8) | ((t & 1) << 2) | ((t >> 1) & 3); }
 
-  __device__ __forceinline__ void load(const LineArgs&, uint32_t st, int lane, const int64_t (&row)[2],
-                                       const bool (&ok)[2]) const {
-    constexpr int kPiece = kRow / 4;
-    const int c = lane & 3;
+  __device__ __forceinline__ PackedStage(const LineArgs& a, int lane) {
+    const int c = lane & 3, t = lane >> 2;
+    kc = static_cast<const uint8_t*>(a.k) + c * kPiece;
+    vc = static_cast<const uint8_t*>(a.v) + c * kPiece;
+    pairs = static_cast<const uint8_t*>(c & 2 ? a.v_params : a.k_params);
+    dk = at(t, c * kPiece);
+    dv = 16 * kRow + at(v_place(t), c * kPiece);
+    dp = (c & 2 ? kVParams : kParams) + (t + 8 * (c & 1)) * kPair;
+  }
+  __device__ __forceinline__ void load(uint32_t st, int lane, const Row (&row)[2], const bool (&ok)[2]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int t = (lane >> 2) + 8 * h;
-      copy_async<kPiece>(st + at(t, c * kPiece), kc + row[h] * kRow + c * kPiece, ok[h]);
-      copy_async<kPiece>(st + 16 * kRow + at(v_place(t), c * kPiece), vc + row[h] * kRow + c * kPiece, ok[h]);
+      copy_async<kPiece>(st + dk + 8 * h * kRow, kc + (uint64_t)row[h] * kRow, ok[h]);
+      copy_async<kPiece>(st + dv + 8 * h * kRow, vc + (uint64_t)row[h] * kRow, ok[h]);
     }
     // K's and V's pairs of the two tokens, one of the four a lane
-    const int64_t r = c & 1 ? row[1] : row[0];
-    const bool have = c & 1 ? ok[1] : ok[0];
-    copy_async<kPair>(st + kParams + (c & 2 ? 16 * kPair : 0) + ((lane >> 2) + 8 * (c & 1)) * kPair,
-                      (c & 2 ? vp : kp) + r * kPair, have);
+    copy_async<kPair>(st + dp, pairs + (uint64_t)(lane & 1 ? row[1] : row[0]) * kPair, lane & 1 ? ok[1] : ok[0]);
   }
-  static __device__ __forceinline__ int64_t row_of(const LineArgs& a, int block, int token, int h) {
-    return (int64_t)(((int64_t)block << a.block_shift) + token) * a.n_kv_heads + h;
+  static __device__ __forceinline__ Row row_of(const LineArgs& a, int block, int token, int h) {
+    return (((Row)block << a.block_shift) + (Row)token) * (Row)a.n_kv_heads + (Row)h;
   }
+};
+
+// bf16 and fp16 queries: every operand is fp16, and the codes of two values become one by a single AND: bits 0-3 of a
+// half are the number code * 2^-24, bits 4-7 code * 2^-20 (what the words hold above them comes down by one shift).
+//
+// Queries.  A head's values are multiplied by the power of two that takes their largest to 2^14 .. 2^15, so that bf16's
+// become fp16 without loss but for those below 2^-29 of the largest; values that meet codes in bits 4-7 are taken 16 times
+// smaller.  With c, z, s a group's codes, zero and scale: score = sum over groups of s * (sum q c - z * sum q).
+//
+// Values.  weight * scale is rounded to fp16 after a power of two that keeps the largest scale of a group so far in
+// 2^5 .. 2^6 (its accumulators are rescaled when it moves, by the same vote as the stabiliser's), so that the smallest step
+// is 2^-30 of the largest product or less; O += C (w s), O += (-z) (w s), the zero as an operand of its own, whose rows
+// are the same.
+template <typename T, int D, int NT>
+struct PackedRows : PackedStage<D> {
+  using Out = T;
+  using Stage = PackedStage<D>;
+  using typename Stage::Row;
+  using Stage::kGroups, Stage::kRow, Stage::kPair, Stage::kParams, Stage::kVParams, Stage::at;
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kWarps = 8, kCtas = NT == 2 ? 1 : 2;
+  static constexpr int kStages = 4;
+  static constexpr int kExtra = 0;
+  static constexpr float kLift = 0.f;
+  static constexpr int kAcc = D / 16;
+
+  uint32_t q[NT][kGroups][4][2];
+  float sum_q[NT][kGroups][2];  // sums of a group's query values, heads 2 tig, 2 tig + 1, times 2^-24
+  float unit[NT][2];            // score of a head per unit of the above
+  float vk[kGroups];            // the power of two of the group's scales
+  uint32_t kb, vb, pb, zb;      // this lane's reads: codes of K and V, pairs, zeros
+
+  __device__ __forceinline__ PackedRows(const LineArgs& a, uint32_t, int lane) : Stage(a, lane) {
+    const int g = lane >> 2, tig = lane & 3;
+    kb = at(g, 8 * tig);
+    vb = 16 * kRow + at(tig, 4 * g);  // (place of token 2 tig)
+    pb = kParams + g * kPair;
+    zb = kVParams + 2 * tig * kPair;
+  }
+  __device__ __forceinline__ void load(const LineArgs&, uint32_t st, int lane, const Row (&row)[2],
+                                       const bool (&ok)[2]) const {
+    Stage::load(st, lane, row, ok);
+  }
+  // the other half of 32 bytes (group 1) of a row of codes
+  static __device__ __forceinline__ uint32_t half(uint32_t at0, int gr) { return gr ? at0 ^ 32u : at0; }
 
   // Lane (g, tig) has the values of dimensions 16 tig .. + 15 of each group of head g; product j of a group takes those
   // at j and j + 4 (the low and the high half of a word of codes), and at j + 8 and j + 12.
-  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane) {
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane, LineState<NT>& ls) {
     const int g = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool have = nt * 8 + g < a.group;
       const T* p = static_cast<const T*>(a.q) + (head0 + nt * 8 + g) * D + 16 * tig;
+      float x[kGroups][16];
+      float top = 0.f;
 #pragma unroll
       for (int gr = 0; gr < kGroups; ++gr) {
-        float x[16];
-        if constexpr (kWide) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 v = have ? *reinterpret_cast<const float4*>(p + gr * kQ4Group + 4 * i) : make_float4(0, 0, 0, 0);
-            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 v = have ? *reinterpret_cast<const uint4*>(p + gr * kQ4Group + 8 * i) : make_uint4(0, 0, 0, 0);
-            Elt<T>::unpack(v, *reinterpret_cast<float(*)[8]>(&x[8 * i]));
-          }
+        for (int i = 0; i < 2; ++i) {
+          const uint4 v = have ? *reinterpret_cast<const uint4*>(p + gr * kQ4Group + 8 * i) : make_uint4(0, 0, 0, 0);
+          Elt<T>::unpack(v, *reinterpret_cast<float(*)[8]>(&x[gr][8 * i]));
         }
-        float part = 0.f;  // of head g; the sums are needed by the lanes that have it as a column
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part += x[i];
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[gr][i]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(14 - exponent); an infinite query has scores that are not finite whatever the factor
+      const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 254);
+      const float f = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+      const float unit_g = __uint_as_float((uint32_t)min(e + 10, 254) << 23);  // 2^24 / f
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr) {
+        float part = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float step = j & 1 ? 0.0625f : 1.f;
+            const uint32_t both = pack2<false>(x[gr][8 * h + j] * f * step, x[gr][8 * h + j + 4] * f * step);
+            q[nt][gr][j][h] = both;
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&both));
+            part = fmaf(v.x + v.y, 1.f / step, part);
+          }
         part += __shfl_xor_sync(0xffffffffu, part, 1);
         part += __shfl_xor_sync(0xffffffffu, part, 2);
+        part *= 1.f / 16777216.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sum_q[nt][gr][e] = __shfl_sync(0xffffffffu, part, (2 * tig + e) * 4);
+        for (int i = 0; i < 2; ++i) sum_q[nt][gr][i] = __shfl_sync(0xffffffffu, part, (2 * tig + i) * 4);
+      }
 #pragma unroll
-        for (int w = 0; w < kQParts; ++w)
+      for (int i = 0; i < 2; ++i) {
+        unit[nt][i] = __shfl_sync(0xffffffffu, unit_g, (2 * tig + i) * 4);
+        ls.sc[nt][i] = fminf(ls.sc[nt][i] * unit[nt][i], FLT_MAX);
+      }
+    }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+    for (int gr = 0; gr < kGroups; ++gr) vk[gr] = 8.50705917302346159e37f;  // 2^126
+  }
+
+  __device__ __forceinline__ void step(uint32_t st, int, bool ok0, bool ok1, LineState<NT>& ls,
+                                       float (&o)[NT][kAcc][4]) {
+    // ---- scores ----
+    uint32_t pair[2][kGroups];  // (scale, zero) of tokens g and g + 8
+    auto read_pairs = [&](uint32_t p) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float &u = x[8 * h + j], &v = x[8 * h + j + 4];
-              const uint32_t both = pack2<!kHalf>(u, v);
-              q[nt][w][gr][j][h] = both;
-              if constexpr (kWide) {  // what is left, exactly
-                u -= __uint_as_float(both << 16);
-                v -= __uint_as_float(both & 0xffff0000u);
-              }
-            }
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (kGroups == 2) {
+          const uint2 v = lds64(p + 8 * h * kPair);
+          pair[h][0] = v.x, pair[h][1] = v.y;
+        } else {
+          pair[h][0] = lds32(p + 8 * h * kPair);
+        }
+      }
+    };
+    read_pairs(st + pb);
+    float s[NT][4];
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      uint2 w[2];  // 16 codes of tokens g and g + 8
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[h] = lds64(st + half(kb, gr) + 8 * h * kRow);
+      float dot[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dot[nt][i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
+        if (j == 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) w[h].x >>= 8, w[h].y >>= 8;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_16816<false>(dot[nt], w[0].x & mask, w[1].x & mask, w[0].y & mask, w[1].y & mask, q[nt][gr][j][0],
+                           q[nt][gr][j][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pr = pair[i >> 1][gr];
+          const float d = fmaf(-q4_zero(pr), sum_q[nt][gr][i & 1], dot[nt][i]);
+          s[nt][i] = gr == 0 ? q4_scale(pr) * d : fmaf(q4_scale(pr), d, s[nt][i]);
+        }
+    }
+    // ---- weights ----
+    read_pairs(st + pb + 16 * kPair);
+    float sv[2][kGroups];
+    bool large = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr) {
+        sv[h][gr] = q4_scale(pair[h][gr]) * vk[gr];
+        large |= sv[h][gr] > 64.f;
+      }
+    float old[kGroups];
+    line_softmax<NT>(s, ok0, ok1, kLift, ls, large, [&](int nt, float f0, float f1) {
+      if (nt == 0) {
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+          old[gr] = vk[gr];
+          const float s0 = q4_scale(pair[0][gr]), s1 = q4_scale(pair[1][gr]);
+          float top = fmaxf(s0, s1);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          if (top * vk[gr] > 64.f)
+            vk[gr] = __uint_as_float((uint32_t)(127 + 127 + 5 - (int)(__float_as_uint(top) >> 23)) << 23);
+          sv[0][gr] = s0 * vk[gr];
+          sv[1][gr] = s1 * vk[gr];
+        }
+      }
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr) {
+        const float g0 = f0 * (vk[gr] / old[gr]), g1 = f1 * (vk[gr] / old[gr]);
+#pragma unroll
+        for (int i = 4 * gr; i < 4 * gr + 4; ++i) {
+          o[nt][i][0] *= g0, o[nt][i][2] *= g0;
+          o[nt][i][1] *= g1, o[nt][i][3] *= g1;
+        }
+      }
+    });
+    // ---- values ----
+    // tokens 2 tig and 2 tig + 1, then those 8 further on: the zeros of both as halves of a word, whole numbers
+    uint32_t zero[2][kGroups];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t za[kGroups], zc[kGroups];
+      if constexpr (kGroups == 2) {
+        const uint4 v = lds128u(st + zb + 8 * h * kPair);
+        za[0] = v.x, za[1] = v.y, zc[0] = v.z, zc[1] = v.w;
+      } else {
+        const uint2 v = lds64(st + zb + 8 * h * kPair);
+        za[0] = v.x, zc[0] = v.y;
+      }
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr)  // (128 + zero in bf16 has it in its low bits)
+        zero[h][gr] = and_or(add_bf16x2(__byte_perm(za[gr], zc[gr], 0x7632), 0x43004300u), 0x000f000fu, 0x80008000u);
+    }
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      uint32_t p[NT][2];  // weights times scales, transposed: rows heads, columns tokens
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          p[nt][h] = transpose8(pack2<false>(s[nt][2 * h] * sv[h][gr], s[nt][2 * h + 1] * sv[h][gr]));
+      uint32_t m[2][2];  // codes, the tokens of a pair in the halves of a word
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t ca = lds32(st + half(vb, gr) + 8 * h * kRow), cb = lds32(st + half(vb, gr) + (8 * h + 4) * kRow);
+        m[h][0] = __byte_perm(ca, cb, 0x5410);
+        m[h][1] = __byte_perm(ca, cb, 0x7632);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
+        if (j == 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) m[h][0] >>= 8, m[h][1] >>= 8;
+        }
+        uint32_t z[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          z[h] = j & 1 ? and_or(zero[h][gr] << 4, 0x00f000f0u, 0x80008000u) : zero[h][gr];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816<false>(o[nt][4 * gr + j], m[0][0] & mask, m[0][1] & mask, m[1][0] & mask, m[1][1] & mask, p[nt][0],
+                           p[nt][1]);
+          mma_16816<false>(o[nt][4 * gr + j], z[0], z[0], z[1], z[1], p[nt][0], p[nt][1]);
+        }
       }
     }
   }
+  // Scores and values in their own units.
+  __device__ __forceinline__ void finish(LineState<NT>& ls, float (&o)[NT][kAcc][4]) const {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (ls.m[nt][e] != -INFINITY) ls.m[nt][e] = fmaxf(ls.m[nt][e] * unit[nt][e], -FLT_MAX);
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[nt][i][k] = o[nt][i][k] * (i & 1 ? 1048576.f : 16777216.f) * (1.f / vk[i / 4]);
+    }
+  }
+  static __device__ __forceinline__ int dim_of(int i, int h, int g) {
+    return kQ4Group * (i / 4) + 8 * g + (i & 3) + 4 * h;
+  }
+};
 
-  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, float sc, LineState<NT>& ls,
+// fp32 queries: three bf16 parts of 8 bits each that make the value, times (128 + code) - (128 + zero) in bf16, which are
+// exact; weight * scale in three parts too.  A step's sums are formed by themselves and added up by rounded additions (the
+// tensor core truncates its sums).
+template <int D, int NT>
+struct PackedWideRows : PackedStage<D> {
+  using Out = float;
+  using Stage = PackedStage<D>;
+  using typename Stage::Row;
+  using Stage::kGroups, Stage::kRow, Stage::kPair, Stage::kParams, Stage::kVParams, Stage::at, Stage::v_place;
+  static constexpr int kParts = 3;
+  static constexpr int kWarps = 8, kCtas = 1;
+  static constexpr int kStages = 4;
+  static constexpr int kExtra = 0;
+  static constexpr float kLift = kLineLift;
+  static constexpr int kAcc = D / 16;
+
+  uint32_t q[NT][kParts][kGroups][4][2];
+
+  __device__ __forceinline__ PackedWideRows(const LineArgs& a, uint32_t, int lane) : Stage(a, lane) {}
+  __device__ __forceinline__ void load(const LineArgs&, uint32_t st, int lane, const Row (&row)[2],
+                                       const bool (&ok)[2]) const {
+    Stage::load(st, lane, row, ok);
+  }
+
+  // (dimensions as above)
+  __device__ __forceinline__ void query(const LineArgs& a, int64_t head0, int lane, LineState<NT>&) {
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool have = nt * 8 + g < a.group;
+      const float* p = static_cast<const float*>(a.q) + (head0 + nt * 8 + g) * D + 16 * tig;
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = have ? *reinterpret_cast<const float4*>(p + gr * kQ4Group + 4 * i) : make_float4(0, 0, 0, 0);
+          x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int w = 0; w < kParts; ++w)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              q[nt][w][gr][j][h] = split(x[8 * h + j], x[8 * h + j + 4]);
+      }
+    }
+  }
+  // Two numbers as bf16; they become what is left of them, exactly.
+  static __device__ __forceinline__ uint32_t split(float& u, float& v) {
+    const uint32_t both = pack2<true>(u, v);
+    u -= __uint_as_float(both << 16);
+    v -= __uint_as_float(both & 0xffff0000u);
+    return both;
+  }
+
+  __device__ __forceinline__ void step(uint32_t st, int lane, bool ok0, bool ok1, LineState<NT>& ls,
                                        float (&o)[NT][kAcc][4]) const {
     const int g = lane >> 2, tig = lane & 3;
     // ---- scores ----
-    uint32_t pair[2][kGroups];  // K's (scale, zero) of tokens g and g + 8
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t p = st + kParams + (g + 8 * h) * kPair;
-      if constexpr (kGroups == 2) {
-        const uint2 v = lds64(p);
-        pair[h][0] = v.x, pair[h][1] = v.y;
-      } else {
-        pair[h][0] = lds32(p);
-      }
-    }
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -661,59 +922,43 @@ struct PackedRows {
 #pragma unroll
     for (int gr = 0; gr < kGroups; ++gr) {
       uint2 w[2];  // 16 codes of tokens g and g + 8
+      uint32_t pair[2], bias[2];  // their (scale, zero); 128 + zero, twice
 #pragma unroll
-      for (int h = 0; h < 2; ++h) w[h] = lds64(st + at(g + 8 * h, 32 * gr + 8 * tig));
-      float c0[NT][4], c1[NT][4];
+      for (int h = 0; h < 2; ++h) {
+        w[h] = lds64(st + at(g + 8 * h, 32 * gr + 8 * tig));
+        pair[h] = lds32(st + kParams + (g + 8 * h) * kPair + 4 * gr);
+        const float b = q4_zero(pair[h]) + kCodeBias;
+        bias[h] = (__float_as_uint(b) >> 16) | __float_as_uint(b);
+      }
+      float dot[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c0[nt][i] = c1[nt][i] = 0.f;
-      uint32_t bias[2];  // 128 + zero, twice
-      if constexpr (kWide) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float b = q4_zero(pair[h][gr]) + kCodeBias;
-          bias[h] = (__float_as_uint(b) >> 16) | __float_as_uint(b);
-        }
-      }
+        for (int i = 0; i < 4; ++i) dot[nt][i] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t x[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if constexpr (kHalf) {  // code * 2^-24 (even j) and code * 2^-20
-            const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
-            x[h] = (j < 2 ? w[h].x : w[h].x >> 8) & mask;
-            x[2 + h] = (j < 2 ? w[h].y : w[h].y >> 8) & mask;
-          } else {
-            x[h] = code_bf16(w[h].x, j);
-            x[2 + h] = code_bf16(w[h].y, j);
-            if constexpr (kWide) {
-              x[h] = sub_bf16x2(x[h], bias[h]);
-              x[2 + h] = sub_bf16x2(x[2 + h], bias[h]);
-            }
-          }
+          x[h] = sub_bf16x2(code_bf16(w[h].x, j), bias[h]);
+          x[2 + h] = sub_bf16x2(code_bf16(w[h].y, j), bias[h]);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int p = 0; p < kQParts; ++p)
-            mma_16816<!kHalf>(j & 1 ? c1[nt] : c0[nt], x[0], x[1], x[2], x[3], q[nt][p][gr][j][0], q[nt][p][gr][j][1]);
+          for (int p = kParts - 1; p >= 0; --p)
+            mma_16816<true>(d, x[0], x[1], x[2], x[3], q[nt][p][gr][j][0], q[nt][p][gr][j][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dot[nt][i] += d[i];
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t pr = pair[i >> 1][gr];
-          float dot;  // sum of q * (code - zero)
-          if constexpr (kWide) dot = c0[nt][i] + c1[nt][i];
-          else if constexpr (kHalf)
-            dot = fmaf(-q4_zero(pr), sum_q[nt][gr][i & 1], fmaf(c1[nt][i], 1048576.f, c0[nt][i] * 16777216.f));
-          else dot = fmaf(-(q4_zero(pr) + kCodeBias), sum_q[nt][gr][i & 1], c0[nt][i] + c1[nt][i]);
-          s[nt][i] = fmaf(q4_scale(pr), dot, s[nt][i]);
-        }
+        for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(q4_scale(pair[i >> 1]), dot[nt][i], s[nt][i]);
     }
-    line_softmax<NT>(s, ok0, ok1, sc, kLift, ls, [&](int nt, float f0, float f1) {
+    line_softmax<NT>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
         o[nt][i][0] *= f0, o[nt][i][2] *= f0;
@@ -721,25 +966,19 @@ struct PackedRows {
       }
     });
     // ---- values ----
-    const uint32_t vst = st + 16 * kRow, vps = st + kParams + 16 * kPair;
+    const uint32_t vst = st + 16 * kRow, vps = st + kVParams;
 #pragma unroll
     for (int gr = 0; gr < kGroups; ++gr) {
       // weights times scales, transposed: rows heads, columns tokens
       const float sv[2] = {q4_scale(lds32(vps + g * kPair + 4 * gr)), q4_scale(lds32(vps + (g + 8) * kPair + 4 * gr))};
-      uint32_t p[NT][kPParts][2];
+      uint32_t p[NT][kParts][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float u = s[nt][2 * h] * sv[h], v = s[nt][2 * h + 1] * sv[h];
-          // (a weight of 0 with a scale that is not finite belongs to no token or is 0 * NaN as the formula has it)
 #pragma unroll
-          for (int w = 0; w < kPParts; ++w) {
-            const uint32_t both = pack2<true>(u, v);
-            p[nt][w][h] = transpose8(both);
-            u -= __uint_as_float(both << 16);
-            v -= __uint_as_float(both & 0xffff0000u);
-          }
+          for (int w = 0; w < kParts; ++w) p[nt][w][h] = transpose8(split(u, v));
         }
       // tokens 2 tig and 2 tig + 1, then those 8 further on: 128 + zero of both, and the codes with the tokens of a pair
       // in the halves of a word
@@ -747,9 +986,8 @@ struct PackedRows {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int t = 2 * tig + 8 * h;
-        const uint32_t za = lds32(vps + t * kPair + 4 * gr), zb = lds32(vps + (t + 1) * kPair + 4 * gr);
-        uint32_t z = __byte_perm(za, zb, 0x7632);
-        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(bias[h]) : "r"(z), "r"(0x43004300u));
+        const uint32_t za = lds32(vps + t * kPair + 4 * gr), zc = lds32(vps + (t + 1) * kPair + 4 * gr);
+        bias[h] = add_bf16x2(__byte_perm(za, zc, 0x7632), 0x43004300u);
         const uint32_t ca = lds32(vst + at(v_place(t), 32 * gr + 4 * g));
         const uint32_t cb = lds32(vst + at(v_place(t + 1), 32 * gr + 4 * g));
         m[h][0] = __byte_perm(ca, cb, 0x5410);
@@ -765,21 +1003,16 @@ struct PackedRows {
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float(&acc)[4] = o[nt][4 * gr + j];
-          if constexpr (kWide) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = kPParts - 1; w >= 0; --w) mma_16816<true>(d, x[0], x[1], x[2], x[3], p[nt][w][0], p[nt][w][1]);
+          for (int w = kParts - 1; w >= 0; --w) mma_16816<true>(d, x[0], x[1], x[2], x[3], p[nt][w][0], p[nt][w][1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] += d[i];
-          } else {
-#pragma unroll
-            for (int w = 0; w < kPParts; ++w) mma_16816<true>(acc, x[0], x[1], x[2], x[3], p[nt][w][0], p[nt][w][1]);
-          }
+          for (int i = 0; i < 4; ++i) o[nt][4 * gr + j][i] += d[i];
         }
       }
     }
   }
+  __device__ __forceinline__ void finish(LineState<NT>&, float (&)[NT][kAcc][4]) const {}
   static __device__ __forceinline__ int dim_of(int i, int h, int g) {
     return kQ4Group * (i / 4) + 8 * g + (i & 3) + 4 * h;
   }
@@ -828,29 +1061,29 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   if (a.split && threadIdx.x == 0) a.ws_rec[blockIdx.x] = TreeRec{0, 0, 0};
 
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * Rows::kStage + Rows::kExtra));
-  Rows rows(a, ring + kStages * Rows::kStage);
+  Rows rows(a, ring + kStages * Rows::kStage, lane);
 
   // ---- the loads, kStages - 1 steps ahead ----
   LineWalk ahead(a, span, step_tokens);
   LineUnit lu;
   bool more = ahead.next(lu);
   int lx = more ? lu.x0 : 0;
-  int block[2];
+  int block[2], at[2];  // block and token in it of this lane's two tokens of the next step
   bool have[2];
   unsigned oks = 0;  // two bits a step in flight: whether this lane's two tokens exist
-  auto position = [&](int v) { return v < lu.sq.first ? v : v + lu.sq.skip; };
-  auto token = [&](int h) { return (lx * lanes_head + part) * 16 + (lane >> 2) + 8 * h; };
   auto look = [&]() {  // table entries of the next step
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int v = token(h);
+      const int v = (lx * lanes_head + part) * 16 + (lane >> 2) + 8 * h;
+      const int pos = v < lu.sq.first ? v : v + lu.sq.skip;
       have[h] = more && v < lu.sq.seen;
-      block[h] = have[h] ? ld_s32(a.block_table + lu.b * a.bt_stride + (position(v) >> a.block_shift)) : 0;
+      at[h] = pos & (a.block_size - 1);
+      block[h] = have[h] ? ld_s32(a.block_table + lu.b * a.bt_stride + (pos >> a.block_shift)) : 0;
     }
   };
   auto load = [&](int stage) {
     if (more) {
-      int64_t row[2];
+      typename Rows::Row row[2];
       bool ok[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -859,7 +1092,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
           raise_error(a.err, PA_DEVERR_BLOCK_ID);
           ok[h] = false;
         }
-        row[h] = ok[h] ? Rows::row_of(a, block[h], position(token(h)) & (a.block_size - 1), lu.hg * a.heads + head) : 0;
+        row[h] = ok[h] ? Rows::row_of(a, block[h], at[h], lu.hg * a.heads + head) : 0;
       }
       rows.load(a, ring + stage * Rows::kStage, lane, row, ok);
       oks = oks << 2 | (ok[1] ? 2u : 0u) | (ok[0] ? 1u : 0u);
@@ -883,13 +1116,13 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   int stage = 0;
   while (walk.next(w)) {
     const int64_t head0 = (int64_t)w.b * a.n_q_heads + (int64_t)(w.hg * a.heads + head) * a.group;
-    rows.query(a, head0, lane);
     LineState<NT> ls;
     float o[NT][Rows::kAcc][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        ls.sc[nt][e] = a.scale_log2;
         ls.m[nt][e] = -INFINITY;
         ls.l[nt][e] = 0.f;
       }
@@ -898,15 +1131,17 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
     }
+    rows.query(a, head0, lane, ls);
     for (int x = w.x0; x < w.x1; ++x) {
       copy_wait<kStages - 2>();
       __syncwarp();  // every lane's copies of this step are there, and the stage before has been read by all
       const unsigned ok = oks >> (2 * (kStages - 2));
       load(stage == 0 ? kStages - 1 : stage - 1);
-      rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, a.scale_log2, ls, o);
+      rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, ls, o);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     // ---- the unit's end: the warps of a head joined ----
+    rows.finish(ls, o);
     const int g = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1055,6 +1290,10 @@ template <typename T, int D>
 cudaError_t launch_packed(const LineArgs& a, cudaStream_t s) {
   return a.group > 8 ? launch_rows<PackedRows<T, D, 2>, D, 2>(a, s) : launch_rows<PackedRows<T, D, 1>, D, 1>(a, s);
 }
+template <int D>
+cudaError_t launch_wide(const LineArgs& a, cudaStream_t s) {
+  return a.group > 8 ? launch_rows<PackedWideRows<D, 2>, D, 2>(a, s) : launch_rows<PackedWideRows<D, 1>, D, 1>(a, s);
+}
 template <typename T, int D>
 cudaError_t launch_full(const LineArgs& a, cudaStream_t s) {
   return a.group > 8 ? launch_rows<FullRows<T, D, 2>, D, 2>(a, s) : launch_rows<FullRows<T, D, 1>, D, 1>(a, s);
@@ -1075,7 +1314,7 @@ int resident_of(bool packed, pa_dtype dt, int group) {
   if (packed)
     return dt == PA_BF16   ? resident<PackedRows<__nv_bfloat16, D, NT>, D>(group)
            : dt == PA_FP16 ? resident<PackedRows<__half, D, NT>, D>(group)
-                           : resident<PackedRows<float, D, NT>, D>(group);
+                           : resident<PackedWideRows<D, NT>, D>(group);
   return dt == PA_FP32 ? resident<FloatRows<D, NT>, D>(group) : resident<FullRows<__half, D, NT>, D>(group);
 }
 
@@ -1102,7 +1341,7 @@ cudaError_t launch_line_decode(const LineArgs& a, pa_dtype dt, bool packed, cuda
   if (packed) {
     if (dt == PA_BF16) e = d64 ? launch_packed<__nv_bfloat16, 64>(a, s) : launch_packed<__nv_bfloat16, 128>(a, s);
     if (dt == PA_FP16) e = d64 ? launch_packed<__half, 64>(a, s) : launch_packed<__half, 128>(a, s);
-    if (dt == PA_FP32) e = d64 ? launch_packed<float, 64>(a, s) : launch_packed<float, 128>(a, s);
+    if (dt == PA_FP32) e = d64 ? launch_wide<64>(a, s) : launch_wide<128>(a, s);
   } else {
     if (dt == PA_BF16) e = d64 ? launch_full<__nv_bfloat16, 64>(a, s) : launch_full<__nv_bfloat16, 128>(a, s);
     if (dt == PA_FP16) e = d64 ? launch_full<__half, 64>(a, s) : launch_full<__half, 128>(a, s);

@@ -160,6 +160,10 @@ __device__ __forceinline__ void s_load64(uint32_t taddr, uint32_t (&sv)[64], con
       const uint32_t v = fix.zero ? 0u : (sv[j] ^ fix.flip);
       sv[j] = (((j < 32 ? m0 : m1) >> (j & 31)) & 1u) ? v : 0xff800000u;  // -inf
     }
+  } else if (kMode == 3) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      if (!(((j < 32 ? m0 : m1) >> (j & 31)) & 1u)) sv[j] = 0xff800000u;
   }
 }
 
@@ -245,6 +249,20 @@ __device__ __forceinline__ float row_softmax(uint32_t srow, float sc, const Scor
   return corr;
 }
 
+// The scores of a warp's rows in the 128 columns from taddr on become (s - m) * sc.  (Rare, and kept out of the loop's
+// code.)
+static __device__ __noinline__ void s_distances(uint32_t taddr, float sc, float m) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < kUmKeys; c0 += 32) {
+    uint32_t sv[32];
+    tmem_ld32_sync(taddr + (uint32_t)c0, sv);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) sv[c] = __float_as_uint((__uint_as_float(sv[c]) - m) * sc);
+    tmem_st32(taddr + (uint32_t)c0, sv);
+  }
+  tmem_wait_st();
+}
+
 // The same with an unscaled stabiliser (windowed form; sc > 0).  Weights are 2^(s * sc - m * sc) in one rounding, but
 // where m * sc of a row is itself rounded by more than an eighth (scores of 2^20): there they are 2^((s - m) * sc).
 template <bool kBf16, int kMode>
@@ -252,10 +270,10 @@ __device__ __forceinline__ float row_softmax_window(uint32_t srow, float sc, con
                                                     const uint32_t (&mask)[kUmKeys / 32], float& m_use, float& l_run) {
   constexpr float kLift = kBf16 ? 0.f : 7.f;
   auto block_empty = [&](int h) {
-    return kMode == 1 && __all_sync(0xffffffffu, fix.nv - 64 * h <= 0);
+    return kMode == 3 && __all_sync(0xffffffffu, (h ? mask[2] | mask[3] : mask[0] | mask[1]) == 0u);
   };
   // (keys that are seen count, whatever their scores: a row of scores of -inf is told from one that sees nothing)
-  float mx = (mask[0] | mask[1] | mask[2] | mask[3]) != 0u ? -FLT_MAX : -INFINITY;
+  float mx = kMode == 0 || (mask[0] | mask[1] | mask[2] | mask[3]) != 0u ? -FLT_MAX : -INFINITY;
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     if (block_empty(h)) continue;
@@ -270,6 +288,7 @@ __device__ __forceinline__ float row_softmax_window(uint32_t srow, float sc, con
   }
   const float m_sub = m_use == -INFINITY ? 0.f : m_use;
   const bool far = __any_sync(0xffffffffu, !(fabsf(m_sub * sc) <= 1048576.f));
+  if (far) s_distances(srow, sc, m_sub);
   const float w_scale = far ? 1.f : sc, w_sub = (far ? 0.f : m_sub * sc) - kLift;
   float rs = 0.f;
 #pragma unroll 1
@@ -283,23 +302,18 @@ __device__ __forceinline__ float row_softmax_window(uint32_t srow, float sc, con
     }
     uint32_t sv[64];
     s_load64<kMode>(srow + 64u * h, sv, fix, 64 * h, h ? mask[2] : mask[0], h ? mask[3] : mask[1]);
-    if (far) {
-#pragma unroll
-      for (int c = 0; c < 64; ++c) sv[c] = __float_as_uint((__uint_as_float(sv[c]) - m_sub) * sc);
-    }
     rs += p_store64<kBf16>(srow + 32u * h, sv, w_scale, w_sub);
   }
   l_run = l_run * corr + rs;
   return corr;
 }
 
-// Whether one of eight 16-bit floats is infinite or NaN (multiplied by 0 they give NaN).
+// Whether one of sixteen 16-bit floats is infinite or NaN (multiplied by 0 they give NaN).
 template <bool kBf16>
-__device__ __forceinline__ bool any_nonfinite(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ bool any_nonfinite(const uint32_t (&w)[8]) {
   uint32_t r = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     if constexpr (kBf16)
       asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(r) : "r"(w[i]), "r"(0u));
     else
@@ -958,8 +972,20 @@ __global__ void __launch_bounds__(kUmThreads)
           const bool mixed = kWindow && split > 0 && split < kUmKeys;
           const bool uncut = !kWindow || (!mixed && __all_sync(0xffffffffu, kb >= low || kb + kUmKeys <= a.sinks));
           const bool unmasked = __all_sync(0xffffffffu, loaded == all_sub && kb + kUmKeys - 1 <= bound) && uncut;
-          uint32_t mask[kUmKeys / 32];
+          const uint32_t srow = tS(grp) + lane_base;
+          ScoreFix fix;
           {
+            const int lim = bound - kb;  // keys c <= lim are causal
+            const int nvc = lim < 0 ? 0 : (lim >= kUmKeys ? kUmKeys : lim + 1);
+            const int nvl = 16 * __popc(loaded);
+            const bool prefix = (loaded & (loaded + 1u)) == 0u && uncut;  // the loaded sub-tiles are 0 .. k-1
+            fix.mode = (unmasked && sc > 0.f) ? 0 : ((prefix && sc > 0.f) ? 1 : 2);
+            fix.nv = nvc < nvl ? nvc : nvl;
+            fix.flip = sc < 0.f ? 0x80000000u : 0u;
+            fix.zero = sc == 0.f;
+          }
+          uint32_t mask[kUmKeys / 32] = {};
+          if (!kWindow || fix.mode != 0) {
             // keys from k0 on that the row sees, 32 columns
             auto seen = [&](int k0) -> uint32_t {
               const int nv = bound - k0 + 1;  // causal
@@ -983,24 +1009,11 @@ __global__ void __launch_bounds__(kUmThreads)
               mask[q] &= lm;
             }
           }
-          const uint32_t srow = tS(grp) + lane_base;
-          ScoreFix fix;
-          {
-            const int lim = bound - kb;  // keys c <= lim are causal
-            const int nvc = lim < 0 ? 0 : (lim >= kUmKeys ? kUmKeys : lim + 1);
-            const int nvl = 16 * __popc(loaded);
-            const bool prefix = (loaded & (loaded + 1u)) == 0u && uncut;  // the loaded sub-tiles are 0 .. k-1
-            fix.mode = (unmasked && sc > 0.f) ? 0 : ((prefix && sc > 0.f) ? 1 : 2);
-            fix.nv = nvc < nvl ? nvc : nvl;
-            fix.flip = sc < 0.f ? 0x80000000u : 0u;
-            fix.zero = sc == 0.f;
-          }
           const float sc_pos = sc > 0.f ? sc : (sc < 0.f ? -sc : 1.f);
           float corr;
           if constexpr (kWindow)
-            corr = fix.mode == 0   ? row_softmax_window<kBf16, 0>(srow, sc, fix, mask, m_use, l_run)
-                   : fix.mode == 1 ? row_softmax_window<kBf16, 1>(srow, sc, fix, mask, m_use, l_run)
-                                   : row_softmax_window<kBf16, 2>(srow, sc, fix, mask, m_use, l_run);
+            corr = fix.mode == 0 ? row_softmax_window<kBf16, 0>(srow, sc, fix, mask, m_use, l_run)
+                                 : row_softmax_window<kBf16, 3>(srow, sc, fix, mask, m_use, l_run);
           else
             corr = fix.mode == 0   ? row_softmax<kBf16, 0>(srow, sc_pos, fix, mask, m_use, l_run)
                    : fix.mode == 1 ? row_softmax<kBf16, 1>(srow, sc_pos, fix, mask, m_use, l_run)
@@ -1047,23 +1060,21 @@ __global__ void __launch_bounds__(kUmThreads)
       const bool have = alive && i > i0 && (kWindow ? m_use != -INFINITY : l_run != 0.f);
       const float inv = have ? 1.f / l_run : 0.f;
       T* orow = static_cast<T*>(a.out) + ((int64_t)tok * a.n_q_heads + head) * D;
+      const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t v[32];
         tmem_ld32_sync(tO(grp) + lane_base + c0, v);
         if (tok < T1 && (!kWindow || mine)) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            float f[8];
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = have ? __uint_as_float(v[j + e]) * inv : 0.f;
-            uint4 wv;
-            wv.x = pack2<kBf16>(f[0], f[1]);
-            wv.y = pack2<kBf16>(f[2], f[3]);
-            wv.z = pack2<kBf16>(f[4], f[5]);
-            wv.w = pack2<kBf16>(f[6], f[7]);
-            if (kWindow && any_nonfinite<kBf16>(wv)) *bad_out = 1;
-            *reinterpret_cast<uint4*>(orow + c0 + j) = wv;
+            for (int e = 0; e < 8; ++e)
+              x[e] = pack2<kBf16>(have ? __uint_as_float(v[j + 2 * e]) * inv : 0.f,
+                                  have ? __uint_as_float(v[j + 2 * e + 1]) * inv : 0.f);
+            if (kWindow && any_nonfinite<kBf16>(x)) *bad_out = 1;
+            st_global32(orow + c0 + j, x, wide);
           }
         }
       }

@@ -128,8 +128,8 @@ class PackedCase(WindowCase):
         k, v = (torch.from_numpy(oracle.window.q4_values(c, p)) for c, p in ((self.kc, self.kp), (self.vc, self.vp)))
         rows, ref, spread, _ = oracle.window.window_attention(self.q, None, k, v, self.table, self.ctx, self.scale,
                                                               self.window, self.sinks)
-        # what the score's sums are made of: query values times codes, in bf16 with 128 added to code and zero
-        top = {torch.bfloat16: 2 * (128 + 15), torch.float16: 2 * 15, torch.float32: 15}[self.dtype]
+        # what the score's sums are made of: query values times codes, and times zeros (fp32: times code - zero)
+        top = 15 if self.dtype == torch.float32 else 2 * 15
         q = self.q.double().abs().unflatten(-1, (-1, 64)).sum(-1).numpy()  # [B, Hq, groups]
         scales = np.zeros(q.shape)
         group = q.shape[1] // self.kp.shape[2]
@@ -140,6 +140,10 @@ class PackedCase(WindowCase):
         return rows, ref, spread, self.scale * (q * scales * top).sum(-1)
 
     def bound(self, ref, spread, size):
-        # weights: one, two or three parts of bf16, each half a step of what the one before left
-        weight = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -24}[self.dtype]
-        return bound(self.dtype, ref, spread, size, self.most_seen(), self.q.shape[2], weight)
+        # weight * scale: three parts of bf16, each half a step of what the one before left; or fp16, half a step, at least
+        # 2^-25 of numbers whose largest scale counts 2^5 or more: times codes of at most 15, for every key
+        if self.dtype == torch.float32:
+            return bound(self.dtype, ref, spread, size, self.most_seen(), self.q.shape[2], 2.0 ** -24)
+        scales = torch.nan_to_num(self.vp[..., 0::2].double(), nan=0.0)
+        floor = self.most_seen() * 2.0 ** -30 * 15 * float(scales.max())
+        return bound(self.dtype, ref, spread, size, self.most_seen(), self.q.shape[2], 2.0 ** -11, floor)
