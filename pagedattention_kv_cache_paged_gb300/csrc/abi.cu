@@ -952,7 +952,7 @@ int run_line(LineArgs& a, bool packed, int64_t bt_stride, int batch, int64_t num
   }
   a.bt_stride = bt_stride;
   a.batch = batch;
-  a.num_blocks = num_blocks;
+  a.block_limit = (unsigned)std::min(num_blocks, int64_t(1) << 31);
   a.block_size = block_size;
   a.block_shift = log2i(block_size);
   a.window = window;
@@ -962,6 +962,7 @@ int run_line(LineArgs& a, bool packed, int64_t bt_stride, int batch, int64_t num
   a.n_q_heads = n_q_heads;
   a.n_kv_heads = n_kv_heads;
   a.group = n_q_heads / n_kv_heads;
+  a.group_shift = log2i(a.group);
   a.head_dim = head_dim;
   a.heads = plan.heads;
   a.units = plan.units;

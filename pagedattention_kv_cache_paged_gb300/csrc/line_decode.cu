@@ -265,6 +265,15 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// D = A * B of fp16 values.
+__device__ __forceinline__ void mma_16816_of(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Nibble k (0 .. 3) of both halves of w as bf16: 128 + code.
 __device__ __forceinline__ uint32_t code_bf16(uint32_t w, int k) {
   return and_or(k == 0 ? w : w >> (4 * k), 0x000f000fu, 0x43004300u);
@@ -296,8 +305,9 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (!(i < 2 ? ok0 : ok1)) s[nt][i] = -INFINITY;
       x[nt][i] = (s[nt][i] - st.m[nt][i & 1]) * st.sc[nt][i & 1];
-      move |= (i < 2 ? ok0 : ok1) && !(x[nt][i] <= kGrow);  // (also at the start, and for NaN)
+      move |= !(x[nt][i] <= kGrow);  // (also at the start, and for NaN)
     }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -313,8 +323,9 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
         f[e] = old == m ? 1.f : fast_exp2((old - m) * st.sc[nt][e]);
         st.m[nt][e] = m;
         st.l[nt][e] *= f[e];
-        x[nt][e] = (s[nt][e] - m) * st.sc[nt][e];
-        x[nt][2 + e] = (s[nt][2 + e] - m) * st.sc[nt][e];
+        const float base = m == -INFINITY ? 0.f : m;
+        x[nt][e] = (s[nt][e] - base) * st.sc[nt][e];
+        x[nt][2 + e] = (s[nt][2 + e] - base) * st.sc[nt][e];
       }
       rescale(nt, f[0], f[1]);
     }
@@ -323,7 +334,7 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float p = (i < 2 ? ok0 : ok1) ? fast_exp2(lift == 0.f ? x[nt][i] : x[nt][i] + lift) : 0.f;
+      const float p = fast_exp2(lift == 0.f ? x[nt][i] : x[nt][i] + lift);
       s[nt][i] = p;
       st.l[nt][i & 1] += p;
     }
@@ -343,6 +354,7 @@ struct FullRows {
   static constexpr int kStage = 2 * 16 * kRow;   // K, then V
   static constexpr int kExtra = 0;               // shared memory of a warp besides its ring
   static constexpr float kLift = kBf16 ? kLineLift : 7.f;
+  static constexpr bool kQuads = false;  // whether accumulators i .. i + 3 hold neighbouring dimensions
   static constexpr int kAcc = D / 16;
 
   const T* k;
@@ -449,6 +461,7 @@ struct FloatRows {
   static constexpr int kQuery = NT * 8 * kRow;               // a warp's queries
   static constexpr int kExtra = kQuery + NT * 16 * 8 * 4;    // and the weights of a step, [nt][token][head]
   static constexpr float kLift = kLineLift;
+  static constexpr bool kQuads = false;
   static constexpr int kAcc = D / 16;
 
   const float* k;
@@ -594,7 +607,7 @@ struct PackedStage {
     copy_async<kPair>(st + dp, pairs + (uint64_t)(lane & 1 ? row[1] : row[0]) * kPair, lane & 1 ? ok[1] : ok[0]);
   }
   static __device__ __forceinline__ Row row_of(const LineArgs& a, int block, int token, int h) {
-    return (((Row)block << a.block_shift) + (Row)token) * (Row)a.n_kv_heads + (Row)h;
+    return ((Row)block * (Row)a.block_size + (Row)token) * (Row)a.n_kv_heads + (Row)h;
   }
 };
 
@@ -607,8 +620,7 @@ struct PackedStage {
 //
 // Values.  weight * scale is rounded to fp16 after a power of two that keeps the largest scale of a group so far in
 // 2^5 .. 2^6 (its accumulators are rescaled when it moves, by the same vote as the stabiliser's), so that the smallest step
-// is 2^-30 of the largest product or less; O += C (w s), O += (-z) (w s), the zero as an operand of its own, whose rows
-// are the same.
+// is 2^-30 of the largest product or less.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
 template <typename T, int D, int NT>
 struct PackedRows : PackedStage<D> {
   using Out = T;
@@ -620,12 +632,14 @@ struct PackedRows : PackedStage<D> {
   static constexpr int kStages = 4;
   static constexpr int kExtra = 0;
   static constexpr float kLift = 0.f;
+  static constexpr bool kQuads = true;
   static constexpr int kAcc = D / 16;
 
   uint32_t q[NT][kGroups][4][2];
   float sum_q[NT][kGroups][2];  // sums of a group's query values, heads 2 tig, 2 tig + 1, times 2^-24
   float unit[NT][2];            // score of a head per unit of the above
   float vk[kGroups];            // the power of two of the group's scales
+  float oz[NT][kGroups][4];     // sums of weights times scales times zeros (rows alike) times 2^-24
   uint32_t kb, vb, pb, zb;      // this lane's reads: codes of K and V, pairs, zeros
 
   __device__ __forceinline__ PackedRows(const LineArgs& a, uint32_t, int lane) : Stage(a, lane) {
@@ -694,7 +708,13 @@ struct PackedRows : PackedStage<D> {
       }
     }
 #pragma unroll
-    for (int gr = 0; gr < kGroups; ++gr) vk[gr] = 8.50705917302346159e37f;  // 2^126
+    for (int gr = 0; gr < kGroups; ++gr) {
+      vk[gr] = 8.50705917302346159e37f;  // 2^126
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oz[nt][gr][k] = 0.f;
+    }
   }
 
   __device__ __forceinline__ void step(uint32_t st, int, bool ok0, bool ok1, LineState<NT>& ls,
@@ -721,10 +741,6 @@ struct PackedRows : PackedStage<D> {
       for (int h = 0; h < 2; ++h) w[h] = lds64(st + half(kb, gr) + 8 * h * kRow);
       float dot[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dot[nt][i] = 0.f;
-#pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
         if (j == 2) {
@@ -732,9 +748,14 @@ struct PackedRows : PackedStage<D> {
           for (int h = 0; h < 2; ++h) w[h].x >>= 8, w[h].y >>= 8;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_16816<false>(dot[nt], w[0].x & mask, w[1].x & mask, w[0].y & mask, w[1].y & mask, q[nt][gr][j][0],
-                           q[nt][gr][j][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (j == 0)
+            mma_16816_of(dot[nt], w[0].x & mask, w[1].x & mask, w[0].y & mask, w[1].y & mask, q[nt][gr][j][0],
+                         q[nt][gr][j][1]);
+          else
+            mma_16816<false>(dot[nt], w[0].x & mask, w[1].x & mask, w[0].y & mask, w[1].y & mask, q[nt][gr][j][0],
+                             q[nt][gr][j][1]);
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -780,6 +801,8 @@ struct PackedRows : PackedStage<D> {
           o[nt][i][0] *= g0, o[nt][i][2] *= g0;
           o[nt][i][1] *= g1, o[nt][i][3] *= g1;
         }
+        oz[nt][gr][0] *= g0, oz[nt][gr][2] *= g0;
+        oz[nt][gr][1] *= g1, oz[nt][gr][3] *= g1;
       }
     });
     // ---- values ----
@@ -797,7 +820,7 @@ struct PackedRows : PackedStage<D> {
       }
 #pragma unroll
       for (int gr = 0; gr < kGroups; ++gr)  // (128 + zero in bf16 has it in its low bits)
-        zero[h][gr] = and_or(add_bf16x2(__byte_perm(za[gr], zc[gr], 0x7632), 0x43004300u), 0x000f000fu, 0x80008000u);
+        zero[h][gr] = add_bf16x2(__byte_perm(za[gr], zc[gr], 0x7632), 0x43004300u) & 0x000f000fu;
     }
 #pragma unroll
     for (int gr = 0; gr < kGroups; ++gr) {
@@ -821,17 +844,14 @@ struct PackedRows : PackedStage<D> {
 #pragma unroll
           for (int h = 0; h < 2; ++h) m[h][0] >>= 8, m[h][1] >>= 8;
         }
-        uint32_t z[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          z[h] = j & 1 ? and_or(zero[h][gr] << 4, 0x00f000f0u, 0x80008000u) : zero[h][gr];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
           mma_16816<false>(o[nt][4 * gr + j], m[0][0] & mask, m[0][1] & mask, m[1][0] & mask, m[1][1] & mask, p[nt][0],
                            p[nt][1]);
-          mma_16816<false>(o[nt][4 * gr + j], z[0], z[0], z[1], z[1], p[nt][0], p[nt][1]);
-        }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma_16816<false>(oz[nt][gr], zero[0][gr], zero[0][gr], zero[1][gr], zero[1][gr], p[nt][0], p[nt][1]);
     }
   }
   // Scores and values in their own units.
@@ -845,7 +865,7 @@ struct PackedRows : PackedStage<D> {
       for (int i = 0; i < kAcc; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[nt][i][k] = o[nt][i][k] * (i & 1 ? 1048576.f : 16777216.f) * (1.f / vk[i / 4]);
+          o[nt][i][k] = fmaf(o[nt][i][k], i & 1 ? 1048576.f : 16777216.f, -16777216.f * oz[nt][i / 4][k]) * (1.f / vk[i / 4]);
     }
   }
   static __device__ __forceinline__ int dim_of(int i, int h, int g) {
@@ -867,6 +887,7 @@ struct PackedWideRows : PackedStage<D> {
   static constexpr int kStages = 4;
   static constexpr int kExtra = 0;
   static constexpr float kLift = kLineLift;
+  static constexpr bool kQuads = true;
   static constexpr int kAcc = D / 16;
 
   uint32_t q[NT][kParts][kGroups][4][2];
@@ -1024,13 +1045,15 @@ struct PackedWideRows : PackedStage<D> {
 template <typename Rows>
 struct LineCfg {
   static constexpr int kThreads = Rows::kWarps * 32;
+  static constexpr int kPad = 4;
   static constexpr int kRing = Rows::kWarps * (Rows::kStages * Rows::kStage + Rows::kExtra);
 };
 
-// Shared memory: the warps' rings (and what else a warp needs), then their states at the end of a unit, [warp][row][head_dim], [warp][row] twice.
+// Shared memory: the warps' rings (and what else a warp needs), then their states at the end of a unit, [warp][row]
+// [head_dim + kPad], [warp][row] twice.
 template <typename Rows, int D>
 constexpr int line_smem(int group) {
-  return LineCfg<Rows>::kRing + Rows::kWarps * group * (D + 2) * 4;
+  return LineCfg<Rows>::kRing + Rows::kWarps * group * (D + LineCfg<Rows>::kPad + 2) * 4;
 }
 constexpr int kLineStatic = 256;  // TreeSched
 static_assert(sizeof(TreeSched) <= kLineStatic, "the schedule's shared memory");
@@ -1041,8 +1064,9 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   constexpr int kWarps = Rows::kWarps, kStages = Rows::kStages, kThreads = LineCfg<Rows>::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ TreeSched sched;
+  constexpr int kOutRow = LineCfg<Rows>::kPad + D;  // (the pad keeps the rows that a store writes in different banks)
   float* const out_o = reinterpret_cast<float*>(smem + LineCfg<Rows>::kRing);
-  float* const out_m = out_o + kWarps * a.group * D;
+  float* const out_m = out_o + kWarps * a.group * kOutRow;
   float* const out_l = out_m + kWarps * a.group;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes_head = kWarps / a.heads;  // warps of a KV head
@@ -1066,8 +1090,10 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   // ---- the loads, kStages - 1 steps ahead ----
   LineWalk ahead(a, span, step_tokens);
   LineUnit lu;
+  lu.b = 0;
   bool more = ahead.next(lu);
   int lx = more ? lu.x0 : 0;
+  const int32_t* table = a.block_table + lu.b * a.bt_stride;
   int block[2], at[2];  // block and token in it of this lane's two tokens of the next step
   bool have[2];
   unsigned oks = 0;  // two bits a step in flight: whether this lane's two tokens exist
@@ -1078,7 +1104,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
       const int pos = v < lu.sq.first ? v : v + lu.sq.skip;
       have[h] = more && v < lu.sq.seen;
       at[h] = pos & (a.block_size - 1);
-      block[h] = have[h] ? ld_s32(a.block_table + lu.b * a.bt_stride + (pos >> a.block_shift)) : 0;
+      block[h] = have[h] ? ld_s32(table + (pos >> a.block_shift)) : 0;
     }
   };
   auto load = [&](int stage) {
@@ -1088,7 +1114,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         ok[h] = have[h];
-        if (have[h] && (block[h] < 0 || block[h] >= a.num_blocks)) {
+        if (have[h] && (unsigned)block[h] >= a.block_limit) {
           raise_error(a.err, PA_DEVERR_BLOCK_ID);
           ok[h] = false;
         }
@@ -1099,6 +1125,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
       if (++lx == lu.x1) {
         more = ahead.next(lu);
         lx = more ? lu.x0 : 0;
+        table = a.block_table + lu.b * a.bt_stride;
       }
       look();
     } else {
@@ -1140,56 +1167,104 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
       rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, ls, o);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    // ---- the unit's end: the warps of a head joined ----
+    // ---- the unit's end ----
     rows.finish(ls, o);
     const int g = lane >> 2, tig = lane & 3;
+    const bool whole = w.x0 == 0 && w.x1 == w.T;
+    const int unit_rows = a.heads << a.group_shift;
+    const int64_t row0 = (int64_t)w.b * a.n_q_heads + (int64_t)w.hg * unit_rows;
+    const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * unit_rows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = ls.l[nt][e];
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        const int r = nt * 8 + 2 * tig + e;
-        if (r < a.group) {
-          float* p = out_o + (warp * a.group + r) * D;
-#pragma unroll
-          for (int i = 0; i < Rows::kAcc; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) p[Rows::dim_of(i, h, g)] = o[nt][i][2 * h + e];
-          if (g == 0) {
-            out_m[warp * a.group + r] = ls.m[nt][e];
-            out_l[warp * a.group + r] = l;
-          }
-        }
-      }
-    __syncthreads();
-    const bool whole = w.x0 == 0 && w.x1 == w.T;
-    const int unit_rows = a.heads * a.group;
-    const int64_t row0 = (int64_t)w.b * a.n_q_heads + (int64_t)w.hg * unit_rows;
-    const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * unit_rows;
-    for (int i = threadIdx.x; i < unit_rows * D; i += kThreads) {
-      const int r = i / D, d = i - r * D;
-      const int w0 = r / a.group * lanes_head, rr = r - r / a.group * a.group;
-      float M = -INFINITY, L = 0.f, A = 0.f;
-      for (int k = 0; k < lanes_head; ++k) M = fmaxf(M, out_m[(w0 + k) * a.group + rr]);
-      if (M != -INFINITY) {
-        for (int k = 0; k < lanes_head; ++k) {
-          const int at = (w0 + k) * a.group + rr;
-          const float f = fast_exp2((out_m[at] - M) * a.scale_log2);
-          L = fmaf(out_l[at], f, L);
-          A = fmaf(out_o[at * D + d], f, A);
-        }
-      }
+        for (int off = 4; off < 32; off <<= 1) ls.l[nt][e] += __shfl_xor_sync(0xffffffffu, ls.l[nt][e], off);
+    // four neighbouring dimensions of a row: its output, or this CTA's part of it
+    auto put = [&](int r, int d, const float4& v, float M, float L) {
       if (whole) {
-        static_cast<T*>(a.out)[(row0 + r) * D + d] = Elt<T>::from_float(M == -INFINITY ? 0.f : A / L);
+        const float norm = M == -INFINITY ? 0.f : 1.f / L;
+        T* out = static_cast<T*>(a.out) + (row0 + r) * D + d;
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(out) = make_float4(v.x * norm, v.y * norm, v.z * norm, v.w * norm);
+        else
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack2<std::is_same<T, __nv_bfloat16>::value>(v.x * norm, v.y * norm),
+                                                      pack2<std::is_same<T, __nv_bfloat16>::value>(v.z * norm, v.w * norm));
       } else {
-        a.ws_acc[(slot0 + r) * D + d] = A;
+        *reinterpret_cast<float4*>(a.ws_acc + (slot0 + r) * D + d) = v;
         if (d == 0) {
           a.ws_m[slot0 + r] = M;
           a.ws_l[slot0 + r] = L;
         }
       }
+    };
+    if (Rows::kQuads && lanes_head == 1) {
+      // a warp has all of its head, and four neighbouring dimensions in four accumulators
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * tig + e;
+          if (r < a.group) {
+#pragma unroll
+            for (int i = 0; i < Rows::kAcc; i += 4)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                put((head << a.group_shift) + r, Rows::dim_of(i, h, g),
+                    make_float4(o[nt][i][2 * h + e], o[nt][i + 1][2 * h + e], o[nt][i + 2][2 * h + e],
+                                o[nt][i + 3][2 * h + e]),
+                    ls.m[nt][e], ls.l[nt][e]);
+          }
+        }
+    } else {
+      // the warps of a head joined in shared memory
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * tig + e;
+          if (r < a.group) {
+            float* p = out_o + ((warp << a.group_shift) + r) * kOutRow;
+            if constexpr (Rows::kQuads) {
+#pragma unroll
+              for (int i = 0; i < Rows::kAcc; i += 4)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  *reinterpret_cast<float4*>(p + Rows::dim_of(i, h, g)) =
+                      make_float4(o[nt][i][2 * h + e], o[nt][i + 1][2 * h + e], o[nt][i + 2][2 * h + e],
+                                  o[nt][i + 3][2 * h + e]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < Rows::kAcc; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) p[Rows::dim_of(i, h, g)] = o[nt][i][2 * h + e];
+            }
+            if (g == 0) {
+              out_m[(warp << a.group_shift) + r] = ls.m[nt][e];
+              out_l[(warp << a.group_shift) + r] = ls.l[nt][e];
+            }
+          }
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < unit_rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        // row r of warp 0 of its head, and how far apart the head's warps are
+        const int at0 = ((r >> a.group_shift) * lanes_head << a.group_shift) + (r & (a.group - 1));
+        float M = -INFINITY, L = 0.f;
+        for (int k = 0; k < lanes_head; ++k) M = fmaxf(M, out_m[at0 + (k << a.group_shift)]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (M != -INFINITY) {
+          for (int k = 0; k < lanes_head; ++k) {
+            const int at = at0 + (k << a.group_shift);
+            const float f = fast_exp2((out_m[at] - M) * a.scale_log2);
+            const float4 x = *reinterpret_cast<const float4*>(out_o + at * kOutRow + d);
+            L = fmaf(out_l[at], f, L);
+            v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
+          }
+        }
+        put(r, d, v, M, L);
+      }
+      __syncthreads();
     }
     if (!whole && w.x0 == 0 && threadIdx.x == 0) {
       // the CTA that the unit's last step went to
@@ -1197,7 +1272,6 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
       if (tree_cut((int64_t)last * sched.share - sched.cut_start, w.T, sched.snap) == w.T) --last;
       a.ws_rec[blockIdx.x] = TreeRec{row0, unit_rows, last};
     }
-    __syncthreads();
   }
   copy_wait<0>();
   // sequences that see nothing

@@ -273,7 +273,7 @@ struct LineArgs {
   int64_t bt_stride;
   const int32_t* context_lens;
   int batch;
-  int64_t num_blocks;
+  unsigned block_limit;            // num_blocks, or 2^31 where there are more (ids are int32)
   int block_size;
   int block_shift;                 // log2(block_size)
   int64_t block_stride;            // elements from one block of a pool to the next
@@ -284,6 +284,7 @@ struct LineArgs {
   int n_q_heads;
   int n_kv_heads;
   int group;                       // n_q_heads / n_kv_heads
+  int group_shift;                 // log2(group)
   int head_dim;
   int heads;                       // KV heads of a CTA
   int units;                       // n_kv_heads / heads
