@@ -1286,22 +1286,26 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
 }
 
 // ------------------------------------------------------------------------------------------------
-// Units cut between CTAs: one warp per row, all its pieces (the first in the second slot of the CTA that the unit
-// begins in, the others in the first slots of the CTAs after it).
-constexpr int kLjWarps = 4;
+// Units cut between CTAs, all pieces of a row (the first in the second slot of the CTA that the unit begins in, the
+// others in the first slots of the CTAs after it).  A warp per row; where units are expected in many pieces (kWide: few
+// sequences with long contexts), a CTA per row, whose warps take pieces in turn.
+constexpr int kLjWarps = 4, kLjWideWarps = 8;
+constexpr int kLjWidePieces = 12;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kLjWarps * 32) line_join_kernel(const LineArgs a) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
+template <typename T, int D, bool kWide>
+__global__ void __launch_bounds__(32 * (kWide ? kLjWideWarps : kLjWarps)) line_join_kernel(const LineArgs a) {
+  constexpr int kPer = D / 32, kWarps = kWide ? kLjWideWarps : 1;
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+  __shared__ float s_acc[kWarps][D], s_l[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.y;
   pdl_launch_dependents();
   pdl_wait_primary();
   const TreeRec rec = a.ws_rec[c];
-  const int r = blockIdx.x * kLjWarps + (threadIdx.x >> 5);
+  const int r = kWide ? blockIdx.x : blockIdx.x * kLjWarps + warp;
   if (r >= rec.rows) return;
-  const int unit_rows = a.heads * a.group;
-  const int pieces = rec.last - c + 1;
+  const int unit_rows = a.heads << a.group_shift;
+  const int pieces = rec.last - c + 1, first = kWide ? warp : 0;
   auto piece = [&](int i) -> int64_t { return ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * unit_rows + r; };
   float M = -INFINITY;
   for (int i = lane; i < pieces; i += 32) M = fmaxf(M, a.ws_m[piece(i)]);
@@ -1311,18 +1315,34 @@ __global__ void __launch_bounds__(kLjWarps * 32) line_join_kernel(const LineArgs
   float L = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
+#pragma unroll 8
+  for (int i = first; i < pieces; i += kWarps) {
     const int64_t p = piece(i);
+    const Vec v = *reinterpret_cast<const Vec*>(a.ws_acc + p * D + lane * kPer);
     const float f = fast_exp2((a.ws_m[p] - base) * a.scale_log2);
     L = fmaf(a.ws_l[p], f, L);
-    const float* x = a.ws_acc + p * D + lane * kPer;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = fmaf(x[k], f, acc[k]);
+    for (int k = 0; k < kPer; ++k) acc[k] = fmaf(reinterpret_cast<const float*>(&v)[k], f, acc[k]);
   }
-  T* o = static_cast<T*>(a.out) + (rec.row0 + r) * D + lane * kPer;
+  T* o = static_cast<T*>(a.out) + (rec.row0 + r) * D;
+  if constexpr (kWide) {
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) o[k] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[k] / L);
+    for (int k = 0; k < kPer; ++k) s_acc[warp][lane * kPer + k] = acc[k];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
+      float sum = 0.f, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sum += s_acc[w][d];
+        total += s_l[w];
+      }
+      o[d] = Elt<T>::from_float(M == -INFINITY ? 0.f : sum / total);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[lane * kPer + k] = Elt<T>::from_float(M == -INFINITY ? 0.f : acc[k] / L);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1392,14 +1412,19 @@ int resident_of(bool packed, pa_dtype dt, int group) {
   return dt == PA_FP32 ? resident<FloatRows<D, NT>, D>(group) : resident<FullRows<__half, D, NT>, D>(group);
 }
 
+template <typename T, int D, bool kWide>
+cudaError_t launch_join_as(const LineArgs& a, cudaStream_t s) {
+  const int rows = a.heads * a.group, warps = kWide ? kLjWideWarps : kLjWarps;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = overlapped(dim3((unsigned)(kWide ? rows : (rows + warps - 1) / warps), (unsigned)a.ctas),
+                                            32 * warps, 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, line_join_kernel<T, D, kWide>, a);
+}
 template <typename T>
 cudaError_t launch_join(const LineArgs& a, cudaStream_t s) {
-  const int rows = a.heads * a.group;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      overlapped(dim3((unsigned)((rows + kLjWarps - 1) / kLjWarps), (unsigned)a.ctas), kLjWarps * 32, 0, s, attr);
-  return a.head_dim == 64 ? cudaLaunchKernelEx(&cfg, line_join_kernel<T, 64>, a)
-                          : cudaLaunchKernelEx(&cfg, line_join_kernel<T, 128>, a);
+  const bool wide = a.ctas >= (int64_t)kLjWidePieces * a.batch * a.units;
+  if (a.head_dim == 64) return wide ? launch_join_as<T, 64, true>(a, s) : launch_join_as<T, 64, false>(a, s);
+  return wide ? launch_join_as<T, 128, true>(a, s) : launch_join_as<T, 128, false>(a, s);
 }
 
 }  // namespace
