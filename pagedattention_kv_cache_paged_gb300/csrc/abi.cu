@@ -1085,7 +1085,7 @@ int write_q4_impl(const void* k_new, const void* v_new, const int64_t* slot_mapp
   const int64_t total_slots = num_blocks * block_size;
   if (checked() && (rc = validate_slots(slot_mapping, n_tokens, total_slots, s))) return rc;
   const Q4WriteArgs a{k_new,    v_new,    slot_mapping, n_tokens,    k_codes,
-                      v_codes,  k_params, v_params,     total_slots, n_kv_heads * head_dim / 8,
+                      v_codes,  k_params, v_params,     total_slots, n_kv_heads * head_dim / 16,
                       err};
   int launches = 0;
   cudaError_t e = launch_kv_write_q4(a, dtype, s, &launches);
@@ -1121,7 +1121,7 @@ int unpack_q4_impl(const void* k_codes, const void* v_codes, const void* k_param
     }
   }
   const Q4UnpackArgs a{k_codes, v_codes,     k_params, v_params, cache_blocks, k_pool, v_pool, num_blocks,
-                       block_pairs, n_pairs, (int)(block_elems / 8), stride_bytes / dtype_bytes(dtype), err};
+                       block_pairs, n_pairs, (int)(block_elems / 16), stride_bytes / dtype_bytes(dtype), err};
   int launches = 0;
   cudaError_t e = launch_kv_unpack_q4(a, dtype, s, &launches);
   return finish(e, launches);

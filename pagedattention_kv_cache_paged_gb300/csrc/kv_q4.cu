@@ -18,42 +18,36 @@
 namespace pa {
 
 constexpr int kQ4Threads = 256;
-constexpr int kQ4Vals = 8;                          // values of a thread
+constexpr int kQ4Vals = 16;                         // values of a thread
 constexpr int kQ4Lanes = kQ4Group / kQ4Vals;        // threads of a group
 
-// Eight consecutive values as 32-bit numbers.
+// Sixteen consecutive values as 32-bit numbers.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    Elt<T>::unpack(ld_stream16(p), x);
-  } else {
-    float lo[4], hi[4];
-    Elt<float>::unpack(ld_stream16(p), lo);
-    Elt<float>::unpack(ld_stream16(p + 4), hi);
+__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+  constexpr int kVec = Elt<T>::kVec;
+  uint4 v[16 / kVec];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = lo[i];
-      x[4 + i] = hi[i];
-    }
-  }
+  for (int i = 0; i < 16 / kVec; ++i) v[i] = ld_stream16(p + i * kVec);
+#pragma unroll
+  for (int i = 0; i < 16 / kVec; ++i) Elt<T>::unpack(v[i], *reinterpret_cast<float(*)[kVec]>(&x[i * kVec]));
 }
 
 // The whole number nearest to x / s (halves to the even one), exactly; |x / s| < 2^20, inv = 1 / s in 32 bits.
-__device__ __forceinline__ int q4_round(float x, float s, float inv) {
+__device__ __forceinline__ float q4_round(float x, float s, float inv) {
   float r = rintf(x * inv);
   const float e = fmaf(-r, s, x), h = 0.5f * s;
   const bool odd = ((int)r & 1) != 0;
   if (e > h || (odd && e == h)) r += 1.f;
   else if (e < -h || (odd && e == -h)) r -= 1.f;
-  return (int)r;
+  return r;
 }
 
-// Packs the eight values of a thread; the kQ4Lanes threads of a group (a part of a warp, all of it here) work
+// Packs the sixteen values of a thread; the kQ4Lanes threads of a group (a part of a warp, all of it here) work
 // together.  Returns the codes; pair: the group's (scale, zero).
-__device__ __forceinline__ uint32_t q4_pack8(const float (&x)[8], uint32_t& pair) {
+__device__ __forceinline__ uint2 q4_pack16(const float (&x)[16], uint32_t& pair) {
   float lo = 0.f, hi = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     lo = min_nan(lo, x[i]);
     hi = max_nan(hi, x[i]);
   }
@@ -65,59 +59,85 @@ __device__ __forceinline__ uint32_t q4_pack8(const float (&x)[8], uint32_t& pair
   const float s = __bfloat162float(__float2bfloat16_rn(__fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f))));
   if (!(s <= FLT_MAX)) {  // a value that is not finite
     pair = 0x7fc0u;       // NaN, 0
-    return 0u;
+    return make_uint2(0u, 0u);
   }
   if (s < FLT_MIN) {  // nothing but zeros, or next to nothing
     pair = 0u;
-    return 0u;
+    return make_uint2(0u, 0u);
   }
   const float inv = 1.f / s;
-  const int z = min(max(q4_round(-lo, s, inv), 0), 15);
-  uint32_t codes = 0;
+  const float z = fminf(fmaxf(q4_round(-lo, s, inv), 0.f), 15.f);
+  pair = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
+  // Every quotient is rounded by adding 1.5 * 2^23 to it; where the remainder of one of the sixteen is not below half a
+  // scale, it may be a half or rounded to the wrong side, and they are all rounded by q4_round.
+  constexpr float kWhole = 12582912.f;
+  float c[16], most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) codes |= (uint32_t)min(max(q4_round(x[i], s, inv) + z, 0), 15) << (4 * i);
-  pair = (__float_as_uint(s) >> 16) | (__float_as_uint((float)z) & 0xffff0000u);
-  return codes;
+  for (int i = 0; i < 16; ++i) {
+    const float r = fmaf(x[i], inv, kWhole) - kWhole;
+    most = fmaxf(most, fabsf(fmaf(-r, s, x[i])));
+    c[i] = r;
+  }
+  if (most >= 0.5f * s) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[i] = q4_round(x[i], s, inv);
+  }
+  uint32_t w[4];  // four codes each, in the low half
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) v = fmaf(v, 16.f, fminf(fmaxf(c[4 * k + i] + z, 0.f), 15.f));
+    w[k] = __float_as_uint(v + 8388608.f);
+  }
+  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
-// Thread (token, KV head and group, eighth of it), K and V.  Bound by HBM.
+// Thread (token, KV head and group, quarter of it); blockIdx.y: K or V.  32,768 rows of 8 x 128 bf16 values take 30 us
+// (5.7 TB/s of what is read and written), near HBM's time and that of the arithmetic, 13 instructions a value.
 template <typename T>
-__global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteArgs a) {
-  const int64_t idx = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x;
-  // (whole groups: the lanes of one are all here or all past the end; rows are computed even if nothing is written,
-  // so that the lanes of a warp stay together)
-  const int64_t t = min(idx / a.row_lanes, a.n_tokens - 1);
-  const int c = (int)(idx - idx / a.row_lanes * a.row_lanes);
-  int64_t slot = __ldg(a.slot_mapping + t);
-  if (idx >= a.n_tokens * a.row_lanes) slot = -1;
-  if (slot >= a.total_slots) {
-    if (c == 0) raise_error(a.err, PA_DEVERR_SLOT);
-    slot = -1;
+__global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteArgs a, const int tokens_cta) {
+  // a CTA takes whole tokens, or (wide rows) a part of one; the threads of a group are all here or all past the end, and
+  // what writes nothing computes all the same, so that the lanes of a warp stay together
+  const int lane_token = threadIdx.x / a.row_lanes;
+  int64_t t;
+  int c;
+  if (tokens_cta > 0) {
+    t = (int64_t)blockIdx.x * tokens_cta + lane_token;
+    c = threadIdx.x - lane_token * a.row_lanes;
+  } else {
+    const unsigned parts = (a.row_lanes + kQ4Threads - 1) / kQ4Threads;
+    t = blockIdx.x / parts;
+    c = (blockIdx.x - (unsigned)t * parts) * kQ4Threads + threadIdx.x;
   }
-  const int64_t src = (t * a.row_lanes + c) * kQ4Vals;
-  float xk[8], xv[8];
-  load8(static_cast<const T*>(a.k_new) + src, xk);
-  load8(static_cast<const T*>(a.v_new) + src, xv);
-  uint32_t pk, pv;
-  const uint32_t ck = q4_pack8(xk, pk), cv = q4_pack8(xv, pv);
-  if (slot < 0) return;
+  bool here = t < a.n_tokens && c < a.row_lanes && (tokens_cta == 0 || lane_token < tokens_cta);
+  if (!here) t = c = 0;
+  const int64_t slot = __ldg(a.slot_mapping + t);
+  if (slot >= a.total_slots && here) {
+    if (c == 0 && blockIdx.y == 0) raise_error(a.err, PA_DEVERR_SLOT);
+    here = false;
+  }
+  float x[16];
+  load16(static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new) + (t * a.row_lanes + c) * kQ4Vals, x);
+  uint32_t pair;
+  const uint2 codes = q4_pack16(x, pair);
+  if (!here || slot < 0) return;
   const int64_t dst = slot * a.row_lanes + c;
-  static_cast<uint32_t*>(a.k_codes)[dst] = ck;
-  static_cast<uint32_t*>(a.v_codes)[dst] = cv;
-  if (c % kQ4Lanes == 0) {
-    static_cast<uint32_t*>(a.k_params)[dst / kQ4Lanes] = pk;
-    static_cast<uint32_t*>(a.v_params)[dst / kQ4Lanes] = pv;
-  }
+  static_cast<uint2*>(blockIdx.y ? a.v_codes : a.k_codes)[dst] = codes;
+  if (c % kQ4Lanes == 0) static_cast<uint32_t*>(blockIdx.y ? a.v_params : a.k_params)[dst / kQ4Lanes] = pair;
 }
 
 cudaError_t launch_kv_write_q4(const Q4WriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
-  const int64_t blocks = (a.n_tokens * a.row_lanes + kQ4Threads - 1) / kQ4Threads;
-  if (blocks == 0) return cudaSuccess;
+  if (a.n_tokens == 0) return cudaSuccess;
+  const int tokens = kQ4Threads / a.row_lanes;
+  const int64_t blocks = tokens > 0 ? (a.n_tokens + tokens - 1) / tokens
+                                    : a.n_tokens * ((a.row_lanes + kQ4Threads - 1) / kQ4Threads);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, 2);
   switch (dt) {
-    case PA_BF16: kv_write_q4_kernel<__nv_bfloat16><<<(unsigned)blocks, kQ4Threads, 0, s>>>(a); break;
-    case PA_FP16: kv_write_q4_kernel<__half><<<(unsigned)blocks, kQ4Threads, 0, s>>>(a); break;
-    case PA_FP32: kv_write_q4_kernel<float><<<(unsigned)blocks, kQ4Threads, 0, s>>>(a); break;
+    case PA_BF16: kv_write_q4_kernel<__nv_bfloat16><<<grid, kQ4Threads, 0, s>>>(a, tokens); break;
+    case PA_FP16: kv_write_q4_kernel<__half><<<grid, kQ4Threads, 0, s>>>(a, tokens); break;
+    case PA_FP32: kv_write_q4_kernel<float><<<grid, kQ4Threads, 0, s>>>(a, tokens); break;
     default: return cudaErrorInvalidValue;
   }
   ++*launches;
@@ -134,22 +154,61 @@ struct Largest<__half> { static constexpr float kValue = 65504.f; };
 template <>
 struct Largest<float> { static constexpr float kValue = FLT_MAX; };
 
-// Eight values of a thread to memory.  The largest codes of a group may stand for a little more than the type's
-// largest number (the scale is rounded): they become that.
+// Sixteen values of a thread to memory.  The largest codes of a group may stand for a little more than the type's
+// largest number (the scale is rounded): they become that.  bf16: 128 + code of two values by two logical instructions,
+// minus 128 + zero, times the scale, all in bf16 pairs, which round once, at the end (code - zero is exact).
 template <typename T>
-__device__ __forceinline__ void unpack8(uint32_t codes, uint32_t pair, T* p) {
+__device__ __forceinline__ void unpack16(const uint2& codes, uint32_t pair, T* p, bool aligned32) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   const float s = q4_scale(pair), z = q4_zero(pair);
-  float x[8];
+  if constexpr (sizeof(T) == 2) {
+    uint32_t y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = s * ((float)((codes >> (4 * i)) & 15u) - z);
-    x[i] = max_nan(min_nan(v, Largest<T>::kValue), -Largest<T>::kValue);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w = k ? codes.y : codes.x;
+      uint32_t q[4];  // values i and i + 4
+      if constexpr (kBf16) {
+        const uint32_t s2 = __byte_perm(pair, pair, 0x1010), top = 0x7f7f7f7fu;
+        uint32_t b2;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(b2) : "r"(__byte_perm(pair, pair, 0x3232)), "r"(0x43004300u));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+          asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(b2));
+          asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(s2));
+          asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(top));
+          asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(top | 0x80008000u));
+          q[i] = v;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u;  // 1024 + code
+          const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&v));
+          const float lo = s * (c.x - (1024.f + z)), hi = s * (c.y - (1024.f + z));
+          constexpr float kTop = Largest<T>::kValue;
+          const __half2 h = __floats2half2_rn(max_nan(min_nan(lo, kTop), -kTop), max_nan(min_nan(hi, kTop), -kTop));
+          q[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      y[4 * k] = __byte_perm(q[0], q[1], 0x5410);
+      y[4 * k + 1] = __byte_perm(q[2], q[3], 0x5410);
+      y[4 * k + 2] = __byte_perm(q[0], q[1], 0x7632);
+      y[4 * k + 3] = __byte_perm(q[2], q[3], 0x7632);
+    }
+    st_global32(p, y, aligned32);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = s * (__uint_as_float((((k ? codes.y : codes.x) >> (4 * i)) & 15u) | 0x4b000000u) - (8388608.f + z));
+        y[i] = __float_as_uint(max_nan(min_nan(v, FLT_MAX), -FLT_MAX));
+      }
+      st_global32(p + 8 * k, y, aligned32);
+    }
   }
-  alignas(16) T y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = Elt<T>::from_float(x[i]);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(y) / 16; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(y)[i];
 }
 
 constexpr int kQ4Unroll = 2;  // words of K and of V in flight per thread
@@ -164,14 +223,16 @@ __global__ void __launch_bounds__(kQ4Threads) kv_unpack_q4_kernel(const Q4Unpack
     if (slice == 0 && threadIdx.x == 0) raise_error(a.err, PA_DEVERR_COPY_PAIR);
     return;
   }
-  const uint32_t* kc = static_cast<const uint32_t*>(a.k_codes) + src * a.block_words;
-  const uint32_t* vc = static_cast<const uint32_t*>(a.v_codes) + src * a.block_words;
+  const uint2* kc = static_cast<const uint2*>(a.k_codes) + src * a.block_words;
+  const uint2* vc = static_cast<const uint2*>(a.v_codes) + src * a.block_words;
   const uint32_t* kp = static_cast<const uint32_t*>(a.k_params) + src * (a.block_words / kQ4Lanes);
   const uint32_t* vp = static_cast<const uint32_t*>(a.v_params) + src * (a.block_words / kQ4Lanes);
   T* ko = static_cast<T*>(a.k_pool) + dst * a.block_stride;
   T* vo = static_cast<T*>(a.v_pool) + dst * a.block_stride;
+  const bool wide = ((reinterpret_cast<uintptr_t>(ko) | reinterpret_cast<uintptr_t>(vo)) & 31u) == 0;
   for (int w0 = slice * kQ4Threads * kQ4Unroll + threadIdx.x; w0 < a.block_words; w0 += slices * kQ4Threads * kQ4Unroll) {
-    uint32_t c[kQ4Unroll][2], p[kQ4Unroll][2];
+    uint2 c[kQ4Unroll][2];
+    uint32_t p[kQ4Unroll][2];
 #pragma unroll
     for (int u = 0; u < kQ4Unroll; ++u) {
       const int w = w0 + u * kQ4Threads;
@@ -186,8 +247,8 @@ __global__ void __launch_bounds__(kQ4Threads) kv_unpack_q4_kernel(const Q4Unpack
     for (int u = 0; u < kQ4Unroll; ++u) {
       const int w = w0 + u * kQ4Threads;
       if (w < a.block_words) {
-        unpack8<T>(c[u][0], p[u][0], ko + (int64_t)w * kQ4Vals);
-        unpack8<T>(c[u][1], p[u][1], vo + (int64_t)w * kQ4Vals);
+        unpack16<T>(c[u][0], p[u][0], ko + (int64_t)w * kQ4Vals, wide);
+        unpack16<T>(c[u][1], p[u][1], vo + (int64_t)w * kQ4Vals, wide);
       }
     }
   }

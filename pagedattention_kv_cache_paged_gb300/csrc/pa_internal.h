@@ -240,7 +240,7 @@ struct Q4WriteArgs {
   void* k_params;
   void* v_params;
   int64_t total_slots;             // num_blocks * block_size
-  int row_lanes;                   // n_kv_heads * head_dim / 8 (values of a thread)
+  int row_lanes;                   // n_kv_heads * head_dim / 16 (values of a thread)
   unsigned* err;
 };
 
@@ -256,7 +256,7 @@ struct Q4UnpackArgs {
   int64_t num_blocks;
   const int64_t* pairs;            // (block of the cache, block of the pools)
   int64_t n_pairs;
-  int block_words;                 // 32-bit words of codes in a block
+  int block_words;                 // 64-bit words of codes in a block
   int64_t block_stride;            // elements from one block of a pool to the next
   unsigned* err;
 };
