@@ -3,10 +3,14 @@
 //
 // Packing.  Of 64 values: lo = min(0, min x), hi = max(0, max x), scale = bf16(fp32(hi / 15) - fp32(lo / 15)),
 // zero = round(-lo / scale), code = round(x / scale) + zero, both clamped to 0 .. 15.  (Zero is on the grid, so
-// x / scale is rounded by itself.)  The quotients are rounded to the nearest whole number, halves to the even one,
-// as real numbers: with r the nearest to x * (1 / scale) in 32 bits, the remainder x - r * scale is exact wherever
-// it decides (r * scale has 13 bits, and next to a half the remainder fits 24), so comparing it with scale / 2
-// says whether r is right.  What a value is packed to therefore depends on nothing but the definition.
+// x / scale is rounded by itself.)  The quotients are rounded to the nearest whole number, halves to the even one, as real
+// numbers, so that what a value is packed to depends on nothing but the definition:
+//   16-bit values.  Their quotient by a scale of 8 bits is a half or at least 2^-12 away from one, so its fp32 rounding
+//     decides.  That is formed from the rounded reciprocal and one exact remainder (Markstein's division): q = x / s
+//     rounded, q += (x - q s) / s.
+//   fp32 values.  With r the nearest to x * (1 / scale) in 32 bits, the remainder x - r * scale is exact wherever it
+//     decides (r * scale has 13 bits, and next to a half the remainder fits 24), so comparing it with scale / 2 says
+//     whether r is right.
 // A group that holds a value that is not finite gets scale NaN, and all its values are NaN.
 #include <float.h>
 
@@ -21,15 +25,40 @@ constexpr int kQ4Threads = 256;
 constexpr int kQ4Vals = 16;                         // values of a thread
 constexpr int kQ4Lanes = kQ4Group / kQ4Vals;        // threads of a group
 
-// Sixteen consecutive values as 32-bit numbers.
+// Sixteen consecutive values as 32-bit numbers, and the smallest and the largest of them and 0 (NaN if one is).
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+__device__ __forceinline__ void load16(const T* p, float (&x)[16], float& lo, float& hi) {
   constexpr int kVec = Elt<T>::kVec;
   uint4 v[16 / kVec];
 #pragma unroll
   for (int i = 0; i < 16 / kVec; ++i) v[i] = ld_stream16(p + i * kVec);
 #pragma unroll
   for (int i = 0; i < 16 / kVec; ++i) Elt<T>::unpack(v[i], *reinterpret_cast<float(*)[kVec]>(&x[i * kVec]));
+  if constexpr (sizeof(T) == 2) {  // two at a time
+    uint32_t a = 0u, b = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(v)[i];
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(w));
+      } else {
+        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(w));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(b) : "r"(w));
+      }
+    }
+    float f[8];
+    Elt<T>::unpack(make_uint4(a, b, 0u, 0u), f);
+    lo = min_nan(f[0], f[1]);
+    hi = max_nan(f[2], f[3]);
+  } else {
+    lo = hi = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      lo = min_nan(lo, x[i]);
+      hi = max_nan(hi, x[i]);
+    }
+  }
 }
 
 // The whole number nearest to x / s (halves to the even one), exactly; |x / s| < 2^20, inv = 1 / s in 32 bits.
@@ -43,14 +72,9 @@ __device__ __forceinline__ float q4_round(float x, float s, float inv) {
 }
 
 // Packs the sixteen values of a thread; the kQ4Lanes threads of a group (a part of a warp, all of it here) work
-// together.  Returns the codes; pair: the group's (scale, zero).
-__device__ __forceinline__ uint2 q4_pack16(const float (&x)[16], uint32_t& pair) {
-  float lo = 0.f, hi = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
-  }
+// together; lo, hi: of its own values.  Returns the codes; pair: the group's (scale, zero); kShort: values of at most 11 bits.
+template <bool kShort>
+__device__ __forceinline__ uint2 q4_pack16(float (&x)[16], float lo, float hi, uint32_t& pair) {
 #pragma unroll
   for (int off = 1; off < kQ4Lanes; off <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
@@ -68,29 +92,48 @@ __device__ __forceinline__ uint2 q4_pack16(const float (&x)[16], uint32_t& pair)
   const float inv = 1.f / s;
   const float z = fminf(fmaxf(q4_round(-lo, s, inv), 0.f), 15.f);
   pair = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
-  // Every quotient is rounded by adding 1.5 * 2^23 to it; where the remainder of one of the sixteen is not below half a
-  // scale, it may be a half or rounded to the wrong side, and they are all rounded by q4_round.
+  // Added to a number, 1.5 * 2^23 rounds it to a whole one, which is then in the sum's low bits: codes are put together
+  // from those, and what 1.5 * 2^23 and zero add to all eight of a word is taken off at the end.  None is below 0: the
+  // smallest rounds to -zero.
   constexpr float kWhole = 12582912.f;
-  float c[16], most = 0.f;
+  const float top = kWhole + 15.f - z;
+  float c[16];
+  if constexpr (kShort) {
+    // (remainders of numbers of 2^-60 and less would not be exact: both sides times 2^64)
+    const bool tiny = s < 8.6736174e-19f;
+    const float s1 = tiny ? s * 18446744073709551616.f : s, inv1 = tiny ? inv * 5.4210109e-20f : inv;
+    if (tiny) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float r = fmaf(x[i], inv, kWhole) - kWhole;
-    most = fmaxf(most, fabsf(fmaf(-r, s, x[i])));
-    c[i] = r;
+      for (int i = 0; i < 16; ++i) x[i] *= 18446744073709551616.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float q = x[i] * inv1;
+      c[i] = fmaf(fmaf(-q, s1, x[i]), inv1, q) + kWhole;
+    }
+  } else {
+    // all rounded again by q4_round where the remainder of one of them is not below half a scale
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      c[i] = fmaf(x[i], inv, kWhole);
+      most = fmaxf(most, fabsf(fmaf(-(c[i] - kWhole), s, x[i])));
+    }
+    if (most >= 0.5f * s) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) c[i] = q4_round(x[i], s, inv) + kWhole;
+    }
   }
-  if (most >= 0.5f * s) {
+  const uint32_t off = (__float_as_uint(kWhole) - (uint32_t)(int)z) * 0x11111111u;
+  uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) c[i] = q4_round(x[i], s, inv);
+  for (int k = 0; k < 2; ++k) {
+    w[k] = 0u;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) w[k] = w[k] * 16u + __float_as_uint(fminf(c[8 * k + i], top));
+    w[k] -= off;
   }
-  uint32_t w[4];  // four codes each, in the low half
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 3; i >= 0; --i) v = fmaf(v, 16.f, fminf(fmaxf(c[4 * k + i] + z, 0.f), 15.f));
-    w[k] = __float_as_uint(v + 8388608.f);
-  }
-  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+  return make_uint2(w[0], w[1]);
 }
 
 // Thread (token, KV head and group, quarter of it); blockIdx.y: K or V.  32,768 rows of 8 x 128 bf16 values take 30 us
@@ -117,10 +160,10 @@ __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteAr
     if (c == 0 && blockIdx.y == 0) raise_error(a.err, PA_DEVERR_SLOT);
     here = false;
   }
-  float x[16];
-  load16(static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new) + (t * a.row_lanes + c) * kQ4Vals, x);
+  float x[16], lo, hi;
+  load16(static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new) + (t * a.row_lanes + c) * kQ4Vals, x, lo, hi);
   uint32_t pair;
-  const uint2 codes = q4_pack16(x, pair);
+  const uint2 codes = q4_pack16<sizeof(T) == 2>(x, lo, hi, pair);
   if (!here || slot < 0) return;
   const int64_t dst = slot * a.row_lanes + c;
   static_cast<uint2*>(blockIdx.y ? a.v_codes : a.k_codes)[dst] = codes;
