@@ -1052,7 +1052,7 @@ int window_impl(void* out, const void* q, const int32_t* query_start_loc, int64_
   a.window = window;
   a.sinks = sinks;
   int launches = 0;
-  cudaError_t e = tc_ok && o.prefill_kernel != 1 ? launch_prefill_umma_window(a, dtype, s, &launches)
+  cudaError_t e = tc_ok && o.prefill_kernel != 1 ? launch_window_umma(a, dtype, s, &launches)
                                                  : launch_attn_simt_window(a, dtype, s, &launches);
   return finish(e, launches);
 }

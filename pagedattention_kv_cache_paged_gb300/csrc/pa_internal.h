@@ -360,8 +360,8 @@ cudaError_t launch_decode_tc(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int
 // tcgen05 causal prefill (TMEM accumulators, TMA rings, warp-specialised) for bf16/fp16 pools with
 // block_size % 16 == 0 (the support set of the tensor-core decode).
 cudaError_t launch_prefill_umma(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
-// Its windowed form (a.window, a.sinks).
-cudaError_t launch_prefill_umma_window(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
+// Chunks behind a sliding window (a.window, a.sinks), the same shapes.
+cudaError_t launch_window_umma(const AttnArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
 
 // Bounded-wait self-test (selftest.cu): one CTA whose two waits run out; see pa_selftest_bounded_wait.
 cudaError_t launch_selftest_wait(unsigned* err, unsigned epoch, uint64_t limit_ns, unsigned long long* elapsed_ns,
