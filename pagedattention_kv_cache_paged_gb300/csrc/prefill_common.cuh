@@ -88,7 +88,7 @@ struct ScoreFix {
 // Columns [c0, c0 + 64) of the row of S into registers (two loads in flight, one wait), rewritten
 // as `fix` says; m0 / m1 are the mask words of the block's two 32-key chunks.  One instantiation
 // per masking mode (kMode = fix.mode): mode 0 runs no masking code at all, mode 1 applies the prefix
-// cut only in a block that the cut falls in, mode 2 is the rare general rewrite, mode 3 the mask alone (window_umma.cu).  (One copy of the
+// cut only in a block that the cut falls in, mode 2 is the rare general rewrite.  (One copy of the
 // code for modes 0 and 1, the cut behind a warp-uniform branch, measured slower.)
 template <int kMode>
 __device__ __forceinline__ void s_load64(uint32_t taddr, uint32_t (&sv)[64], const ScoreFix& fix, int c0,
@@ -110,10 +110,6 @@ __device__ __forceinline__ void s_load64(uint32_t taddr, uint32_t (&sv)[64], con
       const uint32_t v = fix.zero ? 0u : (sv[j] ^ fix.flip);
       sv[j] = (((j < 32 ? m0 : m1) >> (j & 31)) & 1u) ? v : 0xff800000u;  // -inf
     }
-  } else if (kMode == 3) {
-#pragma unroll
-    for (int j = 0; j < 64; ++j)
-      if (!(((j < 32 ? m0 : m1) >> (j & 31)) & 1u)) sv[j] = 0xff800000u;
   }
 }
 
