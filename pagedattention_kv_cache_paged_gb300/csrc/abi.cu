@@ -878,7 +878,8 @@ LinePlan plan_line(bool packed, int batch, int n_q_heads, int n_kv_heads, int he
   p.heads = line_heads(packed, n_kv_heads);
   p.units = n_kv_heads / p.heads;
   const int step = 16 * (line_warps(packed) / p.heads);
-  const int64_t max_seen = std::min(table_capacity(bt_stride, block_size), (int64_t)window + sinks);
+  // (and up to 15 tokens next to the window's beginning and the sinks' end, see LineArgs.aligned)
+  const int64_t max_seen = std::min(table_capacity(bt_stride, block_size), (int64_t)window + sinks + 30);
   const int64_t tiles = (max_seen + step - 1) / step;
   p.fits = (int64_t)p.units * batch < (int64_t(1) << 30) / (tiles + kLineGap);
   if (!p.fits) return p;
@@ -977,7 +978,9 @@ int run_line(LineArgs& a, bool packed, int64_t bt_stride, int batch, int64_t num
     a.ws_l = reinterpret_cast<float*>(base + plan.off_l);
     a.ws_rec = reinterpret_cast<TreeRec*>(base + plan.off_rec);
   }
+  a.aligned = !packed && decode_tc_supported(dtype, block_size, head_dim, a.group, num_blocks);
   a.err = err;
+  a.epoch = next_epoch();
   int launches = 0;
   cudaError_t e = launch_line_decode(a, dtype, packed, s, &launches);
   return finish(e, launches);

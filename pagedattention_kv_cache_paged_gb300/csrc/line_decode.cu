@@ -34,14 +34,22 @@
 
 namespace pa {
 
+// TMA views of the pools (16-bit pools in blocks of a multiple of 16 tokens).
+struct LineMaps {
+  CUtensorMap k, v;
+};
+
 // ------------------------------------------------------------------------------------------------
 // Sequences and the line
 // ------------------------------------------------------------------------------------------------
 
 // What is visible of a sequence: its first tokens and its last ones, `seen` in all; position of visible token v is v, or
 // v + skip from `first` on.
+// With a.aligned both parts are whole 16-key sub-tiles, whose ends a row's mask cuts off: positions below a.sinks and from
+// `low` up to n.
 struct LineSeq {
   int first, skip, seen;
+  int low, n;
   bool bad;
 };
 
@@ -53,9 +61,16 @@ __device__ __forceinline__ LineSeq line_seq(const LineArgs& a, int b) {
     return s;
   }
   const int low = n > a.window ? n - a.window : 0;
+  s.low = low;
+  s.n = n;
   s.first = min(a.sinks, low);
   s.skip = low - s.first;
   s.seen = n - s.skip;
+  if (a.aligned) {
+    s.first = (s.first + 15) & ~15;
+    s.skip = max((low & ~15) - s.first, 0);
+    s.seen = ((n + 15) & ~15) - s.skip;
+  }
   return s;
 }
 
@@ -343,9 +358,12 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
 // ------------------------------------------------------------------------------------------------
 // 16-bit pools
 // ------------------------------------------------------------------------------------------------
-template <typename T, int D, int NT>
+// kTma (block sizes that are multiples of 16): a warp's step is a sub-tile of 16 keys of one block, loaded by lane 0 in TMA
+// boxes of 16 keys by 64 columns; otherwise its 16 tokens lie anywhere, and every lane copies parts of two of them.
+template <typename T, int D, int NT, bool kTmaBoxes>
 struct FullRows {
   using Out = T;
+  static constexpr bool kTma = kTmaBoxes;
   using Row = int64_t;  // offset of a row
   static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   static constexpr int kWarps = 4, kCtas = 3;
@@ -365,7 +383,29 @@ struct FullRows {
       : k(static_cast<const T*>(a.k)), v(static_cast<const T*>(a.v)) {}
 
   // 8-element chunk c of token t of an operand, in its place (ldmatrix reads eight rows of a chunk without conflicts)
-  static __device__ __forceinline__ uint32_t at(int t, int c) { return (uint32_t)(t * kRow + ((c ^ (t & 7)) << 4)); }
+  // (a TMA box puts 64 columns of the 16 tokens together, with the 128-byte swizzle)
+  static __device__ __forceinline__ uint32_t at(int t, int c) {
+    return kTma ? (uint32_t)((c >> 3) * 2048 + t * 128 + (((c & 7) ^ (t & 7)) << 4))
+                : (uint32_t)(t * kRow + ((c ^ (t & 7)) << 4));
+  }
+
+  // kTma: the boxes of KV head h, block `block`, from token `token` of it on (one lane).
+  static __device__ __forceinline__ void load_boxes(uint8_t* st, const LineMaps& maps, int block, int token,
+                                                    int h, uint64_t* bar, uint64_t policy) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      tma_load_3d_hint(st + i * 2048, &maps.k, h * D + i * 64, token, block, bar, policy);
+      tma_load_3d_hint(st + 16 * kRow + i * 2048, &maps.v, h * D + i * 64, token, block, bar, policy);
+    }
+  }
+  // kTma: zeros in the V rows of tokens that do not exist (whatever lies there times a weight of 0 has to be 0).
+  static __device__ __forceinline__ void clear_rows(uint8_t* st, int lane, unsigned exist) {
+    for (int i = lane; i < 16 * (D / 8); i += 32) {
+      const int t = i / (D / 8);
+      if (!((exist >> t) & 1u)) *reinterpret_cast<uint4*>(st + 16 * kRow + at(t, i % (D / 8))) = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+  }
 
   // tokens r and r + 8 of the step (r = lane / 4), rows `row` of the pools (element offsets)
   __device__ __forceinline__ void load(const LineArgs& a, uint32_t st, int lane, const int64_t (&row)[2],
@@ -452,6 +492,7 @@ struct FullRows {
 // ------------------------------------------------------------------------------------------------
 template <int D, int NT>
 struct FloatRows {
+  static constexpr bool kTma = false;
   using Out = float;
   using Row = int64_t;
   static constexpr int kWarps = 4, kCtas = 1;
@@ -623,6 +664,7 @@ struct PackedStage {
 // is 2^-30 of the largest product or less.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
 template <typename T, int D, int NT>
 struct PackedRows : PackedStage<D> {
+  static constexpr bool kTma = false;
   using Out = T;
   using Stage = PackedStage<D>;
   using typename Stage::Row;
@@ -878,6 +920,7 @@ struct PackedRows : PackedStage<D> {
 // tensor core truncates its sums).
 template <int D, int NT>
 struct PackedWideRows : PackedStage<D> {
+  static constexpr bool kTma = false;
   using Out = float;
   using Stage = PackedStage<D>;
   using typename Stage::Row;
@@ -1053,17 +1096,23 @@ struct LineCfg {
 // [head_dim + kPad], [warp][row] twice.
 template <typename Rows, int D>
 constexpr int line_smem(int group) {
-  return LineCfg<Rows>::kRing + Rows::kWarps * group * (D + LineCfg<Rows>::kPad + 2) * 4;
+  return (Rows::kTma ? 1024 : 0) + LineCfg<Rows>::kRing + Rows::kWarps * group * (D + LineCfg<Rows>::kPad + 2) * 4;
 }
-constexpr int kLineStatic = 256;  // TreeSched
-static_assert(sizeof(TreeSched) <= kLineStatic, "the schedule's shared memory");
+constexpr int kLineStatic = 512;  // the schedule, the rings' barriers
+
 
 template <typename Rows, int D, int NT>
-__global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_decode_kernel(const LineArgs a) {
+__global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
+    line_decode_kernel(const LineArgs a, const __grid_constant__ LineMaps maps) {
   using T = typename Rows::Out;
   constexpr int kWarps = Rows::kWarps, kStages = Rows::kStages, kThreads = LineCfg<Rows>::kThreads;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem =
+      Rows::kTma ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) : smem_raw;
   __shared__ TreeSched sched;
+  // kTma: a warp's ring, when its steps have landed and the position of their first key (-1: no keys)
+  __shared__ uint64_t landed[Rows::kTma ? kWarps : 1][kStages];
+  __shared__ int32_t step_key[Rows::kTma ? kWarps : 1][kStages];
   constexpr int kOutRow = LineCfg<Rows>::kPad + D;  // (the pad keeps the rows that a store writes in different banks)
   float* const out_o = reinterpret_cast<float*>(smem + LineCfg<Rows>::kRing);
   float* const out_m = out_o + kWarps * a.group * kOutRow;
@@ -1076,6 +1125,13 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
     sched.span = TreeSpan{a.batch, 0, 0, a.batch, 0, 0};
     sched.refused = 0;
   }
+  if (Rows::kTma && lane == 0) {
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+    for (int s = 0; s < kStages; ++s) mbar_init(&landed[warp][s], 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
   __syncthreads();
   pdl_wait_primary();
   line_schedule<kThreads>(a, step_tokens, sched);
@@ -1087,7 +1143,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * Rows::kStage + Rows::kExtra));
   Rows rows(a, ring + kStages * Rows::kStage, lane);
 
-  // ---- the loads, kStages - 1 steps ahead ----
+  // ---- the loads, kStages - 1 steps ahead (kTma: kStages, a stage is filled again as soon as it has been read) ----
   LineWalk ahead(a, span, step_tokens);
   LineUnit lu;
   lu.b = 0;
@@ -1097,17 +1153,43 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   int block[2], at[2];  // block and token in it of this lane's two tokens of the next step
   bool have[2];
   unsigned oks = 0;  // two bits a step in flight: whether this lane's two tokens exist
+  const uint64_t policy = Rows::kTma ? l2_policy_evict_first() : 0;  // (keys and values are read once)
   auto look = [&]() {  // table entries of the next step
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int v = (lx * lanes_head + part) * 16 + (lane >> 2) + 8 * h;
+    for (int h = 0; h < (Rows::kTma ? 1 : 2); ++h) {
+      const int v = (lx * lanes_head + part) * 16 + (Rows::kTma ? 0 : (lane >> 2) + 8 * h);
       const int pos = v < lu.sq.first ? v : v + lu.sq.skip;
-      have[h] = more && v < lu.sq.seen;
-      at[h] = pos & (a.block_size - 1);
+      have[h] = more && v < lu.sq.seen && (!Rows::kTma || lane == 0);
+      at[h] = Rows::kTma ? pos : pos & (a.block_size - 1);
       block[h] = have[h] ? ld_s32(table + (pos >> a.block_shift)) : 0;
     }
   };
   auto load = [&](int stage) {
+    if constexpr (Rows::kTma) {
+      if (!more) return;
+      if (lane == 0) {
+        bool ok = have[0];
+        if (ok && (unsigned)block[0] >= a.block_limit) {
+          raise_error(a.err, PA_DEVERR_BLOCK_ID);
+          ok = false;
+        }
+        step_key[warp][stage] = ok ? at[0] : -1;
+        if (ok) {
+          mbar_arrive_expect_tx(&landed[warp][stage], Rows::kStage);
+          Rows::load_boxes(smem + (warp * kStages + stage) * Rows::kStage, maps, block[0], at[0] & (a.block_size - 1),
+                           lu.hg * a.heads + head, &landed[warp][stage], policy);
+        } else {
+          mbar_arrive(&landed[warp][stage]);
+        }
+      }
+      if (++lx == lu.x1) {
+        more = ahead.next(lu);
+        lx = more ? lu.x0 : 0;
+        table = a.block_table + lu.b * a.bt_stride;
+      }
+      look();
+      return;
+    }
     if (more) {
       typename Rows::Row row[2];
       bool ok[2];
@@ -1120,7 +1202,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
         }
         row[h] = ok[h] ? Rows::row_of(a, block[h], at[h], lu.hg * a.heads + head) : 0;
       }
-      rows.load(a, ring + stage * Rows::kStage, lane, row, ok);
+      if constexpr (!Rows::kTma) rows.load(a, ring + stage * Rows::kStage, lane, row, ok);
       oks = oks << 2 | (ok[1] ? 2u : 0u) | (ok[0] ? 1u : 0u);
       if (++lx == lu.x1) {
         more = ahead.next(lu);
@@ -1135,12 +1217,14 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
   };
   look();
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load(s);
+  for (int s = 0; s < (Rows::kTma ? kStages : kStages - 1); ++s) load(s);
 
   // ---- the products ----
   LineWalk walk(a, span, step_tokens);
   LineUnit w;
   int stage = 0;
+  unsigned phase = 0;  // kTma: of the ring's barriers
+  bool alive = true;   // kTma: no wait has given up (if one has, the units are walked through without their keys)
   while (walk.next(w)) {
     const int64_t head0 = (int64_t)w.b * a.n_q_heads + (int64_t)(w.hg * a.heads + head) * a.group;
     LineState<NT> ls;
@@ -1160,11 +1244,38 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
     }
     rows.query(a, head0, lane, ls);
     for (int x = w.x0; x < w.x1; ++x) {
+      if constexpr (Rows::kTma) {
+        if (alive && !__all_sync(0xffffffffu, mbar_wait(&landed[warp][stage], phase, a.err, a.epoch))) {
+          alive = false;
+          if (lane == 0) raise_timeout(a.err, a.epoch);
+        }
+        if (!alive) continue;
+        const int key = step_key[warp][stage], t = lane >> 2;
+        if (key >= 0) {
+          auto exists = [&](int p) { return p < w.sq.n && (p >= w.sq.low || p < a.sinks); };
+          bool ok0 = true, ok1 = true;
+          if (key + 16 > w.sq.n || key < w.sq.low) {  // (whole steps below the sinks' end take this way too)
+            ok0 = exists(key + t);
+            ok1 = exists(key + t + 8);
+            Rows::clear_rows(smem + (warp * kStages + stage) * Rows::kStage, lane,
+                             __ballot_sync(0xffffffffu, exists(key + (lane & 15))));
+          }
+          rows.step(ring + stage * Rows::kStage, lane, ok0, ok1, ls, o);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        load(stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        continue;
+      }
       copy_wait<kStages - 2>();
       __syncwarp();  // every lane's copies of this step are there, and the stage before has been read by all
       const unsigned ok = oks >> (2 * (kStages - 2));
       load(stage == 0 ? kStages - 1 : stage - 1);
-      rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, ls, o);
+      if constexpr (!Rows::kTma) rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, ls, o);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     // ---- the unit's end ----
@@ -1274,6 +1385,11 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas) line_dec
     }
   }
   copy_wait<0>();
+  if constexpr (Rows::kTma) {
+    // after a wait gave up: leave no copy in flight (bounded again; every stage was filled once more than it was read)
+    if (!alive && lane == 0)
+      for (int s = 0; s < kStages; ++s) mbar_wait(&landed[warp][s], s < stage ? phase ^ 1u : phase);
+  }
   // sequences that see nothing
   if (sched.refused) {
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -1362,9 +1478,9 @@ cudaLaunchConfig_t overlapped(dim3 grid, int threads, int smem, cudaStream_t s, 
 }
 
 template <typename Rows, int D, int NT>
-cudaError_t launch_rows(const LineArgs& a, cudaStream_t s) {
+cudaError_t launch_rows(const LineArgs& a, cudaStream_t s, const LineMaps& maps = LineMaps{}) {
   constexpr int most = line_smem<Rows, D>(8 * NT);
-  static_assert(most + kLineStatic <= 227 * 1024, "shared memory of a CTA");
+  static_assert(most + (Rows::kTma ? kLineStatic : 256) <= 227 * 1024, "shared memory of a CTA");
   static bool attr_set[64] = {};  // per instantiation and device; idempotent, so a race is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1377,7 +1493,7 @@ cudaError_t launch_rows(const LineArgs& a, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       overlapped(dim3((unsigned)a.ctas), LineCfg<Rows>::kThreads, line_smem<Rows, D>(a.group), s, attr);
-  return cudaLaunchKernelEx(&cfg, line_decode_kernel<Rows, D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, line_decode_kernel<Rows, D, NT>, a, maps);
 }
 
 template <typename T, int D>
@@ -1389,8 +1505,16 @@ cudaError_t launch_wide(const LineArgs& a, cudaStream_t s) {
   return a.group > 8 ? launch_rows<PackedWideRows<D, 2>, D, 2>(a, s) : launch_rows<PackedWideRows<D, 1>, D, 1>(a, s);
 }
 template <typename T, int D>
-cudaError_t launch_full(const LineArgs& a, cudaStream_t s) {
-  return a.group > 8 ? launch_rows<FullRows<T, D, 2>, D, 2>(a, s) : launch_rows<FullRows<T, D, 1>, D, 1>(a, s);
+cudaError_t launch_full(const LineArgs& a, pa_dtype dt, cudaStream_t s) {
+  if (a.aligned) {
+    LineMaps maps;
+    if (!encode_pool_map(&maps.k, a.k, dt, a.block_limit, a.block_size, a.n_kv_heads, D, a.block_stride) ||
+        !encode_pool_map(&maps.v, a.v, dt, a.block_limit, a.block_size, a.n_kv_heads, D, a.block_stride))
+      return cudaErrorInvalidValue;
+    return a.group > 8 ? launch_rows<FullRows<T, D, 2, true>, D, 2>(a, s, maps)
+                       : launch_rows<FullRows<T, D, 1, true>, D, 1>(a, s, maps);
+  }
+  return a.group > 8 ? launch_rows<FullRows<T, D, 2, false>, D, 2>(a, s) : launch_rows<FullRows<T, D, 1, false>, D, 1>(a, s);
 }
 
 template <int D>
@@ -1409,7 +1533,7 @@ int resident_of(bool packed, pa_dtype dt, int group) {
     return dt == PA_BF16   ? resident<PackedRows<__nv_bfloat16, D, NT>, D>(group)
            : dt == PA_FP16 ? resident<PackedRows<__half, D, NT>, D>(group)
                            : resident<PackedWideRows<D, NT>, D>(group);
-  return dt == PA_FP32 ? resident<FloatRows<D, NT>, D>(group) : resident<FullRows<__half, D, NT>, D>(group);
+  return dt == PA_FP32 ? resident<FloatRows<D, NT>, D>(group) : resident<FullRows<__half, D, NT, true>, D>(group);
 }
 
 template <typename T, int D, bool kWide>
@@ -1442,8 +1566,8 @@ cudaError_t launch_line_decode(const LineArgs& a, pa_dtype dt, bool packed, cuda
     if (dt == PA_FP16) e = d64 ? launch_packed<__half, 64>(a, s) : launch_packed<__half, 128>(a, s);
     if (dt == PA_FP32) e = d64 ? launch_wide<64>(a, s) : launch_wide<128>(a, s);
   } else {
-    if (dt == PA_BF16) e = d64 ? launch_full<__nv_bfloat16, 64>(a, s) : launch_full<__nv_bfloat16, 128>(a, s);
-    if (dt == PA_FP16) e = d64 ? launch_full<__half, 64>(a, s) : launch_full<__half, 128>(a, s);
+    if (dt == PA_BF16) e = d64 ? launch_full<__nv_bfloat16, 64>(a, dt, s) : launch_full<__nv_bfloat16, 128>(a, dt, s);
+    if (dt == PA_FP16) e = d64 ? launch_full<__half, 64>(a, dt, s) : launch_full<__half, 128>(a, dt, s);
     if (dt == PA_FP32) e = d64 ? launch_float<64>(a, s) : launch_float<128>(a, s);
   }
   if (e != cudaSuccess) return e;

@@ -279,6 +279,7 @@ struct LineArgs {
   int64_t block_stride;            // elements from one block of a pool to the next
   int window;
   int sinks;
+  int aligned;                     // visible tokens are taken in aligned groups of 16 (the TMA form)
   int32_t max_context;             // longest context that a table row and kTreeMaxContext allow
   float scale_log2;                // scale * log2(e)
   int n_q_heads;
@@ -299,6 +300,7 @@ struct LineArgs {
   float* ws_l;
   float* ws_acc;
   unsigned* err;
+  unsigned epoch;
 };
 
 // Warps of a CTA of the line decode (each takes 16 tokens of a KV head a step) and KV heads that it has side by side:
