@@ -134,23 +134,38 @@ __device__ __forceinline__ void line_schedule(const LineArgs& a, int step_tokens
     tiles = (s.seen + step_tokens - 1) / step_tokens;
     return a.units * (tiles + gap);
   };
-  int total = 0, longest = 0;
-  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    const int c = look(b);
-    total += c;
-    longest = max(longest, c > 0 ? tiles + gap : 0);
+  auto scan = [&](int x) {  // inclusive, over the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += u;
+    }
+    return x;
+  };
+  // (a batch of up to kThreads sequences: one look and one scan for both passes)
+  const bool one_chunk = a.batch <= kThreads;
+  int c = look(threadIdx.x);
+  int total = c, longest = c > 0 ? tiles + gap : 0;
+  for (int b = threadIdx.x + kThreads; b < a.batch; b += kThreads) {
+    const int more = look(b);
+    total += more;
+    longest = max(longest, more > 0 ? tiles + gap : 0);
   }
-  total = __reduce_add_sync(0xffffffffu, total);
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) {
-    sm.sums[warp] = total;
-    sm.tops[warp] = longest;
+  int v = one_chunk ? scan(c) : 0;
+  const int warp_total = one_chunk ? v : __reduce_add_sync(0xffffffffu, total);  // (in lane 31)
+  const int warp_top = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    sm.sums[warp] = warp_total;
+    sm.tops[warp] = warp_top;
   }
   __syncthreads();
+  int pre = 0;
   total = longest = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    total += sm.sums[w];
+    const int x = sm.sums[w];
+    if (w < warp) pre += x;
+    total += x;
     longest = max(longest, sm.tops[w]);
   }
   int share = a.share;
@@ -164,42 +179,42 @@ __device__ __forceinline__ void line_schedule(const LineArgs& a, int step_tokens
     sm.share = share;
     sm.snap = snap;
   }
+  // this thread's sequence b lies at [at, at + c) of the line
+  auto place = [&](int b, int64_t at) {
+    if (c <= 0) return;
+    const unsigned len = (unsigned)(tiles + gap);
+    if (lo >= at && lo < at + c) {
+      const unsigned off = (unsigned)(lo - at), u = off / len;
+      sm.span.b0 = b;
+      sm.span.u0 = (int)u;
+      sm.span.x0 = tree_cut(off - u * len, tiles, snap);
+    }
+    if (hi >= at && hi < at + c) {
+      const unsigned off = (unsigned)(hi - at), u = off / len;
+      sm.span.b1 = b;
+      sm.span.u1 = (int)u;
+      sm.span.x1 = tree_cut(off - u * len, tiles, snap);
+      sm.cut_start = (int)(hi - (off - u * len));
+    }
+  };
+  if (one_chunk) {
+    place(threadIdx.x, (int64_t)pre + v - c);
+    return;
+  }
   int carry = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const int c = look(b);
-    int v = c;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, off);
-      if (lane >= off) v += u;
-    }
+    c = look(b0 + threadIdx.x);
+    v = scan(c);
     __syncthreads();  // the sums before have been read
     if (lane == 31) sm.sums[warp] = v;
     __syncthreads();
-    int pre = carry;
+    pre = carry;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) pre += sm.sums[w];
       carry += sm.sums[w];
     }
-    if (c > 0) {
-      const int64_t at = (int64_t)pre + v - c;  // this thread's sequence lies at [at, at + c)
-      const unsigned len = (unsigned)(tiles + gap);
-      if (lo >= at && lo < at + c) {
-        const unsigned off = (unsigned)(lo - at), u = off / len;
-        sm.span.b0 = b;
-        sm.span.u0 = (int)u;
-        sm.span.x0 = tree_cut(off - u * len, tiles, snap);
-      }
-      if (hi >= at && hi < at + c) {
-        const unsigned off = (unsigned)(hi - at), u = off / len;
-        sm.span.b1 = b;
-        sm.span.u1 = (int)u;
-        sm.span.x1 = tree_cut(off - u * len, tiles, snap);
-        sm.cut_start = (int)(hi - (off - u * len));
-      }
-    }
+    place(b0 + threadIdx.x, (int64_t)pre + v - c);
   }
 }
 
@@ -1154,6 +1169,12 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
   bool have[2];
   unsigned oks = 0;  // two bits a step in flight: whether this lane's two tokens exist
   const uint64_t policy = Rows::kTma ? l2_policy_evict_first() : 0;  // (keys and values are read once)
+  auto prefetch_queries = [&]() {  // of the unit that the loads have come to
+    const int64_t head0 = (int64_t)lu.b * a.n_q_heads + (int64_t)(lu.hg * a.heads + head) * a.group;
+    const int bytes = a.group * D * (int)sizeof(T);
+    for (int i = lane * 128; i < bytes; i += 32 * 128)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(a.q) + head0 * D * (int)sizeof(T) + i));
+  };
   auto look = [&]() {  // table entries of the next step
 #pragma unroll
     for (int h = 0; h < (Rows::kTma ? 1 : 2); ++h) {
@@ -1186,6 +1207,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
         more = ahead.next(lu);
         lx = more ? lu.x0 : 0;
         table = a.block_table + lu.b * a.bt_stride;
+        if (more) prefetch_queries();
       }
       look();
       return;
@@ -1208,6 +1230,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
         more = ahead.next(lu);
         lx = more ? lu.x0 : 0;
         table = a.block_table + lu.b * a.bt_stride;
+        if (more) prefetch_queries();
       }
       look();
     } else {
@@ -1414,13 +1437,23 @@ __global__ void __launch_bounds__(32 * (kWide ? kLjWideWarps : kLjWarps)) line_j
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   __shared__ float s_acc[kWarps][D], s_l[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.y;
+  const int unit_rows = a.heads << a.group_shift;
+  int c = blockIdx.y;
   pdl_launch_dependents();
   pdl_wait_primary();
+  if constexpr (kWide) {  // blockIdx.y: a unit; its record, if it was cut
+    __shared__ int s_cta;
+    if (threadIdx.x == 0) s_cta = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.ctas; i += 32 * kWarps)
+      if (a.ws_rec[i].rows > 0 && a.ws_rec[i].row0 == (int64_t)c * unit_rows) s_cta = i;
+    __syncthreads();
+    c = s_cta;
+    if (c < 0) return;
+  }
   const TreeRec rec = a.ws_rec[c];
   const int r = kWide ? blockIdx.x : blockIdx.x * kLjWarps + warp;
   if (r >= rec.rows) return;
-  const int unit_rows = a.heads << a.group_shift;
   const int pieces = rec.last - c + 1, first = kWide ? warp : 0;
   auto piece = [&](int i) -> int64_t { return ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * unit_rows + r; };
   float M = -INFINITY;
@@ -1540,7 +1573,7 @@ template <typename T, int D, bool kWide>
 cudaError_t launch_join_as(const LineArgs& a, cudaStream_t s) {
   const int rows = a.heads * a.group, warps = kWide ? kLjWideWarps : kLjWarps;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = overlapped(dim3((unsigned)(kWide ? rows : (rows + warps - 1) / warps), (unsigned)a.ctas),
+  const cudaLaunchConfig_t cfg = overlapped(dim3((unsigned)(kWide ? rows : (rows + warps - 1) / warps), (unsigned)(kWide ? a.batch * a.units : a.ctas)),
                                             32 * warps, 0, s, attr);
   return cudaLaunchKernelEx(&cfg, line_join_kernel<T, D, kWide>, a);
 }
