@@ -423,7 +423,8 @@ PA_API size_t paged_attention_window_workspace_size(int batch, int64_t block_tab
 /*
  * The 4-bit cache.  Keys and values of [num_blocks][block_size][n_kv_heads] rows as
  *   k_codes, v_codes    uint8 [..][head_dim / 2]: two codes of 0 .. 15 in a byte, the even dimension in its low half
- *   k_params, v_params  bf16 [..][head_dim / 32]: (scale, zero) of each group of 64 dimensions, zero a whole number
+ *   k_params, v_params  bf16 [..][head_dim / 32]: (scale, zero) of each group of 64 dimensions; scale 0, at least 2^-126 or
+ *                       NaN, zero a whole number of 0 .. 15 (what other programs pack has to keep to that)
  * value = scale * (code - zero).  Four contiguous arrays, 16-byte aligned; 72 bytes instead of 256 a row of 128 bf16
  * values.  Slots and tables are those of the pools.  copy_blocks and swap_blocks move blocks of it (codes and params
  * are two pairs of pools of their own block bytes).

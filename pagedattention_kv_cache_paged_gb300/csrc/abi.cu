@@ -187,10 +187,10 @@ int validate_slots(const int64_t* slot_mapping, int64_t n_tokens, int64_t total_
   std::vector<int64_t> slots;
   int rc = copy_to_host(slots, slot_mapping, n_tokens, s);
   if (rc) return rc;
-  std::unordered_set<int64_t> seen;
-  for (int64_t v : slots) {
-    if (v < 0) continue;
-    if (v >= total_slots || !seen.insert(v).second) return PA_ERANGE;
+  std::sort(slots.begin(), slots.end());  // (in place: nothing is allocated that could throw)
+  for (size_t i = 0; i < slots.size(); ++i) {
+    if (slots[i] < 0) continue;
+    if (slots[i] >= total_slots || (i > 0 && slots[i] == slots[i - 1])) return PA_ERANGE;
   }
   return PA_OK;
 }
@@ -1116,12 +1116,13 @@ int unpack_q4_impl(const void* k_codes, const void* v_codes, const void* k_param
   if (checked()) {
     std::vector<int64_t> pairs;
     if ((rc = copy_to_host(pairs, block_pairs, 2 * n_pairs, s))) return rc;
-    std::unordered_set<int64_t> dsts;
     for (int64_t i = 0; i < n_pairs; ++i) {
       const int64_t src = pairs[(size_t)(2 * i)], dst = pairs[(size_t)(2 * i + 1)];
       if (src < 0 || src >= cache_blocks || dst < 0 || dst >= num_blocks) return PA_ERANGE;
-      if (!dsts.insert(dst).second) return PA_ERANGE;
+      pairs[(size_t)i] = dst;  // (in front of every pair that is still to be read)
     }
+    std::sort(pairs.begin(), pairs.begin() + n_pairs);
+    if (std::adjacent_find(pairs.begin(), pairs.begin() + n_pairs) != pairs.begin() + n_pairs) return PA_ERANGE;
   }
   const Q4UnpackArgs a{k_codes, v_codes,     k_params, v_params, cache_blocks, k_pool, v_pool, num_blocks,
                        block_pairs, n_pairs, (int)(block_elems / 16), stride_bytes / dtype_bytes(dtype), err};
