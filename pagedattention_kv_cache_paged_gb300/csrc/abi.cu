@@ -1088,7 +1088,7 @@ int write_q4_impl(const void* k_new, const void* v_new, const int64_t* slot_mapp
   const int64_t total_slots = num_blocks * block_size;
   if (checked() && (rc = validate_slots(slot_mapping, n_tokens, total_slots, s))) return rc;
   const Q4WriteArgs a{k_new,    v_new,    slot_mapping, n_tokens,    k_codes,
-                      v_codes,  k_params, v_params,     total_slots, n_kv_heads * head_dim / 16,
+                      v_codes,  k_params, v_params,     total_slots, n_kv_heads * head_dim / 32,
                       err};
   int launches = 0;
   cudaError_t e = launch_kv_write_q4(a, dtype, s, &launches);

@@ -22,29 +22,32 @@
 namespace pa {
 
 constexpr int kQ4Threads = 256;
-constexpr int kQ4Vals = 16;                         // values of a thread
-constexpr int kQ4Lanes = kQ4Group / kQ4Vals;        // threads of a group
+constexpr int kPackVals = 32;                       // values of a thread that packs
+constexpr int kPackLanes = kQ4Group / kPackVals;    // threads of a group
+constexpr int kQ4Vals = 16;                         // the same for unpacking
+constexpr int kQ4Lanes = kQ4Group / kQ4Vals;
 
-// Sixteen consecutive values as 32-bit numbers, and the smallest and the largest of them and 0 (NaN if one is).
+// A thread's consecutive values as 32-bit numbers, and the smallest and the largest of them and 0 (NaN if one is).
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16], float& lo, float& hi) {
-  constexpr int kVec = Elt<T>::kVec;
-  uint4 v[16 / kVec];
+__device__ __forceinline__ void load_values(const T* p, bool aligned32, float (&x)[kPackVals], float& lo, float& hi) {
+  constexpr int kVec = Elt<T>::kVec, kWords = kPackVals * (int)sizeof(T) / 4;
+  uint32_t v[kWords];
 #pragma unroll
-  for (int i = 0; i < 16 / kVec; ++i) v[i] = ld_stream16(p + i * kVec);
+  for (int i = 0; i < kWords; i += 8)
+    ld_stream32(reinterpret_cast<const uint32_t*>(p) + i, *reinterpret_cast<uint32_t(*)[8]>(&v[i]), aligned32);
 #pragma unroll
-  for (int i = 0; i < 16 / kVec; ++i) Elt<T>::unpack(v[i], *reinterpret_cast<float(*)[kVec]>(&x[i * kVec]));
+  for (int i = 0; i < kPackVals / kVec; ++i)
+    Elt<T>::unpack(make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]), *reinterpret_cast<float(*)[kVec]>(&x[i * kVec]));
   if constexpr (sizeof(T) == 2) {  // two at a time
     uint32_t a = 0u, b = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(v)[i];
+    for (int i = 0; i < kWords; ++i) {
       if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w));
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(w));
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v[i]));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v[i]));
       } else {
-        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(w));
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(b) : "r"(w));
+        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(v[i]));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(b) : "r"(v[i]));
       }
     }
     float f[8];
@@ -54,7 +57,7 @@ __device__ __forceinline__ void load16(const T* p, float (&x)[16], float& lo, fl
   } else {
     lo = hi = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kPackVals; ++i) {
       lo = min_nan(lo, x[i]);
       hi = max_nan(hi, x[i]);
     }
@@ -71,23 +74,23 @@ __device__ __forceinline__ float q4_round(float x, float s, float inv) {
   return r;
 }
 
-// Packs the sixteen values of a thread; the kQ4Lanes threads of a group (a part of a warp, all of it here) work
+// Packs the values of a thread; the kPackLanes threads of a group (a part of a warp, all of it here) work
 // together; lo, hi: of its own values.  Returns the codes; pair: the group's (scale, zero); kShort: values of at most 11 bits.
 template <bool kShort>
-__device__ __forceinline__ uint2 q4_pack16(float (&x)[16], float lo, float hi, uint32_t& pair) {
+__device__ __forceinline__ uint4 q4_pack(float (&x)[kPackVals], float lo, float hi, uint32_t& pair) {
 #pragma unroll
-  for (int off = 1; off < kQ4Lanes; off <<= 1) {
+  for (int off = 1; off < kPackLanes; off <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
   const float s = __bfloat162float(__float2bfloat16_rn(__fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f))));
   if (!(s <= FLT_MAX)) {  // a value that is not finite
     pair = 0x7fc0u;       // NaN, 0
-    return make_uint2(0u, 0u);
+    return make_uint4(0u, 0u, 0u, 0u);
   }
   if (s < FLT_MIN) {  // nothing but zeros, or next to nothing
     pair = 0u;
-    return make_uint2(0u, 0u);
+    return make_uint4(0u, 0u, 0u, 0u);
   }
   const float inv = 1.f / s;
   const float z = fminf(fmaxf(q4_round(-lo, s, inv), 0.f), 15.f);
@@ -97,17 +100,17 @@ __device__ __forceinline__ uint2 q4_pack16(float (&x)[16], float lo, float hi, u
   // smallest rounds to -zero.
   constexpr float kWhole = 12582912.f;
   const float top = kWhole + 15.f - z;
-  float c[16];
+  float c[kPackVals];
   if constexpr (kShort) {
     // (remainders of numbers of 2^-60 and less would not be exact: both sides times 2^64)
     const bool tiny = s < 8.6736174e-19f;
     const float s1 = tiny ? s * 18446744073709551616.f : s, inv1 = tiny ? inv * 5.4210109e-20f : inv;
     if (tiny) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= 18446744073709551616.f;
+      for (int i = 0; i < kPackVals; ++i) x[i] *= 18446744073709551616.f;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kPackVals; ++i) {
       const float q = x[i] * inv1;
       c[i] = fmaf(fmaf(-q, s1, x[i]), inv1, q) + kWhole;
     }
@@ -115,28 +118,28 @@ __device__ __forceinline__ uint2 q4_pack16(float (&x)[16], float lo, float hi, u
     // all rounded again by q4_round where the remainder of one of them is not below half a scale
     float most = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kPackVals; ++i) {
       c[i] = fmaf(x[i], inv, kWhole);
       most = fmaxf(most, fabsf(fmaf(-(c[i] - kWhole), s, x[i])));
     }
     if (most >= 0.5f * s) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) c[i] = q4_round(x[i], s, inv) + kWhole;
+      for (int i = 0; i < kPackVals; ++i) c[i] = q4_round(x[i], s, inv) + kWhole;
     }
   }
   const uint32_t off = (__float_as_uint(kWhole) - (uint32_t)(int)z) * 0x11111111u;
-  uint32_t w[2];
+  uint32_t w[kPackVals / 8];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < kPackVals / 8; ++k) {
     w[k] = 0u;
 #pragma unroll
     for (int i = 7; i >= 0; --i) w[k] = w[k] * 16u + __float_as_uint(fminf(c[8 * k + i], top));
     w[k] -= off;
   }
-  return make_uint2(w[0], w[1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Thread (token, KV head and group, quarter of it); blockIdx.y: K or V.  32,768 rows of 8 x 128 bf16 values take 30 us
+// Thread (token, KV head and group, half of it); blockIdx.y: K or V.  32,768 rows of 8 x 128 bf16 values take 30 us
 // (5.7 TB/s of what is read and written), near HBM's time and that of the arithmetic, 13 instructions a value.
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteArgs a, const int tokens_cta) {
@@ -160,14 +163,15 @@ __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteAr
     if (c == 0 && blockIdx.y == 0) raise_error(a.err, PA_DEVERR_SLOT);
     here = false;
   }
-  float x[16], lo, hi;
-  load16(static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new) + (t * a.row_lanes + c) * kQ4Vals, x, lo, hi);
+  const T* src = static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new);
+  float x[kPackVals], lo, hi;
+  load_values(src + (t * a.row_lanes + c) * kPackVals, (reinterpret_cast<uintptr_t>(src) & 31u) == 0, x, lo, hi);
   uint32_t pair;
-  const uint2 codes = q4_pack16<sizeof(T) == 2>(x, lo, hi, pair);
+  const uint4 codes = q4_pack<sizeof(T) == 2>(x, lo, hi, pair);
   if (!here || slot < 0) return;
   const int64_t dst = slot * a.row_lanes + c;
-  static_cast<uint2*>(blockIdx.y ? a.v_codes : a.k_codes)[dst] = codes;
-  if (c % kQ4Lanes == 0) static_cast<uint32_t*>(blockIdx.y ? a.v_params : a.k_params)[dst / kQ4Lanes] = pair;
+  static_cast<uint4*>(blockIdx.y ? a.v_codes : a.k_codes)[dst] = codes;
+  if (c % kPackLanes == 0) static_cast<uint32_t*>(blockIdx.y ? a.v_params : a.k_params)[dst / kPackLanes] = pair;
 }
 
 cudaError_t launch_kv_write_q4(const Q4WriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {

@@ -45,6 +45,19 @@ __device__ __forceinline__ int64_t ld_s64(const int64_t* p) {
   return v;
 }
 
+// 32 bytes that nothing writes meanwhile, read once: one load when the address is a multiple of 32, else two of 16 bytes.
+__device__ __forceinline__ void ld_stream32(const void* p, uint32_t (&x)[8], bool aligned32) {
+  if (aligned32) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = ld_stream16(p), b = ld_stream16(static_cast<const uint4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+}
+
 // 32 bytes to global memory: one store when the address is a multiple of 32, else two of 16 bytes.
 __device__ __forceinline__ void st_global32(void* p, const uint32_t (&x)[8], bool aligned32) {
   if (aligned32) {

@@ -240,7 +240,7 @@ struct Q4WriteArgs {
   void* k_params;
   void* v_params;
   int64_t total_slots;             // num_blocks * block_size
-  int row_lanes;                   // n_kv_heads * head_dim / 16 (values of a thread)
+  int row_lanes;                   // n_kv_heads * head_dim / 32 (values of a thread)
   unsigned* err;
 };
 
