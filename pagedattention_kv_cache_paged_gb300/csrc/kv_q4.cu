@@ -24,17 +24,23 @@ namespace pa {
 constexpr int kQ4Threads = 256;
 constexpr int kPackVals = 32;                       // values of a thread that packs
 constexpr int kPackLanes = kQ4Group / kPackVals;    // threads of a group
+constexpr int kPackCtas = 3;                        // CTAs of an SM, which take parts in turn
 constexpr int kQ4Vals = 16;                         // the same for unpacking
 constexpr int kQ4Lanes = kQ4Group / kQ4Vals;
 
-// A thread's consecutive values as 32-bit numbers, and the smallest and the largest of them and 0 (NaN if one is).
-template <typename T>
-__device__ __forceinline__ void load_values(const T* p, bool aligned32, float (&x)[kPackVals], float& lo, float& hi) {
-  constexpr int kVec = Elt<T>::kVec, kWords = kPackVals * (int)sizeof(T) / 4;
-  uint32_t v[kWords];
+// A thread's consecutive values.
+template <typename T, int kWords>
+__device__ __forceinline__ void load_raw(const T* p, bool aligned32, uint32_t (&v)[kWords]) {
 #pragma unroll
   for (int i = 0; i < kWords; i += 8)
     ld_stream32(reinterpret_cast<const uint32_t*>(p) + i, *reinterpret_cast<uint32_t(*)[8]>(&v[i]), aligned32);
+}
+
+// They as 32-bit numbers, and the smallest and the largest of them and 0 (NaN if one is).
+template <typename T>
+__device__ __forceinline__ void unpack_raw(const uint32_t (&v)[kPackVals * sizeof(T) / 4], float (&x)[kPackVals], float& lo,
+                                           float& hi) {
+  constexpr int kVec = Elt<T>::kVec, kWords = kPackVals * (int)sizeof(T) / 4;
 #pragma unroll
   for (int i = 0; i < kPackVals / kVec; ++i)
     Elt<T>::unpack(make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]), *reinterpret_cast<float(*)[kVec]>(&x[i * kVec]));
@@ -142,53 +148,69 @@ __device__ __forceinline__ uint4 q4_pack(float (&x)[kPackVals], float lo, float 
 // Thread (token, KV head and group, half of it); blockIdx.y: K or V.  32,768 rows of 8 x 128 bf16 values take 30 us
 // (5.7 TB/s of what is read and written), near HBM's time and that of the arithmetic, 13 instructions a value.
 template <typename T>
-__global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteArgs a, const int tokens_cta) {
-  // a CTA takes whole tokens, or (wide rows) a part of one; the threads of a group are all here or all past the end, and
-  // what writes nothing computes all the same, so that the lanes of a warp stay together
-  const int lane_token = threadIdx.x / a.row_lanes;
-  int64_t t;
-  int c;
-  if (tokens_cta > 0) {
-    t = (int64_t)blockIdx.x * tokens_cta + lane_token;
-    c = threadIdx.x - lane_token * a.row_lanes;
-  } else {
-    const unsigned parts = (a.row_lanes + kQ4Threads - 1) / kQ4Threads;
-    t = blockIdx.x / parts;
-    c = (blockIdx.x - (unsigned)t * parts) * kQ4Threads + threadIdx.x;
-  }
-  bool here = t < a.n_tokens && c < a.row_lanes && (tokens_cta == 0 || lane_token < tokens_cta);
-  if (!here) t = c = 0;
-  const int64_t slot = __ldg(a.slot_mapping + t);
-  if (slot >= a.total_slots && here) {
-    if (c == 0 && blockIdx.y == 0) raise_error(a.err, PA_DEVERR_SLOT);
-    here = false;
-  }
+__global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteArgs a, const int64_t total) {
   const T* src = static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new);
-  float x[kPackVals], lo, hi;
-  load_values(src + (t * a.row_lanes + c) * kPackVals, (reinterpret_cast<uintptr_t>(src) & 31u) == 0, x, lo, hi);
-  uint32_t pair;
-  const uint4 codes = q4_pack<sizeof(T) == 2>(x, lo, hi, pair);
-  if (!here || slot < 0) return;
-  const int64_t dst = slot * a.row_lanes + c;
-  static_cast<uint4*>(blockIdx.y ? a.v_codes : a.k_codes)[dst] = codes;
-  if (c % kPackLanes == 0) static_cast<uint32_t*>(blockIdx.y ? a.v_params : a.k_params)[dst / kPackLanes] = pair;
+  const bool wide = (reinterpret_cast<uintptr_t>(src) & 31u) == 0;
+  const int64_t stride = (int64_t)gridDim.x * kQ4Threads;
+  // (the threads of a group are all here or all past the end, and what writes nothing computes all the same, so that
+  // the lanes of a warp stay together)
+  int64_t i = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x;
+  uint32_t raw[kPackVals * sizeof(T) / 4];
+  int64_t slot = -1;
+  int c = 0;
+  auto fetch = [&](int64_t at) {  // values and slot of part `at`
+    const bool here = at < total;
+    if (!here) at = 0;
+    int64_t t;
+    if (total <= 0xffffffffLL) {
+      t = (unsigned)at / (unsigned)a.row_lanes;
+    } else {
+      t = at / a.row_lanes;
+    }
+    c = (int)(at - t * a.row_lanes);
+    load_raw(src + at * kPackVals, wide, raw);
+    slot = __ldg(a.slot_mapping + t);
+    if (slot >= a.total_slots && here && c == 0 && blockIdx.y == 0) raise_error(a.err, PA_DEVERR_SLOT);
+    if (!here || slot >= a.total_slots) slot = -1;
+  };
+  const int64_t warp0 = i - (threadIdx.x & 31);
+  if (warp0 >= total) return;
+  fetch(i);
+  for (int64_t w = warp0; w < total; w += stride) {
+    float x[kPackVals], lo, hi;
+    unpack_raw<T>(raw, x, lo, hi);
+    const int64_t dst = slot * a.row_lanes + c;
+    const bool writes = slot >= 0, first = c % kPackLanes == 0;
+    i += stride;
+    if (w + stride < total) fetch(i);
+    uint32_t pair;
+    const uint4 codes = q4_pack<sizeof(T) == 2>(x, lo, hi, pair);
+    if (!writes) continue;
+    static_cast<uint4*>(blockIdx.y ? a.v_codes : a.k_codes)[dst] = codes;
+    if (first) static_cast<uint32_t*>(blockIdx.y ? a.v_params : a.k_params)[dst / kPackLanes] = pair;
+  }
+}
+
+template <typename T>
+static cudaError_t launch_write(const Q4WriteArgs& a, cudaStream_t s) {
+  const int64_t total = a.n_tokens * a.row_lanes, need = (total + kQ4Threads - 1) / kQ4Threads;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)std::min<int64_t>(need, (int64_t)sms * kPackCtas / 2), 2);
+  kv_write_q4_kernel<T><<<grid, kQ4Threads, 0, s>>>(a, total);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv_write_q4(const Q4WriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches) {
   if (a.n_tokens == 0) return cudaSuccess;
-  const int tokens = kQ4Threads / a.row_lanes;
-  const int64_t blocks = tokens > 0 ? (a.n_tokens + tokens - 1) / tokens
-                                    : a.n_tokens * ((a.row_lanes + kQ4Threads - 1) / kQ4Threads);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks, 2);
-  switch (dt) {
-    case PA_BF16: kv_write_q4_kernel<__nv_bfloat16><<<grid, kQ4Threads, 0, s>>>(a, tokens); break;
-    case PA_FP16: kv_write_q4_kernel<__half><<<grid, kQ4Threads, 0, s>>>(a, tokens); break;
-    case PA_FP32: kv_write_q4_kernel<float><<<grid, kQ4Threads, 0, s>>>(a, tokens); break;
-    default: return cudaErrorInvalidValue;
-  }
+  cudaError_t e = cudaErrorInvalidValue;
+  if (dt == PA_BF16) e = launch_write<__nv_bfloat16>(a, s);
+  if (dt == PA_FP16) e = launch_write<__half>(a, s);
+  if (dt == PA_FP32) e = launch_write<float>(a, s);
   ++*launches;
-  return cudaGetLastError();
+  return e;
 }
 
 // ------------------------------------------------------------------------------------------------
