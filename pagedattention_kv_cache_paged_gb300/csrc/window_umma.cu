@@ -8,7 +8,7 @@
 //   for rows of another sequence and short chunks spread over the SMs.  The K producer alone finds them, walking the batch
 //   once (the next item while the current one's tiles are on their way), and hands a record to every other role.
 //   (Blocks of the packed rows, as the prefill kernel takes them: 24 chunks of 1 to 300 tokens, 12 heads, head_dim 64,
-//   window 500: 130 us.)
+//   window 500: 130 us.)  An item of one Q tile leaves the second softmax group out.
 // * Keys: a query at position p attends to j > p - window and j < sinks.  An item's keys are the 16-key sub-tiles that hold
 //   sinks and those from its first row's window on, packed into tiles without a gap (a sub-tile is a box of its own
 //   anyway); nothing else is loaded or looked up.  Tiles that every row sees whole take no mask, the others one bit a key.
@@ -44,6 +44,8 @@ struct WinItem {
   int b, T0, T1, first, n;
   bool ok;
   __device__ __forceinline__ int kv_end() const { return ok ? first + (T1 - T0) : 0; }
+  // Whether the second Q tile has rows (tile_tokens: of a Q tile).
+  __device__ __forceinline__ bool both(int tile_tokens) const { return T1 - T0 > tile_tokens; }
 };
 
 // Items of a call at most: every sequence may end inside a block.  (An unordered query_start_loc could claim rows again and
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kUmThreads)
   uint64_t* kempty = bars + 4;    // [kUmKStages] completes when both groups' S products have read the tile
   uint64_t* vfull = bars + 8;     // [kUmVStages]
   uint64_t* vempty = bars + 12;   // [kUmVStages] completes when both groups' P V products have read the tile
-  uint64_t* q_ready = bars + 16;  // one phase per item: both Q tiles landed
+  uint64_t* q_ready = bars + 16;  // one phase per item: its Q tiles landed
   // per group k, one phase per tile
   uint64_t* s_full = bars + 17;   // [2] S_k computed (and, with it, every earlier product of the CTA)
   uint64_t* p_full = bars + 19;   // [2] P_k written to TMEM (and O_k rescaled)
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kUmThreads)
   uint64_t* fin = bars + 23;
   uint64_t* mready = bars + 24;   // [8] per tile slot: the sub-tile mask below is written
   uint64_t* q_empty = bars + 32;  // one phase per item: its S products completed, Q may be reloaded
-  uint64_t* o_free = bars + 33;   // [2] one phase per item: group k has read O_k
+  uint64_t* o_free = bars + 33;   // [2] one phase per item with tiles of group k: it has read O_k
   uint64_t* rec_full = bars + 36;   // [kWinSlots] the record in the slot is written
   uint64_t* rec_empty = bars + 44;  // [kWinSlots] the V producer, the MMA warp and all 8 softmax warps have read it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
@@ -380,9 +382,9 @@ __global__ void __launch_bounds__(kUmThreads)
             alive = false;
             break;
           }
-          mbar_arrive_expect_tx(q_ready, 2 * Cfg::kQBytes);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
+          const int q_tiles = it.both(kUmTileRows / G) ? 2 : 1;
+          mbar_arrive_expect_tx(q_ready, (uint32_t)(q_tiles * Cfg::kQBytes));
+          for (int k = 0; k < q_tiles; ++k)
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
               tma_load_3d(qs + k * Cfg::kQBytes + h * Cfg::kQHalf, &qmap, h * 64, kvh * G, it.T0 + k * (kUmTileRows / G),
@@ -509,8 +511,10 @@ __global__ void __launch_bounds__(kUmThreads)
       umma_commit(&pv_done[k]);
     };
     // lane 0 alone issues (no warp-collective step, as for the producers)
-    int g = 0;  // tiles of earlier items
-    int n = 0;  // items done
+    int g = 0;   // tiles of earlier items
+    int g1 = 0;  // those that group 1 took part in
+    int turns = 0, turns1 = 0;  // earlier items with tiles, and with tiles of group 1
+    int n = 0;   // items done
     bool alive = lane == 0;
     for (; alive; ++n) {
       WinItem it;
@@ -520,29 +524,27 @@ __global__ void __launch_bounds__(kUmThreads)
       }
       mbar_arrive(&rec_empty[n % kWinSlots]);
       const int n_all = WinSubs(a, it).tiles();
+      const bool both = it.both(kUmTileRows / G);
       bool ok = true;
       auto wait = [&](uint64_t* bar, unsigned parity) {
         ok = ok && win_wait(bar, parity, a.err, a.epoch);
         return ok;
       };
-      // the item's first P V into O_k waits until group k has read O_k of the previous item
-      bool o_ready[2] = {n == 0, n == 0};
-      auto own_o = [&](int k) {
-        if (!o_ready[k]) {
-          o_ready[k] = true;
-          return wait(&o_free[k], (unsigned)((n - 1) & 1));
-        }
-        return ok;
+      // the item's first P V into O_k waits until group k has read O_k of its previous item.  (Of those with tiles: the
+      // groups go through items without any on their own, and may be several ahead.)
+      auto own_o = [&](int k, int j) {
+        const int before = k == 0 ? turns : turns1;
+        return j > 0 || before == 0 || wait(&o_free[k], (unsigned)((before - 1) & 1));
       };
-      // O_k += P_k V of item tile j; group 1's product closes the V tile
+      // O_k += P_k V of item tile j; group 1's product, if there is one, closes the V tile
       auto pv_of = [&](int k, int j) {
         const int gj = g + j;
-        if (!own_o(k) || !wait(&p_full[k], (unsigned)(gj & 1)) ||
+        if (!own_o(k, j) || !wait(&p_full[k], (unsigned)((k == 0 ? gj : g1 + j) & 1)) ||
             !wait(&vfull[gj % kUmVStages], (unsigned)((gj / kUmVStages) & 1)))
           return false;
         tc_fence_after();
         issue_pv(k, gj, j == 0);
-        if (k == 1) umma_commit(&vempty[gj % kUmVStages]);
+        if (k == 1 || !both) umma_commit(&vempty[gj % kUmVStages]);
         return true;
       };
       // Fixed issue order per tile: S_0(j), P_1(j-1) V, S_1(j), P_0(j) V (see prefill_umma.cu)
@@ -552,19 +554,24 @@ __global__ void __launch_bounds__(kUmThreads)
         if (!wait(&kfull[gj % kUmKStages], (unsigned)((gj / kUmKStages) & 1))) break;
         tc_fence_after();
         issue_s(0, gj);
-        if (j > 0 && !pv_of(1, j - 1)) break;
-        tc_fence_after();
-        issue_s(1, gj);
+        if (both) {
+          if (j > 0 && !pv_of(1, j - 1)) break;
+          tc_fence_after();
+          issue_s(1, gj);
+        }
         umma_commit(&kempty[gj % kUmKStages]);
         if (j == n_all - 1) umma_commit(q_empty);  // after the item's last S products
         if (!pv_of(0, j)) break;
       }
-      if (ok && n_all > 0) pv_of(1, n_all - 1);
+      if (ok && both && n_all > 0) pv_of(1, n_all - 1);
       if (ok && n_all == 0) umma_commit(q_empty);
-      own_o(0);  // an item without tiles still takes its turn of both O buffers
-      own_o(1);
       alive = ok;
       g += n_all;
+      if (n_all > 0) ++turns;
+      if (both) {
+        g1 += n_all;
+        if (n_all > 0) ++turns1;
+      }
     }
     if (lane == 0) {
       if (!alive) raise_timeout(a.err, a.epoch);
@@ -580,7 +587,8 @@ __global__ void __launch_bounds__(kUmThreads)
     const int row = grp * kUmTileRows + r;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const float sc = a.scale_log2;
-    int i = 0;  // tiles of this CTA so far
+    int i = 0;     // tiles of this CTA so far
+    int mine = 0;  // those of this group
     bool alive = true;
     int rec = 0;
     for (int w = blockIdx.x; alive; w += gridDim.x, ++rec) {
@@ -594,14 +602,14 @@ __global__ void __launch_bounds__(kUmThreads)
       if (!it.ok && threadIdx.x == 0) raise_error(a.err, PA_DEVERR_QUERY_LOC);
       const int tok = it.T0 + row / G;
       const int head = w % a.n_kv_heads * G + row % G;
-      const int i0 = i;
       float m_use = -INFINITY;  // stabilising maximum (a score) the exponentials are taken against
       float l_run = 0.f;
       const int bound = it.ok && tok < it.T1 ? it.first + (tok - it.T0) : -1;  // the row's position
       const int low = bound + 1 - a.window;                                    // first key of its window
       const WinSubs sb(a, it);
-      const int nt = sb.tiles();
-      for (int tile = 0; tile < nt; ++tile, ++i) {
+      const int all = sb.tiles();
+      const int nt = grp == 0 || it.both(kUmTileRows / G) ? all : 0;
+      for (int tile = 0; tile < nt; ++tile, ++i, ++mine) {
         // Key of the tile's first column.  A tile may begin with sub-tiles of sinks: columns below `split` are keys from
         // tile * kUmKeys on, the others continue to kb + column.
         const int split = 16 * max(sb.sinks - tile * kUmSub, 0);
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(kUmThreads)
         }
         const unsigned loaded = kmask[i & 7];
         // S_k of this tile is complete, and with it O_k += P_k V of the previous tile (issued before)
-        if (!__all_sync(0xffffffffu, win_wait(&s_full[grp], (unsigned)(i & 1), a.err, a.epoch))) {
+        if (!__all_sync(0xffffffffu, win_wait(&s_full[grp], (unsigned)(mine & 1), a.err, a.epoch))) {
           alive = false;
           break;
         }
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(kUmThreads)
         const float corr = row_softmax_window<kBf16>(srow, sc, sees, m_use, l_run);
         // O_k is stable here (its last product completed before this S_k was issued); the item's
         // first tile starts O_k afresh, so only later tiles rescale it
-        if (i > i0 && __any_sync(0xffffffffu, corr != 1.f)) {
+        if (tile > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t v[32];
@@ -683,11 +691,12 @@ __global__ void __launch_bounds__(kUmThreads)
         mbar_arrive(&p_full[grp]);
       }
       if (!alive && lane == 0) raise_timeout(a.err, a.epoch);
-      if (alive && i > i0) {
-        alive = __all_sync(0xffffffffu, win_wait(&pv_done[grp], (unsigned)((i - 1) & 1), a.err, a.epoch));
+      if (alive && nt > 0) {
+        alive = __all_sync(0xffffffffu, win_wait(&pv_done[grp], (unsigned)((mine - 1) & 1), a.err, a.epoch));
         tc_fence_after();
       }
-      const bool have = alive && i > i0 && m_use != -INFINITY;
+      i += all - nt;
+      const bool have = alive && nt > 0 && m_use != -INFINITY;
       const float inv = have ? 1.f / l_run : 0.f;
       T* orow = static_cast<T*>(a.out) + ((int64_t)tok * a.n_q_heads + head) * D;
       const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
@@ -709,8 +718,10 @@ __global__ void __launch_bounds__(kUmThreads)
         }
       }
       // O_k has been read: the next item's first P V may overwrite it
-      tc_fence_before();
-      mbar_arrive(&o_free[grp]);
+      if (nt > 0) {
+        tc_fence_before();
+        mbar_arrive(&o_free[grp]);
+      }
     }
     if (!alive && lane == 0) raise_timeout(a.err, a.epoch);
   }

@@ -365,6 +365,35 @@ def test_query_start_locs_out_of_order(cuda_lib, kernel, qsl):
     assert e.value.status == pa.PA_ERANGE
 
 
+@pytest.mark.parametrize("every", [0, 2, 5, 40])
+def test_many_refused_chunks_in_a_row(cuda_lib, every):
+    """More of them than a CTA's pipeline is deep, with chunks that are not refused in between, of one Q tile and of two."""
+    pa, n = cuda_lib, 2400
+    good = [every > 0 and b % every == 0 for b in range(n)]
+    new = [1 + 97 * b % 270 if ok else 1 + b % 3 for b, ok in enumerate(good)]
+    ctx = [m + b % 40 if ok else 0 for b, (m, ok) in enumerate(zip(new, good))]
+    case = WindowCase(17, ctx, [m if ok else 0 for m, ok in zip(new, good)], 50, 2, q_heads=2, kv_heads=2, head_dim=64,
+                      block_size=16, dtype=BF16)
+    d = case.device()
+    qsl = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn((int(qsl[-1]), 2, 64), generator=torch.Generator().manual_seed(1)).to(BF16)
+    mine = torch.cat([torch.arange(qsl[b], qsl[b + 1]) for b in range(n) if good[b]] + [torch.arange(0)])
+    q[mine] = case.q
+    d["q"], d["query_start_loc"] = q.cuda(), int32(qsl).cuda()
+    got = pa.paged_attention_window(**d, window=50, sinks=2, scale=case.scale)
+    torch.cuda.synchronize()
+    assert pa.device_error_flags() == pa.PA_DEVERR_QUERY_LOC  # (nothing timed out)
+    other = torch.ones(q.shape[0], dtype=torch.bool)
+    other[mine] = False
+    got = got.cpu()
+    assert (got[other] == 0).all()
+    if every >= 5:
+        rows, ref, spread, size = case.oracle()
+        assert (np.abs(got[mine].double().numpy()[rows] - ref) <= pool_bound(case, ref, spread, size)).all()
+    elif every:
+        assert torch.isfinite(got).all() and (got[mine] != 0).any()
+
+
 @pytest.mark.parametrize("kernel", [0, 1])
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 def test_chunks_whose_every_value_is_nan(cuda_lib, kernel, dtype):
