@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kUmThreads)
   uint64_t* fin = bars + 23;
   uint64_t* mready = bars + 24;   // [8] per tile slot: the sub-tile mask below is written
   uint64_t* q_empty = bars + 32;  // one phase per work item: its S products completed, Q may be reloaded
-  uint64_t* o_free = bars + 33;   // [2] one phase per work item: group k has read O_k
+  uint64_t* o_free = bars + 33;   // [2] one phase per work item with tiles: group k has read O_k
   uint64_t* seg_full = bars + 36;    // [kUmSegSlots] the record in the slot is written
   uint64_t* seg_empty = bars + 44;   // [kUmSegSlots] the V producer and all 8 softmax warps have read it
   uint64_t* item_full = bars + 52;   // [kUmItemSlots] the item's tile count is written
@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kUmThreads)
     // lane 0 alone issues (no warp-collective step, as for the producers)
     int g = 0;  // tiles of earlier items
     int n = 0;  // items done
+    int turns = 0;  // of which with tiles
     bool alive = lane == 0;
     for (int w = blockIdx.x; w < n_items && alive; w += gridDim.x, ++n) {
       // the item's tile count, from the K producer
@@ -525,19 +526,15 @@ __global__ void __launch_bounds__(kUmThreads)
           ok = ok && mbar_wait(bar, parity, a.err, a.epoch);
           return ok;
         };
-        // the item's first P V into O_k waits until group k has read O_k of the previous item
-        bool o_ready[2] = {n == 0, n == 0};
-        auto own_o = [&](int k) {
-          if (!o_ready[k]) {
-            o_ready[k] = true;
-            return wait(&o_free[k], (unsigned)((n - 1) & 1));
-          }
-          return ok;
+        // the item's first P V into O_k waits until group k has read O_k of the last item with tiles (the groups go
+        // through items without any on their own, and may be several ahead)
+        auto own_o = [&](int k, int j) {
+          return j > 0 || turns == 0 || wait(&o_free[k], (unsigned)((turns - 1) & 1));
         };
         // O_k += P_k V of item tile j; group 1's product closes the V tile
         auto pv_of = [&](int k, int j) {
           const int gj = g + j;
-          if (!own_o(k) || !wait(&p_full[k], (unsigned)(gj & 1)) ||
+          if (!own_o(k, j) || !wait(&p_full[k], (unsigned)(gj & 1)) ||
               !wait(&vfull[gj % kUmVStages], (unsigned)((gj / kUmVStages) & 1)))
             return false;
           tc_fence_after();
@@ -563,11 +560,10 @@ __global__ void __launch_bounds__(kUmThreads)
         }
         if (ok && n_all > 0) pv_of(1, n_all - 1);
         if (ok && n_all == 0) umma_commit(q_empty);
-        own_o(0);  // an item without tiles still takes its turn of both O buffers
-        own_o(1);
       }
       alive = ok;
       g += n_all;
+      if (n_all > 0) ++turns;
     }
     if (lane == 0) {
       if (!alive) raise_timeout(a.err, a.epoch);
@@ -713,8 +709,10 @@ __global__ void __launch_bounds__(kUmThreads)
         }
       }
       // O_k has been read: the next item's first P V may overwrite it
-      tc_fence_before();
-      mbar_arrive(&o_free[grp]);
+      if (i > i0) {
+        tc_fence_before();
+        mbar_arrive(&o_free[grp]);
+      }
     }
   }
   tc_fence_before();
