@@ -429,8 +429,8 @@ PA_API size_t paged_attention_window_workspace_size(int batch, int64_t block_tab
  * values.  Slots and tables are those of the pools.  copy_blocks and swap_blocks move blocks of it (codes and params
  * are two pairs of pools of their own block bytes).
  * What a group of values x is packed to: lo = min(0, min x), hi = max(0, max x),
- *   scale = bf16(fp32(hi / 15) - fp32(lo / 15)), the difference rounded to fp32 first, or 0 (and all codes 0) if that
- *           is below 2^-126
+ *   scale = bf16(fp32(hi * r) - fp32(lo * r)) with r = fp32(1 / 15), the difference rounded to fp32 first, or 0 (and
+ *           all codes 0) if that is below 2^-126
  *   zero  = round(-lo / scale), code = round(x / scale) + zero, both clamped to 0 .. 15; the quotients, as real numbers,
  *           are rounded to the nearest whole number, halves to the even one
  * so a value that lies between lo and hi comes back within half a scale or so (one next to the ends within 9/16).

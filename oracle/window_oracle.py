@@ -72,7 +72,8 @@ def pack_group(x) -> tuple:
         return [0] * len(x), float("nan"), 0
     lo, hi = min(0.0, *x), max(0.0, *x)
     f32 = np.float32
-    scale = float(torch.tensor(f32(f32(hi) / f32(15)) - f32(f32(lo) / f32(15))).to(torch.bfloat16))
+    r = f32(1) / f32(15)
+    scale = float(torch.tensor(f32(hi) * r - f32(lo) * r).to(torch.bfloat16))
     if scale < 2.0 ** -126:
         return [0] * len(x), 0.0, 0
     s = Fraction(scale)

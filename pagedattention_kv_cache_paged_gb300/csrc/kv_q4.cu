@@ -1,7 +1,7 @@
 // paged_kv_write_q4 and paged_kv_unpack_q4: rows packed into the 4-bit cache, blocks of it back as values
 // (format: q4_common.cuh).
 //
-// Packing.  Of 64 values: lo = min(0, min x), hi = max(0, max x), scale = bf16(fp32(hi / 15) - fp32(lo / 15)),
+// Packing.  Of 64 values: lo = min(0, min x), hi = max(0, max x), scale = bf16(fp32(hi r) - fp32(lo r)), r = fp32(1 / 15),
 // zero = round(-lo / scale), code = round(x / scale) + zero, both clamped to 0 .. 15.  (Zero is on the grid, so
 // x / scale is rounded by itself.)  The quotients are rounded to the nearest whole number, halves to the even one, as real
 // numbers, so that what a value is packed to depends on nothing but the definition:
@@ -89,7 +89,7 @@ __device__ __forceinline__ uint4 q4_pack(float (&x)[kPackVals], float lo, float 
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
-  const float s = __bfloat162float(__float2bfloat16_rn(__fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f))));
+  const float s = __bfloat162float(__float2bfloat16_rn(__fsub_rn(__fmul_rn(hi, 1.f / 15.f), __fmul_rn(lo, 1.f / 15.f))));
   if (!(s <= FLT_MAX)) {  // a value that is not finite
     pair = 0x7fc0u;       // NaN, 0
     return make_uint4(0u, 0u, 0u, 0u);
@@ -145,8 +145,10 @@ __device__ __forceinline__ uint4 q4_pack(float (&x)[kPackVals], float lo, float 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Thread (token, KV head and group, half of it); blockIdx.y: K or V.  32,768 rows of 8 x 128 bf16 values take 30 us
-// (5.7 TB/s of what is read and written), near HBM's time and that of the arithmetic, 13 instructions a value.
+// Thread (token, KV head and group, half of it); blockIdx.y: K or V.  Bound by the instructions to issue (14 a value, 25 us
+// for 67 million values) next to HBM (256 bytes read and 72 written a row of 128 bf16 values, also 25 us), so each thread
+// fetches the values of its next part before it packs this one.  32,768 tokens of 8 x 128 bf16 values take 35 us (4.9
+// TB/s of what is read and written), fp32 61 us (5.0); 16 values a thread took 46 us, 32 without fetching ahead 40.
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteArgs a, const int64_t total) {
   const T* src = static_cast<const T*>(blockIdx.y ? a.v_new : a.k_new);
@@ -282,7 +284,8 @@ __device__ __forceinline__ void unpack16(const uint2& codes, uint32_t pair, T* p
 
 constexpr int kQ4Unroll = 2;  // words of K and of V in flight per thread
 
-// CTA (block pair, slice of it).  Bound by HBM: 72 bytes read and 256 written per row of 128 bf16 values.
+// CTA (block pair, slice of it).  Bound by HBM: 72 bytes read and 256 written per row of 128 bf16 values.  2,048 blocks of 16
+// x 8 x 128 bf16 values take 28 us (6.15 TB/s), fp32 48 us (6.4).
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) kv_unpack_q4_kernel(const Q4UnpackArgs a, const int slices) {
   const int64_t pair = blockIdx.x / slices;

@@ -249,7 +249,7 @@ def test_groups_of_nothing_and_of_what_is_not_finite():
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 def test_values_come_back_near_where_they_were(dtype):
-    """The scale is at most one bf16 half step (2^-9) and two fp32 ones below (hi - lo) / 15.  Inside the codes' range a
+    """The scale is at most one bf16 half step (2^-9) and a few fp32 ones below (hi - lo) / 15.  Inside the codes' range a
     value moves by half a scale for its own code, and its zero's rounding moves only which codes are cut off: a value next
     to an end lies at most 15 2^-9 + 1/2 of a zero's step outside the middle of the last code, 1/2 + 15/512 + 1/512 of a
     scale and its rounding in all, below 9/16."""

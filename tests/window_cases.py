@@ -98,7 +98,8 @@ def pack(rows):
     x = rows.double().unflatten(-1, (-1, 64))
     lo, hi = x.amin(-1).clamp(max=0), x.amax(-1).clamp(min=0)
     f = lambda t: t.float().double()  # noqa: E731
-    s = f(f(hi / 15) - f(lo / 15)).to(torch.bfloat16).double()
+    r = float(np.float32(1) / np.float32(15))  # (a product of two fp32 numbers is exact in 64 bits)
+    s = f(f(hi * r) - f(lo * r)).to(torch.bfloat16).double()
     bad = ~torch.isfinite(x).all(-1)
     none = s < 2.0 ** -126
     step = torch.where(none | bad, 1.0, s)
