@@ -878,20 +878,19 @@ LinePlan plan_line(bool packed, int batch, int n_q_heads, int n_kv_heads, int he
   p.heads = line_heads(packed, n_kv_heads);
   p.units = n_kv_heads / p.heads;
   const int step = 16 * (line_warps(packed) / p.heads);
-  // (and up to 15 tokens next to the window's beginning and the sinks' end, see LineArgs.aligned)
-  const int64_t max_seen = std::min(table_capacity(bt_stride, block_size), (int64_t)window + sinks + 30);
+  // (pools: and up to 15 tokens next to the window's beginning and the sinks' end, see LineArgs.aligned)
+  const int64_t max_seen = std::min(table_capacity(bt_stride, block_size), (int64_t)window + sinks + (packed ? 0 : 30));
   const int64_t tiles = (max_seen + step - 1) / step;
   p.fits = (int64_t)p.units * batch < (int64_t(1) << 30) / (tiles + kLineGap);
   if (!p.fits) return p;
   const int64_t work = (int64_t)p.units * batch * tiles;
   int64_t ctas = std::min(work, (int64_t)(sms > 0 ? sms : 1) * line_ctas(packed, dtype, head_dim, group));
-  p.split = tiles + kLineGap > line_min_share(packed);  // (shorter contexts are never cut, see line_schedule)
+  p.split = tiles > 1;
   if (partition_tokens > 0) {
     int64_t share = (partition_tokens + step - 1) / step;
     if ((work + share - 1) / share > 65535) share = (work + 65534) / 65535;  // (grid of the join)
     p.share = (int)share;
     ctas = (work + share - 1) / share;
-    p.split = tiles > 1;
   }
   p.ctas = (int)ctas;
   if (p.split) {
@@ -969,7 +968,6 @@ int run_line(LineArgs& a, bool packed, int64_t bt_stride, int batch, int64_t num
   a.units = plan.units;
   a.ctas = plan.ctas;
   a.share = plan.share;
-  a.min_share = line_min_share(packed);
   a.split = split;
   if (split) {
     char* base = static_cast<char*>(workspace);

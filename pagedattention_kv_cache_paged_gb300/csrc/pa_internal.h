@@ -289,11 +289,9 @@ struct LineArgs {
   int head_dim;
   int heads;                       // KV heads of a CTA
   int units;                       // n_kv_heads / heads
-  // `ctas` CTAs that take `share` steps each (0: an equal share, at least min_share), units cut where needed if `split`;
-  // partial states and records as in TreeArgs, with heads * group rows a unit
+  // `ctas` CTAs that take `share` steps each (0: an equal share), units cut where needed if `split`; partial states and records as in TreeArgs, with heads * group rows a unit
   int ctas;
   int share;
-  int min_share;
   int split;
   struct TreeRec* ws_rec;
   float* ws_m;
@@ -311,9 +309,10 @@ inline int line_heads(bool packed, int n_kv_heads) {
   while (n_kv_heads % h != 0) h >>= 1;
   return h;
 }
-// What a unit costs besides its steps, and the fewest steps that a CTA takes; shorter units are never cut.
+// What a unit costs besides its steps, in steps.  (Geometric means over 11 shapes of pools and 12 of the 4-bit cache, 1 to
+// 128 requests of 1 to 60,000 tokens: 14.9 and 17.1 us with 2; 14.8 and 17.4 with 1; 16.0 and 18.0 with 3; 17.7 and 21.5 with
+// 6.  A CTA takes one step at least: with two 14.9 and 17.4, with four 15.6 and 18.9, with eight 17.1 and 21.3.)
 constexpr int kLineGap = 2;
-constexpr int line_min_share(bool packed) { return packed ? 4 : 4; }
 
 // Launchers: return cudaSuccess or the launch error.  `launches` is incremented per kernel.
 cudaError_t launch_kv_write(const KvWriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches);

@@ -208,7 +208,7 @@ def test_a_workspace_of_the_size_it_says(cuda_lib, packed):
 def test_sizes_of_short_contexts_are_zero(cuda_lib):
     pa = cuda_lib
     for size in (pa.window_workspace_size, pa.decode_q4_workspace_size):
-        assert size(4, 2, 16, ALL, 0, 8, 8, 128, BF16) == 0  # a table of 32 tokens
+        assert size(4, 1, 16, ALL, 0, 8, 8, 128, BF16) == 0  # a table of 16 tokens
         assert size(4, 4096, 16, 1, 1, 8, 8, 128, BF16) == 0  # a window of as few
         assert size(4, 4096, 16, 5000, 4, 8, 8, 128, BF16) > 0
         assert size(4, 4096, 24, ALL, 0, 8, 8, 128, BF16) == 0 and size(4, 4096, 16, 0, 0, 8, 8, 128, BF16) == 0
