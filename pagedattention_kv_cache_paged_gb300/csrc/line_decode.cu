@@ -493,8 +493,8 @@ struct FullRows {
 // ------------------------------------------------------------------------------------------------
 // fp32 pools: products on CUDA cores, in 32 bits throughout.  A lane has the scores of its two tokens and two heads
 // (16 products for four 16-byte reads), and of its two heads D / 8 dimensions of the output; weights pass through
-// shared memory.  Bound by latency: the rings of four warps fill an SM's shared memory (issue 34 %, shared memory 38 %, DRAM
-// 41 % busy).  64 requests behind a window of 1,024 and 4, 32 / 8 heads, head_dim 128 take 160 us (3.3 TB/s).
+// shared memory.  Bound by latency, one warp a scheduler (issue 34 %, DRAM 41 % busy): a third of its time goes into waits for
+// rows and shared memory, a tenth into issuing the copies; five or eight warps with two stages each take as long.  64 requests behind a window of 1,024 and 4, 32 / 8 heads, head_dim 128 take 160 us (3.3 TB/s).
 // ------------------------------------------------------------------------------------------------
 template <int D, int NT>
 struct FloatRows {
