@@ -494,7 +494,8 @@ struct FullRows {
 // fp32 pools: products on CUDA cores, in 32 bits throughout.  A lane has the scores of its two tokens and two heads
 // (16 products for four 16-byte reads), and of its two heads D / 8 dimensions of the output; weights pass through
 // shared memory.  Bound by latency, one warp a scheduler (issue 34 %, DRAM 41 % busy): a third of its time goes into waits for
-// rows and shared memory, a tenth into issuing the copies; five or eight warps with two stages each take as long.  64 requests behind a window of 1,024 and 4, 32 / 8 heads, head_dim 128 take 160 us (3.3 TB/s).
+// rows and shared memory, a tenth into issuing the copies; five or eight warps with two stages each take as long.  64
+// requests behind a window of 1,024 and 4, 32 / 8 heads, head_dim 128 take 160 us (3.3 TB/s).
 // ------------------------------------------------------------------------------------------------
 template <int D, int NT>
 struct FloatRows {
@@ -1569,8 +1570,8 @@ template <typename T, int D, bool kWide>
 cudaError_t launch_join_as(const LineArgs& a, cudaStream_t s) {
   const int rows = a.heads * a.group, warps = kWide ? kLjWideWarps : kLjWarps;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = overlapped(dim3((unsigned)(kWide ? rows : (rows + warps - 1) / warps), (unsigned)(kWide ? a.batch * a.units : a.ctas)),
-                                            32 * warps, 0, s, attr);
+  const dim3 grid((unsigned)(kWide ? rows : (rows + warps - 1) / warps), (unsigned)(kWide ? a.batch * a.units : a.ctas));
+  const cudaLaunchConfig_t cfg = overlapped(grid, 32 * warps, 0, s, attr);
   return cudaLaunchKernelEx(&cfg, line_join_kernel<T, D, kWide>, a);
 }
 template <typename T>
