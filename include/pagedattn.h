@@ -468,8 +468,9 @@ PA_API int paged_kv_unpack_q4(const void* k_codes, const void* v_codes, const vo
  * paged_attention_decode_q4_workspace_size bytes) as for paged_attention_window without query_start_loc; opts: only
  * partition_tokens applies (rounded up to steps of 16 to 128 tokens).
  * Products of queries and codes are exact (bf16 queries: but for values below 2^-25 of a head's largest).  Each weight
- * times its value's scale is rounded to fp16, by at least 2^-30 of the largest such product, for bf16 and fp16 queries,
- * and split into bf16 parts that hold its 24 bits for fp32.
+ * times its value's scale is rounded to fp16 for bf16 and fp16 queries, by at most 2^-11 of itself or 2^-26 of the largest
+ * such product of the head and the group of dimensions, whichever is more, and split into bf16 parts that hold its 24 bits
+ * for fp32.
  */
 PA_API int paged_attention_decode_q4(void* out, const void* q, const void* k_codes, const void* v_codes,
                                      const void* k_params, const void* v_params, const int32_t* block_table,

@@ -310,12 +310,12 @@ struct LineState {
 };
 
 // Weights of a step: s[nt][0..1] token g, [2..3] token g + 8 (rows), heads 2 tig, 2 tig + 1 (columns); ok0, ok1: whether
-// the two tokens exist.  Scores become weights; where a stabiliser moved, or `more` of a lane asked for it,
-// `rescale(nt, f0, f1)` is called with the factors of the columns' accumulators.
-template <int NT, typename Rescale>
+// the two tokens exist.  Scores become weights; where a stabiliser moved (a weight would pass 2^kGrow), or `more` of a lane
+// asked for it, `rescale(nt, f0, f1, x)` is called with the factors of the columns' accumulators and the logarithms (base 2)
+// of the column's weights.
+template <int NT, int kGrow, typename Rescale>
 __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool ok1, float lift, LineState<NT>& st,
                                              bool more, Rescale rescale) {
-  constexpr float kGrow = 8.f;
   float x[NT][4];
   bool move = more;
 #pragma unroll
@@ -324,7 +324,7 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
     for (int i = 0; i < 4; ++i) {
       if (!(i < 2 ? ok0 : ok1)) s[nt][i] = -INFINITY;
       x[nt][i] = (s[nt][i] - st.m[nt][i & 1]) * st.sc[nt][i & 1];
-      move |= !(x[nt][i] <= kGrow);  // (also at the start, and for NaN)
+      move |= !(x[nt][i] <= (float)kGrow);  // (also at the start, and for NaN)
     }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -344,7 +344,7 @@ __device__ __forceinline__ void line_softmax(float (&s)[NT][4], bool ok0, bool o
         x[nt][e] = (s[nt][e] - base) * st.sc[nt][e];
         x[nt][2 + e] = (s[nt][2 + e] - base) * st.sc[nt][e];
       }
-      rescale(nt, f[0], f[1]);
+      rescale(nt, f[0], f[1], x[nt]);
     }
   }
 #pragma unroll
@@ -465,7 +465,7 @@ struct FullRows {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
-    line_softmax<NT>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1) {
+    line_softmax<NT, 8>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1, const float (&)[4]) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
         o[nt][i][0] *= f0, o[nt][i][2] *= f0;
@@ -570,7 +570,7 @@ struct FloatRows {
           s[nt][2 + e] = dot4(x, k1, s[nt][2 + e]);
         }
     }
-    line_softmax<NT>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1) {
+    line_softmax<NT, 8>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1, const float (&)[4]) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
         o[nt][i][0] *= f0, o[nt][i][2] *= f0;
@@ -666,14 +666,16 @@ struct PackedStage {
 // become fp16 without loss but for those below 2^-29 of the largest; values that meet codes in bits 4-7 are taken 16 times
 // smaller.  With c, z, s a group's codes, zero and scale: score = sum over groups of s * (sum q c - z * sum q).
 //
-// Values.  weight * scale is rounded to fp16 after a power of two that keeps the largest scale of a group so far in
-// 2^5 .. 2^6 (its accumulators are rescaled when it moves, by the same vote as the stabiliser's), so that the smallest step
-// is 2^-30 of the largest product or less.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
+// Values.  weight * scale is rounded to fp16 after a factor of the head's and the group's own, chosen so that the largest
+// product so far lies in 2 .. 4: fp16's smallest step is 2^-25 of it or less, and rounds by half of that.  The factor is
+// chosen again (with the stabiliser's vote; accumulators are rescaled) when a product passes that or a scale 2^11 over the
+// factor (a weight may be 2^kGrow, and their product has to fit), and it follows a stabiliser that moves: a large scale
+// of a small weight costs the others nothing.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
 //
 // Bound by instructions: 425 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
 // clock by the 16 warps that the registers allow (more warps at fewer registers, and the next step's scores next to this
-// one's values, spill and are slower).  32 / 8 heads: 64 requests of 512 to 4,096 tokens (171 MB) take 56 us, 4 of 32,768 to
-// 131,000 (378 MB) 109 us.
+// one's values, spill and are slower).  32 / 8 heads: 64 requests of 512 to 4,096 tokens (171 MB) take 59 us, 4 of 32,768 to
+// 131,000 (378 MB) 112 us.
 template <typename T, int D, int NT>
 struct PackedRows : PackedStage<D> {
   static constexpr bool kTma = false;
@@ -688,11 +690,15 @@ struct PackedRows : PackedStage<D> {
   static constexpr float kLift = 0.f;
   static constexpr bool kQuads = true;
   static constexpr int kAcc = D / 16;
+  static constexpr int kGrow = 4;
+  static constexpr float kMostVk = 8.50705917302346159e37f;     // 2^126
+  static constexpr float kMostScale = 1.06338239662793269e37f;  // 2^123: times a weight of 2^kGrow it is finite
 
   uint32_t q[NT][kGroups][4][2];
   float sum_q[NT][kGroups][2];  // sums of a group's query values, heads 2 tig, 2 tig + 1, times 2^-24
   float unit[NT][2];            // score of a head per unit of the above
-  float vk[kGroups];            // the power of two of the group's scales
+  float vk[NT][kGroups][2];     // the factor of a head's products of weights and scales
+  float most;                   // the largest scale that all of these allow
   float oz[NT][kGroups][4];     // sums of weights times scales times zeros (rows alike) times 2^-24
   uint32_t kb, vb, pb, zb;      // this lane's reads: codes of K and V, pairs, zeros
 
@@ -761,13 +767,15 @@ struct PackedRows : PackedStage<D> {
         ls.sc[nt][i] = fminf(ls.sc[nt][i] * unit[nt][i], FLT_MAX);
       }
     }
+    most = 0.f;
 #pragma unroll
     for (int gr = 0; gr < kGroups; ++gr) {
-      vk[gr] = 8.50705917302346159e37f;  // 2^126
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        vk[nt][gr][0] = vk[nt][gr][1] = kMostVk;
 #pragma unroll
         for (int k = 0; k < 4; ++k) oz[nt][gr][k] = 0.f;
+      }
     }
   }
 
@@ -822,41 +830,35 @@ struct PackedRows : PackedStage<D> {
     }
     // ---- weights ----
     read_pairs(st + pb + 16 * kPair);
-    float sv[2][kGroups];
     bool large = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int gr = 0; gr < kGroups; ++gr) {
-        sv[h][gr] = q4_scale(pair[h][gr]) * vk[gr];
-        large |= sv[h][gr] > 64.f;
-      }
-    float old[kGroups];
-    line_softmax<NT>(s, ok0, ok1, kLift, ls, large, [&](int nt, float f0, float f1) {
-      if (nt == 0) {
+      for (int gr = 0; gr < kGroups; ++gr) large |= q4_scale(pair[h][gr]) > most;
+    line_softmax<NT, kGrow>(s, ok0, ok1, kLift, ls, large, [&](int nt, float f0, float f1, const float (&x)[4]) {
 #pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr) {
-          old[gr] = vk[gr];
-          const float s0 = q4_scale(pair[0][gr]), s1 = q4_scale(pair[1][gr]);
-          float top = fmaxf(s0, s1);
+      for (int gr = 0; gr < kGroups; ++gr) {
+        float g[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // (no weight of this step is above 1, and the products so far shrank by f)
+          const float f = e ? f1 : f0, old = vk[nt][gr][e];
+          float top = fmaxf(fast_exp2(x[e]) * q4_scale(pair[0][gr]), fast_exp2(x[2 + e]) * q4_scale(pair[1][gr]));
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          if (top * vk[gr] > 64.f)
-            vk[gr] = __uint_as_float((uint32_t)(127 + 127 + 5 - (int)(__float_as_uint(top) >> 23)) << 23);
-          sv[0][gr] = s0 * vk[gr];
-          sv[1][gr] = s1 * vk[gr];
+          float now = fminf(old / f, kMostVk);
+          if (top * now >= 4.f) now = __uint_as_float((uint32_t)(255 - (int)(__float_as_uint(top) >> 23)) << 23);
+          vk[nt][gr][e] = now;
+          g[e] = f == 0.f ? 0.f : f * (now / old);
         }
-      }
-#pragma unroll
-      for (int gr = 0; gr < kGroups; ++gr) {
-        const float g0 = f0 * (vk[gr] / old[gr]), g1 = f1 * (vk[gr] / old[gr]);
 #pragma unroll
         for (int i = 4 * gr; i < 4 * gr + 4; ++i) {
-          o[nt][i][0] *= g0, o[nt][i][2] *= g0;
-          o[nt][i][1] *= g1, o[nt][i][3] *= g1;
+          o[nt][i][0] *= g[0], o[nt][i][2] *= g[0];
+          o[nt][i][1] *= g[1], o[nt][i][3] *= g[1];
         }
-        oz[nt][gr][0] *= g0, oz[nt][gr][2] *= g0;
-        oz[nt][gr][1] *= g1, oz[nt][gr][3] *= g1;
+        oz[nt][gr][0] *= g[0], oz[nt][gr][2] *= g[0];
+        oz[nt][gr][1] *= g[1], oz[nt][gr][3] *= g[1];
+        most = fminf(nt == 0 && gr == 0 ? kMostScale : most, 2048.f / fmaxf(vk[nt][gr][0], vk[nt][gr][1]));
       }
     });
     // ---- values ----
@@ -883,7 +885,8 @@ struct PackedRows : PackedStage<D> {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          p[nt][h] = transpose8(pack2<false>(s[nt][2 * h] * sv[h][gr], s[nt][2 * h + 1] * sv[h][gr]));
+          p[nt][h] = transpose8(pack2<false>(s[nt][2 * h] * q4_scale(pair[h][gr]) * vk[nt][gr][0],
+                                             s[nt][2 * h + 1] * q4_scale(pair[h][gr]) * vk[nt][gr][1]));
       uint32_t m[2][2];  // codes, the tokens of a pair in the halves of a word
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -919,7 +922,8 @@ struct PackedRows : PackedStage<D> {
       for (int i = 0; i < kAcc; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[nt][i][k] = fmaf(o[nt][i][k], i & 1 ? 1048576.f : 16777216.f, -16777216.f * oz[nt][i / 4][k]) * (1.f / vk[i / 4]);
+          o[nt][i][k] = fmaf(o[nt][i][k], i & 1 ? 1048576.f : 16777216.f, -16777216.f * oz[nt][i / 4][k]) *
+                        (1.f / vk[nt][i / 4][k & 1]);
     }
   }
   static __device__ __forceinline__ int dim_of(int i, int h, int g) {
@@ -1034,7 +1038,7 @@ struct PackedWideRows : PackedStage<D> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(q4_scale(pair[i >> 1]), dot[nt][i], s[nt][i]);
     }
-    line_softmax<NT>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1) {
+    line_softmax<NT, 8>(s, ok0, ok1, kLift, ls, false, [&](int nt, float f0, float f1, const float (&)[4]) {
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) {
         o[nt][i][0] *= f0, o[nt][i][2] *= f0;
