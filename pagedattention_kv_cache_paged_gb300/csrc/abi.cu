@@ -868,6 +868,7 @@ struct LinePlan {
   bool fits = false;
   int heads = 0, units = 0, ctas = 0, share = 0;
   bool split = false;
+  int64_t longest = 0, longest_cut = 0;  // steps of a unit at most, and of what a CTA has of it if units are cut
   size_t bytes = 0, off_m = 0, off_l = 0, off_rec = 0;
 };
 
@@ -893,6 +894,10 @@ LinePlan plan_line(bool packed, int batch, int n_q_heads, int n_kv_heads, int he
     ctas = (work + share - 1) / share;
   }
   p.ctas = (int)ctas;
+  p.longest = tiles;
+  // (a cut moves by less than kLineGap steps)
+  const int64_t share = p.share > 0 ? p.share : ((int64_t)p.units * batch * (tiles + kLineGap) + ctas - 1) / ctas;
+  p.longest_cut = std::min(tiles, share + kLineGap);
   if (p.split) {
     auto up16 = [](size_t x) { return (x + 15) & ~size_t(15); };
     const size_t rows = (size_t)p.ctas * 2 * (size_t)(p.heads * group);
@@ -969,6 +974,7 @@ int run_line(LineArgs& a, bool packed, int64_t bt_stride, int batch, int64_t num
   a.ctas = plan.ctas;
   a.share = plan.share;
   a.split = split;
+  a.runs = (split ? plan.longest_cut : plan.longest) > kLineRun;
   if (split) {
     char* base = static_cast<char*>(workspace);
     a.ws_acc = reinterpret_cast<float*>(base);

@@ -667,10 +667,10 @@ struct PackedStage {
 // smaller.  With c, z, s a group's codes, zero and scale: score = sum over groups of s * (sum q c - z * sum q).
 //
 // Values.  weight * scale is rounded to fp16 after a factor of the head's and the group's own, chosen so that the largest
-// product so far lies in 2 .. 4: fp16's smallest step is 2^-25 of it or less, and rounds by half of that.  The factor is
-// chosen again (with the stabiliser's vote; accumulators are rescaled) when a product passes that or a scale 2^11 over the
-// factor (a weight may be 2^kGrow, and their product has to fit), and it follows a stabiliser that moves: a large scale
-// of a small weight costs the others nothing.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
+// product so far lies at 2 or more: fp16's smallest step is 2^-25 of it or less, and rounds by half of that.  The factor is
+// looked at again, with the stabiliser's vote, where a scale passes 2^11 over it (a weight may be 2^kGrow, and the product
+// has to fit): it is taken down to products of 2 .. 4 if need be, accumulators with it.  It grows as a stabiliser
+// that moves takes the products down.  So a large scale of a small weight costs the others nothing.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
 //
 // Bound by instructions: 425 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
 // clock by the 16 warps that the registers allow (more warps at fewer registers, and the next step's scores next to this
@@ -1117,7 +1117,12 @@ constexpr int line_smem(int group) {
 constexpr int kLineStatic = 512;  // the schedule, the rings' barriers
 
 
-template <typename Rows, int D, int NT>
+// kRuns: a warp's sums of kLineRun steps at most are formed in registers, and runs added up in shared memory.  The tensor core
+// cuts its sums off where it should round: a step takes up to 2^-23 of what a sum holds from it, always in the same
+// direction (131,072 tokens by one warp lost 8e-4 of the result over the 4-bit cache, whose codes are not centred, and two
+// million 1.3 %); now 3e-5 at most, and sums of rounded additions have fewer summands as well.  Calls in which no CTA can
+// have that many steps of a unit take the form without (4-bit serving batch 59.0 and 60.5 us, window of 8,192 90 and 93).
+template <typename Rows, int D, int NT, bool kRuns>
 __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
     line_decode_kernel(const LineArgs a, const __grid_constant__ LineMaps maps) {
   using T = typename Rows::Out;
@@ -1251,70 +1256,131 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
   bool alive = true;   // kTma: no wait has given up (if one has, the units are walked through without their keys)
   while (walk.next(w)) {
     const int64_t head0 = (int64_t)w.b * a.n_q_heads + (int64_t)(w.hg * a.heads + head) * a.group;
+    const int g = lane >> 2, tig = lane & 3;
     LineState<NT> ls;
     float o[NT][Rows::kAcc][4];
+    // this warp's sums to its rows in shared memory, or added to what is there (every lane has the same elements each time)
+    auto store = [&](bool add) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        ls.sc[nt][e] = a.scale_log2;
-        ls.m[nt][e] = -INFINITY;
-        ls.l[nt][e] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < Rows::kAcc; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-    }
-    rows.query(a, head0, lane, ls);
-    for (int x = w.x0; x < w.x1; ++x) {
-      if constexpr (Rows::kTma) {
-        if (alive && !__all_sync(0xffffffffu, mbar_wait(&landed[warp][stage], phase, a.err, a.epoch))) {
-          alive = false;
-          if (lane == 0) raise_timeout(a.err, a.epoch);
-        }
-        if (!alive) continue;
-        const int key = step_key[warp][stage], t = lane >> 2;
-        if (key >= 0) {
-          auto exists = [&](int p) { return p < w.sq.n && (p >= w.sq.low || p < a.sinks); };
-          bool ok0 = true, ok1 = true;
-          if (key + 16 > w.sq.n || key < w.sq.low) {  // (whole steps below the sinks' end take this way too)
-            ok0 = exists(key + t);
-            ok1 = exists(key + t + 8);
-            Rows::clear_rows(smem + (warp * kStages + stage) * Rows::kStage, lane,
-                             __ballot_sync(0xffffffffu, exists(key + (lane & 15))));
+        for (int e = 0; e < 2; ++e) {
+          const int r = (warp << a.group_shift) + nt * 8 + 2 * tig + e;
+          const bool here = nt * 8 + 2 * tig + e < a.group;
+          float* p = out_o + r * kOutRow;
+          float f_old = 0.f, f_new = 1.f, m = ls.m[nt][e], l = ls.l[nt][e];
+          if (add) {
+            __syncwarp();
+            if (here) {
+              const float before = out_m[r], most = fmaxf(before, m), base = most == -INFINITY ? 0.f : most;
+              f_old = fast_exp2((before - base) * a.scale_log2);
+              f_new = fast_exp2((m - base) * a.scale_log2);
+              l = fmaf(out_l[r], f_old, l * f_new);
+              m = most;
+            }
+            __syncwarp();
           }
-          rows.step(ring + stage * Rows::kStage, lane, ok0, ok1, ls, o);
+          if (here) {
+            if constexpr (Rows::kQuads) {
+#pragma unroll
+              for (int i = 0; i < Rows::kAcc; i += 4)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float4* at = reinterpret_cast<float4*>(p + Rows::dim_of(i, h, g));
+                  float4 v = make_float4(o[nt][i][2 * h + e], o[nt][i + 1][2 * h + e], o[nt][i + 2][2 * h + e],
+                                         o[nt][i + 3][2 * h + e]);
+                  if (add) {
+                    const float4 y = *at;
+                    v = make_float4(fmaf(y.x, f_old, v.x * f_new), fmaf(y.y, f_old, v.y * f_new),
+                                    fmaf(y.z, f_old, v.z * f_new), fmaf(y.w, f_old, v.w * f_new));
+                  }
+                  *at = v;
+                }
+            } else {
+#pragma unroll
+              for (int i = 0; i < Rows::kAcc; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float* at = p + Rows::dim_of(i, h, g);
+                  const float v = o[nt][i][2 * h + e];
+                  *at = add ? fmaf(*at, f_old, v * f_new) : v;
+                }
+            }
+            if (g == 0) {
+              out_m[r] = m;
+              out_l[r] = l;
+            }
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        load(stage);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+    };
+    // whether a warp has all of its head, and four neighbouring dimensions in four accumulators
+    auto direct = [&]() { return Rows::kQuads && lanes_head == 1 && (!kRuns || w.x1 - w.x0 <= kLineRun); };
+    int x = w.x0;
+    do {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ls.sc[nt][e] = a.scale_log2;
+          ls.m[nt][e] = -INFINITY;
+          ls.l[nt][e] = 0.f;
         }
-        continue;
+#pragma unroll
+        for (int i = 0; i < Rows::kAcc; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
       }
-      copy_wait<kStages - 2>();
-      __syncwarp();  // every lane's copies of this step are there, and the stage before has been read by all
-      const unsigned ok = oks >> (2 * (kStages - 2));
-      load(stage == 0 ? kStages - 1 : stage - 1);
-      if constexpr (!Rows::kTma) rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, ls, o);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
-    }
+      rows.query(a, head0, lane, ls);
+      do {
+        if constexpr (Rows::kTma) {
+          if (alive && !__all_sync(0xffffffffu, mbar_wait(&landed[warp][stage], phase, a.err, a.epoch))) {
+            alive = false;
+            if (lane == 0) raise_timeout(a.err, a.epoch);
+          }
+          if (!alive) continue;
+          const int key = step_key[warp][stage], t = lane >> 2;
+          if (key >= 0) {
+            auto exists = [&](int p) { return p < w.sq.n && (p >= w.sq.low || p < a.sinks); };
+            bool ok0 = true, ok1 = true;
+            if (key + 16 > w.sq.n || key < w.sq.low) {  // (whole steps below the sinks' end take this way too)
+              ok0 = exists(key + t);
+              ok1 = exists(key + t + 8);
+              Rows::clear_rows(smem + (warp * kStages + stage) * Rows::kStage, lane,
+                               __ballot_sync(0xffffffffu, exists(key + (lane & 15))));
+            }
+            rows.step(ring + stage * Rows::kStage, lane, ok0, ok1, ls, o);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          load(stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          continue;
+        }
+        copy_wait<kStages - 2>();
+        __syncwarp();  // every lane's copies of this step are there, and the stage before has been read by all
+        const unsigned ok = oks >> (2 * (kStages - 2));
+        load(stage == 0 ? kStages - 1 : stage - 1);
+        if constexpr (!Rows::kTma) rows.step(ring + stage * Rows::kStage, lane, ok & 1, (ok & 2) != 0, ls, o);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+      } while (++x < w.x1 && (!kRuns || (unsigned)(x - w.x0) % kLineRun != 0));
+      // the sums in their own units, and l of all lanes
+      rows.finish(ls, o);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) ls.l[nt][e] += __shfl_xor_sync(0xffffffffu, ls.l[nt][e], off);
+      if (!direct()) store(kRuns && x - w.x0 > kLineRun);
+    } while (kRuns && x < w.x1);
     // ---- the unit's end ----
-    rows.finish(ls, o);
-    const int g = lane >> 2, tig = lane & 3;
     const bool whole = w.x0 == 0 && w.x1 == w.T;
     const int unit_rows = a.heads << a.group_shift;
     const int64_t row0 = (int64_t)w.b * a.n_q_heads + (int64_t)w.hg * unit_rows;
     const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (w.x0 == 0 ? 1 : 0)) * unit_rows;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) ls.l[nt][e] += __shfl_xor_sync(0xffffffffu, ls.l[nt][e], off);
     // four neighbouring dimensions of a row: its output, or this CTA's part of it
     auto put = [&](int r, int d, const float4& v, float M, float L) {
       if (whole) {
@@ -1333,8 +1399,7 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
         }
       }
     };
-    if (Rows::kQuads && lanes_head == 1) {
-      // a warp has all of its head, and four neighbouring dimensions in four accumulators
+    if (direct()) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1353,33 +1418,6 @@ __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
         }
     } else {
       // the warps of a head joined in shared memory
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = nt * 8 + 2 * tig + e;
-          if (r < a.group) {
-            float* p = out_o + ((warp << a.group_shift) + r) * kOutRow;
-            if constexpr (Rows::kQuads) {
-#pragma unroll
-              for (int i = 0; i < Rows::kAcc; i += 4)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  *reinterpret_cast<float4*>(p + Rows::dim_of(i, h, g)) =
-                      make_float4(o[nt][i][2 * h + e], o[nt][i + 1][2 * h + e], o[nt][i + 2][2 * h + e],
-                                  o[nt][i + 3][2 * h + e]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < Rows::kAcc; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) p[Rows::dim_of(i, h, g)] = o[nt][i][2 * h + e];
-            }
-            if (g == 0) {
-              out_m[(warp << a.group_shift) + r] = ls.m[nt][e];
-              out_l[(warp << a.group_shift) + r] = ls.l[nt][e];
-            }
-          }
-        }
       __syncthreads();
       for (int i = threadIdx.x; i < unit_rows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -1511,8 +1549,8 @@ cudaLaunchConfig_t overlapped(dim3 grid, int threads, int smem, cudaStream_t s, 
   return cfg;
 }
 
-template <typename Rows, int D, int NT>
-cudaError_t launch_rows(const LineArgs& a, cudaStream_t s, const LineMaps& maps = LineMaps{}) {
+template <typename Rows, int D, int NT, bool kRuns>
+cudaError_t launch_form(const LineArgs& a, cudaStream_t s, const LineMaps& maps) {
   constexpr int most = line_smem<Rows, D>(8 * NT);
   static_assert(most + (Rows::kTma ? kLineStatic : 256) <= 227 * 1024, "shared memory of a CTA");
   static bool attr_set[64] = {};  // per instantiation and device; idempotent, so a race is harmless
@@ -1520,14 +1558,18 @@ cudaError_t launch_rows(const LineArgs& a, cudaStream_t s, const LineMaps& maps 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(line_decode_kernel<Rows, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    e = cudaFuncSetAttribute(line_decode_kernel<Rows, D, NT, kRuns>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       overlapped(dim3((unsigned)a.ctas), LineCfg<Rows>::kThreads, line_smem<Rows, D>(a.group), s, attr);
-  return cudaLaunchKernelEx(&cfg, line_decode_kernel<Rows, D, NT>, a, maps);
+  return cudaLaunchKernelEx(&cfg, line_decode_kernel<Rows, D, NT, kRuns>, a, maps);
+}
+template <typename Rows, int D, int NT>
+cudaError_t launch_rows(const LineArgs& a, cudaStream_t s, const LineMaps& maps = LineMaps{}) {
+  return a.runs ? launch_form<Rows, D, NT, true>(a, s, maps) : launch_form<Rows, D, NT, false>(a, s, maps);
 }
 
 template <typename T, int D>

@@ -293,6 +293,7 @@ struct LineArgs {
   int ctas;
   int share;
   int split;
+  int runs;                        // whether a CTA may have more than kLineRun steps of a unit
   struct TreeRec* ws_rec;
   float* ws_m;
   float* ws_l;
@@ -313,6 +314,8 @@ inline int line_heads(bool packed, int n_kv_heads) {
 // 128 requests of 1 to 60,000 tokens: 14.9 and 17.1 us with 2; 14.8 and 17.4 with 1; 16.0 and 18.0 with 3; 17.7 and 21.5 with
 // 6.  A CTA takes one step at least: with two 14.9 and 17.4, with four 15.6 and 18.9, with eight 17.1 and 21.3.)
 constexpr int kLineGap = 2;
+// Steps whose sums a warp of the line decode holds in registers.
+constexpr int kLineRun = 256;
 
 // Launchers: return cudaSuccess or the launch error.  `launches` is incremented per kernel.
 cudaError_t launch_kv_write(const KvWriteArgs& a, pa_dtype dt, cudaStream_t s, int* launches);
