@@ -28,6 +28,7 @@
 #include <cudaTypedefs.h>
 
 #include "prefill_common.cuh"
+#include "window_mask.h"
 
 namespace pa {
 
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kUmThreads)
       float m_use = -INFINITY;  // stabilising maximum (a score) the exponentials are taken against
       float l_run = 0.f;
       const int bound = it.ok && tok < it.T1 ? it.first + (tok - it.T0) : -1;  // the row's position
-      const int low = bound + 1 - a.window;                                    // first key of its window
+      const int low = window_low(bound, a.window);                             // first key of its window
       const WinSubs sb(a, it);
       const int all = sb.tiles();
       const int nt = grp == 0 || it.both(kUmTileRows / G) ? all : 0;
@@ -638,13 +639,7 @@ __global__ void __launch_bounds__(kUmThreads)
         bool sees = true;
         if (!whole) {
           uint32_t mask[kUmKeys / 32];
-          // keys from k0 on that the row sees, 32 columns: up to its own, from the window's first on or below the sinks'
-          // end
-          auto seen = [&](int k0) -> uint32_t {
-            const int nv = bound - k0 + 1, from = max(low - k0, 0), to = max(a.sinks - k0, 0);
-            const uint32_t m = nv >= 32 ? 0xFFFFFFFFu : (nv <= 0 ? 0u : ((1u << nv) - 1u));
-            return m & ((from < 32 ? 0xFFFFFFFFu << from : 0u) | (to < 32 ? (1u << to) - 1u : 0xFFFFFFFFu));
-          };
+          auto seen = [&](int k0) { return window_seen32(bound, low, a.sinks, k0); };  // keys from k0 on, 32 columns
 #pragma unroll
           for (int q = 0; q < kUmKeys / 32; ++q) {
             const uint32_t lm = (((loaded >> (2 * q)) & 1u) ? 0x0000FFFFu : 0u) |
