@@ -434,6 +434,10 @@ PA_API size_t paged_attention_window_workspace_size(int batch, int64_t block_tab
  *   zero  = round(-lo / scale), code = round(x / scale) + zero, both clamped to 0 .. 15; the quotients, as real numbers,
  *           are rounded to the nearest whole number, halves to the even one
  * so a value that lies between lo and hi comes back within half a scale or so (one next to the ends within 9/16).
+ * The scale is made of products with r, not of quotients by 15, because that is what PyTorch computes on a GPU for x / 15:
+ * rows packed by ordinary tensor operations there are the same, bit for bit.  Quotients (the same operations on a CPU) give
+ * another scale, by one step of bf16, for about one group in a thousand of fp16 values and seven in a million of fp32
+ * values, and the same one for bf16 values: who packs on a CPU multiplies by r.
  * A group that holds an infinity or NaN gets scale NaN: all its values are NaN.
  */
 
