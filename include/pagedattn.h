@@ -394,6 +394,10 @@ PA_API int paged_kv_accept(void* k_pool, void* v_pool, int num_layers, int64_t l
  *   scale           > 0, and finite times log2(e) as well (at most 2.35e38)
  * An empty context gives zeros.  What a row does not see does not enter it, whatever it holds (infinities and NaN
  * included); a non-finite value that it sees gives non-finite outputs, a non-finite key those of its score.
+ * Scores, maxima and sums are of 32 bits.  For the product with V a weight is rounded to the pool's type: bf16 by at most 2^-8
+ * of itself, fp16 by 2^-11 or 2^-32 of the head's largest, fp32 not at all; with prefill_kernel 1 in no type.  The tcgen05
+ * kernel's sums over the keys are cut off where others round: they lose about 1e-7 of themselves every 16 keys (8e-4 of
+ * the result over 131,072 visible keys, 6.6e-3 over a million); those of single tokens do not.
  *   workspace       without query_start_loc: optional scratch for splitting contexts, at least
  *                   paged_attention_window_workspace_size(...) bytes for the same sizes and opts, 16-byte aligned, no
  *                   initialisation needed.  NULL: no splitting (slower for few sequences).  Calls that may overlap
@@ -471,7 +475,8 @@ PA_API int paged_kv_unpack_q4(const void* k_codes, const void* v_codes, const vo
  * window, sinks, context_lens, scale, empty contexts, refused sequences and blocks, and the workspace (of
  * paged_attention_decode_q4_workspace_size bytes) as for paged_attention_window without query_start_loc; opts: only
  * partition_tokens applies (rounded up to steps of 16 to 128 tokens).
- * Products of queries and codes are exact (bf16 queries: but for values below 2^-25 of a head's largest).  Each weight
+ * Query values of fp16 and bf16 are rounded by at most 2^-35 of a head's largest, and only those below 2^-24 (fp16) or 2^-27
+ * (bf16) of it; apart from that, products of queries and codes are exact.  Each weight
  * times its value's scale is rounded to fp16 for bf16 and fp16 queries, by at most 2^-11 of itself or 2^-26 of the largest
  * such product of the head and the group of dimensions, whichever is more, and split into bf16 parts that hold its 24 bits
  * for fp32.

@@ -662,9 +662,10 @@ struct PackedStage {
 // bf16 and fp16 queries: every operand is fp16, and the codes of two values become one by a single AND: bits 0-3 of a
 // half are the number code * 2^-24, bits 4-7 code * 2^-20 (what the words hold above them comes down by one shift).
 //
-// Queries.  A head's values are multiplied by the power of two that takes their largest to 2^14 .. 2^15, so that bf16's
-// become fp16 without loss but for those below 2^-29 of the largest; values that meet codes in bits 4-7 are taken 16 times
-// smaller.  With c, z, s a group's codes, zero and scale: score = sum over groups of s * (sum q c - z * sum q).
+// Queries.  A head's values are multiplied by the power of two that takes their largest to 2^14 .. 2^15, and become fp16; those
+// that meet codes in bits 4-7 are taken 16 times smaller, the largest to 2^10 or more.  fp16's smallest step, 2^-24, holds
+// the 8 bits of bf16 from 2^-17 on and the 11 of fp16 from 2^-14 on: smaller values than 2^-27 and 2^-24 of the largest are
+// rounded, by 2^-25 or 2^-35 of it.  With c, z, s a group's codes, zero and scale: score = sum over groups of s * (sum q c - z * sum q).
 //
 // Values.  weight * scale is rounded to fp16 after a factor of the head's and the group's own, chosen so that the largest
 // product so far lies at 2 or more: fp16's smallest step is 2^-25 of it or less, and rounds by half of that.  The factor is

@@ -127,3 +127,38 @@ def test_a_scale_near_the_largest_without_weight(cuda_lib, dtype):
 def test_scales_near_the_ends_of_the_range(cuda_lib, dtype, power):
     scale = {t: power + t % 5 for t in range(400)}
     Case(6, 400, dtype, {t: t % 7 - 3.0 for t in range(0, 400, 9)}, scale).check(cuda_lib)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("largest", [1.0, 2.0 ** -12, 30000.0])
+def test_small_values_of_a_query(cuda_lib, dtype, D, largest):
+    """A head's largest value meets keys of 0 and the others are 2^-12 to 2^-30 of it: each enters by itself, rounded by 2^-35
+    of the largest at most, and only below 2^-27 (bf16) or 2^-24 (fp16)."""
+    pa, n, H = cuda_lib, 64, 2
+    g = torch.Generator().manual_seed(D)
+    size = torch.exp2(-12 - 18 * torch.rand((1, H, D), generator=g))
+    q = (size * torch.randn((1, H, D), generator=g)).clamp(-2.0 ** -9, 2.0 ** -9)
+    q[..., ::16] = 1.0
+    q = (q * largest).to(dtype)
+    k = torch.rand((n // 16, 16, H, D), generator=g)
+    k[..., ::16] = 0.0
+    (kc, kp), (vc, vp) = pack(k), pack(torch.randn(k.shape, generator=g))
+    assert (kp[..., 1::2] == 0).all()  # (so that the largest value is multiplied by nothing but codes of 0)
+    scale = 2.0 ** 10 / largest
+    got = pa.paged_attention_decode_q4(q.cuda(), pa.Q4Cache(*(x.cuda() for x in (kc, vc, kp, vp))),
+                                       torch.arange(n // 16, dtype=torch.int32)[None].cuda(), int32([n]).cuda(), scale=scale)
+    kf, vf = (oracle.window.q4_values(c, p).reshape(n, H, D) for c, p in ((kc, kp), (vc, vp)))
+    qf, u32 = q[0].double().numpy(), 2.0 ** -24
+    z = scale * np.einsum("hd,nhd->nh", qf, kf)
+    w = np.exp(z - z.max(0))
+    w /= w.sum(0)
+    ref, spread = np.einsum("nh,nhd->hd", w, vf), np.einsum("nh,nhd->hd", w, np.abs(vf))
+    top = np.abs(qf).max(1)[:, None]
+    small = np.abs(qf) < top * (2.0 ** -27 if dtype == BF16 else 2.0 ** -24)
+    assert small.any() and not small.all()
+    lost = scale * (np.einsum("hd,nhd->nh", small * top * 2.0 ** -35, kf) + (D + 4) * u32 * np.einsum("hd,nhd->nh", np.abs(qf) * (qf != top), kf)).max(0)
+    rel = 2 * (lost + 2.0 ** -22 + u32 * np.abs(z).max(0)) + 2 * (n + 16) * u32 + 2.0 ** -11
+    off = spread * rel[:, None] + n * 15 * 2.0 ** -26 * vp[..., 0::2].double().numpy().max()
+    half = torch.finfo(dtype).eps / 2
+    assert (np.abs(got[0].double().cpu().numpy() - ref) <= (off + half * np.abs(ref)) * (1 + half)).all()
