@@ -15,10 +15,12 @@
 //   Two instantiations of the softmax, no more: the code has to stay in the instruction cache (a third for causal cuts
 //   alone cost 4 %, code for very large scores inside the loop 20 %).
 // * The stabiliser is an unscaled score (see tree_umma.cu for why, and for the lift of fp16 weights).
-// * A masked value cannot be deselected in a product (0 * NaN): a row's outputs may be non-finite because of a value that
-//   another row of the item sees.  Looking through V for that in every tile that some row sees in part cost a quarter of
-//   the time, so it is looked for in the results: a CTA that has written a non-finite output goes through its rows
-//   again at its end, and recomputes those whose own keys do not explain it (win_mend).
+// * A masked value cannot be deselected in a product (0 * NaN), and a tile that some rows of an item do not see whole may
+//   hold a value that is not finite.  A warp of its own, the guard, looks through every such V tile before its products and
+//   makes those values 0 that not every row sees; rows that do see one get their NaN when they are written (win_poison).
+//   (Without the guard the softmax groups' time for that look cost a quarter of the call's; looked for in the results instead,
+//   with such rows computed again key by key, one NaN took 8 prompts from 344 us to 16 ms and a context of 8,192 without a
+//   window from 264 us to 236 ms.)
 //
 // Bound by the round S, softmax, P V of a tile (4,000 cycles for two Q tiles).  8 prompts of 2,048 rows, 32 / 8 heads,
 // head_dim 128, bf16, window 1,024 and 4: 330 us (810 TFLOP/s over the pairs that are seen; 449 with the prefill kernel's
@@ -42,6 +44,7 @@ __device__ __forceinline__ bool win_wait(uint64_t* bar, unsigned parity, const u
   return mbar_try_wait(bar, parity) || win_wait_on(bar, parity, err, epoch);
 }
 
+constexpr int kWinThreads = kUmThreads + 32;  // the guard is the last warp
 constexpr int kWinSlots = 8;  // item records in flight between the K producer and their readers
 
 // Rows [T0, T1) of sequence b; first: position of row T0; n: the sequence's context (0 and !ok: refused).
@@ -108,6 +111,34 @@ struct WinSubs {
   __device__ __forceinline__ int key(int u) const { return 16 * (u >= sinks ? u + skip : u); }  // first key of sub-tile u
 };
 
+// A tile of an item.  It may begin with sub-tiles of sinks: columns below `split` are keys from `start` on, the others continue
+// to kb + column.
+struct WinTile {
+  int start, split, kb;
+  __device__ __forceinline__ WinTile(const WinSubs& sb, int tile) {
+    start = tile * kUmKeys;
+    split = 16 * max(sb.sinks - tile * kUmSub, 0);
+    kb = start + (split < kUmKeys ? 16 * sb.skip : 0);
+  }
+  __device__ __forceinline__ bool mixed() const { return split > 0 && split < kUmKeys; }
+  __device__ __forceinline__ int key(int column) const { return (column < split ? start : kb) + column; }
+};
+
+// What the rows of an item see of the keys: all of them, some, none.
+struct WinSees {
+  int first, last, low_first, low_last, sinks;  // positions of the first and the last row, and where their windows begin
+  __device__ __forceinline__ WinSees(const AttnArgs& a, const WinItem& it)
+      : first(it.first), last(it.kv_end() - 1), low_first(window_low(it.first, a.window)),
+        low_last(window_low(it.kv_end() - 1, a.window)), sinks(a.sinks) {}
+  __device__ __forceinline__ bool all(int key) const { return key <= first && (key >= low_last || key < sinks); }
+  __device__ __forceinline__ bool some(int key) const { return key <= last && (key >= low_first || key < sinks); }
+  // Whether every row sees every key of the tile.
+  __device__ __forceinline__ bool whole(const WinTile& t, unsigned loaded) const {
+    return loaded == (1u << kUmSub) - 1u && !t.mixed() && t.kb + kUmKeys - 1 <= first &&
+           (t.kb >= low_last || t.kb + kUmKeys <= sinks);
+  }
+};
+
 // The scores of a warp's rows in the 128 columns from taddr on become (s - m) * sc.  (Rare, and kept out of the loop's
 // code.)
 static __device__ __noinline__ void s_distances(uint32_t taddr, float sc, float m) {
@@ -142,7 +173,8 @@ static __device__ __noinline__ void s_mask(uint32_t taddr, uint32_t m0, uint32_t
 // more than an eighth (scores of 2^20): there they are 2^((s - m) * sc).
 template <bool kBf16>
 __device__ __forceinline__ float row_softmax_window(uint32_t srow, float sc, bool sees, float& m_use, float& l_run) {
-  constexpr float kLift = kBf16 ? 0.f : 7.f;
+  // (bf16: 2^8 lower, so that a weight is 1 at most and its product with the largest values stays finite)
+  constexpr float kLift = kBf16 ? -8.f : 7.f;
   const ScoreFix fix{};
   // (keys that are seen count, whatever their scores: a row of scores of -inf is told from one that sees nothing)
   float mx = sees ? -FLT_MAX : -INFINITY;
@@ -172,92 +204,110 @@ __device__ __forceinline__ float row_softmax_window(uint32_t srow, float sc, boo
   return corr;
 }
 
-// Whether one of sixteen 16-bit floats is infinite or NaN (multiplied by 0 they give NaN).
+// acc, NaN from then on if one of eight 16-bit floats is infinite or NaN (multiplied by 0 they give NaN).
 template <bool kBf16>
-__device__ __forceinline__ bool any_nonfinite(const uint32_t (&w)[8]) {
-  uint32_t r = 0u;
+__device__ __forceinline__ void note_nonfinite(const uint4& v, uint32_t& acc) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     if constexpr (kBf16)
-      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(r) : "r"(w[i]), "r"(0u));
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0u));
     else
-      asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(r) : "r"(w[i]), "r"(0u));
+      asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0u));
   }
-  return (r & 0x7fff7fffu) != 0u;
 }
 
-// After the CTA's last item: its outputs that are not finite are kept where a value that the row sees, or
-// a score of it, is not finite either; the others come from a product of weight 0 with another row's value, and the
-// row is computed again, on CUDA cores.  A warp takes a row, a lane D / 32 of its columns; keys from the row's own
-// down, so that a row of a model that has diverged is explained by the first.
-template <typename T, int D, int G>
-__device__ __noinline__ void win_mend(const AttnArgs& a, int max_len) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  WinWalk walk(a, kUmRows / G, max_len);
-  WinItem it;
-  for (int w = blockIdx.x; walk.find(w, it); w += gridDim.x) {
-    const int kvh = w % a.n_kv_heads;
-    if (!it.ok) continue;
-    for (int r = threadIdx.x >> 5; r < kUmRows; r += kUmThreads / 32) {
-      const int tok = it.T0 + r / G;
-      if (tok >= it.T1) break;
-      const int64_t at = ((int64_t)tok * a.n_q_heads + kvh * G + r % G) * D + lane * kPer;
-      T* out = static_cast<T*>(a.out) + at;
-      bool open[kPer];  // columns to explain
-      bool any = false;
+// The guard's look through a V tile (one warp): false if all of it is finite.
+template <bool kBf16, int kBytes>
+__device__ __forceinline__ bool v_nonfinite(const uint8_t* tile, int lane) {
+  uint32_t acc[2] = {0u, 0u};
+#pragma unroll 1
+  for (int e = lane; e < kBytes / 16; e += 8 * 32) {
+    uint4 v[8];
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        open[c] = !(fabsf(static_cast<float>(out[c])) <= FLT_MAX);
-        any |= open[c];
-      }
-      if (!__any_sync(0xffffffffu, any)) continue;
-      const int pos = it.first + (tok - it.T0);
-      const int low = max(pos + 1 - a.window, 0), first = min(a.sinks, low);
-      const int32_t* table = a.block_table + (int64_t)it.b * a.bt_stride;
-      float q[kPer], acc[kPer];
+    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const uint4*>(tile + 16 * (e + 32 * u));
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        q[c] = static_cast<float>(static_cast<const T*>(a.q)[at + c]);
-        acc[c] = 0.f;
-      }
-      float m = -INFINITY, l = 0.f;
-      bool keep = false;  // a score is not finite, or every column is explained
-      for (int j = pos; j >= 0 && !keep; --j) {
-        if (j < low && j >= first) j = first - 1;
-        if (j < 0) break;
-        const int blk = ld_nc_s32(table + (j >> a.block_shift));
-        if (blk < 0 || blk >= a.num_blocks) continue;
-        const int64_t src = (int64_t)blk * a.kv_block_stride +
-                            ((int64_t)(j & (a.block_size - 1)) * a.n_kv_heads + kvh) * D + lane * kPer;
-        const T* k = static_cast<const T*>(a.k_pool) + src;
-        const T* v = static_cast<const T*>(a.v_pool) + src;
-        float s = 0.f;
+    for (int u = 0; u < 8; ++u) note_nonfinite<kBf16>(v[u], acc[u & 1]);
+  }
+  return __any_sync(0xffffffffu, ((acc[0] | acc[1]) & 0x7fff7fffu) != 0u);
+}
+
+// Zeros for the rows of a V tile that hold no data or lie past the context, and for the values that are not finite and that
+// not every row of the item sees.  Returns whether some row sees one of these.
+template <bool kBf16, int kBytes>
+__device__ __noinline__ bool v_clear(uint8_t* tile, int lane, const WinTile t, const WinSees sees, int n, unsigned loaded) {
+  constexpr uint32_t kExp = kBf16 ? 0x7f80u : 0x7c00u;
+  bool seen = false;
+#pragma unroll 1
+  for (int e = lane; e < kBytes / 16; e += 32) {
+    const int row = (e >> 3) & (kUmKeys - 1), key = t.key(row);
+    uint4* p = reinterpret_cast<uint4*>(tile + 16 * e);
+    if (!((loaded >> (row >> 4)) & 1u) || key >= n) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    if (sees.all(key)) continue;
+    uint4 v = *p;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    bool found = false;
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) s = fmaf(q[c], static_cast<float>(k[c]), s);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const float m_new = fmaxf(m, fmaxf(s, -FLT_MAX));
-        const float f = fast_exp2((m - m_new) * a.scale_log2), p = fast_exp2((s - m_new) * a.scale_log2);
-        m = m_new;
-        l = fmaf(l, f, p);
-        any = false;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) {
-          const float x = static_cast<float>(v[c]);
-          acc[c] = fmaf(p, x, acc[c] * f);
-          if (!(fabsf(x) <= FLT_MAX)) open[c] = false;
-          any |= open[c];
-        }
-        // (the scores are the same in every lane; +inf has the weight NaN)
-        keep = s != s || s == INFINITY || !__any_sync(0xffffffffu, any);
-      }
-      if (keep) continue;
-#pragma unroll
-      for (int c = 0; c < kPer; ++c)
-        if (open[c]) out[c] = Elt<T>::from_float(m == -INFINITY ? 0.f : acc[c] / l);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t keep = 0xffffffffu;
+      if ((w[i] & kExp) == kExp) keep &= 0xffff0000u;
+      if (((w[i] >> 16) & kExp) == kExp) keep &= 0x0000ffffu;
+      found |= keep != 0xffffffffu;
+      w[i] &= keep;
+    }
+    if (found) {
+      *p = v;
+      seen |= sees.some(key);
     }
   }
+  return __any_sync(0xffffffffu, seen);
+}
+
+// NaN for the outputs of a warp's rows (`out` a lane's row, `bound` its position; -1: none) whose columns hold a value that is not finite
+// and that the row sees, among the keys that only some rows of the item see: the guard made these 0.
+template <typename T, int D>
+__device__ __noinline__ void win_poison(const AttnArgs& a, const WinItem it, int kvh, int bound, T* out) {
+  constexpr int kPer = D / 32, kUnroll = 8;
+  const int lane = threadIdx.x & 31;
+  const WinSees sees(a, it);
+  const int low = window_low(bound, a.window);
+  const int32_t* table = a.block_table + (int64_t)it.b * a.bt_stride;
+  uint32_t cols[kPer] = {};  // column lane' * kPer + c: bit lane' of cols[c]
+  // keys behind the first row's, then those before the last row's window
+#pragma unroll 1
+  for (int range = 0; range < 2; ++range) {
+    const int end = range == 0 ? sees.last + 1 : min(sees.low_last, sees.first + 1);
+#pragma unroll 1
+    for (int j0 = range == 0 ? sees.first + 1 : sees.low_first; j0 < end; j0 += kUnroll) {
+      T v[kUnroll][kPer];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int j = j0 + u;
+        const int blk = j < end ? ld_nc_s32(table + (j >> a.block_shift)) : -1;
+        const bool here = blk >= 0 && blk < a.num_blocks;
+        const T* src = static_cast<const T*>(a.v_pool) + (here ? (int64_t)blk * a.kv_block_stride : 0) +
+                       ((int64_t)(j & (a.block_size - 1)) * a.n_kv_heads + kvh) * D + lane * kPer;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) v[u][c] = here ? src[c] : Elt<T>::from_float(0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int j = j0 + u;
+        const bool mine = j <= bound && (j >= low || j < a.sinks);
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+          const unsigned bad = __ballot_sync(0xffffffffu, !(fabsf(static_cast<float>(v[u][c])) <= FLT_MAX));
+          if (mine) cols[c] |= bad;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kPer; ++c)
+    for (uint32_t m = cols[c]; m != 0u; m &= m - 1u) out[(__ffs(m) - 1) * kPer + c] = Elt<T>::from_float(NAN);
 }
 
 // Record number idx of the K producer's ring; false: the wait gave up, or there are no more items (it.b < 0).
@@ -276,7 +326,7 @@ __device__ __forceinline__ bool win_read(const AttnArgs& a, uint64_t* rec_full, 
 }
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kUmThreads)
+__global__ void __launch_bounds__(kWinThreads, 1)
     window_umma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
   using Cfg = UmCfg<D>;
@@ -301,16 +351,17 @@ __global__ void __launch_bounds__(kUmThreads)
   uint64_t* q_empty = bars + 32;  // one phase per item: its S products completed, Q may be reloaded
   uint64_t* o_free = bars + 33;   // [2] one phase per item with tiles of group k: it has read O_k
   uint64_t* rec_full = bars + 36;   // [kWinSlots] the record in the slot is written
-  uint64_t* rec_empty = bars + 44;  // [kWinSlots] the V producer, the MMA warp and all 8 softmax warps have read it
+  uint64_t* rec_empty = bars + 44;  // [kWinSlots] the V producer, the MMA warp, the guard and all 8 softmax warps have read it
+  uint64_t* guarded = bars + 52;    // [kUmVStages] the V tile has landed and the guard is done with it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
-  volatile int* bad_out = reinterpret_cast<int*>(base + 516);  // an output was not finite
+  volatile int* v_flag = reinterpret_cast<int*>(base + 520);   // [kUmVStages] some rows see a value that the guard made 0
   uint32_t* kmask = reinterpret_cast<uint32_t*>(base + 544);   // [8] sub-tiles holding data, per tile slot
   int* recs = reinterpret_cast<int*>(base + 576);              // [kWinSlots][8] item records; b < 0: no more
   uint8_t* qs = base + 1024;                       // [2][Q tile]
   uint8_t* ks = qs + 2 * Cfg::kQBytes;             // [kUmKStages][K tile]
   uint8_t* vs = ks + kUmKStages * Cfg::kKvBytes;   // [kUmVStages][V tile]
   static_assert(kUmKStages <= 4 && kUmVStages <= 4, "barrier slots");
-  static_assert(576 + kWinSlots * 32 <= 1024 && 52 * 8 <= 512, "records and barriers fit their 1 KB slot");
+  static_assert(576 + kWinSlots * 32 <= 1024 && 56 * 8 <= 512, "records and barriers fit their 1 KB slot");
 
   // Item w: block w / n_kv_heads of the batch, KV head w % n_kv_heads; this CTA takes blockIdx.x, blockIdx.x + gridDim.x, ...
   const int warp = threadIdx.x >> 5;
@@ -330,6 +381,7 @@ __global__ void __launch_bounds__(kUmThreads)
     for (int s = 0; s < kUmVStages; ++s) {
       mbar_init(&vfull[s], 1);
       mbar_init(&vempty[s], 1);
+      mbar_init(&guarded[s], 1);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&s_full[k], 1);
@@ -341,11 +393,10 @@ __global__ void __launch_bounds__(kUmThreads)
     mbar_init(q_empty, 1);
     for (int k = 0; k < kWinSlots; ++k) {
       mbar_init(&rec_full[k], 1);
-      mbar_init(&rec_empty[k], 10);  // V producer, MMA, 8 softmax warps
+      mbar_init(&rec_empty[k], 11);  // V producer, MMA, guard, 8 softmax warps
     }
     mbar_init(fin, 1);
     for (int s = 0; s < 8; ++s) mbar_init(&mready[s], 1);
-    *bad_out = 0;
     fence_barrier_init();
   }
   if (warp == 10) tmem_alloc(tmem_slot, kUmTmemCols);
@@ -545,7 +596,7 @@ __global__ void __launch_bounds__(kUmThreads)
       auto pv_of = [&](int k, int j) {
         const int gj = g + j;
         if (!own_o(k, j) || !wait(&p_full[k], (unsigned)((k == 0 ? gj : g1 + j) & 1)) ||
-            !wait(&vfull[gj % kUmVStages], (unsigned)((gj / kUmVStages) & 1)))
+            !wait(&guarded[gj % kUmVStages], (unsigned)((gj / kUmVStages) & 1)))
           return false;
         tc_fence_after();
         issue_pv(k, gj, j == 0);
@@ -585,6 +636,46 @@ __global__ void __launch_bounds__(kUmThreads)
         win_wait(fin, 0, a.err, a.epoch);
       }
     }
+  } else if (warp == 11) {
+    // ------------------------------------------ guard -------------------------------------------
+    // (never more than the ring ahead of the products, which wait for it and not for vfull: another wait in the MMA warp's
+    // code costs 2 %)
+    int i = 0;  // tiles of earlier items
+    bool alive = true;
+    for (int rec = 0; alive; ++rec) {
+      WinItem it;
+      if (!__all_sync(0xffffffffu, win_read(a, rec_full, recs, rec, it))) {
+        alive = __all_sync(0xffffffffu, it.b < 0);
+        break;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rec_empty[rec % kWinSlots]);
+      const WinSubs sb(a, it);
+      const WinSees sees(a, it);
+      const int nt = sb.tiles();
+      for (int tile = 0; tile < nt; ++tile, ++i) {
+        const int s = i % kUmVStages;
+        const unsigned parity = (unsigned)((i / kUmVStages) & 1);
+        if (!__all_sync(0xffffffffu, win_wait(&mready[i & 7], (unsigned)((i >> 3) & 1), a.err, a.epoch)) ||
+            !__all_sync(0xffffffffu, win_wait(&vfull[s], parity, a.err, a.epoch))) {
+          alive = false;
+          break;
+        }
+        const unsigned loaded = kmask[i & 7];
+        const WinTile t(sb, tile);
+        bool seen = false;
+        if (!sees.whole(t, loaded) && v_nonfinite<kBf16, Cfg::kKvBytes>(vs + s * Cfg::kKvBytes, lane)) {
+          seen = v_clear<kBf16, Cfg::kKvBytes>(vs + s * Cfg::kKvBytes, lane, t, sees, it.n, loaded);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          v_flag[s] = seen ? 1 : 0;
+          mbar_arrive(&guarded[s]);
+        }
+      }
+    }
+    if (!alive && lane == 0) raise_timeout(a.err, a.epoch);
   } else {
     // --------------------------------------- softmax groups ---------------------------------------
     const int grp = warp >> 2;           // 0 or 1
@@ -612,13 +703,13 @@ __global__ void __launch_bounds__(kUmThreads)
       const int bound = it.ok && tok < it.T1 ? it.first + (tok - it.T0) : -1;  // the row's position
       const int low = window_low(bound, a.window);                             // first key of its window
       const WinSubs sb(a, it);
+      const WinSees sees_all(a, it);
+      bool poison = false;  // some rows see a value that the guard made 0
       const int all = sb.tiles();
       const int nt = grp == 0 || it.both(kUmTileRows / G) ? all : 0;
       for (int tile = 0; tile < nt; ++tile, ++i, ++mine) {
-        // Key of the tile's first column.  A tile may begin with sub-tiles of sinks: columns below `split` are keys from
-        // tile * kUmKeys on, the others continue to kb + column.
-        const int split = 16 * max(sb.sinks - tile * kUmSub, 0);
-        const int kb = tile * kUmKeys + (split < kUmKeys ? 16 * sb.skip : 0);
+        const WinTile t(sb, tile);
+        const int split = t.split, kb = t.kb;
         if (!__all_sync(0xffffffffu, win_wait(&mready[i & 7], (unsigned)((i >> 3) & 1), a.err, a.epoch))) {
           alive = false;
           break;
@@ -632,7 +723,7 @@ __global__ void __launch_bounds__(kUmThreads)
         tc_fence_after();
         // tiles that every row of the warp sees whole, with every sub-tile loaded, need no mask
         const unsigned all_sub = (1u << kUmSub) - 1u;
-        const bool mixed = split > 0 && split < kUmKeys;
+        const bool mixed = t.mixed();
         const bool whole = __all_sync(0xffffffffu, loaded == all_sub && kb + kUmKeys - 1 <= bound && !mixed &&
                                                        (kb >= low || kb + kUmKeys <= a.sinks));
         const uint32_t srow = tS(grp) + lane_base;
@@ -668,22 +759,13 @@ __global__ void __launch_bounds__(kUmThreads)
             tmem_st32(tO(grp) + lane_base + c0, v);
           }
         }
-        // group 0 zeroes V rows that hold no data or lie past the context (group 1's P V is issued
-        // after group 0's, so it sees the zeros too)
-        if (grp == 0 && (kb + kUmKeys > it.n || loaded != all_sub)) {
+        if (!sees_all.whole(t, loaded)) {  // (the stage, and its flag, are not filled again before this P's product)
           if (!__all_sync(0xffffffffu,
-                          win_wait(&vfull[i % kUmVStages], (unsigned)((i / kUmVStages) & 1), a.err, a.epoch))) {
+                          win_wait(&guarded[i % kUmVStages], (unsigned)((i / kUmVStages) & 1), a.err, a.epoch))) {
             alive = false;
             break;
           }
-          uint8_t* vst = vs + (i % kUmVStages) * Cfg::kKvBytes;
-          for (int e = r; e < kUmKeys * 8 * kHalves; e += 128) {
-            const int key = e / (8 * kHalves);
-            const int c = e % (8 * kHalves);
-            if (kb + key >= it.n || !((loaded >> (key >> 4)) & 1u))
-              *reinterpret_cast<uint4*>(vst + sw_off(key, c, Cfg::kKvHalf)) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+          poison |= v_flag[i % kUmVStages] != 0;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -711,11 +793,11 @@ __global__ void __launch_bounds__(kUmThreads)
             for (int e = 0; e < 8; ++e)
               x[e] = pack2<kBf16>(have ? __uint_as_float(v[j + 2 * e]) * inv : 0.f,
                                   have ? __uint_as_float(v[j + 2 * e + 1]) * inv : 0.f);
-            if (any_nonfinite<kBf16>(x)) *bad_out = 1;
             st_global32(orow + c0 + j, x, wide);
           }
         }
       }
+      if (poison) win_poison<T, D>(a, it, w % a.n_kv_heads, bound, orow);
       // O_k has been read: the next item's first P V may overwrite it
       if (nt > 0) {
         tc_fence_before();
@@ -731,7 +813,6 @@ __global__ void __launch_bounds__(kUmThreads)
     tc_fence_after();
     tmem_dealloc(tmem, kUmTmemCols);
   }
-  if (*bad_out != 0) win_mend<T, D, G>(a, max_len);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -763,7 +844,7 @@ static cudaError_t launch_win_g(const AttnArgs& a, const CUtensorMap& km, const 
   // (how many there are is known on the device alone)
   const int64_t items = win_items(a.batch, a.rows, kUmRows / G, a.n_kv_heads);
   if (items > 0x7fffffffLL - sms) return cudaErrorInvalidConfiguration;  // (item numbers are int32)
-  window_umma_kernel<T, D, G><<<(unsigned)std::min<int64_t>(items, sms), kUmThreads, smem, s>>>(a, km, vm, qm);
+  window_umma_kernel<T, D, G><<<(unsigned)std::min<int64_t>(items, sms), kWinThreads, smem, s>>>(a, km, vm, qm);
   return cudaGetLastError();
 }
 
