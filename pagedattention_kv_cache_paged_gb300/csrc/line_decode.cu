@@ -675,8 +675,8 @@ struct PackedStage {
 //
 // Bound by instructions: 425 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
 // clock by the 16 warps that the registers allow (more warps at fewer registers, and the next step's scores next to this
-// one's values, spill and are slower).  32 / 8 heads: 64 requests of 512 to 4,096 tokens (171 MB) take 59 us, 4 of 32,768 to
-// 131,000 (378 MB) 112 us.
+// one's values, spill and are slower).  32 / 8 heads: 64 requests of 512 to 4,096 tokens (171 MB) take 57 us, 4 of 32,768 to
+// 131,000 (378 MB) 110 us.
 template <typename T, int D, int NT>
 struct PackedRows : PackedStage<D> {
   static constexpr bool kTma = false;
@@ -842,15 +842,16 @@ struct PackedRows : PackedStage<D> {
         float g[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // (no weight of this step is above 1, and the products so far shrank by f)
+          // (no weight of this step is above 1, and the products so far shrank by f; approximate quotients, since exact ones
+          // cost a unit 1 to 5 us in code that runs once)
           const float f = e ? f1 : f0, old = vk[nt][gr][e];
           float top = fmaxf(fast_exp2(x[e]) * q4_scale(pair[0][gr]), fast_exp2(x[2 + e]) * q4_scale(pair[1][gr]));
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          float now = fminf(old / f, kMostVk);
+          float now = fminf(__fdividef(old, f), kMostVk);
           if (top * now >= 4.f) now = __uint_as_float((uint32_t)(255 - (int)(__float_as_uint(top) >> 23)) << 23);
           vk[nt][gr][e] = now;
-          g[e] = f == 0.f ? 0.f : f * (now / old);
+          g[e] = f == 0.f ? 0.f : f * __fdividef(now, old);
         }
 #pragma unroll
         for (int i = 4 * gr; i < 4 * gr + 4; ++i) {
@@ -1122,7 +1123,7 @@ constexpr int kLineStatic = 512;  // the schedule, the rings' barriers
 // cuts its sums off where it should round: a step takes up to 2^-23 of what a sum holds from it, always in the same
 // direction (131,072 tokens by one warp lost 8e-4 of the result over the 4-bit cache, whose codes are not centred, and two
 // million 1.3 %); now 3e-5 at most, and sums of rounded additions have fewer summands as well.  Calls in which no CTA can
-// have that many steps of a unit take the form without (4-bit serving batch 59.0 and 60.5 us, window of 8,192 90 and 93).
+// have that many steps of a unit take the form without (window of 8,192: 90 us without, 93 with).
 template <typename Rows, int D, int NT, bool kRuns>
 __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
     line_decode_kernel(const LineArgs a, const __grid_constant__ LineMaps maps) {

@@ -18,9 +18,9 @@
 // * A masked value cannot be deselected in a product (0 * NaN), and a tile that some rows of an item do not see whole may
 //   hold a value that is not finite.  A warp of its own, the guard, looks through every such V tile before its products and
 //   makes those values 0 that not every row sees; rows that do see one get their NaN when they are written (win_poison).
-//   (Without the guard the softmax groups' time for that look cost a quarter of the call's; looked for in the results instead,
-//   with such rows computed again key by key, one NaN took 8 prompts from 344 us to 16 ms and a context of 8,192 without a
-//   window from 264 us to 236 ms.)
+//   (That look by the softmax groups took a quarter of the call.  Looked for in the results instead, with such rows
+//   computed again key by key, one NaN took 8 prompts from 344 us to 16 ms, and 2,048 rows over 8,192 tokens without a window
+//   from 264 us to 236 ms; by the guard both take as long with it as without.)
 //
 // Bound by the round S, softmax, P V of a tile (4,000 cycles for two Q tiles).  8 prompts of 2,048 rows, 32 / 8 heads,
 // head_dim 128, bf16, window 1,024 and 4: 330 us (810 TFLOP/s over the pairs that are seen; 449 with the prefill kernel's
