@@ -673,7 +673,7 @@ struct PackedStage {
 // has to fit): it is taken down to products of 2 .. 4 if need be, accumulators with it.  It grows as a stabiliser
 // that moves takes the products down.  So a large scale of a small weight costs the others nothing.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
 //
-// Bound by instructions: 425 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
+// Bound by instructions: 443 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
 // clock by the 16 warps that the registers allow (more warps at fewer registers, and the next step's scores next to this
 // one's values, spill and are slower).  32 / 8 heads: 64 requests of 512 to 4,096 tokens (171 MB) take 57 us, 4 of 32,768 to
 // 131,000 (378 MB) 110 us.
@@ -1123,7 +1123,8 @@ constexpr int kLineStatic = 512;  // the schedule, the rings' barriers
 // cuts its sums off where it should round: a step takes up to 2^-23 of what a sum holds from it, always in the same
 // direction (131,072 tokens by one warp lost 8e-4 of the result over the 4-bit cache, whose codes are not centred, and two
 // million 1.3 %); now 3e-5 at most, and sums of rounded additions have fewer summands as well.  Calls in which no CTA can
-// have that many steps of a unit take the form without (window of 8,192: 90 us without, 93 with).
+// have that many steps of a unit take the form without (4-bit serving
+// batch: 57.0 us, and 58.4 by this form, which it takes with a table as wide as for 131,072 tokens).
 template <typename Rows, int D, int NT, bool kRuns>
 __global__ void __launch_bounds__(LineCfg<Rows>::kThreads, Rows::kCtas)
     line_decode_kernel(const LineArgs a, const __grid_constant__ LineMaps maps) {
