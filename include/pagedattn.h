@@ -479,7 +479,9 @@ PA_API int paged_kv_unpack_q4(const void* k_codes, const void* v_codes, const vo
  * (bf16) of it; apart from that, products of queries and codes are exact.  Each weight
  * times its value's scale is rounded to fp16 for bf16 and fp16 queries, by at most 2^-11 of itself or 2^-26 of the largest
  * such product of the head and the group of dimensions, whichever is more, and split into bf16 parts that hold its 24 bits
- * for fp32.
+ * for fp32.  With bf16 and fp16 queries codes are small parts of a tensor core's operands, and zeros are taken off whole sums:
+ * a product over 16 tokens (or dimensions) is cut off at up to 17 * 2^-14 of the largest weight times scale (query value) in
+ * it, so that a dimension whose visible values are all 0 gives up to 2^-10 of the scale; with fp32 queries 0.
  */
 PA_API int paged_attention_decode_q4(void* out, const void* q, const void* k_codes, const void* v_codes,
                                      const void* k_params, const void* v_params, const int32_t* block_table,

@@ -665,13 +665,19 @@ struct PackedStage {
 // Queries.  A head's values are multiplied by the power of two that takes their largest to 2^14 .. 2^15, and become fp16; those
 // that meet codes in bits 4-7 are taken 16 times smaller, the largest to 2^10 or more.  fp16's smallest step, 2^-24, holds
 // the 8 bits of bf16 from 2^-17 on and the 11 of fp16 from 2^-14 on: smaller values than 2^-27 and 2^-24 of the largest are
-// rounded, by 2^-25 or 2^-35 of it.  With c, z, s a group's codes, zero and scale: score = sum over groups of s * (sum q c - z * sum q).
+// rounded, by 2^-25 or 2^-35 of it.  With c, z, s a group's codes, zero and scale: score = sum over groups of
+// s * (sum q c - z * sum q).
 //
 // Values.  weight * scale is rounded to fp16 after a factor of the head's and the group's own, chosen so that the largest
 // product so far lies at 2 or more: fp16's smallest step is 2^-25 of it or less, and rounds by half of that.  The factor is
 // looked at again, with the stabiliser's vote, where a scale passes 2^11 over it (a weight may be 2^kGrow, and the product
 // has to fit): it is taken down to products of 2 .. 4 if need be, accumulators with it.  It grows as a stabiliser
-// that moves takes the products down.  So a large scale of a small weight costs the others nothing.  O = C (w s) - z (w s): the second product once for all dimensions of a group.
+// that moves takes the products down.  So a large scale of a small weight costs the others nothing.
+// O = C (w s) - z (w s): the second product once for all dimensions of a group.
+//
+// A sum's summands are aligned with the largest exponent of their operands and cut off 24 bits below it, and a code of bits 0-3
+// lies 2^10 below what its operand's exponent stands for: of 16 products and a sum each may lose 2^-14 of the largest weight
+// times scale, per code's unit (measured 2^-12.4 of a scale where all values are 0; fp16's own half step is 2^-11).
 //
 // Bound by instructions: 443 for 16 tokens of a KV head at head_dim 128, half of them on the integer pipe, issued at 0.6 a
 // clock by the 16 warps that the registers allow (more warps at fewer registers, and the next step's scores next to this

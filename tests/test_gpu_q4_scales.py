@@ -162,3 +162,25 @@ def test_small_values_of_a_query(cuda_lib, dtype, D, largest):
     off = spread * rel[:, None] + n * 15 * 2.0 ** -26 * vp[..., 0::2].double().numpy().max()
     half = torch.finfo(dtype).eps / 2
     assert (np.abs(got[0].double().cpu().numpy() - ref) <= (off + half * np.abs(ref)) * (1 + half)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 3, 16, 64, 700])
+@pytest.mark.parametrize("gain", [1.0, 3.0])
+def test_dimensions_of_zeros(cuda_lib, dtype, D, n, gain):
+    """Values of 0 are code = zero: two sums that are taken from one another.  With fp32 queries the difference is formed
+    first, and is 0; else 16 products and a sum are each cut off at 2^-14 of a step's largest product of weight and scale, in
+    units of a code, and the largest of the steps, summed, are at most the sum of all weights."""
+    pa, H, S = cuda_lib, 4, 16
+    g = torch.Generator().manual_seed(n)
+    rows = (-(-n // S), S, H, D)
+    k, v = gain * torch.randn(rows, generator=g), torch.zeros(rows)
+    v[..., 0::64] = -0.5 - 4 * torch.rand(v[..., 0::64].shape, generator=g)
+    v[..., 1::64] = 0.5 + 4 * torch.rand(v[..., 1::64].shape, generator=g)
+    (kc, kp), (vc, vp) = pack(k), pack(v)
+    q = torch.randn((1, 4 * H, D), generator=g).to(dtype)
+    got = pa.paged_attention_decode_q4(q.cuda(), pa.Q4Cache(*(x.cuda() for x in (kc, vc, kp, vp))),
+                                       torch.arange(rows[0], dtype=torch.int32)[None].cuda(), int32([n]).cuda())
+    zeros = got[0].float().cpu().unflatten(-1, (-1, 64))[..., 2:].abs().max()
+    assert zeros <= (0.0 if dtype == FP32 else 17 * 2.0 ** -14 * float(vp[..., 0::2].float().max()))
